@@ -421,6 +421,100 @@ pic_status pic_op_attention_plan(int32_t dtype, int32_t n_heads, int32_t n_kv_he
  * angles formed in fp64 on the host. */
 pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void* out, pic_stream_t stream);
 
+/* ------------------------------------------------------------------ batched calls on device-resident lengths
+ * The steps of one decode (or append) step of a batch whose page tables live on the GPU: every
+ * length, position and table is a DEVICE array, nothing is read on the host and nothing is
+ * allocated, so the calls can be captured in a CUDA graph and replayed with other lengths.
+ *
+ * A batch: request r has kv_len[r] keys in its own pages -- block_table[r][0..] of
+ * [n_reqs][table_stride] int32 block ids -- and its rows (queries) are rows
+ * [row_start[r], row_start[r + 1]) of q and out, the last ones of the request: row i of m is at
+ * position first + kv_len[r] - m + i, where `first` is the position of the request's first page
+ * (the prefix length of pic_op_attention_prefix, else 0). A request may have no rows.
+ * Pages: without page_pos page p holds positions first + 16 p ... With page_pos
+ * ([n_reqs][table_stride], absolute position of each page's row 0, ascending) a page may hold
+ * fewer than 16 rows (the ragged tails of linked chunks), up to the next page's position, and
+ * n_pages [n_reqs] counts the pages; page_pos and n_pages come together. Entries past a
+ * request's pages are not read.
+ *
+ * The host checks shapes, pointers and alignment (16 bytes; scratch 256). What only the device
+ * sees is checked there: a request whose lengths do not fit together is skipped (its rows of out
+ * stay as they were), a page whose block lies outside the pool counts as empty, a position
+ * outside the RoPE table is skipped; pic_sync then reports PIC_ERR_INVALID_ARG once. No such
+ * value makes a kernel read or write out of bounds. The RoPE table must hold pure rotations by
+ * p times one angle per pair (pic_op_rope_table): the tensor-core kernel composes the angle of a
+ * key from those of its page's row 0 and of its row within the page.
+ * head_dim is 64 or 128, at most 16 query heads share a KV head (PIC_ERR_UNSUPPORTED beyond).
+ * Calls on several streams at once need scratch of their own each. */
+
+/* Block tables and slot maps of the next step: request r appends new_len[r] >= 0 rows to its
+ * kv_len[r]. Rows go to the free places of its last page, then to new blocks: free_blocks
+ * (n_free ids) from entry *free_used on (0 when free_used is NULL), in request order, within a
+ * request in position order. block_table (and page_pos, when given) get the new pages' entries in
+ * place. Outputs: kv_len_out, n_pages_out [n_reqs]; row_start [n_reqs + 1]; row_pos, row_slot
+ * [max_rows]: position and block * 16 + row of every new row in request order, 0 and -1 in the
+ * places behind the last one; counts [3]: rows, entries of free_blocks used so far (*free_used
+ * included), 0. kv_len_out may be kv_len, n_pages_out n_pages, and free_used &counts[1] (a
+ * captured loop advances them in place); other overlaps are not allowed. All or nothing: with
+ * too few free blocks (pic_sync: PIC_ERR_OUT_OF_BLOCKS), a table row or max_rows too short
+ * (PIC_ERR_CAPACITY) or lengths that do not fit together (PIC_ERR_INVALID_ARG) no table changes,
+ * the lengths come out as they went in, there are no rows, and counts[2] is not 0.
+ * At most 12288 requests (PIC_ERR_CAPACITY). One launch. */
+pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int32_t* new_len, int32_t* block_table,
+                               int32_t table_stride, int32_t* page_pos, const int32_t* n_pages,
+                               const int32_t* free_blocks, int32_t n_free, const int32_t* free_used, int32_t first,
+                               int32_t max_rows, int32_t* kv_len_out, int32_t* n_pages_out, int32_t* row_start,
+                               int32_t* row_pos, int32_t* row_slot, int32_t* counts, pic_stream_t stream);
+
+/* Per-head norms of q and k, the rotation of q, and the K/V rows into their pages, in one pass
+ * over qkv: fp32 rows of qkv_stride floats (>= (n_heads + 2 n_kv_heads) head_dim, a multiple of
+ * 4), Q heads, K heads, V heads. For each row t: q and k heads divided by their root mean square
+ * (sqrt(mean(x^2) + eps) over the head) times q_gain / k_gain ([head_dim], NULL: no norm);
+ * q_out[t][h] = RoPE(q, row_pos[t]) in fp16 for bf16 pools, fp32 for fp32 pools; k (before RoPE)
+ * and v go to slot row_slot[t] of one layer of the pools. A row with row_slot -1 is padding:
+ * nothing of it is read or written. Slots must be distinct. Values bound for fp16 operands are
+ * checked against fp16's range as everywhere (PIC_ERR_RANGE from pic_sync). */
+pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                               const float* qkv, int64_t qkv_stride, const float* q_gain, const float* k_gain,
+                               float eps, const int32_t* row_pos, const int32_t* row_slot, const void* rope_cs,
+                               int32_t rope_positions, void* q_out, void* k_layer, void* v_layer, int32_t pool_blocks,
+                               pic_stream_t stream);
+
+/* Scratch of the two attention calls below; prefix_len 0 for pic_op_attention_window. 0 for
+ * shapes they refuse. The scratch need not be initialised and is free again when the call's work
+ * is done. */
+size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_reqs, int32_t n_heads,
+                                            int32_t n_kv_heads, int32_t head_dim, int32_t prefix_len);
+
+/* Attention of a batch with a sliding window and a few first tokens that stay visible: row at
+ * position p sees key u of its request when u <= p and (u > p - window or u < sinks); window 0:
+ * every key up to p. out[t][h] = softmax_u(q[t][h] . RoPE(K[u][g]) / sqrt(head_dim)) V[u][g],
+ * g = h / (n_heads / n_kv_heads). q: [T][n_heads][head_dim], rotated (pic_op_qk_norm_rope), fp16
+ * for bf16 pools, fp32 for fp32 pools; out likewise. Pages that no row sees are not read. Rows
+ * from row_start[n_reqs] on stay as they were. */
+pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   const void* q, const int32_t* row_start, int32_t n_reqs, const int32_t* kv_len,
+                                   const int32_t* block_table, int32_t table_stride, const int32_t* page_pos,
+                                   const int32_t* n_pages, int32_t window, int32_t sinks, const void* k_layer,
+                                   const void* v_layer, int32_t pool_blocks, const void* rope_cs,
+                                   int32_t rope_positions, void* out, void* scratch, size_t scratch_bytes,
+                                   pic_stream_t stream);
+
+/* Attention of a batch behind one shared prefix: positions [0, prefix_len) are the pages
+ * prefix_blocks [prefix_pages] (device; prefix_pos: their positions, or NULL for 16 p), seen by
+ * every row; each request's own pages follow at position prefix_len, seen causally. The prefix is
+ * attended to by the rows of the whole batch together -- its pages are read once for all requests
+ * (once per 256 rows x query heads of a KV head) -- and joined with each request's own part.
+ * prefix_len may be 0. q, out, rows and pages as above (kv_len counts own keys only). */
+pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   const void* q, const int32_t* row_start, const int32_t* prefix_blocks,
+                                   const int32_t* prefix_pos, int32_t prefix_pages, int32_t prefix_len, int32_t n_reqs,
+                                   const int32_t* kv_len, const int32_t* block_table, int32_t table_stride,
+                                   const int32_t* page_pos, const int32_t* n_pages, const void* k_layer,
+                                   const void* v_layer, int32_t pool_blocks, const void* rope_cs,
+                                   int32_t rope_positions, void* out, void* scratch, size_t scratch_bytes,
+                                   pic_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

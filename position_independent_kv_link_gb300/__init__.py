@@ -8,12 +8,14 @@ loudly if it has not been built.
 from ._lib import LIB_PATH, PicError, load  # noqa: F401
 
 __all__ = ["LIB_PATH", "PicError", "load", "PicModel", "PicStore", "gemm", "gemm_packed", "pack_weight", "attention",
-           "attention_plan", "rope_table"]
+           "attention_plan", "rope_table", "BatchPages", "BlockTables", "block_tables", "qk_norm_rope",
+           "attention_window", "attention_prefix"]
 
 
 def __getattr__(name):
     if name in ("PicModel", "PicStore", "gemm", "gemm_packed", "pack_weight", "attention", "attention_plan",
-                "rope_table", "LinkResult", "DecodeResult"):
+                "rope_table", "LinkResult", "DecodeResult", "BatchPages", "BlockTables", "block_tables", "qk_norm_rope",
+                "attention_window", "attention_prefix"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

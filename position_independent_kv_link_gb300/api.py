@@ -398,3 +398,185 @@ def attention_plan(dtype: torch.dtype, n_heads: int, n_kv_heads: int, head_dim: 
             continue
         L.check(st)
         return items[:counts[0]].copy(), combs[:counts[1]].copy(), int(counts[2])
+
+
+# ----------------------------------------------------------------------------- batched calls on device-resident lengths
+
+def _need(x: Optional[torch.Tensor], what: str, dtype: torch.dtype, shape, dev) -> Optional[int]:
+    """The address of a contiguous tensor of this type and shape (-1: any length) on `dev`; None for None."""
+    if x is None:
+        return None
+    if x.dtype is not dtype or x.device != dev or not x.is_contiguous() or \
+            len(x.shape) != len(shape) or any(n >= 0 and n != m for n, m in zip(shape, x.shape)):
+        want = "x".join("?" if n < 0 else str(n) for n in shape)
+        raise ValueError(f"{what}: a contiguous {dtype} tensor [{want}] on {dev} is needed, got {x.dtype} "
+                         f"{list(x.shape)} (strides {list(x.stride())}) on {x.device}")
+    return x.data_ptr()
+
+
+def _batch_device(x: torch.Tensor) -> torch.device:
+    if not x.is_cuda:
+        raise ValueError(f"device tensors are needed, got one on {x.device}")
+    return x.device
+
+
+def _batch_stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return stream.cuda_stream
+
+
+def _call(dev: torch.device, f, *args):
+    """f(*args) with `dev` current, its status checked."""
+    if torch.cuda.current_device() == dev.index:
+        L.check(f(*args))
+    else:
+        with torch.cuda.device(dev):
+            L.check(f(*args))
+
+
+class BatchPages:
+    """The pages of a batch of requests, all device int32: kv_len [n], block_table [n, stride], and, for pages with
+    fewer than 16 rows (linked chunks), page_pos [n, stride] with n_pages [n]."""
+
+    __slots__ = ("kv_len", "block_table", "page_pos", "n_pages")
+
+    def __init__(self, kv_len: torch.Tensor, block_table: torch.Tensor, page_pos: Optional[torch.Tensor] = None,
+                 n_pages: Optional[torch.Tensor] = None):
+        self.kv_len, self.block_table, self.page_pos, self.n_pages = kv_len, block_table, page_pos, n_pages
+
+    def _args(self, dev):
+        n = self.kv_len.shape[0]
+        i32 = torch.int32
+        kv = _need(self.kv_len, "kv_len", i32, (n,), dev)
+        table = _need(self.block_table, "block_table", i32, (n, -1), dev)
+        stride = self.block_table.shape[1]
+        return n, (kv, table, stride, _need(self.page_pos, "page_pos", i32, (n, stride), dev),
+                   _need(self.n_pages, "n_pages", i32, (n,), dev))
+
+
+class BlockTables:
+    """Result of block_tables: device int32 tensors."""
+
+    __slots__ = ("kv_len", "n_pages", "row_start", "row_pos", "row_slot", "counts")
+
+    def __init__(self, kv_len, n_pages, row_start, row_pos, row_slot, counts):
+        self.kv_len = kv_len          # [n]
+        self.n_pages = n_pages        # [n]
+        self.row_start = row_start    # [n + 1]
+        self.row_pos = row_pos        # [max_rows], 0 behind the last row
+        self.row_slot = row_slot      # [max_rows], -1 behind the last row
+        self.counts = counts          # [3]: rows, entries of free_blocks used, 0 (not 0: nothing was done)
+
+
+def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_blocks: torch.Tensor,
+                 max_rows: int, page_pos: Optional[torch.Tensor] = None, n_pages: Optional[torch.Tensor] = None,
+                 free_used: Optional[torch.Tensor] = None, first: int = 0, out: Optional[BlockTables] = None,
+                 stream=None) -> BlockTables:
+    """Block tables and slot maps of the next step, on the GPU (pic_op_block_tables): request r appends new_len[r]
+    rows to its kv_len[r]; new pages come from free_blocks (from entry free_used[0] on) and are entered in
+    block_table (and page_pos) in place. `out`: tensors to write (out.kv_len may be kv_len, out.n_pages n_pages,
+    and free_used out.counts[1:2])."""
+    dev = _batch_device(kv_len)
+    n, i32 = kv_len.shape[0], torch.int32
+    if out is None:
+        buf = torch.empty(3 * n + 4 + 2 * max_rows, dtype=i32, device=dev)
+        out = BlockTables(*buf.split([n, n, n + 1, max_rows, max_rows, 3]))
+    stride = block_table.shape[1] if block_table.dim() == 2 else -1
+    _call(dev, L.load().pic_op_block_tables, n, _need(kv_len, "kv_len", i32, (n,), dev),
+          _need(new_len, "new_len", i32, (n,), dev), _need(block_table, "block_table", i32, (n, stride), dev), stride,
+          _need(page_pos, "page_pos", i32, (n, stride), dev), _need(n_pages, "n_pages", i32, (n,), dev),
+          _need(free_blocks, "free_blocks", i32, (-1,), dev), free_blocks.shape[0],
+          _need(free_used, "free_used", i32, (1,), dev), first, max_rows, _need(out.kv_len, "out.kv_len", i32, (n,), dev),
+          _need(out.n_pages, "out.n_pages", i32, (n,), dev), _need(out.row_start, "out.row_start", i32, (n + 1,), dev),
+          _need(out.row_pos, "out.row_pos", i32, (max_rows,), dev),
+          _need(out.row_slot, "out.row_slot", i32, (max_rows,), dev), _need(out.counts, "out.counts", i32, (3,), dev),
+          _batch_stream(stream, dev))
+    return out
+
+
+def _pool_args(k_layer, v_layer, rope, dev):
+    if k_layer.dim() != 4 or k_layer.shape[2] != BLOCK:
+        raise ValueError(f"a pool layer is [blocks, n_kv_heads, 16, head_dim], got {list(k_layer.shape)}")
+    nb, G, _, D = k_layer.shape
+    t = k_layer.dtype
+    dt = _dtype_code(t)
+    return (nb, G, D, dt, torch.float16 if dt == L.PIC_BF16 else torch.float32,
+            _need(k_layer, "k_layer", t, (nb, G, BLOCK, D), dev), _need(v_layer, "v_layer", t, (nb, G, BLOCK, D), dev),
+            _need(rope, "rope", torch.float32, (-1, D // 2, 2), dev))
+
+
+def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torch.Tensor, row_slot: torch.Tensor,
+                 rope: torch.Tensor, k_layer: torch.Tensor, v_layer: torch.Tensor, q_gain: Optional[torch.Tensor] = None,
+                 k_gain: Optional[torch.Tensor] = None, eps: float = 1e-5, q_out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Per-head norms of q and k, q rotated, K (unrotated) and V rows into their pages (pic_op_qk_norm_rope).
+
+    qkv: fp32 [T, >= (n_heads + 2 n_kv_heads) head_dim], rows contiguous. Returns q [T, n_heads, head_dim], fp16 for
+    bf16 pools, fp32 for fp32 pools; rows with row_slot -1 are left alone."""
+    dev = _batch_device(qkv)
+    nb, G, D, dt, act, kp, vp, rp = _pool_args(k_layer, v_layer, rope, dev)
+    if qkv.dim() != 2 or qkv.dtype is not torch.float32 or qkv.stride(1) != 1 or \
+            qkv.shape[1] < (n_heads + 2 * n_kv_heads) * D or G != n_kv_heads:
+        raise ValueError(f"qkv: fp32 rows of at least {(n_heads + 2 * n_kv_heads) * D} values for pools of {G} KV heads "
+                         f"are needed, got {qkv.dtype} {list(qkv.shape)}")
+    T = qkv.shape[0]
+    if q_out is None:
+        q_out = torch.empty((T, n_heads, D), dtype=act, device=dev)
+    _call(dev, L.load().pic_op_qk_norm_rope, dt, T, n_heads, n_kv_heads, D, qkv.data_ptr(),
+          qkv.stride(0) if T > 1 else max(qkv.stride(0), qkv.shape[1]),
+          _need(q_gain, "q_gain", torch.float32, (D,), dev), _need(k_gain, "k_gain", torch.float32, (D,), dev), eps,
+          _need(row_pos, "row_pos", torch.int32, (T,), dev), _need(row_slot, "row_slot", torch.int32, (T,), dev), rp,
+          rope.shape[0], _need(q_out, "q_out", act, (T, n_heads, D), dev), kp, vp, nb, _batch_stream(stream, dev))
+    return q_out
+
+
+def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len):
+    dev = _batch_device(q)
+    nb, G, D, dt, act, kp, vp, rp = _pool_args(k_layer, v_layer, rope, dev)
+    if q.dim() != 3:
+        raise ValueError(f"q is [rows, n_heads, head_dim], got {list(q.shape)}")
+    T, H = q.shape[0], q.shape[1]
+    qp = _need(q, "q", act, (T, H, D), dev)
+    n, pg = pages._args(dev)
+    lib = L.load()
+    if out is None:
+        out = torch.empty((T, H, D), dtype=act, device=dev)
+    if scratch is None:
+        with torch.cuda.device(dev):
+            nbytes = lib.pic_op_attention_batch_scratch_bytes(dt, T, n, H, G, D, prefix_len)
+        scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    tail = (kp, vp, nb, rp, rope.shape[0], _need(out, "out", act, (T, H, D), dev),
+            _need(scratch, "scratch", torch.uint8, (-1,), dev), scratch.shape[0])
+    return dev, lib, out, (dt, T, H, G, D, qp, _need(row_start, "row_start", torch.int32, (n + 1,), dev)), n, pg, tail
+
+
+def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages, k_layer: torch.Tensor,
+                     v_layer: torch.Tensor, rope: torch.Tensor, window: int, sinks: int = 0,
+                     out: Optional[torch.Tensor] = None, scratch: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of a batch over its pages with a sliding window and `sinks` first tokens that stay visible
+    (pic_op_attention_window). q: rotated [T, H, D], fp16 for bf16 pools, fp32 for fp32 pools; so is the result. Rows
+    that belong to no request are left alone (uninitialised unless `out` is given). Buffers made here belong to
+    the current stream; with another `stream`, pass `out` and `scratch`."""
+    dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 0)
+    _call(dev, lib.pic_op_attention_window, *head, n, *pg, window, sinks, *tail, _batch_stream(stream, dev))
+    return out
+
+
+def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: torch.Tensor, prefix_len: int,
+                     pages: BatchPages, k_layer: torch.Tensor, v_layer: torch.Tensor, rope: torch.Tensor,
+                     prefix_pos: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     scratch: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of a batch whose requests share the prefix_len first positions (pic_op_attention_prefix): the pages
+    prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
+    `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
+    dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
+                                                        prefix_len)
+    pb = _need(prefix_blocks, "prefix_blocks", torch.int32, (-1,), dev)
+    n_pre = prefix_blocks.shape[0]
+    _call(dev, lib.pic_op_attention_prefix, *head, pb, _need(prefix_pos, "prefix_pos", torch.int32, (n_pre,), dev), n_pre,
+          prefix_len, n, *pg, *tail, _batch_stream(stream, dev))
+    return out

@@ -1395,7 +1395,8 @@ pic_status pic_sync(pic_store* s, pic_stream_t stream) {
   const pic_status a = attn_check_timeout();
   const pic_status g = tc_check_timeout();
   const pic_status r = rows_check_range();
-  return a != PIC_OK ? a : g != PIC_OK ? g : r;
+  const pic_status b = batch_check_flags();
+  return a != PIC_OK ? a : g != PIC_OK ? g : r != PIC_OK ? r : b;
 }
 
 pic_status pic_debug_raise_device_flag(int32_t which) {

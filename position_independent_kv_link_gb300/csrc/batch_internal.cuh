@@ -1,0 +1,159 @@
+// Shared device side of the batched paged-attention kernels: the plan (batch_plan.h) computed by
+// every CTA for itself, and the arguments of the attention and merge kernels.
+#pragma once
+#include "batch_plan.h"
+#include "pic_internal.h"
+
+namespace pic {
+
+struct BatchHead {        // first 32 bytes of the scratch, written by CTA 0
+  long long U;            // length of the cost axis
+  int n_prefix, n_blocks; // prefix row blocks; all row blocks
+  int pad[4];
+};
+
+struct BatchArgs {
+  BatchView v;
+  int H, D;
+  int n_blocks_max;       // capacity of blocks[]
+  int grid;               // CTAs of the attention kernel (shares of the plan)
+  int part_rows;          // rows of one partial slot
+  const void* q;          // [T][H][D] rotated; fp16 for bf16 pools, fp32 for fp32 pools
+  const void* k_layer;    // [pool_blocks][G][16][D], K unrotated
+  const void* v_layer;
+  const float2* rope_cs;  // [rope_positions][D / 2]
+  void* out;              // [T][H][D], q's type
+  unsigned* flag;         // the device's word of kBatch* bits
+  // scratch
+  BatchHead* head;
+  int* base;              // [n_reqs + 1] row blocks of the requests before
+  BatchBlock* blocks;     // [n_blocks_max]
+  float2* part_ml;        // [2 grid][part_rows] (maximum, sum) in the log2 domain
+  float* part_o;          // [2 grid][part_rows][D] normalized
+  // prefix batches: whole items' results, [2][T][H] (segment 0: the prefix, 1: own pages)
+  float2* seg_ml;
+  float* seg_o;           // [2][T][H][D]
+};
+
+__device__ __forceinline__ void batch_flag(unsigned* flag, unsigned bad) {
+  if (bad) atomicOr(flag, bad);
+}
+
+// Exclusive sum of x over the NT threads; `total` gets the whole sum. sh: NT / 32 + 1 values.
+template <int NT>
+__device__ __forceinline__ long long block_scan(long long x, long long* sh, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = lane < NT / 32 ? sh[lane] : 0, wi = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, wi, o);
+      if (lane >= o) wi += y;
+    }
+    if (lane < NT / 32) sh[lane] = wi - w;
+    if (lane == 31) sh[NT / 32] = wi;
+  }
+  __syncthreads();
+  total = sh[NT / 32];
+  const long long r = sh[warp] + inc - x;
+  __syncthreads();
+  return r;
+}
+
+struct BatchShare {   // one CTA's part of the plan
+  long long U, x0, x1;
+  int first, n_blocks;   // the block holding x0; all blocks
+};
+
+// The CTA's share of the plan. Every thread of the CTA (NT of them) calls it; the blocks that meet
+// the share are in a.blocks afterwards. CTAs whose shares meet the same block write the same
+// values there, and each reads only after its own writes.
+template <int NT>
+__device__ BatchShare plan_batch(const BatchArgs& a, long long* sh, int* sh_first) {
+  const BatchView& v = a.v;
+  const int tid = threadIdx.x, n = v.n_reqs;
+  unsigned bad = 0;
+  const int live = pmax(0, pmin(v.row_start[n], v.T));
+  const int n_pre = v.pre_len > 0 ? pdiv(live, v.rb) : 0;
+  if (tid == 0) *sh_first = 0;
+  // row blocks of the requests
+  const int per_r = pdiv(n, NT), r0 = pmin(tid * per_r, n), r1 = pmin(r0 + per_r, n);
+  long long cnt = 0, total;
+  for (int r = r0; r < r1; ++r) {
+    int row0;
+    cnt += pdiv(request_rows(v, r, row0, bad), v.rb);
+  }
+  long long at = block_scan<NT>(cnt, sh, total);
+  for (int r = r0; r < r1; ++r) {
+    int row0;
+    a.base[r] = (int)at;
+    at += per_r == 1 ? cnt : pdiv(request_rows(v, r, row0, bad), v.rb);
+  }
+  int n_own = (int)total;
+  if (n_own > a.n_blocks_max - n_pre) {   // overlapping row ranges
+    n_own = pmax(0, a.n_blocks_max - n_pre);
+    bad |= kBatchBadLengths;
+  }
+  __syncthreads();
+  const int nb = n_pre + n_own;
+  auto block = [&](int b) {
+    if (b < n_pre) return prefix_block(v, live, b);
+    const int k = b - n_pre;
+    int lo = 0, hi = n - 1;   // the last request with base <= k
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.base[mid] <= k) lo = mid;
+      else hi = mid - 1;
+    }
+    int row0;
+    unsigned ignored = 0;
+    const int m = request_rows(v, lo, row0, ignored);
+    return own_block(v, lo, row0, m, k - a.base[lo]);
+  };
+  const int per_b = pdiv(nb, NT), b0 = pmin(tid * per_b, nb), b1 = pmin(b0 + per_b, nb);
+  long long len = 0;
+  BatchBlock kept{};
+  for (int b = b0; b < b1; ++b) {
+    kept = block(b);
+    len += block_len(v, kept);
+  }
+  BatchShare s;
+  long long cum = block_scan<NT>(len, sh, s.U);
+  s.n_blocks = nb;
+  s.x0 = share(s.U, a.grid, blockIdx.x);
+  s.x1 = share(s.U, a.grid, blockIdx.x + 1);
+  for (int b = b0; b < b1; ++b) {
+    if (per_b > 1) kept = block(b);
+    kept.cum = cum;
+    cum += block_len(v, kept);
+    if (kept.cum < s.x1 && cum > s.x0) a.blocks[b] = kept;
+    if (kept.cum <= s.x0 && cum > s.x0) *sh_first = b;
+  }
+  if (blockIdx.x == 0) {
+    batch_flag(a.flag, bad);
+    if (tid == 0) *a.head = BatchHead{s.U, n_pre, nb, {}};
+  }
+  __syncthreads();
+  s.first = *sh_first;
+  return s;
+}
+
+// Where an item's result goes when its tiles [j0, j1) of nt are done by CTA c: whole items of a
+// batch without prefix straight to out, whole items of a prefix batch to their segment, parts to
+// a slot.
+__device__ __forceinline__ int part_slot(int c, long long start, long long x0) { return start < x0 ? 2 * c : 2 * c + 1; }
+
+void launch_batch_simt(BatchArgs a, int dtype, cudaStream_t st);
+void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st);
+int batch_simt_grid(int dtype, int D);
+void batch_simt_view(BatchView& v);
+
+}  // namespace pic

@@ -1,0 +1,552 @@
+// Batched paged attention over device-resident page tables: a sliding window with a few first
+// tokens that stay visible, and a batch behind one shared prefix.
+//
+//   out[t][h] = sum_u p_u V[u][g] / sum_u p_u,   p_u = exp(q[t][h] . RoPE(K[u][g], pos(u)) / sqrt(D))
+//
+// over the keys u that row t sees; g = h / (H / G). The plan (batch_plan.h) cuts the work evenly
+// over the CTAs; items cut at a share's edge, and the two segments of a prefix batch, are joined by
+// the merge kernel from their normalized sums, maxima and denominators (log-sum-exp), in a fixed
+// order.
+//
+// This file: the fp32 kernel (any head size, fp32 arithmetic, bf16 pools of shapes the tensor-core
+// kernel does not take), the merge kernel and the C entry points.
+#include <mutex>
+
+#include "batch_internal.cuh"
+
+namespace pic {
+
+namespace {
+
+__device__ unsigned g_batch_flag = 0;   // kBatch* bits since the last pic_sync
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;
+constexpr int kRows = 16;             // rows (token x head) of an item
+constexpr int kPages = 4;             // pages of a key tile
+constexpr int kKeys = kPages * kPage;
+
+template <typename T> struct ActOf { using type = float; };
+template <> struct ActOf<__nv_bfloat16> { using type = __half; };
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float4 load4(const __half* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void put4(__half* p, float4 x) {
+  const __half2 a = __floats2half2_rn(x.x, x.y), b = __floats2half2_rn(x.z, x.w);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&a);
+  u.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+template <int D> struct SimtSmem {
+  float q[kRows][D];
+  float k[kKeys][D + 4];              // + 4: rows of neighbouring keys start in different banks
+  float v[kKeys][D];
+  float p[kRows][kKeys];
+  int pos[kKeys];                     // key positions (INT_MAX: no key)
+  PageMeta page[kPages];
+  long long scan[kThreads / 32 + 1];
+  int first;
+};
+
+// 16 threads per row: each has 4 of the tile's 64 scores and D / 16 of the row's output columns.
+// fp32 throughout: 2 D FMA per (row, key) pair bound it where rows are many, the pool's bytes
+// where they are few (two to four CTAs per SM hide the loads' latency).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_constant__ BatchArgs a) {
+  using A = typename ActOf<T>::type;
+  extern __shared__ __align__(16) uint8_t raw[];
+  SimtSmem<D>& s = *reinterpret_cast<SimtSmem<D>*>(raw);
+  const BatchView& v = a.v;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const BatchShare sh = plan_batch<kThreads>(a, s.scan, &s.first);
+  const int tid = threadIdx.x, row = tid >> 4, lane = tid & 15;
+  constexpr int NO = D / 64;          // float4 groups of output columns per thread
+  const float scale = kLog2e * rsqrtf((float)D);
+  unsigned bad = 0;
+  for (int bi = sh.first; bi < sh.n_blocks; ++bi) {
+    const BatchBlock b = a.blocks[bi];
+    if (b.cum >= sh.x1) break;
+    const int nt = block_tiles(v, b), c = tile_cost(v, b);
+    const long long ilen = item_len(v, b);
+    const int tok = row / v.rep, hh = row % v.rep;
+    const bool mine = tok < b.nrows && row < v.rb * v.rep;
+    const int qp = b.req < 0 ? INT_MAX - 1 : b.pos0 + tok;
+    for (int g = 0; g < v.G; ++g) {
+      const long long start = b.cum + g * ilen;
+      const int j0 = tile_lower(v, start, nt, c, sh.x0), j1 = tile_lower(v, start, nt, c, sh.x1);
+      if (j0 >= j1) continue;
+      const size_t head = mine ? (size_t)(b.row0 + tok) * a.H + g * v.rep + hh : 0;
+      const A* q = static_cast<const A*>(a.q) + head * D;
+      for (int i = 0; i < NO; ++i) {
+        float4 x = mine ? load4(q + 4 * lane + 64 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x.x *= scale, x.y *= scale, x.z *= scale, x.w *= scale;
+        *reinterpret_cast<float4*>(&s.q[row][4 * lane + 64 * i]) = x;
+      }
+      float m = -INFINITY, l = 0.f;
+      float4 o[NO] = {};
+      for (int j = j0; j < j1; ++j) {
+        __syncthreads();              // the tile before is used up
+        if (tid < kPages) {
+          const int i = j * kPages + tid;
+          s.page[tid] = i < b.nv ? page_meta(v, b, i, bad) : PageMeta{0, 0, 0};
+        }
+        __syncthreads();
+        // K rotated by its position, V; rows that hold no key are zero
+        const T* kl = static_cast<const T*>(a.k_layer);
+        const T* vl = static_cast<const T*>(a.v_layer);
+        for (int u = tid; u < kKeys * (D / 8); u += kThreads) {
+          const int key = u / (D / 8), i = u % (D / 8) * 4, r = key % kPage;
+          const PageMeta pm = s.page[key / kPage];
+          float4 y1 = make_float4(0.f, 0.f, 0.f, 0.f), y2 = y1, z1 = y1, z2 = y1;
+          if (r < pm.len) {
+            const size_t at = (((size_t)pm.blk * v.G + g) * kPage + r) * D;
+            const float4 x1 = load4(kl + at + i), x2 = load4(kl + at + D / 2 + i);
+            z1 = load4(vl + at + i);
+            z2 = load4(vl + at + D / 2 + i);
+            const float4* f = reinterpret_cast<const float4*>(a.rope_cs + (size_t)(pm.pos + r) * (D / 2) + i);
+            const float4 f0 = f[0], f1 = f[1];
+            y1 = make_float4(x1.x * f0.x - x2.x * f0.y, x1.y * f0.z - x2.y * f0.w, x1.z * f1.x - x2.z * f1.y,
+                             x1.w * f1.z - x2.w * f1.w);
+            y2 = make_float4(x2.x * f0.x + x1.x * f0.y, x2.y * f0.z + x1.y * f0.w, x2.z * f1.x + x1.z * f1.y,
+                             x2.w * f1.z + x1.w * f1.w);
+          }
+          *reinterpret_cast<float4*>(&s.k[key][i]) = y1;
+          *reinterpret_cast<float4*>(&s.k[key][D / 2 + i]) = y2;
+          *reinterpret_cast<float4*>(&s.v[key][i]) = z1;
+          *reinterpret_cast<float4*>(&s.v[key][D / 2 + i]) = z2;
+        }
+        if (tid < kKeys) {
+          const PageMeta pm = s.page[tid / kPage];
+          s.pos[tid] = tid % kPage < pm.len ? pm.pos + tid % kPage : INT_MAX;
+        }
+        __syncthreads();
+        float x[4] = {};
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+          const float4 qv = *reinterpret_cast<const float4*>(&s.q[row][d]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 kv = *reinterpret_cast<const float4*>(&s.k[lane + 16 * e][d]);
+            x[e] += qv.x * kv.x + qv.y * kv.y + qv.z * kv.z + qv.w * kv.w;
+          }
+        }
+        float mx = m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int u = s.pos[lane + 16 * e];
+          const bool seen = b.req < 0 ? u != INT_MAX : sees(v, qp, u);
+          if (!seen) x[e] = -INFINITY;
+          mx = fmaxf(mx, x[e]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d, 16));
+        const float ref = mx == -INFINITY ? 0.f : mx;   // nothing seen so far: every p is 0
+        const float keep = exp2f(m - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp2f(x[e] - ref);
+          s.p[row][lane + 16 * e] = p;
+          sum += p;
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, 16);
+        l = l * keep + sum;
+        m = mx;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) o[i].x *= keep, o[i].y *= keep, o[i].z *= keep, o[i].w *= keep;
+        __syncwarp();                 // a row's p is written and read by one half-warp
+#pragma unroll 8
+        for (int key = 0; key < kKeys; ++key) {
+          const float p = s.p[row][key];
+#pragma unroll
+          for (int i = 0; i < NO; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(&s.v[key][4 * lane + 64 * i]);
+            o[i].x += p * y.x, o[i].y += p * y.y, o[i].z += p * y.z, o[i].w += p * y.w;
+          }
+        }
+      }
+      const bool whole = j0 == 0 && j1 == nt;
+      if (mine) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // NaN stays NaN
+        float* po;
+        float2* pml;
+        if (whole && v.pre_len == 0) {
+          A* dst = static_cast<A*>(a.out) + head * D;
+          for (int i = 0; i < NO; ++i)
+            put4(dst + 4 * lane + 64 * i, make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv));
+        } else {
+          if (whole) {
+            const size_t at = (b.req < 0 ? 0 : (size_t)v.T * a.H) + head;
+            po = a.seg_o + at * D;
+            pml = a.seg_ml + at;
+          } else {
+            const size_t at = (size_t)part_slot(blockIdx.x, start, sh.x0) * a.part_rows + row;
+            po = a.part_o + at * D;
+            pml = a.part_ml + at;
+          }
+          for (int i = 0; i < NO; ++i)
+            put4(po + 4 * lane + 64 * i, make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv));
+          if (lane == 0) *pml = make_float2(m, l);
+        }
+      }
+    }
+  }
+  batch_flag(a.flag, bad);
+}
+
+// Joins what the attention kernel left in parts: one warp per (row, head), D / 32 columns per
+// lane; result = sum_i w_i O_i / sum_i w_i with w_i = l_i 2^(m_i - max). Rows that see no key
+// (sum 0) give zeros. grid (own row blocks, G).
+template <typename A, int D>
+__global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant__ BatchArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const BatchView& v = a.v;
+  const BatchHead hd = *a.head;
+  constexpr int C = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
+  for (int bi = hd.n_prefix + blockIdx.x; bi < hd.n_blocks; bi += gridDim.x) {
+    const BatchBlock b = a.blocks[bi];
+    const int nt = block_tiles(v, b), c = tile_cost(v, b);
+    const long long start = b.cum + g * item_len(v, b);
+    const int c0 = owner(hd.U, a.grid, start), c1 = owner(hd.U, a.grid, tile_place(v, start, c, nt - 1));
+    if (c0 == c1 && v.pre_len == 0) continue;   // the attention kernel wrote out itself
+    for (int rr = warp; rr < b.nrows * v.rep; rr += 8) {
+      const int tok = rr / v.rep, hh = rr % v.rep;
+      const size_t head = (size_t)(b.row0 + tok) * a.H + g * v.rep + hh;
+      float M = -INFINITY, L = 0.f, o[C] = {};
+      auto add = [&](int n, auto&& where) {     // n parts; where(i): index of part i's row, or -1
+        for (int i0 = 0; i0 < n; i0 += 32) {
+          float2 ml = make_float2(-INFINITY, 0.f);
+          const float* src = nullptr;
+          if (i0 + lane < n) src = where(i0 + lane, ml);
+          float mx = ml.x;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          mx = fmaxf(mx, M);
+          const float ref = mx == -INFINITY ? 0.f : mx, keep = exp2f(M - ref);
+          float w = ml.y * exp2f(ml.x - ref), sum = w;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          M = mx;
+          L = L * keep + sum;
+#pragma unroll
+          for (int e = 0; e < C; ++e) o[e] *= keep;
+          const unsigned live = __ballot_sync(0xffffffffu, src != nullptr && ml.y != 0.f);
+          unsigned left = live;
+          while (left) {                        // four parts' rows in flight
+            float x[4][C], ww[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int i = left ? __ffs(left) - 1 : 0;
+              const bool on = left != 0;
+              left &= left - 1;
+              const float* p = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, i));
+              const float wi = __shfl_sync(0xffffffffu, w, i);
+              ww[u] = on ? wi : 0.f;
+#pragma unroll
+              for (int e = 0; e < C; ++e) x[u][e] = on ? p[lane * C + e] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int e = 0; e < C; ++e) o[e] += ww[u] * x[u][e];
+          }
+        }
+      };
+      auto add_item = [&](const BatchBlock& bb, int lrow, int seg) {
+        const int nt_ = block_tiles(v, bb), cc = tile_cost(v, bb);
+        const long long st = bb.cum + g * item_len(v, bb);
+        const int p0 = owner(hd.U, a.grid, st), p1 = owner(hd.U, a.grid, tile_place(v, st, cc, nt_ - 1));
+        if (p0 == p1) {
+          add(1, [&](int, float2& ml) {
+            const size_t at = (size_t)seg * v.T * a.H + head;
+            ml = a.seg_ml[at];
+            return (const float*)(a.seg_o + at * D);
+          });
+        } else {
+          add(p1 - p0 + 1, [&](int i, float2& ml) {
+            const int p = p0 + i;
+            const long long x0 = share(hd.U, a.grid, p), x1 = share(hd.U, a.grid, p + 1);
+            if (tile_lower(v, st, nt_, cc, x0) >= tile_lower(v, st, nt_, cc, x1)) return (const float*)nullptr;
+            const size_t at = (size_t)part_slot(p, st, x0) * a.part_rows + lrow * v.rep + hh;
+            ml = a.part_ml[at];
+            return (const float*)(a.part_o + at * D);
+          });
+        }
+      };
+      if (hd.n_prefix > 0) {
+        const int t = b.row0 + tok;
+        add_item(a.blocks[t / v.rb], t % v.rb, 0);
+      }
+      add_item(b, tok, 1);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      A* dst = static_cast<A*>(a.out) + head * D + lane * C;
+#pragma unroll
+      for (int e = 0; e < C; ++e) dst[e] = from_f<A>(o[e] * inv);
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_simt(const BatchArgs& a, cudaStream_t st) {
+  const int smem = (int)sizeof(SimtSmem<D>);
+  cudaError_t e = cudaFuncSetAttribute(batch_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  batch_simt_kernel<T, D><<<a.grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+int device_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  return n;
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Scratch layout of a call (bytes); `base` null: the size alone.
+size_t layout(BatchArgs& a, char* base) {
+  const BatchView& v = a.v;
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    char* p = base ? base + o : nullptr;
+    o += align256(n);
+    return p;
+  };
+  a.n_blocks_max = v.T / v.rb + v.n_reqs + (v.pre_len > 0 ? v.T / v.rb + 1 : 0);
+  a.part_rows = (int)(((long long)v.T * v.rep < v.mrows) ? (long long)v.T * v.rep : v.mrows);
+  a.head = (BatchHead*)take(sizeof(BatchHead));
+  a.base = (int*)take(((size_t)v.n_reqs + 1) * 4);
+  a.blocks = (BatchBlock*)take((size_t)a.n_blocks_max * sizeof(BatchBlock));
+  const size_t rows = 2 * (size_t)a.grid * a.part_rows;
+  a.part_ml = (float2*)take(rows * sizeof(float2));
+  a.part_o = (float*)take(rows * a.D * 4);
+  if (v.pre_len > 0) {
+    a.seg_ml = (float2*)take(2 * (size_t)v.T * a.H * sizeof(float2));
+    a.seg_o = (float*)take(2 * (size_t)v.T * a.H * a.D * 4);
+  }
+  return o;
+}
+
+bool set_shape(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, int prefix_len) {
+  a.v.T = T;
+  a.v.n_reqs = n_reqs;
+  a.v.G = G;
+  a.v.rep = H / G;
+  a.v.pre_len = prefix_len;
+  a.H = H;
+  a.D = D;
+  batch_simt_view(a.v);
+  a.grid = batch_simt_grid(dtype, D);
+  return true;
+}
+
+bool shape_ok(int dtype, int T, int n_reqs, int H, int G, int D) {
+  return (dtype == PIC_F32 || dtype == PIC_BF16) && T >= 1 && n_reqs >= 1 && G >= 1 && H >= 1 && H % G == 0 &&
+         (D == 64 || D == 128);
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+pic_status run(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, void* scratch, size_t scratch_bytes,
+               cudaStream_t st) {
+  set_shape(a, dtype, T, n_reqs, H, G, D, a.v.pre_len);
+  if (scratch_bytes < layout(a, nullptr)) return fail(PIC_ERR_INVALID_ARG, "attention scratch too small");
+  pic_status e = batch_flag_address(&a.flag);
+  if (e != PIC_OK) return e;
+  layout(a, (char*)scratch);
+  launch_batch_simt(a, dtype, st);
+  PIC_CUDA(cudaGetLastError());
+  launch_batch_merge(a, dtype, st);
+  PIC_CUDA(cudaGetLastError());
+  return PIC_OK;
+}
+
+// What both calls check: the shapes, pointers and their alignment.
+pic_status check_common(int32_t dtype, int32_t T, int32_t n_reqs, int32_t H, int32_t G, int32_t D, const void* q,
+                        const int32_t* row_start, const int32_t* kv_len, const int32_t* block_table,
+                        int32_t table_stride, const int32_t* page_pos, const int32_t* n_pages, const void* k_layer,
+                        const void* v_layer, int32_t pool_blocks, const void* rope_cs, int32_t rope_positions,
+                        void* out, void* scratch) {
+  if (!shape_ok(dtype, T, n_reqs, H, G, D)) return fail(PIC_ERR_INVALID_ARG, "invalid attention shape");
+  if (H / G > kRows) return fail(PIC_ERR_UNSUPPORTED, "more than 16 query heads per KV head");
+  if (!q || !row_start || !kv_len || !block_table || table_stride < 1 || !k_layer || !v_layer || pool_blocks < 1 ||
+      !rope_cs || rope_positions < kPage || !out || !scratch)
+    return fail(PIC_ERR_INVALID_ARG, "invalid attention arguments");
+  if ((page_pos == nullptr) != (n_pages == nullptr))
+    return fail(PIC_ERR_INVALID_ARG, "page_pos and n_pages come together");
+  if (!aligned16(q) || !aligned16(k_layer) || !aligned16(v_layer) || !aligned16(rope_cs) || !aligned16(out) ||
+      ((uintptr_t)scratch & 255))
+    return fail(PIC_ERR_INVALID_ARG, "q, pools, RoPE table and out must be 16-byte aligned, scratch 256-byte aligned");
+  return PIC_OK;
+}
+
+BatchArgs common_args(const void* q, const int32_t* row_start, const int32_t* kv_len, const int32_t* block_table,
+                      int32_t table_stride, const int32_t* page_pos, const int32_t* n_pages, const void* k_layer,
+                      const void* v_layer, int32_t pool_blocks, const void* rope_cs, int32_t rope_positions,
+                      void* out) {
+  BatchArgs a{};
+  a.v.row_start = row_start;
+  a.v.kv_len = kv_len;
+  a.v.block_table = block_table;
+  a.v.stride = table_stride;
+  a.v.page_pos = page_pos;
+  a.v.n_pages = n_pages;
+  a.v.window = INT_MAX;
+  a.v.pool_blocks = pool_blocks;
+  a.v.rope_positions = rope_positions;
+  a.q = q;
+  a.k_layer = k_layer;
+  a.v_layer = v_layer;
+  a.rope_cs = (const float2*)rope_cs;
+  a.out = out;
+  return a;
+}
+
+}  // namespace
+
+void batch_simt_view(BatchView& v) {
+  v.mrows = kRows;
+  v.rb = kRows / v.rep;
+  v.kpages = kPages;
+  v.cost_item = 1;
+  v.cost_full = v.cost_half = 2;
+}
+
+int batch_simt_grid(int dtype, int D) {
+  (void)dtype;
+  return device_sms() * (D == 128 ? 2 : 4);   // resident CTAs by shared memory (84 and 45 KB)
+}
+
+void launch_batch_simt(BatchArgs a, int dtype, cudaStream_t st) {
+  if (dtype == PIC_BF16)
+    a.D == 128 ? launch_simt<__nv_bfloat16, 128>(a, st) : launch_simt<__nv_bfloat16, 64>(a, st);
+  else
+    a.D == 128 ? launch_simt<float, 128>(a, st) : launch_simt<float, 64>(a, st);
+}
+
+void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st) {
+  const int own = a.v.T / a.v.rb + a.v.n_reqs;
+  const dim3 grid(pmin(own, 65535), a.v.G);
+  if (dtype == PIC_BF16) {
+    if (a.D == 128) launch_dependent(batch_merge_kernel<__half, 128>, grid, dim3(256), 0, st, a);
+    else launch_dependent(batch_merge_kernel<__half, 64>, grid, dim3(256), 0, st, a);
+  } else {
+    if (a.D == 128) launch_dependent(batch_merge_kernel<float, 128>, grid, dim3(256), 0, st, a);
+    else launch_dependent(batch_merge_kernel<float, 64>, grid, dim3(256), 0, st, a);
+  }
+}
+
+// The flag word's device address, looked up once per device.
+pic_status batch_flag_address(unsigned** out) {
+  static std::mutex mu;
+  static unsigned* addr[64] = {};
+  int dev = 0;
+  PIC_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(PIC_ERR_UNSUPPORTED, "device index beyond the supported range");
+  std::lock_guard<std::mutex> lock(mu);
+  if (!addr[dev]) {
+    void* p = nullptr;
+    PIC_CUDA(cudaGetSymbolAddress(&p, g_batch_flag));
+    addr[dev] = (unsigned*)p;
+  }
+  *out = addr[dev];
+  return PIC_OK;
+}
+
+pic_status batch_check_flags() {
+  unsigned f = 0;
+  const unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&f, g_batch_flag, sizeof(f));
+  if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("batch flag: ") + cudaGetErrorString(e));
+  if (!f) return PIC_OK;
+  cudaMemcpyToSymbol(g_batch_flag, &zero, sizeof(zero));
+  if (f & kBatchTimeout) return fail(PIC_ERR_DEVICE_TIMEOUT, "the batched attention kernel gave up a bounded wait");
+  // in the order in which the host calls check: what is inconsistent, what does not fit, what is not free
+  if (f & (kBatchBadLengths | kBatchBadBlock | kBatchBadPosition)) {
+    std::string what = "device metadata:";
+    if (f & kBatchBadLengths) what += " lengths that do not fit together (the request was skipped)";
+    if (f & kBatchBadBlock) what += " a block outside the pool (taken as empty)";
+    if (f & kBatchBadPosition) what += " a position outside the RoPE table (skipped)";
+    return fail(PIC_ERR_INVALID_ARG, what);
+  }
+  if (f & kBatchCapacity)
+    return fail(PIC_ERR_CAPACITY, "block tables: a request's pages exceed its table row, or the rows max_rows; nothing changed");
+  return fail(PIC_ERR_OUT_OF_BLOCKS, "block tables: not enough free blocks; nothing changed");
+}
+
+}  // namespace pic
+
+using namespace pic;
+
+extern "C" {
+
+size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_reqs, int32_t n_heads,
+                                            int32_t n_kv_heads, int32_t head_dim, int32_t prefix_len) {
+  if (!shape_ok(dtype, T, n_reqs, n_heads, n_kv_heads, head_dim) || n_heads / n_kv_heads > kRows || prefix_len < 0)
+    return 0;
+  BatchArgs a{};
+  set_shape(a, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, prefix_len);
+  return layout(a, nullptr);
+}
+
+pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   const void* q, const int32_t* row_start, int32_t n_reqs, const int32_t* kv_len,
+                                   const int32_t* block_table, int32_t table_stride, const int32_t* page_pos,
+                                   const int32_t* n_pages, int32_t window, int32_t sinks, const void* k_layer,
+                                   const void* v_layer, int32_t pool_blocks, const void* rope_cs,
+                                   int32_t rope_positions, void* out, void* scratch, size_t scratch_bytes,
+                                   pic_stream_t stream) {
+  pic_status e = check_common(dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, q, row_start, kv_len, block_table,
+                              table_stride, page_pos, n_pages, k_layer, v_layer, pool_blocks, rope_cs, rope_positions,
+                              out, scratch);
+  if (e != PIC_OK) return e;
+  if (window < 0 || sinks < 0) return fail(PIC_ERR_INVALID_ARG, "window and sinks must not be negative");
+  BatchArgs a = common_args(q, row_start, kv_len, block_table, table_stride, page_pos, n_pages, k_layer, v_layer,
+                            pool_blocks, rope_cs, rope_positions, out);
+  a.v.window = window > 0 ? window : INT_MAX;
+  a.v.sinks = sinks;
+  return run(a, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, scratch, scratch_bytes, (cudaStream_t)stream);
+}
+
+pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   const void* q, const int32_t* row_start, const int32_t* prefix_blocks,
+                                   const int32_t* prefix_pos, int32_t prefix_pages, int32_t prefix_len, int32_t n_reqs,
+                                   const int32_t* kv_len, const int32_t* block_table, int32_t table_stride,
+                                   const int32_t* page_pos, const int32_t* n_pages, const void* k_layer,
+                                   const void* v_layer, int32_t pool_blocks, const void* rope_cs,
+                                   int32_t rope_positions, void* out, void* scratch, size_t scratch_bytes,
+                                   pic_stream_t stream) {
+  pic_status e = check_common(dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, q, row_start, kv_len, block_table,
+                              table_stride, page_pos, n_pages, k_layer, v_layer, pool_blocks, rope_cs, rope_positions,
+                              out, scratch);
+  if (e != PIC_OK) return e;
+  if (prefix_len < 0 || prefix_len > rope_positions || (prefix_len > 0 && !prefix_blocks) ||
+      prefix_pages < pdiv(prefix_len, kPage) || (prefix_pages > prefix_len) ||
+      (!prefix_pos && prefix_pages != pdiv(prefix_len, kPage)))
+    return fail(PIC_ERR_INVALID_ARG, "invalid prefix: its pages must hold prefix_len positions of the RoPE table");
+  BatchArgs a = common_args(q, row_start, kv_len, block_table, table_stride, page_pos, n_pages, k_layer, v_layer,
+                            pool_blocks, rope_cs, rope_positions, out);
+  a.v.pre_blocks = prefix_blocks;
+  a.v.pre_pos = prefix_pos;
+  a.v.pre_pages = prefix_pages;
+  a.v.pre_len = prefix_len;
+  return run(a, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, scratch, scratch_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"

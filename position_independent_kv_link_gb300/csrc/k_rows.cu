@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "batch_plan.h"
 #include "pic_internal.h"
 
 namespace pic {
@@ -158,6 +159,76 @@ __global__ void qkv_epilogue_kernel(int H, int G, int D, const float* __restrict
   }
 }
 
+// Per-head norms with the rotation: x of head h of row t, r = 1 / sqrt(mean(x^2) + eps) over the
+// head's D dims (fp32),
+//   q_out[t][h] = RoPE(x r q_gain, pos[t]),   K slot: x r k_gain (unrotated),   V slot: x.
+// D / 4 lanes hold a head, 4 dims each; a dim's partner (+ D/2) is D/8 lanes away. Every byte is
+// read and written once: HBM-bound (a row moves (H + 2G) D x (4 + 2) bytes for bf16 pools). A CTA
+// takes one row, so that the row's table entries and the gains are loaded once per thread, and a
+// thread loads all its heads (kHeadsInFlight) before it uses the first; few rows are split over
+// gridDim.y CTAs by heads. Measured: see the launch.
+template <typename T, typename A, int D>
+__global__ void __launch_bounds__(kRowThreads) qk_norm_rope_kernel(
+    int H, int G, const float* __restrict__ qkv, size_t stride, const float* __restrict__ q_gain,
+    const float* __restrict__ k_gain, float eps, const int* __restrict__ pos, const int* __restrict__ slot,
+    const float2* __restrict__ rope_cs, int rope_positions, A* __restrict__ q_out, T* __restrict__ kl,
+    T* __restrict__ vl, int pool_blocks, unsigned* flag) {
+  constexpr int L = D / 4, kGroups = kRowThreads / L, kHeadsInFlight = 6;
+  const int t = blockIdx.x, lane = threadIdx.x % L, grp = threadIdx.x / L;
+  const int sl = slot[t], p = pos[t];
+  if (sl < 0) return;
+  if (p < 0 || p >= rope_positions || sl >= pool_blocks * kBlock) {
+    if (threadIdx.x == 0) atomicOr(flag, sl >= pool_blocks * kBlock ? kBatchBadBlock : kBatchBadPosition);
+    return;
+  }
+  const int n = H + 2 * G, step = kGroups * gridDim.y;
+  const float* row = qkv + (size_t)t * stride + 4 * lane;
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
+  const float4* cs = reinterpret_cast<const float4*>(rope_cs + (size_t)p * (D / 2) + 4 * (lane % (L / 2)));
+  const float4 c0 = cs[0], c1 = cs[1];
+  const float4 gq = q_gain ? reinterpret_cast<const float4*>(q_gain)[lane] : one;
+  const float4 gk = k_gain ? reinterpret_cast<const float4*>(k_gain)[lane] : one;
+  const size_t at = ((size_t)(sl / kBlock) * G * kBlock + sl % kBlock) * D + 4 * lane;   // + g * kBlock * D
+  for (int h0 = blockIdx.y * kGroups + grp; h0 - grp < n; h0 += step * kHeadsInFlight) {
+    float4 x[kHeadsInFlight];
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int h = h0 + i * step;
+      x[i] = h < n ? __ldcs(reinterpret_cast<const float4*>(row + (size_t)h * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int h = h0 + i * step;
+      float4 y = x[i];
+      const bool is_q = h < H, normed = is_q ? q_gain != nullptr : h < H + G && k_gain != nullptr;
+      float ss = y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (normed) {
+        const float r = rsqrtf(ss / D + eps);
+        const float4 gn = is_q ? gq : gk;
+        y = make_float4(y.x * r * gn.x, y.y * r * gn.y, y.z * r * gn.z, y.w * r * gn.w);
+      }
+      float4 z;   // the partner dims
+      z.x = __shfl_xor_sync(0xffffffffu, y.x, L / 2);
+      z.y = __shfl_xor_sync(0xffffffffu, y.y, L / 2);
+      z.z = __shfl_xor_sync(0xffffffffu, y.z, L / 2);
+      z.w = __shfl_xor_sync(0xffffffffu, y.w, L / 2);
+      if (h >= n) continue;
+      if (is_q) {
+        const float s = lane < L / 2 ? -1.f : 1.f;
+        y = make_float4(y.x * c0.x + s * z.x * c0.y, y.y * c0.z + s * z.y * c0.w, y.z * c1.x + s * z.z * c1.y,
+                        y.w * c1.z + s * z.w * c1.w);
+        store4<A>(q_out + ((size_t)t * H + h) * D + 4 * lane, y);
+      } else {
+        const bool is_k = h < H + G;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) flag_range(outside4(y, is_k ? kKRotMax : kF16Max));
+        store4<T>((is_k ? kl : vl) + at + (size_t)(h - H - (is_k ? 0 : G)) * kBlock * D, y);
+      }
+    }
+  }
+}
+
 // y = RMSNorm(h[t]) * gain (the projection GEMMs have already added into h). Not final:
 // x[t] = y in the model dtype. Final: hidden_out[out_row[t]] = y (fp32) and
 // lm_x[lg_row[t]] = y (model dtype) where those indices are >= 0.
@@ -296,6 +367,31 @@ void launch_qkv_epilogue(int dtype, int T, int H, int G, int D, float* acc, floa
   else
     launch_dependent(qkv_epilogue_kernel<float>, grid, dim3(kRowThreads), 0, st, H, G, D, acc, q, slot, (float*)k_layer,
                                                              (float*)v_layer, pos, rope_cs, nullptr);
+}
+
+void launch_qk_norm_rope(int dtype, int T, int H, int G, int D, const float* qkv, size_t stride, const float* q_gain,
+                         const float* k_gain, float eps, const int* pos, const int* slot, const float2* rope_cs,
+                         int rope_positions, void* q_out, void* k_layer, void* v_layer, int pool_blocks,
+                         unsigned* flag, cudaStream_t st) {
+  const int groups = kRowThreads / (D / 4), per = (H + 2 * G + groups - 1) / groups;   // heads of a thread, one CTA a row
+  const int split = std::max(1, std::min(per, 1024 / T));
+  const dim3 grid(T, split);
+  auto go = [&](auto* k, auto* pool, auto* act) {
+    using P = decltype(pool);
+    using Q = decltype(act);
+    k<<<grid, kRowThreads, 0, st>>>(H, G, qkv, stride, q_gain, k_gain, eps, pos, slot, rope_cs, rope_positions,
+                                    (Q)q_out, (P)k_layer, (P)v_layer, pool_blocks, flag);
+  };
+  __nv_bfloat16* b = nullptr;
+  __half* hf = nullptr;
+  float* f = nullptr;
+  if (dtype == PIC_BF16) {
+    if (D == 128) go(qk_norm_rope_kernel<__nv_bfloat16, __half, 128>, b, hf);
+    else go(qk_norm_rope_kernel<__nv_bfloat16, __half, 64>, b, hf);
+  } else {
+    if (D == 128) go(qk_norm_rope_kernel<float, float, 128>, f, f);
+    else go(qk_norm_rope_kernel<float, float, 64>, f, f);
+  }
 }
 
 namespace {

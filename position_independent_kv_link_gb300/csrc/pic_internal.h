@@ -91,6 +91,14 @@ void launch_rmsnorm_rows(int dtype, int T, int d, const float* h, const float* g
 // act[t][j] = silu(gate) * up (activation type) from the accumulator [T][2F] (gate cols, then
 // up cols).
 void launch_swiglu(int dtype, int T, int F, float* acc, void* act, cudaStream_t st);
+// Rows t with slot[t] >= 0 of qkv [T][stride] (q heads, k heads, v heads): q and k divided by their
+// head's root mean square times the gains (null: as they are), q rotated at pos[t] to q_out
+// [T][H][D] (activation type), k unrotated and v to the page slots (k_rows.cu). flag: the word of
+// kBatch* bits.
+void launch_qk_norm_rope(int dtype, int T, int H, int G, int D, const float* qkv, size_t stride, const float* q_gain,
+                         const float* k_gain, float eps, const int* pos, const int* slot, const float2* rope_cs,
+                         int rope_positions, void* q_out, void* k_layer, void* v_layer, int pool_blocks,
+                         unsigned* flag, cudaStream_t st);
 // n floats at p (and n2 at p2, when given) set to zero, in one launch (a forward kernel:
 // programmatic dependent launch).
 void launch_zero(float* p, size_t n, cudaStream_t st, float* p2 = nullptr, size_t n2 = 0);
@@ -229,6 +237,12 @@ pic_status attention_prepare_tc(AttnArgs& a, int T, int pool_blocks, __half* q16
 void plan_attention(const AttnPlanInput& in, std::vector<AttnItem>& items, std::vector<AttnCombine>& combines,
                     int& n_parts);
 size_t attention_part_bytes(int n_parts, int rep, int D);
+
+// ------------------------------------------------------------------ batched paged attention (k_batch_*.cu)
+// Device word of what the batched kernels met and skipped (batch_plan.h: kBatch* bits), and its
+// report and reset by pic_sync.
+pic_status batch_flag_address(unsigned** out);
+pic_status batch_check_flags();
 
 // ------------------------------------------------------------------ dynamic selection (k_select.cu)
 // One request of a dynamic-selection pass: its query rows [row0, row0 + lq) of the pass's
