@@ -70,20 +70,20 @@ __device__ __forceinline__ long long block_scan(long long x, long long* sh, long
 
 struct BatchShare {   // one CTA's part of the plan
   long long U, x0, x1;
-  int first, n_blocks;   // the block holding x0; all blocks
+  int first, last;       // the blocks that meet it
 };
 
 // The CTA's share of the plan. Every thread of the CTA (NT of them) calls it; the blocks that meet
 // the share are in a.blocks afterwards. CTAs whose shares meet the same block write the same
 // values there, and each reads only after its own writes.
 template <int NT>
-__device__ BatchShare plan_batch(const BatchArgs& a, long long* sh, int* sh_first) {
+__device__ BatchShare plan_batch(const BatchArgs& a, long long* sh, int* sh_ends) {
   const BatchView& v = a.v;
   const int tid = threadIdx.x, n = v.n_reqs;
   unsigned bad = 0;
   const int live = pmax(0, pmin(v.row_start[n], v.T));
   const int n_pre = v.pre_len > 0 ? pdiv(live, v.rb) : 0;
-  if (tid == 0) *sh_first = 0;
+  if (tid == 0) sh_ends[0] = 0, sh_ends[1] = -1;
   // row blocks of the requests
   const int per_r = pdiv(n, NT), r0 = pmin(tid * per_r, n), r1 = pmin(r0 + per_r, n);
   long long cnt = 0, total;
@@ -127,22 +127,25 @@ __device__ BatchShare plan_batch(const BatchArgs& a, long long* sh, int* sh_firs
   }
   BatchShare s;
   long long cum = block_scan<NT>(len, sh, s.U);
-  s.n_blocks = nb;
   s.x0 = share(s.U, a.grid, blockIdx.x);
   s.x1 = share(s.U, a.grid, blockIdx.x + 1);
   for (int b = b0; b < b1; ++b) {
     if (per_b > 1) kept = block(b);
     kept.cum = cum;
     cum += block_len(v, kept);
-    if (kept.cum < s.x1 && cum > s.x0) a.blocks[b] = kept;
-    if (kept.cum <= s.x0 && cum > s.x0) *sh_first = b;
+    if (kept.cum < s.x1 && cum > s.x0) {
+      a.blocks[b] = kept;
+      if (kept.cum <= s.x0) sh_ends[0] = b;
+      if (cum >= s.x1) sh_ends[1] = b;
+    }
   }
   if (blockIdx.x == 0) {
     batch_flag(a.flag, bad);
     if (tid == 0) *a.head = BatchHead{s.U, n_pre, nb, {}};
   }
   __syncthreads();
-  s.first = *sh_first;
+  s.first = sh_ends[0];
+  s.last = sh_ends[1];
   return s;
 }
 
@@ -151,9 +154,11 @@ __device__ BatchShare plan_batch(const BatchArgs& a, long long* sh, int* sh_firs
 // a slot.
 __device__ __forceinline__ int part_slot(int c, long long start, long long x0) { return start < x0 ? 2 * c : 2 * c + 1; }
 
-void launch_batch_simt(BatchArgs a, int dtype, cudaStream_t st);
+void launch_batch_simt(const BatchArgs& a, cudaStream_t st);
 void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st);
-int batch_simt_grid(int dtype, int D);
+int batch_simt_grid(int D);
 void batch_simt_view(BatchView& v);
+void batch_tc_view(BatchView& v, int D);
+pic_status launch_batch_tc(const BatchArgs& a, cudaStream_t st);
 
 }  // namespace pic

@@ -59,7 +59,7 @@ struct BatchBlock {        // one row block, 48 bytes
   int row0, nrows;         // rows of q / out
   int pos0;                // position of row 0 (own blocks)
   int sp, wp, nv, np;      // page list: [0, sp) and [wp, wp + nv - sp) of the request's np pages
-  int pad[2];
+  int pad[2];              // 48 bytes
 };
 
 PIC_HD int pdiv(int a, int b) { return (a + b - 1) / b; }
@@ -164,7 +164,8 @@ PIC_HD long long tile_place(const BatchView& v, long long start, int c, int j) {
 }
 
 struct PageMeta {
-  int blk, pos, len;   // block, position of row 0, rows holding a key (0: the page is skipped)
+  int blk, pos;        // block, position of row 0
+  unsigned rows;       // bit r: row r holds a key that some row of the block sees (0: the page is skipped)
 };
 // Page `i` of block b's page list (0 <= i < b.nv).
 PIC_HD PageMeta page_meta(const BatchView& v, const BatchBlock& b, int i, unsigned& bad) {
@@ -182,16 +183,26 @@ PIC_HD PageMeta page_meta(const BatchView& v, const BatchBlock& b, int i, unsign
     m.pos = v.page_pos ? v.page_pos[at + p] : first + kPage * p;
     end = v.page_pos && p + 1 < b.np ? v.page_pos[at + p + 1] : first + v.kv_len[b.req];
   }
-  m.len = m.pos >= 0 && end > m.pos ? pmin(kPage, end - m.pos) : 0;
-  if (m.pos < 0 || m.pos > v.rope_positions - m.len) {
+  int len = m.pos >= 0 && end > m.pos ? pmin(kPage, end - m.pos) : 0;
+  if (m.pos < 0 || m.pos > v.rope_positions - len) {
     bad |= kBatchBadPosition;
     m.pos = 0;
-    m.len = 0;
+    len = 0;
   }
   if (m.blk < 0 || m.blk >= v.pool_blocks) {
-    if (m.len > 0) bad |= kBatchBadBlock;
+    if (len > 0) bad |= kBatchBadBlock;
     m.blk = 0;
-    m.len = 0;
+    len = 0;
+  }
+  if (b.req >= 0 && len > 0) {
+    len = pmax(0, pmin(len, b.pos0 + b.nrows - m.pos));      // keys after the block's last row
+    m.rows = (1u << len) - 1u;
+    // keys between the sinks and the first row's window
+    const int lo = b.pos0 - v.window + 1;
+    const int r0 = pmax(0, pmin(len, v.sinks - m.pos)), r1 = pmax(r0, lo > m.pos ? pmin(len, lo - m.pos) : 0);
+    m.rows &= ~(((1u << r1) - 1u) ^ ((1u << r0) - 1u));
+  } else {
+    m.rows = (1u << len) - 1u;
   }
   return m;
 }

@@ -58,27 +58,27 @@ template <int D> struct SimtSmem {
   int pos[kKeys];                     // key positions (INT_MAX: no key)
   PageMeta page[kPages];
   long long scan[kThreads / 32 + 1];
-  int first;
+  int ends[2];
 };
 
 // 16 threads per row: each has 4 of the tile's 64 scores and D / 16 of the row's output columns.
 // fp32 throughout: 2 D FMA per (row, key) pair bound it where rows are many, the pool's bytes
 // where they are few (two to four CTAs per SM hide the loads' latency).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_constant__ BatchArgs a) {
-  using A = typename ActOf<T>::type;
+  using T = float;
+  using A = float;
   extern __shared__ __align__(16) uint8_t raw[];
   SimtSmem<D>& s = *reinterpret_cast<SimtSmem<D>*>(raw);
   const BatchView& v = a.v;
   asm volatile("griddepcontrol.launch_dependents;");
-  const BatchShare sh = plan_batch<kThreads>(a, s.scan, &s.first);
+  const BatchShare sh = plan_batch<kThreads>(a, s.scan, s.ends);
   const int tid = threadIdx.x, row = tid >> 4, lane = tid & 15;
   constexpr int NO = D / 64;          // float4 groups of output columns per thread
   const float scale = kLog2e * rsqrtf((float)D);
   unsigned bad = 0;
-  for (int bi = sh.first; bi < sh.n_blocks; ++bi) {
+  for (int bi = sh.first; bi <= sh.last; ++bi) {
     const BatchBlock b = a.blocks[bi];
-    if (b.cum >= sh.x1) break;
     const int nt = block_tiles(v, b), c = tile_cost(v, b);
     const long long ilen = item_len(v, b);
     const int tok = row / v.rep, hh = row % v.rep;
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
           const int key = u / (D / 8), i = u % (D / 8) * 4, r = key % kPage;
           const PageMeta pm = s.page[key / kPage];
           float4 y1 = make_float4(0.f, 0.f, 0.f, 0.f), y2 = y1, z1 = y1, z2 = y1;
-          if (r < pm.len) {
+          if (pm.rows >> r & 1u) {
             const size_t at = (((size_t)pm.blk * v.G + g) * kPage + r) * D;
             const float4 x1 = load4(kl + at + i), x2 = load4(kl + at + D / 2 + i);
             z1 = load4(vl + at + i);
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
         }
         if (tid < kKeys) {
           const PageMeta pm = s.page[tid / kPage];
-          s.pos[tid] = tid % kPage < pm.len ? pm.pos + tid % kPage : INT_MAX;
+          s.pos[tid] = pm.rows >> tid % kPage & 1u ? pm.pos + tid % kPage : INT_MAX;
         }
         __syncthreads();
         float x[4] = {};
@@ -301,12 +301,12 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt(const BatchArgs& a, cudaStream_t st) {
   const int smem = (int)sizeof(SimtSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(batch_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(batch_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  batch_simt_kernel<T, D><<<a.grid, kThreads, smem, st>>>(a);
+  batch_simt_kernel<D><<<a.grid, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -343,7 +343,7 @@ size_t layout(BatchArgs& a, char* base) {
   return o;
 }
 
-bool set_shape(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, int prefix_len) {
+void set_shape(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, int prefix_len) {
   a.v.T = T;
   a.v.n_reqs = n_reqs;
   a.v.G = G;
@@ -351,9 +351,13 @@ bool set_shape(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, 
   a.v.pre_len = prefix_len;
   a.H = H;
   a.D = D;
-  batch_simt_view(a.v);
-  a.grid = batch_simt_grid(dtype, D);
-  return true;
+  if (dtype == PIC_BF16) {
+    batch_tc_view(a.v, D);
+    a.grid = device_sms();
+  } else {
+    batch_simt_view(a.v);
+    a.grid = batch_simt_grid(D);
+  }
 }
 
 bool shape_ok(int dtype, int T, int n_reqs, int H, int G, int D) {
@@ -370,8 +374,13 @@ pic_status run(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, 
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
   layout(a, (char*)scratch);
-  launch_batch_simt(a, dtype, st);
-  PIC_CUDA(cudaGetLastError());
+  if (dtype == PIC_BF16) {
+    e = launch_batch_tc(a, st);
+    if (e != PIC_OK) return e;
+  } else {
+    launch_batch_simt(a, st);
+    PIC_CUDA(cudaGetLastError());
+  }
   launch_batch_merge(a, dtype, st);
   PIC_CUDA(cudaGetLastError());
   return PIC_OK;
@@ -428,16 +437,12 @@ void batch_simt_view(BatchView& v) {
   v.cost_full = v.cost_half = 2;
 }
 
-int batch_simt_grid(int dtype, int D) {
-  (void)dtype;
+int batch_simt_grid(int D) {
   return device_sms() * (D == 128 ? 2 : 4);   // resident CTAs by shared memory (84 and 45 KB)
 }
 
-void launch_batch_simt(BatchArgs a, int dtype, cudaStream_t st) {
-  if (dtype == PIC_BF16)
-    a.D == 128 ? launch_simt<__nv_bfloat16, 128>(a, st) : launch_simt<__nv_bfloat16, 64>(a, st);
-  else
-    a.D == 128 ? launch_simt<float, 128>(a, st) : launch_simt<float, 64>(a, st);
+void launch_batch_simt(const BatchArgs& a, cudaStream_t st) {
+  a.D == 128 ? launch_simt<128>(a, st) : launch_simt<64>(a, st);
 }
 
 void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st) {

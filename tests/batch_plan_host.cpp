@@ -11,7 +11,7 @@ extern "C" {
 // ints: T, G, rep, stride, pre_len, pre_pages, window, sinks, pool_blocks, rope_positions, mrows, kpages,
 //       cost_item, cost_full, cost_half, grid, n_reqs
 // items out: [max][12] = cta, req, row0, nrows, pos0, g, j0, j1, tiles, slot (-1: whole), block, sp
-// pages out: [max][5] = block, index, blk, pos, len
+// pages out: [max][5] = block, index, blk, pos, mask of rows
 // counts: items, pages, blocks, flags, owners that disagree with the shares
 int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const int* table, const int* page_pos,
                     const int* n_pages, const int* pre_blocks, const int* pre_pos, int* items, int max_items,
@@ -44,7 +44,7 @@ int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const
       const PageMeta m = page_meta(v, b, j, bad);
       if (np >= max_pages) return 1;
       int* o = pages + 5 * np++;
-      o[0] = (int)i, o[1] = j, o[2] = m.blk, o[3] = m.pos, o[4] = m.len;
+      o[0] = (int)i, o[1] = j, o[2] = m.blk, o[3] = m.pos, o[4] = (int)m.rows;
     }
   }
   for (int c = 0; c < grid && U > 0; ++c) {

@@ -42,6 +42,10 @@ def plan(tmp_path_factory):
     return run
 
 
+def positions(start, mask):
+    return start + np.array([i for i in range(PAGE) if mask >> i & 1], dtype=int)
+
+
 def page_lengths(total, ragged, rng):
     out = []
     while total > 0:
@@ -114,7 +118,7 @@ def test_plan_covers_the_work_once(plan, i):
         pg = pages[pages[:, 0] == blk]
         assert -(-len(pg) // kw.get("kpages", 8)) == e["nt"]
         assert len(set(pg[:, 2].tolist())) == len(pg)                # no page twice
-        have = np.concatenate([np.arange(p, p + n) for _, _, _, p, n in pg.tolist()])
+        have = np.concatenate([positions(p, m) for _, _, _, p, m in pg.tolist()])
         assert len(set(have.tolist())) == len(have)
         if e["req"] < 0:
             assert np.array_equal(np.sort(have), np.arange(b["pre_len"]))
@@ -125,10 +129,8 @@ def test_plan_covers_the_work_once(plan, i):
         qp = e["pos0"] + np.arange(e["nrows"])[:, None]
         u = np.arange(first, first + b["kv"][r])[None]
         need = u[0, ((u <= qp) & ((u > qp - window) | (u < sinks))).any(0)]
-        assert set(need.tolist()) <= set(have.tolist())
-        # and not a page more than holds one of them
-        for _, _, _, p, n in pg.tolist():
-            assert ((need >= p) & (need < p + n)).any()
+        assert np.array_equal(np.sort(have), need)                   # no key that nobody sees
+        assert (pg[:, 4] != 0).all()                                 # and no page without one
     assert (rows_own == 1).all() and (rows_pre == (1 if b["pre_len"] else 0)).all()
 
 
@@ -159,7 +161,7 @@ def test_bad_blocks_and_positions_are_empty_pages(plan):
     _, pages, _, bad = plan(b)
     assert bad == BAD_BLOCK | BAD_POSITION
     assert (pages[:, 2] >= 0).all() and (pages[:, 2] < b["pool"]).all()
-    assert (pages[:, 3] >= 0).all() and (pages[:, 3] + pages[:, 4] <= b["rope"]).all()
+    assert all(0 <= p and (m == 0 or positions(p, m).max() < b["rope"]) for p, m in pages[:, 3:].tolist())
     assert (pages[:, 4] == 0).sum() == 3
 
 
@@ -175,5 +177,6 @@ def test_garbage_tables_stay_in_bounds(plan):
             b[k] = a
         items, pages, _, _ = plan(b, window=50, sinks=4, mrows=16, kpages=4)
         assert (pages[:, 2] >= 0).all() and (pages[:, 2] < b["pool"]).all()
-        assert (pages[:, 3] >= 0).all() and (pages[:, 3] + pages[:, 4] <= b["rope"]).all() and (pages[:, 4] <= 16).all()
+        assert all(0 <= m < 1 << 16 and 0 <= p and (m == 0 or positions(p, m).max() < b["rope"])
+                   for p, m in pages[:, 3:].tolist())
         assert (items[:, 2] >= 0).all() and (items[:, 2] + items[:, 3] <= b["T"]).all()
