@@ -6,10 +6,9 @@
 
 namespace pic {
 
-struct BatchHead {        // first 32 bytes of the scratch, written by CTA 0
-  long long U;            // length of the cost axis
+struct BatchHead {        // written by CTA 0
+  unsigned U, len;        // length of the cost axis, of a share
   int n_prefix, n_blocks; // prefix row blocks; all row blocks
-  int pad[4];
 };
 
 struct BatchArgs {
@@ -40,22 +39,23 @@ __device__ __forceinline__ void batch_flag(unsigned* flag, unsigned bad) {
 }
 
 // Exclusive sum of x over the NT threads; `total` gets the whole sum. sh: NT / 32 + 1 values.
-template <int NT>
-__device__ __forceinline__ long long block_scan(long long x, long long* sh, long long& total) {
+template <int NT, typename T>
+__device__ __noinline__ T block_scan(T x, T* sh, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long inc = x;
+  T inc = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    const T y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) sh[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    long long w = lane < NT / 32 ? sh[lane] : 0, wi = w;
+    const T w = lane < NT / 32 ? sh[lane] : 0;
+    T wi = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, wi, o);
+      const T y = __shfl_up_sync(0xffffffffu, wi, o);
       if (lane >= o) wi += y;
     }
     if (lane < NT / 32) sh[lane] = wi - w;
@@ -63,96 +63,132 @@ __device__ __forceinline__ long long block_scan(long long x, long long* sh, long
   }
   __syncthreads();
   total = sh[NT / 32];
-  const long long r = sh[warp] + inc - x;
+  const T r = sh[warp] + inc - x;
   __syncthreads();
   return r;
 }
 
 struct BatchShare {   // one CTA's part of the plan
-  long long U, x0, x1;
+  unsigned x0, x1;
   int first, last;       // the blocks that meet it
 };
+struct PlanShared {
+  unsigned scan[33];
+  BatchBlock block;      // a copy of the first one
+  int ends[2];
+};
+
+// The kernels' code is kept small: what runs once or seldom is not inlined (an instruction cache
+// that turns over between tiles cost more than all the arithmetic).
+static __device__ __noinline__ int plan_rows(const BatchView& v, int r, int& row0, unsigned& bad) {
+  return request_rows(v, r, row0, bad);
+}
+// Row block b: of the n_pre prefix blocks, else of a request (one: request b - n_pre has one block).
+static __device__ __noinline__ void plan_block(const BatchArgs& a, int b, int n_pre, int live, bool one, BatchBlock& out) {
+  const BatchView& v = a.v;
+  if (b < n_pre) {
+    out = prefix_block(v, live, b);
+    return;
+  }
+  int r = b - n_pre, k = 0;
+  if (!one) {
+    int lo = 0, hi = v.n_reqs - 1;   // the last request with base <= r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.base[mid] <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    k = r - a.base[lo];
+    r = lo;
+  }
+  int row0;
+  unsigned ignored = 0;
+  const int m = plan_rows(v, r, row0, ignored);
+  out = own_block(v, r, row0, m, k);
+}
 
 // The CTA's share of the plan. Every thread of the CTA (NT of them) calls it; the blocks that meet
-// the share are in a.blocks afterwards. CTAs whose shares meet the same block write the same
-// values there, and each reads only after its own writes.
+// the share are in a.blocks afterwards, the first also in sh.block. CTAs whose shares meet the same
+// block write the same values there, and each reads only after its own writes.
 template <int NT>
-__device__ BatchShare plan_batch(const BatchArgs& a, long long* sh, int* sh_ends) {
+__device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared& sh) {
   const BatchView& v = a.v;
   const int tid = threadIdx.x, n = v.n_reqs;
   unsigned bad = 0;
   const int live = pmax(0, pmin(v.row_start[n], v.T));
   const int n_pre = v.pre_len > 0 ? pdiv(live, v.rb) : 0;
-  if (tid == 0) sh_ends[0] = 0, sh_ends[1] = -1;
+  if (tid == 0) sh.ends[0] = 0, sh.ends[1] = -1;
   // row blocks of the requests
   const int per_r = pdiv(n, NT), r0 = pmin(tid * per_r, n), r1 = pmin(r0 + per_r, n);
-  long long cnt = 0, total;
+  unsigned cnt = 0;
+  bool one = true;
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     int row0;
-    cnt += pdiv(request_rows(v, r, row0, bad), v.rb);
+    const int k = pdiv(plan_rows(v, r, row0, bad), v.rb);
+    one = one && k == 1;
+    cnt += k;
   }
-  long long at = block_scan<NT>(cnt, sh, total);
-  for (int r = r0; r < r1; ++r) {
-    int row0;
-    a.base[r] = (int)at;
-    at += per_r == 1 ? cnt : pdiv(request_rows(v, r, row0, bad), v.rb);
-  }
-  int n_own = (int)total;
-  if (n_own > a.n_blocks_max - n_pre) {   // overlapping row ranges
-    n_own = pmax(0, a.n_blocks_max - n_pre);
-    bad |= kBatchBadLengths;
-  }
-  __syncthreads();
-  const int nb = n_pre + n_own;
-  auto block = [&](int b) {
-    if (b < n_pre) return prefix_block(v, live, b);
-    const int k = b - n_pre;
-    int lo = 0, hi = n - 1;   // the last request with base <= k
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.base[mid] <= k) lo = mid;
-      else hi = mid - 1;
+  int n_own = n;
+  one = __syncthreads_and(one);
+  if (!one) {   // some request has no block or several: base[r] blocks come before request r's
+    unsigned total, at = block_scan<NT>(cnt, sh.scan, total);
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+      int row0;
+      unsigned ignored = 0;
+      a.base[r] = (int)at;
+      if (r + 1 < r1) at += pdiv(plan_rows(v, r, row0, ignored), v.rb);
     }
-    int row0;
-    unsigned ignored = 0;
-    const int m = request_rows(v, lo, row0, ignored);
-    return own_block(v, lo, row0, m, k - a.base[lo]);
-  };
+    n_own = (int)total;
+    if (n_own > a.n_blocks_max - n_pre) {   // overlapping row ranges
+      n_own = pmax(0, a.n_blocks_max - n_pre);
+      bad |= kBatchBadLengths;
+    }
+    __syncthreads();
+  }
+  const int nb = n_pre + n_own;
   const int per_b = pdiv(nb, NT), b0 = pmin(tid * per_b, nb), b1 = pmin(b0 + per_b, nb);
-  long long len = 0;
+  unsigned len = 0, U;
   BatchBlock kept{};
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    kept = block(b);
+    plan_block(a, b, n_pre, live, one, kept);
     len += block_len(v, kept);
   }
   BatchShare s;
-  long long cum = block_scan<NT>(len, sh, s.U);
-  s.x0 = share(s.U, a.grid, blockIdx.x);
-  s.x1 = share(s.U, a.grid, blockIdx.x + 1);
+  unsigned cum = block_scan<NT>(len, sh.scan, U);
+  const unsigned part = share_len(U, a.grid);
+  s.x0 = share(U, part, blockIdx.x);
+  s.x1 = share(U, part, blockIdx.x + 1);
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    if (per_b > 1) kept = block(b);
+    if (per_b > 1) plan_block(a, b, n_pre, live, one, kept);
     kept.cum = cum;
     cum += block_len(v, kept);
     if (kept.cum < s.x1 && cum > s.x0) {
       a.blocks[b] = kept;
-      if (kept.cum <= s.x0) sh_ends[0] = b;
-      if (cum >= s.x1) sh_ends[1] = b;
+      if (kept.cum <= s.x0) {
+        sh.ends[0] = b;
+        sh.block = kept;
+      }
+      if (cum >= s.x1) sh.ends[1] = b;
     }
   }
   if (blockIdx.x == 0) {
     batch_flag(a.flag, bad);
-    if (tid == 0) *a.head = BatchHead{s.U, n_pre, nb, {}};
+    if (tid == 0) *a.head = BatchHead{U, part, n_pre, nb};
   }
   __syncthreads();
-  s.first = sh_ends[0];
-  s.last = sh_ends[1];
+  s.first = sh.ends[0];
+  s.last = sh.ends[1];
   return s;
 }
 
 // Where an item's result goes when its tiles [j0, j1) of nt are done by CTA c: whole items of a
 // batch without prefix straight to out, whole items of a prefix batch to their segment, parts to
 // a slot.
-__device__ __forceinline__ int part_slot(int c, long long start, long long x0) { return start < x0 ? 2 * c : 2 * c + 1; }
+__device__ __forceinline__ int part_slot(int c, unsigned start, unsigned x0) { return start < x0 ? 2 * c : 2 * c + 1; }
 
 void launch_batch_simt(const BatchArgs& a, cudaStream_t st);
 void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st);

@@ -7,7 +7,7 @@
 // head): the block's rows x the rep query heads of that KV head against the block's pages, in key
 // tiles of kpages pages. Items lie end to end on a cost axis, blocks in order (prefix blocks
 // first), the KV heads of a block in order, each item cost_item + tiles x tile_cost long. The axis
-// is cut into `grid` equal shares: CTA c takes the key tiles whose start lies in [X_c, X_c+1).
+// is cut into equal shares, one per CTA: CTA c takes the key tiles whose start lies in [X_c, X_c+1).
 // An item cut by a share boundary leaves partial results: CTA c's slot 2c holds its part of an
 // item begun by an earlier CTA, slot 2c + 1 its part of an item it begins and does not finish
 // (at most one of each per CTA, so the slots never collide).
@@ -39,6 +39,7 @@ struct BatchView {
   int window, sinks;        // key u seen from p when u <= p and (u > p - window or u < sinks)
   int pool_blocks, rope_positions;
   int mrows, rb, kpages;    // rows (token x head) of an item, tokens of a row block (mrows / rep), pages of a tile
+  unsigned rep_inv;         // ceil(2^16 / rep): m / rep = m * rep_inv >> 16 for m < 256
   int cost_item;            // cost of an item's start and drain,
   int cost_full, cost_half; // of a key tile, and of one whose item fills no more than half of its rows
 };
@@ -54,11 +55,12 @@ enum : unsigned {
 };
 
 struct BatchBlock {        // one row block, 48 bytes
-  long long cum;           // its first item's place on the cost axis
+  unsigned cum;            // its first item's place on the cost axis
   int req;                 // request, or -1: prefix block
   int row0, nrows;         // rows of q / out
   int pos0;                // position of row 0 (own blocks)
   int sp, wp, nv, np;      // page list: [0, sp) and [wp, wp + nv - sp) of the request's np pages
+  int end;                 // position after the request's last key
   int pad[2];              // 48 bytes
 };
 
@@ -116,7 +118,8 @@ PIC_HD BatchBlock own_block(const BatchView& v, int r, int row0, int m, int k) {
   b.req = r;
   b.row0 = row0 + a;
   b.nrows = pmin(v.rb, m - a);
-  b.pos0 = own_first(v) + v.kv_len[r] - m + a;
+  b.end = own_first(v) + v.kv_len[r];
+  b.pos0 = b.end - m + a;
   b.np = own_pages(v, r);
   const int last = b.pos0 + b.nrows - 1;
   const int pe = a + b.nrows == m ? b.np : page_of(v, r, b.np, last) + 1;
@@ -142,47 +145,64 @@ PIC_HD int block_tiles(const BatchView& v, const BatchBlock& b) { return pdiv(b.
 PIC_HD int tile_cost(const BatchView& v, const BatchBlock& b) {
   return b.nrows * v.rep * 2 <= v.mrows ? v.cost_half : v.cost_full;
 }
-PIC_HD long long item_len(const BatchView& v, const BatchBlock& b) {
-  return v.cost_item + (long long)block_tiles(v, b) * tile_cost(v, b);
+// Lengths on the cost axis: 32 bits hold the whole axis (axis_bound below 2^31 is checked on the host).
+PIC_HD unsigned item_len(const BatchView& v, const BatchBlock& b) {
+  return v.cost_item + (unsigned)block_tiles(v, b) * tile_cost(v, b);
 }
-PIC_HD long long block_len(const BatchView& v, const BatchBlock& b) {
+PIC_HD unsigned block_len(const BatchView& v, const BatchBlock& b) {
   return b.nrows > 0 && b.nv > 0 ? item_len(v, b) * v.G : 0;
 }
-// Left end of CTA c's share of an axis of length U, and the CTA a place x belongs to.
-PIC_HD long long share(long long U, int grid, int c) { return U * c / grid; }
-PIC_HD int owner(long long U, int grid, long long x) { return (int)(((x + 1) * grid - 1) / U); }
+// No plan over tables of this width is longer: every row block as long as its table allows.
+inline double axis_bound(const BatchView& v, double n_own, double n_prefix) {
+  const double item = v.cost_item + (pdiv(v.stride, v.kpages) + 1.0) * v.cost_full;
+  const double pre = v.cost_item + (pdiv(v.pre_pages, v.kpages) + 1.0) * v.cost_full;
+  return (n_own * item + n_prefix * pre) * v.G;
+}
+// Shares of an axis of length U: the length of each (the last ones may be shorter or empty), the left
+// end of CTA c's, the CTA a place x belongs to.
+PIC_HD unsigned share_len(unsigned U, int grid) { return U > (unsigned)grid ? (U + grid - 1) / grid : 1; }
+PIC_HD unsigned share(unsigned U, unsigned len, int c) { return (unsigned)c * len < U ? c * len : U; }
+PIC_HD int owner(unsigned len, unsigned x) { return (int)(x / len); }
 // First tile of an item starting at `start` whose place is >= x (place of tile 0: start; of tile j:
 // start + cost_item + j c), at most nt.
-PIC_HD int tile_lower(const BatchView& v, long long start, int nt, int c, long long x) {
+PIC_HD int tile_lower(const BatchView& v, unsigned start, int nt, int c, unsigned x) {
   if (x <= start) return 0;
-  const long long d = x - start - v.cost_item;
-  const long long j = d <= 0 ? 0 : (d + c - 1) / c;
-  return (int)(j < 1 ? 1 : j > nt ? nt : j);
+  const unsigned d = x - start;
+  const unsigned j = d <= (unsigned)v.cost_item ? 0 : (d - v.cost_item + c - 1) / c;
+  return (int)(j < 1 ? 1 : j > (unsigned)nt ? nt : j);
 }
-PIC_HD long long tile_place(const BatchView& v, long long start, int c, int j) {
-  return j == 0 ? start : start + v.cost_item + (long long)j * c;
+PIC_HD unsigned tile_place(const BatchView& v, unsigned start, int c, int j) {
+  return j == 0 ? start : start + v.cost_item + (unsigned)j * c;
 }
 
 struct PageMeta {
   int blk, pos;        // block, position of row 0
   unsigned rows;       // bit r: row r holds a key that some row of the block sees (0: the page is skipped)
 };
-// Page `i` of block b's page list (0 <= i < b.nv).
-PIC_HD PageMeta page_meta(const BatchView& v, const BatchBlock& b, int i, unsigned& bad) {
-  PageMeta m;
+struct PageRaw {
+  int blk, pos, end;   // block, position of row 0, position after the last row
+};
+// Page `i` of block b's page list (0 <= i < b.nv), as the tables have it.
+PIC_HD PageRaw page_raw(const BatchView& v, const BatchBlock& b, int i) {
+  PageRaw m;
   const int p = i < b.sp ? i : b.wp + i - b.sp;
-  int end;
   if (b.req < 0) {
     m.blk = v.pre_blocks[p];
     m.pos = v.pre_pos ? v.pre_pos[p] : kPage * p;
-    end = v.pre_pos && p + 1 < v.pre_pages ? v.pre_pos[p + 1] : v.pre_len;
+    m.end = v.pre_pos && p + 1 < v.pre_pages ? v.pre_pos[p + 1] : v.pre_len;
   } else {
     const size_t at = (size_t)b.req * v.stride;
     const int first = own_first(v);
     m.blk = v.block_table[at + p];
     m.pos = v.page_pos ? v.page_pos[at + p] : first + kPage * p;
-    end = v.page_pos && p + 1 < b.np ? v.page_pos[at + p + 1] : first + v.kv_len[b.req];
+    m.end = v.page_pos && p + 1 < b.np ? v.page_pos[at + p + 1] : b.end;
   }
+  return m;
+}
+// What of it block b uses, checked.
+PIC_HD PageMeta page_meta(const BatchView& v, const BatchBlock& b, const PageRaw& raw, unsigned& bad) {
+  PageMeta m{raw.blk, raw.pos, 0};
+  const int end = raw.end;
   int len = m.pos >= 0 && end > m.pos ? pmin(kPage, end - m.pos) : 0;
   if (m.pos < 0 || m.pos > v.rope_positions - len) {
     bad |= kBatchBadPosition;

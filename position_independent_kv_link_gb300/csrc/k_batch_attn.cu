@@ -26,30 +26,8 @@ constexpr int kRows = 16;             // rows (token x head) of an item
 constexpr int kPages = 4;             // pages of a key tile
 constexpr int kKeys = kPages * kPage;
 
-template <typename T> struct ActOf { using type = float; };
-template <> struct ActOf<__nv_bfloat16> { using type = __half; };
-
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ float4 load4(const __half* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
 __device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void put4(__half* p, float4 x) {
-  const __half2 a = __floats2half2_rn(x.x, x.y), b = __floats2half2_rn(x.z, x.w);
-  uint2 u;
-  u.x = *reinterpret_cast<const uint32_t*>(&a);
-  u.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
-
 template <int D> struct SimtSmem {
   float q[kRows][D];
   float k[kKeys][D + 4];              // + 4: rows of neighbouring keys start in different banks
@@ -57,8 +35,7 @@ template <int D> struct SimtSmem {
   float p[kRows][kKeys];
   int pos[kKeys];                     // key positions (INT_MAX: no key)
   PageMeta page[kPages];
-  long long scan[kThreads / 32 + 1];
-  int ends[2];
+  PlanShared plan;
 };
 
 // 16 threads per row: each has 4 of the tile's 64 scores and D / 16 of the row's output columns.
@@ -72,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
   SimtSmem<D>& s = *reinterpret_cast<SimtSmem<D>*>(raw);
   const BatchView& v = a.v;
   asm volatile("griddepcontrol.launch_dependents;");
-  const BatchShare sh = plan_batch<kThreads>(a, s.scan, s.ends);
+  const BatchShare sh = plan_batch<kThreads>(a, s.plan);
   const int tid = threadIdx.x, row = tid >> 4, lane = tid & 15;
   constexpr int NO = D / 64;          // float4 groups of output columns per thread
   const float scale = kLog2e * rsqrtf((float)D);
@@ -80,12 +57,12 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
   for (int bi = sh.first; bi <= sh.last; ++bi) {
     const BatchBlock b = a.blocks[bi];
     const int nt = block_tiles(v, b), c = tile_cost(v, b);
-    const long long ilen = item_len(v, b);
-    const int tok = row / v.rep, hh = row % v.rep;
+    const unsigned ilen = item_len(v, b);
+    const int tok = row * v.rep_inv >> 16, hh = row - tok * v.rep;
     const bool mine = tok < b.nrows && row < v.rb * v.rep;
     const int qp = b.req < 0 ? INT_MAX - 1 : b.pos0 + tok;
     for (int g = 0; g < v.G; ++g) {
-      const long long start = b.cum + g * ilen;
+      const unsigned start = b.cum + g * ilen;
       const int j0 = tile_lower(v, start, nt, c, sh.x0), j1 = tile_lower(v, start, nt, c, sh.x1);
       if (j0 >= j1) continue;
       const size_t head = mine ? (size_t)(b.row0 + tok) * a.H + g * v.rep + hh : 0;
@@ -101,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
         __syncthreads();              // the tile before is used up
         if (tid < kPages) {
           const int i = j * kPages + tid;
-          s.page[tid] = i < b.nv ? page_meta(v, b, i, bad) : PageMeta{0, 0, 0};
+          s.page[tid] = i < b.nv ? page_meta(v, b, page_raw(v, b, i), bad) : PageMeta{0, 0, 0};
         }
         __syncthreads();
         // K rotated by its position, V; rows that hold no key are zero
@@ -218,81 +195,77 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
   const BatchHead hd = *a.head;
   constexpr int C = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
+#pragma unroll 1
   for (int bi = hd.n_prefix + blockIdx.x; bi < hd.n_blocks; bi += gridDim.x) {
-    const BatchBlock b = a.blocks[bi];
-    const int nt = block_tiles(v, b), c = tile_cost(v, b);
-    const long long start = b.cum + g * item_len(v, b);
-    const int c0 = owner(hd.U, a.grid, start), c1 = owner(hd.U, a.grid, tile_place(v, start, c, nt - 1));
-    if (c0 == c1 && v.pre_len == 0) continue;   // the attention kernel wrote out itself
-    for (int rr = warp; rr < b.nrows * v.rep; rr += 8) {
-      const int tok = rr / v.rep, hh = rr % v.rep;
-      const size_t head = (size_t)(b.row0 + tok) * a.H + g * v.rep + hh;
+    const BatchBlock own = a.blocks[bi];
+#pragma unroll 1
+    for (int rr = warp; rr < own.nrows * v.rep; rr += 8) {
+      const int tok = rr * v.rep_inv >> 16, hh = rr - tok * v.rep, t = own.row0 + tok;
+      const size_t head = (size_t)t * a.H + g * v.rep + hh;
       float M = -INFINITY, L = 0.f, o[C] = {};
-      auto add = [&](int n, auto&& where) {     // n parts; where(i): index of part i's row, or -1
-        for (int i0 = 0; i0 < n; i0 += 32) {
-          float2 ml = make_float2(-INFINITY, 0.f);
-          const float* src = nullptr;
-          if (i0 + lane < n) src = where(i0 + lane, ml);
-          float mx = ml.x;
+      bool any = false;
+      // the row's item of the prefix, then its own
+#pragma unroll 1
+      for (int seg = hd.n_prefix > 0 ? 0 : 1; seg < 2; ++seg) {
+        const int pb = (unsigned)t / (unsigned)v.rb, lrow = seg ? tok : t - pb * v.rb;
+        const BatchBlock b = seg ? own : a.blocks[pb];
+        const int nt = block_tiles(v, b), c = tile_cost(v, b);
+        const unsigned start = b.cum + g * item_len(v, b);
+        const int c0 = owner(hd.len, start), c1 = owner(hd.len, tile_place(v, start, c, nt - 1));
+        if (c0 == c1 && v.pre_len == 0) break;   // the attention kernel wrote out itself
+        any = true;
+#pragma unroll 1
+        for (int i0 = c0; i0 <= c1; i0 += 32) {   // lane: one part
+          const int p = i0 + lane;
+          size_t at = 0;
+          bool on = p <= c1;
+          const float2* ml = a.part_ml;
+          const float* po = a.part_o;
+          if (c0 == c1) {
+            at = (size_t)seg * v.T * a.H + head;
+            ml = a.seg_ml;
+            po = a.seg_o;
+          } else if (on) {
+            const unsigned x0 = share(hd.U, hd.len, p), x1 = share(hd.U, hd.len, p + 1);
+            on = tile_lower(v, start, nt, c, x0) < tile_lower(v, start, nt, c, x1);
+            at = (size_t)part_slot(p, start, x0) * a.part_rows + lrow * v.rep + hh;
+          }
+          const float2 x = on ? ml[at] : make_float2(-INFINITY, 0.f);
+          float mx = x.x;
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
           mx = fmaxf(mx, M);
-          const float ref = mx == -INFINITY ? 0.f : mx, keep = exp2f(M - ref);
-          float w = ml.y * exp2f(ml.x - ref), sum = w;
+          const float ref = mx == -INFINITY ? 0.f : mx, keep = exp2f(M - ref), w = x.y * exp2f(x.x - ref);
+          float sum = w;
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
           M = mx;
           L = L * keep + sum;
 #pragma unroll
           for (int e = 0; e < C; ++e) o[e] *= keep;
-          const unsigned live = __ballot_sync(0xffffffffu, src != nullptr && ml.y != 0.f);
-          unsigned left = live;
-          while (left) {                        // four parts' rows in flight
-            float x[4][C], ww[4];
+          unsigned left = __ballot_sync(0xffffffffu, on && x.y != 0.f);
+          const unsigned row = (unsigned)at;      // rows of partials: below 2^32 (checked on the host)
+#pragma unroll 1
+          while (left) {                          // eight parts' rows in flight
+            float y[8][C], ww[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 8; ++u) {
               const int i = left ? __ffs(left) - 1 : 0;
-              const bool on = left != 0;
-              left &= left - 1;
-              const float* p = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, i));
               const float wi = __shfl_sync(0xffffffffu, w, i);
-              ww[u] = on ? wi : 0.f;
+              const float* src = po + (size_t)__shfl_sync(0xffffffffu, row, i) * D + lane * C;
+              ww[u] = left ? wi : 0.f;
 #pragma unroll
-              for (int e = 0; e < C; ++e) x[u][e] = on ? p[lane * C + e] : 0.f;
+              for (int e = 0; e < C; ++e) y[u][e] = left ? src[e] : 0.f;
+              left &= left - 1;
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 8; ++u)
 #pragma unroll
-              for (int e = 0; e < C; ++e) o[e] += ww[u] * x[u][e];
+              for (int e = 0; e < C; ++e) o[e] += ww[u] * y[u][e];
           }
         }
-      };
-      auto add_item = [&](const BatchBlock& bb, int lrow, int seg) {
-        const int nt_ = block_tiles(v, bb), cc = tile_cost(v, bb);
-        const long long st = bb.cum + g * item_len(v, bb);
-        const int p0 = owner(hd.U, a.grid, st), p1 = owner(hd.U, a.grid, tile_place(v, st, cc, nt_ - 1));
-        if (p0 == p1) {
-          add(1, [&](int, float2& ml) {
-            const size_t at = (size_t)seg * v.T * a.H + head;
-            ml = a.seg_ml[at];
-            return (const float*)(a.seg_o + at * D);
-          });
-        } else {
-          add(p1 - p0 + 1, [&](int i, float2& ml) {
-            const int p = p0 + i;
-            const long long x0 = share(hd.U, a.grid, p), x1 = share(hd.U, a.grid, p + 1);
-            if (tile_lower(v, st, nt_, cc, x0) >= tile_lower(v, st, nt_, cc, x1)) return (const float*)nullptr;
-            const size_t at = (size_t)part_slot(p, st, x0) * a.part_rows + lrow * v.rep + hh;
-            ml = a.part_ml[at];
-            return (const float*)(a.part_o + at * D);
-          });
-        }
-      };
-      if (hd.n_prefix > 0) {
-        const int t = b.row0 + tok;
-        add_item(a.blocks[t / v.rb], t % v.rb, 0);
       }
-      add_item(b, tok, 1);
+      if (!any) continue;
       const float inv = L == 0.f ? 0.f : 1.f / L;
       A* dst = static_cast<A*>(a.out) + head * D + lane * C;
 #pragma unroll
@@ -370,6 +343,10 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 pic_status run(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, void* scratch, size_t scratch_bytes,
                cudaStream_t st) {
   set_shape(a, dtype, T, n_reqs, H, G, D, a.v.pre_len);
+  const double n_own = T / a.v.rb + (double)n_reqs, n_pre = a.v.pre_len > 0 ? T / a.v.rb + 1.0 : 0.0;
+  if (axis_bound(a.v, n_own, n_pre) >= 2147483647.0) a.v.cost_item = a.v.cost_full = a.v.cost_half = 1;
+  if (axis_bound(a.v, n_own, n_pre) >= 2147483647.0 || 2.0 * T * H >= 4294967295.0)
+    return fail(PIC_ERR_CAPACITY, "batch too large: rows x heads, or row blocks x KV heads x pages of a table row");
   if (scratch_bytes < layout(a, nullptr)) return fail(PIC_ERR_INVALID_ARG, "attention scratch too small");
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
@@ -432,6 +409,7 @@ BatchArgs common_args(const void* q, const int32_t* row_start, const int32_t* kv
 void batch_simt_view(BatchView& v) {
   v.mrows = kRows;
   v.rb = kRows / v.rep;
+  v.rep_inv = (65535 + v.rep) / v.rep;
   v.kpages = kPages;
   v.cost_item = 1;
   v.cost_full = v.cost_half = 2;

@@ -2,21 +2,22 @@
 // heads per KV head, one persistent CTA per SM over its share of the plan (batch_plan.h).
 //
 // An item is a row block x a KV head: MT tiles of 128 MMA rows, row m = token * rep + head of the
-// group. Key tiles of KT keys pass through a ring of stages (K and V released apart: K when its
-// S products have retired, V when its PV products have):
+// group. Its pages come in windows of 32 (one record each) and key tiles of 64 keys, which pass
+// through rings of stages in shared memory:
 //
-//   load warp   per key tile one TMA box per page and 64-dim half of K and of V (16 rows x 128 B,
-//               128-byte swizzled: the MMA operand layout, wherever the page's block lies), one
-//               bulk copy of the RoPE table row of each page's position, the keys' positions for
-//               the mask. Page tables are read a tile ahead.
-//   rotation    4 warps turn K in place in the stage: thread = row of a page x 8 pairs of dims; the
-//               angle of row r of a page at position P is composed from the table rows of P (with
-//               the stage) and of r (in registers), so that a key needs no table row of its own.
-//               bf16 -> fp16, one rounding (the MMA takes Q and K as fp16: 3 bits more than bf16 in
-//               S). Rows that hold no key any row of the block sees are zeroed in K and V.
+//   meta warp   walks the share: reads the page tables a window ahead, writes the windows' records
+//               (item, rows, pages with the rows that hold keys), and asks for V, one TMA box a page
+//               (16 rows x D, 128-byte swizzled, wherever the block lies: a page is one K = 16 step of
+//               the PV product, so pages need not be neighbours).
+//   rotation    copies K of its pages into the stages (cp.async, PD tiles ahead, each thread what it
+//               will rotate itself) and turns it in place: thread = row of a page x 8 pairs of dims; the
+//               angle of row r of a page at position P is composed from the table rows of P (shared
+//               memory, one row a page) and of r (registers), so that a key needs no table row of its
+//               own. bf16 -> fp16, one rounding (Q and K as fp16: 3 bits more than bf16 in S). Rows that
+//               hold no key any row of the block sees are zeroed in K and V.
 //   MMA warps   one issuing thread per MMA tile: O_t += P_t V of key tile j as soon as P_t(j) is
-//               written, S_t of tile j + NBS (Q_t K^T, fp16) into the S buffer that PV has just
-//               read (one thread's MMAs run in order), also across items.
+//               written, S_t of tile j + 2 (Q_t K^T, fp16) into the S buffer that PV has just read (one
+//               thread's MMAs run in order), also across items.
 //   Q warp      copies the items' rows of q into the swizzled A operand (double-buffered for one MMA
 //               tile, else when the item's last S product has retired).
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
@@ -25,11 +26,11 @@
 //               fp32 weights), and the item's result: out, or for parts of items and for prefix
 //               batches the normalized fp32 row with its maximum and sum for the merge.
 //
-// MT = 1, KT = 64, two S buffers, many small stages: few rows, HBM-bound -- what counts is bytes in
-// flight. MT = 2, KT = 128, one S buffer per tile: many rows, MMA-bound -- a K tile is rotated once
-// for 256 rows, and an S product of 128 keys reads its operands from shared memory as fast as it
-// multiplies (64 cycles each), which one of 64 keys does not; the two tiles alternate on the tensor
-// pipe, one's softmax under the other's products.
+// The roles' loops together are kept near the size of the instruction cache: with three times the
+// code every role ran at 8 cycles an instruction (ncu: no_instruction the largest stall).
+//
+// MT = 1, eight rotation warps: few rows, HBM-bound. MT = 2, four: many rows; a K tile is loaded and
+// rotated once for 256 rows.
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
@@ -46,46 +47,65 @@ namespace {
 constexpr float kRescale = 8.f;           // rescale O when the row maximum grows by more than 2^8
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
+constexpr int KT = 64, KP = KT / kPage;   // keys, pages of a tile
+constexpr int NBS = 2;                    // S buffers per MMA tile
+constexpr int WIN = 32, WT = WIN / KP;    // pages, tiles of a window
+constexpr int NWIN = 6;                   // window records
+
 template <int D_, int MT_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
-  static constexpr int KT = MT == 2 ? 128 : 64;       // keys per tile
-  static constexpr int KP = KT / kPage;               // pages per tile
-  static constexpr int NBS = MT == 2 ? 1 : 2;         // S buffers per MMA tile
   static constexpr int NQ = MT == 2 ? 1 : 2;          // Q buffers per MMA tile
-  static constexpr int NH = D / 64;                   // 64-dim halves
-  static constexpr int NST = D == 128 ? (MT == 2 ? 2 : 4) : (MT == 2 ? 4 : 8);
-  static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, CS_ROW = D * 4, CS_BYTES = KP * CS_ROW;
-  static constexpr int W_MMA = 4 * MT, W_LOAD = W_MMA + MT, W_Q = W_LOAD + 1, W_ROT = 4 * MT + 4;
-  static constexpr int THREADS = (W_ROT + 4) * 32;
-  static constexpr int NPOS = 2 * NST;                // slots of key positions (see the load warp)
+  static constexpr int NK = D == 128 ? 4 : 6;         // K stages (and of table rows)
+  static constexpr int NV = NK;                       // V stages
+  static constexpr int PD = NK - 2;                   // K tiles on their way ahead of the one being rotated
+  static constexpr int NR = MT == 2 ? 4 : 8;          // rotation warps
+  static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
+  static constexpr int CH = D / 16, PP = NR * 32 / (16 * CH);   // rotation: threads of a row, pages at once
+  static constexpr int W_MMA = 4 * MT, W_META = W_MMA + MT, W_Q = W_META + 1, W_ROT = MT == 2 ? 12 : 8;
+  static constexpr int THREADS = (W_ROT + NR) * 32;
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;
-  static constexpr int OFF_V = OFF_K + NST * K_BYTES;
-  static constexpr int OFF_CS = OFF_V + NST * K_BYTES;
-  static constexpr int OFF_POS = OFF_CS + NST * CS_BYTES;     // int [NPOS][KT] key positions (INT_MAX: no key)
-  static constexpr int OFF_LIM = OFF_POS + NPOS * KT * 4;     // int2 [NPOS] last key, first key behind the sinks
-  static constexpr int OFF_MASK = OFF_LIM + NPOS * 8;         // uint [NST][KP] rows of each page that hold a key
-  static constexpr int OFF_BAR = (OFF_MASK + NST * KP * 4 + 7) / 8 * 8;
+  static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
+  static constexpr int OFF_V = OFF_K + NK * K_BYTES;          // [NV] [page][64-dim half][16 keys][128 B]
+  static constexpr int OFF_CS = OFF_V + NV * K_BYTES;         // [NK][KP] table rows
+  static constexpr int OFF_REC = OFF_CS + NK * KP * CS_ROW;   // WinRec [NWIN]
+  static constexpr int OFF_PAGE = OFF_REC + NWIN * 48;        // int4 [NWIN][WIN] page of the pool, position, rows
+  static constexpr int OFF_LIM = OFF_PAGE + NWIN * WIN * 16;  // int2 [NWIN][WT] last key, first one behind the sinks
+  static constexpr int OFF_BAR = OFF_LIM + NWIN * WT * 8;
   // barriers
-  static constexpr int B_KFULL = 0, B_VFULL = B_KFULL + NST, B_READY = B_VFULL + NST, B_KEMPTY = B_READY + NST,
-                       B_VEMPTY = B_KEMPTY + NST, B_SFULL = B_VEMPTY + NST, B_PREADY = B_SFULL + MT * NBS,
-                       B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS, B_QEMPTY = B_QFULL + MT * NQ,
-                       B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + MT;
+  static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_KLAND = B_RFREE + NWIN, B_READY = B_KLAND + NK, B_KEMPTY = B_READY + NK,
+                       B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_SFULL = B_VEMPTY + NV,
+                       B_PREADY = B_SFULL + MT * NBS, B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS,
+                       B_QEMPTY = B_QFULL + MT * NQ, B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + MT;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
-  // TMEM columns: O_t at D t, S buffer b of tile t at TM_S + 128 t + KT b
+  static_assert(PD < NWIN, "a record is free before the rotation asks for it");
+  // TMEM columns: O_t at D t, S buffer b of tile t at TM_S + 128 t + 64 b, its P over the first half
   static constexpr uint32_t TM_S = MT * D;
   static constexpr uint32_t TMEM_COLS = MT == 2 ? 512 : 256;
 };
+
+constexpr int kFirst = 1, kLast = 2, kTwo = 4, kEnd = 8, kWhole = 16;
+struct WinRec {           // 48 bytes
+  int flags;              // first / last window of the item's part, the item has rows for MMA tile 1, no more
+                          // windows, the part is the whole item
+  int tiles, req, row0, nrows, pos0, g;
+  int slot;               // partial slot (parts)
+  int pad[4];
+};
+
 // Every waiter of a barrier sees each of its phases before the next can complete (a parity wait
-// cannot tell phase n from n + 2): KFULL (rotation warps): a stage is refilled after KEMPTY, i.e.
-// after the S products that followed READY. VFULL (MMA warps; rotation warps of a tile with empty
-// rows): after VEMPTY, to which every MMA warp arrives once per tile, after its wait for VFULL.
-// READY (MMA warps): needs KFULL. SFULL, PREADY, PVDONE as a ring between MMA thread t and
-// warpgroup t: S(j + NBS) follows PV(j), which waits for all four warps' P(j). QFULL, QEMPTY:
-// between the Q warp and MMA thread t.
+// cannot tell phase n from n + 2). META, RFREE: a record is rewritten only when every warp that
+// reads records has arrived at RFREE for the window before in its slot. KLAND: every rotation thread
+// arrives with its copies of a tile and waits before it asks for the tile NK later. READY (MMA warps), KEMPTY:
+// rotation of tile j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows
+// PV of j; every MMA warp arrives at VEMPTY once per tile, after its wait for VFULL. SFULL, PREADY,
+// PVDONE: a ring between MMA thread t and warpgroup t; S(j + 2) follows PV(j), which waits for all
+// four warps' P(j). QFULL, QEMPTY: between the Q warp and MMA thread t.
+// No wait is for what waits in turn, windows of one tile being the tightest case: record i needs the
+// readers' passage of window i - NWIN and V of tile i - 3, that is the PV products of tile i - 3 - NV.
+// The rotation waits for record i before it turns tile i - PD, with PD < NWIN and PD < NV + 3.
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ unsigned long long gtimer() {
@@ -114,39 +134,43 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(20000u)
       : "memory");
   return ok != 0;
 }
-// false (and the timeout flag) after kWaitLimitNs, or when the CTA has given up
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* flag) {
-  if (mbar_try(bar, parity)) return true;
+// false (and the timeout flag) after kWaitLimitNs, or when the CTA has given up (`abort`: its word in
+// shared memory, 0: wait on). Not inlined: there are some thirty waits.
+__device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, uint32_t abort, unsigned* flag) {
   const unsigned long long t0 = gtimer();
-  for (uint32_t i = 1;; ++i) {
+  for (;;) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort) return false;
-      if (gtimer() - t0 > kWaitLimitNs) {
-        atomicOr(flag, kBatchTimeout);
-        *abort = 1;
-        return false;
-      }
+    uint32_t gone = 0;
+    if (abort) asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
+    if (gone) return false;
+    if (gtimer() - t0 > kWaitLimitNs) {
+      atomicOr(flag, kBatchTimeout);
+      if (abort) asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
+      return false;
     }
   }
 }
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort, unsigned* flag) {
+  return mbar_try(bar, parity) || mbar_wait_on(bar, parity, abort, flag);
 }
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int half, int g, int blk, uint32_t bar) {
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int page, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, "
-      "%5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(half), "r"(g), "r"(blk), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(page), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t at, uint32_t* x) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t* x) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
 }
 // 16-byte chunk c (0..7) of row r of a [rows][128 B] tile, 128-byte swizzle (the TMA and UMMA layout)
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -219,11 +243,29 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  tmem_ld16(taddr, v);
+  tmem_ld16(taddr + 16, v + 16);
+}
+// two fp32 operations at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 struct TcArgs {
-  CUtensorMap kmap, vmap;
+  CUtensorMap vmap;
   BatchArgs b;
 };
 
@@ -232,23 +274,25 @@ struct TcArgs {
 struct Walk {
   BatchBlock b;
   int bi, last, g, nt, c, j0, j1;
-  long long start, ilen, x0, x1;
+  unsigned start, ilen, x0, x1;
   __device__ __forceinline__ void range(const BatchView& v) {
-    j0 = start < x0 ? tile_lower(v, start, nt, c, x0) : 0;
-    j1 = start + ilen > x1 ? tile_lower(v, start, nt, c, x1) : nt;
+    j0 = 0, j1 = nt;
+    if (start < x0) j0 = lower(v, x0);
+    if (start + ilen > x1) j1 = lower(v, x1);
   }
-  __device__ __forceinline__ void load(const BatchArgs& a) {
-    b = a.blocks[bi];
+  __device__ __noinline__ int lower(const BatchView& v, unsigned x) const { return tile_lower(v, start, nt, c, x); }
+  __device__ __forceinline__ void load(const BatchArgs& a, const BatchBlock& from) {
+    b = from;
     nt = block_tiles(a.v, b);
     c = tile_cost(a.v, b);
     ilen = item_len(a.v, b);
   }
   // the first item with tiles of this CTA; false: none
-  __device__ __forceinline__ bool begin(const BatchArgs& a, const BatchShare& s) {
+  __device__ __forceinline__ bool begin(const BatchArgs& a, const BatchShare& s, const BatchBlock& block) {
     x0 = s.x0, x1 = s.x1, bi = s.first, last = s.last;
     if (bi > last) return false;
-    load(a);
-    const long long skip = x0 > b.cum ? (x0 - b.cum) / ilen : 0;
+    load(a, block);
+    const unsigned skip = x0 > b.cum ? (x0 - b.cum) / ilen : 0;
     g = (int)skip;
     start = b.cum + skip * ilen;
     range(a.v);
@@ -258,7 +302,7 @@ struct Walk {
     for (;;) {
       if (++g == a.v.G) {
         if (++bi > last) return false;
-        load(a);
+        load(a, a.blocks[bi]);
         g = 0;
         start = b.cum;
       } else {
@@ -271,44 +315,62 @@ struct Walk {
   }
 };
 
+// Bit i: the row at qp (own keys at or below lo as sinks only) sees key i of two pages (chunk of 32 keys).
+__device__ __forceinline__ unsigned seen_bits(int4 p0, int4 p1, int qp, int lo, int sinks) {
+  auto page = [&](int pos, unsigned rows) {
+    const int up = min(max(qp - pos + 1, 0), 16), from = min(max(lo - pos + 1, 0), 16), sk = min(max(sinks - pos, 0), 16);
+    const unsigned upto = (1u << up) - 1u, old = (1u << from) - 1u, first = (1u << sk) - 1u;
+    return rows & upto & (~old | first);
+  };
+  return page(p0.y, (unsigned)p0.z) | page(p1.y, (unsigned)p1.z) << 16;
+}
+
+// Page i of a block's list as the tables have it (zeros past its end).
+__device__ __noinline__ PageRaw fetch_page(const BatchView& v, const BatchBlock& b, int i) {
+  return i < b.nv ? page_raw(v, b, i) : PageRaw{0, 0, 0};
+}
+
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_constant__ TcArgs ta) {
-  constexpr int D = C::D, MT = C::MT, KT = C::KT, KP = C::KP, NBS = C::NBS, NQ = C::NQ, NH = C::NH, NST = C::NST;
+  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NK = C::NK, NV = C::NV;
   const BatchArgs& a = ta.b;
   const BatchView& v = a.v;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  int* sPos = reinterpret_cast<int*>(sm + C::OFF_POS);
+  WinRec* sRec = reinterpret_cast<WinRec*>(sm + C::OFF_REC);
+  int4* sPage = reinterpret_cast<int4*>(sm + C::OFF_PAGE);
   int2* sLim = reinterpret_cast<int2*>(sm + C::OFF_LIM);
-  unsigned* sMask = reinterpret_cast<unsigned*>(sm + C::OFF_MASK);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
-  auto bar = [&](int i) { return smem_u32(bars + i); };
-  __shared__ long long s_scan[C::THREADS / 32 + 1];
-  __shared__ int s_ends[2];
-  __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
+  const uint32_t base = smem_u32(sm);
+  auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
+  __shared__ PlanShared s_plan;
+  __shared__ uint32_t s_tmem, s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity, &s_abort, a.flag); };
+  const uint32_t abort = smem_u32(&s_abort);
+  auto give_up = [&] { asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory"); };
+  auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity, abort, a.flag); };
+  auto wait_meta = [&](uint32_t w) { return wait(C::B_META + w % NWIN, (w / NWIN) & 1); };
+  auto done_with = [&](uint32_t w) {   // this warp (all its lanes) reads window w's record no more
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::B_RFREE + w % NWIN));
+  };
 
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(bar(C::B_KFULL + i), 1);
-      mbar_init(bar(C::B_VFULL + i), 1);
-      mbar_init(bar(C::B_READY + i), 4);
-      mbar_init(bar(C::B_KEMPTY + i), MT);
-      mbar_init(bar(C::B_VEMPTY + i), MT);
-    }
-    for (int i = 0; i < MT * NBS; ++i) {
-      mbar_init(bar(C::B_SFULL + i), 1);
-      mbar_init(bar(C::B_PREADY + i), 4);
-      mbar_init(bar(C::B_PVDONE + i), 1);
-    }
-    for (int i = 0; i < MT * NQ; ++i) {
-      mbar_init(bar(C::B_QFULL + i), 1);
-      mbar_init(bar(C::B_QEMPTY + i), 1);
-    }
-    for (int t = 0; t < MT; ++t) mbar_init(bar(C::B_DONE + t), 1);
+    auto init = [&](int i, int n, int count) {
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) mbar_init(bar(i + k), count);
+    };
+    init(C::B_META, NWIN, 1);
+    init(C::B_RFREE, NWIN, 4 * MT + MT + 1 + C::NR);
+    init(C::B_KLAND, NK, C::NR * 32);
+    init(C::B_READY, NK, C::NR);
+    init(C::B_KEMPTY, NK, MT);
+    init(C::B_VFULL, NV, 1);
+    init(C::B_VEMPTY, NV, MT);
+    init(C::B_SFULL, MT * NBS, 1);
+    init(C::B_PREADY, MT * NBS, 4);
+    init(C::B_PVDONE, MT * NBS, 1);
+    init(C::B_QFULL, 2 * MT * NQ + MT, 1);   // QFULL, QEMPTY, DONE
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == C::W_MMA) {
@@ -318,81 +380,84 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   }
   asm volatile("griddepcontrol.launch_dependents;");
   fence_before();
-  const BatchShare share_ = plan_batch<C::THREADS>(a, s_scan, s_ends);   // ends with a __syncthreads
+  const BatchShare share_ = plan_batch<C::THREADS>(a, s_plan);   // ends with a __syncthreads
   fence_after();
   const uint32_t tmem = s_tmem;
-  Walk w;
 
   if (warp < 4 * MT) {
     // =============================== softmax: MMA tile t, row m of the item
-    if constexpr (MT == 2) regs_inc<176>();
     const int t = warp >> 2, m = 128 * t + 32 * (warp & 3) + lane;
-    const int tok = m / v.rep, hh = m % v.rep;
+    const int tok = m * v.rep_inv >> 16, hh = m - tok * v.rep;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_o = trow + D * t, t_sb = trow + C::TM_S + 128 * t;
     const float sl = 1.4426950408889634f * rsqrtf((float)D);
-    uint32_t gt = 0, ct = 0;   // key tiles of the CTA, of this MMA tile
-    bool ok = true;
-    for (bool more = w.begin(a, share_); more && ok; more = w.next(a)) {
-      const int n = w.j1 - w.j0;
-      if (w.b.nrows * v.rep <= 128 * t) {   // the item has no rows for this MMA tile
-        gt += n;
-        continue;
+    uint32_t ct = 0;           // key tiles of this MMA tile
+    bool ok = true, mine = false, idle = false;
+    int qp = 0, lo = 0;
+    float mref = 0.f, l = 0.f;
+#pragma unroll 1
+    for (uint32_t win = 0; ok; ++win) {
+      ok = __all_sync(0xffffffffu, wait_meta(win));
+      if (!ok) break;
+      const WinRec& rec = sRec[win % NWIN];
+      const int flags = rec.flags, row0 = rec.row0, g = rec.g, slot = rec.slot, req = rec.req;
+      if (flags & kEnd) break;
+      const int n = t == 1 && !(flags & kTwo) ? 0 : rec.tiles;
+      if (flags & kFirst) {
+        mine = tok < rec.nrows && m < v.rb * v.rep;
+        idle = !__any_sync(0xffffffffu, mine);
+        qp = req < 0 ? INT_MAX - 1 : rec.pos0 + (mine ? tok : 0);
+        lo = req < 0 ? -1 : qp - v.window;   // own keys at or below lo are seen as sinks only
+        mref = -INFINITY;
+        l = 0.f;
       }
-      const bool mine = tok < w.b.nrows && m < v.rb * v.rep;
-      const bool idle = !__any_sync(0xffffffffu, mine);
-      const int qp = w.b.req < 0 ? INT_MAX - 1 : w.b.pos0 + (mine ? tok : 0);
-      const int lo = w.b.req < 0 ? -1 : qp - v.window;   // own keys at or below lo are seen as sinks only
-      float mref = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j, ++gt, ++ct) {
-        const int b = ct % NBS, slot = gt % C::NPOS;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j, ++ct) {
+        const int b = ct % NBS;
         const uint32_t t_s = t_sb + KT * b;
+        const int2 lim = sLim[win % NWIN * WT + j];
+        const bool masked = __any_sync(0xffffffffu, lim.x > qp || lim.y <= lo);
         ok = __all_sync(0xffffffffu, wait(C::B_SFULL + t * NBS + b, (ct / NBS) & 1));
         if (!ok) break;
-        fence_after();
         if (!idle) {
-          const int2 lim = sLim[slot];
+          fence_after();
           float s[KT];
 #pragma unroll
           for (int c = 0; c < KT; c += 16) tmem_ld16(t_s + c, s + c);
           tmem_wait_ld();
-          if (__any_sync(0xffffffffu, lim.x > qp || lim.y <= lo)) {
-            const int4* kp = reinterpret_cast<const int4*>(sPos + slot * KT);
+          if (masked) {
+            const int4* pages = sPage + win % NWIN * WIN + j * KP;
 #pragma unroll
-            for (int i = 0; i < KT / 4; ++i) {
-              const int4 k4 = kp[i];
-              auto out = [&](int u) { return u > qp || (u <= lo && u >= v.sinks); };
-              if (out(k4.x)) s[4 * i] = -INFINITY;
-              if (out(k4.y)) s[4 * i + 1] = -INFINITY;
-              if (out(k4.z)) s[4 * i + 2] = -INFINITY;
-              if (out(k4.w)) s[4 * i + 3] = -INFINITY;
+            for (int c = 0; c < 2; ++c) {
+              const unsigned seen = seen_bits(pages[2 * c], pages[2 * c + 1], qp, lo, v.sinks);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[32 * c + i] = seen >> i & 1u ? s[32 * c + i] : -INFINITY;
             }
           }
-          float m4[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) m4[u] = s[u];
+          float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int i = 4; i < KT; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
           const bool grow = mx > mref + kRescale;
           const float mnew = grow ? mx : mref;
           const float scale = (grow && mref != -INFINITY) ? ex2(mref - mnew) : 1.f;
-          l *= scale;
           mref = mnew;
-          const float mz = mref == -INFINITY ? 0.f : mref;   // nothing seen so far: every s is -inf, p = 0
-          float r4[4] = {0.f, 0.f, 0.f, 0.f};
+          const float mz = mref == -INFINITY ? 0.f : -mref;   // nothing seen so far: every s is -inf, p = 0
+          float2 sum[2] = {make_float2(l * scale, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < KT / 32; ++h) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t pv[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(s[32 * h + 2 * e], sl, -mz)), p1 = ex2(fmaf(s[32 * h + 2 * e + 1], sl, -mz));
-              r4[e & 3] += p0 + p1;
-              pv[e] = pack_bf16x2(p0, p1);
+              float2 p = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), make_float2(sl, sl), make_float2(mz, mz));
+              p.x = ex2(p.x);
+              p.y = ex2(p.y);
+              sum[e & 1] = add2(sum[e & 1], p);
+              pv[e] = pack_bf16x2(p.x, p.y);
             }
-            tmem_st16(t_s + KT / 2 + 16 * h, pv);
+            tmem_st16(t_s + 16 * c, pv);
           }
-          l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
+          l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           if (__any_sync(0xffffffffu, scale != 1.f)) {
             // O holds the item's earlier tiles (a finite earlier maximum): their PVs first
             ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBS + (ct - 1) % NBS, ((ct - 1) / NBS) & 1));
@@ -416,39 +481,41 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (lane == 0) mbar_arrive(bar(C::B_PREADY + t * NBS + b));
       }
       if (!ok) break;
+      done_with(win);
+      if (!(flags & kLast) || n == 0) continue;
+      // the item's result
       ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBS + (ct - 1) % NBS, ((ct - 1) / NBS) & 1));
       if (!ok) break;
       if (idle) continue;
       fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;   // no key seen: zeros; NaN stays NaN
-      const bool whole = w.j0 == 0 && w.j1 == w.nt;
-      const size_t head = mine ? (size_t)(w.b.row0 + tok) * a.H + w.g * v.rep + hh : 0;
+      const bool whole = flags & kWhole;
+      const size_t head = mine ? (size_t)(row0 + tok) * a.H + g * v.rep + hh : 0;
       __half* dst = nullptr;
       float* po = nullptr;
-      if (whole && v.pre_len == 0) {
-        dst = static_cast<__half*>(a.out) + head * D;
-      } else if (mine) {
-        const size_t at = whole ? (w.b.req < 0 ? 0 : (size_t)v.T * a.H) + head
-                                : (size_t)part_slot(blockIdx.x, w.start, w.x0) * a.part_rows + m;
-        po = (whole ? a.seg_o : a.part_o) + at * D;
-        (whole ? a.seg_ml : a.part_ml)[at] = make_float2(mref, l);
+      if (mine) {
+        if (whole && v.pre_len == 0) {
+          dst = static_cast<__half*>(a.out) + head * D;
+        } else {
+          const size_t at = whole ? (req < 0 ? 0 : (size_t)v.T * a.H) + head : (size_t)slot * a.part_rows + m;
+          po = (whole ? a.seg_o : a.part_o) + at * D;
+          (whole ? a.seg_ml : a.part_ml)[at] = make_float2(mref, l);
+        }
       }
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
-        tmem_ld16(t_o + c0, o);
-        tmem_ld16(t_o + c0 + 16, o + 16);
+        tmem_ld32(t_o + c0, o);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-        if (!mine) continue;
         if (dst) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             *reinterpret_cast<uint4*>(dst + c0 + 8 * c) =
                 make_uint4(pack_f16x2(o[8 * c], o[8 * c + 1]), pack_f16x2(o[8 * c + 2], o[8 * c + 3]),
                            pack_f16x2(o[8 * c + 4], o[8 * c + 5]), pack_f16x2(o[8 * c + 6], o[8 * c + 7]));
-        } else {
+        } else if (po) {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<float4*>(po + c0 + 4 * c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
@@ -456,280 +523,356 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       }
       fence_before();   // the next item's first PV overwrites O only after this warp's next P
     }
-    if (!ok) s_abort = 1;
-  } else if (warp < C::W_ROT) {
-    if constexpr (MT == 2) regs_dec<80>();
-    if (warp < C::W_LOAD) {
-      // =============================== MMA tile t: one thread issues its products
-      const int t = warp - C::W_MMA;
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
-        // two walks over the same tiles: S products up to NBS tiles ahead of the PV products
-        Walk ws;
-        bool mp = w.begin(a, share_), ms = ws.begin(a, share_);
-        uint32_t gs = 0, gp = 0, cs = 0, cp = 0, qs = 0;   // tiles of the CTA, of this MMA tile; items of it
-        int js = ws.j0, jp = w.j0;
-        bool ok = true;
-        uint32_t idle = 0;
-        unsigned long long t_idle = 0;
-        while (mp && ok) {
-          bool prog = false;
-          if (w.b.nrows * v.rep <= 128 * t) {
-            // no rows in this item: its share of each stage is released once the tile is there
-            for (; jp < w.j1 && ok; ++jp, ++gp) {
-              const int st = gp % NST;
-              ok = wait(C::B_READY + st, (gp / NST) & 1) && wait(C::B_VFULL + st, (gp / NST) & 1);
-              if (ok) {
-                mbar_arrive(bar(C::B_KEMPTY + st));
-                mbar_arrive(bar(C::B_VEMPTY + st));
-              }
-            }
-            mp = w.next(a);
-            jp = w.j0;
-            continue;
-          }
-          if (cp < cs) {   // PV of the next tile
-            const int b = cp % NBS, st = gp % NST;
-            if (mbar_test(bar(C::B_PREADY + t * NBS + b), (cp / NBS) & 1) &&
-                mbar_test(bar(C::B_VFULL + st), (gp / NST) & 1)) {
-              fence_after();
-              const uint32_t vb = smem_u32(sm + C::OFF_V + st * C::K_BYTES);
-              const uint32_t pa = tmem + C::TM_S + 128 * t + KT * b + KT / 2;
-#pragma unroll
-              for (int k = 0; k < KT / 16; ++k)
-                umma_ts(tmem + D * t, pa + 8 * k, desc_mnmajor(vb + k * 2048, KT * 128), id_pv, jp != w.j0 || k != 0);
-              umma_commit(bar(C::B_PVDONE + t * NBS + b));
-              umma_commit(bar(C::B_VEMPTY + st));
-              ++cp, ++gp;
-              if (++jp == w.j1) {
-                mp = w.next(a);
-                jp = w.j0;
-              }
-              prog = true;
-            }
-          }
-          if (ms && cs < cp + NBS) {   // S of the tile after
-            if (ws.b.nrows * v.rep <= 128 * t) {   // released in the PV walk above
-              gs += ws.j1 - ws.j0;
-              ms = ws.next(a);
-              js = ws.j0;
-              prog = true;
-            } else {
-              const int b = cs % NBS, st = gs % NST, qb = qs % NQ;
-              if (mbar_test(bar(C::B_READY + st), (gs / NST) & 1) &&
-                  (js > ws.j0 || mbar_test(bar(C::B_QFULL + t * NQ + qb), (qs / NQ) & 1))) {
-                fence_after();
-                const uint32_t qa = smem_u32(sm + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
-                const uint32_t kb = smem_u32(sm + C::OFF_K + st * C::K_BYTES);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                  const uint32_t off = (k & 3) * 32;
-                  umma_ss(tmem + C::TM_S + 128 * t + KT * b, desc_kmajor(qa + (k >> 2) * 16384 + off),
-                          desc_kmajor(kb + (k >> 2) * (KT * 128) + off), id_s, k != 0);
-                }
-                umma_commit(bar(C::B_SFULL + t * NBS + b));
-                umma_commit(bar(C::B_KEMPTY + st));
-                ++cs, ++gs;
-                if (++js == ws.j1) {
-                  umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
-                  ++qs;
-                  ms = ws.next(a);
-                  js = ws.j0;
-                }
-                prog = true;
-              }
-            }
-          }
-          if (prog) {
-            idle = 0;
-          } else if (idle++ == 0) {
-            t_idle = gtimer();
-          } else if ((idle & 255) == 0 && (s_abort || gtimer() - t_idle > kWaitLimitNs)) {
-            if (!s_abort) atomicOr(a.flag, kBatchTimeout);
-            ok = false;
-          }
-        }
-        if (!ok) s_abort = 1;
-        umma_commit(bar(C::B_DONE + t));   // fires once every MMA of this thread has retired
-        volatile int never = 0;
-        mbar_wait(bar(C::B_DONE + t), 0, &never, a.flag);
-      }
-    } else if (warp == C::W_LOAD) {
-      // =============================== loads
-      // A stage's K is free when its S products have retired, but its keys' positions are read by
-      // the softmax after that: they have a ring of their own, twice as long (S(j + NST) is only
-      // issued after P(j + NST - NBS), so the softmax of tile j is over when slot j is reused).
-      bool more = w.begin(a, share_), ok = true;
-      uint32_t gt = 0, gk = 0;   // tiles whose V, whose K is asked for
-      unsigned bad = 0;
-      PageMeta nx{0, 0, 0};
-      auto fetch = [&](int j) {   // lane p: page p of tile j of the item w
-        const int i = j * KP + lane;
-        nx = lane < KP && i < w.b.nv ? page_meta(v, w.b, i, bad) : PageMeta{0, 0, 0};
+    if (!ok) give_up();
+  } else if (warp < C::W_META) {
+    // =============================== MMA tile t: one thread issues its products
+    const int t = warp - C::W_MMA;
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
+      // places of the next S and of the next PV product: window, tile in it, tile of the CTA (g), of
+      // this MMA tile (c)
+      uint32_t ws = 0, wp = 0, gs = 0, gp = 0, cs = 0, cp = 0, qs = 0;
+      int ns = 0, np = 0, js = 0, jp = 0, fs = 0, fp = 0;
+      bool ok = wait_meta(0);
+      // the first window, or the one after: its flags (kEnd: none)
+      auto enter = [&](uint32_t w, int& n, int& f) {
+        ok = wait_meta(w);
+        f = ok ? sRec[w % NWIN].flags : kEnd;
+        n = f & kEnd ? 0 : sRec[w % NWIN].tiles;
       };
-      int j = more ? w.j0 : 0;
-      if (more) fetch(j);
-      while (more && ok) {
-        const PageMeta pm = nx;
-        const int st = gt % NST, slot = gt % C::NPOS, g = w.g;
-        const uint32_t kr = gt / NST;
-        if (++j == w.j1) {
-          more = w.next(a);
-          j = w.j0;
+      if (ok) {
+        enter(0, ns, fs);
+        fp = fs, np = ns;
+      }
+      unsigned long long t_idle = 0;
+#pragma unroll 1
+      while (ok && !(fp & kEnd)) {
+        bool prog = false;
+        if (t == 1 && !(fp & kTwo)) {
+          // no rows for this MMA tile: its share of the stages is released (the S walk is here too)
+          const int sk = gp % NK, sv = gp % NV;
+          ok = wait(C::B_READY + sk, (gp / NK) & 1) && wait(C::B_VFULL + sv, (gp / NV) & 1);
+          if (!ok) break;
+          mbar_arrive(bar(C::B_KEMPTY + sk));
+          mbar_arrive(bar(C::B_VEMPTY + sv));
+          ++gs, ++js, ++gp;
+          if (++jp == np) {
+            mbar_arrive(bar(C::B_RFREE + wp % NWIN));
+            enter(++wp, np, fp);
+            ws = wp, ns = np, fs = fp, js = jp = 0;
+          }
+          continue;
         }
-        if (more) fetch(j);
-        if (lane == 0) ok = kr == 0 || wait(C::B_KEMPTY + st, (kr - 1) & 1);
+        if (cp < cs && mbar_test(bar(C::B_PREADY + t * NBS + cp % NBS), (cp / NBS) & 1) &&
+            mbar_test(bar(C::B_VFULL + gp % NV), (gp / NV) & 1)) {   // PV
+          const int b = cp % NBS, st = gp % NV;
+          fence_after();
+          const bool first = jp == 0 && (fp & kFirst);
+          const uint64_t vd = desc_mnmajor(base + C::OFF_V + st * C::K_BYTES, 2048);
+          const uint32_t pa = tmem + C::TM_S + 128 * t + KT * b;
+#pragma unroll
+          for (int k = 0; k < KP; ++k)      // 16 keys: a page
+            umma_ts(tmem + D * t, pa + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
+          umma_commit(bar(C::B_PVDONE + t * NBS + b));
+          umma_commit(bar(C::B_VEMPTY + st));
+          ++cp, ++gp;
+          if (++jp == np) {
+            mbar_arrive(bar(C::B_RFREE + wp % NWIN));
+            enter(++wp, np, fp);
+            jp = 0;
+            if (t == 1 && !(fp & kTwo)) ws = wp, ns = np, fs = fp, js = 0;   // the S walk has waited here
+          }
+          prog = true;
+        }
+        // S, at most NBS tiles ahead, not beyond a window without rows for this MMA tile
+        if (ok && !(fs & kEnd) && !(t == 1 && !(fs & kTwo)) && cs < cp + NBS &&
+            mbar_test(bar(C::B_READY + gs % NK), (gs / NK) & 1) &&
+            (js > 0 || !(fs & kFirst) || mbar_test(bar(C::B_QFULL + t * NQ + qs % NQ), (qs / NQ) & 1))) {
+          const int b = cs % NBS, st = gs % NK, qb = qs % NQ;
+          fence_after();
+          const uint32_t qa = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE, kb = base + C::OFF_K + st * C::K_BYTES;
+#pragma unroll 1
+          for (int h = 0; h < D / 64; ++h) {
+            const uint64_t qd = desc_kmajor(qa + h * 16384), kd = desc_kmajor(kb + h * (KT * 128));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)     // 16 dims: 32 bytes
+              umma_ss(tmem + C::TM_S + 128 * t + KT * b, qd + 2 * k, kd + 2 * k, id_s, h + k != 0);
+          }
+          umma_commit(bar(C::B_SFULL + t * NBS + b));
+          umma_commit(bar(C::B_KEMPTY + st));
+          ++cs, ++gs;
+          if (++js == ns) {
+            if (fs & kLast) {
+              umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
+              ++qs;
+            }
+            enter(++ws, ns, fs);
+            js = 0;
+          }
+          prog = true;
+        }
+        if (prog) {
+          t_idle = 0;
+        } else if (t_idle == 0) {
+          t_idle = gtimer();
+        } else if (gtimer() - t_idle > kWaitLimitNs) {
+          atomicOr(a.flag, kBatchTimeout);
+          ok = false;
+        } else {
+          uint32_t gone;
+          asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
+          ok = !gone;
+        }
+      }
+      if (!ok) give_up();
+      umma_commit(bar(C::B_DONE + t));   // fires once every MMA of this thread has retired
+      mbar_wait_on(bar(C::B_DONE + t), 0, 0, a.flag);
+    }
+  } else if (warp == C::W_META) {
+    // =============================== window records, V
+    // Lane i holds page i of a window. `next`: the tables' entries of the window after the last one
+    // written (the same item's or the next one's), on their way.
+    Walk w;
+    bool more = w.begin(a, share_, s_plan.block), ok = true;
+    unsigned bad = 0;
+    int j = more ? w.j0 : 0;             // next tile to be described
+    uint32_t n_win = 0, gt = 0;          // windows written, tiles whose V is asked for
+    PageRaw next{0, 0, 0};
+    if (more) next = fetch_page(v, w.b, j * KP + lane);
+    bool ended = false;
+#pragma unroll 1
+    for (uint32_t win = 0; ok;) {        // V of window win, when the two after it are described
+      if (!ended && n_win < win + 3) {
+        const int ws = n_win % NWIN;
+        if (lane == 0) ok = n_win < NWIN || wait(C::B_RFREE + ws, (n_win / NWIN - 1) & 1);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        // key positions, two or four keys per lane; the last key (INT_MAX when a row holds none)
-        // and the first one behind the sinks
-        int last = -1, first = INT_MAX;
+        if (!more) {
+          if (lane == 0) sRec[ws].flags = kEnd;
+          ended = true;
+        } else {
+          const int i = j * KP + lane, n = min(w.j1 - j, WT);
+          PageMeta pm{0, 0, 0};
+          if (lane < n * KP && i < w.b.nv) pm = page_meta(v, w.b, next, bad);
+          int top = pm.rows == 0xffffu ? pm.pos + 15 : INT_MAX;
+          const int sk = min(max(v.sinks - pm.pos, 0), 16);
+          const unsigned behind = pm.rows >> sk << sk;
+          int low = behind ? pm.pos + __ffs(behind) - 1 : INT_MAX;
 #pragma unroll
-        for (int e = 0; e < KT / 32; ++e) {
-          const int key = 32 * e + lane, q = key / kPage, r = key % kPage;
-          const int pos = __shfl_sync(0xffffffffu, pm.pos, q);
-          const unsigned rows = __shfl_sync(0xffffffffu, pm.rows, q);
-          const int u = rows >> r & 1u ? pos + r : INT_MAX;
-          sPos[slot * KT + key] = u;
-          last = max(last, u);
-          if (u >= v.sinks) first = min(first, u);
+          for (int d = 1; d < KP; d <<= 1) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
+          }
+          sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, 0);
+          if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
+          if (lane == 0) {
+            WinRec& r = sRec[ws];
+            r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows * v.rep > 128 ? kTwo : 0) |
+                      (w.j0 == 0 && w.j1 == w.nt ? kWhole : 0);
+            r.tiles = n, r.req = w.b.req, r.row0 = w.b.row0, r.nrows = w.b.nrows, r.pos0 = w.b.pos0, r.g = w.g;
+            r.slot = part_slot(blockIdx.x, w.start, w.x0);
+          }
+          j += n;
+          if (j == w.j1) {
+            more = w.next(a);
+            j = w.j0;
+          }
+          if (more) next = fetch_page(v, w.b, j * KP + lane);
         }
-        last = __reduce_max_sync(0xffffffffu, last);
-        first = __reduce_min_sync(0xffffffffu, first);
-        if (lane == 0) sLim[slot] = make_int2(last, first);
-        if (lane < KP) sMask[st * KP + lane] = pm.rows;
-        const int n_full = __popc(__ballot_sync(0xffffffffu, pm.rows != 0));
         __syncwarp();
-        const uint32_t kf = bar(C::B_KFULL + st), vf = bar(C::B_VFULL + st);
-        if (lane == 0) mbar_expect_tx(kf, (uint32_t)n_full * (kPage * D * 2 + C::CS_ROW));
-        __syncwarp();
-        const int pg = lane / NH, half = lane % NH;   // one box per lane
-        const int blk = __shfl_sync(0xffffffffu, pm.blk, pg % KP);
-        const unsigned rows = __shfl_sync(0xffffffffu, pm.rows, pg % KP);
-        const uint32_t box = half * (KT * 128) + pg * 2048;
-        const bool boxed = pg < KP && rows != 0;
-        if (boxed) tma_page(smem_u32(sm + C::OFF_K + st * C::K_BYTES) + box, &ta.kmap, half, g, blk, kf);
-        if (lane < KP && pm.rows != 0)
-          bulk_g2s(smem_u32(sm + C::OFF_CS + st * C::CS_BYTES + lane * C::CS_ROW), a.rope_cs + (size_t)pm.pos * (D / 2),
-                   C::CS_ROW, kf);
-        ++gk;
-        if (lane == 0) ok = kr == 0 || wait(C::B_VEMPTY + st, (kr - 1) & 1);
+        if (lane == 0) mbar_arrive(bar(C::B_META + ws));
+        ++n_win;
+        continue;
+      }
+      if (sRec[win % NWIN].flags & kEnd) break;
+      const int n = sRec[win % NWIN].tiles;
+      const int4 pg = sPage[win % NWIN * WIN + lane];
+      ++win;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++gt) {
+        const int st = gt % NV;
+        if (lane == 0) ok = gt < NV || wait(C::B_VEMPTY + st, (gt / NV - 1) & 1);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(vf, (uint32_t)n_full * (kPage * D * 2));
+        const bool live = lane / KP == i && pg.z != 0;
+        const unsigned who = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) mbar_expect_tx(bar(C::B_VFULL + st), (uint32_t)__popc(who) * C::PAGE_BYTES);
         __syncwarp();
-        if (boxed) tma_page(smem_u32(sm + C::OFF_V + st * C::K_BYTES) + box, &ta.vmap, half, g, blk, vf);
-        ++gt;
-      }
-      batch_flag(a.flag, bad);
-      // every copy has landed before the shared memory is given up (at once on the normal path)
-      if (lane == 0) {
-        volatile int never = 0;
-        for (uint32_t s = 0; s < NST; ++s) {
-          const uint32_t nk = (gk + NST - 1 - s) / NST, nv = (gt + NST - 1 - s) / NST;
-          if (nk) mbar_wait(bar(C::B_KFULL + s), (nk - 1) & 1, &never, a.flag);
-          if (nv) mbar_wait(bar(C::B_VFULL + s), (nv - 1) & 1, &never, a.flag);
-        }
-      }
-    } else if (warp == C::W_Q) {
-      // =============================== q of the items into the A operands
-      uint32_t qi[MT] = {};
-      bool ok = true;
-      for (bool more = w.begin(a, share_); more && ok; more = w.next(a)) {
-        const int rows = w.b.nrows * v.rep;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          if (rows <= 128 * t || !ok) continue;
-          const uint32_t q = qi[t]++, qb = q % NQ;
-          if (q >= NQ) {
-            if (lane == 0) ok = wait(C::B_QEMPTY + t * NQ + qb, (q / NQ - 1) & 1);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-          }
-          const uint32_t dst = smem_u32(sm + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
-          const int n = min(128, rows - 128 * t) * (D / 8);   // 16-byte chunks; rows behind the item's stay as they are
-          for (int i = lane; i < n; i += 32) {
-            const int mr = i / (D / 8), ch = i % (D / 8), mm = 128 * t + mr;
-            const __half* src = static_cast<const __half*>(a.q) +
-                                ((size_t)(w.b.row0 + mm / v.rep) * a.H + w.g * v.rep + mm % v.rep) * D + 8 * ch;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (ch >> 3) * 16384 + sw128(mr, ch & 7)),
-                         "l"(src)
-                         : "memory");
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::B_QFULL + t * NQ + qb));
-        }
+        if (live) tma_page(base + C::OFF_V + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.vmap, pg.x, bar(C::B_VFULL + st));
       }
     }
-  } else {
-    // =============================== rotation of K in the stages
-    if constexpr (MT == 2) regs_dec<80>();
-    constexpr int CH = D / 16;                 // 16-byte chunks of the first half of a row's dims
-    constexpr int PP = 128 / (16 * CH);        // pages at once: 1 (D 128), 2 (D 64)
+    if (!ok) give_up();
+    batch_flag(a.flag, bad);
+    // every copy has landed before the shared memory is given up (at once on the normal path)
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t s = 0; s < NV; ++s) {
+        const uint32_t n = (gt + NV - 1 - s) / NV;
+        if (n) mbar_wait_on(bar(C::B_VFULL + s), (n - 1) & 1, 0, a.flag);
+      }
+    }
+  } else if (warp == C::W_Q) {
+    // =============================== q of the items into the A operands
+    uint32_t qi[MT] = {};
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t win = 0; ok; ++win) {
+      ok = __all_sync(0xffffffffu, wait_meta(win));
+      if (!ok) break;
+      const WinRec& rec = sRec[win % NWIN];
+      const int flags = rec.flags;
+      if (flags & kEnd) break;
+      const int row0 = rec.row0, g = rec.g, rows = rec.nrows * v.rep;
+      done_with(win);
+      if (!(flags & kFirst)) continue;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (rows <= 128 * t || !ok) continue;
+        const uint32_t q = qi[t]++, qb = q % NQ;
+        if (q >= NQ) {
+          if (lane == 0) ok = wait(C::B_QEMPTY + t * NQ + qb, (q / NQ - 1) & 1);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+        }
+        const uint32_t dst = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE;
+        const int n = min(128, rows - 128 * t) * (D / 8);   // 16-byte chunks; rows behind the item's stay as they are
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) {
+          const int mr = i / (D / 8), ch = i % (D / 8), mm = 128 * t + mr, tok = mm * v.rep_inv >> 16;
+          const __half* src = static_cast<const __half*>(a.q) +
+                              ((size_t)(row0 + tok) * a.H + g * v.rep + mm - tok * v.rep) * D + 8 * ch;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (ch >> 3) * 16384 + sw128(mr, ch & 7)),
+                       "l"(src)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_QFULL + t * NQ + qb));
+      }
+    }
+    if (!ok) give_up();
+  } else if (warp >= C::W_ROT) {
+    // =============================== K: load and rotate in place
+    constexpr int CH = C::CH, PP = C::PP, PD = C::PD;
+    constexpr int NP = PP < KP ? KP / PP : 1;   // pages of a tile per thread (none for the threads beyond, p0 >= KP)
     const int rt = tid - C::W_ROT * 32, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
     // (cos, sin) of r theta for the thread's 8 frequencies
     float4 off[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) off[e] = reinterpret_cast<const float4*>(a.rope_cs + (size_t)r * (D / 2) + 8 * c)[e];
-    uint32_t gt = 0;
+    const __nv_bfloat16* kl = static_cast<const __nv_bfloat16*>(a.k_layer) + r * D + 8 * c;
+    // the thread's two 16-byte chunks (dims 8c.. and their partners) of page 0 of a K and of a V stage
+    const uint32_t k1 = base + C::OFF_K + sw128(r, c);
+    const uint32_t k2 = base + C::OFF_K + (D == 128 ? KT * 128 + sw128(r, c) : sw128(r, c + CH));
+    const uint32_t v1 = base + C::OFF_V + sw128(r, c);
+    const uint32_t v2 = base + C::OFF_V + (D == 128 ? 2048 + sw128(r, c) : sw128(r, c + CH));
+    // table rows: thread rt < KP D / 4 brings 16-byte chunk x of page rt / (D / 4) (thread c's e-th is
+    // 4 c + e) to place e CH + c, so that the threads that use it read neighbouring chunks
+    const int cp_ = rt / (D / 4), cx = rt % (D / 4);
+    const uint32_t cs_to = base + C::OFF_CS + cp_ * C::CS_ROW + ((cx & 3) * CH + (cx >> 2)) * 16;
+    uint32_t end = 0x7fffffffu;               // tiles in all, once known
+    uint32_t wi = 0, wt = 0;                  // windows of the tile asked for, of the tile turned
+    int ji = 0, ni = 0, jt = 0, nt = 0;
     bool ok = true;
-    for (bool more = w.begin(a, share_); more && ok; more = w.next(a)) {
-      for (int j = w.j0; j < w.j1; ++j, ++gt) {
-        const int st = gt % NST;
-        const uint32_t ph = (gt / NST) & 1;
-        ok = wait(C::B_KFULL + st, ph);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        uint8_t* ks = sm + C::OFF_K + st * C::K_BYTES;
-        const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + st * C::CS_BYTES);
-        bool holes = false;
-#pragma unroll 2
-        for (int p = p0; p < KP; p += PP) {
-          const unsigned rows = sMask[st * KP + p];
-          holes |= rows != 0xffffu;
-          uint4* k1 = reinterpret_cast<uint4*>(ks + sw128(p * kPage + r, c));
-          uint4* k2 = reinterpret_cast<uint4*>(D == 128 ? ks + KT * 128 + sw128(p * kPage + r, c)
-                                                        : ks + sw128(p * kPage + r, c + CH));
-          uint4 y1 = make_uint4(0, 0, 0, 0), y2 = y1;
-          if (rows >> r & 1u) {
-            const uint4 u1 = *k1, u2 = *k2;
-            const uint32_t w1[4] = {u1.x, u1.y, u1.z, u1.w}, w2[4] = {u2.x, u2.y, u2.z, u2.w};
-            uint32_t o1[4], o2[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 f = cs[p * (D / 4) + 4 * c + e];   // (cos, sin) of P theta, two frequencies
-              const float c0 = f.x * off[e].x - f.y * off[e].y, s0 = f.y * off[e].x + f.x * off[e].y;
-              const float c1 = f.z * off[e].z - f.w * off[e].w, s1 = f.w * off[e].z + f.z * off[e].w;
-              const float a0 = __uint_as_float(w1[e] << 16), a1 = __uint_as_float(w1[e] & 0xffff0000u);
-              const float b0 = __uint_as_float(w2[e] << 16), b1 = __uint_as_float(w2[e] & 0xffff0000u);
-              o1[e] = pack_f16x2(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-              o2[e] = pack_f16x2(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
-            }
-            y1 = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-            y2 = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-          }
-          *k1 = y1;
-          *k2 = y2;
-        }
-        if (__any_sync(0xffffffffu, holes)) {   // rows of V without a key: P is 0 there, V must be finite
-          ok = wait(C::B_VFULL + st, ph);
-          ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+    for (uint32_t i = 0; i < end + PD; ++i) {
+      if (i < end) {                          // ask for tile i
+        if (ji == ni) {
+          if (i > 0) ++wi;
+          ok = __all_sync(0xffffffffu, wait_meta(wi));
           if (!ok) break;
-          uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES;
-          for (int p = p0; p < KP; p += PP)
-            if (!(sMask[st * KP + p] >> r & 1u)) {
-              *reinterpret_cast<uint4*>(vs + sw128(p * kPage + r, c)) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(D == 128 ? vs + KT * 128 + sw128(p * kPage + r, c)
-                                                 : vs + sw128(p * kPage + r, c + CH)) = make_uint4(0, 0, 0, 0);
-            }
+          ji = 0;
+          ni = sRec[wi % NWIN].tiles;
+          if (sRec[wi % NWIN].flags & kEnd) end = i;
         }
-        fence_async_smem();   // the MMAs read these rows through the async proxy
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_READY + st));
+        if (i < end) {
+          const int st = i % NK;
+          ok = __all_sync(0xffffffffu, i < NK || wait(C::B_KEMPTY + st, (i / NK - 1) & 1));
+          if (!ok) break;
+          const int4* pages = sPage + wi % NWIN * WIN + ji * KP;
+          if (cp_ < KP) {
+            const int4 pg = pages[cp_];
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(cs_to + st * KP * C::CS_ROW),
+                         "l"(reinterpret_cast<const float4*>(a.rope_cs + (size_t)pg.y * (D / 2)) + cx)
+                         : "memory");
+          }
+#pragma unroll
+          for (int q = 0; q < NP; ++q) {
+            const int p = p0 + q * PP;
+            const int4 pg = pages[min(p, KP - 1)];
+            if (p < KP && ((unsigned)pg.z >> r & 1u)) {
+              const __nv_bfloat16* src = kl + (size_t)pg.x * (kPage * D);
+              const uint32_t to = st * C::K_BYTES + p * 2048;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(k1 + to), "l"(src) : "memory");
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(k2 + to), "l"(src + D / 2) : "memory");
+            }
+          }
+          ++ji;
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(C::B_KLAND + st)) : "memory");
+        }
       }
+      if (i < PD) continue;
+      const uint32_t gt = i - PD;             // turn tile i - PD
+      if (gt >= end) break;
+      if (jt == nt) {
+        if (gt > 0) ++wt;
+        jt = 0;
+        nt = sRec[wt % NWIN].tiles;
+      }
+      const int st = gt % NK;
+      ok = __all_sync(0xffffffffu, wait(C::B_KLAND + st, (gt / NK) & 1));   // everyone's K and table rows
+      if (!ok) break;
+      const int4* pages = sPage + wt % NWIN * WIN + jt * KP;
+      bool holes = false;
+#pragma unroll 2
+      for (int p = p0; p < KP; p += PP) {
+        const unsigned rows = (unsigned)pages[p].z;
+        const uint32_t to = st * C::K_BYTES + p * 2048;
+        const uint8_t* cs = sm + C::OFF_CS + (st * KP + p) * C::CS_ROW + c * 16;
+        uint32_t w1[4], w2[4], o1[4], o2[4];
+        lds128(k1 + to, w1);
+        lds128(k2 + to, w2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // (cos, sin) of P theta, two frequencies
+          const float4 f = *reinterpret_cast<const float4*>(cs + e * (CH * 16));
+          const float c0 = f.x * off[e].x - f.y * off[e].y, s0 = f.y * off[e].x + f.x * off[e].y;
+          const float c1 = f.z * off[e].z - f.w * off[e].w, s1 = f.w * off[e].z + f.z * off[e].w;
+          const float x0 = __uint_as_float(w1[e] << 16), x1 = __uint_as_float(w1[e] & 0xffff0000u);
+          const float y0 = __uint_as_float(w2[e] << 16), y1 = __uint_as_float(w2[e] & 0xffff0000u);
+          o1[e] = pack_f16x2(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
+          o2[e] = pack_f16x2(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
+        }
+        if (rows != 0xffffu) {
+          holes = true;
+          if (!(rows >> r & 1u)) {            // nothing was loaded here
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o1[e] = o2[e] = 0;
+          }
+        }
+        sts128(k1 + to, o1);
+        sts128(k2 + to, o2);
+      }
+      if (__any_sync(0xffffffffu, holes)) {   // rows of V without a key: P is 0 there, V must be finite
+        ok = __all_sync(0xffffffffu, wait(C::B_VFULL + gt % NV, (gt / NV) & 1));
+        if (!ok) break;
+        const uint32_t zero[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int p = p0; p < KP; p += PP)
+          if (!((unsigned)pages[p].z >> r & 1u)) {
+            const uint32_t to = gt % NV * C::K_BYTES + p * C::PAGE_BYTES;
+            sts128(v1 + to, zero);
+            sts128(v2 + to, zero);
+          }
+      }
+      fence_async_smem();   // the MMAs read these rows through the async proxy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_READY + st));
+      if (++jt == nt) done_with(wt);
     }
+    if (!ok) give_up();
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   __syncwarp();
   fence_before();
@@ -751,15 +894,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A pool layer [blocks][G][16][D] of bf16 as (64 dims, D / 64 halves, 16 rows, G, blocks); a box is
-// one half of one page.
+// A pool layer [blocks][G][16][D] of bf16 as (64 dims, 16 rows, D / 64 halves, G x blocks pages); a
+// box is one page, landing as [half][row][128 B].
 bool page_map(CUtensorMap* m, const void* base, int blocks, int G, int D) {
   auto enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[5] = {64, (cuuint64_t)(D / 64), (cuuint64_t)kPage, (cuuint64_t)G, (cuuint64_t)blocks};
-  const cuuint64_t strides[4] = {128, (cuuint64_t)D * 2, (cuuint64_t)kPage * D * 2, (cuuint64_t)G * kPage * D * 2};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1}, box[5] = {64, 1, kPage, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint64_t dims[4] = {64, (cuuint64_t)kPage, (cuuint64_t)(D / 64), (cuuint64_t)G * blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)kPage * D * 2};
+  const cuuint32_t estr[4] = {1, 1, 1, 1}, box[4] = {64, kPage, (cuuint32_t)(D / 64), 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -789,7 +932,8 @@ void batch_tc_view(BatchView& v, int D) {
   const bool two = rows > 128;
   v.mrows = two ? 256 : 128;
   v.rb = v.mrows / v.rep;
-  v.kpages = two ? Cfg<128, 2>::KP : Cfg<128, 1>::KP;
+  v.rep_inv = (65535 + v.rep) / v.rep;
+  v.kpages = KP;
   v.cost_item = 4;
   v.cost_full = 8;
   v.cost_half = two ? 5 : 8;
@@ -799,9 +943,8 @@ void batch_tc_view(BatchView& v, int D) {
 pic_status launch_batch_tc(const BatchArgs& a, cudaStream_t st) {
   TcArgs ta;
   ta.b = a;
-  if (!page_map(&ta.kmap, a.k_layer, a.v.pool_blocks, a.v.G, a.D) ||
-      !page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D))
-    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the pools");
+  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D))
+    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the V pool");
   if (a.D == 128) return a.v.mrows == 256 ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
   return a.v.mrows == 256 ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
 }

@@ -34,30 +34,33 @@ int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const
     const int m = request_rows(v, r, row0, bad);
     for (int k = 0; k < pdiv(m, v.rb); ++k) blocks.push_back(own_block(v, r, row0, m, k));
   }
-  long long U = 0;
+  unsigned U = 0;
   int np = 0, ni = 0, wrong = 0;
   for (size_t i = 0; i < blocks.size(); ++i) {
     BatchBlock& b = blocks[i];
     b.cum = U;
     U += block_len(v, b);
     for (int j = 0; j < b.nv; ++j) {
-      const PageMeta m = page_meta(v, b, j, bad);
+      const PageMeta m = page_meta(v, b, page_raw(v, b, j), bad);
       if (np >= max_pages) return 1;
       int* o = pages + 5 * np++;
       o[0] = (int)i, o[1] = j, o[2] = m.blk, o[3] = m.pos, o[4] = (int)m.rows;
     }
   }
+  if (U > axis_bound(v, v.T / v.rb + v.n_reqs, v.pre_len > 0 ? v.T / v.rb + 1 : 0)) return 3;
+  const unsigned len = share_len(U, grid);
+  if (share(U, len, grid) != U) return 2;   // the shares do not reach the end
   for (int c = 0; c < grid && U > 0; ++c) {
-    const long long x0 = share(U, grid, c), x1 = share(U, grid, c + 1);
+    const unsigned x0 = share(U, len, c), x1 = share(U, len, c + 1);
     for (size_t i = 0; i < blocks.size(); ++i) {
       const BatchBlock& b = blocks[i];
       const int nt = block_tiles(v, b), tc = tile_cost(v, b);
       for (int g = 0; g < v.G; ++g) {
-        const long long start = b.cum + g * item_len(v, b);
+        const unsigned start = b.cum + g * item_len(v, b);
         const int j0 = tile_lower(v, start, nt, tc, x0), j1 = tile_lower(v, start, nt, tc, x1);
         if (j0 >= j1) continue;
         for (int j = j0; j < j1; ++j)
-          if (owner(U, grid, tile_place(v, start, tc, j)) != c) ++wrong;
+          if (owner(len, tile_place(v, start, tc, j)) != c) ++wrong;
         if (ni >= max_items) return 1;
         int* o = items + 12 * ni++;
         const bool whole = j0 == 0 && j1 == nt;
