@@ -39,9 +39,10 @@ struct BatchView {
   int window, sinks;        // key u seen from p when u <= p and (u > p - window or u < sinks)
   int pool_blocks, rope_positions;
   int mrows, rb, kpages;    // rows (token x head) of an item, tokens of a row block (mrows / rep), pages of a tile
+  int half_rows;            // tokens up to which an item costs cost_half a tile
   unsigned rep_inv;         // ceil(2^16 / rep): m / rep = m * rep_inv >> 16 for m < 256
   int cost_item;            // cost of an item's start and drain,
-  int cost_full, cost_half; // of a key tile, and of one whose item fills no more than half of its rows
+  int cost_full, cost_half; // of a key tile, and of one whose item has at most half_rows tokens
 };
 
 // what a kernel met and skipped; pic_sync reports it
@@ -143,7 +144,7 @@ PIC_HD BatchBlock prefix_block(const BatchView& v, int live, int k) {
 
 PIC_HD int block_tiles(const BatchView& v, const BatchBlock& b) { return pdiv(b.nv, v.kpages); }
 PIC_HD int tile_cost(const BatchView& v, const BatchBlock& b) {
-  return b.nrows * v.rep * 2 <= v.mrows ? v.cost_half : v.cost_full;
+  return b.nrows <= v.half_rows ? v.cost_half : v.cost_full;
 }
 // Lengths on the cost axis: 32 bits hold the whole axis (axis_bound below 2^31 is checked on the host).
 PIC_HD unsigned item_len(const BatchView& v, const BatchBlock& b) {

@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
 
 // Joins what the attention kernel left in parts: one warp per (row, head), D / 32 columns per
 // lane; result = sum_i w_i O_i / sum_i w_i with w_i = l_i 2^(m_i - max). Rows that see no key
-// (sum 0) give zeros. grid (own row blocks, G).
+// (sum 0) give zeros. A lane finds one part each (of the row's item of the prefix, then of its own);
+// their rows are read eight at a time. grid (own row blocks, G, rows of a block / 8).
 template <typename A, int D>
 __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant__ BatchArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -195,77 +196,81 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
   const BatchHead hd = *a.head;
   constexpr int C = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
+  struct Parts {          // the parts of one item
+    unsigned start;
+    int nt, c, c0, n;
+  };
+  auto parts = [&](const BatchBlock& b) {
+    Parts p;
+    p.nt = block_tiles(v, b), p.c = tile_cost(v, b);
+    p.start = b.cum + g * item_len(v, b);
+    p.c0 = owner(hd.len, p.start);
+    p.n = owner(hd.len, tile_place(v, p.start, p.c, p.nt - 1)) - p.c0 + 1;
+    return p;
+  };
 #pragma unroll 1
   for (int bi = hd.n_prefix + blockIdx.x; bi < hd.n_blocks; bi += gridDim.x) {
     const BatchBlock own = a.blocks[bi];
 #pragma unroll 1
-    for (int rr = warp; rr < own.nrows * v.rep; rr += 8) {
+    for (int rr = blockIdx.z * 8 + warp; rr < own.nrows * v.rep; rr += 8 * gridDim.z) {
       const int tok = rr * v.rep_inv >> 16, hh = rr - tok * v.rep, t = own.row0 + tok;
       const size_t head = (size_t)t * a.H + g * v.rep + hh;
+      const Parts po = parts(own);
+      if (po.n == 1 && v.pre_len == 0) break;   // the attention kernel wrote out itself
+      const int pb = hd.n_prefix > 0 ? (unsigned)t / (unsigned)v.rb : 0;
+      Parts pp{};
+      if (hd.n_prefix > 0) pp = parts(a.blocks[pb]);
       float M = -INFINITY, L = 0.f, o[C] = {};
-      bool any = false;
-      // the row's item of the prefix, then its own
 #pragma unroll 1
-      for (int seg = hd.n_prefix > 0 ? 0 : 1; seg < 2; ++seg) {
-        const int pb = (unsigned)t / (unsigned)v.rb, lrow = seg ? tok : t - pb * v.rb;
-        const BatchBlock b = seg ? own : a.blocks[pb];
-        const int nt = block_tiles(v, b), c = tile_cost(v, b);
-        const unsigned start = b.cum + g * item_len(v, b);
-        const int c0 = owner(hd.len, start), c1 = owner(hd.len, tile_place(v, start, c, nt - 1));
-        if (c0 == c1 && v.pre_len == 0) break;   // the attention kernel wrote out itself
-        any = true;
+      for (int i0 = 0; i0 < pp.n + po.n; i0 += 32) {
+        const int i = i0 + lane, seg = i >= pp.n, p = seg ? i - pp.n : i;
+        const Parts& q = seg ? po : pp;
+        bool on = i < pp.n + po.n;
+        size_t at = (size_t)seg * v.T * a.H + head;   // a whole item's result
+        const bool whole = q.n == 1;
+        if (on && !whole) {
+          const unsigned x0 = share(hd.U, hd.len, q.c0 + p), x1 = share(hd.U, hd.len, q.c0 + p + 1);
+          on = tile_lower(v, q.start, q.nt, q.c, x0) < tile_lower(v, q.start, q.nt, q.c, x1);
+          const int lrow = seg ? rr : (t - pb * v.rb) * v.rep + hh;
+          at = (size_t)part_slot(q.c0 + p, q.start, x0) * a.part_rows + lrow;
+        }
+        const float2 x = on ? (whole ? a.seg_ml : a.part_ml)[at] : make_float2(-INFINITY, 0.f);
+        const float* src = (whole ? a.seg_o : a.part_o) + at * D;
+        float mx = x.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        mx = fmaxf(mx, M);
+        const float ref = mx == -INFINITY ? 0.f : mx, keep = exp2f(M - ref), w = x.y * exp2f(x.x - ref);
+        float sum = w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        M = mx;
+        L = L * keep + sum;
+#pragma unroll
+        for (int e = 0; e < C; ++e) o[e] *= keep;
+        unsigned left = __ballot_sync(0xffffffffu, on && x.y != 0.f);
 #pragma unroll 1
-        for (int i0 = c0; i0 <= c1; i0 += 32) {   // lane: one part
-          const int p = i0 + lane;
-          size_t at = 0;
-          bool on = p <= c1;
-          const float2* ml = a.part_ml;
-          const float* po = a.part_o;
-          if (c0 == c1) {
-            at = (size_t)seg * v.T * a.H + head;
-            ml = a.seg_ml;
-            po = a.seg_o;
-          } else if (on) {
-            const unsigned x0 = share(hd.U, hd.len, p), x1 = share(hd.U, hd.len, p + 1);
-            on = tile_lower(v, start, nt, c, x0) < tile_lower(v, start, nt, c, x1);
-            at = (size_t)part_slot(p, start, x0) * a.part_rows + lrow * v.rep + hh;
-          }
-          const float2 x = on ? ml[at] : make_float2(-INFINITY, 0.f);
-          float mx = x.x;
+        while (left) {
+          float y[8][C], ww[8];
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-          mx = fmaxf(mx, M);
-          const float ref = mx == -INFINITY ? 0.f : mx, keep = exp2f(M - ref), w = x.y * exp2f(x.x - ref);
-          float sum = w;
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          M = mx;
-          L = L * keep + sum;
-#pragma unroll
-          for (int e = 0; e < C; ++e) o[e] *= keep;
-          unsigned left = __ballot_sync(0xffffffffu, on && x.y != 0.f);
-          const unsigned row = (unsigned)at;      // rows of partials: below 2^32 (checked on the host)
-#pragma unroll 1
-          while (left) {                          // eight parts' rows in flight
-            float y[8][C], ww[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int i = left ? __ffs(left) - 1 : 0;
-              const float wi = __shfl_sync(0xffffffffu, w, i);
-              const float* src = po + (size_t)__shfl_sync(0xffffffffu, row, i) * D + lane * C;
-              ww[u] = left ? wi : 0.f;
-#pragma unroll
-              for (int e = 0; e < C; ++e) y[u][e] = left ? src[e] : 0.f;
-              left &= left - 1;
+          for (int u = 0; u < 8; ++u) {
+            const int k = left ? __ffs(left) - 1 : 0;
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float* row = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, k)) + lane * C;
+            ww[u] = left ? wk : 0.f;
+            if constexpr (C == 4) {
+              *reinterpret_cast<float4*>(y[u]) = left ? *reinterpret_cast<const float4*>(row) : make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+              *reinterpret_cast<float2*>(y[u]) = left ? *reinterpret_cast<const float2*>(row) : make_float2(0.f, 0.f);
             }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-              for (int e = 0; e < C; ++e) o[e] += ww[u] * y[u][e];
+            left &= left - 1;
           }
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int e = 0; e < C; ++e) o[e] += ww[u] * y[u][e];
         }
       }
-      if (!any) continue;
       const float inv = L == 0.f ? 0.f : 1.f / L;
       A* dst = static_cast<A*>(a.out) + head * D + lane * C;
 #pragma unroll
@@ -424,8 +429,9 @@ void launch_batch_simt(const BatchArgs& a, cudaStream_t st) {
 }
 
 void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st) {
-  const int own = a.v.T / a.v.rb + a.v.n_reqs;
-  const dim3 grid(pmin(own, 65535), a.v.G);
+  // as many warps as a block has rows when the requests have equally many
+  const int own = a.v.T / a.v.rb + a.v.n_reqs, rows = pmin(a.v.rb, pdiv(a.v.T, a.v.n_reqs)) * a.v.rep;
+  const dim3 grid(own, a.v.G, pdiv(rows, 8));
   if (dtype == PIC_BF16) {
     if (a.D == 128) launch_dependent(batch_merge_kernel<__half, 128>, grid, dim3(256), 0, st, a);
     else launch_dependent(batch_merge_kernel<__half, 64>, grid, dim3(256), 0, st, a);

@@ -1,8 +1,8 @@
 // tcgen05 kernel of the batched paged attention: bf16 pools, head_dim 64 or 128, up to 16 query
 // heads per KV head, one persistent CTA per SM over its share of the plan (batch_plan.h).
 //
-// An item is a row block x a KV head: MT tiles of 128 MMA rows, row m = token * rep + head of the
-// group. Its pages come in windows of 32 (one record each) and key tiles of 64 keys, which pass
+// An item is a row block x a KV head: MT tiles of up to 128 MMA rows (half_rows tokens x the rep heads
+// of the group, a multiple of 8 tokens). Its pages come in windows of 32 (one record each) and key tiles of 64 keys, which pass
 // through rings of stages in shared memory:
 //
 //   meta warp   walks the share: reads the page tables a window ahead, writes the windows' records
@@ -18,8 +18,8 @@
 //   MMA warps   one issuing thread per MMA tile: O_t += P_t V of key tile j as soon as P_t(j) is
 //               written, S_t of tile j + 2 (Q_t K^T, fp16) into the S buffer that PV has just read (one
 //               thread's MMAs run in order), also across items.
-//   Q warp      copies the items' rows of q into the swizzled A operand (double-buffered for one MMA
-//               tile, else when the item's last S product has retired).
+//   Q warp      asks for the items' rows of q, TMA boxes of 8 tokens x rep heads (double-buffered for
+//               one MMA tile, else when the item's last S product has retired).
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
 //               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 over the S columns
 //               (V is stored bf16 and both operands have one type; the sum is of the unrounded
@@ -45,7 +45,7 @@ namespace pic {
 namespace {
 
 constexpr float kRescale = 8.f;           // rescale O when the row maximum grows by more than 2^8
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr unsigned long long kWaitLimit = 4000000000ull;   // cycles, about 2 s
 
 constexpr int KT = 64, KP = KT / kPage;   // keys, pages of a tile
 constexpr int NBS = 2;                    // S buffers per MMA tile
@@ -62,8 +62,15 @@ struct Cfg {
   static constexpr int NR = MT == 2 ? 4 : 8;          // rotation warps
   static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
   static constexpr int CH = D / 16, PP = NR * 32 / (16 * CH);   // rotation: threads of a row, pages at once
-  static constexpr int W_MMA = 4 * MT, W_META = W_MMA + MT, W_Q = W_META + 1, W_ROT = MT == 2 ? 12 : 8;
-  static constexpr int THREADS = (W_ROT + NR) * 32;
+  // Roles of the 16 warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
+  // instruction cache is shared by its warps: each scheduler gets as few roles as possible, and the
+  // MMA threads one away from the rotation.
+  static constexpr int THREADS = 512;
+  static constexpr int W_MMA0 = MT == 2 ? 11 : 7, W_MMA1 = 15, W_META = MT == 2 ? 10 : 11, W_Q = MT == 2 ? 14 : 15;
+  // number of a rotation warp: MT 2: warps 8 9 12 13; MT 1: 5 6 8 9 10 12 13 14
+  static __device__ __forceinline__ int rot(int w) {
+    return MT == 2 ? (w & 1) + (w >> 1 & 2) : w < 8 ? w - 5 : w < 12 ? w - 6 : w - 7;
+  }
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
@@ -108,9 +115,10 @@ struct WinRec {           // 48 bytes
 // The rotation waits for record i before it turns tile i - PD, with PD < NWIN and PD < NV + 3.
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ unsigned long long gtimer() {
+// SM clock cycles (reading the global timer instead takes long enough to delay every wait)
+__device__ __forceinline__ unsigned long long cycles() {
   unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  asm volatile("mov.u64 %0, %%clock64;" : "=l"(t));
   return t;
 }
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -140,16 +148,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// false (and the timeout flag) after kWaitLimitNs, or when the CTA has given up (`abort`: its word in
+// false (and the timeout flag) after kWaitLimit, or when the CTA has given up (`abort`: its word in
 // shared memory, 0: wait on). Not inlined: there are some thirty waits.
 __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, uint32_t abort, unsigned* flag) {
-  const unsigned long long t0 = gtimer();
+  const unsigned long long t0 = cycles();
   for (;;) {
     if (mbar_try(bar, parity)) return true;
     uint32_t gone = 0;
     if (abort) asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
     if (gone) return false;
-    if (gtimer() - t0 > kWaitLimitNs) {
+    if (cycles() - t0 > kWaitLimit) {
       atomicOr(flag, kBatchTimeout);
       if (abort) asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory");
       return false;
@@ -157,7 +165,7 @@ __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, uint32_
   }
 }
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort, unsigned* flag) {
-  return mbar_try(bar, parity) || mbar_wait_on(bar, parity, abort, flag);
+  return mbar_test(bar, parity) || mbar_wait_on(bar, parity, abort, flag);   // a test is far cheaper than a try
 }
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int page, uint32_t bar) {
   asm volatile(
@@ -166,22 +174,23 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(page), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void lds128(uint32_t at, uint32_t* x) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int half, int head, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(half), "r"(row), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t at, const uint32_t* x) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
 }
 // 16-byte chunk c (0..7) of row r of a [rows][128 B] tile, 128-byte swizzle (the TMA and UMMA layout)
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-// K-major operand: 8-row atoms 1024 B apart
-__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-// MN-major operand [k rows][n], 64 n per 128-byte row: blocks of 64 n `lbo` bytes apart, groups of 8 k rows 1024 B
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t addr, uint32_t lbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Matrix descriptors, 128-byte swizzle, 8-row groups 1024 B apart: the low word is the address and, for
+// the MN-major V ([16 keys][64 dims] a half), the distance of the halves; the high word is fixed.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo = 0) {
+  return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16;
 }
 // kind::f16, fp32 accumulator, M x N: fp16 K-major operands; bf16 A (TMEM) with MN-major B
 __device__ __forceinline__ constexpr uint32_t idesc_s(int M, int N) {
@@ -190,17 +199,18 @@ __device__ __forceinline__ constexpr uint32_t idesc_s(int M, int N) {
 __device__ __forceinline__ constexpr uint32_t idesc_pv(int M, int N) {
   return idesc_s(M, N) | (1u << 7) | (1u << 10) | (1u << 16);
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+template <bool ACC>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "n"((int)ACC));
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc));
 }
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -265,7 +275,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 struct TcArgs {
-  CUtensorMap vmap;
+  CUtensorMap vmap, qmap;
   BatchArgs b;
 };
 
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     init(C::B_QFULL, 2 * MT * NQ + MT, 1);   // QFULL, QEMPTY, DONE
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == C::W_MMA) {
+  if (warp == C::W_MMA0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(C::TMEM_COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -386,8 +396,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 
   if (warp < 4 * MT) {
     // =============================== softmax: MMA tile t, row m of the item
-    const int t = warp >> 2, m = 128 * t + 32 * (warp & 3) + lane;
-    const int tok = m * v.rep_inv >> 16, hh = m - tok * v.rep;
+    const int t = warp >> 2, i0 = 32 * (warp & 3) + lane, tok0 = i0 * v.rep_inv >> 16;
+    const int tok = tok0 < v.half_rows ? t * v.half_rows + tok0 : INT_MAX, hh = i0 - tok0 * v.rep;   // INT_MAX: unused row
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_o = trow + D * t, t_sb = trow + C::TM_S + 128 * t;
     const float sl = 1.4426950408889634f * rsqrtf((float)D);
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       if (flags & kEnd) break;
       const int n = t == 1 && !(flags & kTwo) ? 0 : rec.tiles;
       if (flags & kFirst) {
-        mine = tok < rec.nrows && m < v.rb * v.rep;
+        mine = tok < rec.nrows;
         idle = !__any_sync(0xffffffffu, mine);
         qp = req < 0 ? INT_MAX - 1 : rec.pos0 + (mine ? tok : 0);
         lo = req < 0 ? -1 : qp - v.window;   // own keys at or below lo are seen as sinks only
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (whole && v.pre_len == 0) {
           dst = static_cast<__half*>(a.out) + head * D;
         } else {
-          const size_t at = whole ? (req < 0 ? 0 : (size_t)v.T * a.H) + head : (size_t)slot * a.part_rows + m;
+          const size_t at = whole ? (req < 0 ? 0 : (size_t)v.T * a.H) + head : (size_t)slot * a.part_rows + tok * v.rep + hh;
           po = (whole ? a.seg_o : a.part_o) + at * D;
           (whole ? a.seg_ml : a.part_ml)[at] = make_float2(mref, l);
         }
@@ -524,9 +534,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       fence_before();   // the next item's first PV overwrites O only after this warp's next P
     }
     if (!ok) give_up();
-  } else if (warp < C::W_META) {
+  } else if (warp == C::W_MMA0 || (MT == 2 && warp == C::W_MMA1)) {
     // =============================== MMA tile t: one thread issues its products
-    const int t = warp - C::W_MMA;
+    const int t = warp == C::W_MMA0 ? 0 : 1;
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
       // places of the next S and of the next PV product: window, tile in it, tile of the CTA (g), of
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           const int b = cp % NBS, st = gp % NV;
           fence_after();
           const bool first = jp == 0 && (fp & kFirst);
-          const uint64_t vd = desc_mnmajor(base + C::OFF_V + st * C::K_BYTES, 2048);
+          const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
           const uint32_t pa = tmem + C::TM_S + 128 * t + KT * b;
 #pragma unroll
           for (int k = 0; k < KP; ++k)      // 16 keys: a page
@@ -590,14 +600,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             (js > 0 || !(fs & kFirst) || mbar_test(bar(C::B_QFULL + t * NQ + qs % NQ), (qs / NQ) & 1))) {
           const int b = cs % NBS, st = gs % NK, qb = qs % NQ;
           fence_after();
-          const uint32_t qa = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE, kb = base + C::OFF_K + st * C::K_BYTES;
-#pragma unroll 1
-          for (int h = 0; h < D / 64; ++h) {
-            const uint64_t qd = desc_kmajor(qa + h * 16384), kd = desc_kmajor(kb + h * (KT * 128));
+          const uint32_t qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE), kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
+          const uint32_t to = tmem + C::TM_S + 128 * t + KT * b;
+          umma_ss<false>(to, qd, kd, id_s);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)     // 16 dims: 32 bytes
-              umma_ss(tmem + C::TM_S + 128 * t + KT * b, qd + 2 * k, kd + 2 * k, id_s, h + k != 0);
-          }
+          for (int k = 1; k < D / 16; ++k)  // 16 dims: 32 bytes; 64 dims: a half
+            umma_ss<true>(to, qd + (k >> 2) * (16384 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
           umma_commit(bar(C::B_SFULL + t * NBS + b));
           umma_commit(bar(C::B_KEMPTY + st));
           ++cs, ++gs;
@@ -614,8 +622,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (prog) {
           t_idle = 0;
         } else if (t_idle == 0) {
-          t_idle = gtimer();
-        } else if (gtimer() - t_idle > kWaitLimitNs) {
+          t_idle = cycles();
+        } else if (cycles() - t_idle > kWaitLimit) {
           atomicOr(a.flag, kBatchTimeout);
           ok = false;
         } else {
@@ -667,7 +675,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
           if (lane == 0) {
             WinRec& r = sRec[ws];
-            r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows * v.rep > 128 ? kTwo : 0) |
+            r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows > v.half_rows ? kTwo : 0) |
                       (w.j0 == 0 && w.j1 == w.nt ? kWhole : 0);
             r.tiles = n, r.req = w.b.req, r.row0 = w.b.row0, r.nrows = w.b.nrows, r.pos0 = w.b.pos0, r.g = w.g;
             r.slot = part_slot(blockIdx.x, w.start, w.x0);
@@ -713,7 +721,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     }
   } else if (warp == C::W_Q) {
     // =============================== q of the items into the A operands
-    uint32_t qi[MT] = {};
+    uint32_t qi[MT] = {};      // items asked for
+    const int tpt = v.half_rows;
     bool ok = true;
 #pragma unroll 1
     for (uint32_t win = 0; ok; ++win) {
@@ -722,41 +731,47 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       const WinRec& rec = sRec[win % NWIN];
       const int flags = rec.flags;
       if (flags & kEnd) break;
-      const int row0 = rec.row0, g = rec.g, rows = rec.nrows * v.rep;
+      const int row0 = rec.row0, g = rec.g, rows = rec.nrows;
       done_with(win);
       if (!(flags & kFirst)) continue;
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        if (rows <= 128 * t || !ok) continue;
-        const uint32_t q = qi[t]++, qb = q % NQ;
+        if (rows <= tpt * t || !ok) continue;
+        const uint32_t q = qi[t], qb = q % NQ;
         if (q >= NQ) {
           if (lane == 0) ok = wait(C::B_QEMPTY + t * NQ + qb, (q / NQ - 1) & 1);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
         }
-        const uint32_t dst = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE;
-        const int n = min(128, rows - 128 * t) * (D / 8);   // 16-byte chunks; rows behind the item's stay as they are
-#pragma unroll 1
-        for (int i = lane; i < n; i += 32) {
-          const int mr = i / (D / 8), ch = i % (D / 8), mm = 128 * t + mr, tok = mm * v.rep_inv >> 16;
-          const __half* src = static_cast<const __half*>(a.q) +
-                              ((size_t)(row0 + tok) * a.H + g * v.rep + mm - tok * v.rep) * D + 8 * ch;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (ch >> 3) * 16384 + sw128(mr, ch & 7)),
-                       "l"(src)
-                       : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_smem();
+        ++qi[t];
+        // boxes of 8 tokens x the rep heads x 64 dims; tokens behind the item's are read with them, rows
+        // of the operand behind the last box stay as they are (their results are not used)
+        const uint32_t dst = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE, full = bar(C::B_QFULL + t * NQ + qb);
+        const int boxes = pdiv(min(rows - t * tpt, tpt), 8);
+        if (lane == 0) mbar_expect_tx(full, boxes * (D / 64) * 8 * v.rep * 128);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_QFULL + t * NQ + qb));
+        for (int i = lane; i < boxes * (D / 64); i += 32) {
+          const int h = i % (D / 64), k = i / (D / 64);
+          tma_q(dst + h * 16384 + k * 8 * v.rep * 128, &ta.qmap, h, g * v.rep, row0 + t * tpt + 8 * k, full);
+        }
       }
     }
+    // at the end every box asked for has landed
+    if (lane == 0) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (uint32_t b = 0; b < NQ; ++b) {
+          const uint32_t n = (qi[t] + NQ - 1 - b) / NQ;
+          if (n) mbar_wait_on(bar(C::B_QFULL + t * NQ + b), (n - 1) & 1, 0, a.flag);
+        }
+    }
     if (!ok) give_up();
-  } else if (warp >= C::W_ROT) {
+  } else if (MT == 2 || warp != 4) {
     // =============================== K: load and rotate in place
     constexpr int CH = C::CH, PP = C::PP, PD = C::PD;
     constexpr int NP = PP < KP ? KP / PP : 1;   // pages of a tile per thread (none for the threads beyond, p0 >= KP)
-    const int rt = tid - C::W_ROT * 32, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
+    const int rt = C::rot(warp) * 32 + lane, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
     // (cos, sin) of r theta for the thread's 8 frequencies
     float4 off[4];
 #pragma unroll
@@ -765,6 +780,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     // the thread's two 16-byte chunks (dims 8c.. and their partners) of page 0 of a K and of a V stage
     const uint32_t k1 = base + C::OFF_K + sw128(r, c);
     const uint32_t k2 = base + C::OFF_K + (D == 128 ? KT * 128 + sw128(r, c) : sw128(r, c + CH));
+    uint8_t *sk1 = sm + (k1 - base), *sk2 = sm + (k2 - base);
     const uint32_t v1 = base + C::OFF_V + sw128(r, c);
     const uint32_t v2 = base + C::OFF_V + (D == 128 ? 2048 + sw128(r, c) : sw128(r, c + CH));
     // table rows: thread rt < KP D / 4 brings 16-byte chunk x of page rt / (D / 4) (thread c's e-th is
@@ -825,34 +841,50 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       if (!ok) break;
       const int4* pages = sPage + wt % NWIN * WIN + jt * KP;
       bool holes = false;
-#pragma unroll 2
-      for (int p = p0; p < KP; p += PP) {
-        const unsigned rows = (unsigned)pages[p].z;
-        const uint32_t to = st * C::K_BYTES + p * 2048;
-        const uint8_t* cs = sm + C::OFF_CS + (st * KP + p) * C::CS_ROW + c * 16;
-        uint32_t w1[4], w2[4], o1[4], o2[4];
-        lds128(k1 + to, w1);
-        lds128(k2 + to, w2);
+      // pages in pairs: the second one's loads under the first one's arithmetic
+      constexpr int NL = NP < 2 ? NP : 2;
+#pragma unroll 1
+      for (int q = 0; q < NP; q += NL) {
+        uint4 w1[NL], w2[NL];
+        float4 f[NL][4];   // (cos, sin) of P theta
+        unsigned rows[NL];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // (cos, sin) of P theta, two frequencies
-          const float4 f = *reinterpret_cast<const float4*>(cs + e * (CH * 16));
-          const float c0 = f.x * off[e].x - f.y * off[e].y, s0 = f.y * off[e].x + f.x * off[e].y;
-          const float c1 = f.z * off[e].z - f.w * off[e].w, s1 = f.w * off[e].z + f.z * off[e].w;
-          const float x0 = __uint_as_float(w1[e] << 16), x1 = __uint_as_float(w1[e] & 0xffff0000u);
-          const float y0 = __uint_as_float(w2[e] << 16), y1 = __uint_as_float(w2[e] & 0xffff0000u);
-          o1[e] = pack_f16x2(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
-          o2[e] = pack_f16x2(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
+        for (int u = 0; u < NL; ++u) {
+          const int p = p0 + (q + u) * PP;
+          if (PP > KP && p >= KP) break;
+          rows[u] = (unsigned)pages[p].z;
+          w1[u] = *reinterpret_cast<const uint4*>(sk1 + st * C::K_BYTES + p * 2048);
+          w2[u] = *reinterpret_cast<const uint4*>(sk2 + st * C::K_BYTES + p * 2048);
+          const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (st * KP + p) * C::CS_ROW) + c;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[u][e] = cs[e * CH];
         }
-        if (rows != 0xffffu) {
-          holes = true;
-          if (!(rows >> r & 1u)) {            // nothing was loaded here
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o1[e] = o2[e] = 0;
+        for (int u = 0; u < NL; ++u) {
+          const int p = p0 + (q + u) * PP;
+          if (PP > KP && p >= KP) break;
+          const uint32_t a1[4] = {w1[u].x, w1[u].y, w1[u].z, w1[u].w}, a2[4] = {w2[u].x, w2[u].y, w2[u].z, w2[u].w};
+          uint32_t o1[4], o2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 g = f[u][e];
+            const float c0 = g.x * off[e].x - g.y * off[e].y, s0 = g.y * off[e].x + g.x * off[e].y;
+            const float c1 = g.z * off[e].z - g.w * off[e].w, s1 = g.w * off[e].z + g.z * off[e].w;
+            const float x0 = __uint_as_float(a1[e] << 16), x1 = __uint_as_float(a1[e] & 0xffff0000u);
+            const float y0 = __uint_as_float(a2[e] << 16), y1 = __uint_as_float(a2[e] & 0xffff0000u);
+            o1[e] = pack_f16x2(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
+            o2[e] = pack_f16x2(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
           }
+          if (rows[u] != 0xffffu) {
+            holes = true;
+            if (!(rows[u] >> r & 1u)) {         // nothing was loaded here
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o1[e] = o2[e] = 0;
+            }
+          }
+          *reinterpret_cast<uint4*>(sk1 + st * C::K_BYTES + p * 2048) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+          *reinterpret_cast<uint4*>(sk2 + st * C::K_BYTES + p * 2048) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
         }
-        sts128(k1 + to, o1);
-        sts128(k2 + to, o2);
       }
       if (__any_sync(0xffffffffu, holes)) {   // rows of V without a key: P is 0 there, V must be finite
         ok = __all_sync(0xffffffffu, wait(C::B_VFULL + gt % NV, (gt / NV) & 1));
@@ -877,7 +909,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (warp == C::W_MMA)
+  if (warp == C::W_MMA0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
 }
 
@@ -907,6 +939,19 @@ bool page_map(CUtensorMap* m, const void* base, int blocks, int G, int D) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q [T][H][D] of fp16 as (64 dims, H heads, D / 64 halves, T rows); a box is one half of the rep heads
+// of a KV head of 8 rows, landing as [row][head][128 B].
+bool q_map(CUtensorMap* m, const BatchArgs& a) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)a.H, (cuuint64_t)(a.D / 64), (cuuint64_t)a.v.T};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.D * 2, 128, (cuuint64_t)a.H * a.D * 2};
+  const cuuint32_t estr[4] = {1, 1, 1, 1}, box[4] = {64, (cuuint32_t)a.v.rep, 1, 8};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename C>
 pic_status launch(const TcArgs& ta, cudaStream_t st) {
   static bool set[64] = {};
@@ -930,8 +975,9 @@ pic_status launch(const TcArgs& ta, cudaStream_t st) {
 void batch_tc_view(BatchView& v, int D) {
   const long long rows = (v.pre_len > 0 ? (long long)v.T : pdiv(v.T, v.n_reqs)) * v.rep;
   const bool two = rows > 128;
-  v.mrows = two ? 256 : 128;
-  v.rb = v.mrows / v.rep;
+  v.half_rows = 128 / v.rep & ~7;   // a box of q is 8 tokens
+  v.rb = two ? 2 * v.half_rows : v.half_rows;
+  v.mrows = v.rb * v.rep;
   v.rep_inv = (65535 + v.rep) / v.rep;
   v.kpages = KP;
   v.cost_item = 4;
@@ -943,10 +989,11 @@ void batch_tc_view(BatchView& v, int D) {
 pic_status launch_batch_tc(const BatchArgs& a, cudaStream_t st) {
   TcArgs ta;
   ta.b = a;
-  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D))
-    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the V pool");
-  if (a.D == 128) return a.v.mrows == 256 ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
-  return a.v.mrows == 256 ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
+  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a))
+    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the V pool or q");
+  const bool two = a.v.rb > a.v.half_rows;
+  if (a.D == 128) return two ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
+  return two ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
 }
 
 }  // namespace pic

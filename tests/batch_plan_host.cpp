@@ -20,6 +20,7 @@ int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const
   v.T = p[0], v.G = p[1], v.rep = p[2], v.stride = p[3], v.pre_len = p[4], v.pre_pages = p[5];
   v.window = p[6], v.sinks = p[7], v.pool_blocks = p[8], v.rope_positions = p[9];
   v.mrows = p[10], v.rb = p[10] / p[2], v.kpages = p[11], v.cost_item = p[12], v.cost_full = p[13], v.cost_half = p[14];
+  v.half_rows = v.rb / 2;
   const int grid = p[15];
   v.n_reqs = p[16];
   v.row_start = row_start, v.kv_len = kv_len, v.block_table = table, v.page_pos = page_pos, v.n_pages = n_pages;
