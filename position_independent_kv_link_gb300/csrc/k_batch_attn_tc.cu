@@ -6,31 +6,31 @@
 // through rings of stages in shared memory:
 //
 //   meta warp   walks the share: reads the page tables a window ahead, writes the windows' records
-//               (item, rows, pages with the rows that hold keys), and asks for V, one TMA box a page
-//               (16 rows x D, 128-byte swizzled, wherever the block lies: a page is one K = 16 step of
-//               the PV product, so pages need not be neighbours).
-//   rotation    copies K of its pages into the stages (cp.async, PD tiles ahead, each thread what it
-//               will rotate itself) and turns it in place: thread = row of a page x 8 pairs of dims; the
-//               angle of row r of a page at position P is composed from the table rows of P (shared
-//               memory, one row a page) and of r (registers), so that a key needs no table row of its
-//               own. bf16 -> fp16, one rounding (Q and K as fp16: 3 bits more than bf16 in S). Rows that
-//               hold no key any row of the block sees are zeroed in K and V.
-//   MMA warps   one issuing thread per MMA tile: O_t += P_t V of key tile j as soon as P_t(j) is
-//               written, S_t of tile j + 2 (Q_t K^T, fp16) into the S buffer that PV has just read (one
-//               thread's MMAs run in order), also across items.
-//   Q warp      asks for the items' rows of q, TMA boxes of 8 tokens x rep heads (double-buffered for
-//               one MMA tile, else when the item's last S product has retired).
+//               (item, rows, pages with the rows that hold keys), and asks for raw K, one TMA box a page
+//               wherever its block lies, with the RoPE table row of the page's position.
+//   load warp   asks for the items' rows of q (TMA boxes of 8 tokens x rep heads; double-buffered for
+//               one MMA tile, else when the item's last S product has retired) and for V, one box a
+//               page: a page is one K = 16 step of the PV product, so pages need not be neighbours.
+//   rotation    turns raw K into the fp16 operand: thread = row of a page x 8 pairs of dims; the angle
+//               of row r of a page at position P is composed from the table rows of P (shared memory,
+//               one row a page) and of r (registers), so that a key needs no table row of its own. One
+//               rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S). Rows that hold no
+//               key any row of the block sees are zeroed in K and V.
+//   S warp      one thread issues S_t = Q_t K^T (fp16) of a key tile for the MMA tiles, two S buffers each.
+//   PV warp     one thread issues O_t += P_t V (bf16, P from TMEM). Apart from the S warp, so that neither
+//               product waits behind the other's inputs: together in one thread the two cost some
+//               2100 cycles a tile, more in tests and jumps than in products.
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
 //               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 over the S columns
 //               (V is stored bf16 and both operands have one type; the sum is of the unrounded
 //               fp32 weights), and the item's result: out, or for parts of items and for prefix
 //               batches the normalized fp32 row with its maximum and sum for the merge.
 //
-// The roles' loops together are kept near the size of the instruction cache: with three times the
-// code every role ran at 8 cycles an instruction (ncu: no_instruction the largest stall).
+// The roles' loops are kept small, and few on each scheduler: with three times the code every role ran
+// at 8 cycles an instruction (ncu: no_instruction the largest stall). At the 5 that are left (a warp
+// on its own waits for its last result) the rotation's control is what is worth saving, hence TMA.
 //
-// MT = 1, eight rotation warps: few rows, HBM-bound. MT = 2, four: many rows; a K tile is loaded and
-// rotated once for 256 rows.
+// MT = 1: few rows, HBM-bound. MT = 2: many rows; a K tile is loaded and rotated once for 256 rows.
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
@@ -56,38 +56,38 @@ template <int D_, int MT_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
   static constexpr int NQ = MT == 2 ? 1 : 2;          // Q buffers per MMA tile
-  static constexpr int NK = D == 128 ? 4 : 6;         // K stages (and of table rows)
-  static constexpr int NV = NK;                       // V stages
-  static constexpr int PD = NK - 2;                   // K tiles on their way ahead of the one being rotated
-  static constexpr int NR = MT == 2 ? 4 : 8;          // rotation warps
+  static constexpr int NX = D == 128 ? 3 : 6;         // raw K stages (with table rows)
+  static constexpr int NK = D == 128 ? 2 : 3;         // K operand stages
+  static constexpr int NV = D == 128 ? 4 : 8;         // V stages
+  static constexpr int NR = 8;                        // rotation warps
   static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
   static constexpr int CH = D / 16, PP = NR * 32 / (16 * CH);   // rotation: threads of a row, pages at once
-  // Roles of the 16 warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
+  // Roles of the warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
   // instruction cache is shared by its warps: each scheduler gets as few roles as possible, and the
   // MMA threads one away from the rotation.
-  static constexpr int THREADS = 512;
-  static constexpr int W_MMA0 = MT == 2 ? 11 : 7, W_MMA1 = 15, W_META = MT == 2 ? 10 : 11, W_Q = MT == 2 ? 14 : 15;
-  // number of a rotation warp: MT 2: warps 8 9 12 13; MT 1: 5 6 8 9 10 12 13 14
-  static __device__ __forceinline__ int rot(int w) {
-    return MT == 2 ? (w & 1) + (w >> 1 & 2) : w < 8 ? w - 5 : w < 12 ? w - 6 : w - 7;
-  }
+  static constexpr int THREADS = MT == 2 ? 640 : 512;
+  static constexpr int W_S = MT == 2 ? 11 : 7, W_PV = MT == 2 ? 15 : 11, W_META = MT == 2 ? 19 : 15, W_LOAD = MT == 2 ? 18 : 6;
+  // number of a rotation warp: MT 2: 8 9 10 12 13 14 16 17; MT 1: 4 5 8 9 10 12 13 14
+  static __device__ __forceinline__ int rot(int w) { return MT == 2 ? w - (w >> 2) - 6 : w < 6 ? w - 4 : w - (w >> 2) - 4; }
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
   static constexpr int OFF_V = OFF_K + NK * K_BYTES;          // [NV] [page][64-dim half][16 keys][128 B]
-  static constexpr int OFF_CS = OFF_V + NV * K_BYTES;         // [NK][KP] table rows
-  static constexpr int OFF_REC = OFF_CS + NK * KP * CS_ROW;   // WinRec [NWIN]
+  static constexpr int OFF_X = OFF_V + NV * K_BYTES;          // [NX] likewise, raw K
+  static constexpr int OFF_CS = OFF_X + NX * K_BYTES;         // [NX][KP] table rows, [4][CH][16 B] each
+  static constexpr int OFF_REC = OFF_CS + NX * KP * CS_ROW;   // WinRec [NWIN]
   static constexpr int OFF_PAGE = OFF_REC + NWIN * 48;        // int4 [NWIN][WIN] page of the pool, position, rows
   static constexpr int OFF_LIM = OFF_PAGE + NWIN * WIN * 16;  // int2 [NWIN][WT] last key, first one behind the sinks
-  static constexpr int OFF_BAR = OFF_LIM + NWIN * WT * 8;
+  static constexpr int OFF_TILE = OFF_LIM + NWIN * WT * 8;    // int4 [NX] rows of the tile's pages, 16 bits each; the end
+  static constexpr int OFF_BAR = OFF_TILE + NX * 16;
   // barriers
-  static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_KLAND = B_RFREE + NWIN, B_READY = B_KLAND + NK, B_KEMPTY = B_READY + NK,
-                       B_VFULL = B_KEMPTY + NK, B_VEMPTY = B_VFULL + NV, B_SFULL = B_VEMPTY + NV,
-                       B_PREADY = B_SFULL + MT * NBS, B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS,
-                       B_QEMPTY = B_QFULL + MT * NQ, B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + MT;
+  static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_XFULL = B_RFREE + NWIN, B_XEMPTY = B_XFULL + NX,
+                       B_READY = B_XEMPTY + NX, B_KEMPTY = B_READY + NK, B_VFULL = B_KEMPTY + NK,
+                       B_VEMPTY = B_VFULL + NV, B_SFULL = B_VEMPTY + NV, B_PREADY = B_SFULL + MT * NBS,
+                       B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS, B_QEMPTY = B_QFULL + MT * NQ,
+                       B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + 2;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
-  static_assert(PD < NWIN, "a record is free before the rotation asks for it");
   // TMEM columns: O_t at D t, S buffer b of tile t at TM_S + 128 t + 64 b, its P over the first half
   static constexpr uint32_t TM_S = MT * D;
   static constexpr uint32_t TMEM_COLS = MT == 2 ? 512 : 256;
@@ -104,15 +104,16 @@ struct WinRec {           // 48 bytes
 
 // Every waiter of a barrier sees each of its phases before the next can complete (a parity wait
 // cannot tell phase n from n + 2). META, RFREE: a record is rewritten only when every warp that
-// reads records has arrived at RFREE for the window before in its slot. KLAND: every rotation thread
-// arrives with its copies of a tile and waits before it asks for the tile NK later. READY (MMA warps), KEMPTY:
-// rotation of tile j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows
-// PV of j; every MMA warp arrives at VEMPTY once per tile, after its wait for VFULL. SFULL, PREADY,
-// PVDONE: a ring between MMA thread t and warpgroup t; S(j + 2) follows PV(j), which waits for all
-// four warps' P(j). QFULL, QEMPTY: between the Q warp and MMA thread t.
-// No wait is for what waits in turn, windows of one tile being the tightest case: record i needs the
-// readers' passage of window i - NWIN and V of tile i - 3, that is the PV products of tile i - 3 - NV.
-// The rotation waits for record i before it turns tile i - PD, with PD < NWIN and PD < NV + 3.
+// reads records has arrived at RFREE for the window before in its slot. XFULL, XEMPTY: between the
+// meta warp and the rotation, all of whose warps arrive. READY (MMA warps), KEMPTY: rotation of tile
+// j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows PV of j. SFULL,
+// PREADY, PVDONE: a ring of the S warp, warpgroup t and the PV warp; S(j + 2) into a buffer follows the
+// end of PV(j), which waits for all four warps' P(j). QFULL, QEMPTY: between the load and the S warp.
+// No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN and raw K
+// of the tiles up to window i - 3, that is the rotation up to NX tiles before, that is the S products
+// NK tiles before that: with windows of one tile, of tile i - 3 - NX - NK at the latest, while its
+// readers are never more than two windows ahead of the S products. V and q of a tile wait for
+// products of earlier tiles only, the rotation of a tile with empty rows for its V.
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // SM clock cycles (reading the global timer instead takes long enough to delay every wait)
@@ -167,22 +168,13 @@ __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, uint32_
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort, unsigned* flag) {
   return mbar_test(bar, parity) || mbar_wait_on(bar, parity, abort, flag);   // a test is far cheaper than a try
 }
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int page, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
-      "[%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(page), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_q(uint32_t dst, const CUtensorMap* map, int half, int head, int row, uint32_t bar) {
+// 4-D box at (0, c1, c2, c3)
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int c1, int c2, int c3, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
       "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(head), "r"(half), "r"(row), "r"(bar)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t at, const uint32_t* x) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
 }
 // 16-byte chunk c (0..7) of row r of a [rows][128 B] tile, 128-byte swizzle (the TMA and UMMA layout)
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -275,7 +267,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 struct TcArgs {
-  CUtensorMap vmap, qmap;
+  CUtensorMap kmap, vmap, qmap, cmap;
   BatchArgs b;
 };
 
@@ -342,7 +334,7 @@ __device__ __noinline__ PageRaw fetch_page(const BatchView& v, const BatchBlock&
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_constant__ TcArgs ta) {
-  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NK = C::NK, NV = C::NV;
+  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NX = C::NX, NK = C::NK, NV = C::NV;
   const BatchArgs& a = ta.b;
   const BatchView& v = a.v;
   extern __shared__ uint8_t smem_raw[];
@@ -350,6 +342,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   WinRec* sRec = reinterpret_cast<WinRec*>(sm + C::OFF_REC);
   int4* sPage = reinterpret_cast<int4*>(sm + C::OFF_PAGE);
   int2* sLim = reinterpret_cast<int2*>(sm + C::OFF_LIM);
+  int4* sTile = reinterpret_cast<int4*>(sm + C::OFF_TILE);
   const uint32_t base = smem_u32(sm);
   auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
   __shared__ PlanShared s_plan;
@@ -371,19 +364,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       for (int k = 0; k < n; ++k) mbar_init(bar(i + k), count);
     };
     init(C::B_META, NWIN, 1);
-    init(C::B_RFREE, NWIN, 4 * MT + MT + 1 + C::NR);
-    init(C::B_KLAND, NK, C::NR * 32);
+    init(C::B_RFREE, NWIN, 4 * MT + 3);
+    init(C::B_XFULL, NX, 1);
+    init(C::B_XEMPTY, NX, C::NR);
     init(C::B_READY, NK, C::NR);
-    init(C::B_KEMPTY, NK, MT);
+    init(C::B_KEMPTY, NK, 1);
     init(C::B_VFULL, NV, 1);
-    init(C::B_VEMPTY, NV, MT);
+    init(C::B_VEMPTY, NV, 1);
     init(C::B_SFULL, MT * NBS, 1);
     init(C::B_PREADY, MT * NBS, 4);
     init(C::B_PVDONE, MT * NBS, 1);
-    init(C::B_QFULL, 2 * MT * NQ + MT, 1);   // QFULL, QEMPTY, DONE
+    init(C::B_QFULL, 2 * MT * NQ + 2, 1);   // QFULL, QEMPTY, DONE
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == C::W_MMA0) {
+  if (warp == C::W_S) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(C::TMEM_COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -534,122 +528,110 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       fence_before();   // the next item's first PV overwrites O only after this warp's next P
     }
     if (!ok) give_up();
-  } else if (warp == C::W_MMA0 || (MT == 2 && warp == C::W_MMA1)) {
-    // =============================== MMA tile t: one thread issues its products
-    const int t = warp == C::W_MMA0 ? 0 : 1;
+  } else if (warp == C::W_S) {
+    // =============================== S products
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
-      // places of the next S and of the next PV product: window, tile in it, tile of the CTA (g), of
-      // this MMA tile (c)
-      uint32_t ws = 0, wp = 0, gs = 0, gp = 0, cs = 0, cp = 0, qs = 0;
-      int ns = 0, np = 0, js = 0, jp = 0, fs = 0, fp = 0;
-      bool ok = wait_meta(0);
-      // the first window, or the one after: its flags (kEnd: none)
-      auto enter = [&](uint32_t w, int& n, int& f) {
-        ok = wait_meta(w);
-        f = ok ? sRec[w % NWIN].flags : kEnd;
-        n = f & kEnd ? 0 : sRec[w % NWIN].tiles;
-      };
-      if (ok) {
-        enter(0, ns, fs);
-        fp = fs, np = ns;
-      }
-      unsigned long long t_idle = 0;
+      constexpr uint32_t id_s = idesc_s(128, KT);
+      uint32_t gt = 0, ct[MT] = {}, qi[MT] = {};   // tiles of the CTA, of the MMA tiles; items of them
+      bool ok = true;
 #pragma unroll 1
-      while (ok && !(fp & kEnd)) {
-        bool prog = false;
-        if (t == 1 && !(fp & kTwo)) {
-          // no rows for this MMA tile: its share of the stages is released (the S walk is here too)
-          const int sk = gp % NK, sv = gp % NV;
-          ok = wait(C::B_READY + sk, (gp / NK) & 1) && wait(C::B_VFULL + sv, (gp / NV) & 1);
+      for (uint32_t win = 0; ok; ++win) {
+        ok = wait_meta(win);
+        if (!ok) break;
+        const int flags = sRec[win % NWIN].flags, n = sRec[win % NWIN].tiles;
+        if (flags & kEnd) break;
+        mbar_arrive(bar(C::B_RFREE + win % NWIN));
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++gt) {
+          const int st = gt % NK;
+          ok = wait(C::B_READY + st, (gt / NK) & 1);
           if (!ok) break;
-          mbar_arrive(bar(C::B_KEMPTY + sk));
-          mbar_arrive(bar(C::B_VEMPTY + sv));
-          ++gs, ++js, ++gp;
-          if (++jp == np) {
-            mbar_arrive(bar(C::B_RFREE + wp % NWIN));
-            enter(++wp, np, fp);
-            ws = wp, ns = np, fs = fp, js = jp = 0;
-          }
-          continue;
-        }
-        if (cp < cs && mbar_test(bar(C::B_PREADY + t * NBS + cp % NBS), (cp / NBS) & 1) &&
-            mbar_test(bar(C::B_VFULL + gp % NV), (gp / NV) & 1)) {   // PV
-          const int b = cp % NBS, st = gp % NV;
-          fence_after();
-          const bool first = jp == 0 && (fp & kFirst);
-          const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
-          const uint32_t pa = tmem + C::TM_S + 128 * t + KT * b;
+          const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
 #pragma unroll
-          for (int k = 0; k < KP; ++k)      // 16 keys: a page
-            umma_ts(tmem + D * t, pa + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
-          umma_commit(bar(C::B_PVDONE + t * NBS + b));
-          umma_commit(bar(C::B_VEMPTY + st));
-          ++cp, ++gp;
-          if (++jp == np) {
-            mbar_arrive(bar(C::B_RFREE + wp % NWIN));
-            enter(++wp, np, fp);
-            jp = 0;
-            if (t == 1 && !(fp & kTwo)) ws = wp, ns = np, fs = fp, js = 0;   // the S walk has waited here
-          }
-          prog = true;
-        }
-        // S, at most NBS tiles ahead, not beyond a window without rows for this MMA tile
-        if (ok && !(fs & kEnd) && !(t == 1 && !(fs & kTwo)) && cs < cp + NBS &&
-            mbar_test(bar(C::B_READY + gs % NK), (gs / NK) & 1) &&
-            (js > 0 || !(fs & kFirst) || mbar_test(bar(C::B_QFULL + t * NQ + qs % NQ), (qs / NQ) & 1))) {
-          const int b = cs % NBS, st = gs % NK, qb = qs % NQ;
-          fence_after();
-          const uint32_t qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE), kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
-          const uint32_t to = tmem + C::TM_S + 128 * t + KT * b;
-          umma_ss<false>(to, qd, kd, id_s);
+          for (int t = 0; t < MT; ++t) {
+            if (t == 1 && !(flags & kTwo)) continue;
+            const int b = ct[t] % NBS, qb = qi[t] % NQ;
+            if (j == 0 && (flags & kFirst)) ok = ok && wait(C::B_QFULL + t * NQ + qb, (qi[t] / NQ) & 1);
+            // the buffer's P has been used; the first round's waits return at once
+            ok = ok && wait(C::B_PVDONE + t * NBS + b, (ct[t] / NBS + 1) & 1);
+            if (!ok) break;
+            fence_after();
+            const uint32_t qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
+            const uint32_t to = tmem + C::TM_S + 128 * t + KT * b;
+            umma_ss<false>(to, qd, kd, id_s);
 #pragma unroll
-          for (int k = 1; k < D / 16; ++k)  // 16 dims: 32 bytes; 64 dims: a half
-            umma_ss<true>(to, qd + (k >> 2) * (16384 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
-          umma_commit(bar(C::B_SFULL + t * NBS + b));
-          umma_commit(bar(C::B_KEMPTY + st));
-          ++cs, ++gs;
-          if (++js == ns) {
-            if (fs & kLast) {
+            for (int k = 1; k < D / 16; ++k)  // 16 dims: 32 bytes; 64 dims: a half
+              umma_ss<true>(to, qd + (k >> 2) * (16384 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
+            umma_commit(bar(C::B_SFULL + t * NBS + b));
+            ++ct[t];
+            if (j == n - 1 && (flags & kLast)) {
               umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
-              ++qs;
+              ++qi[t];
             }
-            enter(++ws, ns, fs);
-            js = 0;
           }
-          prog = true;
-        }
-        if (prog) {
-          t_idle = 0;
-        } else if (t_idle == 0) {
-          t_idle = cycles();
-        } else if (cycles() - t_idle > kWaitLimit) {
-          atomicOr(a.flag, kBatchTimeout);
-          ok = false;
-        } else {
-          uint32_t gone;
-          asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(gone) : "r"(abort) : "memory");
-          ok = !gone;
+          if (!ok) break;
+          umma_commit(bar(C::B_KEMPTY + st));
         }
       }
       if (!ok) give_up();
-      umma_commit(bar(C::B_DONE + t));   // fires once every MMA of this thread has retired
-      mbar_wait_on(bar(C::B_DONE + t), 0, 0, a.flag);
+      umma_commit(bar(C::B_DONE));   // fires once every MMA of this thread has retired
+      mbar_wait_on(bar(C::B_DONE), 0, 0, a.flag);
+    }
+  } else if (warp == C::W_PV) {
+    // =============================== PV products
+    if (lane == 0) {
+      constexpr uint32_t id_pv = idesc_pv(128, D);
+      uint32_t gt = 0, ct[MT] = {};
+      bool ok = true;
+#pragma unroll 1
+      for (uint32_t win = 0; ok; ++win) {
+        ok = wait_meta(win);
+        if (!ok) break;
+        const int flags = sRec[win % NWIN].flags, n = sRec[win % NWIN].tiles;
+        if (flags & kEnd) break;
+        mbar_arrive(bar(C::B_RFREE + win % NWIN));
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++gt) {
+          const int st = gt % NV;
+          const bool first = j == 0 && (flags & kFirst);
+          const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
+          ok = wait(C::B_VFULL + st, (gt / NV) & 1);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            if (t == 1 && !(flags & kTwo)) continue;
+            const int b = ct[t] % NBS;
+            ok = ok && wait(C::B_PREADY + t * NBS + b, (ct[t] / NBS) & 1);
+            if (!ok) break;
+            fence_after();
+            const uint32_t pa = tmem + C::TM_S + 128 * t + KT * b;
+#pragma unroll
+            for (int k = 0; k < KP; ++k)      // 16 keys: a page
+              umma_ts(tmem + D * t, pa + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
+            umma_commit(bar(C::B_PVDONE + t * NBS + b));
+            ++ct[t];
+          }
+          if (!ok) break;
+          umma_commit(bar(C::B_VEMPTY + st));
+        }
+      }
+      if (!ok) give_up();
+      umma_commit(bar(C::B_DONE + 1));
+      mbar_wait_on(bar(C::B_DONE + 1), 0, 0, a.flag);
     }
   } else if (warp == C::W_META) {
-    // =============================== window records, V
+    // =============================== window records, raw K
     // Lane i holds page i of a window. `next`: the tables' entries of the window after the last one
     // written (the same item's or the next one's), on their way.
     Walk w;
     bool more = w.begin(a, share_, s_plan.block), ok = true;
     unsigned bad = 0;
     int j = more ? w.j0 : 0;             // next tile to be described
-    uint32_t n_win = 0, gt = 0;          // windows written, tiles whose V is asked for
+    uint32_t n_win = 0, gt = 0;          // windows written, tiles whose K is asked for
     PageRaw next{0, 0, 0};
     if (more) next = fetch_page(v, w.b, j * KP + lane);
     bool ended = false;
 #pragma unroll 1
-    for (uint32_t win = 0; ok;) {        // V of window win, when the two after it are described
+    for (uint32_t win = 0; ok;) {        // K of window win, when the two after it are described
       if (!ended && n_win < win + 3) {
         const int ws = n_win % NWIN;
         if (lane == 0) ok = n_win < NWIN || wait(C::B_RFREE + ws, (n_win / NWIN - 1) & 1);
@@ -692,36 +674,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         ++n_win;
         continue;
       }
-      if (sRec[win % NWIN].flags & kEnd) break;
-      const int n = sRec[win % NWIN].tiles;
+      const bool end = sRec[win % NWIN].flags & kEnd;
+      const int n = end ? 1 : sRec[win % NWIN].tiles;   // the end: a tile without pages, for the rotation to see
       const int4 pg = sPage[win % NWIN * WIN + lane];
       ++win;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++gt) {
-        const int st = gt % NV;
-        if (lane == 0) ok = gt < NV || wait(C::B_VEMPTY + st, (gt / NV - 1) & 1);
+        const int st = gt % NX;
+        if (lane == 0) ok = gt < NX || wait(C::B_XEMPTY + st, (gt / NX - 1) & 1);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        const bool live = lane / KP == i && pg.z != 0;
+        const bool live = !end && lane / KP == i && pg.z != 0;
         const unsigned who = __ballot_sync(0xffffffffu, live);
-        if (lane == 0) mbar_expect_tx(bar(C::B_VFULL + st), (uint32_t)__popc(who) * C::PAGE_BYTES);
+        // the pages' rows, from the lanes that hold them
+        const unsigned r0 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP), r1 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 1);
+        const unsigned r2 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 2), r3 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 3);
+        if (lane == 0) {
+          sTile[st] = make_int4((int)(r0 | r1 << 16), (int)(r2 | r3 << 16), end, 0);
+          mbar_expect_tx(bar(C::B_XFULL + st), (uint32_t)__popc(who) * (C::PAGE_BYTES + C::CS_ROW));
+        }
         __syncwarp();
-        if (live) tma_page(base + C::OFF_V + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.vmap, pg.x, bar(C::B_VFULL + st));
+        if (live) {
+          tma_4d(base + C::OFF_X + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.kmap, 0, 0, pg.x, bar(C::B_XFULL + st));
+          tma_4d(base + C::OFF_CS + (st * KP + lane % KP) * C::CS_ROW, &ta.cmap, 0, 0, pg.y, bar(C::B_XFULL + st));
+        }
       }
+      if (end) break;
     }
     if (!ok) give_up();
     batch_flag(a.flag, bad);
     // every copy has landed before the shared memory is given up (at once on the normal path)
     if (lane == 0) {
 #pragma unroll 1
-      for (uint32_t s = 0; s < NV; ++s) {
-        const uint32_t n = (gt + NV - 1 - s) / NV;
-        if (n) mbar_wait_on(bar(C::B_VFULL + s), (n - 1) & 1, 0, a.flag);
+      for (uint32_t s = 0; s < NX; ++s) {
+        const uint32_t n = (gt + NX - 1 - s) / NX;
+        if (n) mbar_wait_on(bar(C::B_XFULL + s), (n - 1) & 1, 0, a.flag);
       }
     }
-  } else if (warp == C::W_Q) {
-    // =============================== q of the items into the A operands
-    uint32_t qi[MT] = {};      // items asked for
+  } else if (warp == C::W_LOAD) {
+    // =============================== q of the items into the A operands, V
+    uint32_t qi[MT] = {}, gt = 0;   // items, tiles asked for
     const int tpt = v.half_rows;
     bool ok = true;
 #pragma unroll 1
@@ -731,33 +723,54 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       const WinRec& rec = sRec[win % NWIN];
       const int flags = rec.flags;
       if (flags & kEnd) break;
-      const int row0 = rec.row0, g = rec.g, rows = rec.nrows;
+      const int row0 = rec.row0, g = rec.g, rows = rec.nrows, n = rec.tiles;
+      const int4 pg = sPage[win % NWIN * WIN + lane];
       done_with(win);
-      if (!(flags & kFirst)) continue;
+      if (flags & kFirst) {
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        if (rows <= tpt * t || !ok) continue;
-        const uint32_t q = qi[t], qb = q % NQ;
-        if (q >= NQ) {
-          if (lane == 0) ok = wait(C::B_QEMPTY + t * NQ + qb, (q / NQ - 1) & 1);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-        }
-        ++qi[t];
-        // boxes of 8 tokens x the rep heads x 64 dims; tokens behind the item's are read with them, rows
-        // of the operand behind the last box stay as they are (their results are not used)
-        const uint32_t dst = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE, full = bar(C::B_QFULL + t * NQ + qb);
-        const int boxes = pdiv(min(rows - t * tpt, tpt), 8);
-        if (lane == 0) mbar_expect_tx(full, boxes * (D / 64) * 8 * v.rep * 128);
-        __syncwarp();
-        for (int i = lane; i < boxes * (D / 64); i += 32) {
-          const int h = i % (D / 64), k = i / (D / 64);
-          tma_q(dst + h * 16384 + k * 8 * v.rep * 128, &ta.qmap, h, g * v.rep, row0 + t * tpt + 8 * k, full);
+        for (int t = 0; t < MT; ++t) {
+          if (rows <= tpt * t || !ok) continue;
+          const uint32_t q = qi[t], qb = q % NQ;
+          if (q >= NQ) {
+            if (lane == 0) ok = wait(C::B_QEMPTY + t * NQ + qb, (q / NQ - 1) & 1);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+          }
+          ++qi[t];
+          // tokens behind the item's are read with the last box, rows of the operand behind it stay as
+          // they are (their results are not used)
+          const uint32_t dst = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE, full = bar(C::B_QFULL + t * NQ + qb);
+          const int boxes = pdiv(min(rows - t * tpt, tpt), 8);
+          if (lane == 0) mbar_expect_tx(full, boxes * (D / 64) * 8 * v.rep * 128);
+          __syncwarp();
+          for (int i = lane; i < boxes * (D / 64); i += 32) {
+            const int h = i % (D / 64), k = i / (D / 64);
+            tma_4d(dst + h * 16384 + k * 8 * v.rep * 128, &ta.qmap, g * v.rep, h, row0 + t * tpt + 8 * k, full);
+          }
         }
       }
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const int st = gt % NV;
+        if (lane == 0) ok = gt < NV || wait(C::B_VEMPTY + st, (gt / NV - 1) & 1);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const bool live = lane / KP == i && pg.z != 0;
+        const unsigned who = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) mbar_expect_tx(bar(C::B_VFULL + st), (uint32_t)__popc(who) * C::PAGE_BYTES);
+        __syncwarp();
+        if (live) tma_4d(base + C::OFF_V + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.vmap, 0, 0, pg.x, bar(C::B_VFULL + st));
+        ++gt;
+      }
     }
+    if (!ok) give_up();
     // at the end every box asked for has landed
     if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t s = 0; s < NV; ++s) {
+        const uint32_t n = (gt + NV - 1 - s) / NV;
+        if (n) mbar_wait_on(bar(C::B_VFULL + s), (n - 1) & 1, 0, a.flag);
+      }
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -766,150 +779,95 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           if (n) mbar_wait_on(bar(C::B_QFULL + t * NQ + b), (n - 1) & 1, 0, a.flag);
         }
     }
-    if (!ok) give_up();
-  } else if (MT == 2 || warp != 4) {
-    // =============================== K: load and rotate in place
-    constexpr int CH = C::CH, PP = C::PP, PD = C::PD;
-    constexpr int NP = PP < KP ? KP / PP : 1;   // pages of a tile per thread (none for the threads beyond, p0 >= KP)
+  } else {
+    // =============================== raw K to the K operand
+    constexpr int CH = C::CH, PP = C::PP, NP = KP / PP;   // pages of a tile per thread
+    static_assert(KP % PP == 0, "");
     const int rt = C::rot(warp) * 32 + lane, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
     // (cos, sin) of r theta for the thread's 8 frequencies
     float4 off[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) off[e] = reinterpret_cast<const float4*>(a.rope_cs + (size_t)r * (D / 2) + 8 * c)[e];
-    const __nv_bfloat16* kl = static_cast<const __nv_bfloat16*>(a.k_layer) + r * D + 8 * c;
-    // the thread's two 16-byte chunks (dims 8c.. and their partners) of page 0 of a K and of a V stage
-    const uint32_t k1 = base + C::OFF_K + sw128(r, c);
-    const uint32_t k2 = base + C::OFF_K + (D == 128 ? KT * 128 + sw128(r, c) : sw128(r, c + CH));
-    uint8_t *sk1 = sm + (k1 - base), *sk2 = sm + (k2 - base);
-    const uint32_t v1 = base + C::OFF_V + sw128(r, c);
-    const uint32_t v2 = base + C::OFF_V + (D == 128 ? 2048 + sw128(r, c) : sw128(r, c + CH));
-    // table rows: thread rt < KP D / 4 brings 16-byte chunk x of page rt / (D / 4) (thread c's e-th is
-    // 4 c + e) to place e CH + c, so that the threads that use it read neighbouring chunks
-    const int cp_ = rt / (D / 4), cx = rt % (D / 4);
-    const uint32_t cs_to = base + C::OFF_CS + cp_ * C::CS_ROW + ((cx & 3) * CH + (cx >> 2)) * 16;
-    uint32_t end = 0x7fffffffu;               // tiles in all, once known
-    uint32_t wi = 0, wt = 0;                  // windows of the tile asked for, of the tile turned
-    int ji = 0, ni = 0, jt = 0, nt = 0;
+    // the thread's two 16-byte chunks (dims 8c.. and their partners): of its first page of a raw K or V
+    // stage, and of a K stage
+    const int x1 = p0 * C::PAGE_BYTES + sw128(r, c), x2 = D == 128 ? x1 + 2048 : p0 * C::PAGE_BYTES + sw128(r, c + CH);
+    const int k1 = p0 * 2048 + sw128(r, c), k2 = D == 128 ? KT * 128 + k1 : p0 * 2048 + sw128(r, c + CH);
+    const int shift = p0 % 2 * 16 + r;
     bool ok = true;
+    uint32_t sx = 0, px = 0, sk = 0, pk = 1;   // stages and their parities
 #pragma unroll 1
-    for (uint32_t i = 0; i < end + PD; ++i) {
-      if (i < end) {                          // ask for tile i
-        if (ji == ni) {
-          if (i > 0) ++wi;
-          ok = __all_sync(0xffffffffu, wait_meta(wi));
-          if (!ok) break;
-          ji = 0;
-          ni = sRec[wi % NWIN].tiles;
-          if (sRec[wi % NWIN].flags & kEnd) end = i;
-        }
-        if (i < end) {
-          const int st = i % NK;
-          ok = __all_sync(0xffffffffu, i < NK || wait(C::B_KEMPTY + st, (i / NK - 1) & 1));
-          if (!ok) break;
-          const int4* pages = sPage + wi % NWIN * WIN + ji * KP;
-          if (cp_ < KP) {
-            const int4 pg = pages[cp_];
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(cs_to + st * KP * C::CS_ROW),
-                         "l"(reinterpret_cast<const float4*>(a.rope_cs + (size_t)pg.y * (D / 2)) + cx)
-                         : "memory");
-          }
-#pragma unroll
-          for (int q = 0; q < NP; ++q) {
-            const int p = p0 + q * PP;
-            const int4 pg = pages[min(p, KP - 1)];
-            if (p < KP && ((unsigned)pg.z >> r & 1u)) {
-              const __nv_bfloat16* src = kl + (size_t)pg.x * (kPage * D);
-              const uint32_t to = st * C::K_BYTES + p * 2048;
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(k1 + to), "l"(src) : "memory");
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(k2 + to), "l"(src + D / 2) : "memory");
-            }
-          }
-          ++ji;
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(C::B_KLAND + st)) : "memory");
-        }
-      }
-      if (i < PD) continue;
-      const uint32_t gt = i - PD;             // turn tile i - PD
-      if (gt >= end) break;
-      if (jt == nt) {
-        if (gt > 0) ++wt;
-        jt = 0;
-        nt = sRec[wt % NWIN].tiles;
-      }
-      const int st = gt % NK;
-      ok = __all_sync(0xffffffffu, wait(C::B_KLAND + st, (gt / NK) & 1));   // everyone's K and table rows
+    for (uint32_t gt = 0;; ++gt) {
+      ok = __all_sync(0xffffffffu, wait(C::B_XFULL + sx, px));
       if (!ok) break;
-      const int4* pages = sPage + wt % NWIN * WIN + jt * KP;
-      bool holes = false;
-      // pages in pairs: the second one's loads under the first one's arithmetic
-      constexpr int NL = NP < 2 ? NP : 2;
-#pragma unroll 1
-      for (int q = 0; q < NP; q += NL) {
-        uint4 w1[NL], w2[NL];
-        float4 f[NL][4];   // (cos, sin) of P theta
-        unsigned rows[NL];
+      const int4 tile = sTile[sx];
+      if (tile.z) break;
+      const bool holes = (tile.x & tile.y) != -1;
+      const uint8_t* xs = sm + C::OFF_X + sx * C::K_BYTES;
+      const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (sx * KP + p0) * C::CS_ROW) + c;
+      uint4 w1[NP], w2[NP];
+      float4 f[NP][4];   // (cos, sin) of P theta
 #pragma unroll
-        for (int u = 0; u < NL; ++u) {
-          const int p = p0 + (q + u) * PP;
-          if (PP > KP && p >= KP) break;
-          rows[u] = (unsigned)pages[p].z;
-          w1[u] = *reinterpret_cast<const uint4*>(sk1 + st * C::K_BYTES + p * 2048);
-          w2[u] = *reinterpret_cast<const uint4*>(sk2 + st * C::K_BYTES + p * 2048);
-          const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (st * KP + p) * C::CS_ROW) + c;
+      for (int u = 0; u < NP; ++u) {
+        w1[u] = *reinterpret_cast<const uint4*>(xs + x1 + u * PP * C::PAGE_BYTES);
+        w2[u] = *reinterpret_cast<const uint4*>(xs + x2 + u * PP * C::PAGE_BYTES);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f[u][e] = cs[e * CH];
-        }
-#pragma unroll
-        for (int u = 0; u < NL; ++u) {
-          const int p = p0 + (q + u) * PP;
-          if (PP > KP && p >= KP) break;
-          const uint32_t a1[4] = {w1[u].x, w1[u].y, w1[u].z, w1[u].w}, a2[4] = {w2[u].x, w2[u].y, w2[u].z, w2[u].w};
-          uint32_t o1[4], o2[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 g = f[u][e];
-            const float c0 = g.x * off[e].x - g.y * off[e].y, s0 = g.y * off[e].x + g.x * off[e].y;
-            const float c1 = g.z * off[e].z - g.w * off[e].w, s1 = g.w * off[e].z + g.z * off[e].w;
-            const float x0 = __uint_as_float(a1[e] << 16), x1 = __uint_as_float(a1[e] & 0xffff0000u);
-            const float y0 = __uint_as_float(a2[e] << 16), y1 = __uint_as_float(a2[e] & 0xffff0000u);
-            o1[e] = pack_f16x2(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
-            o2[e] = pack_f16x2(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
-          }
-          if (rows[u] != 0xffffu) {
-            holes = true;
-            if (!(rows[u] >> r & 1u)) {         // nothing was loaded here
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o1[e] = o2[e] = 0;
-            }
-          }
-          *reinterpret_cast<uint4*>(sk1 + st * C::K_BYTES + p * 2048) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-          *reinterpret_cast<uint4*>(sk2 + st * C::K_BYTES + p * 2048) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-        }
+        for (int e = 0; e < 4; ++e) f[u][e] = cs[u * PP * (D / 4) + e * CH];
       }
-      if (__any_sync(0xffffffffu, holes)) {   // rows of V without a key: P is 0 there, V must be finite
+      uint4 y1[NP], y2[NP];
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        const uint32_t a1[4] = {w1[u].x, w1[u].y, w1[u].z, w1[u].w}, a2[4] = {w2[u].x, w2[u].y, w2[u].z, w2[u].w};
+        uint32_t o1[4], o2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 g = f[u][e];
+          const float c0 = g.x * off[e].x - g.y * off[e].y, s0 = g.y * off[e].x + g.x * off[e].y;
+          const float c1 = g.z * off[e].z - g.w * off[e].w, s1 = g.w * off[e].z + g.z * off[e].w;
+          const float q0 = __uint_as_float(a1[e] << 16), q1 = __uint_as_float(a1[e] & 0xffff0000u);
+          const float z0 = __uint_as_float(a2[e] << 16), z1 = __uint_as_float(a2[e] & 0xffff0000u);
+          o1[e] = pack_f16x2(q0 * c0 - z0 * s0, q1 * c1 - z1 * s1);
+          o2[e] = pack_f16x2(z0 * c0 + q0 * s0, z1 * c1 + q1 * s1);
+        }
+        y1[u] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+        y2[u] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+      }
+      if (holes) {
+        // rows without a key: K is zero, and V must be finite (P is 0 there)
         ok = __all_sync(0xffffffffu, wait(C::B_VFULL + gt % NV, (gt / NV) & 1));
         if (!ok) break;
-        const uint32_t zero[4] = {0, 0, 0, 0};
-#pragma unroll 1
-        for (int p = p0; p < KP; p += PP)
-          if (!((unsigned)pages[p].z >> r & 1u)) {
-            const uint32_t to = gt % NV * C::K_BYTES + p * C::PAGE_BYTES;
-            sts128(v1 + to, zero);
-            sts128(v2 + to, zero);
-          }
+        uint8_t* vs = sm + C::OFF_V + gt % NV * C::K_BYTES;
+#pragma unroll
+        for (int u = 0; u < NP; ++u) {
+          const int p = p0 + u * PP;
+          if ((unsigned)(p < 2 ? tile.x : tile.y) >> shift & 1u) continue;
+          y1[u] = y2[u] = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vs + x1 + u * PP * C::PAGE_BYTES) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vs + x2 + u * PP * C::PAGE_BYTES) = make_uint4(0, 0, 0, 0);
+        }
       }
-      fence_async_smem();   // the MMAs read these rows through the async proxy
+      ok = __all_sync(0xffffffffu, wait(C::B_KEMPTY + sk, pk));   // the first round's waits return at once
+      if (!ok) break;
+      uint8_t* ks = sm + C::OFF_K + sk * C::K_BYTES;
+#pragma unroll
+      for (int u = 0; u < NP; ++u) {
+        *reinterpret_cast<uint4*>(ks + k1 + u * PP * 2048) = y1[u];
+        *reinterpret_cast<uint4*>(ks + k2 + u * PP * 2048) = y2[u];
+      }
+      fence_async_smem();   // the MMAs read these rows through the async proxy, TMA rewrites the raw ones
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_READY + st));
-      if (++jt == nt) done_with(wt);
+      if (lane == 0) {
+        mbar_arrive(bar(C::B_READY + sk));
+        mbar_arrive(bar(C::B_XEMPTY + sx));
+      }
+      if (++sx == NX) sx = 0, px ^= 1;
+      if (++sk == NK) sk = 0, pk ^= 1;
     }
     if (!ok) give_up();
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (warp == C::W_MMA0)
+  if (warp == C::W_S)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
 }
 
@@ -943,13 +901,25 @@ bool page_map(CUtensorMap* m, const void* base, int blocks, int G, int D) {
 // of a KV head of 8 rows, landing as [row][head][128 B].
 bool q_map(CUtensorMap* m, const BatchArgs& a) {
   auto enc = encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[4] = {64, (cuuint64_t)a.H, (cuuint64_t)(a.D / 64), (cuuint64_t)a.v.T};
   const cuuint64_t strides[3] = {(cuuint64_t)a.D * 2, 128, (cuuint64_t)a.H * a.D * 2};
   const cuuint32_t estr[4] = {1, 1, 1, 1}, box[4] = {64, (cuuint32_t)a.v.rep, 1, 8};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The RoPE table [positions][D / 2] of (cos, sin) as (4 floats, D / 16 threads' chunks, 4 chunks of a
+// thread, positions): a box is one row with its 16-byte chunks ordered [chunk of a thread][thread], so
+// that the rotation's threads read neighbouring ones (no bank conflicts).
+bool cs_map(CUtensorMap* m, const BatchArgs& a) {
+  auto enc = encode_fn();
+  const cuuint64_t dims[4] = {4, (cuuint64_t)(a.D / 16), 4, (cuuint64_t)a.v.rope_positions};
+  const cuuint64_t strides[3] = {64, 16, (cuuint64_t)a.D * 4};
+  const cuuint32_t estr[4] = {1, 1, 1, 1}, box[4] = {4, (cuuint32_t)(a.D / 16), 4, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, (void*)a.rope_cs, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename C>
@@ -989,8 +959,9 @@ void batch_tc_view(BatchView& v, int D) {
 pic_status launch_batch_tc(const BatchArgs& a, cudaStream_t st) {
   TcArgs ta;
   ta.b = a;
-  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a))
-    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the V pool or q");
+  if (!page_map(&ta.kmap, a.k_layer, a.v.pool_blocks, a.v.G, a.D) ||
+      !page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a) || !cs_map(&ta.cmap, a))
+    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the pools, q or the RoPE table");
   const bool two = a.v.rb > a.v.half_rows;
   if (a.D == 128) return two ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
   return two ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
