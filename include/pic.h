@@ -480,11 +480,13 @@ pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_
                                int32_t rope_positions, void* q_out, void* k_layer, void* v_layer, int32_t pool_blocks,
                                pic_stream_t stream);
 
-/* Scratch of the two attention calls below; prefix_len 0 for pic_op_attention_window. 0 for
- * shapes they refuse. The scratch need not be initialised and is free again when the call's work
- * is done. */
+/* Scratch of the two attention calls below; prefix_len and prefix_pages 0 for
+ * pic_op_attention_window. 0 for shapes they refuse. The scratch need not be initialised and is
+ * free again when the call's work is done. (bf16 batches with many rows per request, or behind
+ * a prefix, keep the rotated K of their pages in it: up to 1 GB for each.) */
 size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_reqs, int32_t n_heads,
-                                            int32_t n_kv_heads, int32_t head_dim, int32_t prefix_len);
+                                            int32_t n_kv_heads, int32_t head_dim, int32_t table_stride,
+                                            int32_t prefix_len, int32_t prefix_pages);
 
 /* Attention of a batch with a sliding window and a few first tokens that stay visible: row at
  * position p sees key u of its request when u <= p and (u > p - window or u < sinks); window 0:

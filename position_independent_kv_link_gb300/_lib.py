@@ -100,7 +100,7 @@ SIGNATURES = {
     "pic_op_block_tables": (I32, [I32, P, P, P, I32, P, P, P, I32, P, I32, I32, P, P, P, P, P, P, P]),
     "pic_op_qk_norm_rope": (I32, [I32, I32, I32, I32, I32, P, C.c_int64, P, P, C.c_float, P, P, P, I32, P, P, P, I32,
                                   P]),
-    "pic_op_attention_batch_scratch_bytes": (C.c_size_t, [I32, I32, I32, I32, I32, I32, I32]),
+    "pic_op_attention_batch_scratch_bytes": (C.c_size_t, [I32, I32, I32, I32, I32, I32, I32, I32, I32]),
     "pic_op_attention_window": (I32, [I32, I32, I32, I32, I32, P, P, I32, P, P, I32, P, P, I32, I32, P, P, I32, P, I32,
                                       P, P, C.c_size_t, P]),
     "pic_op_attention_prefix": (I32, [I32, I32, I32, I32, I32, P, P, P, P, I32, I32, I32, P, P, I32, P, P, P, P, I32, P,

@@ -533,7 +533,7 @@ def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torc
     return q_out
 
 
-def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len):
+def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len, prefix_pages):
     dev = _batch_device(q)
     nb, G, D, dt, act, kp, vp, rp = _pool_args(k_layer, v_layer, rope, dev)
     if q.dim() != 3:
@@ -546,7 +546,7 @@ def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 
         out = torch.empty((T, H, D), dtype=act, device=dev)
     if scratch is None:
         with torch.cuda.device(dev):
-            nbytes = lib.pic_op_attention_batch_scratch_bytes(dt, T, n, H, G, D, prefix_len)
+            nbytes = lib.pic_op_attention_batch_scratch_bytes(dt, T, n, H, G, D, pg[2], prefix_len, prefix_pages)
         scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
     tail = (kp, vp, nb, rp, rope.shape[0], _need(out, "out", act, (T, H, D), dev),
             _need(scratch, "scratch", torch.uint8, (-1,), dev), scratch.shape[0])
@@ -561,7 +561,7 @@ def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages
     (pic_op_attention_window). q: rotated [T, H, D], fp16 for bf16 pools, fp32 for fp32 pools; so is the result. Rows
     that belong to no request are left alone (uninitialised unless `out` is given). Buffers made here belong to
     the current stream; with another `stream`, pass `out` and `scratch`."""
-    dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 0)
+    dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 0, 0)
     _call(dev, lib.pic_op_attention_window, *head, n, *pg, window, sinks, *tail, _batch_stream(stream, dev))
     return out
 
@@ -574,7 +574,7 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
     dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
-                                                        prefix_len)
+                                                        prefix_len, prefix_blocks.shape[0])
     pb = _need(prefix_blocks, "prefix_blocks", torch.int32, (-1,), dev)
     n_pre = prefix_blocks.shape[0]
     _call(dev, lib.pic_op_attention_prefix, *head, pb, _need(prefix_pos, "prefix_pos", torch.int32, (n_pre,), dev), n_pre,

@@ -21,6 +21,8 @@ struct BatchArgs {
   const void* k_layer;    // [pool_blocks][G][16][D], K unrotated
   const void* v_layer;
   const float2* rope_cs;  // [rope_positions][D / 2]
+  __half* krot;           // scratch, K rotated ahead: [request][page] or [prefix page] x [G][16][D]; or null
+  int krot_slots;         // pages of krot
   void* out;              // [T][H][D], q's type
   unsigned* flag;         // the device's word of kBatch* bits
   // scratch
@@ -113,10 +115,10 @@ static __device__ __noinline__ void plan_block(const BatchArgs& a, int b, int n_
 template <int NT>
 __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared& sh) {
   const BatchView& v = a.v;
-  const int tid = threadIdx.x, n = v.n_reqs;
+  const int tid = threadIdx.x, n = v.only == 1 ? 0 : v.n_reqs;
   unsigned bad = 0;
-  const int live = pmax(0, pmin(v.row_start[n], v.T));
-  const int n_pre = v.pre_len > 0 ? pdiv(live, v.rb) : 0;
+  const int live = pmax(0, pmin(v.row_start[v.n_reqs], v.T));
+  const int n_pre = v.pre_len > 0 && v.only != 2 ? pdiv(live, v.rb) : 0;
   if (tid == 0) sh.ends[0] = 0, sh.ends[1] = -1;
   // row blocks of the requests
   const int per_r = pdiv(n, NT), r0 = pmin(tid * per_r, n), r1 = pmin(r0 + per_r, n);
@@ -190,11 +192,32 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
 // a slot.
 __device__ __forceinline__ int part_slot(int c, unsigned start, unsigned x0) { return start < x0 ? 2 * c : 2 * c + 1; }
 
+// The merge kernel's view of one segment's plan (0: the shared prefix, 1: the requests' own pages).
+struct MergeSegment {
+  BatchView v;
+  const BatchHead* head;
+  const BatchBlock* blocks;
+  const float2* part_ml;
+  const float* part_o;
+  int part_rows;
+};
+struct MergeArgs {
+  MergeSegment s[2];
+  int T, H, G, rep;
+  unsigned rep_inv;
+  bool prefix;
+  const float2* seg_ml;
+  const float* seg_o;
+  void* out;
+};
+
 void launch_batch_simt(const BatchArgs& a, cudaStream_t st);
-void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st);
 int batch_simt_grid(int D);
 void batch_simt_view(BatchView& v);
-void batch_tc_view(BatchView& v, int D);
-pic_status launch_batch_tc(const BatchArgs& a, cudaStream_t st);
+// wide: two MMA tiles and K rotated ahead
+void batch_tc_view(BatchView& v, bool wide);
+// K of the plan's pages, rotated, into a.krot.
+pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st);
+pic_status launch_batch_tc(const BatchArgs& a, bool wide, cudaStream_t st);
 
 }  // namespace pic

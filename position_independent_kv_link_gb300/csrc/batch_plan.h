@@ -40,6 +40,8 @@ struct BatchView {
   int pool_blocks, rope_positions;
   int mrows, rb, kpages;    // rows (token x head) of an item, tokens of a row block (mrows / rep), pages of a tile
   int half_rows;            // tokens up to which an item costs cost_half a tile
+  int only;                 // 1: a plan of the prefix blocks alone, 2: of the own ones, 0: of both
+  int whole_tiles;          // the pages of the sinks fill whole tiles (a tile's pages are then neighbours)
   unsigned rep_inv;         // ceil(2^16 / rep): m / rep = m * rep_inv >> 16 for m < 256
   int cost_item;            // cost of an item's start and drain,
   int cost_full, cost_half; // of a key tile, and of one whose item has at most half_rows tokens
@@ -128,10 +130,22 @@ PIC_HD BatchBlock own_block(const BatchView& v, int r, int row0, int m, int k) {
   const int lo = b.pos0 - v.window + 1;
   b.wp = lo > own_first(v) ? page_of(v, r, b.np, lo) : 0;
   b.sp = v.sinks > 0 ? pmin(b.wp, page_of(v, r, b.np, pmin(v.sinks - 1, last)) + 1) : 0;
+  if (v.whole_tiles) b.sp = pmin(b.wp, pdiv(b.sp, v.kpages) * v.kpages);
   b.nv = b.sp + pe - b.wp;
   return b;
 }
 // Row block k of the shared prefix over the batch's first `live` rows.
+// A request's rows as one block, its page list all its pages.
+PIC_HD BatchBlock request_block(const BatchView& v, int r, int row0, int m) {
+  BatchBlock b{};
+  b.req = r;
+  b.row0 = row0;
+  b.nrows = m;
+  b.np = b.nv = own_pages(v, r);
+  b.end = own_first(v) + v.kv_len[r];
+  b.pos0 = b.end - m;
+  return b;
+}
 PIC_HD BatchBlock prefix_block(const BatchView& v, int live, int k) {
   BatchBlock b{};
   b.req = -1;
@@ -183,10 +197,11 @@ struct PageMeta {
 struct PageRaw {
   int blk, pos, end;   // block, position of row 0, position after the last row
 };
-// Page `i` of block b's page list (0 <= i < b.nv), as the tables have it.
+// Place in the tables of page `i` of block b's page list (0 <= i < b.nv), and what they have there.
+PIC_HD int page_index(const BatchBlock& b, int i) { return i < b.sp ? i : b.wp + i - b.sp; }
 PIC_HD PageRaw page_raw(const BatchView& v, const BatchBlock& b, int i) {
   PageRaw m;
-  const int p = i < b.sp ? i : b.wp + i - b.sp;
+  const int p = page_index(b, i);
   if (b.req < 0) {
     m.blk = v.pre_blocks[p];
     m.pos = v.pre_pos ? v.pre_pos[p] : kPage * p;

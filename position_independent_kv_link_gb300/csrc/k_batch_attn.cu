@@ -185,57 +185,58 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
   batch_flag(a.flag, bad);
 }
 
-// Joins what the attention kernel left in parts: one warp per (row, head), D / 32 columns per
+// Joins what the attention kernels left in parts: one warp per (row, head), D / 32 columns per
 // lane; result = sum_i w_i O_i / sum_i w_i with w_i = l_i 2^(m_i - max). Rows that see no key
 // (sum 0) give zeros. A lane finds one part each (of the row's item of the prefix, then of its own);
 // their rows are read eight at a time. grid (own row blocks, G, rows of a block / 8).
 template <typename A, int D>
-__global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant__ BatchArgs a) {
+__global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant__ MergeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const BatchView& v = a.v;
-  const BatchHead hd = *a.head;
   constexpr int C = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
   struct Parts {          // the parts of one item
-    unsigned start;
+    unsigned start, U, len;
     int nt, c, c0, n;
   };
-  auto parts = [&](const BatchBlock& b) {
+  auto parts = [&](const MergeSegment& s, const BatchHead& hd, const BatchBlock& b) {
     Parts p;
-    p.nt = block_tiles(v, b), p.c = tile_cost(v, b);
-    p.start = b.cum + g * item_len(v, b);
-    p.c0 = owner(hd.len, p.start);
-    p.n = owner(hd.len, tile_place(v, p.start, p.c, p.nt - 1)) - p.c0 + 1;
+    p.U = hd.U, p.len = hd.len;
+    p.nt = block_tiles(s.v, b), p.c = tile_cost(s.v, b);
+    p.start = b.cum + g * item_len(s.v, b);
+    p.c0 = owner(p.len, p.start);
+    p.n = owner(p.len, tile_place(s.v, p.start, p.c, p.nt - 1)) - p.c0 + 1;
     return p;
   };
+  const BatchHead hd = *a.s[1].head, hp = *a.s[0].head;
 #pragma unroll 1
   for (int bi = hd.n_prefix + blockIdx.x; bi < hd.n_blocks; bi += gridDim.x) {
-    const BatchBlock own = a.blocks[bi];
+    const BatchBlock own = a.s[1].blocks[bi];
+    const Parts po = parts(a.s[1], hd, own);
+    if (po.n == 1 && !a.prefix) continue;   // the attention kernel wrote out itself
 #pragma unroll 1
-    for (int rr = blockIdx.z * 8 + warp; rr < own.nrows * v.rep; rr += 8 * gridDim.z) {
-      const int tok = rr * v.rep_inv >> 16, hh = rr - tok * v.rep, t = own.row0 + tok;
-      const size_t head = (size_t)t * a.H + g * v.rep + hh;
-      const Parts po = parts(own);
-      if (po.n == 1 && v.pre_len == 0) break;   // the attention kernel wrote out itself
-      const int pb = hd.n_prefix > 0 ? (unsigned)t / (unsigned)v.rb : 0;
+    for (int rr = blockIdx.z * 8 + warp; rr < own.nrows * a.rep; rr += 8 * gridDim.z) {
+      const int tok = rr * a.rep_inv >> 16, hh = rr - tok * a.rep, t = own.row0 + tok;
+      const size_t head = (size_t)t * a.H + g * a.rep + hh;
+      const int pb = a.prefix ? (unsigned)t / (unsigned)a.s[0].v.rb : 0;
       Parts pp{};
-      if (hd.n_prefix > 0) pp = parts(a.blocks[pb]);
+      if (a.prefix) pp = parts(a.s[0], hp, a.s[0].blocks[pb]);
       float M = -INFINITY, L = 0.f, o[C] = {};
 #pragma unroll 1
       for (int i0 = 0; i0 < pp.n + po.n; i0 += 32) {
         const int i = i0 + lane, seg = i >= pp.n, p = seg ? i - pp.n : i;
         const Parts& q = seg ? po : pp;
+        const MergeSegment& s = a.s[seg];
         bool on = i < pp.n + po.n;
-        size_t at = (size_t)seg * v.T * a.H + head;   // a whole item's result
+        size_t at = (size_t)seg * a.T * a.H + head;   // a whole item's result
         const bool whole = q.n == 1;
         if (on && !whole) {
-          const unsigned x0 = share(hd.U, hd.len, q.c0 + p), x1 = share(hd.U, hd.len, q.c0 + p + 1);
-          on = tile_lower(v, q.start, q.nt, q.c, x0) < tile_lower(v, q.start, q.nt, q.c, x1);
-          const int lrow = seg ? rr : (t - pb * v.rb) * v.rep + hh;
-          at = (size_t)part_slot(q.c0 + p, q.start, x0) * a.part_rows + lrow;
+          const unsigned x0 = share(q.U, q.len, q.c0 + p), x1 = share(q.U, q.len, q.c0 + p + 1);
+          on = tile_lower(s.v, q.start, q.nt, q.c, x0) < tile_lower(s.v, q.start, q.nt, q.c, x1);
+          const int lrow = seg ? rr : (t - pb * a.s[0].v.rb) * a.rep + hh;
+          at = (size_t)part_slot(q.c0 + p, q.start, x0) * s.part_rows + lrow;
         }
-        const float2 x = on ? (whole ? a.seg_ml : a.part_ml)[at] : make_float2(-INFINITY, 0.f);
-        const float* src = (whole ? a.seg_o : a.part_o) + at * D;
+        const float2 x = on ? (whole ? a.seg_ml : s.part_ml)[at] : make_float2(-INFINITY, 0.f);
+        const float* src = (whole ? a.seg_o : s.part_o) + at * D;
         float mx = x.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -297,45 +298,105 @@ int device_sms() {
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+void launch_batch_merge(const MergeArgs& m, int dtype, int D, cudaStream_t st) {
+  // as many warps as a block has rows when the requests have equally many
+  const BatchView& v = m.s[1].v;
+  const int own = v.T / v.rb + v.n_reqs, rows = pmin(v.rb, pdiv(v.T, v.n_reqs)) * v.rep;
+  const dim3 grid(own, v.G, pdiv(rows, 8));
+  if (dtype == PIC_BF16) {
+    if (D == 128) launch_dependent(batch_merge_kernel<__half, 128>, grid, dim3(256), 0, st, m);
+    else launch_dependent(batch_merge_kernel<__half, 64>, grid, dim3(256), 0, st, m);
+  } else {
+    if (D == 128) launch_dependent(batch_merge_kernel<float, 128>, grid, dim3(256), 0, st, m);
+    else launch_dependent(batch_merge_kernel<float, 64>, grid, dim3(256), 0, st, m);
+  }
+}
+
+// A call as one or two plans: both segments of a batch in one, or, when the prefix or the own pages
+// take K rotated ahead, one each.
+struct BatchCall {
+  BatchArgs a[2] = {};
+  int n = 1;
+  bool wide[2] = {false, false};
+};
+
+// When K is rotated ahead, once per page, and items have two MMA tiles: when a KV head's keys meet
+// enough rows that the MMAs bound the time -- in-kernel rotation, done for every 128 rows anew,
+// would then take longer than they do. Below that HBM bounds, and rotating ahead moves K three
+// times. The rotated pages (of the whole tables: the host does not know the lengths) must stay within 1 GB.
+// Measured on 8 KV heads of 4 query heads, D = 128, window 1024: two prompts of 4096 rows -- ahead / in
+// the kernel -- see the launch; 64 single rows behind a prefix of 16384: see there.
+constexpr size_t kMaxRotated = (size_t)1 << 30;
+bool wide_pays(long long rows, double slots, int G, int D) {
+  return rows >= 512 && slots * G * kPage * D * 2 <= (double)kMaxRotated;
+}
+
+void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, int table_stride, int prefix_len,
+               int prefix_pages) {
+  BatchArgs& a = c.a[0];
+  a.v.T = T;
+  a.v.n_reqs = n_reqs;
+  a.v.G = G;
+  a.v.rep = H / G;
+  a.v.rep_inv = (65535 + a.v.rep) / a.v.rep;
+  a.v.stride = table_stride;
+  a.v.pre_len = prefix_len;
+  a.v.pre_pages = prefix_pages;
+  a.H = H;
+  a.D = D;
+  if (dtype == PIC_F32) {
+    batch_simt_view(a.v);
+    a.grid = batch_simt_grid(D);
+    return;
+  }
+  a.grid = device_sms();
+  const double own_slots = (double)n_reqs * table_stride;
+  const bool own = n_reqs <= 65535 && wide_pays((long long)pdiv(T, n_reqs) * a.v.rep, own_slots, G, D);   // a grid's y
+  const bool pre = prefix_len > 0 && wide_pays((long long)T * a.v.rep, prefix_pages, G, D);
+  if (prefix_len > 0 && (own || pre)) {
+    c.n = 2;
+    c.a[1] = a;
+    c.a[0].v.only = 1;
+    c.a[1].v.only = 2;
+    c.wide[0] = pre;
+    c.wide[1] = own;
+    c.a[0].krot_slots = pre ? prefix_pages : 0;
+    c.a[1].krot_slots = own ? n_reqs * table_stride : 0;
+  } else {
+    c.wide[0] = own;
+    a.krot_slots = own ? n_reqs * table_stride : 0;
+  }
+  for (int i = 0; i < c.n; ++i) batch_tc_view(c.a[i].v, c.wide[i]);
+}
+
 // Scratch layout of a call (bytes); `base` null: the size alone.
-size_t layout(BatchArgs& a, char* base) {
-  const BatchView& v = a.v;
+size_t layout(BatchCall& c, char* base) {
   size_t o = 0;
   auto take = [&](size_t n) {
     char* p = base ? base + o : nullptr;
     o += align256(n);
     return p;
   };
-  a.n_blocks_max = v.T / v.rb + v.n_reqs + (v.pre_len > 0 ? v.T / v.rb + 1 : 0);
-  a.part_rows = (int)(((long long)v.T * v.rep < v.mrows) ? (long long)v.T * v.rep : v.mrows);
-  a.head = (BatchHead*)take(sizeof(BatchHead));
-  a.base = (int*)take(((size_t)v.n_reqs + 1) * 4);
-  a.blocks = (BatchBlock*)take((size_t)a.n_blocks_max * sizeof(BatchBlock));
-  const size_t rows = 2 * (size_t)a.grid * a.part_rows;
-  a.part_ml = (float2*)take(rows * sizeof(float2));
-  a.part_o = (float*)take(rows * a.D * 4);
-  if (v.pre_len > 0) {
-    a.seg_ml = (float2*)take(2 * (size_t)v.T * a.H * sizeof(float2));
-    a.seg_o = (float*)take(2 * (size_t)v.T * a.H * a.D * 4);
+  for (int i = 0; i < c.n; ++i) {
+    BatchArgs& a = c.a[i];
+    const BatchView& v = a.v;
+    const bool own = v.only != 1, pre = v.pre_len > 0 && v.only != 2;
+    a.n_blocks_max = (own ? v.T / v.rb + v.n_reqs : 0) + (pre ? v.T / v.rb + 1 : 0);
+    a.part_rows = (int)(((long long)v.T * v.rep < v.mrows) ? (long long)v.T * v.rep : v.mrows);
+    a.head = (BatchHead*)take(sizeof(BatchHead));
+    a.base = (int*)take(((size_t)v.n_reqs + 1) * 4);
+    a.blocks = (BatchBlock*)take((size_t)a.n_blocks_max * sizeof(BatchBlock));
+    const size_t rows = 2 * (size_t)a.grid * a.part_rows;
+    a.part_ml = (float2*)take(rows * sizeof(float2));
+    a.part_o = (float*)take(rows * a.D * 4);
+    a.krot = a.krot_slots ? (__half*)take((size_t)a.krot_slots * v.G * kPage * a.D * 2) : nullptr;
+  }
+  if (c.a[0].v.pre_len > 0) {
+    const size_t rows = 2 * (size_t)c.a[0].v.T * c.a[0].H;
+    c.a[0].seg_ml = c.a[1].seg_ml = (float2*)take(rows * sizeof(float2));
+    c.a[0].seg_o = c.a[1].seg_o = (float*)take(rows * c.a[0].D * 4);
   }
   return o;
-}
-
-void set_shape(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, int prefix_len) {
-  a.v.T = T;
-  a.v.n_reqs = n_reqs;
-  a.v.G = G;
-  a.v.rep = H / G;
-  a.v.pre_len = prefix_len;
-  a.H = H;
-  a.D = D;
-  if (dtype == PIC_BF16) {
-    batch_tc_view(a.v, D);
-    a.grid = device_sms();
-  } else {
-    batch_simt_view(a.v);
-    a.grid = batch_simt_grid(D);
-  }
 }
 
 bool shape_ok(int dtype, int T, int n_reqs, int H, int G, int D) {
@@ -345,25 +406,48 @@ bool shape_ok(int dtype, int T, int n_reqs, int H, int G, int D) {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-pic_status run(BatchArgs& a, int dtype, int T, int n_reqs, int H, int G, int D, void* scratch, size_t scratch_bytes,
+// c.a[0] holds the caller's pointers and numbers.
+pic_status run(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, void* scratch, size_t scratch_bytes,
                cudaStream_t st) {
-  set_shape(a, dtype, T, n_reqs, H, G, D, a.v.pre_len);
-  const double n_own = T / a.v.rb + (double)n_reqs, n_pre = a.v.pre_len > 0 ? T / a.v.rb + 1.0 : 0.0;
-  if (axis_bound(a.v, n_own, n_pre) >= 2147483647.0) a.v.cost_item = a.v.cost_full = a.v.cost_half = 1;
-  if (axis_bound(a.v, n_own, n_pre) >= 2147483647.0 || 2.0 * T * H >= 4294967295.0)
-    return fail(PIC_ERR_CAPACITY, "batch too large: rows x heads, or row blocks x KV heads x pages of a table row");
-  if (scratch_bytes < layout(a, nullptr)) return fail(PIC_ERR_INVALID_ARG, "attention scratch too small");
-  pic_status e = batch_flag_address(&a.flag);
-  if (e != PIC_OK) return e;
-  layout(a, (char*)scratch);
-  if (dtype == PIC_BF16) {
-    e = launch_batch_tc(a, st);
-    if (e != PIC_OK) return e;
-  } else {
-    launch_batch_simt(a, st);
-    PIC_CUDA(cudaGetLastError());
+  const BatchView v0 = c.a[0].v;
+  set_shape(c, dtype, T, n_reqs, H, G, D, v0.stride, v0.pre_len, v0.pre_pages);
+  bool fits = 2.0 * T * H < 4294967295.0;
+  for (int i = 0; i < c.n; ++i) {
+    BatchView& v = c.a[i].v;
+    const double n_own = v.only == 1 ? 0.0 : T / v.rb + (double)n_reqs;
+    const double n_pre = v.pre_len > 0 && v.only != 2 ? T / v.rb + 1.0 : 0.0;
+    if (axis_bound(v, n_own, n_pre) >= 2147483647.0) v.cost_item = v.cost_full = v.cost_half = 1;
+    fits = fits && axis_bound(v, n_own, n_pre) < 2147483647.0;
   }
-  launch_batch_merge(a, dtype, st);
+  if (!fits)
+    return fail(PIC_ERR_CAPACITY, "batch too large: rows x heads, or row blocks x KV heads x pages of a table row");
+  if (scratch_bytes < layout(c, nullptr)) return fail(PIC_ERR_INVALID_ARG, "attention scratch too small");
+  unsigned* flag = nullptr;
+  pic_status e = batch_flag_address(&flag);
+  if (e != PIC_OK) return e;
+  layout(c, (char*)scratch);
+  MergeArgs m{};
+  for (int i = 0; i < c.n; ++i) {
+    BatchArgs& a = c.a[i];
+    a.flag = flag;
+    if (dtype == PIC_BF16) {
+      if (c.wide[i] && (e = launch_batch_rotate(a, st)) != PIC_OK) return e;
+      if ((e = launch_batch_tc(a, c.wide[i], st)) != PIC_OK) return e;
+    } else {
+      launch_batch_simt(a, st);
+      PIC_CUDA(cudaGetLastError());
+    }
+  }
+  for (int i = 0; i < 2; ++i) {
+    const BatchArgs& a = c.a[c.n == 2 ? i : 0];
+    m.s[i] = MergeSegment{a.v, a.head, a.blocks, a.part_ml, a.part_o, a.part_rows};
+  }
+  m.T = T, m.H = H, m.G = G, m.rep = H / G;
+  m.rep_inv = c.a[0].v.rep_inv;
+  m.prefix = v0.pre_len > 0;
+  m.seg_ml = c.a[0].seg_ml, m.seg_o = c.a[0].seg_o;
+  m.out = c.a[0].out;
+  launch_batch_merge(m, dtype, D, st);
   PIC_CUDA(cudaGetLastError());
   return PIC_OK;
 }
@@ -387,11 +471,12 @@ pic_status check_common(int32_t dtype, int32_t T, int32_t n_reqs, int32_t H, int
   return PIC_OK;
 }
 
-BatchArgs common_args(const void* q, const int32_t* row_start, const int32_t* kv_len, const int32_t* block_table,
+BatchCall common_args(const void* q, const int32_t* row_start, const int32_t* kv_len, const int32_t* block_table,
                       int32_t table_stride, const int32_t* page_pos, const int32_t* n_pages, const void* k_layer,
                       const void* v_layer, int32_t pool_blocks, const void* rope_cs, int32_t rope_positions,
                       void* out) {
-  BatchArgs a{};
+  BatchCall c;
+  BatchArgs& a = c.a[0];
   a.v.row_start = row_start;
   a.v.kv_len = kv_len;
   a.v.block_table = block_table;
@@ -406,7 +491,7 @@ BatchArgs common_args(const void* q, const int32_t* row_start, const int32_t* kv
   a.v_layer = v_layer;
   a.rope_cs = (const float2*)rope_cs;
   a.out = out;
-  return a;
+  return c;
 }
 
 }  // namespace
@@ -414,7 +499,6 @@ BatchArgs common_args(const void* q, const int32_t* row_start, const int32_t* kv
 void batch_simt_view(BatchView& v) {
   v.mrows = kRows;
   v.rb = kRows / v.rep;
-  v.rep_inv = (65535 + v.rep) / v.rep;
   v.kpages = kPages;
   v.cost_item = 1;
   v.cost_full = v.cost_half = 2;
@@ -426,19 +510,6 @@ int batch_simt_grid(int D) {
 
 void launch_batch_simt(const BatchArgs& a, cudaStream_t st) {
   a.D == 128 ? launch_simt<128>(a, st) : launch_simt<64>(a, st);
-}
-
-void launch_batch_merge(const BatchArgs& a, int dtype, cudaStream_t st) {
-  // as many warps as a block has rows when the requests have equally many
-  const int own = a.v.T / a.v.rb + a.v.n_reqs, rows = pmin(a.v.rb, pdiv(a.v.T, a.v.n_reqs)) * a.v.rep;
-  const dim3 grid(own, a.v.G, pdiv(rows, 8));
-  if (dtype == PIC_BF16) {
-    if (a.D == 128) launch_dependent(batch_merge_kernel<__half, 128>, grid, dim3(256), 0, st, a);
-    else launch_dependent(batch_merge_kernel<__half, 64>, grid, dim3(256), 0, st, a);
-  } else {
-    if (a.D == 128) launch_dependent(batch_merge_kernel<float, 128>, grid, dim3(256), 0, st, a);
-    else launch_dependent(batch_merge_kernel<float, 64>, grid, dim3(256), 0, st, a);
-  }
 }
 
 // The flag word's device address, looked up once per device.
@@ -486,12 +557,14 @@ using namespace pic;
 extern "C" {
 
 size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_reqs, int32_t n_heads,
-                                            int32_t n_kv_heads, int32_t head_dim, int32_t prefix_len) {
-  if (!shape_ok(dtype, T, n_reqs, n_heads, n_kv_heads, head_dim) || n_heads / n_kv_heads > kRows || prefix_len < 0)
+                                            int32_t n_kv_heads, int32_t head_dim, int32_t table_stride,
+                                            int32_t prefix_len, int32_t prefix_pages) {
+  if (!shape_ok(dtype, T, n_reqs, n_heads, n_kv_heads, head_dim) || n_heads / n_kv_heads > kRows || table_stride < 1 ||
+      prefix_len < 0 || prefix_pages < 0)
     return 0;
-  BatchArgs a{};
-  set_shape(a, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, prefix_len);
-  return layout(a, nullptr);
+  BatchCall c;
+  set_shape(c, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, table_stride, prefix_len, prefix_pages);
+  return layout(c, nullptr);
 }
 
 pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
@@ -506,11 +579,11 @@ pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, in
                               out, scratch);
   if (e != PIC_OK) return e;
   if (window < 0 || sinks < 0) return fail(PIC_ERR_INVALID_ARG, "window and sinks must not be negative");
-  BatchArgs a = common_args(q, row_start, kv_len, block_table, table_stride, page_pos, n_pages, k_layer, v_layer,
+  BatchCall c = common_args(q, row_start, kv_len, block_table, table_stride, page_pos, n_pages, k_layer, v_layer,
                             pool_blocks, rope_cs, rope_positions, out);
-  a.v.window = window > 0 ? window : INT_MAX;
-  a.v.sinks = sinks;
-  return run(a, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, scratch, scratch_bytes, (cudaStream_t)stream);
+  c.a[0].v.window = window > 0 ? window : INT_MAX;
+  c.a[0].v.sinks = sinks;
+  return run(c, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, scratch, scratch_bytes, (cudaStream_t)stream);
 }
 
 pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
@@ -529,13 +602,14 @@ pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, in
       prefix_pages < pdiv(prefix_len, kPage) || (prefix_pages > prefix_len) ||
       (!prefix_pos && prefix_pages != pdiv(prefix_len, kPage)))
     return fail(PIC_ERR_INVALID_ARG, "invalid prefix: its pages must hold prefix_len positions of the RoPE table");
-  BatchArgs a = common_args(q, row_start, kv_len, block_table, table_stride, page_pos, n_pages, k_layer, v_layer,
+  BatchCall c = common_args(q, row_start, kv_len, block_table, table_stride, page_pos, n_pages, k_layer, v_layer,
                             pool_blocks, rope_cs, rope_positions, out);
+  BatchArgs& a = c.a[0];
   a.v.pre_blocks = prefix_blocks;
   a.v.pre_pos = prefix_pos;
   a.v.pre_pages = prefix_pages;
   a.v.pre_len = prefix_len;
-  return run(a, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, scratch, scratch_bytes, (cudaStream_t)stream);
+  return run(c, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, scratch, scratch_bytes, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -6,16 +6,17 @@
 // through rings of stages in shared memory:
 //
 //   meta warp   walks the share: reads the page tables a window ahead, writes the windows' records
-//               (item, rows, pages with the rows that hold keys), and asks for raw K, one TMA box a page
+//               (item, rows, pages with the rows that hold keys), and asks for K, one TMA box a page
 //               wherever its block lies, with the RoPE table row of the page's position.
 //   load warp   asks for the items' rows of q (TMA boxes of 8 tokens x rep heads; double-buffered for
 //               one MMA tile, else when the item's last S product has retired) and for V, one box a
 //               page: a page is one K = 16 step of the PV product, so pages need not be neighbours.
-//   rotation    turns raw K into the fp16 operand: thread = row of a page x 8 pairs of dims; the angle
-//               of row r of a page at position P is composed from the table rows of P (shared memory,
-//               one row a page) and of r (registers), so that a key needs no table row of its own. One
-//               rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S). Rows that hold no
-//               key any row of the block sees are zeroed in K and V.
+//   rotation    (MT = 1) turns raw K into the fp16 operand: thread = row of a page x 8 pairs of dims; the
+//               angle of row r of a page at position P is composed from the table rows of P (shared
+//               memory, one row a page) and of r (registers), so that a key needs no table row of its
+//               own. One rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S).
+//   V mending   rows that hold no key any row of the block sees are zeroed in V (P is 0 there, V must be
+//               finite), by the rotation or (MT = 2) a warp of its own.
 //   S warp      one thread issues S_t = Q_t K^T (fp16) of a key tile for the MMA tiles, two S buffers each.
 //   PV warp     one thread issues O_t += P_t V (bf16, P from TMEM). Apart from the S warp, so that neither
 //               product waits behind the other's inputs: together in one thread the two cost some
@@ -30,7 +31,10 @@
 // at 8 cycles an instruction (ncu: no_instruction the largest stall). At the 5 that are left (a warp
 // on its own waits for its last result) the rotation's control is what is worth saving, hence TMA.
 //
-// MT = 1: few rows, HBM-bound. MT = 2: many rows; a K tile is loaded and rotated once for 256 rows.
+// MT = 1: few rows, HBM-bound; K is rotated on its way. MT = 2: many rows, MMA-bound; K has been rotated
+// ahead, once per page, into a scratch (batch_rotate_kernel) and comes as two boxes of four pages.
+// Rotating it here instead, for every 256 rows anew, kept the schedulers busier than the MMAs (2900
+// cycles a key tile against 1300).
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
@@ -56,19 +60,16 @@ template <int D_, int MT_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
   static constexpr int NQ = MT == 2 ? 1 : 2;          // Q buffers per MMA tile
-  static constexpr int NX = D == 128 ? 3 : 6;         // raw K stages (with table rows)
-  static constexpr int NK = D == 128 ? 2 : 3;         // K operand stages
+  static constexpr int NX = MT == 2 ? 0 : D == 128 ? 3 : 6;   // raw K stages (with table rows)
+  static constexpr int NK = MT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 3);   // K operand stages
   static constexpr int NV = D == 128 ? 4 : 8;         // V stages
-  static constexpr int NR = 8;                        // rotation warps
+  static constexpr int NR = MT == 2 ? 0 : 8;          // rotation warps
   static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
-  static constexpr int CH = D / 16, PP = NR * 32 / (16 * CH);   // rotation: threads of a row, pages at once
   // Roles of the warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
-  // instruction cache is shared by its warps: each scheduler gets as few roles as possible, and the
-  // MMA threads one away from the rotation.
-  static constexpr int THREADS = MT == 2 ? 640 : 512;
-  static constexpr int W_S = MT == 2 ? 11 : 7, W_PV = MT == 2 ? 15 : 11, W_META = MT == 2 ? 19 : 15, W_LOAD = MT == 2 ? 18 : 6;
-  // number of a rotation warp: MT 2: 8 9 10 12 13 14 16 17; MT 1: 4 5 8 9 10 12 13 14
-  static __device__ __forceinline__ int rot(int w) { return MT == 2 ? w - (w >> 2) - 6 : w < 6 ? w - 4 : w - (w >> 2) - 4; }
+  // instruction cache is shared by its warps. Rotation: warps 4..11.
+  static constexpr int THREADS = MT == 2 ? 416 : 512;
+  static constexpr int W_S = MT == 2 ? 8 : 15, W_PV = MT == 2 ? 9 : 13, W_META = MT == 2 ? 10 : 14, W_LOAD = MT == 2 ? 11 : 12,
+                       W_MEND = MT == 2 ? 12 : -1;
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
@@ -76,14 +77,14 @@ struct Cfg {
   static constexpr int OFF_X = OFF_V + NV * K_BYTES;          // [NX] likewise, raw K
   static constexpr int OFF_CS = OFF_X + NX * K_BYTES;         // [NX][KP] table rows, [4][CH][16 B] each
   static constexpr int OFF_REC = OFF_CS + NX * KP * CS_ROW;   // WinRec [NWIN]
-  static constexpr int OFF_PAGE = OFF_REC + NWIN * 48;        // int4 [NWIN][WIN] page of the pool, position, rows
+  static constexpr int OFF_PAGE = OFF_REC + NWIN * 48;        // int4 [NWIN][WIN] page of the pool, position, rows, page of the rotated K
   static constexpr int OFF_LIM = OFF_PAGE + NWIN * WIN * 16;  // int2 [NWIN][WT] last key, first one behind the sinks
   static constexpr int OFF_TILE = OFF_LIM + NWIN * WT * 8;    // int4 [NX] rows of the tile's pages, 16 bits each; the end
   static constexpr int OFF_BAR = OFF_TILE + NX * 16;
   // barriers
   static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_XFULL = B_RFREE + NWIN, B_XEMPTY = B_XFULL + NX,
                        B_READY = B_XEMPTY + NX, B_KEMPTY = B_READY + NK, B_VFULL = B_KEMPTY + NK,
-                       B_VEMPTY = B_VFULL + NV, B_SFULL = B_VEMPTY + NV, B_PREADY = B_SFULL + MT * NBS,
+                       B_VEMPTY = B_VFULL + NV, B_VREADY = B_VEMPTY + NV, B_SFULL = B_VREADY + (MT == 2 ? NV : 0), B_PREADY = B_SFULL + MT * NBS,
                        B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS, B_QEMPTY = B_QFULL + MT * NQ,
                        B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + 2;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
@@ -105,14 +106,15 @@ struct WinRec {           // 48 bytes
 // Every waiter of a barrier sees each of its phases before the next can complete (a parity wait
 // cannot tell phase n from n + 2). META, RFREE: a record is rewritten only when every warp that
 // reads records has arrived at RFREE for the window before in its slot. XFULL, XEMPTY: between the
-// meta warp and the rotation, all of whose warps arrive. READY (MMA warps), KEMPTY: rotation of tile
-// j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows PV of j. SFULL,
-// PREADY, PVDONE: a ring of the S warp, warpgroup t and the PV warp; S(j + 2) into a buffer follows the
-// end of PV(j), which waits for all four warps' P(j). QFULL, QEMPTY: between the load and the S warp.
-// No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN and raw K
-// of the tiles up to window i - 3, that is the rotation up to NX tiles before, that is the S products
-// NK tiles before that: with windows of one tile, of tile i - 3 - NX - NK at the latest, while its
-// readers are never more than two windows ahead of the S products. V and q of a tile wait for
+// meta warp and the rotation, all of whose warps arrive. READY (of K), KEMPTY: the rotation, or the meta
+// warp's TMA, of tile j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows
+// PV of j, which waits for VREADY (or VFULL); VREADY: VFULL seen and mended. SFULL, PREADY, PVDONE: a
+// ring of the S warp, warpgroup t and the PV warp; S(j + 2) into a buffer follows the end of PV(j),
+// which waits for all four warps' P(j). QFULL, QEMPTY: between the load and the S warp.
+// No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN and K asked
+// for up to window i - 3, that is the S products NX + NK tiles before: with windows of one tile, of
+// tile i - 3 - NX - NK at the latest, while its readers are never more than two windows ahead of the S
+// products. V and q of a tile wait for
 // products of earlier tiles only, the rotation of a tile with empty rows for its V.
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -174,6 +176,14 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
       "[%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+// 5-D box at (0, 0, c2, c3, c4)
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int c2, int c3, int c4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4, "
+      "%5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
 // 16-byte chunk c (0..7) of row r of a [rows][128 B] tile, 128-byte swizzle (the TMA and UMMA layout)
@@ -334,7 +344,7 @@ __device__ __noinline__ PageRaw fetch_page(const BatchView& v, const BatchBlock&
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_constant__ TcArgs ta) {
-  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NX = C::NX, NK = C::NK, NV = C::NV;
+  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NK = C::NK, NV = C::NV;
   const BatchArgs& a = ta.b;
   const BatchView& v = a.v;
   extern __shared__ uint8_t smem_raw[];
@@ -364,10 +374,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       for (int k = 0; k < n; ++k) mbar_init(bar(i + k), count);
     };
     init(C::B_META, NWIN, 1);
-    init(C::B_RFREE, NWIN, 4 * MT + 3);
-    init(C::B_XFULL, NX, 1);
-    init(C::B_XEMPTY, NX, C::NR);
-    init(C::B_READY, NK, C::NR);
+    init(C::B_RFREE, NWIN, 4 * MT + (MT == 2 ? 4 : 3));
+    init(C::B_XFULL, C::NX, 1);
+    init(C::B_XEMPTY, C::NX, C::NR);
+    init(C::B_READY, NK, MT == 2 ? 1 : C::NR);
+    if (MT == 2) init(C::B_VREADY, NV, 1);
     init(C::B_KEMPTY, NK, 1);
     init(C::B_VFULL, NV, 1);
     init(C::B_VEMPTY, NV, 1);
@@ -595,7 +606,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           const int st = gt % NV;
           const bool first = j == 0 && (flags & kFirst);
           const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
-          ok = wait(C::B_VFULL + st, (gt / NV) & 1);
+          ok = wait((MT == 2 ? C::B_VREADY : C::B_VFULL) + st, (gt / NV) & 1);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             if (t == 1 && !(flags & kTwo)) continue;
@@ -619,7 +630,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       mbar_wait_on(bar(C::B_DONE + 1), 0, 0, a.flag);
     }
   } else if (warp == C::W_META) {
-    // =============================== window records, raw K
+    // =============================== window records, K
+    if (MT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotated K
     // Lane i holds page i of a window. `next`: the tables' entries of the window after the last one
     // written (the same item's or the next one's), on their way.
     Walk w;
@@ -627,6 +639,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     unsigned bad = 0;
     int j = more ? w.j0 : 0;             // next tile to be described
     uint32_t n_win = 0, gt = 0;          // windows written, tiles whose K is asked for
+    constexpr int NS = MT == 2 ? NK : C::NX;   // stages K goes to
     PageRaw next{0, 0, 0};
     if (more) next = fetch_page(v, w.b, j * KP + lane);
     bool ended = false;
@@ -653,7 +666,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
             low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
           }
-          sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, 0);
+          int krot = 0;                    // the page's place in the rotated K
+          if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : w.b.req * v.stride);
+          sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, krot);
           if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
           if (lane == 0) {
             WinRec& r = sRec[ws];
@@ -675,28 +690,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         continue;
       }
       const bool end = sRec[win % NWIN].flags & kEnd;
-      const int n = end ? 1 : sRec[win % NWIN].tiles;   // the end: a tile without pages, for the rotation to see
+      if (MT == 2 && end) break;
+      const int n = end ? 1 : sRec[win % NWIN].tiles, g = sRec[win % NWIN].g;   // MT 1: the rotation sees the end as a tile
       const int4 pg = sPage[win % NWIN * WIN + lane];
       ++win;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++gt) {
-        const int st = gt % NX;
-        if (lane == 0) ok = gt < NX || wait(C::B_XEMPTY + st, (gt / NX - 1) & 1);
+        const int st = gt % NS;
+        if (lane == 0) ok = gt < NS || wait((MT == 2 ? C::B_KEMPTY : C::B_XEMPTY) + st, (gt / NS - 1) & 1);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        const bool live = !end && lane / KP == i && pg.z != 0;
-        const unsigned who = __ballot_sync(0xffffffffu, live);
-        // the pages' rows, from the lanes that hold them
-        const unsigned r0 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP), r1 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 1);
-        const unsigned r2 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 2), r3 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 3);
-        if (lane == 0) {
-          sTile[st] = make_int4((int)(r0 | r1 << 16), (int)(r2 | r3 << 16), end, 0);
-          mbar_expect_tx(bar(C::B_XFULL + st), (uint32_t)__popc(who) * (C::PAGE_BYTES + C::CS_ROW));
-        }
-        __syncwarp();
-        if (live) {
-          tma_4d(base + C::OFF_X + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.kmap, 0, 0, pg.x, bar(C::B_XFULL + st));
-          tma_4d(base + C::OFF_CS + (st * KP + lane % KP) * C::CS_ROW, &ta.cmap, 0, 0, pg.y, bar(C::B_XFULL + st));
+        if constexpr (MT == 2) {
+          const int slot = __shfl_sync(0xffffffffu, pg.w, i * KP);
+          if (lane == 0) mbar_expect_tx(bar(C::B_READY + st), C::K_BYTES);
+          __syncwarp();
+          if (lane < D / 64)
+            tma_5d(base + C::OFF_K + st * C::K_BYTES + lane * (KT * 128), &ta.kmap, lane, g, slot, bar(C::B_READY + st));
+        } else {
+          const bool live = !end && lane / KP == i && pg.z != 0;
+          const unsigned who = __ballot_sync(0xffffffffu, live);
+          // the pages' rows, from the lanes that hold them
+          const unsigned r0 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP), r1 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 1);
+          const unsigned r2 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 2), r3 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 3);
+          if (lane == 0) {
+            sTile[st] = make_int4((int)(r0 | r1 << 16), (int)(r2 | r3 << 16), end, 0);
+            mbar_expect_tx(bar(C::B_XFULL + st), (uint32_t)__popc(who) * (C::PAGE_BYTES + C::CS_ROW));
+          }
+          __syncwarp();
+          if (live) {
+            tma_4d(base + C::OFF_X + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.kmap, 0, 0, pg.x, bar(C::B_XFULL + st));
+            tma_4d(base + C::OFF_CS + (st * KP + lane % KP) * C::CS_ROW, &ta.cmap, 0, 0, pg.y, bar(C::B_XFULL + st));
+          }
         }
       }
       if (end) break;
@@ -706,9 +730,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     // every copy has landed before the shared memory is given up (at once on the normal path)
     if (lane == 0) {
 #pragma unroll 1
-      for (uint32_t s = 0; s < NX; ++s) {
-        const uint32_t n = (gt + NX - 1 - s) / NX;
-        if (n) mbar_wait_on(bar(C::B_XFULL + s), (n - 1) & 1, 0, a.flag);
+      for (uint32_t s = 0; s < NS; ++s) {
+        const uint32_t n = (gt + NS - 1 - s) / NS;
+        if (n) mbar_wait_on(bar((MT == 2 ? C::B_READY : C::B_XFULL) + s), (n - 1) & 1, 0, a.flag);
       }
     }
   } else if (warp == C::W_LOAD) {
@@ -779,11 +803,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           if (n) mbar_wait_on(bar(C::B_QFULL + t * NQ + b), (n - 1) & 1, 0, a.flag);
         }
     }
-  } else {
+  } else if (warp == C::W_MEND) {
+    // =============================== rows of V without a key to zero
+    uint32_t gt = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t win = 0; ok; ++win) {
+      ok = __all_sync(0xffffffffu, wait_meta(win));
+      if (!ok || (sRec[win % NWIN].flags & kEnd)) break;
+      const int n = sRec[win % NWIN].tiles;
+      const unsigned rows = (unsigned)sPage[win % NWIN * WIN + lane].z;
+      done_with(win);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++gt) {
+        const int st = gt % NV;
+        ok = __all_sync(0xffffffffu, wait(C::B_VFULL + st, (gt / NV) & 1));
+        if (!ok) break;
+        unsigned todo = __ballot_sync(0xffffffffu, lane / KP == i && rows != 0xffffu);   // pages, by lane
+#pragma unroll 1
+        for (; todo; todo &= todo - 1) {
+          const int l = __ffs(todo) - 1;
+          const unsigned have = __shfl_sync(0xffffffffu, rows, l);
+          uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + l % KP * C::PAGE_BYTES;
+#pragma unroll 1
+          for (int u = lane; u < C::PAGE_BYTES / 16; u += 32) {   // [half][row][8 chunks]
+            const int r = u / 8 % kPage;
+            if (!(have >> r & 1u)) *reinterpret_cast<uint4*>(vs + u * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_VREADY + st));
+      }
+    }
+    if (!ok) give_up();
+  } else if constexpr (MT == 1) {
     // =============================== raw K to the K operand
-    constexpr int CH = C::CH, PP = C::PP, NP = KP / PP;   // pages of a tile per thread
+    constexpr int NX = C::NX;
+    constexpr int CH = D / 16, PP = C::NR * 32 / (16 * CH), NP = KP / PP;   // threads of a row; pages at once, per thread
     static_assert(KP % PP == 0, "");
-    const int rt = C::rot(warp) * 32 + lane, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
+    const int rt = tid - 128, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
     // (cos, sin) of r theta for the thread's 8 frequencies
     float4 off[4];
 #pragma unroll
@@ -922,6 +981,18 @@ bool cs_map(CUtensorMap* m, const BatchArgs& a) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// K rotated ahead, [slots][G][16][D] of fp16, as (64 dims, 16 rows, D / 64 halves, G, slots); a box is
+// one half of four neighbouring pages, landing as [key][128 B].
+bool krot_map(CUtensorMap* m, const BatchArgs& a) {
+  auto enc = encode_fn();
+  const cuuint64_t dims[5] = {64, (cuuint64_t)kPage, (cuuint64_t)(a.D / 64), (cuuint64_t)a.v.G, (cuuint64_t)a.krot_slots};
+  const cuuint64_t strides[4] = {(cuuint64_t)a.D * 2, 128, (cuuint64_t)kPage * a.D * 2, (cuuint64_t)a.v.G * kPage * a.D * 2};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1}, box[5] = {64, kPage, 1, 1, KP};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, a.krot, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename C>
 pic_status launch(const TcArgs& ta, cudaStream_t st) {
   static bool set[64] = {};
@@ -932,39 +1003,93 @@ pic_status launch(const TcArgs& ta, cudaStream_t st) {
     PIC_CUDA(cudaFuncSetAttribute(batch_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  batch_tc_kernel<C><<<ta.b.grid, C::THREADS, smem, st>>>(ta);
-  PIC_CUDA(cudaGetLastError());
+  if (C::MT == 2) {   // its plan under the tail of the rotation
+    PIC_CUDA(launch_dependent(batch_tc_kernel<C>, dim3(ta.b.grid), dim3(C::THREADS), smem, st, ta));
+  } else {
+    batch_tc_kernel<C><<<ta.b.grid, C::THREADS, smem, st>>>(ta);
+    PIC_CUDA(cudaGetLastError());
+  }
   return PIC_OK;
+}
+
+// K of every page that some row of the batch sees (or of the prefix), rotated to its keys' positions,
+// bf16 -> fp16, [slot][G][16][D]. One CTA a page: a thread has one row and 8 pairs of dims, and takes
+// their table entries once for all KV heads. HBM-bound: K read and written once.
+template <int D>
+__global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant__ BatchArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const BatchView& v = a.v;
+  constexpr int CH = D / 16, HP = 256 / (16 * CH);   // KV heads at once
+  const int p = blockIdx.x, r = blockIdx.y, c = threadIdx.x % CH, row = threadIdx.x / CH % kPage, g0 = threadIdx.x / (16 * CH);
+  unsigned bad = 0;
+  BatchBlock b;
+  if (v.only == 1) {
+    b = prefix_block(v, 1, 0);
+  } else {
+    int row0;
+    const int m = request_rows(v, r, row0, bad);
+    if (m == 0) return;                              // the plan flags what is wrong with it
+    b = request_block(v, r, row0, m);
+    if (p >= b.np) return;
+  }
+  bad = 0;
+  const PageMeta pm = page_meta(v, b, page_raw(v, b, p), bad);
+  if (threadIdx.x == 0) batch_flag(a.flag, bad);
+  if (!(pm.rows >> row & 1u)) return;
+  const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (size_t)(pm.pos + row) * (D / 2) + 8 * c);
+  float4 f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = cs[e];
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k_layer) + (size_t)pm.blk * v.G * kPage * D + row * D + 8 * c;
+  const size_t slot = v.only == 1 ? (size_t)p : (size_t)r * v.stride + p;
+  __half* dst = a.krot + slot * v.G * kPage * D + row * D + 8 * c;
+#pragma unroll 2
+  for (int g = g0; g < v.G; g += HP) {
+    const uint4 u1 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D);
+    const uint4 u2 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D + D / 2);
+    const uint32_t a1[4] = {u1.x, u1.y, u1.z, u1.w}, a2[4] = {u2.x, u2.y, u2.z, u2.w};
+    uint32_t o1[4], o2[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float q0 = __uint_as_float(a1[e] << 16), q1 = __uint_as_float(a1[e] & 0xffff0000u);
+      const float z0 = __uint_as_float(a2[e] << 16), z1 = __uint_as_float(a2[e] & 0xffff0000u);
+      o1[e] = pack_f16x2(q0 * f[e].x - z0 * f[e].y, q1 * f[e].z - z1 * f[e].w);
+      o2[e] = pack_f16x2(z0 * f[e].x + q0 * f[e].y, z1 * f[e].z + q1 * f[e].w);
+    }
+    *reinterpret_cast<uint4*>(dst + (size_t)g * kPage * D) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    *reinterpret_cast<uint4*>(dst + (size_t)g * kPage * D + D / 2) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  }
 }
 
 }  // namespace
 
-// Rows of an item: 128 (one MMA tile) or 256. Two tiles share every K and V tile they load and
-// rotate, which pays when blocks fill them; with fewer rows one tile and smaller stages keep more
-// bytes in flight.
-void batch_tc_view(BatchView& v, int D) {
-  const long long rows = (v.pre_len > 0 ? (long long)v.T : pdiv(v.T, v.n_reqs)) * v.rep;
-  const bool two = rows > 128;
+void batch_tc_view(BatchView& v, bool wide) {
   v.half_rows = 128 / v.rep & ~7;   // a box of q is 8 tokens
-  v.rb = two ? 2 * v.half_rows : v.half_rows;
+  v.rb = wide ? 2 * v.half_rows : v.half_rows;
   v.mrows = v.rb * v.rep;
-  v.rep_inv = (65535 + v.rep) / v.rep;
   v.kpages = KP;
+  v.whole_tiles = wide;
   v.cost_item = 4;
   v.cost_full = 8;
-  v.cost_half = two ? 5 : 8;
-  (void)D;
+  v.cost_half = wide ? 5 : 8;
 }
 
-pic_status launch_batch_tc(const BatchArgs& a, cudaStream_t st) {
+pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st) {
+  const dim3 grid(a.v.only == 1 ? a.v.pre_pages : a.v.stride, a.v.only == 1 ? 1 : a.v.n_reqs);
+  if (a.D == 128) batch_rotate_kernel<128><<<grid, 256, 0, st>>>(a);
+  else batch_rotate_kernel<64><<<grid, 256, 0, st>>>(a);
+  PIC_CUDA(cudaGetLastError());
+  return PIC_OK;
+}
+
+pic_status launch_batch_tc(const BatchArgs& a, bool wide, cudaStream_t st) {
   TcArgs ta;
   ta.b = a;
-  if (!page_map(&ta.kmap, a.k_layer, a.v.pool_blocks, a.v.G, a.D) ||
-      !page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a) || !cs_map(&ta.cmap, a))
-    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the pools, q or the RoPE table");
-  const bool two = a.v.rb > a.v.half_rows;
-  if (a.D == 128) return two ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
-  return two ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
+  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a) ||
+      !(wide ? krot_map(&ta.kmap, a) : page_map(&ta.kmap, a.k_layer, a.v.pool_blocks, a.v.G, a.D) && cs_map(&ta.cmap, a)))
+    return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the pools, q, the RoPE table or the rotated K");
+  if (a.D == 128) return wide ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
+  return wide ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
 }
 
 }  // namespace pic

@@ -38,7 +38,7 @@ def test_window_refuses(lib, kw):
 
 def test_too_many_heads_for_a_kv_head(lib):
     assert window(lib, H=34, G=2) == L.PIC_ERR_UNSUPPORTED
-    assert lib.pic_op_attention_batch_scratch_bytes(L.PIC_BF16, 1, 1, 34, 2, 128, 0) == 0
+    assert lib.pic_op_attention_batch_scratch_bytes(L.PIC_BF16, 1, 1, 34, 2, 128, 4, 0, 0) == 0
 
 
 @pytest.mark.parametrize("kw", [dict(n_len=-1), dict(blocks=None), dict(pages=1), dict(n_len=100), dict(pages=18, pos=A),
