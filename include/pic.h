@@ -437,7 +437,7 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  * n_pages [n_reqs] counts the pages; page_pos and n_pages come together. Entries past a
  * request's pages are not read.
  *
- * The host checks shapes, pointers and alignment (16 bytes; scratch 256). What only the device
+ * The host checks shapes, pointers and alignment (16 bytes; attention outputs 32, scratch 256). What only the device
  * sees is checked there: a request whose lengths do not fit together is skipped (its rows of out
  * stay as they were), a page whose block lies outside the pool counts as empty, a position
  * outside the RoPE table is skipped; pic_sync then reports PIC_ERR_INVALID_ARG once. No such

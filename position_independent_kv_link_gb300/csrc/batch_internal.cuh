@@ -6,6 +6,9 @@
 
 namespace pic {
 
+struct BatchCut {         // the item that CTA c's share begins inside of, for the first CTA it continues in; block -1: none
+  int block, g;
+};
 struct BatchHead {        // written by CTA 0
   unsigned U, len;        // length of the cost axis, of a share
   int n_prefix, n_blocks; // prefix row blocks; all row blocks
@@ -29,6 +32,7 @@ struct BatchArgs {
   BatchHead* head;
   int* base;              // [n_reqs + 1] row blocks of the requests before
   BatchBlock* blocks;     // [n_blocks_max]
+  BatchCut* cuts;         // [grid]
   float2* part_ml;        // [2 grid][part_rows] (maximum, sum) in the log2 domain
   float* part_o;          // [2 grid][part_rows][D] normalized
   // prefix batches: whole items' results, [2][T][H] (segment 0: the prefix, 1: own pages)
@@ -177,6 +181,17 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
       if (cum >= s.x1) sh.ends[1] = b;
     }
   }
+  // the item the share begins inside of, when the CTA before began it: the merge finds the cut items here
+  __syncthreads();
+  if (tid == 0) {
+    BatchCut cut{-1, 0};
+    const BatchBlock& b = sh.block;
+    if (s.x0 < s.x1 && s.x0 > 0) {
+      const unsigned ilen = item_len(v, b), g = (s.x0 - b.cum) / ilen, start = b.cum + g * ilen;
+      if (start < s.x0 && owner(part, start) == (int)blockIdx.x - 1) cut = BatchCut{sh.ends[0], (int)g};
+    }
+    a.cuts[blockIdx.x] = cut;
+  }
   if (blockIdx.x == 0) {
     batch_flag(a.flag, bad);
     if (tid == 0) *a.head = BatchHead{U, part, n_pre, nb};
@@ -197,13 +212,14 @@ struct MergeSegment {
   BatchView v;
   const BatchHead* head;
   const BatchBlock* blocks;
+  const BatchCut* cuts;
   const float2* part_ml;
   const float* part_o;
   int part_rows;
 };
 struct MergeArgs {
   MergeSegment s[2];
-  int T, H, G, rep;
+  int T, H, G, rep, grid;
   unsigned rep_inv;
   bool prefix;
   const float2* seg_ml;

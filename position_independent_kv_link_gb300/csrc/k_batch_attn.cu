@@ -188,12 +188,14 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
 // Joins what the attention kernels left in parts: one warp per (row, head), D / 32 columns per
 // lane; result = sum_i w_i O_i / sum_i w_i with w_i = l_i 2^(m_i - max). Rows that see no key
 // (sum 0) give zeros. A lane finds one part each (of the row's item of the prefix, then of its own);
-// their rows are read eight at a time. grid (own row blocks, G, rows of a block / 8).
+// their rows are read eight at a time. A batch with a prefix merges every row: grid (own row blocks, G,
+// rows of a block / 8); one without only the items that a share's edge cuts: grid (shares, 1, rows / 8).
 template <typename A, int D>
 __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant__ MergeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int C = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int g = blockIdx.y, first = blockIdx.x;
   struct Parts {          // the parts of one item
     unsigned start, U, len;
     int nt, c, c0, n;
@@ -208,11 +210,18 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
     return p;
   };
   const BatchHead hd = *a.s[1].head, hp = *a.s[0].head;
+  int last = hd.n_blocks - hd.n_prefix - 1;
+  if (!a.prefix) {
+    const BatchCut cut = a.s[1].cuts[blockIdx.x];
+    if (cut.block < 0) return;
+    first = last = cut.block;
+    g = cut.g;
+  }
 #pragma unroll 1
-  for (int bi = hd.n_prefix + blockIdx.x; bi < hd.n_blocks; bi += gridDim.x) {
+  for (int bi = hd.n_prefix + first; bi <= hd.n_prefix + last; bi += gridDim.x) {
     const BatchBlock own = a.s[1].blocks[bi];
     const Parts po = parts(a.s[1], hd, own);
-    if (po.n == 1 && !a.prefix) continue;   // the attention kernel wrote out itself
+    if (po.n == 1 && !a.prefix) continue;   // the edge fell between the item's tiles and its end: out is written
 #pragma unroll 1
     for (int rr = blockIdx.z * 8 + warp; rr < own.nrows * a.rep; rr += 8 * gridDim.z) {
       const int tok = rr * a.rep_inv >> 16, hh = rr - tok * a.rep, t = own.row0 + tok;
@@ -302,7 +311,7 @@ void launch_batch_merge(const MergeArgs& m, int dtype, int D, cudaStream_t st) {
   // as many warps as a block has rows when the requests have equally many
   const BatchView& v = m.s[1].v;
   const int own = v.T / v.rb + v.n_reqs, rows = pmin(v.rb, pdiv(v.T, v.n_reqs)) * v.rep;
-  const dim3 grid(own, v.G, pdiv(rows, 8));
+  const dim3 grid = m.prefix ? dim3(own, v.G, pdiv(rows, 8)) : dim3(m.grid, 1, pdiv(rows, 8));
   if (dtype == PIC_BF16) {
     if (D == 128) launch_dependent(batch_merge_kernel<__half, 128>, grid, dim3(256), 0, st, m);
     else launch_dependent(batch_merge_kernel<__half, 64>, grid, dim3(256), 0, st, m);
@@ -386,6 +395,7 @@ size_t layout(BatchCall& c, char* base) {
     a.head = (BatchHead*)take(sizeof(BatchHead));
     a.base = (int*)take(((size_t)v.n_reqs + 1) * 4);
     a.blocks = (BatchBlock*)take((size_t)a.n_blocks_max * sizeof(BatchBlock));
+    a.cuts = (BatchCut*)take((size_t)a.grid * sizeof(BatchCut));
     const size_t rows = 2 * (size_t)a.grid * a.part_rows;
     a.part_ml = (float2*)take(rows * sizeof(float2));
     a.part_o = (float*)take(rows * a.D * 4);
@@ -440,7 +450,8 @@ pic_status run(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
   }
   for (int i = 0; i < 2; ++i) {
     const BatchArgs& a = c.a[c.n == 2 ? i : 0];
-    m.s[i] = MergeSegment{a.v, a.head, a.blocks, a.part_ml, a.part_o, a.part_rows};
+    m.s[i] = MergeSegment{a.v, a.head, a.blocks, a.cuts, a.part_ml, a.part_o, a.part_rows};
+    m.grid = a.grid;
   }
   m.T = T, m.H = H, m.G = G, m.rep = H / G;
   m.rep_inv = c.a[0].v.rep_inv;
@@ -465,9 +476,10 @@ pic_status check_common(int32_t dtype, int32_t T, int32_t n_reqs, int32_t H, int
     return fail(PIC_ERR_INVALID_ARG, "invalid attention arguments");
   if ((page_pos == nullptr) != (n_pages == nullptr))
     return fail(PIC_ERR_INVALID_ARG, "page_pos and n_pages come together");
-  if (!aligned16(q) || !aligned16(k_layer) || !aligned16(v_layer) || !aligned16(rope_cs) || !aligned16(out) ||
+  if (!aligned16(q) || !aligned16(k_layer) || !aligned16(v_layer) || !aligned16(rope_cs) || ((uintptr_t)out & 31) ||
       ((uintptr_t)scratch & 255))
-    return fail(PIC_ERR_INVALID_ARG, "q, pools, RoPE table and out must be 16-byte aligned, scratch 256-byte aligned");
+    return fail(PIC_ERR_INVALID_ARG,
+                "q, pools and RoPE table must be 16-byte, out 32-byte, scratch 256-byte aligned");
   return PIC_OK;
 }
 

@@ -17,10 +17,11 @@
 //               own. One rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S).
 //   V mending   rows that hold no key any row of the block sees are zeroed in V (P is 0 there, V must be
 //               finite), by the rotation or (MT = 2) a warp of its own.
-//   S warp      one thread issues S_t = Q_t K^T (fp16) of a key tile for the MMA tiles, two S buffers each.
-//   PV warp     one thread issues O_t += P_t V (bf16, P from TMEM). Apart from the S warp, so that neither
-//               product waits behind the other's inputs: together in one thread the two cost some
-//               2100 cycles a tile, more in tests and jumps than in products.
+//   S warps     (one per MMA tile) one thread issues S_t = Q_t K^T (fp16) of a key tile, two S buffers.
+//   PV warps    (one per MMA tile) one thread issues O_t += P_t V (bf16, P from TMEM). A warp for each
+//               product of each tile: an issuing thread takes about as long for its waits and jumps as
+//               for the products. One thread for both products of a tile, S(j + 2) right behind PV(j) in
+//               its in-order queue, took 1500 ns a key tile of two MMA tiles where this takes 1050.
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
 //               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 over the S columns
 //               (V is stored bf16 and both operands have one type; the sum is of the unrounded
@@ -67,9 +68,9 @@ struct Cfg {
   static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
   // Roles of the warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
   // instruction cache is shared by its warps. Rotation: warps 4..11.
-  static constexpr int THREADS = MT == 2 ? 416 : 512;
-  static constexpr int W_S = MT == 2 ? 8 : 15, W_PV = MT == 2 ? 9 : 13, W_META = MT == 2 ? 10 : 14, W_LOAD = MT == 2 ? 11 : 12,
-                       W_MEND = MT == 2 ? 12 : -1;
+  static constexpr int THREADS = MT == 2 ? 480 : 512;
+  static constexpr int W_S = MT == 2 ? 8 : 15, W_PV = MT == 2 ? 10 : 13;   // the first of MT
+  static constexpr int W_META = MT == 2 ? 12 : 14, W_LOAD = MT == 2 ? 13 : 12, W_MEND = MT == 2 ? 14 : -1;
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
@@ -86,7 +87,7 @@ struct Cfg {
                        B_READY = B_XEMPTY + NX, B_KEMPTY = B_READY + NK, B_VFULL = B_KEMPTY + NK,
                        B_VEMPTY = B_VFULL + NV, B_VREADY = B_VEMPTY + NV, B_SFULL = B_VREADY + (MT == 2 ? NV : 0), B_PREADY = B_SFULL + MT * NBS,
                        B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS, B_QEMPTY = B_QFULL + MT * NQ,
-                       B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + 2;
+                       B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + 2 * MT;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
   // TMEM columns: O_t at D t, S buffer b of tile t at TM_S + 128 t + 64 b, its P over the first half
@@ -255,6 +256,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// 32 bytes, a whole sector: the rows of a warp's store lie a row apart
+__device__ __forceinline__ void stg256(void* p, const uint32_t* u) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+               "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   tmem_ld16(taddr, v);
   tmem_ld16(taddr + 16, v + 16);
@@ -374,18 +381,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       for (int k = 0; k < n; ++k) mbar_init(bar(i + k), count);
     };
     init(C::B_META, NWIN, 1);
-    init(C::B_RFREE, NWIN, 4 * MT + (MT == 2 ? 4 : 3));
+    init(C::B_RFREE, NWIN, 4 * MT + 2 * MT + (MT == 2 ? 2 : 1));
     init(C::B_XFULL, C::NX, 1);
     init(C::B_XEMPTY, C::NX, C::NR);
     init(C::B_READY, NK, MT == 2 ? 1 : C::NR);
     if (MT == 2) init(C::B_VREADY, NV, 1);
-    init(C::B_KEMPTY, NK, 1);
+    init(C::B_KEMPTY, NK, MT);
     init(C::B_VFULL, NV, 1);
-    init(C::B_VEMPTY, NV, 1);
+    init(C::B_VEMPTY, NV, MT);
     init(C::B_SFULL, MT * NBS, 1);
     init(C::B_PREADY, MT * NBS, 4);
     init(C::B_PVDONE, MT * NBS, 1);
-    init(C::B_QFULL, 2 * MT * NQ + 2, 1);   // QFULL, QEMPTY, DONE
+    init(C::B_QFULL, 2 * MT * NQ + 2 * MT, 1);   // QFULL, QEMPTY, DONE
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == C::W_S) {
@@ -526,24 +533,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
         if (dst) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(dst + c0 + 8 * c) =
-                make_uint4(pack_f16x2(o[8 * c], o[8 * c + 1]), pack_f16x2(o[8 * c + 2], o[8 * c + 3]),
-                           pack_f16x2(o[8 * c + 4], o[8 * c + 5]), pack_f16x2(o[8 * c + 6], o[8 * c + 7]));
+          for (int c = 0; c < 32; c += 16) {
+            uint32_t u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = pack_f16x2(o[c + 2 * e], o[c + 2 * e + 1]);
+            stg256(dst + c0 + c, u);
+          }
         } else if (po) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<float4*>(po + c0 + 4 * c) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+          for (int c = 0; c < 32; c += 8) stg256(po + c0 + c, reinterpret_cast<const uint32_t*>(o + c));
         }
       }
       fence_before();   // the next item's first PV overwrites O only after this warp's next P
     }
     if (!ok) give_up();
-  } else if (warp == C::W_S) {
-    // =============================== S products
+  } else if ((warp >= C::W_S && warp < C::W_S + MT) || (warp >= C::W_PV && warp < C::W_PV + MT)) {
+    // =============================== products: S or PV of MMA tile t
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_s(128, KT);
-      uint32_t gt = 0, ct[MT] = {}, qi[MT] = {};   // tiles of the CTA, of the MMA tiles; items of them
+      const bool s_warp = warp >= C::W_S && warp < C::W_S + MT;
+      const int t = s_warp ? warp - C::W_S : warp - C::W_PV;
+      constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
+      const int full = s_warp ? C::B_READY : MT == 2 ? C::B_VREADY : C::B_VFULL, empty = s_warp ? C::B_KEMPTY : C::B_VEMPTY;
+      uint32_t gt = 0, ct = 0, qi = 0;   // tiles of the CTA, of the MMA tile; items of it
       bool ok = true;
 #pragma unroll 1
       for (uint32_t win = 0; ok; ++win) {
@@ -552,82 +563,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         const int flags = sRec[win % NWIN].flags, n = sRec[win % NWIN].tiles;
         if (flags & kEnd) break;
         mbar_arrive(bar(C::B_RFREE + win % NWIN));
+        const bool mine = t == 0 || (flags & kTwo);
+        const uint32_t qb = qi % NQ, qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
+        if (s_warp && mine && (flags & kFirst)) ok = wait(C::B_QFULL + t * NQ + qb, (qi / NQ) & 1);
 #pragma unroll 1
-        for (int j = 0; j < n; ++j, ++gt) {
-          const int st = gt % NK;
-          ok = wait(C::B_READY + st, (gt / NK) & 1);
+        for (int j = 0; j < n && ok; ++j, ++gt) {
+          const int st = s_warp ? gt % NK : gt % NV;
+          ok = wait(full + st, (s_warp ? gt / NK : gt / NV) & 1);
+          if (!mine) {                  // its share of the stage is released
+            if (ok) mbar_arrive(bar(empty + st));
+            continue;
+          }
+          const int b = ct % NBS;
+          // S: the buffer's P has been used (the first round's waits return at once); PV: its P is written
+          ok = ok && (s_warp ? wait(C::B_PVDONE + t * NBS + b, (ct / NBS + 1) & 1) : wait(C::B_PREADY + t * NBS + b, (ct / NBS) & 1));
           if (!ok) break;
-          const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            if (t == 1 && !(flags & kTwo)) continue;
-            const int b = ct[t] % NBS, qb = qi[t] % NQ;
-            if (j == 0 && (flags & kFirst)) ok = ok && wait(C::B_QFULL + t * NQ + qb, (qi[t] / NQ) & 1);
-            // the buffer's P has been used; the first round's waits return at once
-            ok = ok && wait(C::B_PVDONE + t * NBS + b, (ct[t] / NBS + 1) & 1);
-            if (!ok) break;
-            fence_after();
-            const uint32_t qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
-            const uint32_t to = tmem + C::TM_S + 128 * t + KT * b;
-            umma_ss<false>(to, qd, kd, id_s);
+          fence_after();
+          const uint32_t buf = tmem + C::TM_S + 128 * t + KT * b;
+          if (s_warp) {
+            const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
+            umma_ss<false>(buf, qd, kd, id_s);
 #pragma unroll
             for (int k = 1; k < D / 16; ++k)  // 16 dims: 32 bytes; 64 dims: a half
-              umma_ss<true>(to, qd + (k >> 2) * (16384 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
-            umma_commit(bar(C::B_SFULL + t * NBS + b));
-            ++ct[t];
-            if (j == n - 1 && (flags & kLast)) {
-              umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
-              ++qi[t];
-            }
-          }
-          if (!ok) break;
-          umma_commit(bar(C::B_KEMPTY + st));
-        }
-      }
-      if (!ok) give_up();
-      umma_commit(bar(C::B_DONE));   // fires once every MMA of this thread has retired
-      mbar_wait_on(bar(C::B_DONE), 0, 0, a.flag);
-    }
-  } else if (warp == C::W_PV) {
-    // =============================== PV products
-    if (lane == 0) {
-      constexpr uint32_t id_pv = idesc_pv(128, D);
-      uint32_t gt = 0, ct[MT] = {};
-      bool ok = true;
-#pragma unroll 1
-      for (uint32_t win = 0; ok; ++win) {
-        ok = wait_meta(win);
-        if (!ok) break;
-        const int flags = sRec[win % NWIN].flags, n = sRec[win % NWIN].tiles;
-        if (flags & kEnd) break;
-        mbar_arrive(bar(C::B_RFREE + win % NWIN));
-#pragma unroll 1
-        for (int j = 0; j < n; ++j, ++gt) {
-          const int st = gt % NV;
-          const bool first = j == 0 && (flags & kFirst);
-          const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
-          ok = wait((MT == 2 ? C::B_VREADY : C::B_VFULL) + st, (gt / NV) & 1);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            if (t == 1 && !(flags & kTwo)) continue;
-            const int b = ct[t] % NBS;
-            ok = ok && wait(C::B_PREADY + t * NBS + b, (ct[t] / NBS) & 1);
-            if (!ok) break;
-            fence_after();
-            const uint32_t pa = tmem + C::TM_S + 128 * t + KT * b;
+              umma_ss<true>(buf, qd + (k >> 2) * (16384 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
+          } else {
+            const bool first = j == 0 && (flags & kFirst);
+            const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
 #pragma unroll
             for (int k = 0; k < KP; ++k)      // 16 keys: a page
-              umma_ts(tmem + D * t, pa + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
-            umma_commit(bar(C::B_PVDONE + t * NBS + b));
-            ++ct[t];
+              umma_ts(tmem + D * t, buf + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
           }
-          if (!ok) break;
-          umma_commit(bar(C::B_VEMPTY + st));
+          umma_commit(bar((s_warp ? C::B_SFULL : C::B_PVDONE) + t * NBS + b));
+          umma_commit(bar(empty + st));
+          ++ct;
+        }
+        if (s_warp && ok && mine && (flags & kLast)) {
+          umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
+          ++qi;
         }
       }
       if (!ok) give_up();
-      umma_commit(bar(C::B_DONE + 1));
-      mbar_wait_on(bar(C::B_DONE + 1), 0, 0, a.flag);
+      const int d = C::B_DONE + (s_warp ? 0 : MT) + t;
+      umma_commit(bar(d));              // fires once every MMA of this thread has retired
+      mbar_wait_on(bar(d), 0, 0, a.flag);
     }
   } else if (warp == C::W_META) {
     // =============================== window records, K
@@ -1069,9 +1047,10 @@ void batch_tc_view(BatchView& v, bool wide) {
   v.mrows = v.rb * v.rep;
   v.kpages = KP;
   v.whole_tiles = wide;
-  v.cost_item = 4;
+  // from per-CTA times: an item's start and drain take about as long as 2.4 key tiles (1.6 of one MMA tile)
+  v.cost_item = wide ? 19 : 13;
   v.cost_full = 8;
-  v.cost_half = wide ? 5 : 8;
+  v.cost_half = wide ? 6 : 8;
 }
 
 pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st) {

@@ -30,7 +30,7 @@ def window(lib, dtype=L.PIC_BF16, T=1, H=8, G=2, D=128, q=A, row_start=A, n=1, k
                                 dict(n=0), dict(kv=None), dict(table=None), dict(stride=0), dict(page_pos=A),
                                 dict(n_pages=A), dict(w=-1), dict(sinks=-1), dict(k=None), dict(v=None), dict(pool=0),
                                 dict(rope=None), dict(positions=15), dict(out=None), dict(scratch=None), dict(size=100),
-                                dict(q=A + 8), dict(k=A + 2), dict(out=A + 4), dict(scratch=A + 16)], ids=str)
+                                dict(q=A + 8), dict(k=A + 2), dict(out=A + 16), dict(scratch=A + 16)], ids=str)
 def test_window_refuses(lib, kw):
     assert window(lib, **kw) == L.PIC_ERR_INVALID_ARG
     assert lib.pic_last_error()
