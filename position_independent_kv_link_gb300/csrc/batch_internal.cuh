@@ -10,7 +10,7 @@ struct BatchCut {         // the item that CTA c's share begins inside of, for t
   int block, g;
 };
 struct BatchHead {        // written by CTA 0
-  unsigned U, len;        // length of the cost axis, of a share
+  unsigned U, len;        // length of the cost axis, of a share (0: no item is cut)
   int n_prefix, n_blocks; // prefix row blocks; all row blocks
 };
 
@@ -82,6 +82,7 @@ struct PlanShared {
   unsigned scan[33];
   BatchBlock block;      // a copy of the first one
   int ends[2];
+  unsigned edge[2];
 };
 
 // The kernels' code is kept small: what runs once or seldom is not inlined (an instruction cache
@@ -167,6 +168,22 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
   const unsigned part = share_len(U, a.grid);
   s.x0 = share(U, part, blockIdx.x);
   s.x1 = share(U, part, blockIdx.x + 1);
+  const bool whole = (long long)nb * v.G >= (long long)kWholeItems * a.grid;
+  if (whole) {   // the edges move to the next item's start
+    if (tid < 2) sh.edge[tid] = U;
+    __syncthreads();
+    unsigned c = cum;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      if (per_b > 1) plan_block(a, b, n_pre, live, one, kept);
+      kept.cum = c;
+      c += block_len(v, kept);
+      if (kept.cum <= s.x0 && s.x0 < c) sh.edge[0] = item_edge(v, kept, s.x0);
+      if (kept.cum <= s.x1 && s.x1 < c) sh.edge[1] = item_edge(v, kept, s.x1);
+    }
+    __syncthreads();
+    s.x0 = sh.edge[0], s.x1 = sh.edge[1];
+  }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     if (per_b > 1) plan_block(a, b, n_pre, live, one, kept);
@@ -186,7 +203,7 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
   if (tid == 0) {
     BatchCut cut{-1, 0};
     const BatchBlock& b = sh.block;
-    if (s.x0 < s.x1 && s.x0 > 0) {
+    if (!whole && s.x0 < s.x1 && s.x0 > 0) {
       const unsigned ilen = item_len(v, b), g = (s.x0 - b.cum) / ilen, start = b.cum + g * ilen;
       if (start < s.x0 && owner(part, start) == (int)blockIdx.x - 1) cut = BatchCut{sh.ends[0], (int)g};
     }
@@ -194,7 +211,7 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
   }
   if (blockIdx.x == 0) {
     batch_flag(a.flag, bad);
-    if (tid == 0) *a.head = BatchHead{U, part, n_pre, nb};
+    if (tid == 0) *a.head = BatchHead{U, whole ? 0 : part, n_pre, nb};
   }
   __syncthreads();
   s.first = sh.ends[0];

@@ -8,6 +8,7 @@
 // tiles of kpages pages. Items lie end to end on a cost axis, blocks in order (prefix blocks
 // first), the KV heads of a block in order, each item cost_item + tiles x tile_cost long. The axis
 // is cut into equal shares, one per CTA: CTA c takes the key tiles whose start lies in [X_c, X_c+1).
+// With many items per CTA (kWholeItems) the shares' edges move to the next item's start instead.
 // An item cut by a share boundary leaves partial results: CTA c's slot 2c holds its part of an
 // item begun by an earlier CTA, slot 2c + 1 its part of an item it begins and does not finish
 // (at most one of each per CTA, so the slots never collide).
@@ -172,6 +173,14 @@ inline double axis_bound(const BatchView& v, double n_own, double n_prefix) {
   const double item = v.cost_item + (pdiv(v.stride, v.kpages) + 1.0) * v.cost_full;
   const double pre = v.cost_item + (pdiv(v.pre_pages, v.kpages) + 1.0) * v.cost_full;
   return (n_own * item + n_prefix * pre) * v.G;
+}
+// From this many items per CTA on, none is cut: the longest share is then at most 1 / 4 over the others'
+// length, less with more items, where cutting costs the parts' way through memory and the merge.
+constexpr int kWholeItems = 4;
+// The right edge of a share at x, inside block b: the item's start at or after x.
+PIC_HD unsigned item_edge(const BatchView& v, const BatchBlock& b, unsigned x) {
+  const unsigned ilen = item_len(v, b);
+  return b.cum + (x - b.cum + ilen - 1) / ilen * ilen;
 }
 // Shares of an axis of length U: the length of each (the last ones may be shorter or empty), the left
 // end of CTA c's, the CTA a place x belongs to.

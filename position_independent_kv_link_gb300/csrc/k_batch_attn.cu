@@ -205,8 +205,11 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
     p.U = hd.U, p.len = hd.len;
     p.nt = block_tiles(s.v, b), p.c = tile_cost(s.v, b);
     p.start = b.cum + g * item_len(s.v, b);
-    p.c0 = owner(p.len, p.start);
-    p.n = owner(p.len, tile_place(s.v, p.start, p.c, p.nt - 1)) - p.c0 + 1;
+    p.c0 = 0, p.n = 1;
+    if (p.len) {
+      p.c0 = owner(p.len, p.start);
+      p.n = owner(p.len, tile_place(s.v, p.start, p.c, p.nt - 1)) - p.c0 + 1;
+    }
     return p;
   };
   const BatchHead hd = *a.s[1].head, hp = *a.s[0].head;

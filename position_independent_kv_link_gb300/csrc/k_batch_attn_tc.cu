@@ -17,13 +17,14 @@
 //               own. One rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S).
 //   V mending   rows that hold no key any row of the block sees are zeroed in V (P is 0 there, V must be
 //               finite), by the rotation or (MT = 2) a warp of its own.
-//   S warps     (one per MMA tile) one thread issues S_t = Q_t K^T (fp16) of a key tile, two S buffers.
+//   S warps     (one per MMA tile) one thread issues S_t = Q_t K^T (fp16) of a key tile as soon as the
+//               softmax has the S before it in registers.
 //   PV warps    (one per MMA tile) one thread issues O_t += P_t V (bf16, P from TMEM). A warp for each
 //               product of each tile: an issuing thread takes about as long for its waits and jumps as
 //               for the products. One thread for both products of a tile, S(j + 2) right behind PV(j) in
 //               its in-order queue, took 1500 ns a key tile of two MMA tiles where this takes 1050.
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
-//               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 over the S columns
+//               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 into one of two P buffers
 //               (V is stored bf16 and both operands have one type; the sum is of the unrounded
 //               fp32 weights), and the item's result: out, or for parts of items and for prefix
 //               batches the normalized fp32 row with its maximum and sum for the merge.
@@ -53,7 +54,7 @@ constexpr float kRescale = 8.f;           // rescale O when the row maximum grow
 constexpr unsigned long long kWaitLimit = 4000000000ull;   // cycles, about 2 s
 
 constexpr int KT = 64, KP = KT / kPage;   // keys, pages of a tile
-constexpr int NBS = 2;                    // S buffers per MMA tile
+constexpr int NBP = 2;                    // P buffers per MMA tile (its S has one)
 constexpr int WIN = 32, WT = WIN / KP;    // pages, tiles of a window
 constexpr int NWIN = 6;                   // window records
 
@@ -85,12 +86,13 @@ struct Cfg {
   // barriers
   static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_XFULL = B_RFREE + NWIN, B_XEMPTY = B_XFULL + NX,
                        B_READY = B_XEMPTY + NX, B_KEMPTY = B_READY + NK, B_VFULL = B_KEMPTY + NK,
-                       B_VEMPTY = B_VFULL + NV, B_VREADY = B_VEMPTY + NV, B_SFULL = B_VREADY + (MT == 2 ? NV : 0), B_PREADY = B_SFULL + MT * NBS,
-                       B_PVDONE = B_PREADY + MT * NBS, B_QFULL = B_PVDONE + MT * NBS, B_QEMPTY = B_QFULL + MT * NQ,
+                       B_VEMPTY = B_VFULL + NV, B_VREADY = B_VEMPTY + NV, B_SFULL = B_VREADY + (MT == 2 ? NV : 0),
+                       B_SFREE = B_SFULL + MT, B_PREADY = B_SFREE + MT, B_PVDONE = B_PREADY + MT * NBP,
+                       B_QFULL = B_PVDONE + MT * NBP, B_QEMPTY = B_QFULL + MT * NQ,
                        B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + 2 * MT;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
-  // TMEM columns: O_t at D t, S buffer b of tile t at TM_S + 128 t + 64 b, its P over the first half
+  // TMEM columns: O_t at D t, S_t at TM_S + 128 t, P buffer b of tile t 64 + 32 b behind it
   static constexpr uint32_t TM_S = MT * D;
   static constexpr uint32_t TMEM_COLS = MT == 2 ? 512 : 256;
 };
@@ -109,9 +111,9 @@ struct WinRec {           // 48 bytes
 // reads records has arrived at RFREE for the window before in its slot. XFULL, XEMPTY: between the
 // meta warp and the rotation, all of whose warps arrive. READY (of K), KEMPTY: the rotation, or the meta
 // warp's TMA, of tile j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows
-// PV of j, which waits for VREADY (or VFULL); VREADY: VFULL seen and mended. SFULL, PREADY, PVDONE: a
-// ring of the S warp, warpgroup t and the PV warp; S(j + 2) into a buffer follows the end of PV(j),
-// which waits for all four warps' P(j). QFULL, QEMPTY: between the load and the S warp.
+// PV of j, which waits for VREADY (or VFULL); VREADY: VFULL seen and mended. SFULL, SFREE: between the
+// S warp and warpgroup t, all of whose warps arrive. PREADY, PVDONE: between warpgroup t and the PV
+// warp; P(j + 2) into a buffer follows the end of PV(j). QFULL, QEMPTY: between the load and the S warp.
 // No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN and K asked
 // for up to window i - 3, that is the S products NX + NK tiles before: with windows of one tile, of
 // tile i - 3 - NX - NK at the latest, while its readers are never more than two windows ahead of the S
@@ -389,9 +391,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     init(C::B_KEMPTY, NK, MT);
     init(C::B_VFULL, NV, 1);
     init(C::B_VEMPTY, NV, MT);
-    init(C::B_SFULL, MT * NBS, 1);
-    init(C::B_PREADY, MT * NBS, 4);
-    init(C::B_PVDONE, MT * NBS, 1);
+    init(C::B_SFULL, MT, 1);
+    init(C::B_SFREE, MT, 4);
+    init(C::B_PREADY, MT * NBP, 4);
+    init(C::B_PVDONE, MT * NBP, 1);
     init(C::B_QFULL, 2 * MT * NQ + 2 * MT, 1);   // QFULL, QEMPTY, DONE
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -435,18 +438,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       }
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++ct) {
-        const int b = ct % NBS;
-        const uint32_t t_s = t_sb + KT * b;
+        const int b = ct % NBP;
+        const uint32_t t_p = t_sb + KT + KT / 2 * b;
         const int2 lim = sLim[win % NWIN * WT + j];
         const bool masked = __any_sync(0xffffffffu, lim.x > qp || lim.y <= lo);
-        ok = __all_sync(0xffffffffu, wait(C::B_SFULL + t * NBS + b, (ct / NBS) & 1));
+        ok = __all_sync(0xffffffffu, wait(C::B_SFULL + t, ct & 1));
         if (!ok) break;
         if (!idle) {
           fence_after();
           float s[KT];
 #pragma unroll
-          for (int c = 0; c < KT; c += 16) tmem_ld16(t_s + c, s + c);
+          for (int c = 0; c < KT; c += 16) tmem_ld16(t_sb + c, s + c);
           tmem_wait_ld();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_SFREE + t));   // the next S may come
           if (masked) {
             const int4* pages = sPage + win % NWIN * WIN + j * KP;
 #pragma unroll
@@ -466,6 +472,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           mref = mnew;
           const float mz = mref == -INFINITY ? 0.f : -mref;   // nothing seen so far: every s is -inf, p = 0
           float2 sum[2] = {make_float2(l * scale, 0.f), make_float2(0.f, 0.f)};
+          // the P buffer's PV two tiles before is done (the first round's waits return at once)
+          ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + b, (ct / NBP + 1) & 1));
+          if (!ok) break;
+          fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pv[16];
@@ -477,12 +487,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
               sum[e & 1] = add2(sum[e & 1], p);
               pv[e] = pack_bf16x2(p.x, p.y);
             }
-            tmem_st16(t_s + 16 * c, pv);
+            tmem_st16(t_p + 16 * c, pv);
           }
           l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           if (__any_sync(0xffffffffu, scale != 1.f)) {
             // O holds the item's earlier tiles (a finite earlier maximum): their PVs first
-            ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBS + (ct - 1) % NBS, ((ct - 1) / NBS) & 1));
+            ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + (ct - 1) % NBP, ((ct - 1) / NBP) & 1));
             if (!ok) break;
             fence_after();
 #pragma unroll 1
@@ -500,13 +510,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           fence_before();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_PREADY + t * NBS + b));
+        if (lane == 0) {
+          if (idle) mbar_arrive(bar(C::B_SFREE + t));
+          mbar_arrive(bar(C::B_PREADY + t * NBP + b));
+        }
       }
       if (!ok) break;
       done_with(win);
       if (!(flags & kLast) || n == 0) continue;
       // the item's result
-      ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBS + (ct - 1) % NBS, ((ct - 1) / NBS) & 1));
+      ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + (ct - 1) % NBP, ((ct - 1) / NBP) & 1));
       if (!ok) break;
       if (idle) continue;
       fence_after();
@@ -574,12 +587,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             if (ok) mbar_arrive(bar(empty + st));
             continue;
           }
-          const int b = ct % NBS;
-          // S: the buffer's P has been used (the first round's waits return at once); PV: its P is written
-          ok = ok && (s_warp ? wait(C::B_PVDONE + t * NBS + b, (ct / NBS + 1) & 1) : wait(C::B_PREADY + t * NBS + b, (ct / NBS) & 1));
+          const int b = ct % NBP;
+          // S: the softmax has read the one before (the first wait returns at once); PV: its P is written
+          ok = ok && (s_warp ? wait(C::B_SFREE + t, (ct + 1) & 1) : wait(C::B_PREADY + t * NBP + b, (ct / NBP) & 1));
           if (!ok) break;
           fence_after();
-          const uint32_t buf = tmem + C::TM_S + 128 * t + KT * b;
+          const uint32_t buf = tmem + C::TM_S + 128 * t + (s_warp ? 0 : KT + KT / 2 * b);
           if (s_warp) {
             const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
             umma_ss<false>(buf, qd, kd, id_s);
@@ -593,7 +606,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             for (int k = 0; k < KP; ++k)      // 16 keys: a page
               umma_ts(tmem + D * t, buf + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
           }
-          umma_commit(bar((s_warp ? C::B_SFULL : C::B_PVDONE) + t * NBS + b));
+          umma_commit(bar(s_warp ? C::B_SFULL + t : C::B_PVDONE + t * NBP + b));
           umma_commit(bar(empty + st));
           ++ct;
         }

@@ -52,7 +52,15 @@ int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const
   const unsigned len = share_len(U, grid);
   if (share(U, len, grid) != U) return 2;   // the shares do not reach the end
   for (int c = 0; c < grid && U > 0; ++c) {
-    const unsigned x0 = share(U, len, c), x1 = share(U, len, c + 1);
+    unsigned x0 = share(U, len, c), x1 = share(U, len, c + 1);
+    const bool whole_items = (long long)blocks.size() * v.G >= (long long)kWholeItems * grid;
+    if (whole_items)
+      for (unsigned* x : {&x0, &x1})
+        for (const BatchBlock& b : blocks)
+          if (b.cum <= *x && *x < b.cum + block_len(v, b)) {
+            *x = item_edge(v, b, *x);
+            break;
+          }
     for (size_t i = 0; i < blocks.size(); ++i) {
       const BatchBlock& b = blocks[i];
       const int nt = block_tiles(v, b), tc = tile_cost(v, b);
@@ -61,7 +69,8 @@ int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const
         const int j0 = tile_lower(v, start, nt, tc, x0), j1 = tile_lower(v, start, nt, tc, x1);
         if (j0 >= j1) continue;
         for (int j = j0; j < j1; ++j)
-          if (owner(len, tile_place(v, start, tc, j)) != c) ++wrong;
+          if (!whole_items && owner(len, tile_place(v, start, tc, j)) != c) ++wrong;
+        if (whole_items && (j0 != 0 || j1 != nt)) ++wrong;
         if (ni >= max_items) return 1;
         int* o = items + 12 * ni++;
         const bool whole = j0 == 0 && j1 == nt;
