@@ -171,7 +171,7 @@ __device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, uint32_
   }
 }
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort, unsigned* flag) {
-  return mbar_test(bar, parity) || mbar_wait_on(bar, parity, abort, flag);   // a test is far cheaper than a try
+  return mbar_test(bar, parity) || mbar_try(bar, parity) || mbar_wait_on(bar, parity, abort, flag);
 }
 // 4-D box at (0, c1, c2, c3)
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int c1, int c2, int c3, uint32_t bar) {
