@@ -5,6 +5,7 @@ marshals arguments (pointers, sizes, host arrays) and keeps borrowed tensors ali
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -401,40 +402,62 @@ def attention_plan(dtype: torch.dtype, n_heads: int, n_kv_heads: int, head_dim: 
 
 
 # ----------------------------------------------------------------------------- batched calls on device-resident lengths
+#
+# A step makes these calls once per layer, so what they check is checked cheaply (get_device, size
+# and dim rather than device and shape objects; the message is put together only on refusal).
 
-def _need(x: Optional[torch.Tensor], what: str, dtype: torch.dtype, shape, dev) -> Optional[int]:
-    """The address of a contiguous tensor of this type and shape (-1: any length) on `dev`; None for None."""
-    if x is None:
-        return None
-    if x.dtype is not dtype or x.device != dev or not x.is_contiguous() or \
-            len(x.shape) != len(shape) or any(n >= 0 and n != m for n, m in zip(shape, x.shape)):
-        want = "x".join("?" if n < 0 else str(n) for n in shape)
-        raise ValueError(f"{what}: a contiguous {dtype} tensor [{want}] on {dev} is needed, got {x.dtype} "
-                         f"{list(x.shape)} (strides {list(x.stride())}) on {x.device}")
+_I32, _F32 = torch.int32, torch.float32
+
+
+def _refuse(x, what: str, dtype, want, idx: int):
+    raise ValueError(f"{what}: a contiguous {dtype} device tensor {want} on cuda:{idx} is needed, got {x.dtype} "
+                     f"{list(x.shape)} (strides {list(x.stride())}) on {x.device}")
+
+
+def _vec(x: torch.Tensor, what: str, dtype, n: int, idx: int) -> int:
+    """The address of a contiguous tensor [n] (n < 0: any length) of this type on device idx."""
+    if x.dtype is not dtype or x.get_device() != idx or x.dim() != 1 or (n >= 0 and x.size(0) != n) or \
+            not x.is_contiguous():
+        _refuse(x, what, dtype, f"[{n if n >= 0 else '?'}]", idx)
     return x.data_ptr()
 
 
-def _batch_device(x: torch.Tensor) -> torch.device:
-    if not x.is_cuda:
+def _mat(x: torch.Tensor, what: str, n: int, m: int, idx: int) -> int:
+    """The same for int32 [n, m]."""
+    if x.dtype is not _I32 or x.get_device() != idx or x.dim() != 2 or x.size(0) != n or x.size(1) != m or \
+            not x.is_contiguous():
+        _refuse(x, what, _I32, f"[{n}, {m}]", idx)
+    return x.data_ptr()
+
+
+def _cube(x: torch.Tensor, what: str, dtype, n: int, m: int, k: int, idx: int) -> int:
+    """The same for [n, m, k] (n < 0: any)."""
+    if x.dtype is not dtype or x.get_device() != idx or x.dim() != 3 or (n >= 0 and x.size(0) != n) or \
+            x.size(1) != m or x.size(2) != k or not x.is_contiguous():
+        _refuse(x, what, dtype, f"[{n if n >= 0 else '?'}, {m}, {k}]", idx)
+    return x.data_ptr()
+
+
+def _device_index(x: torch.Tensor) -> int:
+    idx = x.get_device()
+    if idx < 0:
         raise ValueError(f"device tensors are needed, got one on {x.device}")
-    return x.device
+    return idx
 
 
-def _batch_stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> int:
+def _call(idx: int, stream: Optional[torch.cuda.Stream], f, *args):
+    """f(*args, stream) with device idx current (the current stream of that device when None), its status checked."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    return stream.cuda_stream
-
-
-def _call(dev: torch.device, f, *args):
-    """f(*args) with `dev` current, its status checked."""
-    if torch.cuda.current_device() == dev.index:
-        L.check(f(*args))
+        stream = torch.cuda.current_stream(idx)
+    elif stream.device_index != idx:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
+    if torch.cuda.current_device() == idx:
+        status = f(*args, stream.cuda_stream)
     else:
-        with torch.cuda.device(dev):
-            L.check(f(*args))
+        with torch.cuda.device(idx):
+            status = f(*args, stream.cuda_stream)
+    if status != L.PIC_OK:
+        L.check(status)
 
 
 class BatchPages:
@@ -447,14 +470,12 @@ class BatchPages:
                  n_pages: Optional[torch.Tensor] = None):
         self.kv_len, self.block_table, self.page_pos, self.n_pages = kv_len, block_table, page_pos, n_pages
 
-    def _args(self, dev):
-        n = self.kv_len.shape[0]
-        i32 = torch.int32
-        kv = _need(self.kv_len, "kv_len", i32, (n,), dev)
-        table = _need(self.block_table, "block_table", i32, (n, -1), dev)
-        stride = self.block_table.shape[1]
-        return n, (kv, table, stride, _need(self.page_pos, "page_pos", i32, (n, stride), dev),
-                   _need(self.n_pages, "n_pages", i32, (n,), dev))
+    def _args(self, idx: int):
+        kv, table, pos, np_ = self.kv_len, self.block_table, self.page_pos, self.n_pages
+        n, stride = kv.size(0) if kv.dim() == 1 else -1, table.size(1) if table.dim() == 2 else -1
+        return n, (_vec(kv, "kv_len", _I32, n, idx), _mat(table, "block_table", n, stride, idx), stride,
+                   None if pos is None else _mat(pos, "page_pos", n, stride, idx),
+                   None if np_ is None else _vec(np_, "n_pages", _I32, n, idx))
 
 
 class BlockTables:
@@ -479,33 +500,50 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     rows to its kv_len[r]; new pages come from free_blocks (from entry free_used[0] on) and are entered in
     block_table (and page_pos) in place. `out`: tensors to write (out.kv_len may be kv_len, out.n_pages n_pages,
     and free_used out.counts[1:2])."""
-    dev = _batch_device(kv_len)
-    n, i32 = kv_len.shape[0], torch.int32
+    idx = _device_index(kv_len)
+    n = kv_len.size(0) if kv_len.dim() == 1 else -1
+    stride = block_table.size(1) if block_table.dim() == 2 else -1
+    args = (n, _vec(kv_len, "kv_len", _I32, n, idx), _vec(new_len, "new_len", _I32, n, idx),
+            _mat(block_table, "block_table", n, stride, idx), stride,
+            None if page_pos is None else _mat(page_pos, "page_pos", n, stride, idx),
+            None if n_pages is None else _vec(n_pages, "n_pages", _I32, n, idx),
+            _vec(free_blocks, "free_blocks", _I32, -1, idx), free_blocks.size(0),
+            None if free_used is None else _vec(free_used, "free_used", _I32, 1, idx), first, max_rows)
     if out is None:
-        buf = torch.empty(3 * n + 4 + 2 * max_rows, dtype=i32, device=dev)
+        if max_rows < 1:
+            raise ValueError("max_rows must be at least 1")
+        # one buffer for all: [n], [n], [n + 1], [max_rows], [max_rows], [3]
+        buf = torch.empty(3 * n + 4 + 2 * max_rows, dtype=_I32, device=kv_len.device)
+        at = buf.data_ptr()
+        ptrs = (at, at + 4 * n, at + 8 * n, at + 12 * n + 4, at + 12 * n + 4 + 4 * max_rows,
+                at + 12 * n + 4 + 8 * max_rows)
         out = BlockTables(*buf.split([n, n, n + 1, max_rows, max_rows, 3]))
-    stride = block_table.shape[1] if block_table.dim() == 2 else -1
-    _call(dev, L.load().pic_op_block_tables, n, _need(kv_len, "kv_len", i32, (n,), dev),
-          _need(new_len, "new_len", i32, (n,), dev), _need(block_table, "block_table", i32, (n, stride), dev), stride,
-          _need(page_pos, "page_pos", i32, (n, stride), dev), _need(n_pages, "n_pages", i32, (n,), dev),
-          _need(free_blocks, "free_blocks", i32, (-1,), dev), free_blocks.shape[0],
-          _need(free_used, "free_used", i32, (1,), dev), first, max_rows, _need(out.kv_len, "out.kv_len", i32, (n,), dev),
-          _need(out.n_pages, "out.n_pages", i32, (n,), dev), _need(out.row_start, "out.row_start", i32, (n + 1,), dev),
-          _need(out.row_pos, "out.row_pos", i32, (max_rows,), dev),
-          _need(out.row_slot, "out.row_slot", i32, (max_rows,), dev), _need(out.counts, "out.counts", i32, (3,), dev),
-          _batch_stream(stream, dev))
+    else:
+        ptrs = (_vec(out.kv_len, "out.kv_len", _I32, n, idx), _vec(out.n_pages, "out.n_pages", _I32, n, idx),
+                _vec(out.row_start, "out.row_start", _I32, n + 1, idx),
+                _vec(out.row_pos, "out.row_pos", _I32, max_rows, idx),
+                _vec(out.row_slot, "out.row_slot", _I32, max_rows, idx), _vec(out.counts, "out.counts", _I32, 3, idx))
+    _call(idx, stream, L.load().pic_op_block_tables, *args, *ptrs)
     return out
 
 
-def _pool_args(k_layer, v_layer, rope, dev):
-    if k_layer.dim() != 4 or k_layer.shape[2] != BLOCK:
-        raise ValueError(f"a pool layer is [blocks, n_kv_heads, 16, head_dim], got {list(k_layer.shape)}")
-    nb, G, _, D = k_layer.shape
-    t = k_layer.dtype
-    dt = _dtype_code(t)
-    return (nb, G, D, dt, torch.float16 if dt == L.PIC_BF16 else torch.float32,
-            _need(k_layer, "k_layer", t, (nb, G, BLOCK, D), dev), _need(v_layer, "v_layer", t, (nb, G, BLOCK, D), dev),
-            _need(rope, "rope", torch.float32, (-1, D // 2, 2), dev))
+def _pool_args(k_layer, v_layer, rope, idx):
+    shape, t = k_layer.shape, k_layer.dtype
+    if len(shape) != 4 or shape[2] != BLOCK:
+        raise ValueError(f"a pool layer is [blocks, n_kv_heads, 16, head_dim], got {list(shape)}")
+    nb, G, _, D = shape
+    if t is torch.bfloat16:
+        dt, act = L.PIC_BF16, torch.float16
+    elif t is _F32:
+        dt, act = L.PIC_F32, _F32
+    else:
+        raise ValueError(f"unsupported dtype {t}")
+    if k_layer.get_device() != idx or not k_layer.is_contiguous():
+        _refuse(k_layer, "k_layer", t, list(shape), idx)
+    if v_layer.dtype is not t or v_layer.get_device() != idx or v_layer.shape != shape or not v_layer.is_contiguous():
+        _refuse(v_layer, "v_layer", t, list(shape), idx)
+    return (nb, G, D, dt, act, k_layer.data_ptr(), v_layer.data_ptr(), _cube(rope, "rope", _F32, -1, D // 2, 2, idx),
+            rope.size(0))
 
 
 def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torch.Tensor, row_slot: torch.Tensor,
@@ -516,41 +554,54 @@ def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torc
 
     qkv: fp32 [T, >= (n_heads + 2 n_kv_heads) head_dim], rows contiguous. Returns q [T, n_heads, head_dim], fp16 for
     bf16 pools, fp32 for fp32 pools; rows with row_slot -1 are left alone."""
-    dev = _batch_device(qkv)
-    nb, G, D, dt, act, kp, vp, rp = _pool_args(k_layer, v_layer, rope, dev)
-    if qkv.dim() != 2 or qkv.dtype is not torch.float32 or qkv.stride(1) != 1 or \
-            qkv.shape[1] < (n_heads + 2 * n_kv_heads) * D or G != n_kv_heads:
-        raise ValueError(f"qkv: fp32 rows of at least {(n_heads + 2 * n_kv_heads) * D} values for pools of {G} KV heads "
-                         f"are needed, got {qkv.dtype} {list(qkv.shape)}")
-    T = qkv.shape[0]
+    idx = _device_index(qkv)
+    nb, G, D, dt, act, kp, vp, rp, positions = _pool_args(k_layer, v_layer, rope, idx)
+    width = (n_heads + 2 * n_kv_heads) * D
+    if qkv.dim() != 2 or qkv.dtype is not _F32 or qkv.stride(1) != 1 or qkv.size(1) < width or G != n_kv_heads:
+        raise ValueError(f"qkv: fp32 rows of at least {width} values for pools of {G} KV heads are needed, got "
+                         f"{qkv.dtype} {list(qkv.shape)} (strides {list(qkv.stride())})")
+    T = qkv.size(0)
     if q_out is None:
-        q_out = torch.empty((T, n_heads, D), dtype=act, device=dev)
-    _call(dev, L.load().pic_op_qk_norm_rope, dt, T, n_heads, n_kv_heads, D, qkv.data_ptr(),
-          qkv.stride(0) if T > 1 else max(qkv.stride(0), qkv.shape[1]),
-          _need(q_gain, "q_gain", torch.float32, (D,), dev), _need(k_gain, "k_gain", torch.float32, (D,), dev), eps,
-          _need(row_pos, "row_pos", torch.int32, (T,), dev), _need(row_slot, "row_slot", torch.int32, (T,), dev), rp,
-          rope.shape[0], _need(q_out, "q_out", act, (T, n_heads, D), dev), kp, vp, nb, _batch_stream(stream, dev))
+        q_out = torch.empty((T, n_heads, D), dtype=act, device=qkv.device)
+        qo = q_out.data_ptr()
+    else:
+        qo = _cube(q_out, "q_out", act, T, n_heads, D, idx)
+    _call(idx, stream, L.load().pic_op_qk_norm_rope, dt, T, n_heads, n_kv_heads, D, qkv.data_ptr(),
+          qkv.stride(0) if T > 1 else max(qkv.stride(0), qkv.size(1)),
+          None if q_gain is None else _vec(q_gain, "q_gain", _F32, D, idx),
+          None if k_gain is None else _vec(k_gain, "k_gain", _F32, D, idx), eps,
+          _vec(row_pos, "row_pos", _I32, T, idx), _vec(row_slot, "row_slot", _I32, T, idx), rp, positions, qo, kp, vp, nb)
     return q_out
 
 
+@functools.lru_cache(maxsize=4096)
+def _attention_scratch(idx, *shape) -> int:
+    """pic_op_attention_batch_scratch_bytes on device idx (its SM count enters)."""
+    with torch.cuda.device(idx):
+        return max(256, L.load().pic_op_attention_batch_scratch_bytes(*shape))
+
+
 def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len, prefix_pages):
-    dev = _batch_device(q)
-    nb, G, D, dt, act, kp, vp, rp = _pool_args(k_layer, v_layer, rope, dev)
+    idx = _device_index(q)
+    nb, G, D, dt, act, kp, vp, rp, positions = _pool_args(k_layer, v_layer, rope, idx)
     if q.dim() != 3:
         raise ValueError(f"q is [rows, n_heads, head_dim], got {list(q.shape)}")
-    T, H = q.shape[0], q.shape[1]
-    qp = _need(q, "q", act, (T, H, D), dev)
-    n, pg = pages._args(dev)
-    lib = L.load()
+    T, H = q.size(0), q.size(1)
+    qp = _cube(q, "q", act, T, H, D, idx)
+    n, pg = pages._args(idx)
     if out is None:
-        out = torch.empty((T, H, D), dtype=act, device=dev)
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _cube(out, "out", act, T, H, D, idx)
     if scratch is None:
-        with torch.cuda.device(dev):
-            nbytes = lib.pic_op_attention_batch_scratch_bytes(dt, T, n, H, G, D, pg[2], prefix_len, prefix_pages)
-        scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-    tail = (kp, vp, nb, rp, rope.shape[0], _need(out, "out", act, (T, H, D), dev),
-            _need(scratch, "scratch", torch.uint8, (-1,), dev), scratch.shape[0])
-    return dev, lib, out, (dt, T, H, G, D, qp, _need(row_start, "row_start", torch.int32, (n + 1,), dev)), n, pg, tail
+        nbytes = _attention_scratch(idx, dt, T, n, H, G, D, pg[2], prefix_len, prefix_pages)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        sp = scratch.data_ptr()
+    else:
+        sp, nbytes = _vec(scratch, "scratch", torch.uint8, -1, idx), scratch.size(0)
+    return idx, out, scratch, (dt, T, H, G, D, qp, _vec(row_start, "row_start", _I32, n + 1, idx)), n, pg, \
+        (kp, vp, nb, rp, positions, op, sp, nbytes)
 
 
 def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages, k_layer: torch.Tensor,
@@ -561,8 +612,9 @@ def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages
     (pic_op_attention_window). q: rotated [T, H, D], fp16 for bf16 pools, fp32 for fp32 pools; so is the result. Rows
     that belong to no request are left alone (uninitialised unless `out` is given). Buffers made here belong to
     the current stream; with another `stream`, pass `out` and `scratch`."""
-    dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 0, 0)
-    _call(dev, lib.pic_op_attention_window, *head, n, *pg, window, sinks, *tail, _batch_stream(stream, dev))
+    idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
+                                                            0, 0)
+    _call(idx, stream, L.load().pic_op_attention_window, *head, n, *pg, window, sinks, *tail)
     return out
 
 
@@ -573,10 +625,9 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     """Attention of a batch whose requests share the prefix_len first positions (pic_op_attention_prefix): the pages
     prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
-    dev, lib, out, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
-                                                        prefix_len, prefix_blocks.shape[0])
-    pb = _need(prefix_blocks, "prefix_blocks", torch.int32, (-1,), dev)
-    n_pre = prefix_blocks.shape[0]
-    _call(dev, lib.pic_op_attention_prefix, *head, pb, _need(prefix_pos, "prefix_pos", torch.int32, (n_pre,), dev), n_pre,
-          prefix_len, n, *pg, *tail, _batch_stream(stream, dev))
+    n_pre = prefix_blocks.size(0) if prefix_blocks.dim() == 1 else -1
+    idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
+                                                            prefix_len, n_pre)
+    _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, n_pre, idx),
+          None if prefix_pos is None else _vec(prefix_pos, "prefix_pos", _I32, n_pre, idx), n_pre, prefix_len, n, *pg, *tail)
     return out
