@@ -13,7 +13,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kCluster = 8;
-constexpr int kMaxReqs = 12288;       // two ints of shared memory per request
+constexpr int kMaxReqs = 12288;       // four ints of shared memory per request
+constexpr int kMaxStride = 1 << 26;    // pages of a request, packed with 5 bits of its last page's rows
+constexpr int kRowsInCluster = 4096;
 
 struct TablesArgs {
   int n, stride, n_free, max_rows, first;
@@ -66,71 +68,85 @@ __device__ __forceinline__ int find(const int* base, int n, int x) {
   return lo;
 }
 
-// One cluster. Every CTA scans all the lengths (so none waits for another's sums), then the rows
-// and the new pages are dealt over the cluster's threads, each finding its request by bisection in
-// shared memory; the lengths themselves are overwritten (the outputs may be the inputs) only after
-// a cluster barrier, when no CTA reads them any more. A call moves a few KB: latency bounds it.
+__device__ __forceinline__ void put_row(const TablesArgs& a, int t, int pos, int blk, int row) {
+  const bool good = blk >= 0 && blk < INT_MAX / kPage;
+  if (!good) batch_flag(a.flag, kBatchBadBlock);
+  a.row_pos[t] = pos + a.first;
+  a.row_slot[t] = good ? blk * kPage + row : -1;
+}
+
+// One cluster. Every CTA scans all the lengths (so none waits for another's sums) and keeps what it
+// read in shared memory; then the new pages, and the rows when there are few, are dealt over the
+// cluster's threads, each finding its request by bisection there. The lengths themselves are
+// overwritten (the outputs may be the inputs) only after a cluster barrier, when no CTA reads them
+// any more. A call moves a few KB: the latency of its loads bounds it.
+template <bool kRowsHere>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tables_kernel(const __grid_constant__ TablesArgs a) {
   extern __shared__ int sm[];
-  int* s_row = sm;                    // [n] rows of the requests before
-  int* s_blk = sm + a.n;              // [n] new pages of the requests before
+  int* s_row = sm;                    // [n] new rows, then those of the requests before
+  int* s_blk = sm + a.n;              // [n] new pages, then those of the requests before
+  int* s_kv = sm + 2 * a.n;           // [n]
+  int* s_np = sm + 3 * a.n;           // [n] pages * 32 + rows of the last page
   __shared__ long long s_scan[kThreads / 32 + 1];
   __shared__ unsigned s_bad;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = cluster.block_rank();
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  const int per = pdiv(a.n, kThreads), r0 = pmin(tid * per, a.n), r1 = pmin(r0 + per, a.n);
   unsigned bad = 0;
-  long long rows = 0, more = 0, all_rows, all_more;
-  for (int r = r0; r < r1; ++r) {
+#pragma unroll 4
+  for (int r = tid; r < a.n; r += kThreads) {
     const Req q = request(a, r, bad);
-    rows += q.m;
-    more += q.more;
+    s_row[r] = q.m;
+    s_blk[r] = q.more;
+    s_kv[r] = q.kv;
+    s_np[r] = q.np * 32 + (q.ok ? q.kv - q.last : 0);
   }
   const int used = a.free_used ? *a.free_used : 0;
+  __syncthreads();
+  const int per = pdiv(a.n, kThreads), r0 = pmin(tid * per, a.n), r1 = pmin(r0 + per, a.n);
+  long long rows = 0, more = 0, all_rows, all_more;
+  for (int r = r0; r < r1; ++r) {
+    rows += s_row[r];
+    more += s_blk[r];
+  }
   long long at_row = block_scan<kThreads>(rows, s_scan, all_rows);
   long long at_blk = block_scan<kThreads>(more, s_scan, all_more);
   if (all_rows > a.max_rows) bad |= kBatchCapacity;
   if (used < 0 || all_more > (long long)a.n_free - used) bad |= kBatchOutOfBlocks;
   if (bad) atomicOr(&s_bad, bad);
   for (int r = r0; r < r1; ++r) {
-    unsigned ignored = 0;
-    const Req q = request(a, r, ignored);
+    const int m = s_row[r], b = s_blk[r];
     s_row[r] = (int)at_row;
     s_blk[r] = (int)at_blk;
-    at_row += q.m;
-    at_blk += q.more;
+    at_row += m;
+    at_blk += b;
   }
   __syncthreads();
   bad = s_bad;                        // the same in every CTA: all or nothing
   const int n_rows = bad ? 0 : (int)all_rows, n_more = bad ? 0 : (int)all_more;
   const int t0 = rank * kThreads + tid, step = kCluster * kThreads;
-  for (int t = t0; t < a.max_rows; t += step) {
-    int pos = 0, slot = -1;
-    if (t < n_rows) {
-      const int r = find(s_row, a.n, t);
-      unsigned ignored = 0;
-      const Req q = request(a, r, ignored);
-      pos = q.kv + t - s_row[r];
-      const int over = pos - q.room;
-      const int blk = over >= 0 ? a.free_blocks[used + s_blk[r] + over / kPage]
-                                : a.block_table[(size_t)r * a.stride + q.np - 1];
-      const bool good = blk >= 0 && blk < INT_MAX / kPage;
-      slot = good ? blk * kPage + (over >= 0 ? over % kPage : pos - q.last) : -1;
-      if (!good) batch_flag(a.flag, kBatchBadBlock);
-      pos += a.first;
+  if constexpr (kRowsHere) {
+    for (int t = t0; t < a.max_rows; t += step) {
+      int pos = 0, slot = -1;
+      if (t < n_rows) {
+        const int r = find(s_row, a.n, t), np = s_np[r] >> 5, kv = s_kv[r], last = kv - (s_np[r] & 31);
+        pos = kv + t - s_row[r];
+        const int over = pos - last - kPage;
+        const int blk = over >= 0 ? a.free_blocks[used + s_blk[r] + over / kPage]
+                                  : a.block_table[(size_t)r * a.stride + np - 1];
+        put_row(a, t, pos, blk, over >= 0 ? over % kPage : pos - last);
+      } else {
+        a.row_pos[t] = 0;
+        a.row_slot[t] = -1;
+      }
     }
-    a.row_pos[t] = pos;
-    a.row_slot[t] = slot;
   }
   for (int i = t0; i < n_more; i += step) {
     const int r = find(s_blk, a.n, i), k = i - s_blk[r];
-    unsigned ignored = 0;
-    const Req q = request(a, r, ignored);
-    const size_t at = (size_t)r * a.stride + q.np + k;
+    const size_t at = (size_t)r * a.stride + (s_np[r] >> 5) + k;
     a.block_table[at] = a.free_blocks[used + i];
-    if (a.page_pos) a.page_pos[at] = a.first + q.room + kPage * k;
+    if (a.page_pos) a.page_pos[at] = a.first + s_kv[r] - (s_np[r] & 31) + kPage * (k + 1);
   }
   // the lengths of this thread's requests, read before the barrier
   constexpr int kKeep = kMaxReqs / (kThreads * kCluster);
@@ -139,10 +155,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tab
   for (int i = 0; i < kKeep; ++i) {
     const int r = t0 + i * step;
     if (r < a.n) {
-      unsigned ignored = 0;
-      const Req q = request(a, r, ignored);
-      kv[i] = bad ? a.kv_len[r] : q.kv + q.m;
-      np[i] = bad ? (a.page_pos ? a.n_pages[r] : q.np) : q.np + q.more;
+      const bool end = r == a.n - 1;
+      kv[i] = bad ? a.kv_len[r] : s_kv[r] + (end ? n_rows : s_row[r + 1]) - s_row[r];
+      np[i] = bad ? (a.page_pos ? a.n_pages[r] : s_np[r] >> 5)
+                  : (s_np[r] >> 5) + (end ? n_more : s_blk[r + 1]) - s_blk[r];
     }
   }
   cluster.sync();
@@ -161,6 +177,46 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) tab
     a.counts[1] = used + n_more;
     a.counts[2] = (int)bad;
     batch_flag(a.flag, bad);
+  }
+}
+
+// The rows of many-row calls, after tables_kernel<false> and from what it wrote: pages from the old
+// last one on lie 16 positions apart, so a row's page is counted back from the request's last.
+// A CTA takes 1024 rows and finds the requests of its first and last one by two parallel counts
+// over row_start; its threads bisect between the two.
+constexpr int kRowThreadsT = 256, kRowsPerCta = 1024;
+__device__ __forceinline__ int count_le(const int* base, int lo, int n, int stride, int x) {
+  // over i = lo, lo + stride, ... < n (at most kRowThreadsT of them): how many base[i] <= x
+  const int i = lo + threadIdx.x * stride;
+  return __syncthreads_count(i < n && base[i] <= x);
+}
+__global__ void __launch_bounds__(kRowThreadsT) table_rows_kernel(const __grid_constant__ TablesArgs a) {
+  pdl_enter();
+  const int t0 = blockIdx.x * kRowsPerCta, n_rows = a.counts[0];
+  int lo = 0, hi = 0;
+  if (t0 < n_rows) {
+    const int jump = pdiv(a.n, kRowThreadsT);    // 48 at most
+    const int t1 = pmin(t0 + kRowsPerCta, n_rows) - 1;
+    // base[0] = 0 <= x: the counts are at least 1
+    lo = (count_le(a.row_start, 0, a.n, jump, t0) - 1) * jump;
+    lo += count_le(a.row_start, lo, pmin(lo + jump, a.n), 1, t0) - 1;
+    hi = (count_le(a.row_start, 0, a.n, jump, t1) - 1) * jump;
+    hi += count_le(a.row_start, hi, pmin(hi + jump, a.n), 1, t1) - 1;
+  }
+#pragma unroll
+  for (int j = 0; j < kRowsPerCta / kRowThreadsT; ++j) {
+    const int t = t0 + j * kRowThreadsT + threadIdx.x;
+    if (t < n_rows) {
+      const int r = lo + find(a.row_start + lo, hi - lo + 1, t);
+      const int kv = a.kv_out[r], np = a.np_out[r], pos = kv - (a.row_start[r + 1] - t);
+      const size_t row = (size_t)r * a.stride;
+      const int last = a.page_pos ? a.page_pos[row + np - 1] - a.first : (np - 1) * kPage;
+      const int back = pos < last ? pdiv(last - pos, kPage) : 0;
+      put_row(a, t, pos, a.block_table[row + np - 1 - back], pos - (last - back * kPage));
+    } else if (t < a.max_rows) {
+      a.row_pos[t] = 0;
+      a.row_slot[t] = -1;
+    }
   }
 }
 
@@ -186,14 +242,19 @@ pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int3
   if ((page_pos == nullptr) != (n_pages == nullptr))
     return fail(PIC_ERR_INVALID_ARG, "page_pos and n_pages come together");
   if (n_reqs > kMaxReqs) return fail(PIC_ERR_CAPACITY, "more than 12288 requests in one block table call");
+  if (table_stride >= kMaxStride) return fail(PIC_ERR_CAPACITY, "more than 2^26 - 1 pages in a request's table row");
   TablesArgs a{n_reqs, table_stride, n_free, max_rows, first, kv_len, new_len, block_table, page_pos, n_pages,
                free_blocks, free_used, kv_len_out, n_pages_out, row_start, row_pos, row_slot, counts, nullptr};
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
-  const int smem = n_reqs * 8;
+  const bool rows_here = max_rows <= kRowsInCluster;
+  const auto kernel = rows_here ? tables_kernel<true> : tables_kernel<false>;
+  const int smem = n_reqs * 16;
   if (smem > 40 * 1024)
-    PIC_CUDA(cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxReqs * 8));
-  tables_kernel<<<kCluster, kThreads, smem, (cudaStream_t)stream>>>(a);
+    PIC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxReqs * 16));
+  kernel<<<kCluster, kThreads, smem, (cudaStream_t)stream>>>(a);
+  if (!rows_here)
+    launch_dependent(table_rows_kernel, dim3(pdiv(max_rows, kRowsPerCta)), dim3(kRowThreadsT), 0, (cudaStream_t)stream, a);
   PIC_CUDA(cudaGetLastError());
   return PIC_OK;
 }

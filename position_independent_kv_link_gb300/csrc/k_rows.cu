@@ -175,27 +175,31 @@ __global__ void __launch_bounds__(kRowThreads) qk_norm_rope_kernel(
     T* __restrict__ vl, int pool_blocks, unsigned* flag) {
   constexpr int L = D / 4, kGroups = kRowThreads / L, kHeadsInFlight = 6;
   const int t = blockIdx.x, lane = threadIdx.x % L, grp = threadIdx.x / L;
+  const int n = H + 2 * G, step = kGroups * gridDim.y;
+  const float* row = qkv + (size_t)t * stride + 4 * lane;
+  float4 x[kHeadsInFlight];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int h = h0 + i * step;
+      x[i] = h < n ? __ldcs(reinterpret_cast<const float4*>(row + (size_t)h * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  int h0 = blockIdx.y * kGroups + grp;
+  load(h0);                            // under way while the slot, the position and its table row are read
   const int sl = slot[t], p = pos[t];
   if (sl < 0) return;
   if (p < 0 || p >= rope_positions || sl >= pool_blocks * kBlock) {
     if (threadIdx.x == 0) atomicOr(flag, sl >= pool_blocks * kBlock ? kBatchBadBlock : kBatchBadPosition);
     return;
   }
-  const int n = H + 2 * G, step = kGroups * gridDim.y;
-  const float* row = qkv + (size_t)t * stride + 4 * lane;
   const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
   const float4* cs = reinterpret_cast<const float4*>(rope_cs + (size_t)p * (D / 2) + 4 * (lane % (L / 2)));
   const float4 c0 = cs[0], c1 = cs[1];
   const float4 gq = q_gain ? reinterpret_cast<const float4*>(q_gain)[lane] : one;
   const float4 gk = k_gain ? reinterpret_cast<const float4*>(k_gain)[lane] : one;
   const size_t at = ((size_t)(sl / kBlock) * G * kBlock + sl % kBlock) * D + 4 * lane;   // + g * kBlock * D
-  for (int h0 = blockIdx.y * kGroups + grp; h0 - grp < n; h0 += step * kHeadsInFlight) {
-    float4 x[kHeadsInFlight];
-#pragma unroll
-    for (int i = 0; i < kHeadsInFlight; ++i) {
-      const int h = h0 + i * step;
-      x[i] = h < n ? __ldcs(reinterpret_cast<const float4*>(row + (size_t)h * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+  for (; h0 - grp < n; h0 += step * kHeadsInFlight, load(h0)) {
 #pragma unroll
     for (int i = 0; i < kHeadsInFlight; ++i) {
       const int h = h0 + i * step;
