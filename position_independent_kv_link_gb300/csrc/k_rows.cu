@@ -162,18 +162,22 @@ __global__ void qkv_epilogue_kernel(int H, int G, int D, const float* __restrict
 // Per-head norms with the rotation: x of head h of row t, r = 1 / sqrt(mean(x^2) + eps) over the
 // head's D dims (fp32),
 //   q_out[t][h] = RoPE(x r q_gain, pos[t]),   K slot: x r k_gain (unrotated),   V slot: x.
-// D / 4 lanes hold a head, 4 dims each; a dim's partner (+ D/2) is D/8 lanes away. Every byte is
-// read and written once: HBM-bound (a row moves (H + 2G) D x (4 + 2) bytes for bf16 pools). A CTA
-// takes one row, so that the row's table entries and the gains are loaded once per thread, and a
-// thread loads all its heads (kHeadsInFlight) before it uses the first; few rows are split over
-// gridDim.y CTAs by heads. Measured: see the launch.
+// D / 4 lanes hold a head, 4 dims each; a dim's partner (+ D/2) is D/8 lanes away. Sums and the
+// rotation in fp32, one rounding at each store. Every byte is read and written once: HBM-bound (a
+// row moves (H + 2G) D x (4 + 2) bytes for bf16 pools). A CTA takes one row, so that the row's table
+// entries and the gains are loaded once per thread, and a thread loads kHeadsInFlight heads before
+// it uses the first; few rows are split over gridDim.y CTAs by heads. Small CTAs keep loads coming
+// while others store: 8192 rows of 32 + 8 + 8 heads of 128 to bf16 pools take 63 us with 256 threads
+// and 6 heads in flight, 55 us (5.5 TB/s) with these, 68 us with 128 threads and 12; without the
+// stores of q 46 us. 64 such rows take 3.5 us (latency: three loads that depend on one another).
+constexpr int kNormThreads = 128, kHeadsInFlight = 4;
 template <typename T, typename A, int D>
-__global__ void __launch_bounds__(kRowThreads) qk_norm_rope_kernel(
+__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(
     int H, int G, const float* __restrict__ qkv, size_t stride, const float* __restrict__ q_gain,
     const float* __restrict__ k_gain, float eps, const int* __restrict__ pos, const int* __restrict__ slot,
     const float2* __restrict__ rope_cs, int rope_positions, A* __restrict__ q_out, T* __restrict__ kl,
     T* __restrict__ vl, int pool_blocks, unsigned* flag) {
-  constexpr int L = D / 4, kGroups = kRowThreads / L, kHeadsInFlight = 6;
+  constexpr int L = D / 4, kGroups = kNormThreads / L;
   const int t = blockIdx.x, lane = threadIdx.x % L, grp = threadIdx.x / L;
   const int n = H + 2 * G, step = kGroups * gridDim.y;
   const float* row = qkv + (size_t)t * stride + 4 * lane;
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kRowThreads) qk_norm_rope_kernel(
 #pragma unroll
     for (int i = 0; i < kHeadsInFlight; ++i) {
       const int h = h0 + i * step;
-      x[i] = h < n ? __ldcs(reinterpret_cast<const float4*>(row + (size_t)h * D)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      x[i] = h < n ? *reinterpret_cast<const float4*>(row + (size_t)h * D) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   int h0 = blockIdx.y * kGroups + grp;
@@ -377,13 +381,13 @@ void launch_qk_norm_rope(int dtype, int T, int H, int G, int D, const float* qkv
                          const float* k_gain, float eps, const int* pos, const int* slot, const float2* rope_cs,
                          int rope_positions, void* q_out, void* k_layer, void* v_layer, int pool_blocks,
                          unsigned* flag, cudaStream_t st) {
-  const int groups = kRowThreads / (D / 4), per = (H + 2 * G + groups - 1) / groups;   // heads of a thread, one CTA a row
+  const int groups = kNormThreads / (D / 4), per = (H + 2 * G + groups - 1) / groups;   // heads of a thread, one CTA a row
   const int split = std::max(1, std::min(per, 1024 / T));
   const dim3 grid(T, split);
   auto go = [&](auto* k, auto* pool, auto* act) {
     using P = decltype(pool);
     using Q = decltype(act);
-    k<<<grid, kRowThreads, 0, st>>>(H, G, qkv, stride, q_gain, k_gain, eps, pos, slot, rope_cs, rope_positions,
+    k<<<grid, kNormThreads, 0, st>>>(H, G, qkv, stride, q_gain, k_gain, eps, pos, slot, rope_cs, rope_positions,
                                     (Q)q_out, (P)k_layer, (P)v_layer, pool_blocks, flag);
   };
   __nv_bfloat16* b = nullptr;
