@@ -284,6 +284,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 struct TcArgs {
   CUtensorMap kmap, vmap, qmap, cmap;
@@ -831,18 +838,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   } else if constexpr (MT == 1) {
     // =============================== raw K to the K operand
     constexpr int NX = C::NX;
-    constexpr int CH = D / 16, PP = C::NR * 32 / (16 * CH), NP = KP / PP;   // threads of a row; pages at once, per thread
-    static_assert(KP % PP == 0, "");
-    const int rt = tid - 128, c = rt % CH, r = rt / CH % kPage, p0 = rt / (16 * CH);
-    // (cos, sin) of r theta for the thread's 8 frequencies
-    float4 off[4];
+    constexpr int CH = D / 16, NP = KT * CH / (C::NR * 32), RS = kPage / NP;   // threads of a row; rows of a thread, their distance
+    static_assert(RS == 8 || RS == 16, "rows of a thread lie whole swizzle atoms apart");
+    const int rt = tid - 128, c = rt % CH, r = rt / CH % RS, p = rt / (RS * CH);
+    // of r theta for the thread's 8 frequencies, pairs of frequencies: cos, sin
+    float2 oc[NP][4], os[NP][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) off[e] = reinterpret_cast<const float4*>(a.rope_cs + (size_t)r * (D / 2) + 8 * c)[e];
-    // the thread's two 16-byte chunks (dims 8c.. and their partners): of its first page of a raw K or V
-    // stage, and of a K stage
-    const int x1 = p0 * C::PAGE_BYTES + sw128(r, c), x2 = D == 128 ? x1 + 2048 : p0 * C::PAGE_BYTES + sw128(r, c + CH);
-    const int k1 = p0 * 2048 + sw128(r, c), k2 = D == 128 ? KT * 128 + k1 : p0 * 2048 + sw128(r, c + CH);
-    const int shift = p0 % 2 * 16 + r;
+    for (int u = 0; u < NP; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 f = reinterpret_cast<const float4*>(a.rope_cs + (size_t)(r + RS * u) * (D / 2) + 8 * c)[e];
+        oc[u][e] = make_float2(f.x, f.z);
+        os[u][e] = make_float2(f.y, f.w);
+      }
+    // the thread's two 16-byte chunks (dims 8c.. and their partners) of its first row: in a raw K or V
+    // stage, and in a K stage
+    const int x1 = p * C::PAGE_BYTES + sw128(r, c), x2 = D == 128 ? x1 + 2048 : p * C::PAGE_BYTES + sw128(r, c + CH);
+    const int k1 = p * 2048 + sw128(r, c), k2 = D == 128 ? KT * 128 + k1 : p * 2048 + sw128(r, c + CH);
+    const int shift = p % 2 * 16 + r;
     bool ok = true;
     uint32_t sx = 0, px = 0, sk = 0, pk = 1;   // stages and their parities
 #pragma unroll 1
@@ -853,33 +866,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       if (tile.z) break;
       const bool holes = (tile.x & tile.y) != -1;
       const uint8_t* xs = sm + C::OFF_X + sx * C::K_BYTES;
-      const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (sx * KP + p0) * C::CS_ROW) + c;
+      const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (sx * KP + p) * C::CS_ROW) + c;
       uint4 w1[NP], w2[NP];
-      float4 f[NP][4];   // (cos, sin) of P theta
+      float4 f[4];       // (cos, sin) of P theta
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        w1[u] = *reinterpret_cast<const uint4*>(xs + x1 + u * PP * C::PAGE_BYTES);
-        w2[u] = *reinterpret_cast<const uint4*>(xs + x2 + u * PP * C::PAGE_BYTES);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[u][e] = cs[u * PP * (D / 4) + e * CH];
+        w1[u] = *reinterpret_cast<const uint4*>(xs + x1 + u * RS * 128);
+        w2[u] = *reinterpret_cast<const uint4*>(xs + x2 + u * RS * 128);
       }
-      uint4 y1[NP], y2[NP];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = cs[e * CH];
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        const uint32_t a1[4] = {w1[u].x, w1[u].y, w1[u].z, w1[u].w}, a2[4] = {w2[u].x, w2[u].y, w2[u].z, w2[u].w};
-        uint32_t o1[4], o2[4];
+        uint32_t* a1 = reinterpret_cast<uint32_t*>(&w1[u]);
+        uint32_t* a2 = reinterpret_cast<uint32_t*>(&w2[u]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float4 g = f[u][e];
-          const float c0 = g.x * off[e].x - g.y * off[e].y, s0 = g.y * off[e].x + g.x * off[e].y;
-          const float c1 = g.z * off[e].z - g.w * off[e].w, s1 = g.w * off[e].z + g.z * off[e].w;
-          const float q0 = __uint_as_float(a1[e] << 16), q1 = __uint_as_float(a1[e] & 0xffff0000u);
-          const float z0 = __uint_as_float(a2[e] << 16), z1 = __uint_as_float(a2[e] & 0xffff0000u);
-          o1[e] = pack_f16x2(q0 * c0 - z0 * s0, q1 * c1 - z1 * s1);
-          o2[e] = pack_f16x2(z0 * c0 + q0 * s0, z1 * c1 + q1 * s1);
+          const float2 k = make_float2(__uint_as_float(a1[e] << 16), __uint_as_float(a1[e] & 0xffff0000u));
+          const float2 z = make_float2(__uint_as_float(a2[e] << 16), __uint_as_float(a2[e] & 0xffff0000u));
+          const float2 y = fma2(make_float2(-z.x, -z.y), os[u][e], mul2(k, oc[u][e])), x = fma2(k, os[u][e], mul2(z, oc[u][e]));
+          a1[e] = pack_f16x2(y.x * f[e].x - x.x * f[e].y, y.y * f[e].z - x.y * f[e].w);
+          a2[e] = pack_f16x2(x.x * f[e].x + y.x * f[e].y, x.y * f[e].z + y.y * f[e].w);
         }
-        y1[u] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-        y2[u] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
       }
       if (holes) {
         // rows without a key: K is zero, and V must be finite (P is 0 there)
@@ -888,11 +896,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         uint8_t* vs = sm + C::OFF_V + gt % NV * C::K_BYTES;
 #pragma unroll
         for (int u = 0; u < NP; ++u) {
-          const int p = p0 + u * PP;
-          if ((unsigned)(p < 2 ? tile.x : tile.y) >> shift & 1u) continue;
-          y1[u] = y2[u] = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vs + x1 + u * PP * C::PAGE_BYTES) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vs + x2 + u * PP * C::PAGE_BYTES) = make_uint4(0, 0, 0, 0);
+          if ((unsigned)(p < 2 ? tile.x : tile.y) >> (shift + RS * u) & 1u) continue;
+          w1[u] = w2[u] = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vs + x1 + u * RS * 128) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vs + x2 + u * RS * 128) = make_uint4(0, 0, 0, 0);
         }
       }
       ok = __all_sync(0xffffffffu, wait(C::B_KEMPTY + sk, pk));   // the first round's waits return at once
@@ -900,8 +907,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       uint8_t* ks = sm + C::OFF_K + sk * C::K_BYTES;
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
-        *reinterpret_cast<uint4*>(ks + k1 + u * PP * 2048) = y1[u];
-        *reinterpret_cast<uint4*>(ks + k2 + u * PP * 2048) = y2[u];
+        *reinterpret_cast<uint4*>(ks + k1 + u * RS * 128) = w1[u];
+        *reinterpret_cast<uint4*>(ks + k2 + u * RS * 128) = w2[u];
       }
       fence_async_smem();   // the MMAs read these rows through the async proxy, TMA rewrites the raw ones
       __syncwarp();
