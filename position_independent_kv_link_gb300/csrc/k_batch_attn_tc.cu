@@ -217,6 +217,12 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "r"(acc));
 }
+// one lane of a whole warp, always the same
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
   __shared__ PlanShared s_plan;
   __shared__ uint32_t s_tmem, s_abort;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t abort = smem_u32(&s_abort);
   auto give_up = [&] { asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort), "r"(1u) : "memory"); };
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity, abort, a.flag); };
@@ -414,7 +420,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   fence_before();
   const BatchShare share_ = plan_batch<C::THREADS>(a, s_plan);   // ends with a __syncthreads
   fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
   if (warp < 4 * MT) {
     // =============================== softmax: MMA tile t, row m of the item
@@ -569,37 +575,41 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     if (!ok) give_up();
   } else if ((warp >= C::W_S && warp < C::W_S + MT) || (warp >= C::W_PV && warp < C::W_PV + MT)) {
     // =============================== products: S or PV of MMA tile t
-    if (lane == 0) {
-      const bool s_warp = warp >= C::W_S && warp < C::W_S + MT;
-      const int t = s_warp ? warp - C::W_S : warp - C::W_PV;
-      constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
-      const int full = s_warp ? C::B_READY : MT == 2 ? C::B_VREADY : C::B_VFULL, empty = s_warp ? C::B_KEMPTY : C::B_VEMPTY;
-      uint32_t gt = 0, ct = 0, qi = 0;   // tiles of the CTA, of the MMA tile; items of it
-      bool ok = true;
+    // The whole warp runs the loop, an elected lane (always the same) issues: operands then stay in
+    // uniform registers.
+    const bool s_warp = warp >= C::W_S && warp < C::W_S + MT;
+    const int t = s_warp ? warp - C::W_S : warp - C::W_PV;
+    const bool one = elect();
+    constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
+    const int full = s_warp ? C::B_READY : MT == 2 ? C::B_VREADY : C::B_VFULL, empty = s_warp ? C::B_KEMPTY : C::B_VEMPTY;
+    uint32_t gt = 0, ct = 0, qi = 0;   // tiles of the CTA, of the MMA tile; items of it
+    bool ok = true;
+    auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
 #pragma unroll 1
-      for (uint32_t win = 0; ok; ++win) {
-        ok = wait_meta(win);
+    for (uint32_t win = 0; ok; ++win) {
+      ok = wait_all(C::B_META + win % NWIN, (win / NWIN) & 1);
+      if (!ok) break;
+      const int flags = __shfl_sync(0xffffffffu, sRec[win % NWIN].flags, 0), n = __shfl_sync(0xffffffffu, sRec[win % NWIN].tiles, 0);
+      if (flags & kEnd) break;
+      done_with(win);
+      const bool mine = t == 0 || (flags & kTwo);
+      const uint32_t qb = qi % NQ, qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
+      if (s_warp && mine && (flags & kFirst)) ok = wait_all(C::B_QFULL + t * NQ + qb, (qi / NQ) & 1);
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j, ++gt) {
+        const int st = s_warp ? gt % NK : gt % NV;
+        ok = wait_all(full + st, (s_warp ? gt / NK : gt / NV) & 1);
+        if (!mine) {                  // its share of the stage is released
+          if (ok && one) mbar_arrive(bar(empty + st));
+          continue;
+        }
+        const int b = ct % NBP;
+        // S: the softmax has read the one before (the first wait returns at once); PV: its P is written
+        ok = ok && (s_warp ? wait_all(C::B_SFREE + t, (ct + 1) & 1) : wait_all(C::B_PREADY + t * NBP + b, (ct / NBP) & 1));
         if (!ok) break;
-        const int flags = sRec[win % NWIN].flags, n = sRec[win % NWIN].tiles;
-        if (flags & kEnd) break;
-        mbar_arrive(bar(C::B_RFREE + win % NWIN));
-        const bool mine = t == 0 || (flags & kTwo);
-        const uint32_t qb = qi % NQ, qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
-        if (s_warp && mine && (flags & kFirst)) ok = wait(C::B_QFULL + t * NQ + qb, (qi / NQ) & 1);
-#pragma unroll 1
-        for (int j = 0; j < n && ok; ++j, ++gt) {
-          const int st = s_warp ? gt % NK : gt % NV;
-          ok = wait(full + st, (s_warp ? gt / NK : gt / NV) & 1);
-          if (!mine) {                  // its share of the stage is released
-            if (ok) mbar_arrive(bar(empty + st));
-            continue;
-          }
-          const int b = ct % NBP;
-          // S: the softmax has read the one before (the first wait returns at once); PV: its P is written
-          ok = ok && (s_warp ? wait(C::B_SFREE + t, (ct + 1) & 1) : wait(C::B_PREADY + t * NBP + b, (ct / NBP) & 1));
-          if (!ok) break;
-          fence_after();
-          const uint32_t buf = tmem + C::TM_S + 128 * t + (s_warp ? 0 : KT + KT / 2 * b);
+        fence_after();
+        const uint32_t buf = tmem + C::TM_S + 128 * t + (s_warp ? 0 : KT + KT / 2 * b);
+        if (one) {
           if (s_warp) {
             const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
             umma_ss<false>(buf, qd, kd, id_s);
@@ -615,14 +625,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           }
           umma_commit(bar(s_warp ? C::B_SFULL + t : C::B_PVDONE + t * NBP + b));
           umma_commit(bar(empty + st));
-          ++ct;
         }
-        if (s_warp && ok && mine && (flags & kLast)) {
-          umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
-          ++qi;
-        }
+        __syncwarp();
+        ++ct;
       }
-      if (!ok) give_up();
+      if (s_warp && ok && mine && (flags & kLast)) {
+        if (one) umma_commit(bar(C::B_QEMPTY + t * NQ + qb));
+        __syncwarp();
+        ++qi;
+      }
+    }
+    if (!ok) give_up();
+    if (one) {
       const int d = C::B_DONE + (s_warp ? 0 : MT) + t;
       umma_commit(bar(d));              // fires once every MMA of this thread has retired
       mbar_wait_on(bar(d), 0, 0, a.flag);
