@@ -69,9 +69,10 @@ struct Cfg {
   static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
   // Roles of the warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
   // instruction cache is shared by its warps. Rotation: warps 4..11.
-  static constexpr int THREADS = MT == 2 ? 480 : 512;
+  static constexpr int THREADS = 512;
   static constexpr int W_S = MT == 2 ? 8 : 15, W_PV = MT == 2 ? 10 : 13;   // the first of MT
-  static constexpr int W_META = MT == 2 ? 12 : 14, W_LOAD = MT == 2 ? 13 : 12, W_MEND = MT == 2 ? 14 : -1;
+  static constexpr int W_META = MT == 2 ? 12 : 14, W_K = MT == 2 ? 13 : 12, W_MEND = MT == 2 ? 14 : -1;
+  static constexpr int W_LOAD = MT == 2 ? 15 : W_META;   // q and V
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       for (int k = 0; k < n; ++k) mbar_init(bar(i + k), count);
     };
     init(C::B_META, NWIN, 1);
-    init(C::B_RFREE, NWIN, 4 * MT + 2 * MT + (MT == 2 ? 2 : 1));
+    init(C::B_RFREE, NWIN, 4 * MT + 2 * MT + (MT == 2 ? 3 : 1));
     init(C::B_XFULL, C::NX, 1);
     init(C::B_XEMPTY, C::NX, C::NR);
     init(C::B_READY, NK, MT == 2 ? 1 : C::NR);
@@ -641,127 +642,81 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       umma_commit(bar(d));              // fires once every MMA of this thread has retired
       mbar_wait_on(bar(d), 0, 0, a.flag);
     }
-  } else if (warp == C::W_META) {
-    // =============================== window records, K
-    if (MT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotated K
+  } else if (warp == C::W_META || warp == C::W_LOAD) {
+    // =============================== window records; q of the items into the A operands, V
     // Lane i holds page i of a window. `next`: the tables' entries of the window after the last one
     // written (the same item's or the next one's), on their way.
     Walk w;
-    bool more = w.begin(a, share_, s_plan.block), ok = true;
+    const bool meta = warp == C::W_META, load = warp == C::W_LOAD;
+    bool more = meta && w.begin(a, share_, s_plan.block), ok = true;
     unsigned bad = 0;
     int j = more ? w.j0 : 0;             // next tile to be described
-    uint32_t n_win = 0, gt = 0;          // windows written, tiles whose K is asked for
-    constexpr int NS = MT == 2 ? NK : C::NX;   // stages K goes to
     PageRaw next{0, 0, 0};
     if (more) next = fetch_page(v, w.b, j * KP + lane);
-    bool ended = false;
+    uint32_t n_win = 0, qi[MT] = {}, gt = 0;   // windows written; items and tiles asked for
+    const int tpt = v.half_rows;
+    bool ended = !meta;
 #pragma unroll 1
-    for (uint32_t win = 0; ok;) {        // K of window win, when the two after it are described
-      if (!ended && n_win < win + 3) {
+    for (uint32_t win = 0; ok; ++win) {  // V of window win, by the same warp when the two after it are described
+#pragma unroll 1
+      for (; !ended && n_win < win + (win == 0 ? 2 : 3); ++n_win) {
         const int ws = n_win % NWIN;
-        if (lane == 0) ok = n_win < NWIN || wait(C::B_RFREE + ws, (n_win / NWIN - 1) & 1);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = n_win < NWIN || __all_sync(0xffffffffu, wait(C::B_RFREE + ws, (n_win / NWIN - 1) & 1));
         if (!ok) break;
         if (!more) {
-          if (lane == 0) sRec[ws].flags = kEnd;
-          ended = true;
-        } else {
-          const int i = j * KP + lane, n = min(w.j1 - j, WT);
-          PageMeta pm{0, 0, 0};
-          if (lane < n * KP && i < w.b.nv) pm = page_meta(v, w.b, next, bad);
-          int top = pm.rows == 0xffffu ? pm.pos + 15 : INT_MAX;
-          const int sk = min(max(v.sinks - pm.pos, 0), 16);
-          const unsigned behind = pm.rows >> sk << sk;
-          int low = behind ? pm.pos + __ffs(behind) - 1 : INT_MAX;
-#pragma unroll
-          for (int d = 1; d < KP; d <<= 1) {
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
-          }
-          int krot = 0;                    // the page's place in the rotated K
-          if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : w.b.req * v.stride);
-          sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, krot);
-          if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
           if (lane == 0) {
-            WinRec& r = sRec[ws];
-            r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows > v.half_rows ? kTwo : 0) |
-                      (w.j0 == 0 && w.j1 == w.nt ? kWhole : 0);
-            r.tiles = n, r.req = w.b.req, r.row0 = w.b.row0, r.nrows = w.b.nrows, r.pos0 = w.b.pos0, r.g = w.g;
-            r.slot = part_slot(blockIdx.x, w.start, w.x0);
+            sRec[ws].flags = kEnd;
+            mbar_arrive(bar(C::B_META + ws));
           }
-          j += n;
-          if (j == w.j1) {
-            more = w.next(a);
-            j = w.j0;
-          }
-          if (more) next = fetch_page(v, w.b, j * KP + lane);
+          ended = true;
+          continue;
         }
+        const int i = j * KP + lane, n = min(w.j1 - j, WT);
+        PageMeta pm{0, 0, 0};
+        if (lane < n * KP && i < w.b.nv) pm = page_meta(v, w.b, next, bad);
+        int top = pm.rows == 0xffffu ? pm.pos + 15 : INT_MAX;
+        const int sk = min(max(v.sinks - pm.pos, 0), 16);
+        const unsigned behind = pm.rows >> sk << sk;
+        int low = behind ? pm.pos + __ffs(behind) - 1 : INT_MAX;
+#pragma unroll
+        for (int d = 1; d < KP; d <<= 1) {
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+          low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
+        }
+        int krot = 0;                    // the page's place in the rotated K
+        if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : w.b.req * v.stride);
+        sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, krot);
+        if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
+        if (lane == 0) {
+          WinRec& r = sRec[ws];
+          r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows > v.half_rows ? kTwo : 0) |
+                    (w.j0 == 0 && w.j1 == w.nt ? kWhole : 0);
+          r.tiles = n, r.req = w.b.req, r.row0 = w.b.row0, r.nrows = w.b.nrows, r.pos0 = w.b.pos0, r.g = w.g;
+          r.slot = part_slot(blockIdx.x, w.start, w.x0);
+        }
+        j += n;
+        if (j == w.j1) {
+          more = w.next(a);
+          j = w.j0;
+        }
+        if (more) next = fetch_page(v, w.b, j * KP + lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_META + ws));
-        ++n_win;
+      }
+      if (!ok) break;
+      if (!load) {
+        if (ended) break;
         continue;
       }
-      const bool end = sRec[win % NWIN].flags & kEnd;
-      if (MT == 2 && end) break;
-      const int n = end ? 1 : sRec[win % NWIN].tiles, g = sRec[win % NWIN].g;   // MT 1: the rotation sees the end as a tile
-      const int4 pg = sPage[win % NWIN * WIN + lane];
-      ++win;
-#pragma unroll 1
-      for (int i = 0; i < n; ++i, ++gt) {
-        const int st = gt % NS;
-        if (lane == 0) ok = gt < NS || wait((MT == 2 ? C::B_KEMPTY : C::B_XEMPTY) + st, (gt / NS - 1) & 1);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if constexpr (MT == 2) {
-          const int slot = __shfl_sync(0xffffffffu, pg.w, i * KP);
-          if (lane == 0) mbar_expect_tx(bar(C::B_READY + st), C::K_BYTES);
-          __syncwarp();
-          if (lane < D / 64)
-            tma_5d(base + C::OFF_K + st * C::K_BYTES + lane * (KT * 128), &ta.kmap, lane, g, slot, bar(C::B_READY + st));
-        } else {
-          const bool live = !end && lane / KP == i && pg.z != 0;
-          const unsigned who = __ballot_sync(0xffffffffu, live);
-          // the pages' rows, from the lanes that hold them
-          const unsigned r0 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP), r1 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 1);
-          const unsigned r2 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 2), r3 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 3);
-          if (lane == 0) {
-            sTile[st] = make_int4((int)(r0 | r1 << 16), (int)(r2 | r3 << 16), end, 0);
-            mbar_expect_tx(bar(C::B_XFULL + st), (uint32_t)__popc(who) * (C::PAGE_BYTES + C::CS_ROW));
-          }
-          __syncwarp();
-          if (live) {
-            tma_4d(base + C::OFF_X + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.kmap, 0, 0, pg.x, bar(C::B_XFULL + st));
-            tma_4d(base + C::OFF_CS + (st * KP + lane % KP) * C::CS_ROW, &ta.cmap, 0, 0, pg.y, bar(C::B_XFULL + st));
-          }
-        }
-      }
-      if (end) break;
-    }
-    if (!ok) give_up();
-    batch_flag(a.flag, bad);
-    // every copy has landed before the shared memory is given up (at once on the normal path)
-    if (lane == 0) {
-#pragma unroll 1
-      for (uint32_t s = 0; s < NS; ++s) {
-        const uint32_t n = (gt + NS - 1 - s) / NS;
-        if (n) mbar_wait_on(bar((MT == 2 ? C::B_READY : C::B_XFULL) + s), (n - 1) & 1, 0, a.flag);
-      }
-    }
-  } else if (warp == C::W_LOAD) {
-    // =============================== q of the items into the A operands, V
-    uint32_t qi[MT] = {}, gt = 0;   // items, tiles asked for
-    const int tpt = v.half_rows;
-    bool ok = true;
-#pragma unroll 1
-    for (uint32_t win = 0; ok; ++win) {
-      ok = __all_sync(0xffffffffu, wait_meta(win));
+      if (!meta) ok = __all_sync(0xffffffffu, wait_meta(win));
       if (!ok) break;
+      __syncwarp();
       const WinRec& rec = sRec[win % NWIN];
       const int flags = rec.flags;
       if (flags & kEnd) break;
       const int row0 = rec.row0, g = rec.g, rows = rec.nrows, n = rec.tiles;
       const int4 pg = sPage[win % NWIN * WIN + lane];
-      done_with(win);
+      if (!meta) done_with(win);
       if (flags & kFirst) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -800,6 +755,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       }
     }
     if (!ok) give_up();
+    batch_flag(a.flag, bad);
     // at the end every box asked for has landed
     if (lane == 0) {
 #pragma unroll 1
@@ -814,6 +770,60 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           const uint32_t n = (qi[t] + NQ - 1 - b) / NQ;
           if (n) mbar_wait_on(bar(C::B_QFULL + t * NQ + b), (n - 1) & 1, 0, a.flag);
         }
+    }
+  } else if (warp == C::W_K) {
+    // =============================== K, raw with table rows (MT 1) or rotated ahead (MT 2)
+    if (MT == 2) asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotated K
+    uint32_t gt = 0;                     // tiles asked for
+    constexpr int NS = MT == 2 ? NK : C::NX;   // stages K goes to
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t win = 0; ok; ++win) {
+      ok = __all_sync(0xffffffffu, wait_meta(win));
+      if (!ok) break;
+      const bool end = sRec[win % NWIN].flags & kEnd;
+      if (MT == 2 && end) break;
+      const int n = end ? 1 : sRec[win % NWIN].tiles, g = sRec[win % NWIN].g;   // MT 1: the rotation sees the end as a tile
+      const int4 pg = sPage[win % NWIN * WIN + lane];
+      done_with(win);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++gt) {
+        const int st = gt % NS;
+        ok = gt < NS || __all_sync(0xffffffffu, wait((MT == 2 ? C::B_KEMPTY : C::B_XEMPTY) + st, (gt / NS - 1) & 1));
+        if (!ok) break;
+        if constexpr (MT == 2) {
+          const int slot = __shfl_sync(0xffffffffu, pg.w, i * KP);
+          if (lane == 0) mbar_expect_tx(bar(C::B_READY + st), C::K_BYTES);
+          __syncwarp();
+          if (lane < D / 64)
+            tma_5d(base + C::OFF_K + st * C::K_BYTES + lane * (KT * 128), &ta.kmap, lane, g, slot, bar(C::B_READY + st));
+        } else {
+          const bool live = !end && lane / KP == i && pg.z != 0;
+          const unsigned who = __ballot_sync(0xffffffffu, live);
+          // the pages' rows, from the lanes that hold them
+          const unsigned r0 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP), r1 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 1);
+          const unsigned r2 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 2), r3 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 3);
+          if (lane == 0) {
+            sTile[st] = make_int4((int)(r0 | r1 << 16), (int)(r2 | r3 << 16), end, 0);
+            mbar_expect_tx(bar(C::B_XFULL + st), (uint32_t)__popc(who) * (C::PAGE_BYTES + C::CS_ROW));
+          }
+          __syncwarp();
+          if (live) {
+            tma_4d(base + C::OFF_X + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.kmap, 0, 0, pg.x, bar(C::B_XFULL + st));
+            tma_4d(base + C::OFF_CS + (st * KP + lane % KP) * C::CS_ROW, &ta.cmap, 0, 0, pg.y, bar(C::B_XFULL + st));
+          }
+        }
+      }
+      if (end) break;
+    }
+    if (!ok) give_up();
+    // every copy has landed before the shared memory is given up (at once on the normal path)
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t s = 0; s < NS; ++s) {
+        const uint32_t n = (gt + NS - 1 - s) / NS;
+        if (n) mbar_wait_on(bar((MT == 2 ? C::B_READY : C::B_XFULL) + s), (n - 1) & 1, 0, a.flag);
+      }
     }
   } else if (warp == C::W_MEND) {
     // =============================== rows of V without a key to zero
