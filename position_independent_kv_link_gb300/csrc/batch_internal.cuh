@@ -248,7 +248,7 @@ void launch_batch_simt(const BatchArgs& a, cudaStream_t st);
 int batch_simt_grid(int D);
 void batch_simt_view(BatchView& v);
 // wide: two MMA tiles and K rotated ahead
-void batch_tc_view(BatchView& v, bool wide);
+void batch_tc_view(BatchView& v, bool wide, bool narrow);
 // K of the plan's pages, rotated, into a.krot.
 pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st);
 pic_status launch_batch_tc(const BatchArgs& a, bool wide, cudaStream_t st);

@@ -378,7 +378,12 @@ void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
     c.wide[0] = own;
     a.krot_slots = own ? n_reqs * table_stride : 0;
   }
-  for (int i = 0; i < c.n; ++i) batch_tc_view(c.a[i].v, c.wide[i]);
+  for (int i = 0; i < c.n; ++i) {
+    BatchView& v = c.a[i].v;
+    const int most = kRows / v.rep;   // tokens of a narrow item
+    const bool narrow = !c.wide[i] && (v.only == 1 || T <= (long long)n_reqs * most) && (v.only == 2 || prefix_len == 0 || T <= most);
+    batch_tc_view(v, c.wide[i], narrow);
+  }
 }
 
 // Scratch layout of a call (bytes); `base` null: the size alone.

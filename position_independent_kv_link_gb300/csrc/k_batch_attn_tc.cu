@@ -54,13 +54,14 @@ constexpr float kRescale = 8.f;           // rescale O when the row maximum grow
 constexpr unsigned long long kWaitLimit = 4000000000ull;   // cycles, about 2 s
 
 constexpr int KT = 64, KP = KT / kPage;   // keys, pages of a tile
-constexpr int NBP = 2;                    // P buffers per MMA tile (its S has one)
+constexpr int NBP = 2;                    // P buffers per MMA tile
 constexpr int WIN = 32, WT = WIN / KP;    // pages, tiles of a window
 constexpr int NWIN = 6;                   // window records
 
-template <int D_, int MT_>
+template <int D_, int MT_, bool NARROW_ = false>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
+  static constexpr bool NARROW = NARROW_;
   static constexpr int NQ = MT == 2 ? 1 : 2;          // Q buffers per MMA tile
   static constexpr int NX = MT == 2 ? 0 : D == 128 ? 3 : 6;   // raw K stages (with table rows)
   static constexpr int NK = MT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 3);   // K operand stages
@@ -82,19 +83,20 @@ struct Cfg {
   static constexpr int OFF_REC = OFF_CS + NX * KP * CS_ROW;   // WinRec [NWIN]
   static constexpr int OFF_PAGE = OFF_REC + NWIN * 48;        // int4 [NWIN][WIN] page of the pool, position, rows, page of the rotated K
   static constexpr int OFF_LIM = OFF_PAGE + NWIN * WIN * 16;  // int2 [NWIN][WT] last key, first one behind the sinks
-  static constexpr int OFF_TILE = OFF_LIM + NWIN * WT * 8;    // int4 [NX] rows of the tile's pages, 16 bits each; the end
-  static constexpr int OFF_BAR = OFF_TILE + NX * 16;
+  static constexpr int OFF_END = OFF_LIM + NWIN * WT * 8;     // int [NX] no tile any more
+  static constexpr int OFF_JOIN = OFF_END + (NX * 4 + 15) / 16 * 16;         // float2 [4][16], float [4][3][16][8] (narrow): the rows' parts
+  static constexpr int OFF_BAR = OFF_JOIN + (NARROW ? 512 + 12 * 16 * 8 * 4 : 0);
   // barriers
   static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_XFULL = B_RFREE + NWIN, B_XEMPTY = B_XFULL + NX,
                        B_READY = B_XEMPTY + NX, B_KEMPTY = B_READY + NK, B_VFULL = B_KEMPTY + NK,
                        B_VEMPTY = B_VFULL + NV, B_VREADY = B_VEMPTY + NV, B_SFULL = B_VREADY + (MT == 2 ? NV : 0),
                        B_SFREE = B_SFULL + MT, B_PREADY = B_SFREE + MT, B_PVDONE = B_PREADY + MT * NBP,
                        B_QFULL = B_PVDONE + MT * NBP, B_QEMPTY = B_QFULL + MT * NQ,
-                       B_DONE = B_QEMPTY + MT * NQ, N_BARS = B_DONE + 2 * MT;
+                       B_DONE = B_QEMPTY + MT * NQ, B_JOIN = B_DONE + 2 * MT, N_BARS = B_JOIN + 1;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
-  // TMEM columns: O_t at D t, S_t at TM_S + 128 t, P buffer b of tile t 64 + 32 b behind it
-  static constexpr uint32_t TM_S = MT * D;
+  // TMEM columns: O_t at D t, S_t at TM_S + 128 t, P buffer b of tile t at TM_P + 128 t + 32 b
+  static constexpr uint32_t TM_S = MT * D, TM_P = TM_S + KT;
   static constexpr uint32_t TMEM_COLS = MT == 2 ? 512 : 256;
 };
 
@@ -237,6 +239,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -244,6 +254,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -350,14 +365,11 @@ struct Walk {
   }
 };
 
-// Bit i: the row at qp (own keys at or below lo as sinks only) sees key i of two pages (chunk of 32 keys).
-__device__ __forceinline__ unsigned seen_bits(int4 p0, int4 p1, int qp, int lo, int sinks) {
-  auto page = [&](int pos, unsigned rows) {
-    const int up = min(max(qp - pos + 1, 0), 16), from = min(max(lo - pos + 1, 0), 16), sk = min(max(sinks - pos, 0), 16);
-    const unsigned upto = (1u << up) - 1u, old = (1u << from) - 1u, first = (1u << sk) - 1u;
-    return rows & upto & (~old | first);
-  };
-  return page(p0.y, (unsigned)p0.z) | page(p1.y, (unsigned)p1.z) << 16;
+// Bit i: the row at qp (own keys at or below lo as sinks only) sees key i of the page.
+__device__ __forceinline__ unsigned seen_bits(int4 p, int qp, int lo, int sinks) {
+  const int pos = p.y, up = min(max(qp - pos + 1, 0), 16), from = min(max(lo - pos + 1, 0), 16), sk = min(max(sinks - pos, 0), 16);
+  const unsigned upto = (1u << up) - 1u, old = (1u << from) - 1u, first = (1u << sk) - 1u;
+  return (unsigned)p.z & upto & (~old | first);
 }
 
 // Page i of a block's list as the tables have it (zeros past its end).
@@ -367,6 +379,7 @@ __device__ __noinline__ PageRaw fetch_page(const BatchView& v, const BatchBlock&
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_constant__ TcArgs ta) {
+  constexpr bool narrow = C::NARROW;
   constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NK = C::NK, NV = C::NV;
   const BatchArgs& a = ta.b;
   const BatchView& v = a.v;
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   WinRec* sRec = reinterpret_cast<WinRec*>(sm + C::OFF_REC);
   int4* sPage = reinterpret_cast<int4*>(sm + C::OFF_PAGE);
   int2* sLim = reinterpret_cast<int2*>(sm + C::OFF_LIM);
-  int4* sTile = reinterpret_cast<int4*>(sm + C::OFF_TILE);
+  int* sEnd = reinterpret_cast<int*>(sm + C::OFF_END);
   const uint32_t base = smem_u32(sm);
   auto bar = [&](int i) { return base + C::OFF_BAR + 8 * i; };
   __shared__ PlanShared s_plan;
@@ -388,6 +401,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
   auto done_with = [&](uint32_t w) {   // this warp (all its lanes) reads window w's record no more
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_RFREE + w % NWIN));
+  };
+
+  // A warp zeroes the rows of V tile i of a window that hold no key any row of the block sees (lane: rows of its page)
+  auto mend = [&](int st, int i, unsigned rows) {
+#pragma unroll 1
+    for (unsigned todo = __ballot_sync(0xffffffffu, lane / KP == i && rows != 0xffffu); todo; todo &= todo - 1) {   // pages, by lane
+      const int l = __ffs(todo) - 1;
+      const unsigned have = __shfl_sync(0xffffffffu, rows, l);
+      uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + l % KP * C::PAGE_BYTES;
+#pragma unroll 1
+      for (int u = lane; u < C::PAGE_BYTES / 16; u += 32) {   // [half][row][8 chunks]
+        const int r = u / 8 % kPage;
+        if (!(have >> r & 1u)) *reinterpret_cast<uint4*>(vs + u * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+    }
+    __syncwarp();
   };
 
   if (tid == 0) {
@@ -410,6 +440,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     init(C::B_PREADY, MT * NBP, 4);
     init(C::B_PVDONE, MT * NBP, 1);
     init(C::B_QFULL, 2 * MT * NQ + 2 * MT, 1);   // QFULL, QEMPTY, DONE
+    init(C::B_JOIN, 1, 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == C::W_S) {
@@ -425,26 +456,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 
   if (warp < 4 * MT) {
     // =============================== softmax: MMA tile t, row m of the item
-    const int t = warp >> 2, i0 = 32 * (warp & 3) + lane, tok0 = i0 * v.rep_inv >> 16;
+    const int t = warp >> 2, wq = warp & 3;
+    const int i0 = narrow ? lane : 32 * wq + lane, tok0 = i0 * v.rep_inv >> 16;
     const int tok = tok0 < v.half_rows ? t * v.half_rows + tok0 : INT_MAX, hh = i0 - tok0 * v.rep;   // INT_MAX: unused row
-    const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t t_o = trow + D * t, t_sb = trow + C::TM_S + 128 * t;
+    uint32_t joins = 0;
+    auto join = [&]() {        // the four warps meet
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_JOIN));
+      return __all_sync(0xffffffffu, wait(C::B_JOIN, joins++ & 1)) != 0;
+    };
+    const uint32_t trow = tmem + ((uint32_t)(32 * wq) << 16);
+    const uint32_t t_o = trow + D * t;
     const float sl = 1.4426950408889634f * rsqrtf((float)D);
     uint32_t ct = 0;           // key tiles of this MMA tile
     bool ok = true, mine = false, idle = false;
     int qp = 0, lo = 0;
     float mref = 0.f, l = 0.f;
+    // O, which holds the item's earlier tiles (a finite earlier maximum), after their PVs
+    auto rescale = [&](float scale, uint32_t ct) {
+      if (!__all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + (ct - 1) % NBP, ((ct - 1) / NBP) & 1))) return false;
+      fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float o[16];
+        uint32_t u[16];
+        tmem_ld16(t_o + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * scale);
+        tmem_st16(t_o + c, u);
+      }
+      return true;
+    };
 #pragma unroll 1
     for (uint32_t win = 0; ok; ++win) {
       ok = __all_sync(0xffffffffu, wait_meta(win));
       if (!ok) break;
       const WinRec& rec = sRec[win % NWIN];
-      const int flags = rec.flags, row0 = rec.row0, g = rec.g, slot = rec.slot, req = rec.req;
+      const int flags = rec.flags, row0 = rec.row0, nrows = rec.nrows, g = rec.g, slot = rec.slot, req = rec.req;
       if (flags & kEnd) break;
       const int n = t == 1 && !(flags & kTwo) ? 0 : rec.tiles;
       if (flags & kFirst) {
         mine = tok < rec.nrows;
-        idle = !__any_sync(0xffffffffu, mine);
+        idle = !narrow && !__any_sync(0xffffffffu, mine);
         qp = req < 0 ? INT_MAX - 1 : rec.pos0 + (mine ? tok : 0);
         lo = req < 0 ? -1 : qp - v.window;   // own keys at or below lo are seen as sinks only
         mref = -INFINITY;
@@ -453,12 +507,60 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++ct) {
         const int b = ct % NBP;
-        const uint32_t t_p = t_sb + KT + KT / 2 * b;
+        const uint32_t t_p = trow + C::TM_P + 128 * t + KT / 2 * b, t_sb = trow + C::TM_S + 128 * t;
         const int2 lim = sLim[win % NWIN * WT + j];
         const bool masked = __any_sync(0xffffffffu, lim.x > qp || lim.y <= lo);
         ok = __all_sync(0xffffffffu, wait(C::B_SFULL + t, ct & 1));
         if (!ok) break;
-        if (!idle) {
+        if constexpr (narrow) {
+          fence_after();
+          float s[16];
+          tmem_ld16(t_sb + 16 * wq, s);
+          tmem_wait_ld();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_SFREE + t));
+          if (masked) {
+            const unsigned seen = seen_bits(sPage[win % NWIN * WIN + j * KP + wq], qp, lo, v.sinks);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = seen >> i & 1u ? s[i] : -INFINITY;
+          }
+          float m2[2] = {s[0], s[1]};
+#pragma unroll
+          for (int i = 2; i < 16; ++i) m2[i & 1] = fmaxf(m2[i & 1], s[i]);
+          const float mx = fmaxf(m2[0], m2[1]) * sl;
+          const bool grow = mx > mref + kRescale;
+          const float mnew = grow ? mx : mref;
+          const float scale = (grow && mref != -INFINITY) ? ex2(mref - mnew) : 1.f;
+          mref = mnew;
+          const float mz = mref == -INFINITY ? 0.f : -mref;
+          float2 sum = make_float2(l * scale, 0.f);
+          uint32_t pv[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float2 p = fma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(sl, sl), make_float2(mz, mz));
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            sum = add2(sum, p);
+            pv[e] = pack_bf16x2(p.x, p.y);
+          }
+          l = sum.x + sum.y;
+          ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + b, (ct / NBP + 1) & 1));
+          if (!ok) break;
+          fence_after();
+          const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < KP; ++k) {
+            if (k == wq) tmem_st8(t_p + 8 * k, pv);
+            else tmem_st8(t_p + 8 * k, none);
+          }
+          if (__any_sync(0xffffffffu, mine && scale != 1.f)) {
+            ok = rescale(scale, ct);
+            if (!ok) break;
+          }
+          tmem_wait_st();
+          fence_before();
+        } else if (!idle) {
           fence_after();
           float s[KT];
 #pragma unroll
@@ -471,7 +573,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             const int4* pages = sPage + win % NWIN * WIN + j * KP;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const unsigned seen = seen_bits(pages[2 * c], pages[2 * c + 1], qp, lo, v.sinks);
+              const unsigned seen = seen_bits(pages[2 * c], qp, lo, v.sinks) | seen_bits(pages[2 * c + 1], qp, lo, v.sinks) << 16;
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[32 * c + i] = seen >> i & 1u ? s[32 * c + i] : -INFINITY;
             }
@@ -504,21 +606,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             tmem_st16(t_p + 16 * c, pv);
           }
           l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if (__any_sync(0xffffffffu, scale != 1.f)) {
-            // O holds the item's earlier tiles (a finite earlier maximum): their PVs first
-            ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + (ct - 1) % NBP, ((ct - 1) / NBP) & 1));
+          if (__any_sync(0xffffffffu, mine && scale != 1.f)) {
+            ok = rescale(scale, ct);
             if (!ok) break;
-            fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float o[16];
-              uint32_t u[16];
-              tmem_ld16(t_o + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * scale);
-              tmem_st16(t_o + c, u);
-            }
           }
           tmem_wait_st();
           fence_before();
@@ -533,11 +623,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       done_with(win);
       if (!(flags & kLast) || n == 0) continue;
       // the item's result
+      float2* ml = reinterpret_cast<float2*>(sm + C::OFF_JOIN);
+      if constexpr (narrow) {
+        if (lane < 16) ml[16 * wq + lane] = make_float2(mref, l);
+        ok = join();
+        if (!ok) break;
+      }
       ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + (ct - 1) % NBP, ((ct - 1) / NBP) & 1));
       if (!ok) break;
       if (idle) continue;
       fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;   // no key seen: zeros; NaN stays NaN
+      float weight = 1.f;
+      if constexpr (narrow) {              // one maximum and sum for the row's four parts
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, ml[16 * k + lane % 16].x);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = ml[16 * k + lane % 16];
+          sum += x.y * ex2(x.x - ref);
+        }
+        weight = ex2(mref - ref);
+        mref = mx;
+        l = sum;
+      }
+      const float inv = l == 0.f ? 0.f : weight / l;   // no key seen: zeros; NaN stays NaN
       const bool whole = flags & kWhole;
       const size_t head = mine ? (size_t)(row0 + tok) * a.H + g * v.rep + hh : 0;
       __half* dst = nullptr;
@@ -548,27 +659,85 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         } else {
           const size_t at = whole ? (req < 0 ? 0 : (size_t)v.T * a.H) + head : (size_t)slot * a.part_rows + tok * v.rep + hh;
           po = (whole ? a.seg_o : a.part_o) + at * D;
-          (whole ? a.seg_ml : a.part_ml)[at] = make_float2(mref, l);
+          if (!narrow || wq == 0) (whole ? a.seg_ml : a.part_ml)[at] = make_float2(mref, l);
         }
       }
+      if constexpr (narrow) {
+        // the sum of the row's four parts, 8 of 32 columns a warp: the others' through shared memory,
+        // [chunk of 32 columns][to][from][row][8]; with few rows several chunks at once
+        const int nr = nrows * v.rep, chunks = min(D / 32, 16 / nr);
+        float* part = reinterpret_cast<float*>(sm + C::OFF_JOIN + 512) + lane * 8;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        float o[32];
-        tmem_ld32(t_o + c0, o);
-        tmem_wait_ld();
+        for (int c0 = 0; c0 < D; c0 += 32 * chunks) {
+          if (c0) ok = join();
+          if (!ok) break;
+          const int n32 = min(chunks, (D - c0) / 32);
+#pragma unroll 1
+          for (int r = 0; r < n32; ++r) {
+            float o[24];
+            __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-        if (dst) {
+            for (int k = 0; k < 3; ++k) tmem_ld8(t_o + c0 + 32 * r + 8 * ((wq + k + 1) & 3), o + 8 * k);
+            tmem_wait_ld();
+            if (mine) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t u[8];
+              for (int k = 0; k < 3; ++k) {
+                float4* to = reinterpret_cast<float4*>(part + ((r * 4 + ((wq + k + 1) & 3)) * 3 + k) * nr * 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = pack_f16x2(o[c + 2 * e], o[c + 2 * e + 1]);
-            stg256(dst + c0 + c, u);
+                for (int e = 0; e < 8; ++e) o[8 * k + e] = l == 0.f ? 0.f : o[8 * k + e] * inv;
+                to[0] = make_float4(o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3]);
+                to[1] = make_float4(o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]);
+              }
+            }
           }
-        } else if (po) {
+          ok = join();
+          if (!ok) break;
+#pragma unroll 1
+          for (int r = 0; r < n32; ++r) {
+            const int col = c0 + 32 * r + 8 * wq;
+            float y[8];
+            __syncwarp();
+            tmem_ld8(t_o + col, y);
+            tmem_wait_ld();
+            if (!mine) continue;
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) stg256(po + c0 + c, reinterpret_cast<const uint32_t*>(o + c));
+            for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : y[e] * inv;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              const float4* from = reinterpret_cast<const float4*>(part + ((r * 4 + wq) * 3 + k) * nr * 8);
+              const float4 x0 = from[0], x1 = from[1];
+              y[0] += x0.x, y[1] += x0.y, y[2] += x0.z, y[3] += x0.w;
+              y[4] += x1.x, y[5] += x1.y, y[6] += x1.z, y[7] += x1.w;
+            }
+            if (dst)
+              *reinterpret_cast<uint4*>(dst + col) =
+                  make_uint4(pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3]), pack_f16x2(y[4], y[5]), pack_f16x2(y[6], y[7]));
+            else
+              stg256(po + col, reinterpret_cast<const uint32_t*>(y));
+          }
+        }
+        if (!ok) break;
+        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          tmem_ld32(t_o + c0, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+          if (dst) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+              uint32_t u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[e] = pack_f16x2(o[c + 2 * e], o[c + 2 * e + 1]);
+              stg256(dst + c0 + c, u);
+            }
+          } else if (po) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) stg256(po + c0 + c, reinterpret_cast<const uint32_t*>(o + c));
+          }
         }
       }
       fence_before();   // the next item's first PV overwrites O only after this warp's next P
@@ -592,6 +761,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       if (!ok) break;
       const int flags = __shfl_sync(0xffffffffu, sRec[win % NWIN].flags, 0), n = __shfl_sync(0xffffffffu, sRec[win % NWIN].tiles, 0);
       if (flags & kEnd) break;
+      unsigned rows = 0;
+      if (MT == 1 && !s_warp) rows = (unsigned)sPage[win % NWIN * WIN + lane].z;
       done_with(win);
       const bool mine = t == 0 || (flags & kTwo);
       const uint32_t qb = qi % NQ, qd = desc_lo(base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE);
@@ -604,12 +775,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           if (ok && one) mbar_arrive(bar(empty + st));
           continue;
         }
+        if (MT == 1 && !s_warp && ok) mend(st, j, rows);
         const int b = ct % NBP;
-        // S: the softmax has read the one before (the first wait returns at once); PV: its P is written
+        // S: the softmax has read the buffer (the first waits return at once); PV: its P is written
         ok = ok && (s_warp ? wait_all(C::B_SFREE + t, (ct + 1) & 1) : wait_all(C::B_PREADY + t * NBP + b, (ct / NBP) & 1));
         if (!ok) break;
         fence_after();
-        const uint32_t buf = tmem + C::TM_S + 128 * t + (s_warp ? 0 : KT + KT / 2 * b);
+        const uint32_t buf = tmem + 128 * t + (s_warp ? C::TM_S : C::TM_P + KT / 2 * b);
         if (one) {
           if (s_warp) {
             const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
@@ -731,6 +903,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           // tokens behind the item's are read with the last box, rows of the operand behind it stay as
           // they are (their results are not used)
           const uint32_t dst = base + C::OFF_Q + (t * NQ + qb) * C::Q_TILE, full = bar(C::B_QFULL + t * NQ + qb);
+          if constexpr (narrow) {         // rows 32 w: the same for each softmax warp w
+            if (lane == 0) mbar_expect_tx(full, 4 * (D / 64) * v.mrows * 128);
+            __syncwarp();
+            if (lane < 4 * (D / 64))
+              tma_4d(dst + lane / 4 * 16384 + lane % 4 * 4096, &ta.qmap, g * v.rep, lane / 4, row0, full);
+            continue;
+          }
           const int boxes = pdiv(min(rows - t * tpt, tpt), 8);
           if (lane == 0) mbar_expect_tx(full, boxes * (D / 64) * 8 * v.rep * 128);
           __syncwarp();
@@ -800,11 +979,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         } else {
           const bool live = !end && lane / KP == i && pg.z != 0;
           const unsigned who = __ballot_sync(0xffffffffu, live);
-          // the pages' rows, from the lanes that hold them
-          const unsigned r0 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP), r1 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 1);
-          const unsigned r2 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 2), r3 = __shfl_sync(0xffffffffu, (unsigned)pg.z, i * KP + 3);
           if (lane == 0) {
-            sTile[st] = make_int4((int)(r0 | r1 << 16), (int)(r2 | r3 << 16), end, 0);
+            sEnd[st] = end;
             mbar_expect_tx(bar(C::B_XFULL + st), (uint32_t)__popc(who) * (C::PAGE_BYTES + C::CS_ROW));
           }
           __syncwarp();
@@ -841,19 +1017,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         const int st = gt % NV;
         ok = __all_sync(0xffffffffu, wait(C::B_VFULL + st, (gt / NV) & 1));
         if (!ok) break;
-        unsigned todo = __ballot_sync(0xffffffffu, lane / KP == i && rows != 0xffffu);   // pages, by lane
-#pragma unroll 1
-        for (; todo; todo &= todo - 1) {
-          const int l = __ffs(todo) - 1;
-          const unsigned have = __shfl_sync(0xffffffffu, rows, l);
-          uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + l % KP * C::PAGE_BYTES;
-#pragma unroll 1
-          for (int u = lane; u < C::PAGE_BYTES / 16; u += 32) {   // [half][row][8 chunks]
-            const int r = u / 8 % kPage;
-            if (!(have >> r & 1u)) *reinterpret_cast<uint4*>(vs + u * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_smem();
-        }
+        mend(st, i, rows);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_VREADY + st));
       }
@@ -879,16 +1043,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     // stage, and in a K stage
     const int x1 = p * C::PAGE_BYTES + sw128(r, c), x2 = D == 128 ? x1 + 2048 : p * C::PAGE_BYTES + sw128(r, c + CH);
     const int k1 = p * 2048 + sw128(r, c), k2 = D == 128 ? KT * 128 + k1 : p * 2048 + sw128(r, c + CH);
-    const int shift = p % 2 * 16 + r;
     bool ok = true;
     uint32_t sx = 0, px = 0, sk = 0, pk = 1;   // stages and their parities
 #pragma unroll 1
-    for (uint32_t gt = 0;; ++gt) {
+    for (;;) {
       ok = __all_sync(0xffffffffu, wait(C::B_XFULL + sx, px));
       if (!ok) break;
-      const int4 tile = sTile[sx];
-      if (tile.z) break;
-      const bool holes = (tile.x & tile.y) != -1;
+      if (sEnd[sx]) break;
       const uint8_t* xs = sm + C::OFF_X + sx * C::K_BYTES;
       const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (sx * KP + p) * C::CS_ROW) + c;
       uint4 w1[NP], w2[NP];
@@ -911,19 +1072,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           const float2 y = fma2(make_float2(-z.x, -z.y), os[u][e], mul2(k, oc[u][e])), x = fma2(k, os[u][e], mul2(z, oc[u][e]));
           a1[e] = pack_f16x2(y.x * f[e].x - x.x * f[e].y, y.y * f[e].z - x.y * f[e].w);
           a2[e] = pack_f16x2(x.x * f[e].x + y.x * f[e].y, x.y * f[e].z + y.y * f[e].w);
-        }
-      }
-      if (holes) {
-        // rows without a key: K is zero, and V must be finite (P is 0 there)
-        ok = __all_sync(0xffffffffu, wait(C::B_VFULL + gt % NV, (gt / NV) & 1));
-        if (!ok) break;
-        uint8_t* vs = sm + C::OFF_V + gt % NV * C::K_BYTES;
-#pragma unroll
-        for (int u = 0; u < NP; ++u) {
-          if ((unsigned)(p < 2 ? tile.x : tile.y) >> (shift + RS * u) & 1u) continue;
-          w1[u] = w2[u] = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vs + x1 + u * RS * 128) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(vs + x2 + u * RS * 128) = make_uint4(0, 0, 0, 0);
         }
       }
       ok = __all_sync(0xffffffffu, wait(C::B_KEMPTY + sk, pk));   // the first round's waits return at once
@@ -979,12 +1127,12 @@ bool page_map(CUtensorMap* m, const void* base, int blocks, int G, int D) {
 }
 
 // q [T][H][D] of fp16 as (64 dims, H heads, D / 64 halves, T rows); a box is one half of the rep heads
-// of a KV head of 8 rows, landing as [row][head][128 B].
-bool q_map(CUtensorMap* m, const BatchArgs& a) {
+// of a KV head of `rows` rows, landing as [row][head][128 B].
+bool q_map(CUtensorMap* m, const BatchArgs& a, int rows) {
   auto enc = encode_fn();
   const cuuint64_t dims[4] = {64, (cuuint64_t)a.H, (cuuint64_t)(a.D / 64), (cuuint64_t)a.v.T};
   const cuuint64_t strides[3] = {(cuuint64_t)a.D * 2, 128, (cuuint64_t)a.H * a.D * 2};
-  const cuuint32_t estr[4] = {1, 1, 1, 1}, box[4] = {64, (cuuint32_t)a.v.rep, 1, 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1}, box[4] = {64, (cuuint32_t)a.v.rep, 1, (cuuint32_t)rows};
   return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(a.q), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1085,8 +1233,8 @@ __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant
 
 }  // namespace
 
-void batch_tc_view(BatchView& v, bool wide) {
-  v.half_rows = 128 / v.rep & ~7;   // a box of q is 8 tokens
+void batch_tc_view(BatchView& v, bool wide, bool narrow) {
+  v.half_rows = narrow ? 16 / v.rep : 128 / v.rep & ~7;   // a box of q is 8 tokens, or all of a narrow item
   v.rb = wide ? 2 * v.half_rows : v.half_rows;
   v.mrows = v.rb * v.rep;
   v.kpages = KP;
@@ -1108,9 +1256,11 @@ pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st) {
 pic_status launch_batch_tc(const BatchArgs& a, bool wide, cudaStream_t st) {
   TcArgs ta;
   ta.b = a;
-  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a) ||
+  const bool narrow = a.v.mrows <= 16;
+  if (!page_map(&ta.vmap, a.v_layer, a.v.pool_blocks, a.v.G, a.D) || !q_map(&ta.qmap, a, narrow ? a.v.half_rows : 8) ||
       !(wide ? krot_map(&ta.kmap, a) : page_map(&ta.kmap, a.k_layer, a.v.pool_blocks, a.v.G, a.D) && cs_map(&ta.cmap, a)))
     return fail(PIC_ERR_CUDA, "cuTensorMapEncodeTiled failed for the pools, q, the RoPE table or the rotated K");
+  if (narrow) return a.D == 128 ? launch<Cfg<128, 1, true>>(ta, st) : launch<Cfg<64, 1, true>>(ta, st);
   if (a.D == 128) return wide ? launch<Cfg<128, 2>>(ta, st) : launch<Cfg<128, 1>>(ta, st);
   return wide ? launch<Cfg<64, 2>>(ta, st) : launch<Cfg<64, 1>>(ta, st);
 }
