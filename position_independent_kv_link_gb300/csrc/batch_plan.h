@@ -211,17 +211,12 @@ PIC_HD int page_index(const BatchBlock& b, int i) { return i < b.sp ? i : b.wp +
 PIC_HD PageRaw page_raw(const BatchView& v, const BatchBlock& b, int i) {
   PageRaw m;
   const int p = page_index(b, i);
-  if (b.req < 0) {
-    m.blk = v.pre_blocks[p];
-    m.pos = v.pre_pos ? v.pre_pos[p] : kPage * p;
-    m.end = v.pre_pos && p + 1 < v.pre_pages ? v.pre_pos[p + 1] : v.pre_len;
-  } else {
-    const size_t at = (size_t)b.req * v.stride;
-    const int first = own_first(v);
-    m.blk = v.block_table[at + p];
-    m.pos = v.page_pos ? v.page_pos[at + p] : first + kPage * p;
-    m.end = v.page_pos && p + 1 < b.np ? v.page_pos[at + p + 1] : b.end;
-  }
+  const bool pre = b.req < 0;
+  const size_t at = pre ? 0 : (size_t)b.req * v.stride;
+  const int* const pos = pre ? v.pre_pos : v.page_pos;
+  m.blk = (pre ? v.pre_blocks : v.block_table)[at + p];
+  m.pos = pos ? pos[at + p] : (pre ? 0 : own_first(v)) + kPage * p;
+  m.end = pos && p + 1 < (pre ? v.pre_pages : b.np) ? pos[at + p + 1] : pre ? v.pre_len : b.end;
   return m;
 }
 // What of it block b uses, checked.

@@ -372,11 +372,6 @@ __device__ __forceinline__ unsigned seen_bits(int4 p, int qp, int lo, int sinks)
   return (unsigned)p.z & upto & (~old | first);
 }
 
-// Page i of a block's list as the tables have it (zeros past its end).
-__device__ __noinline__ PageRaw fetch_page(const BatchView& v, const BatchBlock& b, int i) {
-  return i < b.nv ? page_raw(v, b, i) : PageRaw{0, 0, 0};
-}
-
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_constant__ TcArgs ta) {
   constexpr bool narrow = C::NARROW;
@@ -824,56 +819,61 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     unsigned bad = 0;
     int j = more ? w.j0 : 0;             // next tile to be described
     PageRaw next{0, 0, 0};
-    if (more) next = fetch_page(v, w.b, j * KP + lane);
+    bool fetched = false;                // (one place for the loads: in line, so that nothing waits for them there)
     uint32_t n_win = 0, qi[MT] = {}, gt = 0;   // windows written; items and tiles asked for
     const int tpt = v.half_rows;
     bool ended = !meta;
 #pragma unroll 1
     for (uint32_t win = 0; ok; ++win) {  // V of window win, by the same warp when the two after it are described
 #pragma unroll 1
-      for (; !ended && n_win < win + (win == 0 ? 2 : 3); ++n_win) {
-        const int ws = n_win % NWIN;
-        ok = n_win < NWIN || __all_sync(0xffffffffu, wait(C::B_RFREE + ws, (n_win / NWIN - 1) & 1));
-        if (!ok) break;
-        if (!more) {
-          if (lane == 0) {
-            sRec[ws].flags = kEnd;
-            mbar_arrive(bar(C::B_META + ws));
+      while (!ended && n_win < win + (win == 0 ? 2 : 3)) {
+        if (fetched) {
+          const int ws = n_win % NWIN;
+          ok = n_win < NWIN || __all_sync(0xffffffffu, wait(C::B_RFREE + ws, (n_win / NWIN - 1) & 1));
+          if (!ok) break;
+          if (!more) {
+            if (lane == 0) {
+              sRec[ws].flags = kEnd;
+              mbar_arrive(bar(C::B_META + ws));
+            }
+            ended = true;
+            break;
           }
-          ended = true;
-          continue;
-        }
-        const int i = j * KP + lane, n = min(w.j1 - j, WT);
-        PageMeta pm{0, 0, 0};
-        if (lane < n * KP && i < w.b.nv) pm = page_meta(v, w.b, next, bad);
-        int top = pm.rows == 0xffffu ? pm.pos + 15 : INT_MAX;
-        const int sk = min(max(v.sinks - pm.pos, 0), 16);
-        const unsigned behind = pm.rows >> sk << sk;
-        int low = behind ? pm.pos + __ffs(behind) - 1 : INT_MAX;
+          const int i = j * KP + lane, n = min(w.j1 - j, WT);
+          PageMeta pm{0, 0, 0};
+          if (lane < n * KP && i < w.b.nv) pm = page_meta(v, w.b, next, bad);
+          int top = pm.rows == 0xffffu ? pm.pos + 15 : INT_MAX;
+          const int sk = min(max(v.sinks - pm.pos, 0), 16);
+          const unsigned behind = pm.rows >> sk << sk;
+          int low = behind ? pm.pos + __ffs(behind) - 1 : INT_MAX;
 #pragma unroll
-        for (int d = 1; d < KP; d <<= 1) {
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-          low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
+          for (int d = 1; d < KP; d <<= 1) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
+          }
+          int krot = 0;                    // the page's place in the rotated K
+          if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : w.b.req * v.stride);
+          sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, krot);
+          if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
+          if (lane == 0) {
+            WinRec& r = sRec[ws];
+            r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows > v.half_rows ? kTwo : 0) |
+                      (w.j0 == 0 && w.j1 == w.nt ? kWhole : 0);
+            r.tiles = n, r.req = w.b.req, r.row0 = w.b.row0, r.nrows = w.b.nrows, r.pos0 = w.b.pos0, r.g = w.g;
+            r.slot = part_slot(blockIdx.x, w.start, w.x0);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_META + ws));
+          ++n_win;
+          j += n;
+          if (j == w.j1) {
+            more = w.next(a);
+            j = w.j0;
+          }
         }
-        int krot = 0;                    // the page's place in the rotated K
-        if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : w.b.req * v.stride);
-        sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, krot);
-        if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
-        if (lane == 0) {
-          WinRec& r = sRec[ws];
-          r.flags = (j == w.j0 ? kFirst : 0) | (j + n == w.j1 ? kLast : 0) | (w.b.nrows > v.half_rows ? kTwo : 0) |
-                    (w.j0 == 0 && w.j1 == w.nt ? kWhole : 0);
-          r.tiles = n, r.req = w.b.req, r.row0 = w.b.row0, r.nrows = w.b.nrows, r.pos0 = w.b.pos0, r.g = w.g;
-          r.slot = part_slot(blockIdx.x, w.start, w.x0);
-        }
-        j += n;
-        if (j == w.j1) {
-          more = w.next(a);
-          j = w.j0;
-        }
-        if (more) next = fetch_page(v, w.b, j * KP + lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_META + ws));
+        fetched = true;
+        const int i = j * KP + lane;
+        next = more && i < w.b.nv ? page_raw(v, w.b, i) : PageRaw{0, 0, 0};
       }
       if (!ok) break;
       if (!load) {
