@@ -262,26 +262,32 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < C; ++e) o[e] *= keep;
         unsigned left = __ballot_sync(0xffffffffu, on && x.y != 0.f);
-#pragma unroll 1
-        while (left) {
-          float y[8][C], ww[8];
+        auto add = [&](auto batch) {   // so many rows on their way at once
+          constexpr int N = decltype(batch)::value;
+          float y[N][C], ww[N];
+          int k = 0;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int k = left ? __ffs(left) - 1 : 0;
+          for (int u = 0; u < N; ++u) {
+            k = left ? __ffs(left) - 1 : k;    // behind the last row: that row again, with weight 0
             const float wk = __shfl_sync(0xffffffffu, w, k);
             const float* row = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, k)) + lane * C;
             ww[u] = left ? wk : 0.f;
             if constexpr (C == 4) {
-              *reinterpret_cast<float4*>(y[u]) = left ? *reinterpret_cast<const float4*>(row) : make_float4(0.f, 0.f, 0.f, 0.f);
+              *reinterpret_cast<float4*>(y[u]) = *reinterpret_cast<const float4*>(row);
             } else {
-              *reinterpret_cast<float2*>(y[u]) = left ? *reinterpret_cast<const float2*>(row) : make_float2(0.f, 0.f);
+              *reinterpret_cast<float2*>(y[u]) = *reinterpret_cast<const float2*>(row);
             }
             left &= left - 1;
           }
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
+          for (int u = 0; u < N; ++u)
 #pragma unroll
             for (int e = 0; e < C; ++e) o[e] += ww[u] * y[u][e];
+        };
+#pragma unroll 1
+        while (left) {
+          if (__popc(left) > 4) add(std::integral_constant<int, 20>());
+          else add(std::integral_constant<int, 4>());
         }
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;

@@ -1239,8 +1239,9 @@ void batch_tc_view(BatchView& v, bool wide, bool narrow) {
   v.mrows = v.rb * v.rep;
   v.kpages = KP;
   v.whole_tiles = wide;
-  // from per-CTA times: an item's start and drain take about as long as 2.4 key tiles (1.6 of one MMA tile)
-  v.cost_item = wide ? 19 : 13;
+  // in eighths of a key tile; from per-CTA times, an item's start and drain take as long as 2.1 to 4.5 key tiles.
+  // Per item 24, 17, 24 instead: prefill 137 us for 135, prefix of 64 requests 74 for 72; 40, 25, 32: 148 and 73
+  v.cost_item = wide ? 28 : narrow ? 32 : 21;
   v.cost_full = 8;
   v.cost_half = wide ? 6 : 8;
 }
