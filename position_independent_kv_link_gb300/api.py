@@ -445,17 +445,24 @@ def _device_index(x: torch.Tensor) -> int:
     return idx
 
 
+def _raw_stream(idx: int) -> int:
+    """The current stream's handle (a stream object costs a microsecond)."""
+    return torch._C._cuda_getCurrentRawStream(idx)
+
+
 def _call(idx: int, stream: Optional[torch.cuda.Stream], f, *args):
     """f(*args, stream) with device idx current (the current stream of that device when None), its status checked."""
     if stream is None:
-        stream = torch.cuda.current_stream(idx)
+        handle = _raw_stream(idx)
     elif stream.device_index != idx:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == idx:
-        status = f(*args, stream.cuda_stream)
+        status = f(*args, handle)
     else:
         with torch.cuda.device(idx):
-            status = f(*args, stream.cuda_stream)
+            status = f(*args, handle)
     if status != L.PIC_OK:
         L.check(status)
 
@@ -517,7 +524,7 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
         at = buf.data_ptr()
         ptrs = (at, at + 4 * n, at + 8 * n, at + 12 * n + 4, at + 12 * n + 4 + 4 * max_rows,
                 at + 12 * n + 4 + 8 * max_rows)
-        out = BlockTables(*buf.split([n, n, n + 1, max_rows, max_rows, 3]))
+        out = BlockTables(*buf.split_with_sizes([n, n, n + 1, max_rows, max_rows, 3]))
     else:
         ptrs = (_vec(out.kv_len, "out.kv_len", _I32, n, idx), _vec(out.n_pages, "out.n_pages", _I32, n, idx),
                 _vec(out.row_start, "out.row_start", _I32, n + 1, idx),

@@ -714,13 +714,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (!ok) break;
         __syncwarp();
       } else {
+        const bool none = __any_sync(0xffffffffu, mine && l == 0.f);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           float o[32];
           tmem_ld32(t_o + c0, o);
           tmem_wait_ld();
+          if (none) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+            for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = mul2(make_float2(o[e], o[e + 1]), make_float2(inv, inv));
+            o[e] = y.x, o[e + 1] = y.y;
+          }
           if (dst) {
 #pragma unroll
             for (int c = 0; c < 32; c += 16) {
