@@ -24,8 +24,9 @@ struct BatchArgs {
   const void* k_layer;    // [pool_blocks][G][16][D], K unrotated
   const void* v_layer;
   const float2* rope_cs;  // [rope_positions][D / 2]
-  __half* krot;           // scratch, K rotated ahead: [request][page] or [prefix page] x [G][16][D]; or null
+  __half* krot;           // scratch, K rotated ahead: [prefix page] (unless of the own pages alone), [request][page], x [G][16][D]; or null
   int krot_slots;         // pages of krot
+  int krot_own;           // prefix pages of a plan of both
   void* out;              // [T][H][D], q's type
   unsigned* flag;         // the device's word of kBatch* bits
   // scratch
@@ -156,19 +157,20 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
   }
   const int nb = n_pre + n_own;
   const int per_b = pdiv(nb, NT), b0 = pmin(tid * per_b, nb), b1 = pmin(b0 + per_b, nb);
-  unsigned len = 0, U;
+  unsigned len = 0, most = 0, U;
   BatchBlock kept{};
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     plan_block(a, b, n_pre, live, one, kept);
     len += block_len(v, kept);
+    if (block_len(v, kept) > 0 && item_len(v, kept) > most) most = item_len(v, kept);
   }
   BatchShare s;
   unsigned cum = block_scan<NT>(len, sh.scan, U);
   const unsigned part = share_len(U, a.grid);
   s.x0 = share(U, part, blockIdx.x);
   s.x1 = share(U, part, blockIdx.x + 1);
-  const bool whole = (long long)nb * v.G >= (long long)kWholeItems * a.grid;
+  const bool whole = __syncthreads_and(whole_pays(most, part));
   if (whole) {   // the edges move to the next item's start
     if (tid < 2) sh.edge[tid] = U;
     __syncthreads();

@@ -8,7 +8,7 @@
 // tiles of kpages pages. Items lie end to end on a cost axis, blocks in order (prefix blocks
 // first), the KV heads of a block in order, each item cost_item + tiles x tile_cost long. The axis
 // is cut into equal shares, one per CTA: CTA c takes the key tiles whose start lies in [X_c, X_c+1).
-// With many items per CTA (kWholeItems) the shares' edges move to the next item's start instead.
+// With only short items (whole_pays) the shares' edges move to the next item's start instead.
 // An item cut by a share boundary leaves partial results: CTA c's slot 2c holds its part of an
 // item begun by an earlier CTA, slot 2c + 1 its part of an item it begins and does not finish
 // (at most one of each per CTA, so the slots never collide).
@@ -174,9 +174,11 @@ inline double axis_bound(const BatchView& v, double n_own, double n_prefix) {
   const double pre = v.cost_item + (pdiv(v.pre_pages, v.kpages) + 1.0) * v.cost_full;
   return (n_own * item + n_prefix * pre) * v.G;
 }
-// From this many items per CTA on, none is cut: the longest share is then at most 1 / 4 over the others'
-// length, less with more items, where cutting costs the parts' way through memory and the merge.
+// When the longest item is at most 1 / kWholeItems of a share, none is cut: the longest share is then at most
+// that much over the others' length, where cutting costs the parts' way through memory and the merge.
+// (Two prompts of 4096 rows: 181 us with items cut, 161 without.)
 constexpr int kWholeItems = 4;
+PIC_HD bool whole_pays(unsigned longest_item, unsigned share) { return longest_item <= share / kWholeItems; }
 // The right edge of a share at x, inside block b: the item's start at or after x.
 PIC_HD unsigned item_edge(const BatchView& v, const BatchBlock& b, unsigned x) {
   const unsigned ilen = item_len(v, b);

@@ -345,9 +345,9 @@ struct BatchCall {
 // Measured on 8 KV heads of 4 query heads, D = 128, window 1024: two prompts of 4096 rows -- ahead / in
 // the kernel -- see the launch; 64 single rows behind a prefix of 16384: see there.
 constexpr size_t kMaxRotated = (size_t)1 << 30;
-bool wide_pays(long long rows, double slots, int G, int D) {
-  return rows >= 512 && slots * G * kPage * D * 2 <= (double)kMaxRotated;
-}
+double most_slots(int G, int D) { return (double)kMaxRotated / ((double)G * kPage * D * 2); }
+bool wide_pays(long long rows, double slots, int G, int D) { return rows >= 512 && slots <= most_slots(G, D); }
+constexpr int kRowsWithPrefix = 64;
 
 void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, int table_stride, int prefix_len,
                int prefix_pages) {
@@ -369,9 +369,15 @@ void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
   }
   a.grid = device_sms();
   const double own_slots = (double)n_reqs * table_stride;
-  const bool own = n_reqs <= 65535 && wide_pays((long long)pdiv(T, n_reqs) * a.v.rep, own_slots, G, D);   // a grid's y
+  const long long own_rows = (long long)pdiv(T, n_reqs) * a.v.rep;
+  bool own = wide_pays(own_rows, own_slots, G, D);
   const bool pre = prefix_len > 0 && wide_pays((long long)T * a.v.rep, prefix_pages, G, D);
-  if (prefix_len > 0 && (own || pre)) {
+  // Behind a prefix for the wide kernel the own pages go with it, in one plan, from half an MMA tile of rows a
+  // request on. One launch less, and their K needs no rotation for every 128 rows: 32 requests of 32 rows behind
+  // 4096, 32 keys of their own: 115 us apart, 100 together; 64 of 16 rows, 64 keys: 120 and 107, 1024 keys: 165
+  // and 173; 8 of 64 rows behind 8192, 2000 keys: 137 and 109.
+  const bool both = pre && own_rows >= kRowsWithPrefix && own_slots + prefix_pages <= most_slots(G, D);
+  if (prefix_len > 0 && (own || pre) && !both) {
     c.n = 2;
     c.a[1] = a;
     c.a[0].v.only = 1;
@@ -381,8 +387,10 @@ void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
     c.a[0].krot_slots = pre ? prefix_pages : 0;
     c.a[1].krot_slots = own ? n_reqs * table_stride : 0;
   } else {
+    own = own || both;
     c.wide[0] = own;
-    a.krot_slots = own ? n_reqs * table_stride : 0;
+    a.krot_own = both ? prefix_pages : 0;
+    a.krot_slots = own ? a.krot_own + n_reqs * table_stride : 0;
   }
   for (int i = 0; i < c.n; ++i) {
     BatchView& v = c.a[i].v;

@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
           }
           int krot = 0;                    // the page's place in the rotated K
-          if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : w.b.req * v.stride);
+          if (MT == 2) krot = page_index(w.b, i) + (w.b.req < 0 ? 0 : a.krot_own + w.b.req * v.stride);
           sPage[ws * WIN + lane] = make_int4(pm.blk * v.G + w.g, pm.pos, (int)pm.rows, krot);
           if (lane % KP == 0) sLim[ws * WT + lane / KP] = make_int2(top, low);
           if (lane == 0) {
@@ -1198,10 +1198,11 @@ __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;");
   const BatchView& v = a.v;
   constexpr int CH = D / 16, HP = 256 / (16 * CH);   // KV heads at once
-  const int p = blockIdx.x, r = blockIdx.y, c = threadIdx.x % CH, row = threadIdx.x / CH % kPage, g0 = threadIdx.x / (16 * CH);
+  const int n_pre = v.only == 1 ? v.pre_pages : a.krot_own, i = (int)blockIdx.x - n_pre;
+  const int r = i < 0 ? -1 : i / v.stride, p = i < 0 ? (int)blockIdx.x : i - r * v.stride, c = threadIdx.x % CH, row = threadIdx.x / CH % kPage, g0 = threadIdx.x / (16 * CH);
   unsigned bad = 0;
   BatchBlock b;
-  if (v.only == 1) {
+  if (r < 0) {
     b = prefix_block(v, 1, 0);
   } else {
     int row0;
@@ -1219,8 +1220,7 @@ __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[e] = cs[e];
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k_layer) + (size_t)pm.blk * v.G * kPage * D + row * D + 8 * c;
-  const size_t slot = v.only == 1 ? (size_t)p : (size_t)r * v.stride + p;
-  __half* dst = a.krot + slot * v.G * kPage * D + row * D + 8 * c;
+  __half* dst = a.krot + (size_t)blockIdx.x * v.G * kPage * D + row * D + 8 * c;
 #pragma unroll 2
   for (int g = g0; g < v.G; g += HP) {
     const uint4 u1 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D);
@@ -1255,7 +1255,7 @@ void batch_tc_view(BatchView& v, bool wide, bool narrow) {
 }
 
 pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st) {
-  const dim3 grid(a.v.only == 1 ? a.v.pre_pages : a.v.stride, a.v.only == 1 ? 1 : a.v.n_reqs);
+  const dim3 grid(a.krot_slots);
   if (a.D == 128) batch_rotate_kernel<128><<<grid, 256, 0, st>>>(a);
   else batch_rotate_kernel<64><<<grid, 256, 0, st>>>(a);
   PIC_CUDA(cudaGetLastError());

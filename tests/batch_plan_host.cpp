@@ -50,10 +50,13 @@ int batch_plan_host(const int* p, const int* row_start, const int* kv_len, const
   }
   if (U > axis_bound(v, v.T / v.rb + v.n_reqs, v.pre_len > 0 ? v.T / v.rb + 1 : 0)) return 3;
   const unsigned len = share_len(U, grid);
+  unsigned longest = 0;
+  for (const BatchBlock& b : blocks)
+    if (block_len(v, b) > 0 && item_len(v, b) > longest) longest = item_len(v, b);
+  const bool whole_items = whole_pays(longest, len);
   if (share(U, len, grid) != U) return 2;   // the shares do not reach the end
   for (int c = 0; c < grid && U > 0; ++c) {
     unsigned x0 = share(U, len, c), x1 = share(U, len, c + 1);
-    const bool whole_items = (long long)blocks.size() * v.G >= (long long)kWholeItems * grid;
     if (whole_items)
       for (unsigned* x : {&x0, &x1})
         for (const BatchBlock& b : blocks)
