@@ -1,45 +1,59 @@
 // tcgen05 kernel of the batched paged attention: bf16 pools, head_dim 64 or 128, up to 16 query
 // heads per KV head, one persistent CTA per SM over its share of the plan (batch_plan.h).
 //
-// An item is a row block x a KV head: MT tiles of up to 128 MMA rows (half_rows tokens x the rep heads
-// of the group, a multiple of 8 tokens). Its pages come in windows of 32 (one record each) and key tiles of 64 keys, which pass
-// through rings of stages in shared memory:
+// An item is a row block x a KV head: MT tiles of up to 128 MMA rows (half_rows tokens x the rep heads of the
+// group, a multiple of 8 tokens), or, narrow, up to 16 rows. Its pages come in windows of 32 (one record each)
+// and key tiles of 64 keys, which pass through rings of stages in shared memory:
 //
-//   meta warp   walks the share: reads the page tables a window ahead, writes the windows' records
-//               (item, rows, pages with the rows that hold keys), and asks for K, one TMA box a page
-//               wherever its block lies, with the RoPE table row of the page's position.
-//   load warp   asks for the items' rows of q (TMA boxes of 8 tokens x rep heads; double-buffered for
-//               one MMA tile, else when the item's last S product has retired) and for V, one box a
-//               page: a page is one K = 16 step of the PV product, so pages need not be neighbours.
-//   rotation    (MT = 1) turns raw K into the fp16 operand: thread = row of a page x 8 pairs of dims; the
-//               angle of row r of a page at position P is composed from the table rows of P (shared
-//               memory, one row a page) and of r (registers), so that a key needs no table row of its
-//               own. One rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S).
+//   meta warp   walks the share: reads the page tables a window ahead and writes the windows' records (item,
+//               rows, pages with the rows that hold keys).
+//   load        (the meta warp, or, MT = 2, a warp of its own) asks for the items' rows of q (TMA boxes of 8
+//               tokens x rep heads; double-buffered for one MMA tile, else when the item's last S product has
+//               retired) and for V, one box a page: a page is one K = 16 step of the PV product, so pages need
+//               not be neighbours.
+//   K warp      asks for K, one TMA box a page wherever its block lies, with the RoPE table row of the page's
+//               position. On its own: with the records' work in the same warp K came late (decode batch below
+//               132 us instead of 112).
+//   rotation    (MT = 1) turns raw K into the fp16 operand: thread = two rows of a page x 8 pairs of dims; the
+//               key in row r of a page at position P is turned by the angle of r (registers) and then by that
+//               of P (shared memory, one table row a page), pairs of fp32 at a time, so that a key needs no
+//               table row of its own. One rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S).
 //   V mending   rows that hold no key any row of the block sees are zeroed in V (P is 0 there, V must be
-//               finite), by the rotation or (MT = 2) a warp of its own.
-//   S warps     (one per MMA tile) one thread issues S_t = Q_t K^T (fp16) of a key tile as soon as the
-//               softmax has the S before it in registers.
-//   PV warps    (one per MMA tile) one thread issues O_t += P_t V (bf16, P from TMEM). A warp for each
-//               product of each tile: an issuing thread takes about as long for its waits and jumps as
-//               for the products. One thread for both products of a tile, S(j + 2) right behind PV(j) in
-//               its in-order queue, took 1500 ns a key tile of two MMA tiles where this takes 1050.
+//               finite), by the PV warp or (MT = 2) a warp of its own. K needs none: their S is masked.
+//   S warps     (one per MMA tile) issue S_t = Q_t K^T (fp16) of a key tile as soon as the softmax has the S
+//               before it in registers.
+//   PV warps    (one per MMA tile) issue O_t += P_t V (bf16, P from TMEM). A warp for each product of each tile:
+//               one thread for both products of a tile, S(j + 2) right behind PV(j) in its in-order queue, took
+//               1500 ns a key tile of two MMA tiles where this took 1050. The warp loops as a whole and an
+//               elected lane issues: operands stay in uniform registers (two prompts below 155 -> 149 us).
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
 //               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 into one of two P buffers
 //               (V is stored bf16 and both operands have one type; the sum is of the unrounded
 //               fp32 weights), and the item's result: out, or for parts of items and for prefix
 //               batches the normalized fp32 row with its maximum and sum for the merge.
+//   narrow      (single decoded tokens) the four softmax warps have the same rows, at MMA rows 32 w (q is loaded
+//               four times), and one page of each key tile each, with zero P for the others: one warp's 64
+//               columns a tile would take longer than anything else (112 us instead of 106). Their four O's, with
+//               maxima and sums of their own, are joined through shared memory at the item's end. A kernel of its
+//               own: both softmaxes in one cost either 5 % (instruction cache).
 //
 // The roles' loops are kept small, and few on each scheduler: with three times the code every role ran
-// at 8 cycles an instruction (ncu: no_instruction the largest stall). At the 5 that are left (a warp
-// on its own waits for its last result) the rotation's control is what is worth saving, hence TMA.
+// at 8 cycles an instruction (ncu: no_instruction the largest stall).
 //
-// MT = 1: few rows, HBM-bound; K is rotated on its way. MT = 2: many rows, MMA-bound; K has been rotated
+// MT = 1: few rows, HBM-bound; K is rotated on its way. MT = 2: many rows; K has been rotated
 // ahead, once per page, into a scratch (batch_rotate_kernel) and comes as two boxes of four pages.
 // Rotating it here instead, for every 256 rows anew, kept the schedulers busier than the MMAs (2900
 // cycles a key tile against 1300).
 //
+// Measured, 8 KV heads of 4 query heads, D = 128, whole call: 32 decoding requests of 3000 to 32000 keys, window
+// 4096 (0.53 GB of K and V): 104 us, 5.1 TB/s, 650 to 800 ns a key tile (21 us of it start, item ends and merge).
+// Two prompts of 4096, window 1024 (123 GFLOP): 135 us, 0.91 PFLOP/s; 810 ns a key tile of two MMA tiles, whose MMAs take
+// 550: the rest is the way S -> registers -> next S (issue 370 cycles, product to softmax 830, read 150,
+// softmax to S warp 300), for which TMEM has no second S buffer.
+//
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
+#include <atomic>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -112,16 +126,15 @@ struct WinRec {           // 48 bytes
 // Every waiter of a barrier sees each of its phases before the next can complete (a parity wait
 // cannot tell phase n from n + 2). META, RFREE: a record is rewritten only when every warp that
 // reads records has arrived at RFREE for the window before in its slot. XFULL, XEMPTY: between the
-// meta warp and the rotation, all of whose warps arrive. READY (of K), KEMPTY: the rotation, or the meta
+// K warp and the rotation, all of whose warps arrive. READY (of K), KEMPTY: the rotation, or the K
 // warp's TMA, of tile j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows
 // PV of j, which waits for VREADY (or VFULL); VREADY: VFULL seen and mended. SFULL, SFREE: between the
 // S warp and warpgroup t, all of whose warps arrive. PREADY, PVDONE: between warpgroup t and the PV
 // warp; P(j + 2) into a buffer follows the end of PV(j). QFULL, QEMPTY: between the load and the S warp.
-// No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN and K asked
-// for up to window i - 3, that is the S products NX + NK tiles before: with windows of one tile, of
-// tile i - 3 - NX - NK at the latest, while its readers are never more than two windows ahead of the S
-// products. V and q of a tile wait for
-// products of earlier tiles only, the rotation of a tile with empty rows for its V.
+// JOIN: the four softmax warps of a narrow item, which all wait.
+// No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN, and by then (MT 1)
+// the meta warp has asked for q and V up to window i - 4; K, S, P and PV of windows up to there need only
+// records before i. V and q of a tile wait for products of earlier tiles only.
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // SM clock cycles (reading the global timer instead takes long enough to delay every wait)
@@ -1173,7 +1186,7 @@ bool krot_map(CUtensorMap* m, const BatchArgs& a) {
 
 template <typename C>
 pic_status launch(const TcArgs& ta, cudaStream_t st) {
-  static bool set[64] = {};
+  static std::atomic<bool> set[64];
   int dev = 0;
   PIC_CUDA(cudaGetDevice(&dev));
   const int smem = C::SMEM + 1024;

@@ -89,6 +89,8 @@ CASES = [
     (batch([64] * 700, [1] * 700, seed=6), dict(rep=3, G=1)),
     (batch([2000, 1, 2000], [2000, 1, 1], seed=7), dict(rep=16, costs=(0, 1, 1), grid=13)),
     (batch([0, 0], [0, 0]), {}),
+    (batch([20] * 400, [9] * 400, prefix=9000, seed=9), dict(kpages=4, costs=(28, 8, 6))),       # many items, some of them long
+    (batch([90] * 900, [1] * 900, ragged=True, seed=10), dict(mrows=16, kpages=4, costs=(32, 8, 8), window=50, sinks=3)),   # none long
 ]
 
 

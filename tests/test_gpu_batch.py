@@ -172,6 +172,9 @@ WINDOW_CASES = [
     ([700, 260], [300, 260], 128, 16, True),
     ([2100], [1], 1000, 4, False),
     ([64] * 37, [1] * 37, 64, 0, False),
+    ([100, 300, 50, 700], [4, 3, 1, 2], 60, 5, True),        # a few rows each
+    ([200] * 20 + [90], [1] * 20 + [40], 0, 0, False),       # and one request of many
+    ([40, 50], [16, 9], 20, 2, False),
 ]
 SHAPES = [(4, 4, 64, False), (8, 2, 128, False), (8, 2, 128, True), (8, 8, 128, True), (7, 1, 128, True), (8, 2, 64, True),
           (16, 1, 128, True)]
@@ -196,6 +199,8 @@ PREFIX_CASES = [
     ([300, 7], [1, 7], 0, True),
     ([300, 290], [300, 1], 700, False),
     ([2] * 3, [1] * 3, 4000, False),
+    ([9, 33], [2, 2], 3000, True),
+    ([90, 64, 200, 77], [90, 64, 64, 77], 1500, True),
 ]
 
 
@@ -205,6 +210,52 @@ def test_prefix_attention(pkl, shape, case):
     kv, rows, prefix, ragged = case
     b = Batch(pkl, kv, rows, *shape, ragged=ragged, prefix=prefix, seed=len(kv) + prefix, spare_rows=2)
     b.check(b.shared())
+
+
+@pytest.mark.parametrize("rows,prefix,rep", [(1, 0, 4), (20, 0, 4), (20, 300, 4), (1, 300, 4), (1, 300, 8)])
+def test_many_requests(pkl, rows, prefix, rep):
+    """More items than CTAs several times over (none is cut then, or, next to long ones of a prefix, some)."""
+    b = Batch(pkl, [30 + rows] * 420, [rows] * 420, 2 * rep, 2, 128, True, prefix=prefix, seed=rows + prefix + rep)
+    b.check(b.shared() if prefix else b.window(25, 3), 0 if prefix else 25, 0 if prefix else 3)
+
+
+@pytest.mark.parametrize("H,G,D", [(6, 2, 128), (10, 2, 64), (12, 1, 128), (15, 1, 64)])
+def test_heads_that_do_not_fill_a_tile(pkl, H, G, D):
+    """Groups of 3, 5, 12 and 15 query heads: single rows, as many as fit one small item, one more, and many."""
+    n = 16 // (H // G)
+    for rows in ([1, 1, 1], [n, n, 1], [n + 1, n, n], [70, 130, 1], [300, 257, 9]):
+        kv = [r + 40 * i + 3 for i, r in enumerate(rows)]
+        b = Batch(pkl, kv, rows, H, G, D, True, ragged=True, prefix=150, seed=sum(rows), spare_rows=1)
+        b.check(b.shared())
+        b = Batch(pkl, kv, rows, H, G, D, True, ragged=True, seed=sum(rows) + 1, spare_rows=1)
+        b.check(b.window(30, 7), 30, 7)
+
+
+def test_rows_and_blocks_behind_2_to_the_32(pkl):
+    """A pool of more than 2^32 elements whose last blocks are used: written by qk_norm_rope, read by the attention."""
+    G, H, D, far = 2, 8, 128, (1 << 32) // (2 * PAGE * 128) + 40
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    small = Batch(pkl, [100, 33, 700], [1, 1, 300], H, G, D, True, seed=17)
+    pool = small.k.shape[0]
+    k = torch.empty((far, G, PAGE, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    # the same rows, through the norm-less call, into blocks at the pool's end
+    N = pool * PAGE
+    qkv = torch.zeros(N, (H + 2 * G) * D, device="cuda")
+    rows = qkv.view(N, H + 2 * G, D)
+    rows[:, H:H + G] = small.k.transpose(1, 2).reshape(N, G, D).float().nan_to_num(0.0)
+    rows[:, H + G:] = small.v.transpose(1, 2).reshape(N, G, D).float().nan_to_num(0.0)
+    slot = i32(np.arange(N) + (far - pool) * PAGE)
+    pkl.qk_norm_rope(qkv, H, G, torch.zeros_like(slot), slot, small.rope, k, v)
+    assert torch.equal(k[far - pool:], small.k.nan_to_num(0.0)) and torch.equal(v[far - pool:], small.v.nan_to_num(0.0))
+    want = small.window(90, 4).clone()
+    t = small.pages.block_table
+    t += (t >= 0) * (far - pool)
+    small.k, small.v = k, v
+    small.out.fill_(0)
+    assert torch.equal(small.window(90, 4), want)
+    del qkv, rows
 
 
 @pytest.mark.parametrize("half", [False, True])
@@ -425,6 +476,44 @@ def test_block_tables(pkl, ragged, n, kv_hi, new_hi, first, used):
     assert np.array_equal(d_table.cpu().numpy(), rt)
     if ragged:
         assert np.array_equal(d_pos.cpu().numpy(), rp)
+
+
+@pytest.mark.parametrize("max_rows", [1, 1023, 1024, 1025, 4095, 4096, 4097, 20000])
+@pytest.mark.parametrize("n", [1, 1024, 1025])
+def test_block_tables_row_counts(pkl, n, max_rows):
+    """One request has all the rows (or every row of max_rows is one of its own), the others none."""
+    new = [0] * n
+    new[n // 2] = max_rows
+    kv = [7] * n
+    table = np.full((n, -(-(7 + max_rows) // PAGE)), -3)
+    table[:, 0] = np.arange(n)
+    free = list(range(n, n + -(-(7 + max_rows) // PAGE)))
+    ref, rt, _ = tables_reference(list(kv), new, [1] * n, table, free, 0, max_rows, 5, None)
+    d = i32(table)
+    r = pkl.block_tables(i32(kv), i32(new), d, i32(free), max_rows, first=5)
+    for key, want in ref.items():
+        assert getattr(r, key).tolist() == want, key
+    assert np.array_equal(d.cpu().numpy(), rt)
+
+
+@pytest.mark.parametrize("max_rows", [40, 9000])
+def test_block_tables_in_place(pkl, max_rows):
+    """The lengths, page counts and used entries updated in place, twice in a row and captured."""
+    kv, new, table = i32([0, 17, 40]), i32([5, 0, 30]), i32(np.arange(300).reshape(3, 100) + 1000)
+    free, used = i32(np.arange(50)), i32([3])
+    out = pkl.BlockTables(kv, torch.empty_like(kv), i32(np.zeros(4)), i32(np.zeros(max_rows)), i32(np.zeros(max_rows)),
+                          torch.zeros(3, dtype=torch.int32, device="cuda"))
+    call = lambda: pkl.block_tables(kv, new, table, free, max_rows, free_used=out.counts[1:2], out=out)
+    out.counts[1:2] = used
+    call()
+    assert kv.tolist() == [5, 17, 70] and out.counts.tolist() == [35, 6, 0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    assert kv.tolist() == [10, 17, 100] and out.counts.tolist() == [35, 8, 0]
+    assert out.row_start.tolist() == [0, 5, 5, 35] and out.row_pos[:5].tolist() == [5, 6, 7, 8, 9]
+    assert table[0, 0] == 3 and table[2, 3:7].tolist() == [4, 5, 6, 7]
 
 
 def test_block_tables_all_or_nothing(pkl):
