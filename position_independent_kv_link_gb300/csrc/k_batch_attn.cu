@@ -347,7 +347,7 @@ struct BatchCall {
 // prefix of 16384) 128 and 122 us; 1024 rows (256 single rows behind it) 206 and 227 us; two prompts of 4096
 // with a window of 1024 135 and 218 us.
 constexpr size_t kMaxRotated = (size_t)1 << 30;
-double most_slots(int G, int D) { return (double)kMaxRotated / ((double)G * kPage * D * 2); }
+double most_slots(int G, int D) { return (double)kMaxRotated / ((double)G * kPage * D * 2 * 3); }
 bool wide_pays(long long rows, double slots, int G, int D) { return rows >= 512 && slots <= most_slots(G, D); }
 constexpr int kRowsWithPrefix = 64;
 
@@ -423,7 +423,7 @@ size_t layout(BatchCall& c, char* base) {
     const size_t rows = 2 * (size_t)a.grid * a.part_rows;
     a.part_ml = (float2*)take(rows * sizeof(float2));
     a.part_o = (float*)take(rows * a.D * 4);
-    a.krot = a.krot_slots ? (__half*)take((size_t)a.krot_slots * v.G * kPage * a.D * 2) : nullptr;
+    a.krot = a.krot_slots ? (__half*)take(3 * (size_t)a.krot_slots * v.G * kPage * a.D * 2) : nullptr;
   }
   if (c.a[0].v.pre_len > 0) {
     const size_t rows = 2 * (size_t)c.a[0].v.T * c.a[0].H;

@@ -65,6 +65,7 @@ namespace pic {
 namespace {
 
 constexpr float kRescale = 8.f;           // rescale O when the row maximum grows by more than 2^8
+constexpr float kLift = 4.f;              // a row's largest P is 2^4 then (2^12 before the next rescaling): fp16 has 2^-24 to 65504
 constexpr unsigned long long kWaitLimit = 4000000000ull;   // cycles, about 2 s
 
 constexpr int KT = 64, KP = KT / kPage;   // keys, pages of a tile
@@ -76,12 +77,15 @@ template <int D_, int MT_, bool NARROW_ = false>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
   static constexpr bool NARROW = NARROW_;
-  static constexpr int NQ = MT == 2 ? 1 : 2;          // Q buffers per MMA tile
+  static constexpr int NQ = 1;                        // Q buffers per MMA tile
   static constexpr int NX = MT == 2 ? 0 : D == 128 ? 3 : 6;   // raw K stages (with table rows)
-  static constexpr int NK = MT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 3);   // K operand stages
-  static constexpr int NV = D == 128 ? 4 : 8;         // V stages
+  static constexpr int NK = MT == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 3);   // K operand stages
+  static constexpr int NV = MT == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);   // V stages
   static constexpr int NR = MT == 2 ? 0 : 8;          // rotation warps
   static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
+  static constexpr int K_STAGE = 2 * K_BYTES;         // fp16 and what it leaves out
+  // V of a tile: [page][64-dim half][16 keys][128 B] (pool pages), MT 2: [half][64 keys][128 B] (scratch pages)
+  static constexpr int V_PAGE = MT == 2 ? 2048 : PAGE_BYTES, V_HALF = MT == 2 ? KT * 128 : 2048;
   // Roles of the warps behind the 4 MT softmax warps. Warp w runs on scheduler w % 4, whose small
   // instruction cache is shared by its warps. Rotation: warps 4..11.
   static constexpr int THREADS = 512;
@@ -90,9 +94,9 @@ struct Cfg {
   static constexpr int W_LOAD = MT == 2 ? 15 : W_META;   // q and V
   // shared memory (bytes from a 1024-aligned base)
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK] [64-dim half][key][128 B]
-  static constexpr int OFF_V = OFF_K + NK * K_BYTES;          // [NV] [page][64-dim half][16 keys][128 B]
-  static constexpr int OFF_X = OFF_V + NV * K_BYTES;          // [NX] likewise, raw K
+  static constexpr int OFF_K = OFF_Q + MT * NQ * Q_TILE;      // [NK][2] [64-dim half][key][128 B]
+  static constexpr int OFF_V = OFF_K + NK * K_STAGE;          // [NV]
+  static constexpr int OFF_X = OFF_V + NV * K_BYTES;          // [NX] raw K [page][64-dim half][16 keys][128 B]
   static constexpr int OFF_CS = OFF_X + NX * K_BYTES;         // [NX][KP] table rows, [4][CH][16 B] each
   static constexpr int OFF_REC = OFF_CS + NX * KP * CS_ROW;   // WinRec [NWIN]
   static constexpr int OFF_PAGE = OFF_REC + NWIN * 48;        // int4 [NWIN][WIN] page of the pool, position, rows, page of the rotated K
@@ -109,9 +113,9 @@ struct Cfg {
                        B_DONE = B_QEMPTY + MT * NQ, B_JOIN = B_DONE + 2 * MT, N_BARS = B_JOIN + 1;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
-  // TMEM columns: O_t at D t, S_t at TM_S + 128 t, P buffer b of tile t at TM_P + 128 t + 32 b
-  static constexpr uint32_t TM_S = MT * D, TM_P = TM_S + KT;
-  static constexpr uint32_t TMEM_COLS = MT == 2 ? 512 : 256;
+  // TMEM columns: O_t at D t, S_t at TM_S + 128 t, P buffer b of tile t at TM_P + 128 t + PW b
+  static constexpr uint32_t TM_S = MT * D, TM_P = TM_S + KT, PW = MT == 2 ? KT / 2 : KT;
+  static constexpr uint32_t TMEM_COLS = 512;
 };
 
 constexpr int kFirst = 1, kLast = 2, kTwo = 4, kEnd = 8, kWhole = 16;
@@ -213,12 +217,12 @@ constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo = 0) {
   return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16;
 }
-// kind::f16, fp32 accumulator, M x N: fp16 K-major operands; bf16 A (TMEM) with MN-major B
+// kind::f16, fp32 accumulator, M x N: fp16 K-major operands; fp16 or bf16 A (TMEM) with MN-major B
 __device__ __forceinline__ constexpr uint32_t idesc_s(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ constexpr uint32_t idesc_pv(int M, int N) {
-  return idesc_s(M, N) | (1u << 7) | (1u << 10) | (1u << 16);
+__device__ __forceinline__ constexpr uint32_t idesc_pv(int M, int N, bool bf16) {
+  return idesc_s(M, N) | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (1u << 16);
 }
 template <bool ACC>
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
@@ -327,6 +331,23 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
+  float2 f;
+  asm("{\n .reg .f16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(f.x), "=f"(f.y) : "r"(x));
+  return f;
+}
+// x = hi + lo: 16 of 24 bits as bf16, 22 as fp16 (as many as lie above 2^-25)
+__device__ __forceinline__ void split_bf16x2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  const float2 d = add2(x, make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u)));
+  lo = pack_bf16x2(d.x, d.y);
+}
+__device__ __forceinline__ void split_f16x2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16x2(x.x, x.y);
+  const float2 h = unpack_f16x2(hi), d = add2(x, make_float2(-h.x, -h.y));
+  lo = pack_f16x2(d.x, d.y);
+}
+
 struct TcArgs {
   CUtensorMap kmap, vmap, qmap, cmap;
   BatchArgs b;
@@ -417,11 +438,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     for (unsigned todo = __ballot_sync(0xffffffffu, lane / KP == i && rows != 0xffffu); todo; todo &= todo - 1) {   // pages, by lane
       const int l = __ffs(todo) - 1;
       const unsigned have = __shfl_sync(0xffffffffu, rows, l);
-      uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + l % KP * C::PAGE_BYTES;
+      uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + l % KP * C::V_PAGE;
 #pragma unroll 1
       for (int u = lane; u < C::PAGE_BYTES / 16; u += 32) {   // [half][row][8 chunks]
-        const int r = u / 8 % kPage;
-        if (!(have >> r & 1u)) *reinterpret_cast<uint4*>(vs + u * 16) = make_uint4(0, 0, 0, 0);
+        const int r = u / 8 % kPage, h = u / (8 * kPage);
+        if (!(have >> r & 1u)) *reinterpret_cast<uint4*>(vs + h * C::V_HALF + u % (8 * kPage) * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_async_smem();
     }
@@ -515,7 +536,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++ct) {
         const int b = ct % NBP;
-        const uint32_t t_p = trow + C::TM_P + 128 * t + KT / 2 * b, t_sb = trow + C::TM_S + 128 * t;
+        const uint32_t t_p = trow + C::TM_P + 128 * t + C::PW * b, t_sb = trow + C::TM_S + 128 * t;
         const int2 lim = sLim[win % NWIN * WT + j];
         const bool masked = __any_sync(0xffffffffu, lim.x > qp || lim.y <= lo);
         ok = __all_sync(0xffffffffu, wait(C::B_SFULL + t, ct & 1));
@@ -537,20 +558,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
           for (int i = 2; i < 16; ++i) m2[i & 1] = fmaxf(m2[i & 1], s[i]);
           const float mx = fmaxf(m2[0], m2[1]) * sl;
-          const bool grow = mx > mref + kRescale;
-          const float mnew = grow ? mx : mref;
+          const bool grow = mx > mref + (kRescale + kLift);
+          const float mnew = grow ? mx - kLift : mref;
           const float scale = (grow && mref != -INFINITY) ? ex2(mref - mnew) : 1.f;
           mref = mnew;
           const float mz = mref == -INFINITY ? 0.f : -mref;
           float2 sum = make_float2(l * scale, 0.f);
-          uint32_t pv[8];
+          uint32_t pv[8], pl[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float2 p = fma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(sl, sl), make_float2(mz, mz));
             p.x = ex2(p.x);
             p.y = ex2(p.y);
             sum = add2(sum, p);
-            pv[e] = pack_bf16x2(p.x, p.y);
+            split_bf16x2(p, pv[e], pl[e]);
           }
           l = sum.x + sum.y;
           ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + b, (ct / NBP + 1) & 1));
@@ -559,8 +580,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
           for (int k = 0; k < KP; ++k) {
-            if (k == wq) tmem_st8(t_p + 8 * k, pv);
-            else tmem_st8(t_p + 8 * k, none);
+            if (k == wq) tmem_st8(t_p + 8 * k, pv), tmem_st8(t_p + KT / 2 + 8 * k, pl);
+            else tmem_st8(t_p + 8 * k, none), tmem_st8(t_p + KT / 2 + 8 * k, none);
           }
           if (__any_sync(0xffffffffu, mine && scale != 1.f)) {
             ok = rescale(scale, ct);
@@ -590,8 +611,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
           for (int i = 4; i < KT; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
-          const bool grow = mx > mref + kRescale;
-          const float mnew = grow ? mx : mref;
+          const bool grow = mx > mref + (kRescale + kLift);
+          const float mnew = grow ? mx - kLift : mref;
           const float scale = (grow && mref != -INFINITY) ? ex2(mref - mnew) : 1.f;
           mref = mnew;
           const float mz = mref == -INFINITY ? 0.f : -mref;   // nothing seen so far: every s is -inf, p = 0
@@ -602,16 +623,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t pv[16];
+            uint32_t pv[16], pl[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 p = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), make_float2(sl, sl), make_float2(mz, mz));
               p.x = ex2(p.x);
               p.y = ex2(p.y);
               sum[e & 1] = add2(sum[e & 1], p);
-              pv[e] = pack_bf16x2(p.x, p.y);
+              if constexpr (MT == 2) pv[e] = pack_f16x2(p.x, p.y);
+              else split_bf16x2(p, pv[e], pl[e]);
             }
             tmem_st16(t_p + 16 * c, pv);
+            if constexpr (MT == 1) tmem_st16(t_p + KT / 2 + 16 * c, pl);
           }
           l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           if (__any_sync(0xffffffffu, mine && scale != 1.f)) {
@@ -766,7 +789,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     const bool s_warp = warp >= C::W_S && warp < C::W_S + MT;
     const int t = s_warp ? warp - C::W_S : warp - C::W_PV;
     const bool one = elect();
-    constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D);
+    constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D, MT == 1);
     const int full = s_warp ? C::B_READY : MT == 2 ? C::B_VREADY : C::B_VFULL, empty = s_warp ? C::B_KEMPTY : C::B_VEMPTY;
     uint32_t gt = 0, ct = 0, qi = 0;   // tiles of the CTA, of the MMA tile; items of it
     bool ok = true;
@@ -797,20 +820,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         ok = ok && (s_warp ? wait_all(C::B_SFREE + t, (ct + 1) & 1) : wait_all(C::B_PREADY + t * NBP + b, (ct / NBP) & 1));
         if (!ok) break;
         fence_after();
-        const uint32_t buf = tmem + 128 * t + (s_warp ? C::TM_S : C::TM_P + KT / 2 * b);
+        const uint32_t buf = tmem + 128 * t + (s_warp ? C::TM_S : C::TM_P + C::PW * b);
         if (one) {
           if (s_warp) {
-            const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_BYTES);
+            const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_STAGE);
             umma_ss<false>(buf, qd, kd, id_s);
 #pragma unroll
-            for (int k = 1; k < D / 16; ++k)  // 16 dims: 32 bytes; 64 dims: a half
-              umma_ss<true>(buf, qd + (k >> 2) * (16384 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
+            for (int k = 1; k < D / 8; ++k) { // 16 dims: 32 bytes; 64 dims: a half; then the same for K's second part
+              const int e = k % (D / 16);
+              umma_ss<true>(buf, qd + (e >> 2) * (16384 / 16) + 2 * (e & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
+            }
           } else {
             const bool first = j == 0 && (flags & kFirst);
-            const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, 2048);
+            const uint32_t vd = desc_lo(base + C::OFF_V + st * C::K_BYTES, C::V_HALF);
 #pragma unroll
             for (int k = 0; k < KP; ++k)      // 16 keys: a page
-              umma_ts(tmem + D * t, buf + 8 * k, vd + k * (C::PAGE_BYTES / 16), id_pv, !first || k != 0);
+              umma_ts(tmem + D * t, buf + 8 * k, vd + k * (C::V_PAGE / 16), id_pv, !first || k != 0);
+            if constexpr (MT == 1) {          // P's second part
+#pragma unroll
+              for (int k = 0; k < KP; ++k)
+                umma_ts(tmem + D * t, buf + KT / 2 + 8 * k, vd + k * (C::V_PAGE / 16), id_pv, 1);
+            }
           }
           umma_commit(bar(s_warp ? C::B_SFULL + t : C::B_PVDONE + t * NBP + b));
           umma_commit(bar(empty + st));
@@ -832,6 +862,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     }
   } else if (warp == C::W_META || warp == C::W_LOAD) {
     // =============================== window records; q of the items into the A operands, V
+    if (MT == 2 && warp == C::W_LOAD) asm volatile("griddepcontrol.wait;" ::: "memory");   // V
     // Lane i holds page i of a window. `next`: the tables' entries of the window after the last one
     // written (the same item's or the next one's), on their way.
     Walk w;
@@ -946,11 +977,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (lane == 0) ok = gt < NV || wait(C::B_VEMPTY + st, (gt / NV - 1) & 1);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        const bool live = lane / KP == i && pg.z != 0;
-        const unsigned who = __ballot_sync(0xffffffffu, live);
-        if (lane == 0) mbar_expect_tx(bar(C::B_VFULL + st), (uint32_t)__popc(who) * C::PAGE_BYTES);
-        __syncwarp();
-        if (live) tma_4d(base + C::OFF_V + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.vmap, 0, 0, pg.x, bar(C::B_VFULL + st));
+        if constexpr (MT == 2) {
+          const int slot = 2 * a.krot_slots + __shfl_sync(0xffffffffu, pg.w, i * KP);
+          if (lane == 0) mbar_expect_tx(bar(C::B_VFULL + st), C::K_BYTES);
+          __syncwarp();
+          if (lane < D / 64)
+            tma_5d(base + C::OFF_V + st * C::K_BYTES + lane * (KT * 128), &ta.kmap, lane, g, slot, bar(C::B_VFULL + st));
+        } else {
+          const bool live = lane / KP == i && pg.z != 0;
+          const unsigned who = __ballot_sync(0xffffffffu, live);
+          if (lane == 0) mbar_expect_tx(bar(C::B_VFULL + st), (uint32_t)__popc(who) * C::PAGE_BYTES);
+          __syncwarp();
+          if (live) tma_4d(base + C::OFF_V + st * C::K_BYTES + lane % KP * C::PAGE_BYTES, &ta.vmap, 0, 0, pg.x, bar(C::B_VFULL + st));
+        }
         ++gt;
       }
     }
@@ -993,10 +1032,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (!ok) break;
         if constexpr (MT == 2) {
           const int slot = __shfl_sync(0xffffffffu, pg.w, i * KP);
-          if (lane == 0) mbar_expect_tx(bar(C::B_READY + st), C::K_BYTES);
+          if (lane == 0) mbar_expect_tx(bar(C::B_READY + st), C::K_STAGE);
           __syncwarp();
-          if (lane < D / 64)
-            tma_5d(base + C::OFF_K + st * C::K_BYTES + lane * (KT * 128), &ta.kmap, lane, g, slot, bar(C::B_READY + st));
+          if (lane < D / 32)
+            tma_5d(base + C::OFF_K + st * C::K_STAGE + lane * (KT * 128), &ta.kmap, lane % (D / 64), g,
+                   slot + (lane < D / 64 ? 0 : a.krot_slots), bar(C::B_READY + st));
         } else {
           const bool live = !end && lane / KP == i && pg.z != 0;
           const unsigned who = __ballot_sync(0xffffffffu, live);
@@ -1073,7 +1113,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       if (sEnd[sx]) break;
       const uint8_t* xs = sm + C::OFF_X + sx * C::K_BYTES;
       const float4* cs = reinterpret_cast<const float4*>(sm + C::OFF_CS + (sx * KP + p) * C::CS_ROW) + c;
-      uint4 w1[NP], w2[NP];
+      uint4 w1[NP], w2[NP], z1[NP], z2[NP];
       float4 f[4];       // (cos, sin) of P theta
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
@@ -1086,22 +1126,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       for (int u = 0; u < NP; ++u) {
         uint32_t* a1 = reinterpret_cast<uint32_t*>(&w1[u]);
         uint32_t* a2 = reinterpret_cast<uint32_t*>(&w2[u]);
+        uint32_t* b1 = reinterpret_cast<uint32_t*>(&z1[u]);
+        uint32_t* b2 = reinterpret_cast<uint32_t*>(&z2[u]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 k = make_float2(__uint_as_float(a1[e] << 16), __uint_as_float(a1[e] & 0xffff0000u));
           const float2 z = make_float2(__uint_as_float(a2[e] << 16), __uint_as_float(a2[e] & 0xffff0000u));
           const float2 y = fma2(make_float2(-z.x, -z.y), os[u][e], mul2(k, oc[u][e])), x = fma2(k, os[u][e], mul2(z, oc[u][e]));
-          a1[e] = pack_f16x2(y.x * f[e].x - x.x * f[e].y, y.y * f[e].z - x.y * f[e].w);
-          a2[e] = pack_f16x2(x.x * f[e].x + y.x * f[e].y, x.y * f[e].z + y.y * f[e].w);
+          split_f16x2(make_float2(y.x * f[e].x - x.x * f[e].y, y.y * f[e].z - x.y * f[e].w), a1[e], b1[e]);
+          split_f16x2(make_float2(x.x * f[e].x + y.x * f[e].y, x.y * f[e].z + y.y * f[e].w), a2[e], b2[e]);
         }
       }
       ok = __all_sync(0xffffffffu, wait(C::B_KEMPTY + sk, pk));   // the first round's waits return at once
       if (!ok) break;
-      uint8_t* ks = sm + C::OFF_K + sk * C::K_BYTES;
+      uint8_t* ks = sm + C::OFF_K + sk * C::K_STAGE;
 #pragma unroll
       for (int u = 0; u < NP; ++u) {
         *reinterpret_cast<uint4*>(ks + k1 + u * RS * 128) = w1[u];
         *reinterpret_cast<uint4*>(ks + k2 + u * RS * 128) = w2[u];
+        *reinterpret_cast<uint4*>(ks + C::K_BYTES + k1 + u * RS * 128) = z1[u];
+        *reinterpret_cast<uint4*>(ks + C::K_BYTES + k2 + u * RS * 128) = z2[u];
       }
       fence_async_smem();   // the MMAs read these rows through the async proxy, TMA rewrites the raw ones
       __syncwarp();
@@ -1176,7 +1220,7 @@ bool cs_map(CUtensorMap* m, const BatchArgs& a) {
 // one half of four neighbouring pages, landing as [key][128 B].
 bool krot_map(CUtensorMap* m, const BatchArgs& a) {
   auto enc = encode_fn();
-  const cuuint64_t dims[5] = {64, (cuuint64_t)kPage, (cuuint64_t)(a.D / 64), (cuuint64_t)a.v.G, (cuuint64_t)a.krot_slots};
+  const cuuint64_t dims[5] = {64, (cuuint64_t)kPage, (cuuint64_t)(a.D / 64), (cuuint64_t)a.v.G, 3 * (cuuint64_t)a.krot_slots};
   const cuuint64_t strides[4] = {(cuuint64_t)a.D * 2, 128, (cuuint64_t)kPage * a.D * 2, (cuuint64_t)a.v.G * kPage * a.D * 2};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1}, box[5] = {64, kPage, 1, 1, KP};
   return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, a.krot, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1203,9 +1247,13 @@ pic_status launch(const TcArgs& ta, cudaStream_t st) {
   return PIC_OK;
 }
 
-// K of every page that some row of the batch sees (or of the prefix), rotated to its keys' positions,
-// bf16 -> fp16, [slot][G][16][D]. One CTA a page: a thread has one row and 8 pairs of dims, and takes
-// their table entries once for all KV heads. HBM-bound: K read and written once.
+// K of every page that some row of the batch sees (or of the prefix), rotated to its keys' positions, as fp16,
+// then what that leaves out, then V (bf16 -> fp16, exact within fp16's range), each [slot][G][16][D]. One CTA
+// a page: a thread has one row and 8 pairs of dims, and takes their table entries once for all KV heads.
+// HBM-bound: K and V read once, three such arrays written.
+__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t x) {
+  return pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
 template <int D>
 __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant__ BatchArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1232,23 +1280,32 @@ __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant
   float4 f[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[e] = cs[e];
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.k_layer) + (size_t)pm.blk * v.G * kPage * D + row * D + 8 * c;
+  const size_t from = (size_t)pm.blk * v.G * kPage * D + row * D + 8 * c, part = (size_t)a.krot_slots * v.G * kPage * D / 8;   // uint4 of an array
+  const __nv_bfloat16 *src = static_cast<const __nv_bfloat16*>(a.k_layer) + from, *vsrc = static_cast<const __nv_bfloat16*>(a.v_layer) + from;
   __half* dst = a.krot + (size_t)blockIdx.x * v.G * kPage * D + row * D + 8 * c;
 #pragma unroll 2
   for (int g = g0; g < v.G; g += HP) {
     const uint4 u1 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D);
     const uint4 u2 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D + D / 2);
     const uint32_t a1[4] = {u1.x, u1.y, u1.z, u1.w}, a2[4] = {u2.x, u2.y, u2.z, u2.w};
-    uint32_t o1[4], o2[4];
+    uint32_t o1[4], o2[4], p1[4], p2[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float q0 = __uint_as_float(a1[e] << 16), q1 = __uint_as_float(a1[e] & 0xffff0000u);
       const float z0 = __uint_as_float(a2[e] << 16), z1 = __uint_as_float(a2[e] & 0xffff0000u);
-      o1[e] = pack_f16x2(q0 * f[e].x - z0 * f[e].y, q1 * f[e].z - z1 * f[e].w);
-      o2[e] = pack_f16x2(z0 * f[e].x + q0 * f[e].y, z1 * f[e].z + q1 * f[e].w);
+      split_f16x2(make_float2(q0 * f[e].x - z0 * f[e].y, q1 * f[e].z - z1 * f[e].w), o1[e], p1[e]);
+      split_f16x2(make_float2(z0 * f[e].x + q0 * f[e].y, z1 * f[e].z + q1 * f[e].w), o2[e], p2[e]);
     }
-    *reinterpret_cast<uint4*>(dst + (size_t)g * kPage * D) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    *reinterpret_cast<uint4*>(dst + (size_t)g * kPage * D + D / 2) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    uint4* d1 = reinterpret_cast<uint4*>(dst + (size_t)g * kPage * D);
+    uint4* d2 = reinterpret_cast<uint4*>(dst + (size_t)g * kPage * D + D / 2);
+    d1[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    d2[0] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    d1[part] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+    d2[part] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+    const uint4 v1 = *reinterpret_cast<const uint4*>(vsrc + (size_t)g * kPage * D);
+    const uint4 v2 = *reinterpret_cast<const uint4*>(vsrc + (size_t)g * kPage * D + D / 2);
+    d1[2 * part] = make_uint4(f16_of_bf16(v1.x), f16_of_bf16(v1.y), f16_of_bf16(v1.z), f16_of_bf16(v1.w));
+    d2[2 * part] = make_uint4(f16_of_bf16(v2.x), f16_of_bf16(v2.y), f16_of_bf16(v2.z), f16_of_bf16(v2.w));
   }
 }
 
