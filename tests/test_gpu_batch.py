@@ -7,8 +7,9 @@ rows, NaN in every place that must not be read, rows and tables that must stay a
 Tolerances are worst cases of the roundings (half a step: eps / 2 of the type, relative):
 * fp32: a dot product of D terms is within (D + 8) 2^-24 sum|q k|; a softmax weight's relative error
   is twice that of its score, and the output adds (N + 8) 2^-24 for N keys.
-* bf16 pools: rotated K rounds to fp16 (2^-11 of each term), the weights to bf16 (2^-8; a weight's
-  rounding enters its product with V but not the denominator), the output to fp16 (2^-11).
+* bf16 pools: rotated K is held as two fp16 numbers (each term within 2^-22, or within 2^-25 where the second one
+  is below fp16's normal range), the weights as two bf16 numbers (2^-16) or one fp16 number (2^-11), which enters
+  the product with V but not the denominator, the output in fp16 (2^-11).
 """
 import numpy as np
 import pytest
@@ -148,14 +149,15 @@ class Batch:
             vmax = V.abs().amax().item()
             es = (self.D + 8) * 2.0 ** -24 * A
             if self.half:
-                tol = (2 * (es + 2.0 ** -11 * A) + 2.0 ** -8 + 2.0 ** -11 + (N + 8) * 2.0 ** -24) * vmax
+                qmax = Q.abs().sum(-1).amax().item() / self.D ** 0.5
+                tol = (2 * (es + 2.0 ** -22 * A + 2.0 ** -25 * qmax) + 2 * 2.0 ** -11 + (N + 8) * 2.0 ** -24) * vmax
             else:
                 tol = (2 * es + (N + 8) * 2.0 ** -24) * vmax
             err = (out[t0:t0 + m].double() - ref).abs().amax().item()
             assert err <= tol, (r, kv, m, err, tol)
             # and on average nowhere near it: a wrong key or page would show
             rel = ((out[t0:t0 + m].double() - ref).norm() / ref.norm()).item()
-            assert rel < (8e-3 if self.half else 2e-5), (r, kv, m, rel)
+            assert rel < (7e-4 if self.half else 2e-5), (r, kv, m, rel)
             t0 += m
         assert (out[t0:] == 7.0).all()          # rows behind the last sequence
 
