@@ -1317,9 +1317,9 @@ void batch_tc_view(BatchView& v, bool wide, bool narrow) {
   v.mrows = v.rb * v.rep;
   v.kpages = KP;
   v.whole_tiles = wide;
-  // in eighths of a key tile; from per-CTA times, an item's start and drain take as long as 2.1 to 4.5 key tiles.
-  // Per item 24, 17, 24 instead: prefill 137 us for 135, prefix of 64 requests 74 for 72; 40, 25, 32: 148 and 73
-  v.cost_item = wide ? 28 : narrow ? 32 : 21;
+  // in eighths of a key tile; from per-CTA times, an item's start and drain take as long as 2 to 4.5 key tiles.
+  // (28, 18, 20 instead: one request's window 21.7 us for 19.2, two prompts 175 us for 166.)
+  v.cost_item = wide ? 24 : narrow ? 32 : 17;
   v.cost_full = 8;
   v.cost_half = wide ? 6 : 8;
 }
