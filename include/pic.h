@@ -459,7 +459,8 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  * too few free blocks (pic_sync: PIC_ERR_OUT_OF_BLOCKS), a table row or max_rows too short
  * (PIC_ERR_CAPACITY) or lengths that do not fit together (PIC_ERR_INVALID_ARG) no table changes,
  * the lengths come out as they went in, there are no rows, and counts[2] is not 0.
- * At most 12288 requests (PIC_ERR_CAPACITY). One launch. */
+ * At most 12288 requests and tables of fewer than 2^26 entries a request (PIC_ERR_CAPACITY). One launch, two
+ * with max_rows above 4096. */
 pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int32_t* new_len, int32_t* block_table,
                                int32_t table_stride, int32_t* page_pos, const int32_t* n_pages,
                                const int32_t* free_blocks, int32_t n_free, const int32_t* free_used, int32_t first,
@@ -472,7 +473,7 @@ pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int3
  * (sqrt(mean(x^2) + eps) over the head) times q_gain / k_gain ([head_dim], NULL: no norm);
  * q_out[t][h] = RoPE(q, row_pos[t]) in fp16 for bf16 pools, fp32 for fp32 pools; k (before RoPE)
  * and v go to slot row_slot[t] of one layer of the pools. A row with row_slot -1 is padding:
- * nothing of it is read or written. Slots must be distinct. Values bound for fp16 operands are
+ * nothing is written for it. Slots must be distinct. Values bound for fp16 operands are
  * checked against fp16's range as everywhere (PIC_ERR_RANGE from pic_sync). */
 pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                const float* qkv, int64_t qkv_stride, const float* q_gain, const float* k_gain,
@@ -483,7 +484,8 @@ pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_
 /* Scratch of the two attention calls below; prefix_len and prefix_pages 0 for
  * pic_op_attention_window. 0 for shapes they refuse. The scratch need not be initialised and is
  * free again when the call's work is done. (bf16 batches with many rows per request, or behind
- * a prefix, keep the rotated K of their pages in it: up to 1 GB for each.) */
+ * a prefix, keep the rotated K of their pages and V as fp16 in it: up to 1 GB for each.) It depends on the
+ * current device's number of SMs. */
 size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_reqs, int32_t n_heads,
                                             int32_t n_kv_heads, int32_t head_dim, int32_t table_stride,
                                             int32_t prefix_len, int32_t prefix_pages);
@@ -492,8 +494,13 @@ size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_
  * position p sees key u of its request when u <= p and (u > p - window or u < sinks); window 0:
  * every key up to p. out[t][h] = softmax_u(q[t][h] . RoPE(K[u][g]) / sqrt(head_dim)) V[u][g],
  * g = h / (n_heads / n_kv_heads). q: [T][n_heads][head_dim], rotated (pic_op_qk_norm_rope), fp16
- * for bf16 pools, fp32 for fp32 pools; out likewise. Pages that no row sees are not read. Rows
- * from row_start[n_reqs] on stay as they were. */
+ * for bf16 pools, fp32 for fp32 pools; out likewise. Pages that no row sees are not read, pool rows that hold
+ * no key may hold anything. V of every key that some row of the request sees must be finite (rows are computed
+ * together, a key that one of them does not see has weight 0 there) and, in bf16 pools, within fp16's
+ * range (pool writes check it). A row that sees no key gets zeros. Rows from row_start[n_reqs] on stay as they
+ * were. fp32 pools: fp32 arithmetic; bf16 pools: fp32 sums and softmax, operands of the products in 16 to
+ * 22 bits (11 for the weights of many rows), so that rounding the result to fp16 is the largest error. The same
+ * call gives the same bits again. */
 pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                    const void* q, const int32_t* row_start, int32_t n_reqs, const int32_t* kv_len,
                                    const int32_t* block_table, int32_t table_stride, const int32_t* page_pos,

@@ -8,48 +8,55 @@
 //   meta warp   walks the share: reads the page tables a window ahead and writes the windows' records (item,
 //               rows, pages with the rows that hold keys).
 //   load        (the meta warp, or, MT = 2, a warp of its own) asks for the items' rows of q (TMA boxes of 8
-//               tokens x rep heads; double-buffered for one MMA tile, else when the item's last S product has
-//               retired) and for V, one box a page: a page is one K = 16 step of the PV product, so pages need
-//               not be neighbours.
+//               tokens x rep heads, when the item before has had its last S product) and for V: one box a page (a
+//               page is one K = 16 step of the PV product, so pages need not be neighbours), or, MT = 2, two
+//               boxes of four pages of its fp16 copy.
 //   K warp      asks for K, one TMA box a page wherever its block lies, with the RoPE table row of the page's
-//               position. On its own: with the records' work in the same warp K came late (decode batch below
-//               132 us instead of 112).
+//               position. On its own: with the records' work in the same warp K came late (the decode batch
+//               below took 18 % longer).
 //   rotation    (MT = 1) turns raw K into the fp16 operand: thread = two rows of a page x 8 pairs of dims; the
 //               key in row r of a page at position P is turned by the angle of r (registers) and then by that
 //               of P (shared memory, one table row a page), pairs of fp32 at a time, so that a key needs no
-//               table row of its own. One rounding, bf16 -> fp16 (Q and K as fp16: 3 bits more than bf16 in S).
+//               table row of its own.
 //   V mending   rows that hold no key any row of the block sees are zeroed in V (P is 0 there, V must be
 //               finite), by the PV warp or (MT = 2) a warp of its own. K needs none: their S is masked.
-//   S warps     (one per MMA tile) issue S_t = Q_t K^T (fp16) of a key tile as soon as the softmax has the S
-//               before it in registers.
-//   PV warps    (one per MMA tile) issue O_t += P_t V (bf16, P from TMEM). A warp for each product of each tile:
-//               one thread for both products of a tile, S(j + 2) right behind PV(j) in its in-order queue, took
-//               1500 ns a key tile of two MMA tiles where this took 1050. The warp loops as a whole and an
-//               elected lane issues: operands stay in uniform registers (two prompts below 155 -> 149 us).
+//   S warps     (one per MMA tile) issue S_t = Q_t K^T of a key tile as soon as the softmax has the S before
+//               it in registers.
+//   PV warps    (one per MMA tile) issue O_t += P_t V (P from TMEM). A warp for each product of each tile: one
+//               thread for both products of a tile, S(j + 2) right behind PV(j) in its in-order queue, took half as
+//               long again. The warp loops as a whole and an elected lane issues: operands stay in uniform
+//               registers (4 to 10 % of a call).
 //   softmax     warpgroup t = MMA tile t, thread = row: mask, running maximum (O in TMEM is rescaled
-//               only when it grows by more than 2^8), P = 2^(S - ref) as bf16 into one of two P buffers
-//               (V is stored bf16 and both operands have one type; the sum is of the unrounded
-//               fp32 weights), and the item's result: out, or for parts of items and for prefix
+//               only when it grows by more than 2^8), P = 2^(S - ref) into one of two P buffers, the sum of the
+//               unrounded fp32 weights, and the item's result: out, or for parts of items and for prefix
 //               batches the normalized fp32 row with its maximum and sum for the merge.
 //   narrow      (single decoded tokens) the four softmax warps have the same rows, at MMA rows 32 w (q is loaded
 //               four times), and one page of each key tile each, with zero P for the others: one warp's 64
-//               columns a tile would take longer than anything else (112 us instead of 106). Their four O's, with
-//               maxima and sums of their own, are joined through shared memory at the item's end. A kernel of its
-//               own: both softmaxes in one cost either 5 % (instruction cache).
+//               columns a tile would take longer than anything else. Their four O's, with maxima and sums of
+//               their own, are joined through shared memory at the item's end. A kernel of its own: both
+//               softmaxes in one cost either 5 % (instruction cache).
+//
+// Roundings. The result is fp16; what comes before it is held to fewer than half that rounding. Rotated K is two
+// fp16 numbers (22 bits), S the sum of both products: with one (11 bits, error of a score about 3e-4 at scores of
+// order 1) the result's error was twice that of its rounding alone. P is two bf16 numbers (16 bits; V is stored bf16,
+// and both operands of a product have one type) in two PV products, or, MT = 2, where the products bound the
+// time, one fp16 number with V as fp16 (exact within fp16's range, which pool writes flag). Error against
+// 64 bits relative to the result's norm: 2.1e-4, that of rounding it; MT = 2: 2.7e-4 to 2.9e-4. One fp16 K and one
+// bf16 P: 1.7e-3, and 16 to 20 % faster.
 //
 // The roles' loops are kept small, and few on each scheduler: with three times the code every role ran
 // at 8 cycles an instruction (ncu: no_instruction the largest stall).
 //
-// MT = 1: few rows, HBM-bound; K is rotated on its way. MT = 2: many rows; K has been rotated
-// ahead, once per page, into a scratch (batch_rotate_kernel) and comes as two boxes of four pages.
-// Rotating it here instead, for every 256 rows anew, kept the schedulers busier than the MMAs (2900
-// cycles a key tile against 1300).
+// MT = 1: few rows, K is rotated on its way. MT = 2: many rows; K has been rotated ahead, once per page, into a
+// scratch (batch_rotate_kernel). Rotating it here instead, for every 256 rows anew, kept the schedulers busier
+// than the MMAs.
 //
 // Measured, 8 KV heads of 4 query heads, D = 128, whole call: 32 decoding requests of 3000 to 32000 keys, window
-// 4096 (0.53 GB of K and V): 104 us, 5.1 TB/s, 650 to 800 ns a key tile (21 us of it start, item ends and merge).
-// Two prompts of 4096, window 1024 (123 GFLOP): 135 us, 0.91 PFLOP/s; 810 ns a key tile of two MMA tiles, whose MMAs take
-// 550: the rest is the way S -> registers -> next S (issue 370 cycles, product to softmax 830, read 150,
-// softmax to S warp 300), for which TMEM has no second S buffer.
+// 4096 (0.53 GB of K and V): 124 us, 4.3 TB/s, about 900 ns a key tile of 64; tensor pipe 50 % busy, issue slots
+// 47 %: the roles' waits for one another bound it. Without K's second product 115 us, without the rotation's arithmetic
+// 119, without P's second product 121. Two prompts of 4096, window 1024 (123 GFLOP by the formula, 186 issued): 166 us,
+// 0.74 PFLOP/s of the formula's; tensor pipe 58 %: the way S -> registers -> next S, for which TMEM has no second S
+// buffer (P in S's place, with two of each, took 169 us).
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
