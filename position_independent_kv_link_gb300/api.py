@@ -410,31 +410,21 @@ _I32, _F32 = torch.int32, torch.float32
 
 
 def _refuse(x, what: str, dtype, want, idx: int):
-    raise ValueError(f"{what}: a contiguous {dtype} device tensor {want} on cuda:{idx} is needed, got {x.dtype} "
+    raise ValueError(f"{what}: a contiguous {dtype} device tensor {list(want)} on cuda:{idx} is needed, got {x.dtype} "
                      f"{list(x.shape)} (strides {list(x.stride())}) on {x.device}")
 
 
-def _vec(x: torch.Tensor, what: str, dtype, n: int, idx: int) -> int:
-    """The address of a contiguous tensor [n] (n < 0: any length) of this type on device idx."""
-    if x.dtype is not dtype or x.get_device() != idx or x.dim() != 1 or (n >= 0 and x.size(0) != n) or \
-            not x.is_contiguous():
-        _refuse(x, what, dtype, f"[{n if n >= 0 else '?'}]", idx)
+def _ptr(x: torch.Tensor, what: str, dtype, shape: tuple, idx: int) -> int:
+    """The address of a contiguous tensor of this type and shape on device idx."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != idx or not x.is_contiguous():
+        _refuse(x, what, dtype, shape, idx)
     return x.data_ptr()
 
 
-def _mat(x: torch.Tensor, what: str, n: int, m: int, idx: int) -> int:
-    """The same for int32 [n, m]."""
-    if x.dtype is not _I32 or x.get_device() != idx or x.dim() != 2 or x.size(0) != n or x.size(1) != m or \
-            not x.is_contiguous():
-        _refuse(x, what, _I32, f"[{n}, {m}]", idx)
-    return x.data_ptr()
-
-
-def _cube(x: torch.Tensor, what: str, dtype, n: int, m: int, k: int, idx: int) -> int:
-    """The same for [n, m, k] (n < 0: any)."""
-    if x.dtype is not dtype or x.get_device() != idx or x.dim() != 3 or (n >= 0 and x.size(0) != n) or \
-            x.size(1) != m or x.size(2) != k or not x.is_contiguous():
-        _refuse(x, what, dtype, f"[{n if n >= 0 else '?'}, {m}, {k}]", idx)
+def _vec(x: torch.Tensor, what: str, dtype, idx: int) -> int:
+    """The same for [n] of any n."""
+    if x.dtype is not dtype or x.dim() != 1 or x.get_device() != idx or not x.is_contiguous():
+        _refuse(x, what, dtype, ("n",), idx)
     return x.data_ptr()
 
 
@@ -458,7 +448,7 @@ def _call(idx: int, stream: Optional[torch.cuda.Stream], f, *args):
         raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == idx:
+    if torch._C._cuda_getDevice() == idx:
         status = f(*args, handle)
     else:
         with torch.cuda.device(idx):
@@ -479,10 +469,12 @@ class BatchPages:
 
     def _args(self, idx: int):
         kv, table, pos, np_ = self.kv_len, self.block_table, self.page_pos, self.n_pages
-        n, stride = kv.size(0) if kv.dim() == 1 else -1, table.size(1) if table.dim() == 2 else -1
-        return n, (_vec(kv, "kv_len", _I32, n, idx), _mat(table, "block_table", n, stride, idx), stride,
-                   None if pos is None else _mat(pos, "page_pos", n, stride, idx),
-                   None if np_ is None else _vec(np_, "n_pages", _I32, n, idx))
+        n, both = len(kv), table.shape
+        if len(both) != 2 or both[0] != n:
+            _refuse(table, "block_table", _I32, (n, "stride"), idx)
+        return n, (_vec(kv, "kv_len", _I32, idx), _ptr(table, "block_table", _I32, both, idx), both[1],
+                   None if pos is None else _ptr(pos, "page_pos", _I32, both, idx),
+                   None if np_ is None else _ptr(np_, "n_pages", _I32, (n,), idx))
 
 
 class BlockTables:
@@ -508,14 +500,15 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     block_table (and page_pos) in place. `out`: tensors to write (out.kv_len may be kv_len, out.n_pages n_pages,
     and free_used out.counts[1:2])."""
     idx = _device_index(kv_len)
-    n = kv_len.size(0) if kv_len.dim() == 1 else -1
-    stride = block_table.size(1) if block_table.dim() == 2 else -1
-    args = (n, _vec(kv_len, "kv_len", _I32, n, idx), _vec(new_len, "new_len", _I32, n, idx),
-            _mat(block_table, "block_table", n, stride, idx), stride,
-            None if page_pos is None else _mat(page_pos, "page_pos", n, stride, idx),
-            None if n_pages is None else _vec(n_pages, "n_pages", _I32, n, idx),
-            _vec(free_blocks, "free_blocks", _I32, -1, idx), free_blocks.size(0),
-            None if free_used is None else _vec(free_used, "free_used", _I32, 1, idx), first, max_rows)
+    n, both = len(kv_len), block_table.shape
+    if len(both) != 2 or both[0] != n:
+        _refuse(block_table, "block_table", _I32, (n, "stride"), idx)
+    args = (n, _vec(kv_len, "kv_len", _I32, idx), _ptr(new_len, "new_len", _I32, (n,), idx),
+            _ptr(block_table, "block_table", _I32, both, idx), both[1],
+            None if page_pos is None else _ptr(page_pos, "page_pos", _I32, both, idx),
+            None if n_pages is None else _ptr(n_pages, "n_pages", _I32, (n,), idx),
+            _vec(free_blocks, "free_blocks", _I32, idx), len(free_blocks),
+            None if free_used is None else _ptr(free_used, "free_used", _I32, (1,), idx), first, max_rows)
     if out is None:
         if max_rows < 1:
             raise ValueError("max_rows must be at least 1")
@@ -526,10 +519,10 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
                 at + 12 * n + 4 + 8 * max_rows)
         out = BlockTables(*buf.split_with_sizes([n, n, n + 1, max_rows, max_rows, 3]))
     else:
-        ptrs = (_vec(out.kv_len, "out.kv_len", _I32, n, idx), _vec(out.n_pages, "out.n_pages", _I32, n, idx),
-                _vec(out.row_start, "out.row_start", _I32, n + 1, idx),
-                _vec(out.row_pos, "out.row_pos", _I32, max_rows, idx),
-                _vec(out.row_slot, "out.row_slot", _I32, max_rows, idx), _vec(out.counts, "out.counts", _I32, 3, idx))
+        ptrs = (_ptr(out.kv_len, "out.kv_len", _I32, (n,), idx), _ptr(out.n_pages, "out.n_pages", _I32, (n,), idx),
+                _ptr(out.row_start, "out.row_start", _I32, (n + 1,), idx),
+                _ptr(out.row_pos, "out.row_pos", _I32, (max_rows,), idx),
+                _ptr(out.row_slot, "out.row_slot", _I32, (max_rows,), idx), _ptr(out.counts, "out.counts", _I32, (3,), idx))
     _call(idx, stream, L.load().pic_op_block_tables, *args, *ptrs)
     return out
 
@@ -545,12 +538,10 @@ def _pool_args(k_layer, v_layer, rope, idx):
         dt, act = L.PIC_F32, _F32
     else:
         raise ValueError(f"unsupported dtype {t}")
-    if k_layer.get_device() != idx or not k_layer.is_contiguous():
-        _refuse(k_layer, "k_layer", t, list(shape), idx)
-    if v_layer.dtype is not t or v_layer.get_device() != idx or v_layer.shape != shape or not v_layer.is_contiguous():
-        _refuse(v_layer, "v_layer", t, list(shape), idx)
-    return (nb, G, D, dt, act, k_layer.data_ptr(), v_layer.data_ptr(), _cube(rope, "rope", _F32, -1, D // 2, 2, idx),
-            rope.size(0))
+    if len(rope.shape) != 3 or rope.shape[1:] != (D // 2, 2):
+        _refuse(rope, "rope", _F32, ("positions", D // 2, 2), idx)
+    return (nb, G, D, dt, act, _ptr(k_layer, "k_layer", t, shape, idx), _ptr(v_layer, "v_layer", t, shape, idx),
+            _ptr(rope, "rope", _F32, rope.shape, idx), rope.shape[0])
 
 
 def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torch.Tensor, row_slot: torch.Tensor,
@@ -572,12 +563,12 @@ def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torc
         q_out = torch.empty((T, n_heads, D), dtype=act, device=qkv.device)
         qo = q_out.data_ptr()
     else:
-        qo = _cube(q_out, "q_out", act, T, n_heads, D, idx)
+        qo = _ptr(q_out, "q_out", act, (T, n_heads, D), idx)
     _call(idx, stream, L.load().pic_op_qk_norm_rope, dt, T, n_heads, n_kv_heads, D, qkv.data_ptr(),
           qkv.stride(0) if T > 1 else max(qkv.stride(0), qkv.size(1)),
-          None if q_gain is None else _vec(q_gain, "q_gain", _F32, D, idx),
-          None if k_gain is None else _vec(k_gain, "k_gain", _F32, D, idx), eps,
-          _vec(row_pos, "row_pos", _I32, T, idx), _vec(row_slot, "row_slot", _I32, T, idx), rp, positions, qo, kp, vp, nb)
+          None if q_gain is None else _ptr(q_gain, "q_gain", _F32, (D,), idx),
+          None if k_gain is None else _ptr(k_gain, "k_gain", _F32, (D,), idx), eps,
+          _ptr(row_pos, "row_pos", _I32, (T,), idx), _ptr(row_slot, "row_slot", _I32, (T,), idx), rp, positions, qo, kp, vp, nb)
     return q_out
 
 
@@ -591,23 +582,24 @@ def _attention_scratch(idx, *shape) -> int:
 def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len, prefix_pages):
     idx = _device_index(q)
     nb, G, D, dt, act, kp, vp, rp, positions = _pool_args(k_layer, v_layer, rope, idx)
-    if q.dim() != 3:
-        raise ValueError(f"q is [rows, n_heads, head_dim], got {list(q.shape)}")
-    T, H = q.size(0), q.size(1)
-    qp = _cube(q, "q", act, T, H, D, idx)
+    rows = q.shape
+    if len(rows) != 3 or rows[2] != D:
+        raise ValueError(f"q is [rows, n_heads, {D}], got {list(rows)}")
+    T, H, _ = rows
+    qp = _ptr(q, "q", act, rows, idx)
     n, pg = pages._args(idx)
     if out is None:
         out = torch.empty_like(q)
         op = out.data_ptr()
     else:
-        op = _cube(out, "out", act, T, H, D, idx)
+        op = _ptr(out, "out", act, rows, idx)
     if scratch is None:
         nbytes = _attention_scratch(idx, dt, T, n, H, G, D, pg[2], prefix_len, prefix_pages)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         sp = scratch.data_ptr()
     else:
-        sp, nbytes = _vec(scratch, "scratch", torch.uint8, -1, idx), scratch.size(0)
-    return idx, out, scratch, (dt, T, H, G, D, qp, _vec(row_start, "row_start", _I32, n + 1, idx)), n, pg, \
+        sp, nbytes = _vec(scratch, "scratch", torch.uint8, idx), len(scratch)
+    return idx, out, scratch, (dt, T, H, G, D, qp, _ptr(row_start, "row_start", _I32, (n + 1,), idx)), n, pg, \
         (kp, vp, nb, rp, positions, op, sp, nbytes)
 
 
@@ -632,9 +624,9 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     """Attention of a batch whose requests share the prefix_len first positions (pic_op_attention_prefix): the pages
     prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
-    n_pre = prefix_blocks.size(0) if prefix_blocks.dim() == 1 else -1
+    n_pre = len(prefix_blocks)
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
                                                             prefix_len, n_pre)
-    _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, n_pre, idx),
-          None if prefix_pos is None else _vec(prefix_pos, "prefix_pos", _I32, n_pre, idx), n_pre, prefix_len, n, *pg, *tail)
+    _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, idx),
+          None if prefix_pos is None else _ptr(prefix_pos, "prefix_pos", _I32, (n_pre,), idx), n_pre, prefix_len, n, *pg, *tail)
     return out
