@@ -496,8 +496,8 @@ size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_
  * g = h / (n_heads / n_kv_heads). q: [T][n_heads][head_dim], rotated (pic_op_qk_norm_rope), fp16
  * for bf16 pools, fp32 for fp32 pools; out likewise. Pages that no row sees are not read, pool rows that hold
  * no key may hold anything. V of every key that some row of the request sees must be finite (rows are computed
- * together, a key that one of them does not see has weight 0 there) and, in bf16 pools, within fp16's
- * range (pool writes check it). A row that sees no key gets zeros. Rows from row_start[n_reqs] on stay as they
+ * together, a key that one of them does not see has weight 0 there); K and V in bf16 pools lie within fp16's
+ * range (pool writes check it). out must not overlap q. A row that sees no key gets zeros. Rows from row_start[n_reqs] on stay as they
  * were. fp32 pools: fp32 arithmetic; bf16 pools: fp32 sums and softmax, operands of the products in 16 to
  * 22 bits (11 for the weights of many rows), so that rounding the result to fp16 is the largest error. The same
  * call gives the same bits again. */

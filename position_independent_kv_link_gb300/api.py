@@ -469,7 +469,7 @@ class BatchPages:
 
     def _args(self, idx: int):
         kv, table, pos, np_ = self.kv_len, self.block_table, self.page_pos, self.n_pages
-        n, both = len(kv), table.shape
+        n, both = kv.numel(), table.shape
         if len(both) != 2 or both[0] != n:
             _refuse(table, "block_table", _I32, (n, "stride"), idx)
         return n, (_vec(kv, "kv_len", _I32, idx), _ptr(table, "block_table", _I32, both, idx), both[1],
@@ -500,14 +500,14 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     block_table (and page_pos) in place. `out`: tensors to write (out.kv_len may be kv_len, out.n_pages n_pages,
     and free_used out.counts[1:2])."""
     idx = _device_index(kv_len)
-    n, both = len(kv_len), block_table.shape
+    n, both = kv_len.numel(), block_table.shape
     if len(both) != 2 or both[0] != n:
         _refuse(block_table, "block_table", _I32, (n, "stride"), idx)
     args = (n, _vec(kv_len, "kv_len", _I32, idx), _ptr(new_len, "new_len", _I32, (n,), idx),
             _ptr(block_table, "block_table", _I32, both, idx), both[1],
             None if page_pos is None else _ptr(page_pos, "page_pos", _I32, both, idx),
             None if n_pages is None else _ptr(n_pages, "n_pages", _I32, (n,), idx),
-            _vec(free_blocks, "free_blocks", _I32, idx), len(free_blocks),
+            _vec(free_blocks, "free_blocks", _I32, idx), free_blocks.numel(),
             None if free_used is None else _ptr(free_used, "free_used", _I32, (1,), idx), first, max_rows)
     if out is None:
         if max_rows < 1:
@@ -598,7 +598,7 @@ def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         sp = scratch.data_ptr()
     else:
-        sp, nbytes = _vec(scratch, "scratch", torch.uint8, idx), len(scratch)
+        sp, nbytes = _vec(scratch, "scratch", torch.uint8, idx), scratch.numel()
     return idx, out, scratch, (dt, T, H, G, D, qp, _ptr(row_start, "row_start", _I32, (n + 1,), idx)), n, pg, \
         (kp, vp, nb, rp, positions, op, sp, nbytes)
 
@@ -624,7 +624,7 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     """Attention of a batch whose requests share the prefix_len first positions (pic_op_attention_prefix): the pages
     prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
-    n_pre = len(prefix_blocks)
+    n_pre = prefix_blocks.numel()
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
                                                             prefix_len, n_pre)
     _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, idx),

@@ -59,6 +59,7 @@ def test_block_tables_refuse(lib, i, x):
 
 def test_block_tables_capacity(lib):
     assert lib.pic_op_block_tables(12289, A, A, A, 4, None, None, A, 4, None, 0, 8, A, A, A, A, A, A, None) == L.PIC_ERR_CAPACITY
+    assert lib.pic_op_block_tables(1, A, A, A, 1 << 26, None, None, A, 4, None, 0, 8, A, A, A, A, A, A, None) == L.PIC_ERR_CAPACITY
 
 
 @pytest.mark.parametrize("i,x", [(0, 5), (1, 0), (2, 0), (3, 0), (4, 32), (5, None), (5, A + 4), (6, 100), (6, 1538), (7, A + 4),
