@@ -89,7 +89,8 @@ struct Cfg {
   static constexpr int NK = MT == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 3);   // K operand stages
   static constexpr int NV = MT == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);   // V stages
   static constexpr int NR = MT == 2 ? 0 : 8;          // rotation warps
-  static constexpr int Q_TILE = 128 * D * 2, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
+  static constexpr int M = NARROW ? 64 : 128;         // MMA rows: of 64, rows 16 w + i are TMEM lanes 32 w + i
+  static constexpr int Q_TILE = M * D * 2, Q_HALF = M * 128, K_BYTES = KT * D * 2, PAGE_BYTES = kPage * D * 2, CS_ROW = D * 4;
   static constexpr int K_STAGE = 2 * K_BYTES;         // fp16 and what it leaves out
   // V of a tile: [page][64-dim half][16 keys][128 B] (pool pages), MT 2: [half][64 keys][128 B] (scratch pages)
   static constexpr int V_PAGE = MT == 2 ? 2048 : PAGE_BYTES, V_HALF = MT == 2 ? KT * 128 : 2048;
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     const bool s_warp = warp >= C::W_S && warp < C::W_S + MT;
     const int t = s_warp ? warp - C::W_S : warp - C::W_PV;
     const bool one = elect();
-    constexpr uint32_t id_s = idesc_s(128, KT), id_pv = idesc_pv(128, D, MT == 1);
+    constexpr uint32_t id_s = idesc_s(C::M, KT), id_pv = idesc_pv(C::M, D, MT == 1);
     const int full = s_warp ? C::B_READY : MT == 2 ? C::B_VREADY : C::B_VFULL, empty = s_warp ? C::B_KEMPTY : C::B_VEMPTY;
     uint32_t gt = 0, ct = 0, qi = 0;   // tiles of the CTA, of the MMA tile; items of it
     bool ok = true;
@@ -835,7 +836,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
             for (int k = 1; k < D / 8; ++k) { // 16 dims: 32 bytes; 64 dims: a half; then the same for K's second part
               const int e = k % (D / 16);
-              umma_ss<true>(buf, qd + (e >> 2) * (16384 / 16) + 2 * (e & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
+              umma_ss<true>(buf, qd + (e >> 2) * (C::Q_HALF / 16) + 2 * (e & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id_s);
             }
           } else {
             const bool first = j == 0 && (flags & kFirst);
@@ -966,7 +967,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             if (lane == 0) mbar_expect_tx(full, 4 * (D / 64) * v.mrows * 128);
             __syncwarp();
             if (lane < 4 * (D / 64))
-              tma_4d(dst + lane / 4 * 16384 + lane % 4 * 4096, &ta.qmap, g * v.rep, lane / 4, row0, full);
+              tma_4d(dst + lane / 4 * C::Q_HALF + lane % 4 * 2048, &ta.qmap, g * v.rep, lane / 4, row0, full);
             continue;
           }
           const int boxes = pdiv(min(rows - t * tpt, tpt), 8);
@@ -974,7 +975,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           __syncwarp();
           for (int i = lane; i < boxes * (D / 64); i += 32) {
             const int h = i % (D / 64), k = i / (D / 64);
-            tma_4d(dst + h * 16384 + k * 8 * v.rep * 128, &ta.qmap, g * v.rep, h, row0 + t * tpt + 8 * k, full);
+            tma_4d(dst + h * C::Q_HALF + k * 8 * v.rep * 128, &ta.qmap, g * v.rep, h, row0 + t * tpt + 8 * k, full);
           }
         }
       }
