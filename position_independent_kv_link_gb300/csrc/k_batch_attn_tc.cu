@@ -30,8 +30,8 @@
 //               only when it grows by more than 2^8), P = 2^(S - ref) into one of two P buffers, the sum of the
 //               unrounded fp32 weights, and the item's result: out, or for parts of items and for prefix
 //               batches the normalized fp32 row with its maximum and sum for the merge.
-//   narrow      (single decoded tokens) the four softmax warps have the same rows, at MMA rows 32 w (q is loaded
-//               four times), and one page of each key tile each, with zero P for the others: one warp's 64
+//   narrow      (single decoded tokens) the four softmax warps have the same rows, at MMA rows 16 w of tiles of 64
+//               (q is loaded four times; with tiles of 128 rows the tensor pipe took 7 % longer calls), and one page of each key tile each, with zero P for the others: one warp's 64
 //               columns a tile would take longer than anything else. Their four O's, with maxima and sums of
 //               their own, are joined through shared memory at the item's end. A kernel of its own: both
 //               softmaxes in one cost either 5 % (instruction cache).
@@ -52,11 +52,11 @@
 // than the MMAs.
 //
 // Measured, 8 KV heads of 4 query heads, D = 128, whole call: 32 decoding requests of 3000 to 32000 keys, window
-// 4096 (0.53 GB of K and V): 124 us, 4.3 TB/s, about 900 ns a key tile of 64; tensor pipe 50 % busy, issue slots
-// 47 %: the roles' waits for one another bound it. Without K's second product 115 us, without the rotation's arithmetic
-// 119, without P's second product 121. Two prompts of 4096, window 1024 (123 GFLOP by the formula, 186 issued): 166 us,
-// 0.74 PFLOP/s of the formula's; tensor pipe 58 %: the way S -> registers -> next S, for which TMEM has no second S
-// buffer (P in S's place, with two of each, took 169 us).
+// 4096 (0.53 GB of K and V): 116 us, 4.6 TB/s, about 850 ns a key tile of 64; neither HBM, tensor pipe nor issue slots are
+// full: the roles' waits for one another bound it. (With tiles of 128 rows, 124 us: without K's second product 115, without
+// the rotation's arithmetic 119, without P's second product 121.) Two prompts of 4096, window 1024 (121 GFLOP by the
+// formula, 181 issued): 166 us, 0.73 PFLOP/s of the formula's; tensor pipe 58 %: the way S -> registers -> next S, for
+// which TMEM has no second S buffer (P in S's place, with two of each, took 169 us).
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
