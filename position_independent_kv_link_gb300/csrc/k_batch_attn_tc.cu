@@ -662,50 +662,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
       done_with(win);
       if (!(flags & kLast) || n == 0) continue;
       // the item's result
-      float2* ml = reinterpret_cast<float2*>(sm + C::OFF_JOIN);
-      if constexpr (narrow) {
-        if (lane < 16) ml[16 * wq + lane] = make_float2(mref, l);
-        ok = join();
-        if (!ok) break;
-      }
       ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + (ct - 1) % NBP, ((ct - 1) / NBP) & 1));
       if (!ok) break;
       if (idle) continue;
       fence_after();
-      float weight = 1.f;
-      if constexpr (narrow) {              // one maximum and sum for the row's four parts
-        float mx = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, ml[16 * k + lane % 16].x);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = ml[16 * k + lane % 16];
-          sum += x.y * ex2(x.x - ref);
-        }
-        weight = ex2(mref - ref);
-        mref = mx;
-        l = sum;
-      }
-      const float inv = l == 0.f ? 0.f : weight / l;   // no key seen: zeros; NaN stays NaN
       const bool whole = flags & kWhole;
       const size_t head = mine ? (size_t)(row0 + tok) * a.H + g * v.rep + hh : 0;
       __half* dst = nullptr;
       float* po = nullptr;
+      float2* pml = nullptr;
       if (mine) {
         if (whole && v.pre_len == 0) {
           dst = static_cast<__half*>(a.out) + head * D;
         } else {
           const size_t at = whole ? (req < 0 ? 0 : (size_t)v.T * a.H) + head : (size_t)slot * a.part_rows + tok * v.rep + hh;
           po = (whole ? a.seg_o : a.part_o) + at * D;
-          if (!narrow || wq == 0) (whole ? a.seg_ml : a.part_ml)[at] = make_float2(mref, l);
+          pml = (whole ? a.seg_ml : a.part_ml) + at;
         }
       }
       if constexpr (narrow) {
-        // the sum of the row's four parts, 8 of 32 columns a warp: the others' through shared memory,
-        // [chunk of 32 columns][to][from][row][8]; with few rows several chunks at once
+        // The row's four parts, sum and maximum each of its own: warp w sums 8 of every 32 columns, the others'
+        // through shared memory, [chunk of 32 columns][to][from][row][8]; with few rows several chunks at once.
         const int nr = nrows * v.rep, chunks = min(D / 32, 16 / nr);
+        // The last product has had P from all four warps: they are done with the parts of the item before.
+        float2* ml = reinterpret_cast<float2*>(sm + C::OFF_JOIN) + lane % 16;
+        if (lane < 16) ml[16 * wq] = make_float2(mref, l);
         float* part = reinterpret_cast<float*>(sm + C::OFF_JOIN + 512) + lane * 8;
+        float own = 0.f, other[3] = {};   // weights, over the sum: no key seen gives zeros, NaN stays NaN
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32 * chunks) {
           if (c0) ok = join();
@@ -722,8 +705,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
               for (int k = 0; k < 3; ++k) {
                 float4* to = reinterpret_cast<float4*>(part + ((r * 4 + ((wq + k + 1) & 3)) * 3 + k) * nr * 8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[8 * k + e] = l == 0.f ? 0.f : o[8 * k + e] * inv;
                 to[0] = make_float4(o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3]);
                 to[1] = make_float4(o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]);
               }
@@ -731,6 +712,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           }
           ok = join();
           if (!ok) break;
+          if (c0 == 0) {
+            float2 x[3];
+            float mx = mref;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              x[k] = ml[16 * ((wq - k - 1) & 3)];
+              mx = fmaxf(mx, x[k].x);
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            own = ex2(mref - ref);
+            // in the warps' order, so that all four have the same sum
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = ml[16 * k];
+              sum += y.y * ex2(y.x - ref);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            own *= inv;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) other[k] = ex2(x[k].x - ref) * inv;
+            if (pml && wq == 0) *pml = make_float2(mx, sum);
+          }
 #pragma unroll 1
           for (int r = 0; r < n32; ++r) {
             const int col = c0 + 32 * r + 8 * wq;
@@ -740,13 +744,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
             tmem_wait_ld();
             if (!mine) continue;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : y[e] * inv;
+            for (int e = 0; e < 8; ++e) y[e] *= own;
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
               const float4* from = reinterpret_cast<const float4*>(part + ((r * 4 + wq) * 3 + k) * nr * 8);
               const float4 x0 = from[0], x1 = from[1];
-              y[0] += x0.x, y[1] += x0.y, y[2] += x0.z, y[3] += x0.w;
-              y[4] += x1.x, y[5] += x1.y, y[6] += x1.z, y[7] += x1.w;
+              const float w = other[k];
+              y[0] += w * x0.x, y[1] += w * x0.y, y[2] += w * x0.z, y[3] += w * x0.w;
+              y[4] += w * x1.x, y[5] += w * x1.y, y[6] += w * x1.z, y[7] += w * x1.w;
             }
             if (dst)
               *reinterpret_cast<uint4*>(dst + col) =
@@ -758,6 +763,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         if (!ok) break;
         __syncwarp();
       } else {
+        if (pml) *pml = make_float2(mref, l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // no key seen: zeros; NaN stays NaN
         const bool none = __any_sync(0xffffffffu, mine && l == 0.f);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
