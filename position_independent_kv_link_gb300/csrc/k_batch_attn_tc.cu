@@ -442,18 +442,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 
   // A warp zeroes the rows of V tile i of a window that hold no key any row of the block sees (lane: rows of its page)
   auto mend = [&](int st, int i, unsigned rows) {
+    unsigned todo = __ballot_sync(0xffffffffu, lane / KP == i && rows != 0xffffu);   // pages, by lane
+    if (!todo) return;
+    uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + lane * 16;
 #pragma unroll 1
-    for (unsigned todo = __ballot_sync(0xffffffffu, lane / KP == i && rows != 0xffffu); todo; todo &= todo - 1) {   // pages, by lane
+    for (; todo; todo &= todo - 1) {
       const int l = __ffs(todo) - 1;
-      const unsigned have = __shfl_sync(0xffffffffu, rows, l);
-      uint8_t* vs = sm + C::OFF_V + st * C::K_BYTES + l % KP * C::V_PAGE;
-#pragma unroll 1
-      for (int u = lane; u < C::PAGE_BYTES / 16; u += 32) {   // [half][row][8 chunks]
-        const int r = u / 8 % kPage, h = u / (8 * kPage);
-        if (!(have >> r & 1u)) *reinterpret_cast<uint4*>(vs + h * C::V_HALF + u % (8 * kPage) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      fence_async_smem();
+      const unsigned gone = ~__shfl_sync(0xffffffffu, rows, l) >> lane / 8;   // bit 4 k: row lane / 8 + 4 k, a lane a 16-byte chunk
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (gone >> 4 * k & 1u) *reinterpret_cast<uint4*>(vs + l % KP * C::V_PAGE + h * C::V_HALF + k * 512) = make_uint4(0, 0, 0, 0);
     }
+    fence_async_smem();
     __syncwarp();
   };
 
