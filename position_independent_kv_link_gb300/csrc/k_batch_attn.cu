@@ -185,16 +185,34 @@ __global__ void __launch_bounds__(kThreads) batch_simt_kernel(const __grid_const
   batch_flag(a.flag, bad);
 }
 
-// Joins what the attention kernels left in parts: one warp per (row, head), D / 32 columns per
+// Joins what the attention kernels left in parts: GL lanes per (row, head), D / GL columns per
 // lane; result = sum_i w_i O_i / sum_i w_i with w_i = l_i 2^(m_i - max). Rows that see no key
 // (sum 0) give zeros. A lane finds one part each (of the row's item of the prefix, then of its own);
-// their rows are read eight at a time. A batch with a prefix merges every row: grid (own row blocks, G,
-// rows of a block / 8); one without only the items that a share's edge cuts: grid (shares, 1, rows / 8).
-template <typename A, int D>
+// their rows are read several at a time. A batch with a prefix merges every row, of few parts: 8 lanes a row, grid
+// (own row blocks, G, rows of a block / 32); one without only the items that a share's edge cuts, of up to dozens
+// of parts: 32 lanes, grid (shares, 1, rows / 8). Latency bounds both, five loads that depend on one another a row.
+template <int N, typename A>
+__device__ __forceinline__ void store_columns(A* dst, const float* o, float f) {
+  alignas(16) A x[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = from_f<A>(o[e] * f);
+  constexpr int B = N * sizeof(A);
+  if constexpr (B % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(x)[i];
+  } else if constexpr (B == 8) {
+    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(x);
+  } else {
+    static_assert(B == 4, "");
+    *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(x);
+  }
+}
+template <typename A, int D, int GL>
 __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant__ MergeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int C = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int C = D / GL, V = C < 4 ? C : 4, RPW = 32 / GL;   // columns of a lane, of a load; rows of a warp
+  constexpr unsigned kAll = 0xffffffffu;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x % GL, group = (threadIdx.x & 31) / GL;
   int g = blockIdx.y, first = blockIdx.x;
   struct Parts {          // the parts of one item
     unsigned start, U, len;
@@ -225,16 +243,18 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
     const BatchBlock own = a.s[1].blocks[bi];
     const Parts po = parts(a.s[1], hd, own);
     if (po.n == 1 && !a.prefix) continue;   // the edge fell between the item's tiles and its end: out is written
+    const int rows = own.nrows * a.rep;
 #pragma unroll 1
-    for (int rr = blockIdx.z * 8 + warp; rr < own.nrows * a.rep; rr += 8 * gridDim.z) {
-      const int tok = rr * a.rep_inv >> 16, hh = rr - tok * a.rep, t = own.row0 + tok;
+    for (int r0 = (blockIdx.z * 8 + warp) * RPW; r0 < rows; r0 += 8 * RPW * gridDim.z) {
+      const bool live = r0 + group < rows;
+      const int rr = live ? r0 + group : r0, tok = rr * a.rep_inv >> 16, hh = rr - tok * a.rep, t = own.row0 + tok;
       const size_t head = (size_t)t * a.H + g * a.rep + hh;
       const int pb = a.prefix ? (unsigned)t / (unsigned)a.s[0].v.rb : 0;
       Parts pp{};
       if (a.prefix) pp = parts(a.s[0], hp, a.s[0].blocks[pb]);
       float M = -INFINITY, L = 0.f, o[C] = {};
 #pragma unroll 1
-      for (int i0 = 0; i0 < pp.n + po.n; i0 += 32) {
+      for (int i0 = 0; __any_sync(kAll, i0 < pp.n + po.n); i0 += GL) {
         const int i = i0 + lane, seg = i >= pp.n, p = seg ? i - pp.n : i;
         const Parts& q = seg ? po : pp;
         const MergeSegment& s = a.s[seg];
@@ -251,31 +271,36 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
         const float* src = (whole ? a.seg_o : s.part_o) + at * D;
         float mx = x.x;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        for (int d = GL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, d));
         mx = fmaxf(mx, M);
         const float ref = mx == -INFINITY ? 0.f : mx, keep = exp2f(M - ref), w = x.y * exp2f(x.x - ref);
         float sum = w;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int d = GL / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
         M = mx;
         L = L * keep + sum;
 #pragma unroll
         for (int e = 0; e < C; ++e) o[e] *= keep;
-        unsigned left = __ballot_sync(0xffffffffu, on && x.y != 0.f);
+        // the group's lanes whose part counts
+        unsigned left = __ballot_sync(kAll, on && x.y != 0.f) >> (GL * group) & (GL < 32 ? (1u << GL) - 1u : kAll);
         auto add = [&](auto batch) {   // so many rows on their way at once
           constexpr int N = decltype(batch)::value;
           float y[N][C], ww[N];
+          const bool any = left != 0;
           int k = 0;
 #pragma unroll
           for (int u = 0; u < N; ++u) {
             k = left ? __ffs(left) - 1 : k;    // behind the last row: that row again, with weight 0
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float* row = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)src, k)) + lane * C;
+            const float wk = __shfl_sync(kAll, w, k, GL);
+            const float* row = reinterpret_cast<const float*>(__shfl_sync(kAll, (unsigned long long)src, k, GL)) + lane * C;
             ww[u] = left ? wk : 0.f;
-            if constexpr (C == 4) {
-              *reinterpret_cast<float4*>(y[u]) = *reinterpret_cast<const float4*>(row);
-            } else {
-              *reinterpret_cast<float2*>(y[u]) = *reinterpret_cast<const float2*>(row);
+#pragma unroll
+            for (int e = 0; e < C; e += V) {
+              if constexpr (V == 4) {
+                *reinterpret_cast<float4*>(y[u] + e) = any ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+              } else {
+                *reinterpret_cast<float2*>(y[u] + e) = any ? *reinterpret_cast<const float2*>(row + e) : make_float2(0.f, 0.f);
+              }
             }
             left &= left - 1;
           }
@@ -285,15 +310,16 @@ __global__ void __launch_bounds__(256) batch_merge_kernel(const __grid_constant_
             for (int e = 0; e < C; ++e) o[e] += ww[u] * y[u][e];
         };
 #pragma unroll 1
-        while (left) {
-          if (__popc(left) > 4) add(std::integral_constant<int, 20>());
-          else add(std::integral_constant<int, 4>());
+        while (__any_sync(kAll, left != 0)) {
+          if constexpr (GL == 32) {
+            if (__popc(left) > 4) add(std::integral_constant<int, 20>());
+            else add(std::integral_constant<int, 4>());
+          } else {
+            add(std::integral_constant<int, 2>());
+          }
         }
       }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      A* dst = static_cast<A*>(a.out) + head * D + lane * C;
-#pragma unroll
-      for (int e = 0; e < C; ++e) dst[e] = from_f<A>(o[e] * inv);
+      if (live) store_columns<C>(static_cast<A*>(a.out) + head * D + lane * C, o, L == 0.f ? 0.f : 1.f / L);
     }
   }
 }
@@ -320,13 +346,19 @@ void launch_batch_merge(const MergeArgs& m, int dtype, int D, cudaStream_t st) {
   // as many warps as a block has rows when the requests have equally many
   const BatchView& v = m.s[1].v;
   const int own = v.T / v.rb + v.n_reqs, rows = pmin(v.rb, pdiv(v.T, v.n_reqs)) * v.rep;
-  const dim3 grid = m.prefix ? dim3(own, v.G, pdiv(rows, 8)) : dim3(m.grid, 1, pdiv(rows, 8));
+  // 8 lanes a row from where 32 would need more warps than are resident at once (4 CTAs of 8 an SM): rows are then
+  // of few parts, as there are many items. 32 requests of 32 rows behind 4096: 117 us, with 32 lanes 120; 64 and 4
+  // single rows with 8 lanes: 90 us for 87, 75 for 61.
+  const bool many = m.prefix && (long long)v.T * m.H > 32ll * m.grid;
+  const int z = pdiv(rows, many ? 32 : 8);
+  const dim3 grid = m.prefix ? dim3(own, v.G, z) : dim3(m.grid, 1, z);
+  auto go = [&](auto* k8, auto* k32) { launch_dependent(many ? k8 : k32, grid, dim3(256), 0, st, m); };
   if (dtype == PIC_BF16) {
-    if (D == 128) launch_dependent(batch_merge_kernel<__half, 128>, grid, dim3(256), 0, st, m);
-    else launch_dependent(batch_merge_kernel<__half, 64>, grid, dim3(256), 0, st, m);
+    if (D == 128) go(batch_merge_kernel<__half, 128, 8>, batch_merge_kernel<__half, 128, 32>);
+    else go(batch_merge_kernel<__half, 64, 8>, batch_merge_kernel<__half, 64, 32>);
   } else {
-    if (D == 128) launch_dependent(batch_merge_kernel<float, 128>, grid, dim3(256), 0, st, m);
-    else launch_dependent(batch_merge_kernel<float, 64>, grid, dim3(256), 0, st, m);
+    if (D == 128) go(batch_merge_kernel<float, 128, 8>, batch_merge_kernel<float, 128, 32>);
+    else go(batch_merge_kernel<float, 64, 8>, batch_merge_kernel<float, 64, 32>);
   }
 }
 

@@ -52,11 +52,11 @@
 // than the MMAs.
 //
 // Measured, 8 KV heads of 4 query heads, D = 128, whole call: 32 decoding requests of 3000 to 32000 keys, window
-// 4096 (0.53 GB of K and V): 116 us, 4.6 TB/s, about 850 ns a key tile of 64; neither HBM, tensor pipe nor issue slots are
+// 4096 (0.53 GB of K and V): 114 us, 4.7 TB/s, about 850 ns a key tile of 64; neither HBM, tensor pipe nor issue slots are
 // full: the roles' waits for one another bound it. (With tiles of 128 rows, 124 us: without K's second product 115, without
 // the rotation's arithmetic 119, without P's second product 121.) Two prompts of 4096, window 1024 (121 GFLOP by the
-// formula, 181 issued): 166 us, 0.73 PFLOP/s of the formula's; tensor pipe 58 %: the way S -> registers -> next S, for
-// which TMEM has no second S buffer (P in S's place, with two of each, took 169 us).
+// formula, 181 issued): 163 us, 0.74 PFLOP/s of the formula's; tensor pipe 59 %: the way S -> registers -> next S, for
+// which TMEM has no second S buffer (P in S's place, with two of each, was 2 % slower).
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
@@ -1301,7 +1301,7 @@ __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant
   const __nv_bfloat16 *src = static_cast<const __nv_bfloat16*>(a.k_layer) + from, *vsrc = static_cast<const __nv_bfloat16*>(a.v_layer) + from;
   __half* dst = a.krot + (size_t)blockIdx.x * v.G * kPage * D + row * D + 8 * c;
 #pragma unroll 2
-  for (int g = g0; g < v.G; g += HP) {
+  for (int g = g0 + HP * blockIdx.y; g < v.G; g += HP * gridDim.y) {
     const uint4 u1 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D);
     const uint4 u2 = *reinterpret_cast<const uint4*>(src + (size_t)g * kPage * D + D / 2);
     const uint32_t a1[4] = {u1.x, u1.y, u1.z, u1.w}, a2[4] = {u2.x, u2.y, u2.z, u2.w};
@@ -1342,7 +1342,9 @@ void batch_tc_view(BatchView& v, bool wide, bool narrow) {
 }
 
 pic_status launch_batch_rotate(const BatchArgs& a, cudaStream_t st) {
-  const dim3 grid(a.krot_slots);
+  // few pages: the KV heads on CTAs of their own too (a CTA takes two heads of 128 or four of 64 at once)
+  const int at_once = a.D == 128 ? 2 : 4;
+  const dim3 grid(a.krot_slots, a.krot_slots < 4096 ? pdiv(a.v.G, at_once) : 1);
   if (a.D == 128) batch_rotate_kernel<128><<<grid, 256, 0, st>>>(a);
   else batch_rotate_kernel<64><<<grid, 256, 0, st>>>(a);
   PIC_CUDA(cudaGetLastError());
