@@ -221,6 +221,13 @@ def test_many_requests(pkl, rows, prefix, rep):
     b.check(b.shared() if prefix else b.window(25, 3), 0 if prefix else 25, 0 if prefix else 3)
 
 
+@pytest.mark.parametrize("n,prefix", [(310, 9000), (1300, 3000)])
+def test_many_rows_of_many_parts(pkl, n, prefix):
+    """One KV head: few long items behind a prefix, each cut into about eight parts (or few) for many rows."""
+    b = Batch(pkl, [5] * n, [1] * n, 16, 1, 128, True, prefix=prefix, seed=n)
+    b.check(b.shared())
+
+
 @pytest.mark.parametrize("H,G,D", [(6, 2, 128), (10, 2, 64), (12, 1, 128), (15, 1, 64)])
 def test_heads_that_do_not_fill_a_tile(pkl, H, G, D):
     """Groups of 3, 5, 12 and 15 query heads: single rows, as many as fit one small item, one more, and many."""
