@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     __syncwarp();
   };
 
-  if (tid == 0) {
+  if (tid == 32 * C::W_PV) {   // not a warp that small plans keep busy
     s_abort = 0;
     auto init = [&](int i, int n, int count) {
 #pragma unroll 1
