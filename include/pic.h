@@ -460,7 +460,7 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  * (PIC_ERR_CAPACITY) or lengths that do not fit together (PIC_ERR_INVALID_ARG) no table changes,
  * the lengths come out as they went in, there are no rows, and counts[2] is not 0.
  * At most 12288 requests and tables of fewer than 2^26 entries a request (PIC_ERR_CAPACITY). One launch, two
- * with max_rows above 4096. */
+ * with max_rows above 24576. */
 pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int32_t* new_len, int32_t* block_table,
                                int32_t table_stride, int32_t* page_pos, const int32_t* n_pages,
                                const int32_t* free_blocks, int32_t n_free, const int32_t* free_used, int32_t first,

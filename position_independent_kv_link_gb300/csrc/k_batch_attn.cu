@@ -429,6 +429,9 @@ void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
   }
   for (int i = 0; i < c.n; ++i) {
     BatchView& v = c.a[i].v;
+    // Narrow when the requests have no more rows on average than one narrow item (the prefix' rows one at most).
+    // Narrow and not: 32 decoding requests 113 and 134 us, 64 of 4 rows and 1000 keys (4 query heads a KV head)
+    // 77 and 78, one of 1024 keys 18.2 and 17.7.
     const int most = kRows / v.rep;   // tokens of a narrow item
     const bool narrow = !c.wide[i] && (v.only == 1 || T <= (long long)n_reqs * most) && (v.only == 2 || prefix_len == 0 || T <= most);
     batch_tc_view(v, c.wide[i], narrow);

@@ -487,7 +487,7 @@ def test_block_tables(pkl, ragged, n, kv_hi, new_hi, first, used):
         assert np.array_equal(d_pos.cpu().numpy(), rp)
 
 
-@pytest.mark.parametrize("max_rows", [1, 1023, 1024, 1025, 4095, 4096, 4097, 20000])
+@pytest.mark.parametrize("max_rows", [1, 1023, 1024, 1025, 4096, 24575, 24576, 24577, 40000])
 @pytest.mark.parametrize("n", [1, 1024, 1025])
 def test_block_tables_row_counts(pkl, n, max_rows):
     """One request has all the rows (or every row of max_rows is one of its own), the others none."""
@@ -505,7 +505,7 @@ def test_block_tables_row_counts(pkl, n, max_rows):
     assert np.array_equal(d.cpu().numpy(), rt)
 
 
-@pytest.mark.parametrize("max_rows", [40, 9000])
+@pytest.mark.parametrize("max_rows", [40, 9000, 30000])
 def test_block_tables_in_place(pkl, max_rows):
     """The lengths, page counts and used entries updated in place, twice in a row and captured."""
     kv, new, table = i32([0, 17, 40]), i32([5, 0, 30]), i32(np.arange(300).reshape(3, 100) + 1000)
