@@ -221,6 +221,23 @@ def test_many_requests(pkl, rows, prefix, rep):
     b.check(b.shared() if prefix else b.window(25, 3), 0 if prefix else 25, 0 if prefix else 3)
 
 
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("spare", [1, 3, 700])
+def test_batches_without_rows(pkl, half, spare):
+    """Room for rows that no request has: nothing is written, whichever form the shapes ask for."""
+    for prefix in (0, 300):
+        b = Batch(pkl, [5, 0, 70], [0, 0, 0], 8, 2, 128, half, prefix=prefix, seed=spare, spare_rows=spare)
+        b.check(b.shared() if prefix else b.window(9, 2))
+        assert (b.out == 7.0).all()
+
+
+@pytest.mark.parametrize("T", range(1, 10))
+def test_fewer_rows_than_a_box(pkl, T):
+    """1 to 9 rows of one request, 16 query heads a KV head (a box of q holds 8)."""
+    b = Batch(pkl, [40 + T], [T], 16, 1, 128, True, seed=T)
+    b.check(b.window(30, 1), 30, 1)
+
+
 @pytest.mark.parametrize("n,prefix", [(310, 9000), (1300, 3000)])
 def test_many_rows_of_many_parts(pkl, n, prefix):
     """One KV head: few long items behind a prefix, each cut into about eight parts (or few) for many rows."""
