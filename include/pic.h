@@ -484,7 +484,7 @@ pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_
 /* Scratch of the two attention calls below; prefix_len and prefix_pages 0 for
  * pic_op_attention_window. 0 for shapes they refuse. The scratch need not be initialised and is
  * free again when the call's work is done. (bf16 batches with many rows per request, or behind
- * a prefix, keep the rotated K of their pages and V as fp16 in it: up to 1 GB for each.) It depends on the
+ * a prefix, keep the rotated K of their pages and V in it: up to 1 GB for each.) It depends on the
  * current device's number of SMs. */
 size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_reqs, int32_t n_heads,
                                             int32_t n_kv_heads, int32_t head_dim, int32_t table_stride,
@@ -499,7 +499,7 @@ size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_
  * together, a key that one of them does not see has weight 0 there); K and V in bf16 pools lie within fp16's
  * range (pool writes check it). out must not overlap q. A row that sees no key gets zeros. Rows from row_start[n_reqs] on stay as they
  * were. fp32 pools: fp32 arithmetic; bf16 pools: fp32 sums and softmax, operands of the products in 16 to
- * 22 bits (11 for the weights of many rows), so that rounding the result to fp16 is the largest error. The same
+ * 22 bits, so that rounding the result to fp16 is the largest error. The same
  * call gives the same bits again. */
 pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                    const void* q, const int32_t* row_start, int32_t n_reqs, const int32_t* kv_len,

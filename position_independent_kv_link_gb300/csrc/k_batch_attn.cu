@@ -372,15 +372,16 @@ struct BatchCall {
 
 // When K is rotated ahead, once per page, and items have two MMA tiles: when a KV head's keys meet
 // enough rows that the MMAs bound the time -- in-kernel rotation, done for every 128 rows anew,
-// would then take longer than they do. Below that HBM bounds, and the rotated K (two fp16 parts) with V as fp16
+// would then take longer than they do. Below that HBM bounds, and the rotated K (two fp16 parts) with V
 // takes five times K's bytes to write and read. These (for the whole tables: the host does not know the lengths) must
 // stay within 1 GB.
-// Measured on 8 KV heads of 4 query heads, D = 128, ahead and in the kernel: 256 rows (32 requests of 64
-// rows and 4096 keys) 384 and 266 us; 512 rows (16 requests of 128) 284 and 275 us, (128 single rows behind a
-// prefix of 16384) 162 and 155 us; 1024 rows (8 requests of 256, 4096 keys, window 1024) 107 and 111 us.
+// Measured on 8 KV heads of 4 query heads, D = 128, ahead and in the kernel, requests of 4096 keys: 512 rows (16 requests
+// of 128) 322 and 266 us; 1024 rows (8 of 256) 273 and 257 us, with a window of 1024 120 and 100 us, (256 single rows behind
+// a prefix of 16384) 195 and 191 us; 2048 rows (4 of 512) 225 and 248 us, with the window, where fewer of them meet a key,
+// 108 and 98 us, (512 single rows behind the prefix) 314 and 359 us; 16384 rows (2 of 4096), window 1024, 200 and 259 us.
 constexpr size_t kMaxRotated = (size_t)1 << 30;
 double most_slots(int G, int D) { return (double)kMaxRotated / ((double)G * kPage * D * 2 * 3); }
-bool wide_pays(long long rows, double slots, int G, int D) { return rows >= 1024 && slots <= most_slots(G, D); }
+bool wide_pays(long long rows, double slots, int G, int D) { return rows >= 2048 && slots <= most_slots(G, D); }
 constexpr int kRowsWithPrefix = 64;
 
 void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, int table_stride, int prefix_len,
@@ -409,8 +410,8 @@ void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
   // Behind a prefix for the wide kernel the own pages go with it, in one plan, from half an MMA tile of rows a
   // request on and when their tables are at most twice as long as the prefix: one launch less, and 128 rows a tile
   // where they are not many more than one. Together and apart: 32 requests of 32 rows behind 4096, 32 keys of their own:
-  // 121 and 136 us; 64 of 16 rows, 64 keys: 130 and 140, 1024 keys: 260 and 194; 8 of 64 rows behind 8192, 2000 keys:
-  // 151 and 164.
+  // 137 and 147 us; 16 of 32 rows: 85 and 97; 64 of 16 rows, 64 keys: equal, 1024 keys: 260 and 210; 8 of 64 rows behind
+  // 8192, 2000 keys: 176 and 179.
   const bool both = pre && own_rows >= kRowsWithPrefix && own_slots <= 2.0 * prefix_pages && own_slots + prefix_pages <= most_slots(G, D);
   if (prefix_len > 0 && (own || pre) && !both) {
     c.n = 2;

@@ -10,7 +10,7 @@
 //   load        (the meta warp, or, MT = 2, a warp of its own) asks for the items' rows of q (TMA boxes of 8
 //               tokens x rep heads, when the item before has had its last S product) and for V: one box a page (a
 //               page is one K = 16 step of the PV product, so pages need not be neighbours), or, MT = 2, two
-//               boxes of four pages of its fp16 copy.
+//               boxes of four pages of its copy.
 //   K warp      asks for K, one TMA box a page wherever its block lies, with the RoPE table row of the page's
 //               position. On its own: with the records' work in the same warp K came late (the decode batch
 //               below took 18 % longer).
@@ -39,10 +39,9 @@
 // Roundings. The result is fp16; what comes before it is held to fewer than half that rounding. Rotated K is two
 // fp16 numbers (22 bits), S the sum of both products: with one (11 bits, error of a score about 3e-4 at scores of
 // order 1) the result's error was twice that of its rounding alone. P is two bf16 numbers (16 bits; V is stored bf16,
-// and both operands of a product have one type) in two PV products, or, MT = 2, where the products bound the
-// time, one fp16 number with V as fp16 (exact within fp16's range, which pool writes flag). Error against
-// 64 bits relative to the result's norm: 2.1e-4, that of rounding it; MT = 2: 2.7e-4 to 2.9e-4. One fp16 K and one
-// bf16 P: 1.7e-3, and 16 to 20 % faster.
+// and both operands of a product have one type) in two PV products. Error against 64 bits relative to the result's
+// norm: 2.1e-4, that of rounding it. One fp16 K and one bf16 P: 1.7e-3, and 16 to 20 % faster; P as one fp16
+// number with V as fp16, in the two-tile form, 2.7e-4 to 2.9e-4, and 18 % faster.
 //
 // The roles' loops are kept small, and few on each scheduler: with three times the code every role ran
 // at 8 cycles an instruction (ncu: no_instruction the largest stall).
@@ -55,8 +54,8 @@
 // 4096 (0.53 GB of K and V): 114 us, 4.7 TB/s, about 850 ns a key tile of 64; neither HBM, tensor pipe nor issue slots are
 // full: the roles' waits for one another bound it. (With tiles of 128 rows, 124 us: without K's second product 115, without
 // the rotation's arithmetic 119, without P's second product 121.) Two prompts of 4096, window 1024 (121 GFLOP by the
-// formula, 181 issued): 163 us, 0.74 PFLOP/s of the formula's; tensor pipe 59 %: the way S -> registers -> next S, for
-// which TMEM has no second S buffer (P in S's place, with two of each, was 2 % slower).
+// formula): 200 us, 0.60 PFLOP/s of the formula's; 268 GFLOP with both operands' second parts and the masked edges of the
+// tiles, 144 us at 1865 TFLOP/s, bound it, with 32 us of rotation ahead and item ends.
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.
@@ -72,11 +71,9 @@ namespace pic {
 namespace {
 
 constexpr float kRescale = 8.f;           // rescale O when the row maximum grows by more than 2^8
-constexpr float kLift = 4.f;              // a row's largest P is 2^4 then (2^12 before the next rescaling): fp16 has 2^-24 to 65504
 constexpr unsigned long long kWaitLimit = 4000000000ull;   // cycles, about 2 s
 
 constexpr int KT = 64, KP = KT / kPage;   // keys, pages of a tile
-constexpr int NBP = 2;                    // P buffers per MMA tile
 constexpr int WIN = 32, WT = WIN / KP;    // pages, tiles of a window
 constexpr int NWIN = 6;                   // window records
 
@@ -85,6 +82,10 @@ struct Cfg {
   static constexpr int D = D_, MT = MT_;
   static constexpr bool NARROW = NARROW_;
   static constexpr int NQ = 1;                        // Q buffers per MMA tile
+  static constexpr int NBP = 2;                       // P buffers per MMA tile
+  // P over its S, two of each per MMA tile (MT = 2 has no room for more; one S and one P beside it take 2 % longer); else
+  // one S beside two P's
+  static constexpr bool OVER = MT == 2;
   static constexpr int NX = MT == 2 ? 0 : D == 128 ? 3 : 6;   // raw K stages (with table rows)
   static constexpr int NK = MT == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 3);   // K operand stages
   static constexpr int NV = MT == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);   // V stages
@@ -116,13 +117,14 @@ struct Cfg {
   static constexpr int B_META = 0, B_RFREE = B_META + NWIN, B_XFULL = B_RFREE + NWIN, B_XEMPTY = B_XFULL + NX,
                        B_READY = B_XEMPTY + NX, B_KEMPTY = B_READY + NK, B_VFULL = B_KEMPTY + NK,
                        B_VEMPTY = B_VFULL + NV, B_VREADY = B_VEMPTY + NV, B_SFULL = B_VREADY + (MT == 2 ? NV : 0),
-                       B_SFREE = B_SFULL + MT, B_PREADY = B_SFREE + MT, B_PVDONE = B_PREADY + MT * NBP,
+                       B_SFREE = B_SFULL + MT * (OVER ? 2 : 1), B_PREADY = B_SFREE + MT, B_PVDONE = B_PREADY + MT * NBP,
                        B_QFULL = B_PVDONE + MT * NBP, B_QEMPTY = B_QFULL + MT * NQ,
                        B_DONE = B_QEMPTY + MT * NQ, B_JOIN = B_DONE + 2 * MT, N_BARS = B_JOIN + 1;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8;
   static_assert(SMEM + 1024 <= 226 * 1024, "shared memory budget (the plan's few static words besides)");
-  // TMEM columns: O_t at D t, S_t at TM_S + 128 t, P buffer b of tile t at TM_P + 128 t + PW b
-  static constexpr uint32_t TM_S = MT * D, TM_P = TM_S + KT, PW = MT == 2 ? KT / 2 : KT;
+  // TMEM columns: O_t at D t; S_t at TM_S + 128 t, P buffer b of tile t (two bf16 parts) at TM_P + 128 t + KT b; OVER:
+  // S and P buffer b there
+  static constexpr uint32_t TM_S = MT * D, TM_P = OVER ? TM_S : TM_S + KT;
   static constexpr uint32_t TMEM_COLS = 512;
 };
 
@@ -140,9 +142,9 @@ struct WinRec {           // 48 bytes
 // reads records has arrived at RFREE for the window before in its slot. XFULL, XEMPTY: between the
 // K warp and the rotation, all of whose warps arrive. READY (of K), KEMPTY: the rotation, or the K
 // warp's TMA, of tile j + NK follows the S products of tile j. VFULL, VEMPTY: V of tile j + NV follows
-// PV of j, which waits for VREADY (or VFULL); VREADY: VFULL seen and mended. SFULL, SFREE: between the
+// PV of j, which waits for VREADY (or VFULL); VREADY: VFULL seen and mended. SFULL, SFREE (MT = 1): between the
 // S warp and warpgroup t, all of whose warps arrive. PREADY, PVDONE: between warpgroup t and the PV
-// warp; P(j + 2) into a buffer follows the end of PV(j). QFULL, QEMPTY: between the load and the S warp.
+// warp; P(j + 2) into a buffer (MT = 2: S(j + 2), then P over it) follows the end of PV(j). QFULL, QEMPTY: between the load and the S warp.
 // JOIN: the four softmax warps of a narrow item, which all wait.
 // No wait is for what waits in turn. Record i needs the readers' passage of window i - NWIN, and by then (MT 1)
 // the meta warp has asked for q and V up to window i - 4; K, S, P and PV of windows up to there need only
@@ -225,12 +227,12 @@ constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo = 0) {
   return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16;
 }
-// kind::f16, fp32 accumulator, M x N: fp16 K-major operands; fp16 or bf16 A (TMEM) with MN-major B
+// kind::f16, fp32 accumulator, M x N: fp16 K-major operands; bf16 A (TMEM) with MN-major B
 __device__ __forceinline__ constexpr uint32_t idesc_s(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ constexpr uint32_t idesc_pv(int M, int N, bool bf16) {
-  return idesc_s(M, N) | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (1u << 16);
+__device__ __forceinline__ constexpr uint32_t idesc_pv(int M, int N) {
+  return idesc_s(M, N) | 1u << 7 | 1u << 10 | (1u << 16);
 }
 template <bool ACC>
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
@@ -417,7 +419,8 @@ __device__ __forceinline__ unsigned seen_bits(int4 p, int qp, int lo, int sinks)
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_constant__ TcArgs ta) {
   constexpr bool narrow = C::NARROW;
-  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NK = C::NK, NV = C::NV;
+  constexpr int D = C::D, MT = C::MT, NQ = C::NQ, NK = C::NK, NV = C::NV, NBP = C::NBP;
+  constexpr bool OVER = C::OVER;
   const BatchArgs& a = ta.b;
   const BatchView& v = a.v;
   extern __shared__ uint8_t smem_raw[];
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     init(C::B_KEMPTY, NK, MT);
     init(C::B_VFULL, NV, 1);
     init(C::B_VEMPTY, NV, MT);
-    init(C::B_SFULL, MT, 1);
+    init(C::B_SFULL, C::B_SFREE - C::B_SFULL, 1);
     init(C::B_SFREE, MT, 4);
     init(C::B_PREADY, MT * NBP, 4);
     init(C::B_PVDONE, MT * NBP, 1);
@@ -546,10 +549,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++ct) {
         const int b = ct % NBP;
-        const uint32_t t_p = trow + C::TM_P + 128 * t + C::PW * b, t_sb = trow + C::TM_S + 128 * t;
+        const uint32_t t_p = trow + C::TM_P + 128 * t + KT * b, t_sb = OVER ? t_p : trow + C::TM_S + 128 * t;
         const int2 lim = sLim[win % NWIN * WT + j];
         const bool masked = __any_sync(0xffffffffu, lim.x > qp || lim.y <= lo);
-        ok = __all_sync(0xffffffffu, wait(C::B_SFULL + t, ct & 1));
+        ok = __all_sync(0xffffffffu, OVER ? wait(C::B_SFULL + 2 * t + b, (ct / 2) & 1) : wait(C::B_SFULL + t, ct & 1));
         if (!ok) break;
         if constexpr (narrow) {
           fence_after();
@@ -568,8 +571,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
           for (int i = 2; i < 16; ++i) m2[i & 1] = fmaxf(m2[i & 1], s[i]);
           const float mx = fmaxf(m2[0], m2[1]) * sl;
-          const bool grow = mx > mref + (kRescale + kLift);
-          const float mnew = grow ? mx - kLift : mref;
+          const bool grow = mx > mref + kRescale;
+          const float mnew = grow ? mx : mref;
           const float scale = (grow && mref != -INFINITY) ? ex2(mref - mnew) : 1.f;
           mref = mnew;
           const float mz = mref == -INFINITY ? 0.f : -mref;
@@ -606,8 +609,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
           for (int c = 0; c < KT; c += 16) tmem_ld16(t_sb + c, s + c);
           tmem_wait_ld();
           fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::B_SFREE + t));   // the next S may come
+          if constexpr (!OVER) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_SFREE + t));   // the next S may come
+          }
           if (masked) {
             const int4* pages = sPage + win % NWIN * WIN + j * KP;
 #pragma unroll
@@ -621,16 +626,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
           for (int i = 4; i < KT; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
           const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
-          const bool grow = mx > mref + (kRescale + kLift);
-          const float mnew = grow ? mx - kLift : mref;
+          const bool grow = mx > mref + kRescale;
+          const float mnew = grow ? mx : mref;
           const float scale = (grow && mref != -INFINITY) ? ex2(mref - mnew) : 1.f;
           mref = mnew;
           const float mz = mref == -INFINITY ? 0.f : -mref;   // nothing seen so far: every s is -inf, p = 0
           float2 sum[2] = {make_float2(l * scale, 0.f), make_float2(0.f, 0.f)};
-          // the P buffer's PV two tiles before is done (the first round's waits return at once)
-          ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + b, (ct / NBP + 1) & 1));
-          if (!ok) break;
-          fence_after();
+          if constexpr (!OVER) {
+            // the P buffer's PV two tiles before is done (the first round's waits return at once)
+            ok = __all_sync(0xffffffffu, wait(C::B_PVDONE + t * NBP + b, (ct / NBP + 1) & 1));
+            if (!ok) break;
+            fence_after();
+          }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pv[16], pl[16];
@@ -640,11 +647,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
               p.x = ex2(p.x);
               p.y = ex2(p.y);
               sum[e & 1] = add2(sum[e & 1], p);
-              if constexpr (MT == 2) pv[e] = pack_f16x2(p.x, p.y);
-              else split_bf16x2(p, pv[e], pl[e]);
+              split_bf16x2(p, pv[e], pl[e]);
             }
             tmem_st16(t_p + 16 * c, pv);
-            if constexpr (MT == 1) tmem_st16(t_p + KT / 2 + 16 * c, pl);
+            tmem_st16(t_p + KT / 2 + 16 * c, pl);
           }
           l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           if (__any_sync(0xffffffffu, mine && scale != 1.f)) {
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         }
         __syncwarp();
         if (lane == 0) {
-          if (idle) mbar_arrive(bar(C::B_SFREE + t));
+          if (!OVER && idle) mbar_arrive(bar(C::B_SFREE + t));
           mbar_arrive(bar(C::B_PREADY + t * NBP + b));
         }
       }
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
     const bool s_warp = warp >= C::W_S && warp < C::W_S + MT;
     const int t = s_warp ? warp - C::W_S : warp - C::W_PV;
     const bool one = elect();
-    constexpr uint32_t id_s = idesc_s(C::M, KT), id_pv = idesc_pv(C::M, D, MT == 1);
+    constexpr uint32_t id_s = idesc_s(C::M, KT), id_pv = idesc_pv(C::M, D);
     const int full = s_warp ? C::B_READY : MT == 2 ? C::B_VREADY : C::B_VFULL, empty = s_warp ? C::B_KEMPTY : C::B_VEMPTY;
     uint32_t gt = 0, ct = 0, qi = 0;   // tiles of the CTA, of the MMA tile; items of it
     bool ok = true;
@@ -833,11 +839,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
         }
         if (MT == 1 && !s_warp && ok) mend(st, j, rows);
         const int b = ct % NBP;
-        // S: the softmax has read the buffer (the first waits return at once); PV: its P is written
-        ok = ok && (s_warp ? wait_all(C::B_SFREE + t, (ct + 1) & 1) : wait_all(C::B_PREADY + t * NBP + b, (ct / NBP) & 1));
+        // S: the softmax has read the buffer, or (OVER) PV the P that was written over it (the first waits return at
+        // once); PV: its P is written
+        ok = ok && (!s_warp ? wait_all(C::B_PREADY + t * NBP + b, (ct / NBP) & 1)
+                    : OVER  ? wait_all(C::B_PVDONE + t * NBP + b, (ct / NBP + 1) & 1)
+                            : wait_all(C::B_SFREE + t, (ct + 1) & 1));
         if (!ok) break;
         fence_after();
-        const uint32_t buf = tmem + 128 * t + (s_warp ? C::TM_S : C::TM_P + C::PW * b);
+        const uint32_t buf = tmem + 128 * t + (s_warp && !OVER ? C::TM_S : C::TM_P + KT * b);
         if (one) {
           if (s_warp) {
             const uint32_t kd = desc_lo(base + C::OFF_K + st * C::K_STAGE);
@@ -853,13 +862,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) batch_tc_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < KP; ++k)      // 16 keys: a page
               umma_ts(tmem + D * t, buf + 8 * k, vd + k * (C::V_PAGE / 16), id_pv, !first || k != 0);
-            if constexpr (MT == 1) {          // P's second part
 #pragma unroll
-              for (int k = 0; k < KP; ++k)
-                umma_ts(tmem + D * t, buf + KT / 2 + 8 * k, vd + k * (C::V_PAGE / 16), id_pv, 1);
-            }
+            for (int k = 0; k < KP; ++k)      // P's second part
+              umma_ts(tmem + D * t, buf + KT / 2 + 8 * k, vd + k * (C::V_PAGE / 16), id_pv, 1);
           }
-          umma_commit(bar(s_warp ? C::B_SFULL + t : C::B_PVDONE + t * NBP + b));
+          umma_commit(bar(!s_warp ? C::B_PVDONE + t * NBP + b : C::B_SFULL + (OVER ? 2 * t + b : t)));
           umma_commit(bar(empty + st));
         }
         __syncwarp();
@@ -1265,12 +1272,9 @@ pic_status launch(const TcArgs& ta, cudaStream_t st) {
 }
 
 // K of every page that some row of the batch sees (or of the prefix), rotated to its keys' positions, as fp16,
-// then what that leaves out, then V (bf16 -> fp16, exact within fp16's range), each [slot][G][16][D]. One CTA
+// then what that leaves out, then V as it is (a tile's four pages are neighbours then), each [slot][G][16][D]. One CTA
 // a page: a thread has one row and 8 pairs of dims, and takes their table entries once for all KV heads.
 // HBM-bound: K and V read once, three such arrays written.
-__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t x) {
-  return pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
 template <int D>
 __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant__ BatchArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1319,10 +1323,8 @@ __global__ void __launch_bounds__(256) batch_rotate_kernel(const __grid_constant
     d2[0] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
     d1[part] = make_uint4(p1[0], p1[1], p1[2], p1[3]);
     d2[part] = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-    const uint4 v1 = *reinterpret_cast<const uint4*>(vsrc + (size_t)g * kPage * D);
-    const uint4 v2 = *reinterpret_cast<const uint4*>(vsrc + (size_t)g * kPage * D + D / 2);
-    d1[2 * part] = make_uint4(f16_of_bf16(v1.x), f16_of_bf16(v1.y), f16_of_bf16(v1.z), f16_of_bf16(v1.w));
-    d2[2 * part] = make_uint4(f16_of_bf16(v2.x), f16_of_bf16(v2.y), f16_of_bf16(v2.z), f16_of_bf16(v2.w));
+    d1[2 * part] = *reinterpret_cast<const uint4*>(vsrc + (size_t)g * kPage * D);
+    d2[2 * part] = *reinterpret_cast<const uint4*>(vsrc + (size_t)g * kPage * D + D / 2);
   }
 }
 
