@@ -430,7 +430,8 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  * [n_reqs][table_stride] int32 block ids -- and its rows (queries) are rows
  * [row_start[r], row_start[r + 1]) of q and out, the last ones of the request: row i of m is at
  * position first + kv_len[r] - m + i, where `first` is the position of the request's first page
- * (the prefix length of pic_op_attention_prefix, else 0). A request may have no rows.
+ * (the prefix length of pic_op_attention_prefix, else 0). A request may have no rows. row_start must not fall: a
+ * request whose rows end before they start or behind row_start[n_reqs] is skipped.
  * Pages: without page_pos page p holds positions first + 16 p ... With page_pos
  * ([n_reqs][table_stride], absolute position of each page's row 0, ascending) a page may hold
  * fewer than 16 rows (the ragged tails of linked chunks), up to the next page's position, and

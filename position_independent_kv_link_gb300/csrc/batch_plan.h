@@ -78,11 +78,12 @@ PIC_HD int own_first(const BatchView& v) { return v.pre_len; }
 // Number of pages of request r (checked by request_rows).
 PIC_HD int own_pages(const BatchView& v, int r) { return v.page_pos ? v.n_pages[r] : pdiv(v.kv_len[r], kPage); }
 
-// Rows of request r and their first row; 0 (and a flag) when its lengths do not fit together.
+// Rows of request r and their first row; 0 (and a flag) when its lengths do not fit together. No row lies behind
+// row_start[n_reqs], up to which the prefix' blocks are planned.
 PIC_HD int request_rows(const BatchView& v, int r, int& row0, unsigned& bad) {
   const int a = v.row_start[r], b = v.row_start[r + 1], kv = v.kv_len[r], first = own_first(v);
   row0 = a;
-  if (a < 0 || b < a || b > v.T || kv < 0 || b - a > kv || kv > v.rope_positions - first) {
+  if (a < 0 || b < a || b > pmin(v.T, v.row_start[v.n_reqs]) || kv < 0 || b - a > kv || kv > v.rope_positions - first) {
     bad |= kBatchBadLengths;
     return 0;
   }
