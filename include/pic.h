@@ -440,7 +440,8 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  *
  * The host checks shapes, pointers and alignment (16 bytes; attention outputs 32, scratch 256). What only the device
  * sees is checked there: a request whose lengths do not fit together is skipped (its rows of out
- * stay as they were), a page whose block lies outside the pool counts as empty, a position
+ * stay as they were), a page whose block lies outside the pool or whose position and the next page's are not 1 to 16
+ * apart counts as empty, a position
  * outside the RoPE table is skipped; pic_sync then reports PIC_ERR_INVALID_ARG once. No such
  * value makes a kernel read or write out of bounds. The RoPE table must hold pure rotations by
  * p times one angle per pair (pic_op_rope_table): the tensor-core kernel composes the angle of a

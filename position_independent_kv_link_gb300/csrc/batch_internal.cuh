@@ -92,7 +92,7 @@ static __device__ __noinline__ int plan_rows(const BatchView& v, int r, int& row
   return request_rows(v, r, row0, bad);
 }
 // Row block b: of the n_pre prefix blocks, else of a request (one: request b - n_pre has one block).
-static __device__ __noinline__ void plan_block(const BatchArgs& a, int b, int n_pre, int live, bool one, BatchBlock& out) {
+static __device__ __noinline__ void plan_block(const BatchArgs& a, int b, int n_pre, int live, bool one, BatchBlock& out, unsigned& bad) {
   const BatchView& v = a.v;
   if (b < n_pre) {
     out = prefix_block(v, live, b);
@@ -112,7 +112,7 @@ static __device__ __noinline__ void plan_block(const BatchArgs& a, int b, int n_
   int row0;
   unsigned ignored = 0;
   const int m = plan_rows(v, r, row0, ignored);
-  out = own_block(v, r, row0, m, k);
+  out = own_block(v, r, row0, m, k, &bad);
 }
 
 // The CTA's share of the plan. Every thread of the CTA (NT of them) calls it; the blocks that meet
@@ -161,7 +161,7 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
   BatchBlock kept{};
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    plan_block(a, b, n_pre, live, one, kept);
+    plan_block(a, b, n_pre, live, one, kept, bad);
     len += block_len(v, kept);
     if (block_len(v, kept) > 0 && item_len(v, kept) > most) most = item_len(v, kept);
   }
@@ -177,7 +177,7 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
     unsigned c = cum;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      if (per_b > 1) plan_block(a, b, n_pre, live, one, kept);
+      if (per_b > 1) plan_block(a, b, n_pre, live, one, kept, bad);
       kept.cum = c;
       c += block_len(v, kept);
       if (kept.cum <= s.x0 && s.x0 < c) sh.edge[0] = item_edge(v, kept, s.x0);
@@ -188,7 +188,7 @@ __device__ __forceinline__ BatchShare plan_batch(const BatchArgs& a, PlanShared&
   }
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    if (per_b > 1) plan_block(a, b, n_pre, live, one, kept);
+    if (per_b > 1) plan_block(a, b, n_pre, live, one, kept, bad);
     kept.cum = cum;
     cum += block_len(v, kept);
     if (kept.cum < s.x1 && cum > s.x0) {

@@ -50,7 +50,8 @@ struct BatchView {
 
 // what a kernel met and skipped; pic_sync reports it
 enum : unsigned {
-  kBatchBadLengths = 1,    // row_start, kv_len, n_pages or page_pos inconsistent: the request is skipped
+  kBatchBadLengths = 1,    // row_start, kv_len, n_pages or the last page's position inconsistent: the request is
+                           // skipped; a page's position and the next one's: it is taken as empty
   kBatchBadBlock = 2,      // a block id outside the pool: its page is taken as empty
   kBatchBadPosition = 4,   // a position outside the RoPE table: its page or row is skipped
   kBatchOutOfBlocks = 8,   // block_tables: not enough free blocks
@@ -116,8 +117,9 @@ PIC_HD int page_of(const BatchView& v, int r, int np, int x) {
   return lo;
 }
 
-// Row block k of request r (rows [k rb, ...) of its m rows, the first at row0): everything but cum.
-PIC_HD BatchBlock own_block(const BatchView& v, int r, int row0, int m, int k) {
+// Row block k of request r (rows [k rb, ...) of its m rows, the first at row0): everything but cum. At least one page,
+// whatever order page_pos has (bad: a flag when its order shows).
+PIC_HD BatchBlock own_block(const BatchView& v, int r, int row0, int m, int k, unsigned* bad = nullptr) {
   BatchBlock b{};
   const int a = k * v.rb;
   b.req = r;
@@ -127,10 +129,14 @@ PIC_HD BatchBlock own_block(const BatchView& v, int r, int row0, int m, int k) {
   b.pos0 = b.end - m + a;
   b.np = own_pages(v, r);
   const int last = b.pos0 + b.nrows - 1;
-  const int pe = a + b.nrows == m ? b.np : page_of(v, r, b.np, last) + 1;
+  int pe = a + b.nrows == m ? b.np : page_of(v, r, b.np, last) + 1;
   // keys below b.pos0 - window + 1 are seen by no row of the block, but for the first `sinks`
   const int lo = b.pos0 - v.window + 1;
   b.wp = lo > own_first(v) ? page_of(v, r, b.np, lo) : 0;
+  if (pe <= b.wp) {
+    pe = b.wp + 1;
+    if (bad) *bad |= kBatchBadLengths;
+  }
   b.sp = v.sinks > 0 ? pmin(b.wp, page_of(v, r, b.np, pmin(v.sinks - 1, last)) + 1) : 0;
   if (v.whole_tiles) b.sp = pmin(b.wp, pdiv(b.sp, v.kpages) * v.kpages);
   b.nv = b.sp + pe - b.wp;
@@ -220,6 +226,7 @@ PIC_HD PageRaw page_raw(const BatchView& v, const BatchBlock& b, int i) {
   m.blk = (pre ? v.pre_blocks : v.block_table)[at + p];
   m.pos = pos ? pos[at + p] : (pre ? 0 : own_first(v)) + kPage * p;
   m.end = pos && p + 1 < (pre ? v.pre_pages : b.np) ? pos[at + p + 1] : pre ? v.pre_len : b.end;
+  if (!pos) m.end = pmin(m.end, m.pos + kPage);
   return m;
 }
 // What of it block b uses, checked.
@@ -230,6 +237,9 @@ PIC_HD PageMeta page_meta(const BatchView& v, const BatchBlock& b, const PageRaw
   if (m.pos < 0 || m.pos > v.rope_positions - len) {
     bad |= kBatchBadPosition;
     m.pos = 0;
+    len = 0;
+  } else if (end <= m.pos || end - m.pos > kPage) {   // no page holds none or more than kPage
+    bad |= kBatchBadLengths;
     len = 0;
   }
   if (m.blk < 0 || m.blk >= v.pool_blocks) {

@@ -33,7 +33,7 @@ int batch_walk_host(const int* p, const int* row_start, const int* kv_len, const
   for (int r = 0; r < v.n_reqs; ++r) {
     int row0;
     const int m = request_rows(v, r, row0, bad);
-    for (int k = 0; k < pdiv(m, v.rb); ++k) blocks.push_back(own_block(v, r, row0, m, k));
+    for (int k = 0; k < pdiv(m, v.rb); ++k) blocks.push_back(own_block(v, r, row0, m, k, &bad));
   }
   const int nb = (int)blocks.size();
   if (nb > max_blocks) return 1;

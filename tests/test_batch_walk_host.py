@@ -73,3 +73,37 @@ def test_garbage_row_starts(walk):
         b["row_start"] = a
         _, _, lost = check(walk, b, mrows=16)
         assert lost == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(20, 0), (20, 40), (2 ** 31 - 1, 0), (90, 3)])
+@pytest.mark.parametrize("costs,grid", [((32, 8, 8), 152), ((17, 8, 8), 5), ((1, 2, 2), 304), ((24, 8, 6), 1)], ids=str)
+def test_page_positions_that_do_not_ascend(walk, window, sinks, costs, grid):
+    """Requests with page_pos in any order between good ones: each has some tiles of its own, the good ones have all of
+    theirs, and what the shuffled ones list is flagged where it does not fit."""
+    flagged = 0
+    for seed in range(60):
+        rng = np.random.default_rng(seed)
+        b = batch([180, 150, 200, 90, 170], [1, 100, 180, 60, 9], ragged=True, prefix=33, seed=seed)
+        good, *_ = check(walk, b, window=window, sinks=sinks, mrows=16, costs=costs, grid=grid)
+        for r in (1, 3):
+            n = b["n_pages"][r]
+            b["page_pos"][r, :n - 1] = rng.permutation(b["page_pos"][r, :n - 1]) + rng.integers(-5, 6, n - 1)
+        got, bad, _ = check(walk, b, window=window, sinks=sinks, mrows=16, costs=costs, grid=grid)
+        keep = lambda x: x[~np.isin(x[:, 0], (1, 3))].tolist()
+        assert keep(got) == keep(good)
+        flagged += bool(bad & BAD_LENGTHS)
+    if window > 200:
+        assert flagged == 60               # every page is listed there
+
+
+def test_pages_whose_positions_do_not_fit_are_flagged(walk):
+    for i, x in ((2, 20), (2, 16), (2, 50), (3, 95)):        # of 0 16 32 48 64 80
+        b = batch([96], [1], prefix=0, seed=2)
+        b["page_pos"], b["n_pages"] = np.zeros_like(b["table"]), [6]
+        b["page_pos"][0, :6] = 16 * np.arange(6)
+        assert check(walk, b)[1] == 0
+        b["page_pos"][0, i] = x
+        assert check(walk, b)[1] == BAD_LENGTHS
+    b = batch([5], [1], ragged=True, prefix=96, seed=2)
+    b["pre_pos"], b["pre_blocks"] = np.array([0, 16, 32, 64, 80]), b["pre_blocks"][:5]
+    assert check(walk, b)[1] == BAD_LENGTHS                  # positions 48 to 63 in no page
