@@ -405,6 +405,9 @@ def attention_plan(dtype: torch.dtype, n_heads: int, n_kv_heads: int, head_dim: 
 #
 # A step makes these calls once per layer, so what they check is checked cheaply (get_device, size
 # and dim rather than device and shape objects; the message is put together only on refusal).
+#
+# With `stream`, a call runs there (the current stream when None), behind what the caller has ordered that stream behind;
+# tensors that the call makes for its results belong to that stream (record_stream where another one uses them).
 
 _I32, _F32 = torch.int32, torch.float32
 
@@ -438,6 +441,15 @@ def _device_index(x: torch.Tensor) -> int:
 def _raw_stream(idx: int) -> int:
     """The current stream's handle (a stream object costs a microsecond)."""
     return torch._C._cuda_getCurrentRawStream(idx)
+
+
+def _empty(stream: Optional[torch.cuda.Stream], shape, dtype, device) -> torch.Tensor:
+    """An empty tensor out of the memory of the call's stream (the current one when None): what is dropped while the
+    call is still under way is then given to nothing that does not wait for it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _call(idx: int, stream: Optional[torch.cuda.Stream], f, *args):
@@ -513,7 +525,7 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
         if max_rows < 1:
             raise ValueError("max_rows must be at least 1")
         # one buffer for all: [n], [n], [n + 1], [max_rows], [max_rows], [3]
-        buf = torch.empty(3 * n + 4 + 2 * max_rows, dtype=_I32, device=kv_len.device)
+        buf = _empty(stream, 3 * n + 4 + 2 * max_rows, _I32, kv_len.device)
         at = buf.data_ptr()
         ptrs = (at, at + 4 * n, at + 8 * n, at + 12 * n + 4, at + 12 * n + 4 + 4 * max_rows,
                 at + 12 * n + 4 + 8 * max_rows)
@@ -560,7 +572,7 @@ def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torc
                          f"{qkv.dtype} {list(qkv.shape)} (strides {list(qkv.stride())})")
     T = qkv.size(0)
     if q_out is None:
-        q_out = torch.empty((T, n_heads, D), dtype=act, device=qkv.device)
+        q_out = _empty(stream, (T, n_heads, D), act, qkv.device)
         qo = q_out.data_ptr()
     else:
         qo = _ptr(q_out, "q_out", act, (T, n_heads, D), idx)
@@ -579,7 +591,7 @@ def _attention_scratch(idx, *shape) -> int:
         return max(256, L.load().pic_op_attention_batch_scratch_bytes(*shape))
 
 
-def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len, prefix_pages):
+def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, prefix_len, prefix_pages, stream):
     idx = _device_index(q)
     nb, G, D, dt, act, kp, vp, rp, positions = _pool_args(k_layer, v_layer, rope, idx)
     rows = q.shape
@@ -589,13 +601,13 @@ def _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch, 
     qp = _ptr(q, "q", act, rows, idx)
     n, pg = pages._args(idx)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, rows, act, q.device)
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", act, rows, idx)
     if scratch is None:
         nbytes = _attention_scratch(idx, dt, T, n, H, G, D, pg[2], prefix_len, prefix_pages)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        scratch = _empty(stream, nbytes, torch.uint8, q.device)
         sp = scratch.data_ptr()
     else:
         sp, nbytes = _vec(scratch, "scratch", torch.uint8, idx), scratch.numel()
@@ -609,10 +621,9 @@ def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages
                      stream=None) -> torch.Tensor:
     """Attention of a batch over its pages with a sliding window and `sinks` first tokens that stay visible
     (pic_op_attention_window). q: rotated [T, H, D], fp16 for bf16 pools, fp32 for fp32 pools; so is the result. Rows
-    that belong to no request are left alone (uninitialised unless `out` is given). Buffers made here belong to
-    the current stream; with another `stream`, pass `out` and `scratch`."""
+    that belong to no request are left alone (uninitialised unless `out` is given)."""
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
-                                                            0, 0)
+                                                            0, 0, stream)
     _call(idx, stream, L.load().pic_op_attention_window, *head, n, *pg, window, sinks, *tail)
     return out
 
@@ -626,7 +637,7 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
     n_pre = prefix_blocks.numel()
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
-                                                            prefix_len, n_pre)
+                                                            prefix_len, n_pre, stream)
     _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, idx),
           None if prefix_pos is None else _ptr(prefix_pos, "prefix_pos", _I32, (n_pre,), idx), n_pre, prefix_len, n, *pg, *tail)
     return out
