@@ -431,6 +431,13 @@ def _vec(x: torch.Tensor, what: str, dtype, idx: int) -> int:
     return x.data_ptr()
 
 
+def _int(x: int, what: str) -> int:
+    """An int of the C calls (ctypes drops the bits that 32 do not hold)."""
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{what}: {x} does not fit 32 bits")
+    return x
+
+
 def _device_index(x: torch.Tensor) -> int:
     idx = x.get_device()
     if idx < 0:
@@ -484,7 +491,8 @@ class BatchPages:
         n, both = kv.numel(), table.shape
         if len(both) != 2 or both[0] != n:
             _refuse(table, "block_table", _I32, (n, "stride"), idx)
-        return n, (_vec(kv, "kv_len", _I32, idx), _ptr(table, "block_table", _I32, both, idx), both[1],
+        return n, (_vec(kv, "kv_len", _I32, idx), _ptr(table, "block_table", _I32, both, idx),
+                   _int(both[1], "pages of a table row"),
                    None if pos is None else _ptr(pos, "page_pos", _I32, both, idx),
                    None if np_ is None else _ptr(np_, "n_pages", _I32, (n,), idx))
 
@@ -516,11 +524,12 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
     if len(both) != 2 or both[0] != n:
         _refuse(block_table, "block_table", _I32, (n, "stride"), idx)
     args = (n, _vec(kv_len, "kv_len", _I32, idx), _ptr(new_len, "new_len", _I32, (n,), idx),
-            _ptr(block_table, "block_table", _I32, both, idx), both[1],
+            _ptr(block_table, "block_table", _I32, both, idx), _int(both[1], "pages of a table row"),
             None if page_pos is None else _ptr(page_pos, "page_pos", _I32, both, idx),
             None if n_pages is None else _ptr(n_pages, "n_pages", _I32, (n,), idx),
-            _vec(free_blocks, "free_blocks", _I32, idx), free_blocks.numel(),
-            None if free_used is None else _ptr(free_used, "free_used", _I32, (1,), idx), first, max_rows)
+            _vec(free_blocks, "free_blocks", _I32, idx), _int(free_blocks.numel(), "free_blocks"),
+            None if free_used is None else _ptr(free_used, "free_used", _I32, (1,), idx), _int(first, "first"),
+            _int(max_rows, "max_rows"))
     if out is None:
         if max_rows < 1:
             raise ValueError("max_rows must be at least 1")
@@ -566,7 +575,7 @@ def qk_norm_rope(qkv: torch.Tensor, n_heads: int, n_kv_heads: int, row_pos: torc
     bf16 pools, fp32 for fp32 pools; rows with row_slot -1 are left alone."""
     idx = _device_index(qkv)
     nb, G, D, dt, act, kp, vp, rp, positions = _pool_args(k_layer, v_layer, rope, idx)
-    width = (n_heads + 2 * n_kv_heads) * D
+    width = (_int(n_heads, "n_heads") + 2 * n_kv_heads) * D
     if qkv.dim() != 2 or qkv.dtype is not _F32 or qkv.stride(1) != 1 or qkv.size(1) < width or G != n_kv_heads:
         raise ValueError(f"qkv: fp32 rows of at least {width} values for pools of {G} KV heads are needed, got "
                          f"{qkv.dtype} {list(qkv.shape)} (strides {list(qkv.stride())})")
@@ -622,9 +631,10 @@ def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages
     """Attention of a batch over its pages with a sliding window and `sinks` first tokens that stay visible
     (pic_op_attention_window). q: rotated [T, H, D], fp16 for bf16 pools, fp32 for fp32 pools; so is the result. Rows
     that belong to no request are left alone (uninitialised unless `out` is given)."""
+    seen = _int(window, "window"), _int(sinks, "sinks")
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
                                                             0, 0, stream)
-    _call(idx, stream, L.load().pic_op_attention_window, *head, n, *pg, window, sinks, *tail)
+    _call(idx, stream, L.load().pic_op_attention_window, *head, n, *pg, *seen, *tail)
     return out
 
 
@@ -635,9 +645,9 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     """Attention of a batch whose requests share the prefix_len first positions (pic_op_attention_prefix): the pages
     prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
-    n_pre = prefix_blocks.numel()
+    n_pre = _int(prefix_blocks.numel(), "prefix_blocks")
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
-                                                            prefix_len, n_pre, stream)
+                                                            _int(prefix_len, "prefix_len"), n_pre, stream)
     _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, idx),
           None if prefix_pos is None else _ptr(prefix_pos, "prefix_pos", _I32, (n_pre,), idx), n_pre, prefix_len, n, *pg, *tail)
     return out
