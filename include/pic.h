@@ -475,7 +475,7 @@ pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int3
  * (sqrt(mean(x^2) + eps) over the head) times q_gain / k_gain ([head_dim], NULL: no norm);
  * q_out[t][h] = RoPE(q, row_pos[t]) in fp16 for bf16 pools, fp32 for fp32 pools; k (before RoPE)
  * and v go to slot row_slot[t] of one layer of the pools. A row with row_slot -1 is padding:
- * nothing is written for it. Slots must be distinct. Values bound for fp16 operands are
+ * nothing is written for it. Slots must be distinct; q_out must not overlap qkv. Values bound for fp16 operands are
  * checked against fp16's range as everywhere (PIC_ERR_RANGE from pic_sync). */
 pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                const float* qkv, int64_t qkv_stride, const float* q_gain, const float* k_gain,

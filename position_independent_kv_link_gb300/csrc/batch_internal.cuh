@@ -41,6 +41,12 @@ struct BatchArgs {
   float* seg_o;           // [2][T][H][D]
 };
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y ? y - x < na : x - y < nb;
+}
+
 __device__ __forceinline__ void batch_flag(unsigned* flag, unsigned bad) {
   if (bad) atomicOr(flag, bad);
 }

@@ -541,6 +541,8 @@ pic_status check_common(int32_t dtype, int32_t T, int32_t n_reqs, int32_t H, int
       ((uintptr_t)scratch & 255))
     return fail(PIC_ERR_INVALID_ARG,
                 "q, pools and RoPE table must be 16-byte, out 32-byte, scratch 256-byte aligned");
+  const size_t size = (size_t)T * H * D * (dtype == PIC_BF16 ? 2 : 4);
+  if (overlap(q, size, out, size)) return fail(PIC_ERR_INVALID_ARG, "out must not overlap q");
   return PIC_OK;
 }
 

@@ -286,6 +286,9 @@ pic_status pic_op_qk_norm_rope(int32_t dtype, int32_t T, int32_t n_heads, int32_
   if (!aligned16(qkv) || !aligned16(rope_cs) || !aligned16(q_out) || !aligned16(k_layer) || !aligned16(v_layer) ||
       !aligned16(q_gain) || !aligned16(k_gain))
     return fail(PIC_ERR_INVALID_ARG, "qkv, gains, RoPE table, q_out and pools must be 16-byte aligned");
+  if (overlap(qkv, 4 * ((size_t)(T - 1) * qkv_stride + (size_t)(n_heads + 2 * n_kv_heads) * head_dim), q_out,
+              (size_t)T * n_heads * head_dim * (dtype == PIC_BF16 ? 2 : 4)))
+    return fail(PIC_ERR_INVALID_ARG, "q_out must not overlap qkv");
   unsigned* flag = nullptr;
   pic_status e = batch_flag_address(&flag);
   if (e != PIC_OK) return e;
