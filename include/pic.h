@@ -443,9 +443,9 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  * stay as they were), a page whose block lies outside the pool or whose position and the next page's are not 1 to 16
  * apart counts as empty, a position
  * outside the RoPE table is skipped; pic_sync then reports PIC_ERR_INVALID_ARG once. No such
- * value makes a kernel read or write out of bounds. The RoPE table must hold pure rotations by
- * p times one angle per pair (pic_op_rope_table): the tensor-core kernel composes the angle of a
- * key from those of its page's row 0 and of its row within the page.
+ * value makes a kernel read or write out of bounds. Row p of the RoPE table must be row 0 turned by
+ * p times one angle per pair (pic_op_rope_table, or that times a factor per pair): the tensor-core kernel
+ * composes a key's row from that of its page's row 0 and the angle of its row within the page.
  * head_dim is 64 or 128, at most 16 query heads share a KV head (PIC_ERR_UNSUPPORTED beyond).
  * Calls on several streams at once need scratch of their own each. */
 

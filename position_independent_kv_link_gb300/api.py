@@ -630,7 +630,8 @@ def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages
                      stream=None) -> torch.Tensor:
     """Attention of a batch over its pages with a sliding window and `sinks` first tokens that stay visible
     (pic_op_attention_window). q: rotated [T, H, D], fp16 for bf16 pools, fp32 for fp32 pools; so is the result. Rows
-    that belong to no request are left alone (uninitialised unless `out` is given)."""
+    that belong to no request are left alone (uninitialised unless `out` is given). rope [positions, D / 2, 2]: row p is
+    row 0 turned by p times one angle per pair (rope_table, or that times a factor per pair)."""
     seen = _int(window, "window"), _int(sinks, "sinks")
     idx, out, scratch, head, n, pg, tail = _attention_batch(q, k_layer, v_layer, rope, pages, row_start, out, scratch,
                                                             0, 0, stream)
