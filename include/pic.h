@@ -287,6 +287,8 @@ pic_status pic_release_request(pic_store* s, pic_request r);
  * 65504 in magnitude, a stored V above 65504 or a stored K above 46000 (RoPE can grow a K
  * component by up to sqrt 2). The pages fix no precision beyond bf16 storage; the fp16
  * operands are this library's reading, and this check is where a model outside it shows.
+ * Else what the batched calls on device-resident lengths skipped or could not do: PIC_ERR_INVALID_ARG for device metadata
+ * that does not fit together, else PIC_ERR_CAPACITY, else PIC_ERR_OUT_OF_BLOCKS.
  * s may be NULL. */
 pic_status pic_sync(pic_store* s, pic_stream_t stream);
 

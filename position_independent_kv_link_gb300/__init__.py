@@ -9,13 +9,13 @@ from ._lib import LIB_PATH, PicError, load  # noqa: F401
 
 __all__ = ["LIB_PATH", "PicError", "load", "PicModel", "PicStore", "gemm", "gemm_packed", "pack_weight", "attention",
            "attention_plan", "rope_table", "BatchPages", "BlockTables", "block_tables", "qk_norm_rope",
-           "attention_window", "attention_prefix"]
+           "attention_window", "attention_prefix", "sync"]
 
 
 def __getattr__(name):
     if name in ("PicModel", "PicStore", "gemm", "gemm_packed", "pack_weight", "attention", "attention_plan",
                 "rope_table", "LinkResult", "DecodeResult", "BatchPages", "BlockTables", "block_tables", "qk_norm_rope",
-                "attention_window", "attention_prefix"):
+                "attention_window", "attention_prefix", "sync"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

@@ -652,3 +652,10 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     _call(idx, stream, L.load().pic_op_attention_prefix, *head, _vec(prefix_blocks, "prefix_blocks", _I32, idx),
           None if prefix_pos is None else _ptr(prefix_pos, "prefix_pos", _I32, (n_pre,), idx), n_pre, prefix_len, n, *pg, *tail)
     return out
+
+
+def sync(stream: Optional[torch.cuda.Stream] = None):
+    """Waits for the stream (the current one when None) and raises PicError for what the calls on its device met since the
+    last time (pic_sync): lengths, blocks and positions that were skipped, too few free blocks, values beyond fp16.
+    PicStore.sync is the same."""
+    _call(torch.cuda.current_device() if stream is None else stream.device_index, stream, L.load().pic_sync, None)
