@@ -177,8 +177,8 @@ PIC_HD unsigned block_len(const BatchView& v, const BatchBlock& b) {
 }
 // No plan over tables of this width is longer: every row block as long as its table allows.
 inline double axis_bound(const BatchView& v, double n_own, double n_prefix) {
-  const double item = v.cost_item + (pdiv(v.stride, v.kpages) + 1.0) * v.cost_full;
-  const double pre = v.cost_item + (pdiv(v.pre_pages, v.kpages) + 1.0) * v.cost_full;
+  const double item = v.cost_item + (v.stride / v.kpages + 2.0) * v.cost_full;
+  const double pre = v.cost_item + (v.pre_pages / v.kpages + 2.0) * v.cost_full;
   return (n_own * item + n_prefix * pre) * v.G;
 }
 // When the longest item is at most 1 / kWholeItems of a share, none is cut: the longest share is then at most

@@ -439,6 +439,19 @@ void set_shape(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
   }
 }
 
+// Whether 31 bits hold the plans' cost axes, if need be with a unit for each tile, and 32 the merge's rows.
+bool fits_plan(BatchCall& c) {
+  bool fits = 2.0 * c.a[0].v.T * c.a[0].H < 4294967295.0;
+  for (int i = 0; i < c.n; ++i) {
+    BatchView& v = c.a[i].v;
+    const double n_own = v.only == 1 ? 0.0 : v.T / v.rb + (double)v.n_reqs;
+    const double n_pre = v.pre_len > 0 && v.only != 2 ? v.T / v.rb + 1.0 : 0.0;
+    if (axis_bound(v, n_own, n_pre) >= 2147483647.0) v.cost_item = v.cost_full = v.cost_half = 1;
+    fits = fits && axis_bound(v, n_own, n_pre) < 2147483647.0;
+  }
+  return fits;
+}
+
 // Scratch layout of a call (bytes); `base` null: the size alone.
 size_t layout(BatchCall& c, char* base) {
   size_t o = 0;
@@ -482,15 +495,7 @@ pic_status run(BatchCall& c, int dtype, int T, int n_reqs, int H, int G, int D, 
                cudaStream_t st) {
   const BatchView v0 = c.a[0].v;
   set_shape(c, dtype, T, n_reqs, H, G, D, v0.stride, v0.pre_len, v0.pre_pages);
-  bool fits = 2.0 * T * H < 4294967295.0;
-  for (int i = 0; i < c.n; ++i) {
-    BatchView& v = c.a[i].v;
-    const double n_own = v.only == 1 ? 0.0 : T / v.rb + (double)n_reqs;
-    const double n_pre = v.pre_len > 0 && v.only != 2 ? T / v.rb + 1.0 : 0.0;
-    if (axis_bound(v, n_own, n_pre) >= 2147483647.0) v.cost_item = v.cost_full = v.cost_half = 1;
-    fits = fits && axis_bound(v, n_own, n_pre) < 2147483647.0;
-  }
-  if (!fits)
+  if (!fits_plan(c))
     return fail(PIC_ERR_CAPACITY, "batch too large: rows x heads, or row blocks x KV heads x pages of a table row");
   if (scratch_bytes < layout(c, nullptr)) return fail(PIC_ERR_INVALID_ARG, "attention scratch too small");
   unsigned* flag = nullptr;
@@ -639,7 +644,7 @@ size_t pic_op_attention_batch_scratch_bytes(int32_t dtype, int32_t T, int32_t n_
     return 0;
   BatchCall c;
   set_shape(c, dtype, T, n_reqs, n_heads, n_kv_heads, head_dim, table_stride, prefix_len, prefix_pages);
-  return layout(c, nullptr);
+  return fits_plan(c) ? layout(c, nullptr) : 0;
 }
 
 pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
