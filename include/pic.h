@@ -463,6 +463,8 @@ pic_status pic_op_rope_table(int32_t n_pos, int32_t head_dim, double base, void*
  * too few free blocks (pic_sync: PIC_ERR_OUT_OF_BLOCKS), a table row or max_rows too short
  * (PIC_ERR_CAPACITY) or lengths that do not fit together (PIC_ERR_INVALID_ARG) no table changes,
  * the lengths come out as they went in, there are no rows, and counts[2] is not 0.
+ * free_blocks holds blocks that nothing else hands out: a store (pic_store_create) hands out the blocks of its own pool, so
+ * that its linked requests' pages can be read through these calls, but not extended.
  * At most 12288 requests and tables of fewer than 2^26 entries a request (PIC_ERR_CAPACITY). One launch, two
  * with max_rows above 24576. */
 pic_status pic_op_block_tables(int32_t n_reqs, const int32_t* kv_len, const int32_t* new_len, int32_t* block_table,
@@ -516,8 +518,9 @@ pic_status pic_op_attention_window(int32_t dtype, int32_t T, int32_t n_heads, in
 /* Attention of a batch behind one shared prefix: positions [0, prefix_len) are the pages
  * prefix_blocks [prefix_pages] (device; prefix_pos: their positions, or NULL for 16 p), seen by
  * every row; each request's own pages follow at position prefix_len, seen causally. The prefix is
- * attended to by the rows of the whole batch together -- its pages are read once for all requests
- * (once per 256 rows x query heads of a KV head) -- and joined with each request's own part.
+ * attended to by the rows of the whole batch together -- its pages are read once for as many rows x query heads of a KV
+ * head as an item holds: 16 (fp32 pools; bf16 pools when that is the whole batch), up to 128 (bf16 pools), up to 256 (from
+ * 2048 in the batch on, when the pages take at most 1 GB of scratch) -- and joined with each request's own part.
  * prefix_len may be 0. q, out, rows and pages as above (kv_len counts own keys only). */
 pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                    const void* q, const int32_t* row_start, const int32_t* prefix_blocks,

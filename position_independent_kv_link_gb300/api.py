@@ -517,7 +517,8 @@ def block_tables(kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch
                  stream=None) -> BlockTables:
     """Block tables and slot maps of the next step, on the GPU (pic_op_block_tables): request r appends new_len[r]
     rows to its kv_len[r]; new pages come from free_blocks (from entry free_used[0] on) and are entered in
-    block_table (and page_pos) in place. `out`: tensors to write (out.kv_len may be kv_len, out.n_pages n_pages,
+    block_table (and page_pos) in place. They are blocks that nothing else hands out, so none of a PicStore's pool (its
+    linked requests' pages can be read by the attention calls, not extended here). `out`: tensors to write (out.kv_len may be kv_len, out.n_pages n_pages,
     and free_used out.counts[1:2])."""
     idx = _device_index(kv_len)
     n, both = kv_len.numel(), block_table.shape

@@ -142,7 +142,6 @@ PIC_HD BatchBlock own_block(const BatchView& v, int r, int row0, int m, int k, u
   b.nv = b.sp + pe - b.wp;
   return b;
 }
-// Row block k of the shared prefix over the batch's first `live` rows.
 // A request's rows as one block, its page list all its pages.
 PIC_HD BatchBlock request_block(const BatchView& v, int r, int row0, int m) {
   BatchBlock b{};
@@ -154,6 +153,7 @@ PIC_HD BatchBlock request_block(const BatchView& v, int r, int row0, int m) {
   b.pos0 = b.end - m;
   return b;
 }
+// Row block k of the shared prefix over the batch's first `live` rows.
 PIC_HD BatchBlock prefix_block(const BatchView& v, int live, int k) {
   BatchBlock b{};
   b.req = -1;
