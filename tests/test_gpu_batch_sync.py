@@ -40,3 +40,34 @@ def test_what_the_calls_met_is_raised(pkl):
     rope = torch.tensor([1.0, 0.0], device="cuda").expand(16, 32, 2).contiguous()
     pkl.qk_norm_rope(x, 1, 1, i32([0]), i32([0]), rope, k, k.clone())
     assert raised().status == L.PIC_ERR_RANGE
+
+
+COPIES = """
+import torch
+from torch.profiler import ProfilerActivity, profile
+import position_independent_kv_link_gb300 as pkl
+
+def copies():
+    with profile(activities=[ProfilerActivity.CUDA]) as p:
+        pkl.sync()
+        torch.cuda.synchronize()
+    return sum(e.count for e in p.key_averages() if "Memcpy DtoH" in e.key)
+
+torch.zeros(1, device="cuda")
+copies()
+before = copies()
+i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+pkl.block_tables(i(3), i(1), i(7).view(1, 1), i(8), 2)
+print("copies", before, copies())
+"""
+
+
+def test_programs_without_batched_calls_read_no_flag_of_theirs(pkl):
+    """pic_sync reads three words of the store's kernels, and a fourth only once a batched call has been made."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", COPIES], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "copies 3 4" in r.stdout, r.stdout
