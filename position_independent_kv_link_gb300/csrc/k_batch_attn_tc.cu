@@ -41,7 +41,7 @@
 // order 1) the result's error was twice that of its rounding alone. P is two bf16 numbers (16 bits; V is stored bf16,
 // and both operands of a product have one type) in two PV products. Error against 64 bits relative to the result's
 // norm: 2.1e-4, that of rounding it. One fp16 K and one bf16 P: 1.7e-3, and 16 to 20 % faster; P as one fp16
-// number with V as fp16, in the two-tile form, 2.7e-4 to 2.9e-4, and 18 % faster.
+// number with V as fp16, in the two-tile form, 2.7e-4 to 2.9e-4, and 15 to 19 % faster.
 //
 // The roles' loops are kept small, and few on each scheduler: with three times the code every role ran
 // at 8 cycles an instruction (ncu: no_instruction the largest stall).
@@ -51,11 +51,11 @@
 // than the MMAs.
 //
 // Measured, 8 KV heads of 4 query heads, D = 128, whole call: 32 decoding requests of 3000 to 32000 keys, window
-// 4096 (0.53 GB of K and V): 114 us, 4.7 TB/s, about 850 ns a key tile of 64; neither HBM, tensor pipe nor issue slots are
+// 4096 (0.53 GB of K and V): 115 us, 4.7 TB/s, about 850 ns a key tile of 64; neither HBM, tensor pipe nor issue slots are
 // full: the roles' waits for one another bound it. (With tiles of 128 rows, 124 us: without K's second product 115, without
 // the rotation's arithmetic 119, without P's second product 121.) Two prompts of 4096, window 1024 (121 GFLOP by the
-// formula): 200 us, 0.60 PFLOP/s of the formula's; 268 GFLOP with both operands' second parts and the masked edges of the
-// tiles, 144 us at 1865 TFLOP/s, bound it, with 32 us of rotation ahead and item ends.
+// formula): 203 us, 0.60 PFLOP/s of the formula's; 268 GFLOP with both operands' second parts and the masked edges of the
+// tiles are 144 us at 1865 TFLOP/s; rotation ahead and item ends 32, tensor pipe 65 % busy.
 //
 // Every wait is bounded: on expiry the CTA raises the timeout flag, stops issuing, waits (bounded)
 // for what is in flight, frees its TMEM and returns.

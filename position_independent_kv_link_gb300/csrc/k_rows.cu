@@ -169,7 +169,7 @@ __global__ void qkv_epilogue_kernel(int H, int G, int D, const float* __restrict
 // it uses the first; few rows are split over gridDim.y CTAs by heads. Small CTAs keep loads coming
 // while others store: 8192 rows of 32 + 8 + 8 heads of 128 to bf16 pools take 63 us with 256 threads
 // and 6 heads in flight, 55 us (5.5 TB/s) with these, 68 us with 128 threads and 12; without the
-// stores of q 46 us. 64 such rows take 3.5 us (latency: three loads that depend on one another).
+// stores of q 46 us. 64 such rows take 3.0 us (latency: three loads that depend on one another).
 constexpr int kNormThreads = 128, kHeadsInFlight = 4;
 template <typename T, typename A, int D>
 __global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(
