@@ -172,9 +172,10 @@ def _norm_plain(s):
 def _logprob_plain(s):
     x = s["logits"].float()
     m = x.amax(-1, keepdim=True)
-    x = x - m
+    x = x - torch.where(m.isinf(), 0.0, m)
     p = x.exp()
     total = p.sum(-1)
+    total = torch.where(total > 0, total, 1.0)          # a row without a token: -inf throughout, entropy 0
     log_total = total.log()
     weighted = torch.where(p > 0, p * x, 0).sum(-1)
     out = dict(logprob=x.gather(1, s["tokens"].long()[:, None])[:, 0] - log_total, entropy=log_total - weighted / total)
@@ -260,7 +261,8 @@ def exact(case, seed):
     logprob, entropy, ids, tops = [], [], [], []
     for a in range(0, case["T"], 64):
         x = s["logits"][a:a + 64].double()
-        lp = x - torch.logsumexp(x, dim=-1, keepdim=True)
+        lse = torch.logsumexp(x, dim=-1, keepdim=True)
+        lp = x - torch.where(lse.isinf(), 0.0, lse)         # all masked: -inf throughout
         seen = torch.isfinite(lp)
         logprob.append(lp[torch.arange(len(lp), device="cuda"), s["tokens"][a:a + 64].long()])
         entropy.append(-torch.where(seen, lp.exp() * lp, 0.0).sum(-1))
