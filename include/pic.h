@@ -58,7 +58,7 @@ typedef enum {
                                   range; the outputs since the last pic_sync are invalid */
 } pic_status;
 
-typedef enum { PIC_F32 = 0, PIC_BF16 = 1 } pic_dtype;
+typedef enum { PIC_F32 = 0, PIC_BF16 = 1, PIC_F16 = 2, PIC_E4M3 = 3 } pic_dtype; /* the last two: of the decode-step calls only */
 
 typedef int32_t pic_chunk;    /* > 0 when valid */
 typedef int32_t pic_request;  /* > 0 when valid */
@@ -287,8 +287,9 @@ pic_status pic_release_request(pic_store* s, pic_request r);
  * 65504 in magnitude, a stored V above 65504 or a stored K above 46000 (RoPE can grow a K
  * component by up to sqrt 2). The pages fix no precision beyond bf16 storage; the fp16
  * operands are this library's reading, and this check is where a model outside it shows.
- * Else what the batched calls on device-resident lengths skipped or could not do: PIC_ERR_INVALID_ARG for device metadata
- * that does not fit together, else PIC_ERR_CAPACITY, else PIC_ERR_OUT_OF_BLOCKS.
+ * Else what the batched calls on device-resident lengths and the decode-step calls skipped or could not do: PIC_ERR_DEVICE_TIMEOUT
+ * and PIC_ERR_RANGE as above, then PIC_ERR_INVALID_ARG for device metadata that does not fit together (tokens and codes
+ * out of range among it), else PIC_ERR_CAPACITY, else PIC_ERR_OUT_OF_BLOCKS.
  * s may be NULL. */
 pic_status pic_sync(pic_store* s, pic_stream_t stream);
 
@@ -530,6 +531,67 @@ pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, in
                                    const void* v_layer, int32_t pool_blocks, const void* rope_cs,
                                    int32_t rope_positions, void* out, void* scratch, size_t scratch_bytes,
                                    pic_stream_t stream);
+
+/* ------------------------------------------------------------------ decode-step calls
+ * The rest of a decode (or append) step between the batched calls above: products of few rows with 4-bit weights, the
+ * residual's addition with the norm, and the log probabilities of tokens. Nothing is allocated and nothing is read on the
+ * host, so that the calls can be captured with the others; they need no scratch and may run on several streams at once.
+ * The same call gives the same bits again.
+ *
+ * 4-bit weights: W[n][k] = scale[n][k / group] * (code[n][k] - zero[n][k / group]), codes and zeros in 0..15, scales in fp16,
+ * group 32, 64 or 128 columns (the last one of a row may be shorter). N >= 1, K a multiple of 32.
+ * Packed layout (pic_op_weight4_bytes bytes, 128-byte aligned): tiles of 128 rows x 128 columns, tile (n / 128, k / 128) at
+ * ((n / 128) * ceil(K / 128) + k / 128) * tile_bytes, tile_bytes = 8192 + (128 / group) * 384. A tile is
+ *   [4][128 rows][16 bytes] codes: the bytes of a row hold 32 columns, each 32-bit word 8 of them, column e of the 8 in bits
+ *                           4 i .. 4 i + 3 with i = e / 2 + 4 (e % 2);
+ *   [128 / group][128 rows] scales (fp16), then [128 / group][128 rows] zeros (bytes);
+ * rows behind N and columns behind K stand for 0. */
+size_t pic_op_weight4_bytes(int32_t N, int32_t K, int32_t group); /* 0 for shapes that the calls refuse */
+
+/* W [N][K] in `dtype` (PIC_F32, PIC_BF16, PIC_F16; 16-byte aligned) to 4 bits. For each row and group, with lo = min(0, least
+ * weight) and hi = max(0, greatest weight): scale = fp16(fp32((hi - lo) / 15)); zero = -lo / scale and code = w / scale + zero,
+ * rounded to the nearest integer (ties to even, the quotients decided exactly) and held to 0..15. A scale that rounds to 0
+ * gives a group of zeros. A group whose weights are not all finite, or whose scale exceeds fp16, is flagged (PIC_ERR_RANGE from
+ * pic_sync) and stands for zeros. */
+pic_status pic_op_pack_weight4(int32_t dtype, const void* W, void* out, int32_t N, int32_t K, int32_t group,
+                               pic_stream_t stream);
+/* The same layout from codes [N][K] (one per byte), scales [N][ceil(K / group)] (fp16) and zeros, shaped as the scales (NULL:
+ * 8 throughout), as other quantisers give them. Codes and zeros above 15 are flagged (PIC_ERR_INVALID_ARG from pic_sync)
+ * and lose their upper bits. */
+pic_status pic_op_pack_codes4(const uint8_t* codes, const void* scales, const uint8_t* zeros, void* out, int32_t N,
+                              int32_t K, int32_t group, pic_stream_t stream);
+/* The fp32 values [N][K] that a packed matrix stands for (each exact). */
+pic_status pic_op_unpack_weight4(const void* W4, float* W, int32_t N, int32_t K, int32_t group, pic_stream_t stream);
+
+/* Y[T][N] (fp32, overwritten) = X[T][K] . W^T with W in the layout above. x_dtype PIC_F16: X fp16, x_scales NULL.
+ * PIC_E4M3: X 8-bit, x_scales fp32 [T][ceil(K / 128)]: X[t][k] stands for that value times x_scales[t][k / 128]
+ * (pic_op_add_rms_norm writes both). x_stride: elements from row to row, its bytes a multiple of 16; X, Y 16-byte aligned.
+ * Products are exact, sums fp32, each group's sum times its scale in fp32. Made for few rows: the weights are read once
+ * for every 64. Y must not overlap X or W4. T up to 4194240. */
+pic_status pic_op_gemm_w4(int32_t x_dtype, const void* W4, const void* X, int64_t x_stride, const float* x_scales,
+                          float* Y, int32_t N, int32_t K, int32_t T, int32_t group, pic_stream_t stream);
+
+/* h[t] += delta[t] (fp32 rows, in place; delta NULL: h stays as it is and is not written), then
+ * y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * gain (gain NULL: 1). out_dtype of y [T][d] (contiguous): PIC_F32; PIC_F16
+ * (values beyond fp16's range are flagged, PIC_ERR_RANGE from pic_sync); PIC_E4M3, with scales [T][ceil(d / 128)] (fp32):
+ * a group's scale is its greatest |y| / 448, its values are y / scale rounded to e4m3 (scale and values 0 where the group is
+ * 0; groups with NaN or infinity are flagged as above). scales is NULL for the other types. d a multiple of 4, up to 32768 (PIC_ERR_UNSUPPORTED
+ * beyond); strides in floats, multiples of 4; all pointers 16-byte aligned. h, delta, y and scales must not overlap. */
+pic_status pic_op_add_rms_norm(int32_t out_dtype, int32_t T, int32_t d, float* h, int64_t h_stride, const float* delta,
+                               int64_t delta_stride, const float* gain, float eps, void* y, float* scales,
+                               pic_stream_t stream);
+
+/* From logits [T][vocab] (PIC_F32, PIC_BF16 or PIC_F16; logits_stride elements from row to row, no alignment but the
+ * type's own), in one pass: logprob[t] = log softmax(logits[t])[tokens[t]]; entropy[t] = -sum p log p in nats;
+ * top_ids, top_logprobs [T][top]: the `top` (0..32, at most vocab) likeliest tokens in falling order, equal logits in ascending order of
+ * their ids. tokens and logprob may be NULL together, entropy may be NULL; top_ids and top_logprobs are NULL when top is 0.
+ * A row whose token is -1 is padding: nothing of it is read or written; other tokens outside the vocabulary are flagged
+ * (PIC_ERR_INVALID_ARG from pic_sync) and their rows left likewise. Logits of -inf are tokens without probability; a row of
+ * nothing else has -inf for every log probability and entropy 0. A row with NaN or +inf gets NaN in its floats; its
+ * alternatives are those of the order in which NaN stands with -inf. */
+pic_status pic_op_token_logprobs(int32_t dtype, int32_t T, int32_t vocab, const void* logits, int64_t logits_stride,
+                                 const int32_t* tokens, int32_t top, float* logprob, float* entropy, int32_t* top_ids,
+                                 float* top_logprobs, pic_stream_t stream);
 
 #ifdef __cplusplus
 }

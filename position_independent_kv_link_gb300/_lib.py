@@ -6,7 +6,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 
 PIC_OK, PIC_ERR_INVALID_ARG, PIC_ERR_OUT_OF_BLOCKS, PIC_ERR_CUDA, PIC_ERR_DEVICE_TIMEOUT, PIC_ERR_CAPACITY, \
     PIC_ERR_UNSUPPORTED, PIC_ERR_RANGE = range(8)
-PIC_F32, PIC_BF16 = 0, 1
+PIC_F32, PIC_BF16, PIC_F16, PIC_E4M3 = range(4)
 
 
 class ModelConfig(C.Structure):
@@ -105,6 +105,13 @@ SIGNATURES = {
                                       P, P, C.c_size_t, P]),
     "pic_op_attention_prefix": (I32, [I32, I32, I32, I32, I32, P, P, P, P, I32, I32, I32, P, P, I32, P, P, P, P, I32, P,
                                       I32, P, P, C.c_size_t, P]),
+    "pic_op_weight4_bytes": (C.c_size_t, [I32, I32, I32]),
+    "pic_op_pack_weight4": (I32, [I32, P, P, I32, I32, I32, P]),
+    "pic_op_pack_codes4": (I32, [P, P, P, P, I32, I32, I32, P]),
+    "pic_op_unpack_weight4": (I32, [P, P, I32, I32, I32, P]),
+    "pic_op_gemm_w4": (I32, [I32, P, P, C.c_int64, P, P, I32, I32, I32, I32, P]),
+    "pic_op_add_rms_norm": (I32, [I32, I32, I32, P, C.c_int64, P, C.c_int64, P, C.c_float, P, P, P]),
+    "pic_op_token_logprobs": (I32, [I32, I32, I32, P, C.c_int64, P, I32, P, P, P, P, P]),
 }
 
 _LIB = None

@@ -655,8 +655,183 @@ def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: to
     return out
 
 
+# ----------------------------------------------------------------------------- decode-step calls
+
+_E4M3, _XGROUP = torch.float8_e4m3fn, 128
+_CODE = {torch.float32: L.PIC_F32, torch.bfloat16: L.PIC_BF16, torch.float16: L.PIC_F16, torch.float8_e4m3fn: L.PIC_E4M3}
+
+
+class Weight4:
+    """A matrix [N, K] in 4 bits (pack_weight4, pack_codes4): the packed bytes (a device tensor) and its shape."""
+
+    __slots__ = ("data", "N", "K", "group")
+
+    def __init__(self, data: torch.Tensor, N: int, K: int, group: int):
+        self.data, self.N, self.K, self.group = data, N, K, group
+
+    def _args(self, idx: int):
+        return _ptr(self.data, "the packed weights", torch.uint8, (_weight4_bytes(self.N, self.K, self.group),), idx)
+
+
+@functools.lru_cache(maxsize=4096)
+def _weight4_bytes(N, K, group) -> int:
+    n = L.load().pic_op_weight4_bytes(_int(N, "N"), _int(K, "K"), _int(group, "group"))
+    if n == 0:
+        raise ValueError(f"4-bit weights of [{N}, {K}] in groups of {group}: K must be a multiple of 32, the group 32, 64 or 128")
+    return n
+
+
+def _matrix(x: torch.Tensor, what: str, dtypes, idx: int):
+    """N, K of a contiguous 2-D tensor of one of these types."""
+    if x.dim() != 2 or x.dtype not in dtypes or x.get_device() != idx or not x.is_contiguous():
+        _refuse(x, what, " or ".join(str(t) for t in dtypes), ("N", "K"), idx)
+    return x.shape
+
+
+def pack_weight4(W: torch.Tensor, group: int = 128, stream=None) -> Weight4:
+    """W [N, K] (fp32, bf16 or fp16) in 4 bits with a scale and a zero for each `group` columns (pic_op_pack_weight4)."""
+    idx = _device_index(W)
+    N, K = _matrix(W, "W", (torch.float32, torch.bfloat16, torch.float16), idx)
+    data = _empty(stream, _weight4_bytes(N, K, group), torch.uint8, W.device)
+    _call(idx, stream, L.load().pic_op_pack_weight4, _CODE[W.dtype], W.data_ptr(), data.data_ptr(), N, K, group)
+    return Weight4(data, N, K, group)
+
+
+def pack_codes4(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, group: int = 128,
+                stream=None) -> Weight4:
+    """The weights scales * (codes - zeros) (pic_op_pack_codes4): codes uint8 [N, K], scales fp16 [N, ceil(K / group)],
+    zeros uint8 shaped as the scales (None: 8)."""
+    idx = _device_index(codes)
+    N, K = _matrix(codes, "codes", (torch.uint8,), idx)
+    data = _empty(stream, _weight4_bytes(N, K, group), torch.uint8, codes.device)
+    shape = (N, -(-K // group))
+    _call(idx, stream, L.load().pic_op_pack_codes4, codes.data_ptr(), _ptr(scales, "scales", torch.float16, shape, idx),
+          None if zeros is None else _ptr(zeros, "zeros", torch.uint8, shape, idx), data.data_ptr(), N, K, group)
+    return Weight4(data, N, K, group)
+
+
+def unpack_weight4(w: Weight4, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The fp32 values [N, K] that packed weights stand for (pic_op_unpack_weight4)."""
+    idx = _device_index(w.data)
+    wp = w._args(idx)
+    if out is None:
+        out = _empty(stream, (w.N, w.K), _F32, w.data.device)
+    _call(idx, stream, L.load().pic_op_unpack_weight4, wp, _ptr(out, "out", _F32, (w.N, w.K), idx), w.N, w.K, w.group)
+    return out
+
+
+def gemm_w4(w: Weight4, X: torch.Tensor, x_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            stream=None) -> torch.Tensor:
+    """Y[T][N] (fp32) = X[T][K] @ W^T of a few rows with packed 4-bit weights (pic_op_gemm_w4). X: fp16, or
+    float8_e4m3fn with x_scales fp32 [T, ceil(K / 128)] (as add_rms_norm gives them); its rows may lie apart."""
+    idx = _device_index(X)
+    t, N, K = X.dtype, w.N, w.K
+    if X.dim() != 2 or X.size(1) != K or X.stride(1) != 1 or (t is not torch.float16 and t is not _E4M3):
+        raise ValueError(f"X: fp16 or float8_e4m3fn rows of {K} values are needed, got {t} {list(X.shape)} "
+                         f"(strides {list(X.stride())})")
+    if (t is _E4M3) != (x_scales is not None):
+        raise ValueError("x_scales come with float8_e4m3fn rows, and only with them")
+    T = X.size(0)
+    wp = w._args(idx)
+    if out is None:
+        out = _empty(stream, (T, N), _F32, X.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", _F32, (T, N), idx)
+    _call(idx, stream, L.load().pic_op_gemm_w4, _CODE[t], wp, X.data_ptr(), X.stride(0) if T > 1 else max(X.stride(0), K),
+          None if x_scales is None else _ptr(x_scales, "x_scales", _F32, (T, -(-K // _XGROUP)), idx), op, N, K, _int(T, "rows"),
+          w.group)
+    return out
+
+
+def _rows(x: torch.Tensor, what: str, d: int, idx: int):
+    """Address and row stride of fp32 rows [T, d]."""
+    if x.dim() != 2 or x.dtype is not _F32 or x.size(1) != d or x.stride(1) != 1 or x.get_device() != idx:
+        raise ValueError(f"{what}: fp32 rows of {d} values on cuda:{idx} are needed, got {x.dtype} {list(x.shape)} "
+                         f"(strides {list(x.stride())}) on {x.device}")
+    return x.data_ptr(), x.stride(0) if x.size(0) > 1 else max(x.stride(0), d)
+
+
+def add_rms_norm(h: torch.Tensor, gain: Optional[torch.Tensor] = None, delta: Optional[torch.Tensor] = None,
+                 eps: float = 1e-5, dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, stream=None):
+    """h += delta in place, then y = RMSNorm(h) * gain (pic_op_add_rms_norm). h, delta: fp32 rows [T, d], which may lie
+    apart. dtype: fp32, fp16, or float8_e4m3fn, which returns (y, scales) with fp32 scales [T, ceil(d / 128)]."""
+    idx = _device_index(h)
+    if h.dim() != 2:
+        raise ValueError(f"h is [rows, d], got {list(h.shape)}")
+    T, d = h.shape
+    hp, hs = _rows(h, "h", d, idx)
+    dp, ds = (None, 0) if delta is None else _rows(delta, "delta", d, idx)
+    if delta is not None and delta.size(0) != T:
+        raise ValueError(f"delta has {delta.size(0)} rows, h {T}")
+    if out is not None:
+        dtype = out.dtype
+    code = _CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if out is None:
+        out = _empty(stream, (T, d), dtype, h.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", dtype, (T, d), idx)
+    if dtype is not _E4M3:
+        if scales is not None:
+            raise ValueError("scales come with float8_e4m3fn, and only with it")
+        sp = None
+    elif scales is None:
+        scales = _empty(stream, (T, -(-d // _XGROUP)), _F32, h.device)
+        sp = scales.data_ptr()
+    else:
+        sp = _ptr(scales, "scales", _F32, (T, -(-d // _XGROUP)), idx)
+    _call(idx, stream, L.load().pic_op_add_rms_norm, code, _int(T, "rows"), _int(d, "d"), hp, hs, dp, ds,
+          None if gain is None else _ptr(gain, "gain", _F32, (d,), idx), eps, op, sp)
+    return out if sp is None else (out, scales)
+
+
+class TokenLogprobs:
+    """Result of token_logprobs (device tensors; None where nothing was asked for)."""
+
+    __slots__ = ("logprob", "entropy", "top_ids", "top_logprobs")
+
+    def __init__(self, logprob, entropy, top_ids, top_logprobs):
+        self.logprob = logprob              # fp32 [T]: of the given tokens
+        self.entropy = entropy              # fp32 [T], in nats
+        self.top_ids = top_ids              # int32 [T, top]: the likeliest tokens, in falling order
+        self.top_logprobs = top_logprobs    # fp32 [T, top]
+
+
+def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, top: int = 0,
+                   out: Optional[TokenLogprobs] = None, stream=None) -> TokenLogprobs:
+    """Log probabilities of the given tokens (int32 [T], -1: a padding row that is left alone), entropy and the `top`
+    likeliest tokens with theirs, from logits [T, vocab] (fp32, bf16 or fp16; rows may lie apart) in one pass
+    (pic_op_token_logprobs). `out`: tensors to write; what is None in it is not computed."""
+    idx = _device_index(logits)
+    code = _CODE.get(logits.dtype)
+    if logits.dim() != 2 or logits.stride(1) != 1 or code is None or code == L.PIC_E4M3:
+        raise ValueError(f"logits: fp32, bf16 or fp16 rows are needed, got {logits.dtype} {list(logits.shape)} "
+                         f"(strides {list(logits.stride())})")
+    T, V = logits.shape
+    _int(top, "top")
+    if top < 0 or top > min(32, V):
+        raise ValueError(f"top: 0 to 32 and at most the vocabulary, got {top}")
+    if out is None:
+        # one buffer for all: [T], [T], [T * top] each
+        buf = _empty(stream, 2 * T + 2 * T * top, _F32, logits.device)
+        p = buf.split_with_sizes([T, T, T * top, T * top])
+        out = TokenLogprobs(None if tokens is None else p[0], p[1], None if top == 0 else p[2].view(_I32).view(T, top),
+                            None if top == 0 else p[3].view(T, top))
+    given = [None if x is None else _ptr(x, what, t, shape, idx) for x, what, t, shape in (
+        (out.logprob, "out.logprob", _F32, (T,)), (out.entropy, "out.entropy", _F32, (T,)),
+        (out.top_ids, "out.top_ids", _I32, (T, top)), (out.top_logprobs, "out.top_logprobs", _F32, (T, top)))]
+    _call(idx, stream, L.load().pic_op_token_logprobs, code, _int(T, "rows"), _int(V, "vocab"), logits.data_ptr(),
+          logits.stride(0) if T > 1 else max(logits.stride(0), V),
+          None if tokens is None else _ptr(tokens, "tokens", _I32, (T,), idx), top, *given)
+    return out
+
+
 def sync(stream: Optional[torch.cuda.Stream] = None):
     """Waits for the stream (the current one when None) and raises PicError for what the calls on its device met since the
-    last time (pic_sync): lengths, blocks and positions that were skipped, too few free blocks, values beyond fp16.
+    last time (pic_sync): lengths, blocks, positions and tokens that were skipped, too few free blocks, values beyond fp16.
     PicStore.sync is the same."""
     _call(torch.cuda.current_device() if stream is None else stream.device_index, stream, L.load().pic_sync, None)

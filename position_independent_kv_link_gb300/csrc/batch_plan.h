@@ -56,7 +56,10 @@ enum : unsigned {
   kBatchBadPosition = 4,   // a position outside the RoPE table: its page or row is skipped
   kBatchOutOfBlocks = 8,   // block_tables: not enough free blocks
   kBatchCapacity = 16,     // block_tables: a table row or the row arrays are too short
-  kBatchTimeout = 32       // a bounded wait was given up
+  kBatchTimeout = 32,      // a bounded wait was given up
+  kBatchRange = 64,        // a value beyond the type it was bound for
+  kBatchBadToken = 128,    // token_logprobs: a token outside the vocabulary: its row is skipped
+  kBatchBadCode = 256      // pack_codes4: a code or zero above 15
 };
 
 struct BatchBlock {        // one row block, 48 bytes

@@ -628,13 +628,18 @@ pic_status batch_check_flags() {
   if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("batch flag: ") + cudaGetErrorString(e));
   if (!f) return PIC_OK;
   cudaMemcpyToSymbol(g_batch_flag, &zero, sizeof(zero));
-  if (f & kBatchTimeout) return fail(PIC_ERR_DEVICE_TIMEOUT, "the batched attention kernel gave up a bounded wait");
+  if (f & kBatchTimeout) return fail(PIC_ERR_DEVICE_TIMEOUT, "a kernel of the batched or decode-step calls gave up a bounded wait");
+  if (f & kBatchRange)
+    return fail(PIC_ERR_RANGE, "a value was beyond the type it was bound for (fp16's range, or not finite where it was to be "
+                               "quantised); the outputs since the last pic_sync are invalid");
   // in the order in which the host calls check: what is inconsistent, what does not fit, what is not free
-  if (f & (kBatchBadLengths | kBatchBadBlock | kBatchBadPosition)) {
+  if (f & (kBatchBadLengths | kBatchBadBlock | kBatchBadPosition | kBatchBadToken | kBatchBadCode)) {
     std::string what = "device metadata:";
     if (f & kBatchBadLengths) what += " lengths that do not fit together (the request was skipped)";
     if (f & kBatchBadBlock) what += " a block outside the pool (taken as empty)";
     if (f & kBatchBadPosition) what += " a position outside the RoPE table (skipped)";
+    if (f & kBatchBadToken) what += " a token outside the vocabulary (its row was skipped)";
+    if (f & kBatchBadCode) what += " a 4-bit code or zero above 15 (upper bits lost)";
     return fail(PIC_ERR_INVALID_ARG, what);
   }
   if (f & kBatchCapacity)
