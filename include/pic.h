@@ -542,9 +542,9 @@ pic_status pic_op_attention_prefix(int32_t dtype, int32_t T, int32_t n_heads, in
  * group 32, 64 or 128 columns (the last one of a row may be shorter). N >= 1, K a multiple of 32.
  * Packed layout (pic_op_weight4_bytes bytes, 128-byte aligned): tiles of 128 rows x 128 columns, tile (n / 128, k / 128) at
  * ((n / 128) * ceil(K / 128) + k / 128) * tile_bytes, tile_bytes = 8192 + (128 / group) * 384. A tile is
- *   [4][128 rows][16 bytes] codes: the bytes of a row hold 32 columns, each 32-bit word 8 of them, column e of the 8 in bits
- *                           4 i .. 4 i + 3 with i = e / 2 + 4 (e % 2);
- *   [128 / group][128 rows] scales (fp16), then [128 / group][128 rows] zeros (bytes);
+ *   codes: row r's 64 bytes at 64 r, four pieces of 16, piece q at 16 (q ^ (r / 2 % 4)): a 32-bit word for each of the four runs of
+ *          32 columns, the run's columns 8 q .. 8 q + 7, column e of them in bits 4 i .. 4 i + 3 with i = e / 2 + 4 (e % 2);
+ *   [128 / group][128] scales (fp16), then [128 / group][128] zeros (bytes), row r at r / 32 * 32 + r % 8 * 4 + r / 8 % 4;
  * rows behind N and columns behind K stand for 0. */
 size_t pic_op_weight4_bytes(int32_t N, int32_t K, int32_t group); /* 0 for shapes that the calls refuse */
 
@@ -567,7 +567,7 @@ pic_status pic_op_unpack_weight4(const void* W4, float* W, int32_t N, int32_t K,
  * PIC_E4M3: X 8-bit, x_scales fp32 [T][ceil(K / 128)]: X[t][k] stands for that value times x_scales[t][k / 128]
  * (pic_op_add_rms_norm writes both). x_stride: elements from row to row, its bytes a multiple of 16; X, Y 16-byte aligned.
  * Products are exact, sums fp32, each group's sum times its scale in fp32. Made for few rows: the weights are read once
- * for every 64. Y must not overlap X or W4. T up to 4194240. */
+ * for every 64. T up to 2^20. Y must not overlap W4, X or x_scales. */
 pic_status pic_op_gemm_w4(int32_t x_dtype, const void* W4, const void* X, int64_t x_stride, const float* x_scales,
                           float* Y, int32_t N, int32_t K, int32_t T, int32_t group, pic_stream_t stream);
 

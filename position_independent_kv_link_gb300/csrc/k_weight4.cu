@@ -1,7 +1,12 @@
 // 4-bit weights with group scales: packing, unpacking, and the product of few rows with them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <climits>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda_fp8.h>
@@ -85,21 +90,18 @@ __global__ void __launch_bounds__(kPackThreads) pack4_kernel(const T* __restrict
     }
     const float s = __half2float(hs);
     const float z = s > 0.f ? fminf(nearest_quotient(-lo, s), 15.f) : 0.f;
-    uint32_t w[4];
+    uint32_t w[4] = {};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      w[q] = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float c = s > 0.f ? fminf(fmaxf(nearest_quotient(x[8 * q + e], s) + z, 0.f), 15.f) : 0.f;
-        w[q] |= (uint32_t)c << w4_shift(e);
-      }
+    for (int e = 0; e < 32; ++e) {
+      const float c = s > 0.f ? fminf(fmaxf(nearest_quotient(x[e], s) + z, 0.f), 15.f) : 0.f;
+      w[e / 8] |= (uint32_t)c << w4_shift(e % 8);
     }
-    *reinterpret_cast<uint4*>(tile + j * (kW4Rows * 16) + r * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t*>(tile + w4_piece(r, q) + 4 * j) = w[q];
     if (j % lanes == 0) {
       const int g = j / lanes;
-      reinterpret_cast<__half*>(tile + kW4Codes)[g * kW4Rows + r] = hs;
-      tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + r] = (uint8_t)z;
+      reinterpret_cast<__half*>(tile + kW4Codes)[g * kW4Rows + w4_place(r)] = hs;
+      tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + w4_place(r)] = (uint8_t)z;
     }
   }
 }
@@ -121,46 +123,39 @@ __global__ void __launch_bounds__(kPackThreads) pack_codes4_kernel(const uint8_t
       const uint4 a = __ldg(src), b = __ldg(src + 1);
       c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w, c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
     }
-    uint32_t over = 0, w[4];
+    uint32_t over = 0, w[4] = {};
 #pragma unroll
     for (int q = 0; q < 8; ++q) over |= c[q] & 0xf0f0f0f0u;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      w[q] = 0;
+    for (int e = 0; e < 32; ++e) w[e / 8] |= (c[e / 4] >> (8 * (e % 4)) & 15u) << w4_shift(e % 8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[q] |= (c[2 * q + e / 4] >> (8 * (e % 4)) & 15u) << w4_shift(e);
-    }
-    *reinterpret_cast<uint4*>(tile + j * (kW4Rows * 16) + r * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t*>(tile + w4_piece(r, q) + 4 * j) = w[q];
     if (j % lanes == 0) {
       const int g = j / lanes;
       const size_t at = (size_t)n * p.groups + (kt * kW4Cols + g * p.group) / p.group;
       const uint8_t z = !in ? 0 : zeros ? zeros[at] : 8;
       over |= z & 0xf0u;
-      reinterpret_cast<__half*>(tile + kW4Codes)[g * kW4Rows + r] = in ? scales[at] : __float2half_rn(0.f);
-      tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + r] = z & 15;
+      reinterpret_cast<__half*>(tile + kW4Codes)[g * kW4Rows + w4_place(r)] = in ? scales[at] : __float2half_rn(0.f);
+      tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + w4_place(r)] = z & 15;
     }
     if (over) batch_flag(flag, kBatchBadCode);
   }
 }
 
-// A thread writes the 8 values of a word, 16 threads a row's part of the tile.
+// A thread writes 4 values, half of a word: a warp writes a row's part of the tile.
 __global__ void __launch_bounds__(kPackThreads) unpack4_kernel(const uint8_t* __restrict__ w4, float* __restrict__ W, W4Shape p) {
   const int nt = blockIdx.x / p.k_tiles, kt = blockIdx.x % p.k_tiles;
   const uint8_t* tile = w4 + (size_t)blockIdx.x * p.tile_bytes;
   const int per = kW4Cols / p.group;
-  for (int i = threadIdx.x; i < kW4Rows * 16; i += kPackThreads) {
-    const int r = i / 16, q = i % 16, n = nt * kW4Rows + r, k = kt * kW4Cols + 8 * q;
+  for (int i = threadIdx.x; i < kW4Rows * 32; i += kPackThreads) {
+    const int r = i / 32, c = 4 * (i % 32), n = nt * kW4Rows + r, k = kt * kW4Cols + c;
     if (n >= p.N || k >= p.K) continue;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + q / 4 * (kW4Rows * 16) + r * 16 + q % 4 * 4));
-    const int g = 8 * q / p.group;
-    const float s = __half2float(reinterpret_cast<const __half*>(tile + kW4Codes)[g * kW4Rows + r]);
-    const int z = tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + r];
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = s * (float)((int)(w >> w4_shift(e) & 15u) - z);
-    float4* dst = reinterpret_cast<float4*>(W + (size_t)n * p.K + k);
-    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + w4_piece(r, c % 32 / 8) + c / 32 * 4)) >> w4_shift(c % 8);
+    const int g = c / p.group;
+    const float s = __half2float(reinterpret_cast<const __half*>(tile + kW4Codes)[g * kW4Rows + w4_place(r)]);
+    const int z = tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + w4_place(r)];
+    auto value = [&](int e) { return s * (float)((int)(w >> w4_shift(e) & 15u) - z); };
+    *reinterpret_cast<float4*>(W + (size_t)n * p.K + k) = make_float4(value(0), value(1), value(2), value(3));
   }
 }
 
@@ -174,57 +169,839 @@ struct Gemm4Args {
   const float* x_scales;
   float* y;
   int T;
+  int lg;                    // log2 of a group's 32-column steps
+  unsigned* flag;
 };
 
-constexpr int kSimpleRows = 8;   // of X per CTA
+// A band is 128 rows of W (256 in the tcgen05 kernel) against one tile of rows of X; its columns come in blocks of 128. With many
+// bands the CTAs take whole ones in turn, and their copies run on over the ends of bands. With few, the CTAs of a cluster share one
+// band's blocks and add their sums through each other's shared memory, in the order of their ranks. So there is no scratch, and
+// the same call gives the same bits again.
 
-// One thread per weight row, kSimpleRows rows of X in shared memory.
-template <bool E4M3>
-__global__ void __launch_bounds__(kW4Rows) gemm4_kernel(Gemm4Args a) {
-  __shared__ float xs[kSimpleRows][kW4Cols];
-  const int nt = blockIdx.x, t0 = blockIdx.y * kSimpleRows, r = threadIdx.x, n = nt * kW4Rows + r;
-  const int per = kW4Cols / a.w.group, x_groups = a.w.k_tiles;
-  float acc[kSimpleRows] = {};
-  for (int kt = 0; kt < a.w.k_tiles; ++kt) {
-    const uint8_t* tile = a.w4 + ((size_t)nt * a.w.k_tiles + kt) * a.w.tile_bytes;
-    for (int i = threadIdx.x; i < kSimpleRows * kW4Cols; i += kW4Rows) {
-      const int t = t0 + i / kW4Cols, k = kt * kW4Cols + i % kW4Cols;
-      float v = 0.f;
-      if (t < a.T && k < a.w.K) {
-        if (E4M3)
-          v = __half2float(__half(__nv_cvt_fp8_to_halfraw(((const uint8_t*)a.x)[t * a.x_stride + k], __NV_E4M3)));
-        else
-          v = __half2float(((const __half*)a.x)[t * a.x_stride + k]);
-      }
-      xs[i / kW4Cols][i % kW4Cols] = v;
+constexpr unsigned long long kGemm4WaitLimit = 4000000000ull;   // SM cycles, about 2 s
+
+struct Gemm4Plan {
+  int stages, x_bytes;       // of X in a stage
+  int across, bands;         // bands of one tile of X, of all
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Shared memory by its own addresses (through pointers that were rounded up the loads become generic ones)
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float lds_half(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ float4 lds_f32x4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// the same, but suspended for up to 20 us before it answers
+__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// false (and the timeout flag) after kGemm4WaitLimit, or when the CTA has given up (`abort`: its word in shared memory)
+__device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
+  const unsigned long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_long(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kGemm4WaitLimit) {
+      atomicOr(flag, kBatchTimeout);
+      *abort = 1;
+      return false;
     }
-    __syncthreads();
-    for (int g = 0; g < per; ++g) {
-      const float s = __half2float(reinterpret_cast<const __half*>(tile + kW4Codes)[g * kW4Rows + r]);
-      const int z = tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + r];
-      float sum[kSimpleRows] = {};
-      for (int q = g * a.w.group / 8; q < (g + 1) * a.w.group / 8; ++q) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + q / 4 * (kW4Rows * 16) + r * 16 + q % 4 * 4));
+  }
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
+  return mbar_try(bar, parity) || mbar_try_long(bar, parity) || mbar_wait_on(bar, parity, abort, flag);
+}
+// for the whole warp: the same answer in every lane
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, flag));
+}
+// waits on when the CTA has given up
+__device__ __forceinline__ void mbar_settle(uint32_t bar, uint32_t parity, unsigned* flag) {
+  unsigned none = 0;
+  if (!mbar_try(bar, parity)) mbar_wait_on(bar, parity, &none, flag);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+// Low word of the descriptor of K-major rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart; the high word is fixed
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr & 0x3FFFFu) >> 4; }
+// D (fp32) in tensor memory += A (tensor memory, 128 lanes) . B^T (shared memory, N rows); fp16, or e4m3
+template <bool E4M3>
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (E4M3)
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kDescHi),
+        "r"(acc));
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(kDescHi),
+        "r"(acc));
+}
+// one lane of a whole warp, always the same
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y), "=f"(v[3].x), "=f"(v[3].y),
+        "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y), "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld(float2* v) {   // the registers are operands, so that no use moves ahead
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0].x), "+f"(v[0].y), "+f"(v[1].x), "+f"(v[1].y), "+f"(v[2].x), "+f"(v[2].y), "+f"(v[3].x),
+                 "+f"(v[3].y), "+f"(v[4].x), "+f"(v[4].y), "+f"(v[5].x), "+f"(v[5].y), "+f"(v[6].x), "+f"(v[6].y),
+                 "+f"(v[7].x), "+f"(v[7].y)
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The sum of *at over the cluster's CTAs, in the order of their ranks.
+__device__ __forceinline__ float cluster_sum(uint32_t at, uint32_t ctas) {
+  float sum = 0.f;
+#pragma unroll 8
+  for (uint32_t c = 0; c < ctas; ++c) {
+    uint32_t there;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(c));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+    sum += v;
+  }
+  return sum;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {   // (a & b) | c
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// The 8 integers code - zero of a word in fp16, exact: z0 = 1024 + zero, z1 = -(64 + zero), twice each
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t z0, uint32_t z1, uint32_t* v) {
+  const uint32_t y = x >> 8;
+  v[0] = hsub2(and_or(x, 0x000f000fu, 0x64006400u), z0);                   // 1024 + c - (1024 + zero)
+  v[1] = hfma2(and_or(x, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);      // (1024 + 16 c) / 16 - (64 + zero)
+  v[2] = hsub2(and_or(y, 0x000f000fu, 0x64006400u), z0);
+  v[3] = hfma2(and_or(y, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);
+}
+
+constexpr int kMaxStages = 12, kFewRows = 16, kTcBlocks = 4096;
+
+// A CTA's blocks, in the order in which all of its warps take them: a share of one band (clusters), or whole bands in turn.
+struct Gemm4Walk {
+  int split, rank;           // CTAs of the cluster
+  int n_band, t_tile, kb;    // the block: band down W, tile of X, block of the band
+  int band, k1, bands, across, step;
+
+  __device__ __forceinline__ Gemm4Walk(const Gemm4Args& a, const Gemm4Plan& p) {
+    uint32_t x, y;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(x));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(y));
+    split = (int)x;
+    rank = (int)y;
+    across = p.across;
+    step = gridDim.x;
+    if (split > 1) {
+      band = blockIdx.x / split;
+      bands = band + 1;
+      kb = (int)((int64_t)a.w.k_tiles * rank / split);
+      k1 = (int)((int64_t)a.w.k_tiles * (rank + 1) / split);
+    } else {
+      band = blockIdx.x;
+      bands = p.bands;
+      kb = 0;
+      k1 = a.w.k_tiles;
+    }
+    n_band = band % across;
+    t_tile = band / across;
+  }
+  __device__ __forceinline__ bool more() const { return band < bands; }
+  __device__ __forceinline__ void next() {         // kb 0 behind a band's end
+    if (++kb < k1) return;
+    kb = 0;
+    band += step;
+    n_band = band % across;
+    t_tile = band / across;
+  }
+};
+
+// More than kFewRows rows of X: tcgen05. A band is two tiles of 128 rows, which share the block of X.
+//
+//   warps 0-7   thread r of a tile's four warps: the 64 bytes of codes of row r become the integers code - zero in fp16, exact, in
+//               tensor memory as the A operand (the row's lane)
+//   warps 8-15  (8-23 with 64 rows of X) thread r: the sums of row r with 32 rows of X are read back for each group of columns, multiplied
+//               by the row's scale and added in fp32 registers. So a scale is a factor of one thread, products and sums within a group are exact integers times X,
+//               and no rounding enters but those of the fp32 sums.
+//   the last but one: one thread asks for the packed tiles (bulk copies of 8.4 to 9.5 KB) and the block of X (TMA) of each stage
+//   the last: issues the products, D[row][t] of both tiles for each group of columns, into one of two accumulators
+//
+// 8-bit X: the integer c = 0..15 is the e4m3 number c 2^-9 (subnormal up to 7, then the first binade with the same spacing), so the
+// codes need only be spread to bytes. The zero goes in by a second product with a row of -zero 2^-9, 8 columns of tensor
+// memory for a whole group; both are exact.
+//
+// Barriers: FULL, EMPTY of a stage: the copies have landed; the warps and the products have read it. AFULL, AEMPTY of an
+// operand buffer: the eight warps have written it; the products of the block have ended. DFULL, DEMPTY of an accumulator: the
+// products of a group have ended; the warps that add have read it. Each is waited for by every thread that could fall a phase behind.
+constexpr int kTcTiles = 2;
+template <int NT>
+constexpr int kTcThreads = (8 + NT / 4 + 2) * 32;
+constexpr int kTcA = 64, kTcTile = 256, kTcCols = 512;   // columns of tensor memory: an A buffer (two a tile), a tile, all
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
+}
+
+template <bool E4M3, int NT>
+__global__ void __launch_bounds__(kTcThreads<NT>, 1)
+    gemm4_tc_kernel(const __grid_constant__ CUtensorMap map_x, const Gemm4Args a, const Gemm4Plan p) {
+  constexpr int kAdd = NT / 4, kLoad = 8 + kAdd, kIssue = kLoad + 1;   // warps that add; the two others
+  static_assert(2 * kTcA + 2 * NT <= kTcTile && kTcTiles * kTcTile == kTcCols, "tensor memory");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages][kTcTiles] tiles
+  __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_afull[2], s_aempty[2], s_dfull[2], s_dempty[2], s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ unsigned s_abort;
+  __shared__ __align__(16) float s_xs[E4M3 ? kAdd : 1][32];
+  volatile unsigned* abort = &s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Gemm4Walk w(a, p);
+  const int per = 4 >> a.lg, last = (1 << a.lg) - 1;   // groups of a block; 32-column steps of one, less one
+
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(s_empty + i), kLoad + 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(s_afull + i), 8);
+      mbar_init(smem_u32(s_aempty + i), 1);
+      mbar_init(smem_u32(s_dfull + i), 1);
+      mbar_init(smem_u32(s_dempty + i), kAdd);
+    }
+    mbar_init(smem_u32(&s_done), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == kLoad) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTcCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  int st = 0;
+  uint32_t ph = 0;                                 // of the stage
+  auto next_stage = [&] {
+    if (++st == p.stages) st = 0, ph ^= 1;
+  };
+
+  if (warp == kLoad) {
+    if (lane == 0) {
+      uint64_t pol_w, pol_x;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol_w));
+      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
+      int issued = 0;
+      for (; w.more(); w.next()) {
+        if (!mbar_wait(smem_u32(s_empty + st), ph ^ 1, abort, a.flag)) break;
+        const int n0 = w.n_band * kTcTiles, tiles = min(kTcTiles, a.w.n_tiles - n0);
+        const uint32_t fb = smem_u32(s_full + st), x = xs + st * p.x_bytes;
+        mbar_expect_tx(fb, p.x_bytes + tiles * a.w.tile_bytes);
+        for (int g = 0; g < tiles; ++g)
+          bulk_load(ws + (st * kTcTiles + g) * a.w.tile_bytes,
+                    a.w4 + ((size_t)(n0 + g) * a.w.k_tiles + w.kb) * a.w.tile_bytes, a.w.tile_bytes, fb, pol_w);
+        tma_2d(x, &map_x, w.kb * kW4Cols, w.t_tile * NT, fb, pol_x);
+        if (!E4M3) tma_2d(x + NT * 128, &map_x, w.kb * kW4Cols + 64, w.t_tile * NT, fb, pol_x);
+        ++issued;
+        next_stage();
+      }
+      for (int j = max(0, issued - p.stages); j < issued; ++j)   // copies under way land before the CTA ends
+        mbar_settle(smem_u32(s_full + j % p.stages), (uint32_t)((j / p.stages) & 1), a.flag);
+    }
+  } else if (warp == kIssue) {
+    // The warp loops as a whole and one lane issues: in a branch of one lane each product took 140 cycles to issue.
+    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kW4Rows >> 4) << 24);
+    uint32_t i = 0, q = 0;                         // blocks, groups so far
+    bool going = true;
+    for (; w.more() && going; w.next(), ++i) {
+      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag) ||
+          !warp_wait(smem_u32(s_afull + (i & 1)), (i >> 1) & 1, abort, a.flag))
+        break;
+      const uint32_t X = desc_lo(xs + st * p.x_bytes), A = tmem + (i & 1) * kTcA;
+      auto issue = [&](auto steps) {               // 32-column steps of a group
+        constexpr int S = decltype(steps)::value;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float c = (float)((int)(w >> w4_shift(e) & 15u) - z);
+        for (int k = 0; k < 4 / S; ++k, ++q) {
+          going = going && warp_wait(smem_u32(s_dempty + (q & 1)), ((q >> 1) & 1) ^ 1, abort, a.flag);
+          if (!going) return;
+          fence_after();
+          const uint32_t D = tmem + 2 * kTcA + (q & 1) * NT;
+          if (elect()) {
 #pragma unroll
-          for (int t = 0; t < kSimpleRows; ++t) sum[t] = fmaf(c, xs[t][8 * q + e], sum[t]);
+            for (int g = 0; g < kTcTiles; ++g)
+#pragma unroll
+              for (int j = k * S; j < (k + 1) * S; ++j) {
+                const uint32_t d = D + g * kTcTile, f = A + g * kTcTile;
+                if constexpr (E4M3) {
+                  umma<true>(d, f + j * 8, X + j * 2, idesc, j > k * S);
+                  umma<true>(d, f + 32 + k * 8, X + j * 2, idesc, 1);
+                } else {
+                  const uint32_t at = X + ((j >> 1) * (NT * 128) + (j & 1) * 64) / 16;
+                  umma<false>(d, f + j * 16, at, idesc, j > k * S);
+                  umma<false>(d, f + j * 16 + 8, at + 2, idesc, 1);
+                }
+              }
+            umma_commit(smem_u32(s_dfull + (q & 1)));
+            if (k == 4 / S - 1) {
+              umma_commit(smem_u32(s_aempty + (i & 1)));
+              umma_commit(smem_u32(s_empty + st));
+            }
+          }
+          __syncwarp();
+        }
+      };
+      if (a.lg == 2) issue(std::integral_constant<int, 4>());
+      else if (a.lg == 1) issue(std::integral_constant<int, 2>());
+      else issue(std::integral_constant<int, 1>());
+      next_stage();
+    }
+    if (elect()) umma_commit(smem_u32(&s_done));     // products under way end before tensor memory is given back
+    __syncwarp();
+    mbar_settle(smem_u32(&s_done), 0, a.flag);
+  } else if (warp < 8) {
+    const int g = warp >> 2, r = threadIdx.x & 127;   // tile; row of the tile = lane of tensor memory
+    const uint32_t T = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * kTcTile;
+    // (the second tile behind the last band's end: what lies in shared memory, its sums are not kept)
+    const uint32_t tile = ws + g * a.w.tile_bytes, zeros = kW4Codes + per * (kW4Rows * 2) + w4_place(r);
+    for (uint32_t i = 0; w.more(); w.next(), ++i) {
+      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag) ||
+          !warp_wait(smem_u32(s_aempty + (i & 1)), ((i >> 1) & 1) ^ 1, abort, a.flag))
+        break;
+      fence_after();
+      const uint32_t at = tile + st * kTcTiles * a.w.tile_bytes;
+      const uint32_t A = T + (i & 1) * kTcA;
+      uint4 u[4];                                  // pieces of the row
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = lds128(at + w4_piece(r, e));
+      uint32_t z0 = 0, z1 = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool begins = (j & last) == 0;
+        if (begins) {
+          z0 = lds8(at + zeros + (j >> a.lg) * kW4Rows);
+          if constexpr (E4M3) {
+            z1 = 0x80808080u | 0x01010101u * z0;                          // -zero 2^-9
+          } else {
+            z0 = 0x64006400u + 0x00010001u * z0;                          // 1024 + zero
+            z1 = hsub2(0x63806380u, z0);                                  // 960 - (1024 + zero)
+          }
+        }
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {              // pieces: columns 8 e .. 8 e + 7
+          const uint32_t x = j == 0 ? u[e].x : j == 1 ? u[e].y : j == 2 ? u[e].z : u[e].w;
+          if constexpr (E4M3) {
+            const uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
+            v[2 * e] = __byte_perm(lo, hi, 0x6420);
+            v[2 * e + 1] = __byte_perm(lo, hi, 0x7531);
+          } else {
+            codes_f16(x, z0, z1, v + 4 * e);
+          }
+        }
+        if constexpr (E4M3) {
+          tmem_st8(A + j * 8, v);
+          if (begins) {
+            const uint32_t same[8] = {z1, z1, z1, z1, z1, z1, z1, z1};
+            tmem_st8(A + 32 + (j >> a.lg) * 8, same);
+          }
+        } else {
+          tmem_st16(A + j * 16, v);
         }
       }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(s_afull + (i & 1)));
+        mbar_arrive(smem_u32(s_empty + st));
+      }
+      next_stage();
+    }
+  }
+
+  float2 acc[16];                                  // rows half .. of the tile of X, two by two
+  const bool adds = warp >= 8 && warp < kLoad;
+  const int half = (warp - 8) / 8 * 32;
+  if (adds) {
 #pragma unroll
-      for (int t = 0; t < kSimpleRows; ++t) {
-        const float sx = E4M3 && t0 + t < a.T ? a.x_scales[(size_t)(t0 + t) * x_groups + kt] : 1.f;
-        acc[t] = fmaf(E4M3 ? sum[t] * sx : sum[t], s, acc[t]);
+    for (int t = 0; t < 16; ++t) acc[t] = make_float2(0.f, 0.f);
+    const int g = (warp - 8) >> 2 & 1, r = threadIdx.x & 127;
+    const uint32_t D = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * kTcTile + 2 * kTcA + half;
+    uint32_t q = 0;                                // groups so far
+    bool going = true;
+    while (w.more() && going) {
+      const int t0 = w.t_tile * NT + half, n = (w.n_band * kTcTiles + g) * kW4Rows + r;
+      const float x_scale = E4M3 && t0 + lane < a.T ? __ldg(a.x_scales + (size_t)(t0 + lane) * a.w.k_tiles + w.kb) : 0.f;
+      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag)) break;
+      const uint32_t scales = ws + (st * kTcTiles + g) * a.w.tile_bytes + kW4Codes + 2 * w4_place(r);
+#pragma unroll 1
+      for (int k = 0; k < per; ++k, ++q) {
+        const float s1 = lds_half(scales + 2 * k * kW4Rows);
+        const float2 s = make_float2(s1, s1);
+        if (!warp_wait(smem_u32(s_dfull + (q & 1)), (q >> 1) & 1, abort, a.flag)) {
+          going = false;
+          break;
+        }
+        if (E4M3 && k == 0) {                      // (asked for before the waits)
+          sts_f32(smem_u32(&s_xs[warp - 8][lane]), 512.f * x_scale);
+          __syncwarp();
+        }
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+          float2 v[8];
+          tmem_ld16(D + (q & 1) * NT + c, v);
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int t = 0; t < 8; t += 2) {
+            float2 f0 = s, f1 = s;
+            if constexpr (E4M3) {
+              const float4 x = lds_f32x4(smem_u32(&s_xs[warp - 8][c + 2 * t]));
+              f0 = mul2(s, make_float2(x.x, x.y));
+              f1 = mul2(s, make_float2(x.z, x.w));
+            }
+            acc[c / 2 + t] = fma2(v[t], f0, acc[c / 2 + t]);
+            acc[c / 2 + t + 1] = fma2(v[t + 1], f1, acc[c / 2 + t + 1]);
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(s_dempty + (q & 1)));
+      }
+      if (lane == 0) mbar_arrive(smem_u32(s_empty + st));
+      next_stage();
+      w.next();
+      if (w.kb == 0 && w.split == 1) {             // a band of this CTA's own
+        float* to = a.y + (size_t)t0 * a.w.N + n;
+#pragma unroll
+        for (int t = 0; t < 32; ++t, to += a.w.N) {
+          if (n < a.w.N && t0 + t < a.T) *to = t % 2 ? acc[t / 2].y : acc[t / 2].x;
+          if (t % 2) acc[t / 2] = make_float2(0.f, 0.f);
+        }
       }
     }
-    __syncthreads();
   }
-  if (n >= a.w.N) return;
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == kLoad) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols));
+  if (w.split == 1) return;
+  const int col = (warp - 8) / 4 % 2 * 128 + (threadIdx.x & 127);
+  const uint32_t sums = xs + 4 * col;              // [NT][256] fp32; every stage has been read
+  if (adds) {
 #pragma unroll
-  for (int t = 0; t < kSimpleRows; ++t)
-    if (t0 + t < a.T) a.y[(size_t)(t0 + t) * a.w.N + n] = acc[t];
+    for (int t = 0; t < 32; ++t) sts_f32(sums + (half + t) * 1024, t % 2 ? acc[t / 2].y : acc[t / 2].x);
+  }
+  cluster_sync();
+  const int band = blockIdx.x / w.split, t0 = band / p.across * NT, n = band % p.across * 256 + col;
+  if (adds && n < a.w.N) {                         // rows of X: this CTA's share, in NT / 32 turns
+    const int rows = min(NT, a.T - t0), end = rows * (w.rank + 1) / w.split;
+    for (int t = rows * w.rank / w.split + half / 32; t < end; t += NT / 32)
+      a.y[(size_t)(t0 + t) * a.w.N + n] = cluster_sum(sums + t * 1024, w.split);
+  }
+  cluster_sync();
 }
+
+// Few rows of X: mma.sync m16n8k16, whose operands are registers, so that no warp waits for another. A band is 128 rows, 32 for each of
+// the four warps; warp 4 asks for the copies. The codes become the integers code - zero in fp16, 8-bit X becomes fp16, both
+// exact. A lane's weights of two products are one word of codes for each row, its part of X the columns 8 q .. 8 q + 7 of a 32-column
+// run, which stand where the products want 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q (the sum over columns does not mind).
+constexpr int kRowsThreads = 160;
+
+// Row of an 8-row tile of X that lane group g reads, and the column of a product that is its: rows that one access of
+// a warp touches together lie in different banks of the swizzled tile.
+template <bool E4M3>
+__host__ __device__ constexpr int x_row(int g) { return E4M3 ? (g & 3) * 2 + (g >> 2) : (g >> 1) + (g & 1) * 4; }
+
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {   // the lower two bytes
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(r) : "r"(two));
+  return r;
+}
+
+template <bool E4M3, int NT>
+struct RowsShape {
+  static constexpr int kCtas = NT == 8 ? 4 : NT == 16 ? 3 : 2;   // an SM, by registers
+};
+
+template <bool E4M3, int NT>
+__global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
+    gemm4_rows_kernel(const __grid_constant__ CUtensorMap map_x, const Gemm4Args a, const Gemm4Plan p) {
+  constexpr int U = NT / 8;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages] tiles
+  __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
+  __shared__ unsigned s_abort;
+  volatile unsigned* abort = &s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, row0 = warp * 32 + g;
+  Gemm4Walk w(a, p);
+  const int per = 4 >> a.lg, last = (1 << a.lg) - 1;   // groups of a block; 32-column steps of one, less one
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(s_empty + i), 4);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+
+  float acc[2][U][4] = {};                         // rows g and g + 8 of two 16-row tiles, columns tok[2 u], tok[2 u + 1]
+  auto tok = [&](int i) { return i / 2 * 8 + x_row<E4M3>(2 * q + i % 2); };   // rows of X that are this lane's columns
+  if (warp == 4) {
+    if (lane == 0) {
+      uint64_t pol_w, pol_x;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol_w));
+      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
+      int st = 0, issued = 0;
+      uint32_t ph = 1;
+      for (; w.more(); w.next()) {
+        if (!mbar_wait(smem_u32(s_empty + st), ph, abort, a.flag)) break;
+        const uint32_t fb = smem_u32(s_full + st), x = xs + st * p.x_bytes;
+        mbar_expect_tx(fb, p.x_bytes + a.w.tile_bytes);
+        bulk_load(ws + st * a.w.tile_bytes, a.w4 + ((size_t)w.n_band * a.w.k_tiles + w.kb) * a.w.tile_bytes,
+                  a.w.tile_bytes, fb, pol_w);
+        tma_2d(x, &map_x, w.kb * kW4Cols, w.t_tile * NT, fb, pol_x);
+        if (!E4M3) tma_2d(x + NT * 128, &map_x, w.kb * kW4Cols + 64, w.t_tile * NT, fb, pol_x);
+        ++issued;
+        if (++st == p.stages) st = 0, ph ^= 1;
+      }
+      for (int j = max(0, issued - p.stages); j < issued; ++j)   // copies under way land before the CTA ends
+        mbar_settle(smem_u32(s_full + j % p.stages), (uint32_t)((j / p.stages) & 1), a.flag);
+    }
+  } else {
+    const uint32_t piece = w4_piece(row0, q);      // (rows 8 apart: 512 bytes)
+    uint32_t x_at[E4M3 ? 4 : 2];                   // columns 8 q .. of a run of X's row
+#pragma unroll
+    for (int j = 0; j < (E4M3 ? 4 : 2); ++j)
+      x_at[j] = x_row<E4M3>(g) * 128 + (E4M3 ? ((2 * j + (q >> 1)) ^ x_row<E4M3>(g)) * 16 + (q & 1) * 8 : ((4 * j + q) ^ x_row<E4M3>(g)) * 16);
+    int st = 0;
+    uint32_t ph = 0;
+    while (w.more()) {
+      const int t0 = w.t_tile * NT;
+      float sx[E4M3 ? 2 * U : 1];
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int i = 0; i < 2 * U; ++i)
+          sx[i] = t0 + tok(i) < a.T ? __ldg(a.x_scales + (size_t)(t0 + tok(i)) * a.w.k_tiles + w.kb) : 0.f;
+      }
+      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag)) break;
+      const uint32_t xt = xs + st * p.x_bytes, tile = ws + st * a.w.tile_bytes;
+      const uint32_t scales = tile + kW4Codes + 2 * (warp * 32 + g * 4), zeros = tile + kW4Codes + per * (kW4Rows * 2) + warp * 32 + g * 4;
+      uint4 c[4];                                  // rows g, g + 8, g + 16, g + 24 of the warp's
+#pragma unroll
+      for (int m = 0; m < 4; ++m) c[m] = lds128(tile + piece + 512 * m);
+      float d[2][U][4], sc[4];
+      uint32_t z0[4], z1[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((j & last) == 0) {
+          const int at = (j >> a.lg) * kW4Rows;
+          const uint2 v = lds64(scales + 2 * at);
+          const uint32_t z = lds32(zeros + at);
+          const float2 s01 = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+          const float2 s23 = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+          sc[0] = s01.x, sc[1] = s01.y, sc[2] = s23.x, sc[3] = s23.y;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            z0[m] = 0x64006400u + (z >> (8 * m) & 255u) * 0x00010001u;     // 1024 + zero
+            z1[m] = hsub2(0x63806380u, z0[m]);                              // 960 - (1024 + zero)
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int u = 0; u < U; ++u) d[m][u][0] = d[m][u][1] = d[m][u][2] = d[m][u][3] = 0.f;
+        }
+        uint32_t f[4][4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) codes_f16(j == 0 ? c[m].x : j == 1 ? c[m].y : j == 2 ? c[m].z : c[m].w, z0[m], z1[m], f[m]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          uint32_t b[4];
+          if constexpr (E4M3) {
+            const uint2 v = lds64(xt + u * 1024 + x_at[j]);
+            b[0] = e4m3_f16(v.x), b[1] = e4m3_f16(v.x >> 16), b[2] = e4m3_f16(v.y), b[3] = e4m3_f16(v.y >> 16);
+          } else {
+            const uint4 v = lds128(xt + (j >> 1) * (NT * 128) + u * 1024 + x_at[j & 1]);
+            b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma_f16(d[m][u], f[2 * m][0], f[2 * m + 1][0], f[2 * m][1], f[2 * m + 1][1], b[0], b[1]);
+            mma_f16(d[m][u], f[2 * m][2], f[2 * m + 1][2], f[2 * m][3], f[2 * m + 1][3], b[2], b[3]);
+          }
+        }
+        if ((j & last) == last) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[m][u][e] = fmaf(d[m][u][e], E4M3 ? sc[2 * m + (e >> 1)] * sx[2 * u + (e & 1)] : sc[2 * m + (e >> 1)], acc[m][u][e]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(s_empty + st));
+      if (++st == p.stages) st = 0, ph ^= 1;
+      const int n0 = w.n_band * kW4Rows + row0;
+      w.next();
+      if (w.kb == 0 && w.split == 1) {             // a band of this CTA's own
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = t0 + tok(2 * u + (e & 1)), n = n0 + m * 16 + (e >> 1) * 8;
+              if (t < a.T && n < a.w.N) a.y[(size_t)t * a.w.N + n] = acc[m][u][e];
+              acc[m][u][e] = 0.f;
+            }
+      }
+    }
+  }
+  if (w.split == 1) return;
+  __syncthreads();
+  constexpr int kPitch = 136;                      // rows of X 4 apart meet no bank twice
+  if (warp < 4) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) 
+            sts_f32(xs + 4 * (tok(2 * u + (e & 1)) * kPitch + row0 + m * 16 + (e >> 1) * 8), acc[m][u][e]);   // every stage has been read
+  }
+  cluster_sync();
+  const int band = blockIdx.x / w.split, t0 = band / p.across * NT, n = band % p.across * kW4Rows + threadIdx.x;
+  if (warp < 4 && n < a.w.N) {
+    const int rows = min(NT, a.T - t0), end = rows * (w.rank + 1) / w.split;
+    for (int t = rows * w.rank / w.split; t < end; ++t)
+      a.y[(size_t)(t0 + t) * a.w.N + n] = cluster_sum(xs + 4 * (t * kPitch + threadIdx.x), w.split);
+  }
+  cluster_sync();
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// CTAs of a cluster that share a band, or 1. An SM takes a block in about 0.19 us whatever runs on it, a CTA by itself in 0.3; so
+// a band is shared while that spreads the blocks better, or lets more CTAs work at once, and all clusters find room together.
+int gemm4_split(int bands, int blocks, int slots, int sms) {
+  int best = 1;
+  double least = 1e30;
+  for (int c = 1; c <= std::min(8, blocks); ++c) {
+    const int64_t ctas = (int64_t)bands * c;
+    if (c > 1 && ctas > slots) break;
+    const int own = (blocks + c - 1) / c;
+    const double cost = std::max((double)((ctas + sms - 1) / sms) * own * 0.19, own * 0.3) + 0.1 * c;
+    if (cost < least) least = cost, best = c;
+  }
+  return best;
+}
+
+template <typename K>
+pic_status launch_gemm4(K kernel, const Gemm4Args& a, bool e4m3, int rows, int tiles, int threads, int per_sm, int ring, int sms,
+                        cudaStream_t st) {
+  Gemm4Plan p;
+  p.x_bytes = rows * kW4Cols * (e4m3 ? 1 : 2);
+  p.stages = std::min(kMaxStages, ring / (p.x_bytes + tiles * a.w.tile_bytes));
+  p.across = (a.w.n_tiles + tiles - 1) / tiles;
+  p.bands = p.across * ((a.T + rows - 1) / rows);
+  const auto enc = encode_tiled();
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.w.K, (cuuint64_t)a.T};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.x_stride * (e4m3 ? 1 : 2)};
+  const cuuint32_t box[2] = {e4m3 ? 128u : 64u, (cuuint32_t)rows}, step[2] = {1, 1};
+  if (!enc || enc(&map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(a.x), dims,
+                  strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return fail(PIC_ERR_CUDA, "4-bit gemm: cuTensorMapEncodeTiled failed");
+  const size_t smem = 1024 + (size_t)p.stages * (p.x_bytes + tiles * a.w.tile_bytes);
+  PIC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  const int split = gemm4_split(p.bands, a.w.k_tiles, per_sm * sms, sms);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(split > 1 ? (unsigned)p.bands * split : (unsigned)std::min(p.bands, per_sm * sms));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  PIC_CUDA(cudaLaunchKernelEx(&cfg, kernel, map, a, p));
+  return PIC_OK;
+}
+
+template <bool E4M3, int NT>
+pic_status launch_gemm4_rows(const Gemm4Args& a, int sms, cudaStream_t st) {
+  constexpr int kCtas = RowsShape<E4M3, NT>::kCtas;
+  return launch_gemm4(gemm4_rows_kernel<E4M3, NT>, a, E4M3, NT, 1, kRowsThreads, kCtas, (kCtas == 4 ? 54 : kCtas == 3 ? 73 : 111) * 1024,
+                      sms, st);
+}
+
+template <bool E4M3, int NT>
+pic_status launch_gemm4_tc(const Gemm4Args& a, int sms, cudaStream_t st) {
+  return launch_gemm4(gemm4_tc_kernel<E4M3, NT>, a, E4M3, NT, kTcTiles, kTcThreads<NT>, 1, 222 * 1024, sms, st);
+}
+
+template <bool E4M3>
+pic_status launch_gemm4(const Gemm4Args& a, int sms, cudaStream_t st) {
+  // tcgen05 (us, LM head of 128256 x 4096): 32 rows 92 for 109, 64 rows 114 for 216; 16 rows 92 for 73. With few blocks its wide bands
+  // leave SMs idle: 6144 x 4096, 64 rows 30 for 18.5.
+  if (a.T > kFewRows && (int64_t)a.w.n_tiles * a.w.k_tiles >= kTcBlocks)
+    return a.T <= 32 ? launch_gemm4_tc<E4M3, 32>(a, sms, st) : launch_gemm4_tc<E4M3, 64>(a, sms, st);
+  return a.T <= 8 ? launch_gemm4_rows<E4M3, 8>(a, sms, st) : a.T <= 16 ? launch_gemm4_rows<E4M3, 16>(a, sms, st) : launch_gemm4_rows<E4M3, 32>(a, sms, st);
+}
+
+int sms_of(int dev) {
+  static std::atomic<int> sms[64];
+  if (dev >= 0 && dev < 64 && sms[dev].load()) return sms[dev].load();
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+  if (dev >= 0 && dev < 64) sms[dev].store(n);
+  return n;
+}
+
+constexpr int kMaxRows = 1 << 20;   // of X
 
 bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
@@ -303,28 +1080,22 @@ pic_status pic_op_gemm_w4(int32_t x_dtype, const void* W4, const void* X, int64_
       x_stride < K || x_stride >= (int64_t)1 << 38 || x_stride % (e4m3 ? 16 : 8))
     return fail(PIC_ERR_INVALID_ARG, "invalid 4-bit gemm arguments (K a multiple of 32, group 32, 64 or 128, rows of X a "
                                      "multiple of 16 bytes apart, x_scales with 8-bit rows)");
-  if (T > 65535 * 64) return fail(PIC_ERR_CAPACITY, "4-bit gemm: more than 4194240 rows");
+  if (T > kMaxRows) return fail(PIC_ERR_CAPACITY, "4-bit gemm: more than 2^20 rows");
   if (misaligned(W4, 128) || misaligned(X, 16) || misaligned(Y, 16) || misaligned(x_scales, 4))
     return fail(PIC_ERR_INVALID_ARG, "4-bit gemm: X and Y must be 16-byte, the packed weights 128-byte aligned");
   const W4Shape s = w4_shape(N, K, group);
+  if ((int64_t)s.n_tiles * ((T + 31) / 32) > INT_MAX / 8) return fail(PIC_ERR_CAPACITY, "4-bit gemm: too many rows of both");
   const size_t y_bytes = (size_t)T * N * 4;
   if (overlap(Y, y_bytes, X, ((size_t)(T - 1) * x_stride + K) * (e4m3 ? 1 : 2)) ||
       overlap(Y, y_bytes, W4, (size_t)s.n_tiles * s.k_tiles * s.tile_bytes) ||
       (x_scales && overlap(Y, y_bytes, x_scales, (size_t)T * s.k_tiles * 4)))
     return fail(PIC_ERR_INVALID_ARG, "4-bit gemm: Y must not overlap the packed weights, X or its scales");
-  const Gemm4Args a{s, (const uint8_t*)W4, X, x_stride, x_scales, Y, T};
-  for (int t0 = 0; t0 < T; t0 += 65535 * kSimpleRows) {
-    Gemm4Args b = a;
-    b.x = (const uint8_t*)X + (size_t)t0 * x_stride * (e4m3 ? 1 : 2);
-    b.x_scales = x_scales ? x_scales + (size_t)t0 * s.k_tiles : nullptr;
-    b.y = Y + (size_t)t0 * N;
-    b.T = std::min(T - t0, 65535 * kSimpleRows);
-    const dim3 grid(s.n_tiles, (b.T + kSimpleRows - 1) / kSimpleRows);
-    if (e4m3) gemm4_kernel<true><<<grid, kW4Rows, 0, (cudaStream_t)stream>>>(b);
-    else gemm4_kernel<false><<<grid, kW4Rows, 0, (cudaStream_t)stream>>>(b);
-    PIC_CUDA(cudaGetLastError());
-  }
-  return PIC_OK;
+  int dev = 0;
+  PIC_CUDA(cudaGetDevice(&dev));
+  Gemm4Args a{s, (const uint8_t*)W4, X, x_stride, x_scales, Y, T, group == 32 ? 0 : group == 64 ? 1 : 2, nullptr};
+  pic_status e = batch_flag_address(&a.flag);
+  if (e != PIC_OK) return e;
+  return e4m3 ? launch_gemm4<true>(a, sms_of(dev), (cudaStream_t)stream) : launch_gemm4<false>(a, sms_of(dev), (cudaStream_t)stream);
 }
 
 }  // extern "C"

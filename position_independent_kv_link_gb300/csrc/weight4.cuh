@@ -30,8 +30,13 @@ inline bool w4_ok(int N, int K, int group) {
          (int64_t)((N + kW4Rows - 1) / kW4Rows) * ((K + kW4Cols - 1) / kW4Cols) <= INT32_MAX;
 }
 
-// The 32-bit word of 8 codes: column e in bits 4 i .. 4 i + 3, i = e / 2 + 4 (e % 2). So (w >> 4 i) & 0x000f000f are columns
-// 2 i and 2 i + 1 in the halves of a register.
+// Where a tile keeps what (include/pic.h). The 16-byte piece q of row r holds one 32-bit word for each of the tile's four
+// 32-column runs: the run's columns 8 q .. 8 q + 7. Column e of the 8 is in bits 4 i .. 4 i + 3, i = e / 2 + 4 (e % 2), so that
+// (w >> 4 i) & 0x000f000f are columns 2 i and 2 i + 1 in the halves of a register. A row's scale and zero stand beside those of
+// the rows 8 apart.
+// A thread that reads its row's pieces meets no other in a bank, nor do four threads that read one row's pieces.
+__host__ __device__ constexpr int w4_piece(int r, int q) { return r * 64 + (q ^ (r >> 1 & 3)) * 16; }
 __host__ __device__ constexpr int w4_shift(int e) { return 4 * (e / 2 + 4 * (e % 2)); }
+__host__ __device__ constexpr int w4_place(int r) { return (r & ~31) + (r & 7) * 4 + (r >> 3 & 3); }
 
 }  // namespace pic
