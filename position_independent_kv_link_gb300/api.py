@@ -643,7 +643,7 @@ def attention_window(q: torch.Tensor, row_start: torch.Tensor, pages: BatchPages
 def attention_prefix(q: torch.Tensor, row_start: torch.Tensor, prefix_blocks: torch.Tensor, prefix_len: int,
                      pages: BatchPages, k_layer: torch.Tensor, v_layer: torch.Tensor, rope: torch.Tensor,
                      prefix_pos: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                     stream=None) -> torch.Tensor:
+                     scratch: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of a batch whose requests share the prefix_len first positions (pic_op_attention_prefix): the pages
     prefix_blocks [n] (prefix_pos [n]: their positions when some hold fewer than 16 rows) are read once for all;
     `pages` are the requests' own, from position prefix_len on. Otherwise as attention_window."""
