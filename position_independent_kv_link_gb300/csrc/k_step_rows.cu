@@ -6,7 +6,7 @@
 
 #include <cuda_fp8.h>
 
-#include "batch_internal.cuh"
+#include "async.cuh"
 
 namespace pic {
 
@@ -113,6 +113,19 @@ void launch_add_norm(const AddNormArgs& a, int T, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ log probabilities
+//
+// One pass over the row: the CTAs of a cluster take a share of it each, which comes in chunks of 16 KB by bulk copies (warp 8), while
+// eight warps read the chunk before. What a warp knows:
+//   m = max;  n = how many are m;  rest = sum over the others of e^(x - m);  e = sum of e^(x - m) (x - m),
+// so that log sum e^(x - m) = log n + log1p(rest / n) keeps its digits when one token has nearly all of the probability. m is the
+// warp's, the others are each lane's; a chunk without a new maximum takes the short loop.
+// Alternatives: the `top`-th greatest of 64 maxima, each of what four threads have seen, is a bound that at least `top` logits reach. It is
+// set anew at chunks 1, 2, 4, 8 .., and a lane whose chunk reaches it puts what does on the CTA's list. At the end the list is ordered by
+// counting, for each, the greater ones. Where more reach the bound than the list holds (ties by the hundred, rising rows), the
+// share's greatest are found one after the other instead, from its logits again.
+// The cluster's first CTA joins the numbers and the lists through shared memory.
+constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32, kLpChunk = 16384, kLpStages = 4, kMaxTop = 32, kLpList = 1024, kLpCluster = 8;
+constexpr int kLpCtas = 3;                         // an SM
 
 struct LogprobArgs {
   int V, top;
@@ -126,82 +139,391 @@ struct LogprobArgs {
   unsigned* flag;
 };
 
-constexpr int kLogprobThreads = 256, kMaxTop = 32;
-
 template <typename T>
 __device__ __forceinline__ float as_float(T x) {
   if constexpr (std::is_same<T, float>::value) return x;
   else if constexpr (std::is_same<T, __half>::value) return __half2float(x);
   else return __bfloat162float(x);
 }
-// Order of the alternatives as that of an unsigned: falling logits (NaN with -inf, -0 with 0), then rising ids.
-__device__ __forceinline__ unsigned long long order_key(float x, int id) {
-  x = x != x ? -INFINITY : x + 0.f;
-  const unsigned u = __float_as_uint(x);
-  return (unsigned long long)(u >> 31 ? ~u : u | 0x80000000u) << 32 | (0xffffffffu - (unsigned)id);
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Order of the alternatives as that of an unsigned: falling logits (-0 with 0), then rising ids. 0: none.
+using Key = unsigned long long;
+__device__ __forceinline__ Key order_key(float x, int id) {
+  const unsigned u = __float_as_uint(x + 0.f);
+  return (Key)(u >> 31 ? ~u : u | 0x80000000u) << 32 | (0xffffffffu - (unsigned)id);
+}
+__device__ __forceinline__ float key_logit(Key k) {
+  const unsigned u = (unsigned)(k >> 32);
+  return __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ int key_id(Key k) { return (int)(0xffffffffu - (unsigned)k); }
+
+// What is known of a part of the row.
+struct LpPart {
+  float m, n, rest, e;       // -inf, 0, 0, 0 without a token
+};
+__device__ __forceinline__ LpPart join(const LpPart& a, const LpPart& b) {
+  const LpPart &hi = a.m >= b.m ? a : b, &lo = a.m >= b.m ? b : a;
+  LpPart r = hi;
+  if (lo.m == hi.m) {
+    r.n += lo.n;
+    r.rest += lo.rest;
+    r.e += lo.e;
+  } else if (lo.n + lo.rest > 0.f) {
+    const float d = lo.m - hi.m, f = ex2(d * kLog2e), l = lo.n + lo.rest;
+    r.rest += f * l;
+    r.e += f * (lo.e + l * fmaxf(d, -1000.f));     // (f is 0 there)
+  }
+  return r;
+}
+__device__ __forceinline__ LpPart join_lanes(LpPart p, int width) {
+  for (int o = width / 2; o > 0; o >>= 1) {
+    LpPart q;
+    q.m = __shfl_xor_sync(0xffffffffu, p.m, o);
+    q.n = __shfl_xor_sync(0xffffffffu, p.n, o);
+    q.rest = __shfl_xor_sync(0xffffffffu, p.rest, o);
+    q.e = __shfl_xor_sync(0xffffffffu, p.e, o);
+    p = join(p, q);
+  }
+  return p;
 }
 
-template <typename T, typename F>
-__device__ T block_reduce(T x, T* sh, F f) {
-  for (int o = 16; o > 0; o >>= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh[0];
-  for (int w = 1; w < kLogprobThreads / 32; ++w) x = f(x, sh[w]);
-  return x;
+struct LpShared {
+  Key list[kLpList];                 // candidates; at the end the cluster's lists
+  Key top[kMaxTop];                  // the CTA's greatest, in order; 0 behind them
+  Key warp_key[kLpWarps];
+  LpPart part[kLpWarps];
+  LpPart all;                        // of the CTA
+  uint64_t full[kLpStages], empty[kLpStages];
+  float group[kLpThreads / 4];       // maxima of four threads
+  float bound;
+  int count, bad;
+  unsigned abort;
+};
+__device__ __forceinline__ void lp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory"); }   // of the eight warps
+
+// The keys of list[0 .. n) in order into s.top (the `top` greatest; they are distinct).
+__device__ __noinline__ void lp_order(LpShared& s, int n, int top) {
+  lp_sync();
+  for (int i = threadIdx.x; i < n; i += kLpThreads) {
+    const Key k = s.list[i];
+    int before = 0;
+    for (int j = 0; j < n; ++j) before += s.list[j] > k;
+    if (before < top) s.top[before] = k;
+  }
+  for (int i = n + threadIdx.x; i < top; i += kLpThreads) s.top[i] = 0;
+  lp_sync();
+}
+
+// The `top` greatest of row[i0 .. i1) into s.top, one after the other.
+template <typename T>
+__device__ __noinline__ void lp_one_by_one(LpShared& s, int top, const T* row, int64_t i0, int64_t i1) {
+  Key before = ~0ull;
+  for (int j = 0; j < top; ++j) {
+    Key best = 0;
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kLpThreads) {
+      const float x = as_float(row[i]);
+      if (x > -INFINITY) {
+        const Key k = order_key(x, (int)i);
+        if (k < before && k > best) best = k;
+      }
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+      const Key k = __shfl_xor_sync(0xffffffffu, best, o);
+      best = k > best ? k : best;
+    }
+    lp_sync();
+    if (threadIdx.x % 32 == 0) s.warp_key[threadIdx.x / 32] = best;
+    lp_sync();
+    for (int w = 0; w < kLpWarps; ++w) best = s.warp_key[w] > best ? s.warp_key[w] : best;
+    if (threadIdx.x == 0) s.top[j] = best;         // 0 when there are no more
+    before = best;
+  }
+  lp_sync();
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLogprobThreads) logprob_kernel(LogprobArgs a) {
-  __shared__ double shd[8];
-  __shared__ unsigned long long shk[8];
-  const int t = blockIdx.x;
-  const T* x = (const T*)a.logits + t * a.stride;
-  const int token = a.tokens ? a.tokens[t] : 0;
-  if (a.tokens && (token < 0 || token >= a.V)) {
-    if (threadIdx.x == 0 && token != -1) batch_flag(a.flag, kBatchBadToken);
+__device__ __forceinline__ T* remote(T* p, unsigned rank) {   // of another CTA of the cluster
+  T* r;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(LogprobArgs a) {
+  constexpr int E = 16 / sizeof(T), kEach = kLpChunk / 16 / kLpThreads * E;   // elements of a vector; of a thread's part of a chunk
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ LpShared s;
+  unsigned ctas, rank;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int t = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* row = (const T*)a.logits + t * a.stride;
+  const int token = a.tokens ? __ldg(a.tokens + t) : 0;
+  if (token < 0 || token >= a.V) {                 // the whole cluster
+    if (tid == 0 && rank == 0 && token != -1) batch_flag(a.flag, kBatchBadToken);
     return;
   }
-  double m = -INFINITY, bad = 0;
-  for (int i = threadIdx.x; i < a.V; i += kLogprobThreads) {
-    const float v = as_float(x[i]);
-    if (v != v || v == INFINITY) bad = 1;
-    else m = fmax(m, (double)v);
-  }
-  auto most = [](double p, double q) { return p > q ? p : q; };
-  auto sum = [](double p, double q) { return p + q; };
-  m = block_reduce(m, shd, most);
-  bad = block_reduce(bad, shd, most);
-  double l = 0, e = 0;
-  if (m > -INFINITY)
-    for (int i = threadIdx.x; i < a.V; i += kLogprobThreads) {
-      const double y = (double)as_float(x[i]) - m;
-      const double p = exp(y);
-      l += p;
-      e += p > 0 ? p * y : 0;
+  // the row: up to E - 1 logits before the first 16-byte border, whole vectors, up to E - 1 behind them
+  const int head = min(a.V, (int)((16 - ((uintptr_t)row & 15)) % 16 / sizeof(T)));
+  const int vectors = (a.V - head) / E, tail = a.V - head - vectors * E;
+  const int chunks = (vectors + kLpChunk / 16 - 1) / (kLpChunk / 16);
+  const int c0 = (int)((int64_t)chunks * rank / ctas), c1 = (int)((int64_t)chunks * (rank + 1) / ctas);
+  if (tid == 0) {
+    s.count = s.bad = 0;
+    s.abort = 0;
+    s.bound = -INFINITY;
+    for (int i = 0; i < kLpStages; ++i) {
+      mbar_init(smem_u32(s.full + i), 1);
+      mbar_init(smem_u32(s.empty + i), kLpWarps);
     }
-  l = block_reduce(l, shd, sum);
-  e = block_reduce(e, shd, sum);
-  const double none = bad ? NAN : 0.0, lse = m > -INFINITY ? m + log(l) : 0.0;
-  if (threadIdx.x == 0) {
-    if (a.tokens) a.logprob[t] = (float)((double)as_float(x[token]) - lse + none);
-    if (a.entropy) a.entropy[t] = (float)((m > -INFINITY ? log(l) - e / l : 0.0) + none);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  unsigned long long before = ~0ull;
-  for (int j = 0; j < a.top; ++j) {
-    unsigned long long best = 0;
-    for (int i = threadIdx.x; i < a.V; i += kLogprobThreads) {
-      const unsigned long long k = order_key(as_float(x[i]), i);
-      if (k < before && k > best) best = k;
+  __syncthreads();
+  if (warp == kLpWarps) {
+    if (lane == 0) {
+      uint64_t policy;
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+      int issued = 0;
+      for (int c = c0; c < c1; ++c, ++issued) {
+        const int st = issued % kLpStages;
+        if (!mbar_wait(smem_u32(s.empty + st), (issued / kLpStages & 1) ^ 1, &s.abort, a.flag)) break;
+        const uint32_t bytes = 16u * min(kLpChunk / 16, vectors - c * (kLpChunk / 16)), fb = smem_u32(s.full + st);
+        mbar_expect_tx(fb, bytes);
+        bulk_load(smem_u32(ring) + st * kLpChunk, (const uint8_t*)(row + head) + (int64_t)c * kLpChunk, bytes, fb, policy);
+      }
+      for (int j = max(0, issued - kLpStages); j < issued; ++j)   // copies under way land before the CTA ends
+        mbar_settle(smem_u32(s.full + j % kLpStages), (uint32_t)((j / kLpStages) & 1), a.flag);
     }
-    before = block_reduce(best, shk, [](unsigned long long p, unsigned long long q) { return p > q ? p : q; });
-    if (threadIdx.x == 0) {
-      const int id = (int)(0xffffffffu - (unsigned)before);
-      a.top_ids[(size_t)t * a.top + j] = id;
-      a.top_logprobs[(size_t)t * a.top + j] = (float)((double)as_float(x[id]) - lse + none);
+  } else {
+    LpPart mine{-INFINITY, 0.f, 0.f, 0.f};         // m the warp's
+    float seen = -INFINITY;                        // this thread's maximum
+    bool bad = false, landed = true;               // (after a wait that was given up chunks count as empty: the barriers below still meet)
+    auto push = [&](float x, int id) {
+      const int at = atomicAdd(&s.count, 1);       // (the order in the list does not matter)
+      if (at < kLpList) s.list[at] = order_key(x, id);
+    };
+    // a new maximum of the warp
+    auto raise = [&](float top1) {
+      float m = top1;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (m > mine.m) {
+        const LpPart none{m, 0.f, 0.f, 0.f};
+        mine = join(none, mine);
+      }
+    };
+    auto exclude = [&](float x) {                  // a logit of a chunk that holds m
+      if (x == mine.m) {
+        mine.n += 1.f;
+      } else {
+        const float d = fmaxf(x - mine.m, -1000.f), p = ex2(d * kLog2e);
+        mine.rest += p;
+        mine.e = fmaf(p, d, mine.e);
+      }
+    };
+    if (warp == 0 && (rank == 0 || rank == ctas - 1)) {   // the row's ends
+      const int i = lane < E ? (rank == 0 && lane < head ? lane : -1) : rank == ctas - 1 && lane - E < tail ? a.V - tail + lane - E : -1;
+      float x = i >= 0 ? as_float(row[i]) : -INFINITY;
+      if (x != x || x == INFINITY) bad = true;
+      if (x != x) x = -INFINITY;
+      raise(x == INFINITY ? -INFINITY : x);
+      if (!bad && x > -INFINITY) exclude(x);
+      if (a.top > 0 && x > -INFINITY) push(x, i);
+    }
+    for (int c = c0; c < c1; ++c) {
+      const int st = (c - c0) % kLpStages, n_vec = min(kLpChunk / 16, vectors - c * (kLpChunk / 16));
+      landed = landed && warp_wait(smem_u32(s.full + st), (c - c0) / kLpStages & 1, &s.abort, a.flag);
+      float x[kEach];
+#pragma unroll
+      for (int v = 0; v < kEach / E; ++v) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        const bool in = landed && v * kLpThreads + tid < n_vec;
+        if (in) u = *reinterpret_cast<const uint4*>(ring + st * kLpChunk + (v * kLpThreads + tid) * 16);
+        if constexpr (sizeof(T) == 4) {
+          x[v * 4] = __uint_as_float(u.x), x[v * 4 + 1] = __uint_as_float(u.y);
+          x[v * 4 + 2] = __uint_as_float(u.z), x[v * 4 + 3] = __uint_as_float(u.w);
+        } else {
+          const T* h = reinterpret_cast<const T*>(&u);
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[v * E + e] = as_float(h[e]);
+        }
+        if (!in) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[v * E + e] = -INFINITY;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(s.empty + st));
+      float top1 = x[0];
+#pragma unroll
+      for (int j = 1; j < kEach; ++j) top1 = max_nan(top1, x[j]);
+      if (top1 != top1 || top1 == INFINITY) {      // the row's numbers are NaN; its order goes on
+        bad = true;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (x[j] != x[j]) x[j] = -INFINITY;
+        top1 = x[0];
+#pragma unroll
+        for (int j = 1; j < kEach; ++j) top1 = fmaxf(top1, x[j]);
+      }
+      raise(top1 == INFINITY ? -INFINITY : top1);
+      if (top1 == mine.m && top1 > -INFINITY) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) exclude(x[j]);
+      } else if (mine.m > -INFINITY) {
+        float rest = 0.f, e = 0.f;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const float d = fmaxf(x[j] - mine.m, -1000.f), p = ex2(d * kLog2e);   // (-inf: p is 0)
+          rest += p;
+          e = fmaf(p, d, e);
+        }
+        mine.rest += rest;
+        mine.e += e;
+      }
+      if (a.top > 0) {
+        seen = fmaxf(seen, top1);
+        const int k = c - c0 + 1;
+        if ((k & (k - 1)) == 0) {                  // the bound
+          float g = fmaxf(seen, __shfl_xor_sync(0xffffffffu, seen, 1));
+          g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+          lp_sync();
+          if (lane % 4 == 0) s.group[tid / 4] = g;
+          lp_sync();
+          if (tid < kLpThreads / 4) {
+            const float v = s.group[tid];
+            int before = 0;
+#pragma unroll 8
+            for (int j = 0; j < kLpThreads / 4; ++j) {
+              const float w = s.group[j];
+              before += w > v || (w == v && j < tid);
+            }
+            if (before == a.top - 1) s.bound = v;
+          }
+          lp_sync();
+        }
+        const float bound = s.bound;
+        if (top1 >= bound && top1 > -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < kEach; ++j)
+            if (x[j] >= bound && x[j] > -INFINITY)
+              push(x[j], head + (c * (kLpChunk / 16) + j / E * kLpThreads + tid) * E + j % E);
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) s.bad = 1;
+    // the CTA's numbers and list
+    LpPart part = join_lanes(mine, 32);
+    if (lane == 0) s.part[warp] = part;
+    lp_sync();
+    if (tid == 0) {
+      for (int w = 1; w < kLpWarps; ++w) part = join(part, s.part[w]);
+      s.all = part;
+    }
+    if (a.top > 0) {
+      if (s.count <= kLpList) {
+        lp_order(s, s.count, a.top);
+      } else {
+        const int64_t per = kLpChunk / sizeof(T);
+        lp_one_by_one(s, a.top, row, rank == 0 ? 0 : head + c0 * per, rank == ctas - 1 ? a.V : head + c1 * per);
+      }
     }
   }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  if (rank == 0 && warp < kLpWarps) {
+    // every thread: the row's numbers
+    LpPart all = s.all;
+    bool bad = s.bad;
+    for (unsigned c = 1; c < ctas; ++c) {
+      all = join(all, *remote(&s.all, c));
+      bad |= *remote(&s.bad, c) != 0;
+    }
+    const float lose = all.n > 0.f ? logf(all.n) + log1pf(all.rest / all.n) : 0.f;   // log sum e^(x - m)
+    const float from = all.n > 0.f ? all.m : 0.f;
+    if (tid == 0) {
+      if (a.tokens) a.logprob[t] = bad ? NAN : as_float(row[token]) - from - lose;
+      if (a.entropy) a.entropy[t] = bad ? NAN : all.n > 0.f ? lose - all.e / (all.n + all.rest) : 0.f;
+    }
+    if (a.top > 0) {
+      if (ctas > 1) {
+        const int n = (int)ctas * a.top;           // 256 at most
+        const Key k = tid < n ? remote(s.top, tid / a.top)[tid % a.top] : 0;   // (its own list is read by this CTA alone)
+        lp_sync();
+        if (tid == 0) s.count = 0;
+        lp_sync();
+        if (k != 0) s.list[atomicAdd(&s.count, 1)] = k;
+        lp_sync();
+        lp_order(s, s.count, a.top);
+      }
+      if (warp == 0) {
+        const Key k = lane < a.top ? s.top[lane] : 0;
+        const int have = __popc(__ballot_sync(0xffffffffu, k != 0));
+        int id = key_id(k);
+        float lp = key_logit(k) - from - lose;
+        if (have < a.top) {                        // tokens without probability, in the order of their ids
+          int found = have;
+          for (int i0 = 0; i0 < a.V && found < a.top; i0 += 32) {
+            const float x = lane < a.V - i0 ? as_float(row[i0 + lane]) : 0.f;
+            const unsigned some = __ballot_sync(0xffffffffu, !(x > -INFINITY));
+            const int nth = lane - found;          // this lane's place wants the nth of them
+            if (nth >= 0 && nth < __popc(some)) {
+              unsigned left = some;
+              for (int q = 0; q < nth; ++q) left &= left - 1;
+              id = i0 + __ffs(left) - 1;
+              lp = -INFINITY;
+            }
+            found += __popc(some);
+          }
+        }
+        if (lane < a.top) {
+          a.top_ids[(size_t)t * a.top + lane] = id;
+          a.top_logprobs[(size_t)t * a.top + lane] = bad ? NAN : lp;
+        }
+      }
+    }
+  }
+  if (ctas > 1) cluster_sync();
+}
+
+template <typename T>
+pic_status launch_logprob(const LogprobArgs& a, int rows, int slots, cudaStream_t st) {
+  // CTAs of a row: the fewest turns of all CTAs over their chunks, each with its start and end (as long as three chunks)
+  const int64_t chunks = std::max<int64_t>(1, ((int64_t)a.V * sizeof(T) + kLpChunk - 1) / kLpChunk);
+  int ctas = 1;
+  int64_t least = INT64_MAX;
+  for (int c = 1; c <= std::min<int64_t>(chunks, kLpCluster); ++c) {
+    const int64_t cost = ((int64_t)rows * c + slots - 1) / slots * ((chunks + c - 1) / c + 3);
+    if (cost < least) least = cost, ctas = c;
+  }
+  PIC_CUDA(cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpStages * kLpChunk));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)rows * ctas);
+  cfg.blockDim = dim3(kLpThreads + 32);
+  cfg.dynamicSmemBytes = kLpStages * kLpChunk;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  PIC_CUDA(cudaLaunchKernelEx(&cfg, logprob_kernel<T>, a));
+  return PIC_OK;
 }
 
 bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
@@ -267,15 +589,17 @@ pic_status pic_op_token_logprobs(int32_t dtype, int32_t T, int32_t vocab, const 
     if (met) return fail(PIC_ERR_INVALID_ARG, "outputs must not overlap logits, tokens or one another");
   }
   if (!logprob && !entropy && !top) return fail(PIC_ERR_INVALID_ARG, "token log probabilities: no output is asked for");
+  if (T > INT_MAX / kLpCluster) return fail(PIC_ERR_CAPACITY, "token log probabilities: too many rows");
   LogprobArgs a{vocab, top, logits, logits_stride, tokens, logprob, entropy, top_ids, top_logprobs, nullptr};
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
+  int dev = 0, sms = 0;
+  PIC_CUDA(cudaGetDevice(&dev));
+  PIC_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == PIC_F32) logprob_kernel<float><<<T, kLogprobThreads, 0, st>>>(a);
-  else if (dtype == PIC_F16) logprob_kernel<__half><<<T, kLogprobThreads, 0, st>>>(a);
-  else logprob_kernel<__nv_bfloat16><<<T, kLogprobThreads, 0, st>>>(a);
-  PIC_CUDA(cudaGetLastError());
-  return PIC_OK;
+  return dtype == PIC_F32   ? launch_logprob<float>(a, T, kLpCtas * sms, st)
+         : dtype == PIC_F16 ? launch_logprob<__half>(a, T, kLpCtas * sms, st)
+                            : launch_logprob<__nv_bfloat16>(a, T, kLpCtas * sms, st);
 }
 
 }  // extern "C"

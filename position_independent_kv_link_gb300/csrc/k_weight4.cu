@@ -11,7 +11,7 @@
 
 #include <cuda_fp8.h>
 
-#include "batch_internal.cuh"
+#include "async.cuh"
 #include "weight4.cuh"
 
 namespace pic {
@@ -178,14 +178,12 @@ struct Gemm4Args {
 // band's blocks and add their sums through each other's shared memory, in the order of their ranks. So there is no scratch, and
 // the same call gives the same bits again.
 
-constexpr unsigned long long kGemm4WaitLimit = 4000000000ull;   // SM cycles, about 2 s
 
 struct Gemm4Plan {
   int stages, x_bytes;       // of X in a stage
   int across, bands;         // bands of one tile of X, of all
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // Shared memory by its own addresses (through pointers that were rounded up the loads become generic ones)
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
@@ -218,65 +216,6 @@ __device__ __forceinline__ float4 lds_f32x4(uint32_t at) {
   return v;
 }
 __device__ __forceinline__ void sts_f32(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// the same, but suspended for up to 20 us before it answers
-__device__ __forceinline__ bool mbar_try_long(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-// false (and the timeout flag) after kGemm4WaitLimit, or when the CTA has given up (`abort`: its word in shared memory)
-__device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
-  const unsigned long long t0 = clock64();
-  for (;;) {
-    if (mbar_try_long(bar, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > kGemm4WaitLimit) {
-      atomicOr(flag, kBatchTimeout);
-      *abort = 1;
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
-  return mbar_try(bar, parity) || mbar_try_long(bar, parity) || mbar_wait_on(bar, parity, abort, flag);
-}
-// for the whole warp: the same answer in every lane
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, flag));
-}
-// waits on when the CTA has given up
-__device__ __forceinline__ void mbar_settle(uint32_t bar, uint32_t parity, unsigned* flag) {
-  unsigned none = 0;
-  if (!mbar_try(bar, parity)) mbar_wait_on(bar, parity, &none, flag);
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
@@ -339,9 +278,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // The sum of *at over the cluster's CTAs, in the order of their ranks.
 __device__ __forceinline__ float cluster_sum(uint32_t at, uint32_t ctas) {
   float sum = 0.f;
