@@ -114,18 +114,20 @@ void launch_add_norm(const AddNormArgs& a, int T, cudaStream_t st) {
 
 // ------------------------------------------------------------------ log probabilities
 //
-// One pass over the row: the CTAs of a cluster take a share of it each, which comes in chunks of 16 KB by bulk copies (warp 8), while
-// eight warps read the chunk before. What a warp knows:
+// One pass over the row: the CTAs of a cluster take a share of it each, which comes in chunks by bulk copies (the last warp), while
+// the other warps read the chunk before. What a warp knows:
 //   m = max;  n = how many are m;  rest = sum over the others of e^(x - m);  e = sum of e^(x - m) (x - m),
 // so that log sum e^(x - m) = log n + log1p(rest / n) keeps its digits when one token has nearly all of the probability. m is the
 // warp's, the others are each lane's; a chunk without a new maximum takes the short loop.
-// Alternatives: the `top`-th greatest of 64 maxima, each of what four threads have seen, is a bound that at least `top` logits reach. It is
-// set anew at chunks 1, 2, 4, 8 .., and a lane whose chunk reaches it puts what does on the CTA's list. At the end the list is ordered by
+// Alternatives: the `top`-th greatest of 64 maxima, each of what a few threads have seen, is a bound that at least `top` logits reach, and
+// a lane whose chunk reaches it puts what does on the CTA's list. After the first chunk, where the warps meet, one warp sets the bound
+// anew (chunks 2, 4, 8 ..) from the maxima as it finds them: an old bound is as right, it lets more through. At the end the list is ordered by
 // counting, for each, the greater ones. Where more reach the bound than the list holds (ties by the hundred, rising rows), the
 // share's greatest are found one after the other instead, from its logits again.
-// The cluster's first CTA joins the numbers and the lists through shared memory.
-constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32, kLpChunk = 16384, kLpStages = 4, kMaxTop = 32, kLpList = 1024, kLpCluster = 8;
-constexpr int kLpCtas = 3;                         // an SM
+// The CTAs of a cluster put their numbers and lists into the first one's shared memory, which joins them.
+constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32, kLpChunk = 32768, kLpStages = 3, kMaxTop = 32, kLpList = 1024, kLpCluster = 8;
+constexpr int kLpCtas = 2;                         // an SM
+constexpr int kLpGroup = kLpThreads / 64;          // threads that share a maximum
 
 struct LogprobArgs {
   int V, top;
@@ -145,9 +147,49 @@ __device__ __forceinline__ float as_float(T x) {
   else if constexpr (std::is_same<T, __half>::value) return __half2float(x);
   else return __bfloat162float(x);
 }
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one of them is
+// The values of 16 bytes
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 u, float* x) {
+  const unsigned w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, float>::value) {
+      x[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {   // NaN if one of them is
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// two fp32 operations at once
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -155,7 +197,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Order of the alternatives as that of an unsigned: falling logits (-0 with 0), then rising ids. 0: none.
 using Key = unsigned long long;
@@ -200,30 +242,51 @@ __device__ __forceinline__ LpPart join_lanes(LpPart p, int width) {
 }
 
 struct LpShared {
-  Key list[kLpList];                 // candidates; at the end the cluster's lists
-  Key top[kMaxTop];                  // the CTA's greatest, in order; 0 behind them
+  Key list[kLpList];                 // candidates
+  Key joined[kLpCluster * kMaxTop];  // the cluster's lists
+  Key top[kMaxTop];                  // the greatest, in order; 0 behind them
   Key warp_key[kLpWarps];
   LpPart part[kLpWarps];
-  LpPart all;                        // of the CTA
+  LpPart all[kLpCluster];            // of the CTAs
+  int bad[kLpCluster];
   uint64_t full[kLpStages], empty[kLpStages];
-  float group[kLpThreads / 4];       // maxima of four threads
+  float group[64];                   // maxima of a few threads
   float bound;
-  int count, bad;
+  int count;
   unsigned abort;
 };
-__device__ __forceinline__ void lp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory"); }   // of the eight warps
+__device__ __forceinline__ void lp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory"); }   // of the warps that read
 
-// The keys of list[0 .. n) in order into s.top (the `top` greatest; they are distinct).
-__device__ __noinline__ void lp_order(LpShared& s, int n, int top) {
+// The `top` greatest keys of list[0 .. n) in order into s.top (they are distinct, but for 0: none).
+__device__ __noinline__ void lp_order(LpShared& s, const Key* list, int n, int top) {
+  if ((int)threadIdx.x < top) s.top[threadIdx.x] = 0;
   lp_sync();
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const Key k = s.list[i];
+  for (int i0 = 0; i0 < n; i0 += kLpThreads / 4) {   // four threads a key
+    const int i = i0 + threadIdx.x / 4;
+    const Key k = i < n ? list[i] : 0;
     int before = 0;
-    for (int j = 0; j < n; ++j) before += s.list[j] > k;
-    if (before < top) s.top[before] = k;
+    for (int j = threadIdx.x % 4; j < n; j += 4) before += list[j] > k;
+    before += __shfl_xor_sync(0xffffffffu, before, 1);
+    before += __shfl_xor_sync(0xffffffffu, before, 2);
+    if (k != 0 && threadIdx.x % 4 == 0 && before < top) s.top[before] = k;
   }
-  for (int i = n + threadIdx.x; i < top; i += kLpThreads) s.top[i] = 0;
   lp_sync();
+}
+
+// The `top`-th greatest of the maxima, by one warp: each lane counts, for two of them, the greater ones.
+__device__ __forceinline__ void lp_bound(LpShared& s, int top) {
+  const int lane = threadIdx.x & 31;
+  const volatile float* group = s.group;           // (others write while this reads: any mixture will do)
+  const float a = group[lane], b = group[lane + 32];
+  int na = 0, nb = 0;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const float x = __shfl_sync(0xffffffffu, a, j), y = __shfl_sync(0xffffffffu, b, j);
+    na += (x > a || (x == a && j < lane)) + (y > a);
+    nb += (x >= b) + (y > b || (y == b && j < lane));
+  }
+  if (na == top - 1) s.bound = a;
+  if (nb == top - 1) s.bound = b;
 }
 
 // The `top` greatest of row[i0 .. i1) into s.top, one after the other.
@@ -262,7 +325,8 @@ __device__ __forceinline__ T* remote(T* p, unsigned rank) {   // of another CTA 
 
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(LogprobArgs a) {
-  constexpr int E = 16 / sizeof(T), kEach = kLpChunk / 16 / kLpThreads * E;   // elements of a vector; of a thread's part of a chunk
+  constexpr int E = 16 / sizeof(T), kVecs = kLpChunk / 16, NV = kVecs / kLpThreads, kEach = NV * E;   // elements of a vector; vectors of a chunk; a thread's
+  static_assert(kEach <= 64, "a bit for each");
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ LpShared s;
   unsigned ctas, rank;
@@ -275,13 +339,15 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
     if (tid == 0 && rank == 0 && token != -1) batch_flag(a.flag, kBatchBadToken);
     return;
   }
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // (waited for before another CTA's memory is written)
   // the row: up to E - 1 logits before the first 16-byte border, whole vectors, up to E - 1 behind them
   const int head = min(a.V, (int)((16 - ((uintptr_t)row & 15)) % 16 / sizeof(T)));
   const int vectors = (a.V - head) / E, tail = a.V - head - vectors * E;
-  const int chunks = (vectors + kLpChunk / 16 - 1) / (kLpChunk / 16);
+  const int chunks = (vectors + kVecs - 1) / kVecs;
   const int c0 = (int)((int64_t)chunks * rank / ctas), c1 = (int)((int64_t)chunks * (rank + 1) / ctas);
   if (tid == 0) {
-    s.count = s.bad = 0;
+    s.count = 0;
+    s.bad[0] = 0;
     s.abort = 0;
     s.bound = -INFINITY;
     for (int i = 0; i < kLpStages; ++i) {
@@ -292,6 +358,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
+  bool bad = false;
   if (warp == kLpWarps) {
     if (lane == 0) {
       uint64_t policy;
@@ -300,7 +367,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
       for (int c = c0; c < c1; ++c, ++issued) {
         const int st = issued % kLpStages;
         if (!mbar_wait(smem_u32(s.empty + st), (issued / kLpStages & 1) ^ 1, &s.abort, a.flag)) break;
-        const uint32_t bytes = 16u * min(kLpChunk / 16, vectors - c * (kLpChunk / 16)), fb = smem_u32(s.full + st);
+        const uint32_t bytes = 16u * min(kVecs, vectors - c * kVecs), fb = smem_u32(s.full + st);
         mbar_expect_tx(fb, bytes);
         bulk_load(smem_u32(ring) + st * kLpChunk, (const uint8_t*)(row + head) + (int64_t)c * kLpChunk, bytes, fb, policy);
       }
@@ -310,29 +377,19 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
   } else {
     LpPart mine{-INFINITY, 0.f, 0.f, 0.f};         // m the warp's
     float seen = -INFINITY;                        // this thread's maximum
-    bool bad = false, landed = true;               // (after a wait that was given up chunks count as empty: the barriers below still meet)
+    bool landed = true;                            // (after a wait that was given up chunks count as empty: the barriers below still meet)
     auto push = [&](float x, int id) {
       const int at = atomicAdd(&s.count, 1);       // (the order in the list does not matter)
       if (at < kLpList) s.list[at] = order_key(x, id);
     };
     // a new maximum of the warp
     auto raise = [&](float top1) {
+      if (!__any_sync(0xffffffffu, top1 > mine.m)) return;
       float m = top1;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (m > mine.m) {
-        const LpPart none{m, 0.f, 0.f, 0.f};
-        mine = join(none, mine);
-      }
-    };
-    auto exclude = [&](float x) {                  // a logit of a chunk that holds m
-      if (x == mine.m) {
-        mine.n += 1.f;
-      } else {
-        const float d = fmaxf(x - mine.m, -1000.f), p = ex2(d * kLog2e);
-        mine.rest += p;
-        mine.e = fmaf(p, d, mine.e);
-      }
+      const LpPart none{m, 0.f, 0.f, 0.f};
+      mine = join(none, mine);
     };
     if (warp == 0 && (rank == 0 || rank == ctas - 1)) {   // the row's ends
       const int i = lane < E ? (rank == 0 && lane < head ? lane : -1) : rank == ctas - 1 && lane - E < tail ? a.V - tail + lane - E : -1;
@@ -340,163 +397,163 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
       if (x != x || x == INFINITY) bad = true;
       if (x != x) x = -INFINITY;
       raise(x == INFINITY ? -INFINITY : x);
-      if (!bad && x > -INFINITY) exclude(x);
+      if (x > -INFINITY && mine.m > -INFINITY) {
+        const float d = fmaxf(x - mine.m, -1000.f), p = ex2(d * kLog2e);
+        if (x == mine.m) mine.n = 1.f;
+        else mine.rest = p;
+        mine.e = p * d;
+      }
       if (a.top > 0 && x > -INFINITY) push(x, i);
     }
+    int st = 0;
+    uint32_t ph = 0;
     for (int c = c0; c < c1; ++c) {
-      const int st = (c - c0) % kLpStages, n_vec = min(kLpChunk / 16, vectors - c * (kLpChunk / 16));
-      landed = landed && warp_wait(smem_u32(s.full + st), (c - c0) / kLpStages & 1, &s.abort, a.flag);
-      float x[kEach];
+      landed = landed && warp_wait(smem_u32(s.full + st), ph, &s.abort, a.flag);
+      const int n_vec = min(kVecs, vectors - c * kVecs);
+      const uint8_t* part = ring + st * kLpChunk + tid * 16;   // this thread's vectors are kLpThreads apart
+      const int own = landed && tid < n_vec ? (n_vec - tid - 1) / kLpThreads + 1 : 0;
+      float x[kEach], top1 = -INFINITY;
+      if (own == NV) {
 #pragma unroll
-      for (int v = 0; v < kEach / E; ++v) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        const bool in = landed && v * kLpThreads + tid < n_vec;
-        if (in) u = *reinterpret_cast<const uint4*>(ring + st * kLpChunk + (v * kLpThreads + tid) * 16);
-        if constexpr (sizeof(T) == 4) {
-          x[v * 4] = __uint_as_float(u.x), x[v * 4 + 1] = __uint_as_float(u.y);
-          x[v * 4 + 2] = __uint_as_float(u.z), x[v * 4 + 3] = __uint_as_float(u.w);
-        } else {
-          const T* h = reinterpret_cast<const T*>(&u);
+        for (int v = 0; v < NV; ++v) unpack<T>(*reinterpret_cast<const uint4*>(part + v * (kLpThreads * 16)), x + v * E);
+      } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[v * E + e] = as_float(h[e]);
-        }
-        if (!in) {
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int e = 0; e < E; ++e) x[v * E + e] = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (v < own) unpack<T>(*reinterpret_cast<const uint4*>(part + v * (kLpThreads * 16)), x + v * E);
+      }
+#pragma unroll
+      for (int v = 0; v < kEach; v += 4) top1 = max_nan(top1, max_nan(x[v], x[v + 1], x[v + 2]), x[v + 3]);
+      auto again = [&](int j) { return as_float(reinterpret_cast<const T*>(part + j / E * (kLpThreads * 16))[j % E]); };   // x[j]
+      if (top1 != top1 || top1 == INFINITY) {      // the row's numbers are NaN; its order goes on
+        bad = true;
+        top1 = -INFINITY;
+#pragma unroll 1
+        for (int j = 0; j < own * E; ++j) top1 = fmaxf(top1, again(j));
+      }
+      raise(top1 == INFINITY ? -INFINITY : top1);
+      if (mine.m > -INFINITY) {
+        // in the log2 domain, two at a time; of a chunk that holds m (few do) the logits that are m count apart
+        const bool holds = __any_sync(0xffffffffu, top1 == mine.m);
+        const float2 from = make_float2(-mine.m, -mine.m), unit = make_float2(kLog2e, kLog2e);
+        float2 rest = make_float2(0.f, 0.f), e = rest;
+        unsigned n = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; j += 2) {
+          float2 d = mul2(add2(make_float2(x[j], x[j + 1]), from), unit);
+          d = make_float2(fmaxf(d.x, -1500.f), fmaxf(d.y, -1500.f));   // (-inf: p is 0)
+          float2 p = make_float2(ex2(d.x), ex2(d.y));
+          if (holds) {
+            n += (x[j] == mine.m) + (x[j + 1] == mine.m);
+            p = make_float2(x[j] == mine.m ? 0.f : p.x, x[j + 1] == mine.m ? 0.f : p.y);
+          }
+          rest = add2(rest, p);
+          e = fma2(p, d, e);
+        }
+        mine.n += (float)n;
+        mine.rest += rest.x + rest.y;
+        mine.e += (e.x + e.y) * kLn2;
+      }
+      if (a.top > 0) {
+        seen = fmaxf(seen, top1);
+        float g = seen;
+#pragma unroll
+        for (int o = 1; o < kLpGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        const int k = c - c0;
+        if (lane % kLpGroup == 0) const_cast<volatile float*>(s.group)[tid / kLpGroup] = g;
+        if (k == 0) {
+          lp_sync();
+          if (warp == 0) lp_bound(s, a.top);
+          lp_sync();
+        } else if ((k & (k + 1)) == 0 && __popc(k) % kLpWarps == warp) {   // chunks 2, 4, 8 ..
+          __syncwarp();
+          lp_bound(s, a.top);
+        }
+        const float bound = *const_cast<volatile float*>(&s.bound);
+        if (top1 >= bound && top1 > -INFINITY) {   // few lanes, of one or two logits mostly
+          unsigned long long reach = 0;
+#pragma unroll
+          for (int j = 0; j < kEach; ++j) reach |= (unsigned long long)(x[j] >= bound) << j;
+          for (; reach; reach &= reach - 1) {
+            const int j = __ffsll(reach) - 1;
+            const float y = again(j);
+            if (j < own * E && y > -INFINITY) push(y, head + (c * kVecs + j / E * kLpThreads + tid) * E + j % E);
+          }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(s.empty + st));
-      float top1 = x[0];
-#pragma unroll
-      for (int j = 1; j < kEach; ++j) top1 = max_nan(top1, x[j]);
-      if (top1 != top1 || top1 == INFINITY) {      // the row's numbers are NaN; its order goes on
-        bad = true;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j)
-          if (x[j] != x[j]) x[j] = -INFINITY;
-        top1 = x[0];
-#pragma unroll
-        for (int j = 1; j < kEach; ++j) top1 = fmaxf(top1, x[j]);
-      }
-      raise(top1 == INFINITY ? -INFINITY : top1);
-      if (top1 == mine.m && top1 > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) exclude(x[j]);
-      } else if (mine.m > -INFINITY) {
-        float rest = 0.f, e = 0.f;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-          const float d = fmaxf(x[j] - mine.m, -1000.f), p = ex2(d * kLog2e);   // (-inf: p is 0)
-          rest += p;
-          e = fmaf(p, d, e);
-        }
-        mine.rest += rest;
-        mine.e += e;
-      }
-      if (a.top > 0) {
-        seen = fmaxf(seen, top1);
-        const int k = c - c0 + 1;
-        if ((k & (k - 1)) == 0) {                  // the bound
-          float g = fmaxf(seen, __shfl_xor_sync(0xffffffffu, seen, 1));
-          g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-          lp_sync();
-          if (lane % 4 == 0) s.group[tid / 4] = g;
-          lp_sync();
-          if (tid < kLpThreads / 4) {
-            const float v = s.group[tid];
-            int before = 0;
-#pragma unroll 8
-            for (int j = 0; j < kLpThreads / 4; ++j) {
-              const float w = s.group[j];
-              before += w > v || (w == v && j < tid);
-            }
-            if (before == a.top - 1) s.bound = v;
-          }
-          lp_sync();
-        }
-        const float bound = s.bound;
-        if (top1 >= bound && top1 > -INFINITY) {
-#pragma unroll
-          for (int j = 0; j < kEach; ++j)
-            if (x[j] >= bound && x[j] > -INFINITY)
-              push(x[j], head + (c * (kLpChunk / 16) + j / E * kLpThreads + tid) * E + j % E);
-        }
-      }
+      if (++st == kLpStages) st = 0, ph ^= 1;
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) s.bad = 1;
     // the CTA's numbers and list
-    LpPart part = join_lanes(mine, 32);
+    const LpPart part = join_lanes(mine, 32);
     if (lane == 0) s.part[warp] = part;
     lp_sync();
-    if (tid == 0) {
-      for (int w = 1; w < kLpWarps; ++w) part = join(part, s.part[w]);
-      s.all = part;
-    }
     if (a.top > 0) {
-      if (s.count <= kLpList) {
-        lp_order(s, s.count, a.top);
+      const int n = s.count;
+      if (n <= kLpList) {
+        lp_order(s, s.list, n, a.top);
       } else {
         const int64_t per = kLpChunk / sizeof(T);
         lp_one_by_one(s, a.top, row, rank == 0 ? 0 : head + c0 * per, rank == ctas - 1 ? a.V : head + c1 * per);
       }
     }
   }
+  bad = __syncthreads_or(bad);
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA has begun
+  if (tid == 0) {
+    LpPart part = s.part[0];
+#pragma unroll
+    for (int w = 1; w < kLpWarps; ++w) part = join(part, s.part[w]);
+    remote(s.all, 0)[rank] = part;
+    remote(s.bad, 0)[rank] = bad;
+  }
+  if (tid < a.top) remote(s.joined, 0)[rank * a.top + tid] = s.top[tid];
   if (ctas > 1) cluster_sync();
   else __syncthreads();
-  if (rank == 0 && warp < kLpWarps) {
-    // every thread: the row's numbers
-    LpPart all = s.all;
-    bool bad = s.bad;
-    for (unsigned c = 1; c < ctas; ++c) {
-      all = join(all, *remote(&s.all, c));
-      bad |= *remote(&s.bad, c) != 0;
-    }
-    const float lose = all.n > 0.f ? logf(all.n) + log1pf(all.rest / all.n) : 0.f;   // log sum e^(x - m)
-    const float from = all.n > 0.f ? all.m : 0.f;
-    if (tid == 0) {
-      if (a.tokens) a.logprob[t] = bad ? NAN : as_float(row[token]) - from - lose;
-      if (a.entropy) a.entropy[t] = bad ? NAN : all.n > 0.f ? lose - all.e / (all.n + all.rest) : 0.f;
-    }
-    if (a.top > 0) {
-      if (ctas > 1) {
-        const int n = (int)ctas * a.top;           // 256 at most
-        const Key k = tid < n ? remote(s.top, tid / a.top)[tid % a.top] : 0;   // (its own list is read by this CTA alone)
-        lp_sync();
-        if (tid == 0) s.count = 0;
-        lp_sync();
-        if (k != 0) s.list[atomicAdd(&s.count, 1)] = k;
-        lp_sync();
-        lp_order(s, s.count, a.top);
+  if (rank != 0 || warp >= kLpWarps) return;
+  // every thread: the row's numbers
+  LpPart all = s.all[0];
+  bad = s.bad[0] != 0;
+  for (unsigned c = 1; c < ctas; ++c) {
+    all = join(all, s.all[c]);
+    bad |= s.bad[c] != 0;
+  }
+  const float lose = all.n > 0.f ? logf(all.n) + log1pf(all.rest / all.n) : 0.f;   // log sum e^(x - m)
+  const float from = all.n > 0.f ? all.m : 0.f;
+  if (tid == 0) {
+    if (a.tokens) a.logprob[t] = bad ? NAN : as_float(row[token]) - from - lose;
+    if (a.entropy) a.entropy[t] = bad ? NAN : all.n > 0.f ? lose - all.e / (all.n + all.rest) : 0.f;
+  }
+  if (a.top == 0) return;
+  if (ctas > 1) lp_order(s, s.joined, (int)ctas * a.top, a.top);
+  if (warp > 0) return;
+  const Key k = lane < a.top ? s.top[lane] : 0;
+  const int have = __popc(__ballot_sync(0xffffffffu, k != 0));
+  int id = key_id(k);
+  float lp = key_logit(k) - from - lose;
+  if (have < a.top) {                              // tokens without probability, in the order of their ids
+    int found = have;
+    for (int i0 = 0; i0 < a.V && found < a.top; i0 += 32) {
+      const float x = lane < a.V - i0 ? as_float(row[i0 + lane]) : 0.f;
+      const unsigned some = __ballot_sync(0xffffffffu, !(x > -INFINITY));
+      const int nth = lane - found;                // this lane's place wants the nth of them
+      if (nth >= 0 && nth < __popc(some)) {
+        unsigned left = some;
+        for (int q = 0; q < nth; ++q) left &= left - 1;
+        id = i0 + __ffs(left) - 1;
+        lp = -INFINITY;
       }
-      if (warp == 0) {
-        const Key k = lane < a.top ? s.top[lane] : 0;
-        const int have = __popc(__ballot_sync(0xffffffffu, k != 0));
-        int id = key_id(k);
-        float lp = key_logit(k) - from - lose;
-        if (have < a.top) {                        // tokens without probability, in the order of their ids
-          int found = have;
-          for (int i0 = 0; i0 < a.V && found < a.top; i0 += 32) {
-            const float x = lane < a.V - i0 ? as_float(row[i0 + lane]) : 0.f;
-            const unsigned some = __ballot_sync(0xffffffffu, !(x > -INFINITY));
-            const int nth = lane - found;          // this lane's place wants the nth of them
-            if (nth >= 0 && nth < __popc(some)) {
-              unsigned left = some;
-              for (int q = 0; q < nth; ++q) left &= left - 1;
-              id = i0 + __ffs(left) - 1;
-              lp = -INFINITY;
-            }
-            found += __popc(some);
-          }
-        }
-        if (lane < a.top) {
-          a.top_ids[(size_t)t * a.top + lane] = id;
-          a.top_logprobs[(size_t)t * a.top + lane] = bad ? NAN : lp;
-        }
-      }
+      found += __popc(some);
     }
   }
-  if (ctas > 1) cluster_sync();
+  if (lane < a.top) {
+    a.top_ids[(size_t)t * a.top + lane] = id;
+    a.top_logprobs[(size_t)t * a.top + lane] = bad ? NAN : lp;
+  }
 }
 
 template <typename T>

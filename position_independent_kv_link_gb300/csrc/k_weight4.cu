@@ -40,15 +40,29 @@ __device__ __forceinline__ void load32(const T* p, float* x) {   // 32 values, 1
   }
 }
 
-// The integer nearest to x / s (ties to even), decided exactly: the quotient in fp32 gives an integer k that may be off by
-// one next to a border; x - k s is exact in fp32 (s has 11 bits, and x lies within 16 s), as is s / 2.
-__device__ __forceinline__ float nearest_quotient(float x, float s) {
-  float k = rintf(x / s);
-  const float d = fmaf(-k, s, x), half = 0.5f * s;
-  const bool odd = fmodf(k, 2.f) != 0.f;
-  if (d > half || (d == half && odd)) k += 1.f;
-  else if (d < -half || (d == -half && odd)) k -= 1.f;
-  return k;
+// The integer nearest to x / s (ties to even), decided exactly: x (1 / s) in fp32 gives an integer k that may be off by one next
+// to a border; x - k s is exact in fp32 (s has 11 bits, and x lies within some 20 s), as is s / 2. rs: 1 / s.
+__device__ __forceinline__ int nearest_quotient(float x, float s, float rs) {
+  constexpr float kMagic = 12582912.f;                 // 1.5 2^23: integers are the spacing there
+  const float t = fmaf(x, rs, kMagic), d = fmaf(kMagic - t, s, x), half = 0.5f * s;
+  const int k = __float_as_int(t) - __float_as_int(kMagic);
+  return k + (d > half || (d == half && (k & 1))) - (d < -half || (d == -half && (k & 1)));
+}
+
+// The four threads of a row hold its runs' words of each piece; they trade them for a piece each, and write 64 bytes together.
+__device__ __forceinline__ void put_pieces(uint8_t* tile, int r, int j, uint32_t* w) {
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const bool up = j & o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int lo = o == 1 ? 2 * i : i, hi = lo + o;
+      const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? w[lo] : w[hi], o);
+      if (up) w[lo] = t;
+      else w[hi] = t;
+    }
+  }
+  *reinterpret_cast<uint4*>(tile + w4_piece(r, j)) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T>
@@ -58,12 +72,12 @@ __global__ void __launch_bounds__(kPackThreads) pack4_kernel(const T* __restrict
   uint8_t* tile = out + (size_t)blockIdx.x * p.tile_bytes;
   const int per = kW4Cols / p.group;                   // groups of a tile's row
   const int lanes = p.group / 32;                      // threads that share a group
+#pragma unroll 1
   for (int i = threadIdx.x; i < kW4Rows * 4; i += kPackThreads) {
     const int r = i / 4, j = i % 4;
     const int n = nt * kW4Rows + r, k = kt * kW4Cols + 32 * j;
     float x[32];
-    const bool in = n < p.N && k < p.K;
-    if (in) {
+    if (n < p.N && k < p.K) {
       load32(W + (size_t)n * p.K + k, x);
     } else {
 #pragma unroll
@@ -75,29 +89,29 @@ __global__ void __launch_bounds__(kPackThreads) pack4_kernel(const T* __restrict
     for (int e = 0; e < 32; ++e) {
       lo = fminf(lo, x[e]);
       hi = fmaxf(hi, x[e]);
-      fine = fine && fabsf(x[e]) <= FLT_MAX;
+      fine = fine && x[e] == x[e];
     }
     for (int o = 1; o < lanes; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       fine = __shfl_xor_sync(0xffffffffu, fine, o) && fine;
     }
+    // (16-bit extremes: their difference divided in fp64, rounded to fp32 and then to fp16)
     __half hs = __float2half_rn((float)(((double)hi - (double)lo) / 15.0));
-    if (__hisinf(hs)) fine = false;
+    if (__hisinf(hs)) fine = false;                    // infinite weights too
     if (!fine) {
       batch_flag(flag, kBatchRange);
       hs = __float2half_rn(0.f);
     }
-    const float s = __half2float(hs);
-    const float z = s > 0.f ? fminf(nearest_quotient(-lo, s), 15.f) : 0.f;
+    const float s = __half2float(hs), rs = s > 0.f ? 1.f / s : 0.f;
+    const int z = s > 0.f ? min(nearest_quotient(-lo, s, rs), 15) : 0;
     uint32_t w[4] = {};
+    if (s > 0.f) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float c = s > 0.f ? fminf(fmaxf(nearest_quotient(x[e], s) + z, 0.f), 15.f) : 0.f;
-      w[e / 8] |= (uint32_t)c << w4_shift(e % 8);
+      for (int e = 0; e < 32; ++e)
+        w[e / 8] |= (uint32_t)min(max(nearest_quotient(x[e], s, rs) + z, 0), 15) << w4_shift(e % 8);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t*>(tile + w4_piece(r, q) + 4 * j) = w[q];
+    put_pieces(tile, r, j, w);
     if (j % lanes == 0) {
       const int g = j / lanes;
       reinterpret_cast<__half*>(tile + kW4Codes)[g * kW4Rows + w4_place(r)] = hs;
@@ -128,8 +142,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_codes4_kernel(const uint8_t
     for (int q = 0; q < 8; ++q) over |= c[q] & 0xf0f0f0f0u;
 #pragma unroll
     for (int e = 0; e < 32; ++e) w[e / 8] |= (c[e / 4] >> (8 * (e % 4)) & 15u) << w4_shift(e % 8);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t*>(tile + w4_piece(r, q) + 4 * j) = w[q];
+    put_pieces(tile, r, j, w);
     if (j % lanes == 0) {
       const int g = j / lanes;
       const size_t at = (size_t)n * p.groups + (kt * kW4Cols + g * p.group) / p.group;
@@ -142,20 +155,23 @@ __global__ void __launch_bounds__(kPackThreads) pack_codes4_kernel(const uint8_t
   }
 }
 
-// A thread writes 4 values, half of a word: a warp writes a row's part of the tile.
+// A warp writes a row's part of the tile, 4 values a lane.
 __global__ void __launch_bounds__(kPackThreads) unpack4_kernel(const uint8_t* __restrict__ w4, float* __restrict__ W, W4Shape p) {
   const int nt = blockIdx.x / p.k_tiles, kt = blockIdx.x % p.k_tiles;
   const uint8_t* tile = w4 + (size_t)blockIdx.x * p.tile_bytes;
-  const int per = kW4Cols / p.group;
-  for (int i = threadIdx.x; i < kW4Rows * 32; i += kPackThreads) {
-    const int r = i / 32, c = 4 * (i % 32), n = nt * kW4Rows + r, k = kt * kW4Cols + c;
-    if (n >= p.N || k >= p.K) continue;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + w4_piece(r, c % 32 / 8) + c / 32 * 4)) >> w4_shift(c % 8);
-    const int g = c / p.group;
-    const float s = __half2float(reinterpret_cast<const __half*>(tile + kW4Codes)[g * kW4Rows + w4_place(r)]);
-    const int z = tile[kW4Codes + per * kW4Rows * 2 + g * kW4Rows + w4_place(r)];
+  const int per = kW4Cols / p.group, c = 4 * (threadIdx.x % 32), g = c / p.group, k = kt * kW4Cols + c;
+  const __half* scales = reinterpret_cast<const __half*>(tile + kW4Codes) + g * kW4Rows;
+  const uint8_t* zeros = tile + kW4Codes + per * kW4Rows * 2 + g * kW4Rows;
+  float* to = W + (size_t)nt * kW4Rows * p.K + k;
+  const int rows = min(kW4Rows, p.N - nt * kW4Rows);
+  if (k >= p.K) return;
+#pragma unroll 8
+  for (int r = threadIdx.x / 32; r < rows; r += kPackThreads / 32) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + w4_piece(r, c % 32 / 8) + c / 32 * 4)) >> (c % 8 ? w4_shift(4) : 0);
+    const float s = __half2float(__ldg(scales + w4_place(r)));
+    const int z = __ldg(zeros + w4_place(r));
     auto value = [&](int e) { return s * (float)((int)(w >> w4_shift(e) & 15u) - z); };
-    *reinterpret_cast<float4*>(W + (size_t)n * p.K + k) = make_float4(value(0), value(1), value(2), value(3));
+    __stcs(reinterpret_cast<float4*>(to + (size_t)r * p.K), make_float4(value(0), value(1), value(2), value(3)));
   }
 }
 
