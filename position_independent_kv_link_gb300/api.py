@@ -99,6 +99,10 @@ class LinkResult:
         self.logits = logits          # [n_reqs or sum Lq, vocab] fp32 (device)
         self.requests = requests      # request handles
 
+    def logprobs(self, tokens: Optional[torch.Tensor] = None, top: int = 0, stream=None) -> "TokenLogprobs":
+        """token_logprobs of the logits: how likely the given next tokens are, and the likeliest ones."""
+        return token_logprobs(self.logits, tokens, top, stream=stream)
+
 
 class DecodeResult:
     def __init__(self, hidden, logits, positions, slots):
@@ -106,6 +110,8 @@ class DecodeResult:
         self.logits = logits          # [n, vocab] fp32 (device)
         self.positions = positions    # int32 [n]: absolute position of each new token
         self.slots = slots            # int32 [n]: block_id * 16 + row of each new token
+
+    logprobs = LinkResult.logprobs
 
 
 class PicStore:
@@ -738,7 +744,7 @@ def gemm_w4(w: Weight4, X: torch.Tensor, x_scales: Optional[torch.Tensor] = None
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", _F32, (T, N), idx)
-    _call(idx, stream, L.load().pic_op_gemm_w4, _CODE[t], wp, X.data_ptr(), X.stride(0) if T > 1 else max(X.stride(0), K),
+    _call(idx, stream, L.load().pic_op_gemm_w4, _CODE[t], wp, X.data_ptr(), X.stride(0) if T > 1 else K,
           None if x_scales is None else _ptr(x_scales, "x_scales", _F32, (T, -(-K // _XGROUP)), idx), op, N, K, _int(T, "rows"),
           w.group)
     return out
@@ -749,7 +755,7 @@ def _rows(x: torch.Tensor, what: str, d: int, idx: int):
     if x.dim() != 2 or x.dtype is not _F32 or x.size(1) != d or x.stride(1) != 1 or x.get_device() != idx:
         raise ValueError(f"{what}: fp32 rows of {d} values on cuda:{idx} are needed, got {x.dtype} {list(x.shape)} "
                          f"(strides {list(x.stride())}) on {x.device}")
-    return x.data_ptr(), x.stride(0) if x.size(0) > 1 else max(x.stride(0), d)
+    return x.data_ptr(), x.stride(0) if x.size(0) > 1 else d
 
 
 def add_rms_norm(h: torch.Tensor, gain: Optional[torch.Tensor] = None, delta: Optional[torch.Tensor] = None,
@@ -767,9 +773,9 @@ def add_rms_norm(h: torch.Tensor, gain: Optional[torch.Tensor] = None, delta: Op
         raise ValueError(f"delta has {delta.size(0)} rows, h {T}")
     if out is not None:
         dtype = out.dtype
-    code = _CODE.get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}")
+    code = _CODE.get(dtype, L.PIC_BF16)
+    if code == L.PIC_BF16:
+        raise ValueError(f"dtype: fp32, fp16 or float8_e4m3fn, got {dtype}")
     if out is None:
         out = _empty(stream, (T, d), dtype, h.device)
         op = out.data_ptr()
@@ -816,16 +822,22 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
     if top < 0 or top > min(32, V):
         raise ValueError(f"top: 0 to 32 and at most the vocabulary, got {top}")
     if out is None:
-        # one buffer for all: [T], [T], [T * top] each
-        buf = _empty(stream, 2 * T + 2 * T * top, _F32, logits.device)
-        p = buf.split_with_sizes([T, T, T * top, T * top])
-        out = TokenLogprobs(None if tokens is None else p[0], p[1], None if top == 0 else p[2].view(_I32).view(T, top),
-                            None if top == 0 else p[3].view(T, top))
-    given = [None if x is None else _ptr(x, what, t, shape, idx) for x, what, t, shape in (
-        (out.logprob, "out.logprob", _F32, (T,)), (out.entropy, "out.entropy", _F32, (T,)),
-        (out.top_ids, "out.top_ids", _I32, (T, top)), (out.top_logprobs, "out.top_logprobs", _F32, (T, top)))]
+        lp = None if tokens is None else _empty(stream, (T,), _F32, logits.device)
+        ent = _empty(stream, (T,), _F32, logits.device)
+        ids = tops = None
+        if top:
+            ids, tops = _empty(stream, (T, top), _I32, logits.device), _empty(stream, (T, top), _F32, logits.device)
+        out = TokenLogprobs(lp, ent, ids, tops)
+        given = (None if lp is None else lp.data_ptr(), ent.data_ptr(), None if ids is None else ids.data_ptr(),
+                 None if tops is None else tops.data_ptr())
+    else:
+        lp, ent, ids, tops = out.logprob, out.entropy, out.top_ids, out.top_logprobs
+        given = (None if lp is None else _ptr(lp, "out.logprob", _F32, (T,), idx),
+                 None if ent is None else _ptr(ent, "out.entropy", _F32, (T,), idx),
+                 None if ids is None else _ptr(ids, "out.top_ids", _I32, (T, top), idx),
+                 None if tops is None else _ptr(tops, "out.top_logprobs", _F32, (T, top), idx))
     _call(idx, stream, L.load().pic_op_token_logprobs, code, _int(T, "rows"), _int(V, "vocab"), logits.data_ptr(),
-          logits.stride(0) if T > 1 else max(logits.stride(0), V),
+          logits.stride(0) if T > 1 else V,
           None if tokens is None else _ptr(tokens, "tokens", _I32, (T,), idx), top, *given)
     return out
 

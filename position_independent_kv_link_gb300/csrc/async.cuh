@@ -1,5 +1,7 @@
 // Barriers in shared memory with bounded waits, bulk copies and the cluster's barrier, for the kernels of the decode-step calls.
 #pragma once
+#include <atomic>
+
 #include "batch_internal.cuh"
 
 namespace pic {
@@ -69,5 +71,31 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// ------------------------------------------------------------------ host
+constexpr int kKnownDevices = 64;
+
+inline int device_sms(int dev) {   // asked for once per device
+  static std::atomic<int> sms[kKnownDevices];
+  const bool known = dev >= 0 && dev < kKnownDevices;
+  int n = known ? sms[dev].load() : 0;
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (known) sms[dev].store(n);
+  return n;
+}
+
+// The dynamic shared memory that a kernel may have, set once per device.
+template <auto kernel>
+struct SharedMemory {
+  std::atomic<bool> set[kKnownDevices] = {};
+  cudaError_t allow(int dev, int bytes) {
+    const bool known = dev >= 0 && dev < kKnownDevices;
+    if (known && set[dev].load()) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) set[dev].store(true);
+    return e;
+  }
+};
 
 }  // namespace pic

@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
 }
 
 template <typename T>
-pic_status launch_logprob(const LogprobArgs& a, int rows, int slots, cudaStream_t st) {
+pic_status launch_logprob(const LogprobArgs& a, int rows, int slots, int dev, cudaStream_t st) {
   // CTAs of a row: the fewest turns of all CTAs over their chunks, each with its start and end (as long as three chunks)
   const int64_t chunks = std::max<int64_t>(1, ((int64_t)a.V * sizeof(T) + kLpChunk - 1) / kLpChunk);
   int ctas = 1;
@@ -576,7 +576,8 @@ pic_status launch_logprob(const LogprobArgs& a, int rows, int slots, cudaStream_
     const int64_t cost = ((int64_t)rows * c + slots - 1) / slots * ((chunks + c - 1) / c + 3);
     if (cost < least) least = cost, ctas = c;
   }
-  PIC_CUDA(cudaFuncSetAttribute(logprob_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpStages * kLpChunk));
+  static SharedMemory<logprob_kernel<T>> memory;
+  PIC_CUDA(memory.allow(dev, kLpStages * kLpChunk));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)rows * ctas);
   cfg.blockDim = dim3(kLpThreads + 32);
@@ -626,9 +627,9 @@ pic_status pic_op_add_rms_norm(int32_t out_dtype, int32_t T, int32_t d, float* h
   AddNormArgs a{d / 4, h, delta, gain, h_stride, delta_stride, 1.f / d, eps, y, scales, groups, nullptr};
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
-  int dev = 0, sms = 0;
+  int dev = 0;
   PIC_CUDA(cudaGetDevice(&dev));
-  PIC_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const int sms = device_sms(dev);
   cudaStream_t st = (cudaStream_t)stream;
   if (e4m3) launch_add_norm<PIC_E4M3>(a, T, sms, st);
   else if (out_dtype == PIC_F16) launch_add_norm<PIC_F16>(a, T, sms, st);
@@ -663,13 +664,13 @@ pic_status pic_op_token_logprobs(int32_t dtype, int32_t T, int32_t vocab, const 
   LogprobArgs a{vocab, top, logits, logits_stride, tokens, logprob, entropy, top_ids, top_logprobs, nullptr};
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
-  int dev = 0, sms = 0;
+  int dev = 0;
   PIC_CUDA(cudaGetDevice(&dev));
-  PIC_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  const int sms = device_sms(dev);
   cudaStream_t st = (cudaStream_t)stream;
-  return dtype == PIC_F32   ? launch_logprob<float>(a, T, kLpCtas * sms, st)
-         : dtype == PIC_F16 ? launch_logprob<__half>(a, T, kLpCtas * sms, st)
-                            : launch_logprob<__nv_bfloat16>(a, T, kLpCtas * sms, st);
+  return dtype == PIC_F32   ? launch_logprob<float>(a, T, kLpCtas * sms, dev, st)
+         : dtype == PIC_F16 ? launch_logprob<__half>(a, T, kLpCtas * sms, dev, st)
+                            : launch_logprob<__nv_bfloat16>(a, T, kLpCtas * sms, dev, st);
 }
 
 }  // extern "C"

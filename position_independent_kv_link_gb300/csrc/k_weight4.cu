@@ -887,9 +887,10 @@ int gemm4_split(int bands, int blocks, int slots, int sms) {
   return best;
 }
 
-template <typename K>
-pic_status launch_gemm4(K kernel, const Gemm4Args& a, bool e4m3, int rows, int tiles, int threads, int per_sm, int ring, int sms,
+template <auto kernel>
+pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int threads, int per_sm, int ring, int dev,
                         cudaStream_t st) {
+  const int sms = device_sms(dev);
   Gemm4Plan p;
   p.x_bytes = rows * kW4Cols * (e4m3 ? 1 : 2);
   p.stages = std::min(kMaxStages, ring / (p.x_bytes + tiles * a.w.tile_bytes));
@@ -905,7 +906,8 @@ pic_status launch_gemm4(K kernel, const Gemm4Args& a, bool e4m3, int rows, int t
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return fail(PIC_ERR_CUDA, "4-bit gemm: cuTensorMapEncodeTiled failed");
   const size_t smem = 1024 + (size_t)p.stages * (p.x_bytes + tiles * a.w.tile_bytes);
-  PIC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  static SharedMemory<kernel> memory;
+  PIC_CUDA(memory.allow(dev, 1024 + ring));
   const int split = gemm4_split(p.bands, a.w.k_tiles, per_sm * sms, sms);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(split > 1 ? (unsigned)p.bands * split : (unsigned)std::min(p.bands, per_sm * sms));
@@ -924,33 +926,24 @@ pic_status launch_gemm4(K kernel, const Gemm4Args& a, bool e4m3, int rows, int t
 }
 
 template <bool E4M3, int NT>
-pic_status launch_gemm4_rows(const Gemm4Args& a, int sms, cudaStream_t st) {
+pic_status launch_gemm4_rows(const Gemm4Args& a, int dev, cudaStream_t st) {
   constexpr int kCtas = RowsShape<E4M3, NT>::kCtas;
-  return launch_gemm4(gemm4_rows_kernel<E4M3, NT>, a, E4M3, NT, 1, kRowsThreads, kCtas, (kCtas == 4 ? 54 : kCtas == 3 ? 73 : 111) * 1024,
-                      sms, st);
+  return launch_gemm4<gemm4_rows_kernel<E4M3, NT>>(a, E4M3, NT, 1, kRowsThreads, kCtas,
+                                                   (kCtas == 4 ? 54 : kCtas == 3 ? 73 : 111) * 1024, dev, st);
 }
 
 template <bool E4M3, int NT>
-pic_status launch_gemm4_tc(const Gemm4Args& a, int sms, cudaStream_t st) {
-  return launch_gemm4(gemm4_tc_kernel<E4M3, NT>, a, E4M3, NT, kTcTiles, kTcThreads<NT>, 1, 222 * 1024, sms, st);
+pic_status launch_gemm4_tc(const Gemm4Args& a, int dev, cudaStream_t st) {
+  return launch_gemm4<gemm4_tc_kernel<E4M3, NT>>(a, E4M3, NT, kTcTiles, kTcThreads<NT>, 1, 222 * 1024, dev, st);
 }
 
 template <bool E4M3>
-pic_status launch_gemm4(const Gemm4Args& a, int sms, cudaStream_t st) {
+pic_status launch_gemm4(const Gemm4Args& a, int dev, cudaStream_t st) {
   // tcgen05 (us, LM head of 128256 x 4096): 32 rows 92 for 109, 64 rows 114 for 216; 16 rows 92 for 73. With few blocks its wide bands
   // leave SMs idle: 6144 x 4096, 64 rows 30 for 18.5.
   if (a.T > kFewRows && (int64_t)a.w.n_tiles * a.w.k_tiles >= kTcBlocks)
-    return a.T <= 32 ? launch_gemm4_tc<E4M3, 32>(a, sms, st) : launch_gemm4_tc<E4M3, 64>(a, sms, st);
-  return a.T <= 8 ? launch_gemm4_rows<E4M3, 8>(a, sms, st) : a.T <= 16 ? launch_gemm4_rows<E4M3, 16>(a, sms, st) : launch_gemm4_rows<E4M3, 32>(a, sms, st);
-}
-
-int sms_of(int dev) {
-  static std::atomic<int> sms[64];
-  if (dev >= 0 && dev < 64 && sms[dev].load()) return sms[dev].load();
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-  if (dev >= 0 && dev < 64) sms[dev].store(n);
-  return n;
+    return a.T <= 32 ? launch_gemm4_tc<E4M3, 32>(a, dev, st) : launch_gemm4_tc<E4M3, 64>(a, dev, st);
+  return a.T <= 8 ? launch_gemm4_rows<E4M3, 8>(a, dev, st) : a.T <= 16 ? launch_gemm4_rows<E4M3, 16>(a, dev, st) : launch_gemm4_rows<E4M3, 32>(a, dev, st);
 }
 
 constexpr int kMaxRows = 1 << 20;   // of X
@@ -1047,7 +1040,7 @@ pic_status pic_op_gemm_w4(int32_t x_dtype, const void* W4, const void* X, int64_
   Gemm4Args a{s, (const uint8_t*)W4, X, x_stride, x_scales, Y, T, group == 32 ? 0 : group == 64 ? 1 : 2, nullptr};
   pic_status e = batch_flag_address(&a.flag);
   if (e != PIC_OK) return e;
-  return e4m3 ? launch_gemm4<true>(a, sms_of(dev), (cudaStream_t)stream) : launch_gemm4<false>(a, sms_of(dev), (cudaStream_t)stream);
+  return e4m3 ? launch_gemm4<true>(a, dev, (cudaStream_t)stream) : launch_gemm4<false>(a, dev, (cudaStream_t)stream);
 }
 
 }  // extern "C"
