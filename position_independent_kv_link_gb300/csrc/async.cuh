@@ -54,8 +54,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return mbar_try(bar, parity) || mbar_try_long(bar, parity) || mbar_wait_on(bar, parity, abort, flag);
 }
 // for the whole warp: the same answer in every lane
+static __device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
+  return __all_sync(0xffffffffu, mbar_try_long(bar, parity) || mbar_wait_on(bar, parity, abort, flag));
+}
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile unsigned* abort, unsigned* flag) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, flag));
+  return __all_sync(0xffffffffu, mbar_try(bar, parity)) || warp_wait_on(bar, parity, abort, flag);
 }
 // waits on when the CTA has given up
 __device__ __forceinline__ void mbar_settle(uint32_t bar, uint32_t parity, unsigned* flag) {
@@ -95,6 +98,26 @@ struct SharedMemory {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && known) set[dev].store(true);
     return e;
+  }
+};
+
+// How many clusters of c <= 8 CTAs of a kernel the device runs at once, asked for once per device (and amount of shared memory: the
+// kernels here use about the same in every launch).
+template <auto kernel>
+struct ClusterRoom {
+  std::atomic<int> known[kKnownDevices][9] = {};
+  int clusters(int dev, int c, cudaLaunchConfig_t cfg, cudaLaunchAttribute* at, int sms) {
+    const bool keep = dev >= 0 && dev < kKnownDevices;
+    int n = keep ? known[dev][c].load() : 0;
+    if (n > 0) return n;
+    cfg.gridDim = dim3((unsigned)(c * sms));
+    at[0].val.clusterDim.x = c;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return 0;
+    }
+    if (keep) known[dev][c].store(n);
+    return n;
   }
 };
 

@@ -190,14 +190,14 @@ struct Gemm4Args {
 };
 
 // A band is 128 rows of W (256 in the tcgen05 kernel) against one tile of rows of X; its columns come in blocks of 128. With many
-// bands the CTAs take whole ones in turn, and their copies run on over the ends of bands. With few, the CTAs of a cluster share one
-// band's blocks and add their sums through each other's shared memory, in the order of their ranks. So there is no scratch, and
-// the same call gives the same bits again.
-
+// bands the CTAs take whole ones in turn, and their copies run on over the ends of bands. With few, and for what is left after the last
+// full turn, the CTAs of a cluster share one band's blocks and add their sums through each other's shared memory, in the order of
+// their ranks. So there is no scratch, and the same call gives the same bits again.
 
 struct Gemm4Plan {
   int stages, x_bytes;       // of X in a stage
   int across, bands;         // bands of one tile of X, of all
+  int whole;                 // the first ones, which CTAs take whole
 };
 
 // Shared memory by its own addresses (through pointers that were rounded up the loads become generic ones)
@@ -239,6 +239,17 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// The scales of `rows` rows of 8-bit X for one block (0 behind the last row) by the lanes of a warp; each lane's arrive follows its copies.
+__device__ __forceinline__ void x_scales_to(uint32_t dst, const float* src, int rows, int k_tiles, int nt, int lane, uint32_t bar) {
+  for (int t = lane; t < nt; t += 32)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * t), "l"(src + (size_t)(t < rows ? t : 0) * k_tiles),
+                 "r"(t < rows ? 4 : 0)
+                 : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // Low word of the descriptor of K-major rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart; the high word is fixed
 constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr & 0x3FFFFu) >> 4; }
@@ -272,11 +283,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2* v) {
         "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y), "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld(float2* v) {   // the registers are operands, so that no use moves ahead
+__device__ __forceinline__ void tmem_wait_ld16(float2* v) {   // the registers are operands, so that no use moves ahead
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0].x), "+f"(v[0].y), "+f"(v[1].x), "+f"(v[1].y), "+f"(v[2].x), "+f"(v[2].y), "+f"(v[3].x),
                  "+f"(v[3].y), "+f"(v[4].x), "+f"(v[4].y), "+f"(v[5].x), "+f"(v[5].y), "+f"(v[6].x), "+f"(v[6].y),
                  "+f"(v[7].x), "+f"(v[7].y)
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float2* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y), "=f"(v[3].x), "=f"(v[3].y)
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld8(float2* v) {   // the registers are operands, so that no use moves ahead
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0].x), "+f"(v[0].y), "+f"(v[1].x), "+f"(v[1].y), "+f"(v[2].x), "+f"(v[2].y), "+f"(v[3].x), "+f"(v[3].y)
                :
                : "memory");
 }
@@ -294,18 +316,33 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-// The sum of *at over the cluster's CTAs, in the order of their ranks.
-__device__ __forceinline__ float cluster_sum(uint32_t at, uint32_t ctas) {
-  float sum = 0.f;
-#pragma unroll 8
-  for (uint32_t c = 0; c < ctas; ++c) {
-    uint32_t there;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(c));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
-    sum += v;
+// Y[t][n] = the sum over the cluster's CTAs, in the order of their ranks, of the fp32 value at `at` + t pitch, for t = first, first +
+// step, .. < end. A value of another CTA takes most of a microsecond, so many are asked for at a time: of R rows and C CTAs.
+template <int R, int C>
+__device__ __forceinline__ void cluster_rows(uint32_t at, uint32_t pitch, uint32_t ctas, int first, int end, int step, float* y,
+                                             int N) {
+  for (int t = first; t < end; t += R * step) {
+    float sum[R] = {};
+#pragma unroll C
+    for (uint32_t c = 0; c < ctas; ++c) {
+      uint32_t there;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(c));
+      float v[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[i]) : "r"(there + min(t + i * step, end - 1) * pitch) : "memory");
+#pragma unroll
+      for (int i = 0; i < R; ++i) sum[i] += v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (t + i * step < end) y[(size_t)(t + i * step) * N] = sum[i];
   }
-  return sum;
+}
+__device__ __forceinline__ void cluster_sums(uint32_t at, uint32_t pitch, uint32_t ctas, int first, int end, int step, float* y,
+                                             int N) {
+  if (end - first <= step) cluster_rows<1, 8>(at, pitch, ctas, first, end, step, y, N);
+  else cluster_rows<4, 2>(at, pitch, ctas, first, end, step, y, N);
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {   // (a & b) | c
   uint32_t r;
@@ -332,13 +369,13 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t z0, uint32_t z1, 
   v[3] = hfma2(and_or(y, 0x00f000f0u, 0x64006400u), 0x2c002c00u, z1);
 }
 
-constexpr int kMaxStages = 12, kFewRows = 16, kTcBlocks = 4096;
+constexpr int kMaxStages = 12, kFewRows = 16, kTcBlocks = 1536;
 
-// A CTA's blocks, in the order in which all of its warps take them: a share of one band (clusters), or whole bands in turn.
+// A CTA's blocks, in the order in which all of its warps take them: whole bands in turn, then its cluster's share of one.
 struct Gemm4Walk {
   int split, rank;           // CTAs of the cluster
   int n_band, t_tile, kb;    // the block: band down W, tile of X, block of the band
-  int band, k1, bands, across, step;
+  int band, k1, k_tiles, bands, whole, across, step;
 
   __device__ __forceinline__ Gemm4Walk(const Gemm4Args& a, const Gemm4Plan& p) {
     uint32_t x, y;
@@ -347,28 +384,32 @@ struct Gemm4Walk {
     split = (int)x;
     rank = (int)y;
     across = p.across;
+    k_tiles = a.w.k_tiles;
+    bands = p.bands;
+    whole = p.whole;
     step = gridDim.x;
-    if (split > 1) {
-      band = blockIdx.x / split;
-      bands = band + 1;
-      kb = (int)((int64_t)a.w.k_tiles * rank / split);
-      k1 = (int)((int64_t)a.w.k_tiles * (rank + 1) / split);
-    } else {
-      band = blockIdx.x;
-      bands = p.bands;
-      kb = 0;
-      k1 = a.w.k_tiles;
+    enter(blockIdx.x);
+  }
+  __device__ __forceinline__ int shared_band() const { return whole + (int)blockIdx.x / split; }   // (bands and up: none)
+  __device__ __forceinline__ void enter(int b) {
+    band = b;
+    kb = 0;
+    k1 = k_tiles;
+    if (band >= whole) {
+      band = split > 1 ? shared_band() : bands;
+      kb = (int)((int64_t)k_tiles * rank / split);
+      k1 = (int)((int64_t)k_tiles * (rank + 1) / split);
     }
     n_band = band % across;
     t_tile = band / across;
   }
   __device__ __forceinline__ bool more() const { return band < bands; }
-  __device__ __forceinline__ void next() {         // kb 0 behind a band's end
-    if (++kb < k1) return;
-    kb = 0;
-    band += step;
-    n_band = band % across;
-    t_tile = band / across;
+  __device__ __forceinline__ bool next() {         // true behind the last block of a whole band
+    if (++kb < k1) return false;
+    const bool was_whole = band < whole;
+    if (was_whole) enter(band + step);
+    else band = bands;
+    return was_whole;
   }
 };
 
@@ -376,22 +417,28 @@ struct Gemm4Walk {
 //
 //   warps 0-7   thread r of a tile's four warps: the 64 bytes of codes of row r become the integers code - zero in fp16, exact, in
 //               tensor memory as the A operand (the row's lane)
-//   warps 8-15  (8-23 with 64 rows of X) thread r: the sums of row r with 32 rows of X are read back for each group of columns, multiplied
+//   warps 8-15  thread r of a tile's four warps: the sums of row r with the rows of X are read back for each group of columns, multiplied
 //               by the row's scale and added in fp32 registers. So a scale is a factor of one thread, products and sums within a group are exact integers times X,
 //               and no rounding enters but those of the fp32 sums.
-//   the last but one: one thread asks for the packed tiles (bulk copies of 8.4 to 9.5 KB) and the block of X (TMA) of each stage
-//   the last: issues the products, D[row][t] of both tiles for each group of columns, into one of two accumulators
+//   one warp: one thread asks for the packed tiles (bulk copies of 8.4 to 9.5 KB) and the block of X (TMA) of each stage
+//   the last two, one a tile: issue the products, D[row][t] for each group of columns, into one of two accumulators
 //
 // 8-bit X: the integer c = 0..15 is the e4m3 number c 2^-9 (subnormal up to 7, then the first binade with the same spacing), so the
 // codes need only be spread to bytes. The zero goes in by a second product with a row of -zero 2^-9, 8 columns of tensor
 // memory for a whole group; both are exact.
 //
-// Barriers: FULL, EMPTY of a stage: the copies have landed; the warps and the products have read it. AFULL, AEMPTY of an
-// operand buffer: the eight warps have written it; the products of the block have ended. DFULL, DEMPTY of an accumulator: the
-// products of a group have ended; the warps that add have read it. Each is waited for by every thread that could fall a phase behind.
+// Barriers: FULL, EMPTY of a stage: the copies have landed (AFULL and DFULL tell the same to those that wait for them); the warps have
+// read it, and the products, which the warps that add have waited for. For each tile by itself, so
+// that the two warps of an SM's quarter that write operands do not wait at the same time: AFULL, AEMPTY of an operand buffer: the four
+// warps have written it; the products of the block have ended. DFULL, DEMPTY of an accumulator: the products of a group have
+// ended; the warps that add have read it. Each is waited for by every thread that could fall a phase behind.
 constexpr int kTcTiles = 2;
-template <int NT>
-constexpr int kTcThreads = (8 + NT / 4 + 2) * 32;
+template <bool E4M3, int NT>
+struct TcShape {
+  static constexpr int kCols = E4M3 ? 32 : NT;         // rows of X that a warp adds
+  static constexpr int kAdd = 8 * (NT / kCols), kLoad = 8 + kAdd;   // warps that add; the one that loads, those behind it that issue
+  static constexpr int kThreads = (kLoad + 1 + kTcTiles) * 32;
+};
 constexpr int kTcA = 64, kTcTile = 256, kTcCols = 512;   // columns of tensor memory: an A buffer (two a tile), a tile, all
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -411,16 +458,18 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 
 template <bool E4M3, int NT>
-__global__ void __launch_bounds__(kTcThreads<NT>, 1)
+__global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
     gemm4_tc_kernel(const __grid_constant__ CUtensorMap map_x, const Gemm4Args a, const Gemm4Plan p) {
-  constexpr int kAdd = NT / 4, kLoad = 8 + kAdd, kIssue = kLoad + 1;   // warps that add; the two others
+  constexpr int kAdd = TcShape<E4M3, NT>::kAdd, kLoad = TcShape<E4M3, NT>::kLoad, kCols = TcShape<E4M3, NT>::kCols,
+                kChunk = E4M3 ? 8 : 16;
   static_assert(2 * kTcA + 2 * NT <= kTcTile && kTcTiles * kTcTile == kTcCols, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages][kTcTiles] tiles
-  __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_afull[2], s_aempty[2], s_dfull[2], s_dempty[2], s_done;
+  const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages][kTcTiles] tiles; [stages][NT] scales of X
+  const uint32_t ss = ws + p.stages * kTcTiles * a.w.tile_bytes;
+  __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_afull[kTcTiles][2], s_aempty[kTcTiles][2], s_dfull[kTcTiles][2],
+      s_dempty[kTcTiles][2], s_done;
   __shared__ uint32_t s_tmem;
   __shared__ unsigned s_abort;
-  __shared__ __align__(16) float s_xs[E4M3 ? kAdd : 1][32];
   volatile unsigned* abort = &s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -429,17 +478,19 @@ __global__ void __launch_bounds__(kTcThreads<NT>, 1)
 
   if (threadIdx.x == 0) {
     s_abort = 0;
+    prefetch_map(&map_x);
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(s_empty + i), kLoad + 1);
+      mbar_init(smem_u32(s_full + i), E4M3 ? 33 : 1);
+      mbar_init(smem_u32(s_empty + i), kLoad);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(s_afull + i), 8);
-      mbar_init(smem_u32(s_aempty + i), 1);
-      mbar_init(smem_u32(s_dfull + i), 1);
-      mbar_init(smem_u32(s_dempty + i), kAdd);
-    }
-    mbar_init(smem_u32(&s_done), 1);
+    for (int g = 0; g < kTcTiles; ++g)
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(s_afull[g] + i), 4);
+        mbar_init(smem_u32(s_aempty[g] + i), 1);
+        mbar_init(smem_u32(s_dfull[g] + i), 1);
+        mbar_init(smem_u32(s_dempty[g] + i), kAdd / kTcTiles);
+      }
+    mbar_init(smem_u32(&s_done), kTcTiles);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -458,65 +509,63 @@ __global__ void __launch_bounds__(kTcThreads<NT>, 1)
   };
 
   if (warp == kLoad) {
-    if (lane == 0) {
-      uint64_t pol_w, pol_x;
-      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol_w));
-      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
-      int issued = 0;
-      for (; w.more(); w.next()) {
-        if (!mbar_wait(smem_u32(s_empty + st), ph ^ 1, abort, a.flag)) break;
-        const int n0 = w.n_band * kTcTiles, tiles = min(kTcTiles, a.w.n_tiles - n0);
-        const uint32_t fb = smem_u32(s_full + st), x = xs + st * p.x_bytes;
+    // Whole warps loop and one lane issues: in a branch of one lane a product took 140 cycles to issue, a stage's copies 1100.
+    uint64_t pol_w, pol_x;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol_w));
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
+    int issued = 0;
+    for (; w.more(); w.next()) {
+      if (!warp_wait(smem_u32(s_empty + st), ph ^ 1, abort, a.flag)) break;
+      const int n0 = w.n_band * kTcTiles, tiles = min(kTcTiles, a.w.n_tiles - n0);
+      const uint32_t fb = smem_u32(s_full + st), x = xs + st * p.x_bytes;
+      if (elect()) {
         mbar_expect_tx(fb, p.x_bytes + tiles * a.w.tile_bytes);
         for (int g = 0; g < tiles; ++g)
           bulk_load(ws + (st * kTcTiles + g) * a.w.tile_bytes,
                     a.w4 + ((size_t)(n0 + g) * a.w.k_tiles + w.kb) * a.w.tile_bytes, a.w.tile_bytes, fb, pol_w);
         tma_2d(x, &map_x, w.kb * kW4Cols, w.t_tile * NT, fb, pol_x);
         if (!E4M3) tma_2d(x + NT * 128, &map_x, w.kb * kW4Cols + 64, w.t_tile * NT, fb, pol_x);
-        ++issued;
-        next_stage();
       }
-      for (int j = max(0, issued - p.stages); j < issued; ++j)   // copies under way land before the CTA ends
-        mbar_settle(smem_u32(s_full + j % p.stages), (uint32_t)((j / p.stages) & 1), a.flag);
+      __syncwarp();
+      if constexpr (E4M3) {
+        const int t0 = w.t_tile * NT;
+        x_scales_to(ss + st * NT * 4, a.x_scales + (size_t)t0 * a.w.k_tiles + w.kb, a.T - t0, a.w.k_tiles, NT, lane, fb);
+      }
+      ++issued;
+      next_stage();
     }
-  } else if (warp == kIssue) {
-    // The warp loops as a whole and one lane issues: in a branch of one lane each product took 140 cycles to issue.
+    for (int j = max(0, issued - p.stages); j < issued; ++j)   // copies under way land before the CTA ends
+      mbar_settle(smem_u32(s_full + j % p.stages), (uint32_t)((j / p.stages) & 1), a.flag);
+  } else if (warp > kLoad) {
     constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kW4Rows >> 4) << 24);
+    const int g = warp - kLoad - 1;                // tile
     uint32_t i = 0, q = 0;                         // blocks, groups so far
     bool going = true;
     for (; w.more() && going; w.next(), ++i) {
-      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag) ||
-          !warp_wait(smem_u32(s_afull + (i & 1)), (i >> 1) & 1, abort, a.flag))
-        break;
-      const uint32_t X = desc_lo(xs + st * p.x_bytes), A = tmem + (i & 1) * kTcA;
+      const uint32_t X = desc_lo(xs + st * p.x_bytes), A = tmem + g * kTcTile + (i & 1) * kTcA;
+      if (!warp_wait(smem_u32(s_afull[g] + (i & 1)), (i >> 1) & 1, abort, a.flag)) break;
       auto issue = [&](auto steps) {               // 32-column steps of a group
         constexpr int S = decltype(steps)::value;
 #pragma unroll
         for (int k = 0; k < 4 / S; ++k, ++q) {
-          going = going && warp_wait(smem_u32(s_dempty + (q & 1)), ((q >> 1) & 1) ^ 1, abort, a.flag);
+          going = going && warp_wait(smem_u32(s_dempty[g] + (q & 1)), ((q >> 1) & 1) ^ 1, abort, a.flag);
           if (!going) return;
           fence_after();
-          const uint32_t D = tmem + 2 * kTcA + (q & 1) * NT;
+          const uint32_t D = tmem + g * kTcTile + 2 * kTcA + (q & 1) * NT;
           if (elect()) {
 #pragma unroll
-            for (int g = 0; g < kTcTiles; ++g)
-#pragma unroll
-              for (int j = k * S; j < (k + 1) * S; ++j) {
-                const uint32_t d = D + g * kTcTile, f = A + g * kTcTile;
-                if constexpr (E4M3) {
-                  umma<true>(d, f + j * 8, X + j * 2, idesc, j > k * S);
-                  umma<true>(d, f + 32 + k * 8, X + j * 2, idesc, 1);
-                } else {
-                  const uint32_t at = X + ((j >> 1) * (NT * 128) + (j & 1) * 64) / 16;
-                  umma<false>(d, f + j * 16, at, idesc, j > k * S);
-                  umma<false>(d, f + j * 16 + 8, at + 2, idesc, 1);
-                }
+            for (int j = k * S; j < (k + 1) * S; ++j) {
+              if constexpr (E4M3) {
+                umma<true>(D, A + j * 8, X + j * 2, idesc, j > k * S);
+                umma<true>(D, A + 32 + k * 8, X + j * 2, idesc, 1);
+              } else {
+                const uint32_t at = X + ((j >> 1) * (NT * 128) + (j & 1) * 64) / 16;
+                umma<false>(D, A + j * 16, at, idesc, j > k * S);
+                umma<false>(D, A + j * 16 + 8, at + 2, idesc, 1);
               }
-            umma_commit(smem_u32(s_dfull + (q & 1)));
-            if (k == 4 / S - 1) {
-              umma_commit(smem_u32(s_aempty + (i & 1)));
-              umma_commit(smem_u32(s_empty + st));
             }
+            umma_commit(smem_u32(s_dfull[g] + (q & 1)));
+            if (k == 4 / S - 1) umma_commit(smem_u32(s_aempty[g] + (i & 1)));
           }
           __syncwarp();
         }
@@ -535,15 +584,14 @@ __global__ void __launch_bounds__(kTcThreads<NT>, 1)
     // (the second tile behind the last band's end: what lies in shared memory, its sums are not kept)
     const uint32_t tile = ws + g * a.w.tile_bytes, zeros = kW4Codes + per * (kW4Rows * 2) + w4_place(r);
     for (uint32_t i = 0; w.more(); w.next(), ++i) {
-      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag) ||
-          !warp_wait(smem_u32(s_aempty + (i & 1)), ((i >> 1) & 1) ^ 1, abort, a.flag))
-        break;
-      fence_after();
+      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag)) break;
       const uint32_t at = tile + st * kTcTiles * a.w.tile_bytes;
       const uint32_t A = T + (i & 1) * kTcA;
       uint4 u[4];                                  // pieces of the row
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = lds128(at + w4_piece(r, e));
+      if (!warp_wait(smem_u32(s_aempty[g] + (i & 1)), ((i >> 1) & 1) ^ 1, abort, a.flag)) break;
+      fence_after();
       uint32_t z0 = 0, z1 = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -583,69 +631,65 @@ __global__ void __launch_bounds__(kTcThreads<NT>, 1)
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(s_afull + (i & 1)));
+        mbar_arrive(smem_u32(s_afull[g] + (i & 1)));
         mbar_arrive(smem_u32(s_empty + st));
       }
       next_stage();
     }
   }
 
-  float2 acc[16];                                  // rows half .. of the tile of X, two by two
+  float2 acc[kCols / 2];                           // rows first .. of the tile of X, two by two
   const bool adds = warp >= 8 && warp < kLoad;
-  const int half = (warp - 8) / 8 * 32;
+  const int first = (warp - 8) / 8 * kCols;
   if (adds) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t) acc[t] = make_float2(0.f, 0.f);
+    for (int t = 0; t < kCols / 2; ++t) acc[t] = make_float2(0.f, 0.f);
     const int g = (warp - 8) >> 2 & 1, r = threadIdx.x & 127;
-    const uint32_t D = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * kTcTile + 2 * kTcA + half;
+    const uint32_t D = tmem + ((uint32_t)((warp & 3) * 32) << 16) + g * kTcTile + 2 * kTcA + first;
     uint32_t q = 0;                                // groups so far
     bool going = true;
     while (w.more() && going) {
-      const int t0 = w.t_tile * NT + half, n = (w.n_band * kTcTiles + g) * kW4Rows + r;
-      const float x_scale = E4M3 && t0 + lane < a.T ? __ldg(a.x_scales + (size_t)(t0 + lane) * a.w.k_tiles + w.kb) : 0.f;
-      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag)) break;
+      const int t0 = w.t_tile * NT + first;
       const uint32_t scales = ws + (st * kTcTiles + g) * a.w.tile_bytes + kW4Codes + 2 * w4_place(r);
 #pragma unroll 1
       for (int k = 0; k < per; ++k, ++q) {
-        const float s1 = lds_half(scales + 2 * k * kW4Rows);
-        const float2 s = make_float2(s1, s1);
-        if (!warp_wait(smem_u32(s_dfull + (q & 1)), (q >> 1) & 1, abort, a.flag)) {
+        if (!warp_wait(smem_u32(s_dfull[g] + (q & 1)), (q >> 1) & 1, abort, a.flag)) {
           going = false;
           break;
         }
-        if (E4M3 && k == 0) {                      // (asked for before the waits)
-          sts_f32(smem_u32(&s_xs[warp - 8][lane]), 512.f * x_scale);
-          __syncwarp();
-        }
+        const float s1 = (E4M3 ? 512.f : 1.f) * lds_half(scales + 2 * k * kW4Rows);
+        const float2 s = make_float2(s1, s1);
         fence_after();
 #pragma unroll
-        for (int c = 0; c < 32; c += 16) {
-          float2 v[8];
-          tmem_ld16(D + (q & 1) * NT + c, v);
-          tmem_wait_ld(v);
+        for (int c = 0; c < kCols; c += kChunk) {
+          float2 v[kChunk / 2], f[kChunk / 2];
+          if constexpr (E4M3) {
+            tmem_ld8(D + (q & 1) * NT + c, v);
 #pragma unroll
-          for (int t = 0; t < 8; t += 2) {
-            float2 f0 = s, f1 = s;
-            if constexpr (E4M3) {
-              const float4 x = lds_f32x4(smem_u32(&s_xs[warp - 8][c + 2 * t]));
-              f0 = mul2(s, make_float2(x.x, x.y));
-              f1 = mul2(s, make_float2(x.z, x.w));
+            for (int t = 0; t < kChunk / 2; t += 2) {
+              const float4 x = lds_f32x4(ss + (st * NT + first + c + 2 * t) * 4);
+              f[t] = mul2(s, make_float2(x.x, x.y));
+              f[t + 1] = mul2(s, make_float2(x.z, x.w));
             }
-            acc[c / 2 + t] = fma2(v[t], f0, acc[c / 2 + t]);
-            acc[c / 2 + t + 1] = fma2(v[t + 1], f1, acc[c / 2 + t + 1]);
+            tmem_wait_ld8(v);
+          } else {
+            tmem_ld16(D + (q & 1) * NT + c, v);
+            tmem_wait_ld16(v);
           }
+#pragma unroll
+          for (int t = 0; t < kChunk / 2; ++t) acc[c / 2 + t] = fma2(v[t], E4M3 ? f[t] : s, acc[c / 2 + t]);
         }
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(s_dempty + (q & 1)));
+        if (lane == 0) mbar_arrive(smem_u32(s_dempty[g] + (q & 1)));
       }
       if (lane == 0) mbar_arrive(smem_u32(s_empty + st));
       next_stage();
-      w.next();
-      if (w.kb == 0 && w.split == 1) {             // a band of this CTA's own
+      const int n = (w.n_band * kTcTiles + g) * kW4Rows + r;
+      if (w.next()) {                              // a band of this CTA's own
         float* to = a.y + (size_t)t0 * a.w.N + n;
 #pragma unroll
-        for (int t = 0; t < 32; ++t, to += a.w.N) {
+        for (int t = 0; t < kCols; ++t, to += a.w.N) {
           if (n < a.w.N && t0 + t < a.T) *to = t % 2 ? acc[t / 2].y : acc[t / 2].x;
           if (t % 2) acc[t / 2] = make_float2(0.f, 0.f);
         }
@@ -656,19 +700,19 @@ __global__ void __launch_bounds__(kTcThreads<NT>, 1)
   fence_before();
   __syncthreads();
   if (warp == kLoad) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols));
-  if (w.split == 1) return;
-  const int col = (warp - 8) / 4 % 2 * 128 + (threadIdx.x & 127);
+  const int band = w.shared_band();
+  if (w.split == 1 || band >= w.bands) return;     // (for all CTAs of the cluster)
+  const int col = threadIdx.x & 255;
   const uint32_t sums = xs + 4 * col;              // [NT][256] fp32; every stage has been read
   if (adds) {
 #pragma unroll
-    for (int t = 0; t < 32; ++t) sts_f32(sums + (half + t) * 1024, t % 2 ? acc[t / 2].y : acc[t / 2].x);
+    for (int t = 0; t < kCols; ++t) sts_f32(sums + (first + t) * 1024, t % 2 ? acc[t / 2].y : acc[t / 2].x);
   }
   cluster_sync();
-  const int band = blockIdx.x / w.split, t0 = band / p.across * NT, n = band % p.across * 256 + col;
-  if (adds && n < a.w.N) {                         // rows of X: this CTA's share, in NT / 32 turns
+  const int t0 = band / p.across * NT, n = band % p.across * 256 + col;
+  if (adds && n < a.w.N) {                         // rows of X: this CTA's share, in kAdd / 8 turns
     const int rows = min(NT, a.T - t0), end = rows * (w.rank + 1) / w.split;
-    for (int t = rows * w.rank / w.split + half / 32; t < end; t += NT / 32)
-      a.y[(size_t)(t0 + t) * a.w.N + n] = cluster_sum(sums + t * 1024, w.split);
+    cluster_sums(sums, 1024, w.split, rows * w.rank / w.split + (warp - 8) / 8, end, kAdd / 8, a.y + (size_t)t0 * a.w.N + n, a.w.N);
   }
   cluster_sync();
 }
@@ -705,7 +749,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
     gemm4_rows_kernel(const __grid_constant__ CUtensorMap map_x, const Gemm4Args a, const Gemm4Plan p) {
   constexpr int U = NT / 8;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages] tiles
+  const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages] tiles; [stages][NT] scales of X
+  const uint32_t ss = ws + p.stages * a.w.tile_bytes;
   __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
   __shared__ unsigned s_abort;
   volatile unsigned* abort = &s_abort;
@@ -714,8 +759,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
   const int per = 4 >> a.lg, last = (1 << a.lg) - 1;   // groups of a block; 32-column steps of one, less one
   if (threadIdx.x == 0) {
     s_abort = 0;
+    prefetch_map(&map_x);
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(s_full + i), E4M3 ? 33 : 1);
       mbar_init(smem_u32(s_empty + i), 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -726,26 +772,31 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
   float acc[2][U][4] = {};                         // rows g and g + 8 of two 16-row tiles, columns tok[2 u], tok[2 u + 1]
   auto tok = [&](int i) { return i / 2 * 8 + x_row<E4M3>(2 * q + i % 2); };   // rows of X that are this lane's columns
   if (warp == 4) {
-    if (lane == 0) {
-      uint64_t pol_w, pol_x;
-      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol_w));
-      asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
-      int st = 0, issued = 0;
-      uint32_t ph = 1;
-      for (; w.more(); w.next()) {
-        if (!mbar_wait(smem_u32(s_empty + st), ph, abort, a.flag)) break;
-        const uint32_t fb = smem_u32(s_full + st), x = xs + st * p.x_bytes;
+    uint64_t pol_w, pol_x;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol_w));
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol_x));
+    int st = 0, issued = 0;
+    uint32_t ph = 1;
+    for (; w.more(); w.next()) {
+      if (!warp_wait(smem_u32(s_empty + st), ph, abort, a.flag)) break;
+      const uint32_t fb = smem_u32(s_full + st), x = xs + st * p.x_bytes;
+      if (elect()) {
         mbar_expect_tx(fb, p.x_bytes + a.w.tile_bytes);
         bulk_load(ws + st * a.w.tile_bytes, a.w4 + ((size_t)w.n_band * a.w.k_tiles + w.kb) * a.w.tile_bytes,
                   a.w.tile_bytes, fb, pol_w);
         tma_2d(x, &map_x, w.kb * kW4Cols, w.t_tile * NT, fb, pol_x);
         if (!E4M3) tma_2d(x + NT * 128, &map_x, w.kb * kW4Cols + 64, w.t_tile * NT, fb, pol_x);
-        ++issued;
-        if (++st == p.stages) st = 0, ph ^= 1;
       }
-      for (int j = max(0, issued - p.stages); j < issued; ++j)   // copies under way land before the CTA ends
-        mbar_settle(smem_u32(s_full + j % p.stages), (uint32_t)((j / p.stages) & 1), a.flag);
+      __syncwarp();
+      if constexpr (E4M3) {
+        const int t0 = w.t_tile * NT;
+        x_scales_to(ss + st * NT * 4, a.x_scales + (size_t)t0 * a.w.k_tiles + w.kb, a.T - t0, a.w.k_tiles, NT, lane, fb);
+      }
+      ++issued;
+      if (++st == p.stages) st = 0, ph ^= 1;
     }
+    for (int j = max(0, issued - p.stages); j < issued; ++j)   // copies under way land before the CTA ends
+      mbar_settle(smem_u32(s_full + j % p.stages), (uint32_t)((j / p.stages) & 1), a.flag);
   } else {
     const uint32_t piece = w4_piece(row0, q);      // (rows 8 apart: 512 bytes)
     uint32_t x_at[E4M3 ? 4 : 2];                   // columns 8 q .. of a run of X's row
@@ -756,14 +807,13 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
     uint32_t ph = 0;
     while (w.more()) {
       const int t0 = w.t_tile * NT;
+      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag)) break;
+      const uint32_t xt = xs + st * p.x_bytes, tile = ws + st * a.w.tile_bytes;
       float sx[E4M3 ? 2 * U : 1];
       if constexpr (E4M3) {
 #pragma unroll
-        for (int i = 0; i < 2 * U; ++i)
-          sx[i] = t0 + tok(i) < a.T ? __ldg(a.x_scales + (size_t)(t0 + tok(i)) * a.w.k_tiles + w.kb) : 0.f;
+        for (int i = 0; i < 2 * U; ++i) sx[i] = __uint_as_float(lds32(ss + (st * NT + tok(i)) * 4));
       }
-      if (!warp_wait(smem_u32(s_full + st), ph, abort, a.flag)) break;
-      const uint32_t xt = xs + st * p.x_bytes, tile = ws + st * a.w.tile_bytes;
       const uint32_t scales = tile + kW4Codes + 2 * (warp * 32 + g * 4), zeros = tile + kW4Codes + per * (kW4Rows * 2) + warp * 32 + g * 4;
       uint4 c[4];                                  // rows g, g + 8, g + 16, g + 24 of the warp's
 #pragma unroll
@@ -822,8 +872,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
       if (lane == 0) mbar_arrive(smem_u32(s_empty + st));
       if (++st == p.stages) st = 0, ph ^= 1;
       const int n0 = w.n_band * kW4Rows + row0;
-      w.next();
-      if (w.kb == 0 && w.split == 1) {             // a band of this CTA's own
+      if (w.next()) {                              // a band of this CTA's own
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -837,7 +886,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
       }
     }
   }
-  if (w.split == 1) return;
+  const int band = w.shared_band();
+  if (w.split == 1 || band >= w.bands) return;     // (for all CTAs of the cluster)
   __syncthreads();
   constexpr int kPitch = 136;                      // rows of X 4 apart meet no bank twice
   if (warp < 4) {
@@ -850,11 +900,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
             sts_f32(xs + 4 * (tok(2 * u + (e & 1)) * kPitch + row0 + m * 16 + (e >> 1) * 8), acc[m][u][e]);   // every stage has been read
   }
   cluster_sync();
-  const int band = blockIdx.x / w.split, t0 = band / p.across * NT, n = band % p.across * kW4Rows + threadIdx.x;
+  const int t0 = band / p.across * NT, n = band % p.across * kW4Rows + threadIdx.x;
   if (warp < 4 && n < a.w.N) {
     const int rows = min(NT, a.T - t0), end = rows * (w.rank + 1) / w.split;
-    for (int t = rows * w.rank / w.split; t < end; ++t)
-      a.y[(size_t)(t0 + t) * a.w.N + n] = cluster_sum(xs + 4 * (t * kPitch + threadIdx.x), w.split);
+    cluster_sums(xs + 4 * threadIdx.x, 4 * kPitch, w.split, rows * w.rank / w.split, end, 1, a.y + (size_t)t0 * a.w.N + n, a.w.N);
   }
   cluster_sync();
 }
@@ -872,14 +921,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   return fn;
 }
 
-// CTAs of a cluster that share a band, or 1. An SM takes a block in about 0.19 us whatever runs on it, a CTA by itself in 0.3; so
-// a band is shared while that spreads the blocks better, or lets more CTAs work at once, and all clusters find room together.
-int gemm4_split(int bands, int blocks, int slots, int sms) {
+// CTAs of a cluster that share a band, or 1. An SM takes a block in about 0.19 us whatever runs on it, a CTA by itself in 0.3 (kernel of
+// few rows); so a band is shared while that spreads the blocks better, or lets more CTAs work at once, and all clusters find room
+// together: 23 clusters of 6 CTAs that fill an SM each do, a 24th waits for a whole turn (6144 x 4096, 64 rows: 29 us for 19).
+template <typename Room>
+int gemm4_split(int bands, int blocks, int slots, int sms, Room room) {
   int best = 1;
   double least = 1e30;
   for (int c = 1; c <= std::min(8, blocks); ++c) {
     const int64_t ctas = (int64_t)bands * c;
-    if (c > 1 && ctas > slots) break;
+    if (c > 1 && (ctas > slots || bands > room(c))) continue;
     const int own = (blocks + c - 1) / c;
     const double cost = std::max((double)((ctas + sms - 1) / sms) * own * 0.19, own * 0.3) + 0.1 * c;
     if (cost < least) least = cost, best = c;
@@ -893,7 +944,8 @@ pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int 
   const int sms = device_sms(dev);
   Gemm4Plan p;
   p.x_bytes = rows * kW4Cols * (e4m3 ? 1 : 2);
-  p.stages = std::min(kMaxStages, ring / (p.x_bytes + tiles * a.w.tile_bytes));
+  const int stage = p.x_bytes + tiles * a.w.tile_bytes + (e4m3 ? 4 * rows : 0);
+  p.stages = std::min(kMaxStages, ring / stage);
   p.across = (a.w.n_tiles + tiles - 1) / tiles;
   p.bands = p.across * ((a.T + rows - 1) / rows);
   const auto enc = encode_tiled();
@@ -905,22 +957,30 @@ pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int 
                   strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return fail(PIC_ERR_CUDA, "4-bit gemm: cuTensorMapEncodeTiled failed");
-  const size_t smem = 1024 + (size_t)p.stages * (p.x_bytes + tiles * a.w.tile_bytes);
+  const size_t smem = 1024 + (size_t)p.stages * stage;
   static SharedMemory<kernel> memory;
   PIC_CUDA(memory.allow(dev, 1024 + ring));
-  const int split = gemm4_split(p.bands, a.w.k_tiles, per_sm * sms, sms);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(split > 1 ? (unsigned)p.bands * split : (unsigned)std::min(p.bands, per_sm * sms));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  const int slots = per_sm * sms, rest = p.bands % slots;
+  int split = 1;
+  p.whole = p.bands;
+  if (p.bands < slots) {
+    static ClusterRoom<kernel> fits;
+    split = gemm4_split(p.bands, a.w.k_tiles, slots, sms, [&](int c) { return fits.clusters(dev, c, cfg, at, sms); });
+  } else if (rest > 0 && rest <= slots / 2 && slots % 2 == 0 && a.w.k_tiles > 1) {
+    split = 2;
+  }
+  if (split > 1) p.whole -= rest;
+  cfg.gridDim = dim3(p.bands >= slots ? (unsigned)slots : (unsigned)(p.bands * split));
+  at[0].val.clusterDim.x = split;
   PIC_CUDA(cudaLaunchKernelEx(&cfg, kernel, map, a, p));
   return PIC_OK;
 }
@@ -934,14 +994,14 @@ pic_status launch_gemm4_rows(const Gemm4Args& a, int dev, cudaStream_t st) {
 
 template <bool E4M3, int NT>
 pic_status launch_gemm4_tc(const Gemm4Args& a, int dev, cudaStream_t st) {
-  return launch_gemm4<gemm4_tc_kernel<E4M3, NT>>(a, E4M3, NT, kTcTiles, kTcThreads<NT>, 1, 222 * 1024, dev, st);
+  return launch_gemm4<gemm4_tc_kernel<E4M3, NT>>(a, E4M3, NT, kTcTiles, TcShape<E4M3, NT>::kThreads, 1, 222 * 1024, dev, st);
 }
 
 template <bool E4M3>
 pic_status launch_gemm4(const Gemm4Args& a, int dev, cudaStream_t st) {
-  // tcgen05 (us, LM head of 128256 x 4096): 32 rows 92 for 109, 64 rows 114 for 216; 16 rows 92 for 73. With few blocks its wide bands
-  // leave SMs idle: 6144 x 4096, 64 rows 30 for 18.5.
-  if (a.T > kFewRows && (int64_t)a.w.n_tiles * a.w.k_tiles >= kTcBlocks)
+  // tcgen05 (us; mma.sync): LM head of 128256 x 4096: 32 rows 76 (110), 64 rows 86 (212), but 16 rows 75 (70). 6144 x 4096 (1536 blocks):
+  // 17 rows 11 (12), 64 rows 14 (16). With fewer blocks its wide bands leave SMs idle: 4096 x 4096: 17 rows 10 (9), 64 rows 12 (13).
+  if (a.T > kFewRows && (int64_t)a.w.n_tiles * a.w.k_tiles * ((a.T + 31) / 32) >= kTcBlocks)
     return a.T <= 32 ? launch_gemm4_tc<E4M3, 32>(a, dev, st) : launch_gemm4_tc<E4M3, 64>(a, dev, st);
   return a.T <= 8 ? launch_gemm4_rows<E4M3, 8>(a, dev, st) : a.T <= 16 ? launch_gemm4_rows<E4M3, 16>(a, dev, st) : launch_gemm4_rows<E4M3, 32>(a, dev, st);
 }
