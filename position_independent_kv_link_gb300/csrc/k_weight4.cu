@@ -40,13 +40,97 @@ __device__ __forceinline__ void load32(const T* p, float* x) {   // 32 values, 1
   }
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN when one is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+constexpr float kMagic = 12582912.f;                   // 1.5 2^23: integers are the spacing there
+
 // The integer nearest to x / s (ties to even), decided exactly: x (1 / s) in fp32 gives an integer k that may be off by one next
-// to a border; x - k s is exact in fp32 (s has 11 bits, and x lies within some 20 s), as is s / 2. rs: 1 / s.
+// to a border; x - k s is exact in fp32 (s has 11 bits, and x lies within some 23 s), as is s / 2. rs: 1 / s.
 __device__ __forceinline__ int nearest_quotient(float x, float s, float rs) {
-  constexpr float kMagic = 12582912.f;                 // 1.5 2^23: integers are the spacing there
   const float t = fmaf(x, rs, kMagic), d = fmaf(kMagic - t, s, x), half = 0.5f * s;
   const int k = __float_as_int(t) - __float_as_int(kMagic);
   return k + (d > half || (d == half && (k & 1))) - (d < -half || (d == -half && (k & 1)));
+}
+
+// fp16 of fp32 of (hi - lo) / 15 in 64 bits. In fp32 the quotient is within 2^-22 of itself, so its fp16 is known unless a border lies
+// within 2^-20: only then 64 bits decide (in every group they took 110 of 117 us for 28672 x 4096: this GPU has few units for them).
+__device__ __forceinline__ __half group_scale(float lo, float hi) {
+  const float q = (hi - lo) * (1.f / 15.f);
+  const __half a = __float2half_rn(q * (1.f - 1.f / 1048576)), b = __float2half_rn(q * (1.f + 1.f / 1048576));
+  if (__half_as_ushort(a) == __half_as_ushort(b)) return a;
+  return __float2half_rn((float)(((double)hi - (double)lo) / 15.0));
+}
+
+// The codes of 32 weights, eight a word. The integer next to x rs + z is nearest_quotient(x) + z, but where x / s is within 2^-18 of a border;
+// then |x - k s| is within 2^-17 of s / 2, and the word is done again one by one, exactly (bf16 weights stand on borders often: in 4 of
+// 10 warps' 1024). So are those of scales so far below fp16's normal range that a zero beyond 15 was cut (`cut`): only there can
+// a code be below 0.
+__device__ __forceinline__ void codes32(const float* x, float s, float rs, int z, bool cut, uint32_t* w) {
+  const float m = kMagic + z, near = 0.5f * s * (1.f - 1.f / 65536);
+  const float2 rs2 = make_float2(rs, rs), m2 = make_float2(m, m), less = make_float2(-m, -m), ns = make_float2(-s, -s);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float far = 0.f;
+    uint32_t u = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 v = make_float2(x[8 * q + e], x[8 * q + e + 1]);
+      const float2 t = fma2(v, rs2, m2), d = fma2(add2(t, less), ns, v);
+      far = max3_abs(far, d.x, d.y);
+      uint32_t two = __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x5410);   // (kMagic's lower half is 0)
+      asm("min.u16x2 %0, %0, %1;" : "+r"(two) : "r"(0x000f000fu));
+      static_assert(w4_shift(1) - w4_shift(0) == 16 && w4_shift(7) - w4_shift(6) == 16, "two columns side by side stand 16 bits apart");
+      u += two << w4_shift(e);
+    }
+    if (far >= near || cut) {
+      u = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u |= (uint32_t)min(max(nearest_quotient(x[8 * q + e], s, rs) + z, 0), 15) << w4_shift(e);
+    }
+    w[q] = u;
+  }
 }
 
 // The four threads of a row hold its runs' words of each piece; they trade them for a piece each, and write 64 bytes together.
@@ -83,34 +167,27 @@ __global__ void __launch_bounds__(kPackThreads) pack4_kernel(const T* __restrict
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = 0.f;
     }
-    float lo = 0.f, hi = 0.f;
-    bool fine = true;
+    float lo = 0.f, hi = 0.f;                          // (NaN when a weight is)
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      fine = fine && x[e] == x[e];
+    for (int e = 0; e < 32; e += 2) {
+      lo = min3(lo, x[e], x[e + 1]);
+      hi = max3_nan(hi, x[e], x[e + 1]);
     }
     for (int o = 1; o < lanes; o <<= 1) {
       lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      fine = __shfl_xor_sync(0xffffffffu, fine, o) && fine;
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    // (16-bit extremes: their difference divided in fp64, rounded to fp32 and then to fp16)
-    __half hs = __float2half_rn((float)(((double)hi - (double)lo) / 15.0));
+    bool fine = hi == hi;
+    __half hs = group_scale(lo, hi);
     if (__hisinf(hs)) fine = false;                    // infinite weights too
     if (!fine) {
       batch_flag(flag, kBatchRange);
       hs = __float2half_rn(0.f);
     }
     const float s = __half2float(hs), rs = s > 0.f ? 1.f / s : 0.f;
-    const int z = s > 0.f ? min(nearest_quotient(-lo, s, rs), 15) : 0;
+    const int z0 = s > 0.f ? nearest_quotient(-lo, s, rs) : 0, z = min(z0, 15);
     uint32_t w[4] = {};
-    if (s > 0.f) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        w[e / 8] |= (uint32_t)min(max(nearest_quotient(x[e], s, rs) + z, 0), 15) << w4_shift(e % 8);
-    }
+    if (s > 0.f) codes32(x, s, rs, z, z0 > 15, w);
     put_pieces(tile, r, j, w);
     if (j % lanes == 0) {
       const int g = j / lanes;
@@ -440,22 +517,6 @@ struct TcShape {
   static constexpr int kThreads = (kLoad + 1 + kTcTiles) * 32;
 };
 constexpr int kTcA = 64, kTcTile = 256, kTcCols = 512;   // columns of tensor memory: an A buffer (two a tile), a tile, all
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-        "l"(reinterpret_cast<unsigned long long&>(c)));
-  return r;
-}
 
 template <bool E4M3, int NT>
 __global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
