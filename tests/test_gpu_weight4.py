@@ -226,6 +226,20 @@ def test_product_of_many_blocks(pkl, T, group, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,N,K,group", [(1, 89500, 256, 128), (5, 90000, 160, 32), (16, 70000, 288, 64), (128, 12000, 256, 128),
+                                         (64, 43520, 256, 128), (50, 43300, 416, 64), (20, 43001, 1120, 32), (130, 30000, 512, 32),
+                                         (190, 30000, 512, 128), (64, 39000, 128, 128), (64, 6144, 4096, 128), (33, 4200, 4096, 64)])
+def test_product_of_what_a_turn_leaves(pkl, T, N, K, group, e4m3):
+    """Somewhat more bands than CTAs that run at once (pairs share the rest; with one block in a band they cannot), and clusters that
+    need not all find room."""
+    w, *parts = weights(pkl, N, K, group)
+    x, sx = rows(T, K, e4m3)
+    y = pkl.gemm_w4(w, x, sx)
+    hold(y, *parts, group, x, sx)
+    assert torch.equal(pkl.gemm_w4(w, x, sx), y)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_product_again_and_in_place(pkl, e4m3):
     """The same bits again; out= written whole, nothing beside it; rows of X that lie apart, NaN between them."""
     T, N, K = 11, 300, 544
