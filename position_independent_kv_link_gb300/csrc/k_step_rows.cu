@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormArgs a) {
   const float4* delta = reinterpret_cast<const float4*>(a.delta + t * a.delta_stride);
   float4 x[VPT];
   float ss = 0.f;
+  pdl_enter();
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int i = threadIdx.x + v * nt;
@@ -109,17 +110,17 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormArgs a) {
 }
 
 template <int OUT>
-void launch_add_norm(const AddNormArgs& a, int T, int sms, cudaStream_t st) {
+cudaError_t launch_add_norm(const AddNormArgs& a, int T, int sms, cudaStream_t st) {
   // Few rows: as many threads as there are float4s (one row of 4096: 2.4 us). Many: 512 at most, two to eight float4s a thread (8192 rows
   // of 4096 to e4m3: 72 us; 83 with 1024 threads, 81 with 256, 92 with 128).
   const int most = T <= 2 * sms ? 1024 : 512;
   int per = 1;
   while (per < 8 && (a.d4 + per - 1) / per > most) per *= 2;
   const int nt = ((a.d4 + per - 1) / per + 31) / 32 * 32;
-  if (per == 1) add_norm_kernel<OUT, 1><<<T, nt, 0, st>>>(a);
-  else if (per == 2) add_norm_kernel<OUT, 2><<<T, nt, 0, st>>>(a);
-  else if (per == 4) add_norm_kernel<OUT, 4><<<T, nt, 0, st>>>(a);
-  else add_norm_kernel<OUT, 8><<<T, nt, 0, st>>>(a);
+  if (per == 1) return launch_dependent(add_norm_kernel<OUT, 1>, dim3(T), dim3(nt), 0, st, a);
+  if (per == 2) return launch_dependent(add_norm_kernel<OUT, 2>, dim3(T), dim3(nt), 0, st, a);
+  if (per == 4) return launch_dependent(add_norm_kernel<OUT, 4>, dim3(T), dim3(nt), 0, st, a);
+  return launch_dependent(add_norm_kernel<OUT, 8>, dim3(T), dim3(nt), 0, st, a);
 }
 
 // ------------------------------------------------------------------ log probabilities
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int t = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* row = (const T*)a.logits + t * a.stride;
+  pdl_wait();
   const int token = a.tokens ? __ldg(a.tokens + t) : 0;
   if (token < 0 || token >= a.V) {                 // the whole cluster
     if (tid == 0 && rank == 0 && token != -1) batch_flag(a.flag, kBatchBadToken);
@@ -583,13 +585,15 @@ pic_status launch_logprob(const LogprobArgs& a, int rows, int slots, int dev, cu
   cfg.blockDim = dim3(kLpThreads + 32);
   cfg.dynamicSmemBytes = kLpStages * kLpChunk;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   PIC_CUDA(cudaLaunchKernelEx(&cfg, logprob_kernel<T>, a));
   return PIC_OK;
 }
@@ -631,10 +635,9 @@ pic_status pic_op_add_rms_norm(int32_t out_dtype, int32_t T, int32_t d, float* h
   PIC_CUDA(cudaGetDevice(&dev));
   const int sms = device_sms(dev);
   cudaStream_t st = (cudaStream_t)stream;
-  if (e4m3) launch_add_norm<PIC_E4M3>(a, T, sms, st);
-  else if (out_dtype == PIC_F16) launch_add_norm<PIC_F16>(a, T, sms, st);
-  else launch_add_norm<PIC_F32>(a, T, sms, st);
-  PIC_CUDA(cudaGetLastError());
+  PIC_CUDA(e4m3                   ? launch_add_norm<PIC_E4M3>(a, T, sms, st)
+           : out_dtype == PIC_F16 ? launch_add_norm<PIC_F16>(a, T, sms, st)
+                                  : launch_add_norm<PIC_F32>(a, T, sms, st));
   return PIC_OK;
 }
 

@@ -560,6 +560,7 @@ __global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     fence_before();
   }
+  pdl_wait();
   __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem;
@@ -760,6 +761,7 @@ __global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
   __syncwarp();
   fence_before();
   __syncthreads();
+  pdl_leave();
   if (warp == kLoad) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols));
   const int band = w.shared_band();
   if (w.split == 1 || band >= w.bands) return;     // (for all CTAs of the cluster)
@@ -828,6 +830,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  pdl_wait();
   __syncthreads();
 
   float acc[2][U][4] = {};                         // rows g and g + 8 of two 16-row tiles, columns tok[2 u], tok[2 u + 1]
@@ -950,6 +953,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
   const int band = w.shared_band();
   if (w.split == 1 || band >= w.bands) return;     // (for all CTAs of the cluster)
   __syncthreads();
+  pdl_leave();
   constexpr int kPitch = 136;                      // rows of X 4 apart meet no bank twice
   if (warp < 4) {
 #pragma unroll
@@ -1025,11 +1029,13 @@ pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int 
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const int slots = per_sm * sms, rest = p.bands % slots;
   int split = 1;
   p.whole = p.bands;
