@@ -21,7 +21,9 @@ namespace {
 // ------------------------------------------------------------------ packing
 //
 // One CTA packs a tile; a thread holds 32 columns of a row (16 bytes of codes), the four threads of a row's 128 columns lie
-// side by side, so that the extremes of a group of 64 or 128 are shuffles away.
+// side by side, so that the extremes of a group of 64 or 128 are shuffles away. Bound by instructions for 16-bit weights (28672 x 4096
+// bf16 in groups of 64: 77 us, 3.8 TB/s, issue slots 69 % busy; fp16 in groups of 128: 69 us), by HBM for fp32 (109 us, 4.8 TB/s).
+// Unpacking writes 8 bytes for every one that it reads: 98 us, 5.4 TB/s, 80 % of a copy.
 constexpr int kPackThreads = 256;
 
 template <typename T>
@@ -266,6 +268,11 @@ struct Gemm4Args {
   unsigned* flag;
 };
 
+// Sums of (code - zero) x, exact products of integers below 16 with fp16 (or e4m3) numbers in fp32, times the group's scale in fp32. The
+// weights' 4 bits are the bytes that count: HBM would allow 0.19 us for a 128 x 128 block a SM. Turning codes into operands costs more: 9
+// instructions for 8 codes, and both kernels stand at about twice that time (LM head of 128256 x 4096: 1 row 55 us, 16 rows 70, 64 rows
+// 83 (fp16) and 101 (e4m3); floors 41, 42, 45). 4096 x 14336: 1 row 12 us, 64 rows 20; floor 4.5 to 5.
+//
 // A band is 128 rows of W (256 in the tcgen05 kernel) against one tile of rows of X; its columns come in blocks of 128. With many
 // bands the CTAs take whole ones in turn, and their copies run on over the ends of bands. With few, and for what is left after the last
 // full turn, the CTAs of a cluster share one band's blocks and add their sums through each other's shared memory, in the order of
@@ -500,15 +507,19 @@ struct Gemm4Walk {
 //   one warp: one thread asks for the packed tiles (bulk copies of 8.4 to 9.5 KB) and the block of X (TMA) of each stage
 //   the last two, one a tile: issue the products, D[row][t] for each group of columns, into one of two accumulators
 //
+// What a warp does besides its arithmetic decides the time (waits, arrivals, the loop): with one issuing warp and 16 that add the issue slots
+// were 73 % busy (64 fp16 rows of 128256 x 4096: 114 us); with an issuing warp a tile, 8 that add and no wait that another implies it is
+// 83. 8-bit X needs a factor for each row and block: 32 rows of X a warp and 16 warps (101 us), as 64 spill (181).
+//
 // 8-bit X: the integer c = 0..15 is the e4m3 number c 2^-9 (subnormal up to 7, then the first binade with the same spacing), so the
 // codes need only be spread to bytes. The zero goes in by a second product with a row of -zero 2^-9, 8 columns of tensor
 // memory for a whole group; both are exact.
 //
 // Barriers: FULL, EMPTY of a stage: the copies have landed (AFULL and DFULL tell the same to those that wait for them); the warps have
-// read it, and the products, which the warps that add have waited for. For each tile by itself, so
-// that the two warps of an SM's quarter that write operands do not wait at the same time: AFULL, AEMPTY of an operand buffer: the four
-// warps have written it; the products of the block have ended. DFULL, DEMPTY of an accumulator: the products of a group have
-// ended; the warps that add have read it. Each is waited for by every thread that could fall a phase behind.
+// read it, and the products, which the warps that add have waited for. For each tile by itself, so that the two warps of an SM's
+// quarter that write operands do not wait at the same time: AFULL, AEMPTY of an operand buffer: the four warps have written it; the
+// products of the block have ended. DFULL, DEMPTY of an accumulator: the products of a group have ended; the warps that add have read
+// it. Each is waited for by every thread that could fall a phase behind.
 constexpr int kTcTiles = 2;
 template <bool E4M3, int NT>
 struct TcShape {
@@ -784,6 +795,8 @@ __global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
 // the four warps; warp 4 asks for the copies. The codes become the integers code - zero in fp16, 8-bit X becomes fp16, both
 // exact. A lane's weights of two products are one word of codes for each row, its part of X the columns 8 q .. 8 q + 7 of a 32-column
 // run, which stand where the products want 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q (the sum over columns does not mind).
+// Bound by the logic pipe, which turns codes into operands: 16 rows of W a warp and twice as many warps are slower (one row of
+// 128256 x 4096: 65 us for 55; 16 rows of 28672 x 4096: 22 for 20), as the loop's own instructions then serve half as many codes.
 constexpr int kRowsThreads = 160;
 
 // Row of an 8-row tile of X that lane group g reads, and the column of a product that is its: rows that one access of
