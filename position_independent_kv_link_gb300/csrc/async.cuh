@@ -75,9 +75,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The two halves of pdl_enter (pic_internal.h): the next kernel's CTAs come once all of this one's have called pdl_leave or have ended. A
-// kernel whose CTAs share out the work of SMs lets them come when its own is done: CTAs that come while it runs take the places that
-// happen to be free, and then share unevenly (4-bit gemm, one row of 128256 x 4096: 62 us for 55).
+// The two halves of pdl_enter (pic_internal.h): the next kernel's CTAs come once all of this one's have called pdl_leave or have ended.
+// CTAs that come while others still work take the places that happen to be free, and then share their own work out unevenly (4-bit
+// gemm, one row of 128256 x 4096 again and again: 62 us for 55), so that long kernels call it late or not at all.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_leave() { asm volatile("griddepcontrol.launch_dependents;"); }
 

@@ -271,7 +271,7 @@ struct Gemm4Args {
 // Sums of (code - zero) x, exact products of integers below 16 with fp16 (or e4m3) numbers in fp32, times the group's scale in fp32. The
 // weights' 4 bits are the bytes that count: HBM would allow 0.19 us for a 128 x 128 block a SM. Turning codes into operands costs more: 9
 // instructions for 8 codes, and both kernels stand at about twice that time (LM head of 128256 x 4096: 1 row 55 us, 16 rows 70, 64 rows
-// 83 (fp16) and 101 (e4m3); floors 41, 42, 45). 4096 x 14336: 1 row 12 us, 64 rows 20; floor 4.5 to 5.
+// 83 (fp16) and 101 (e4m3); floors 41, 42, 45). 4096 x 14336: 1 row 12 us, 16 rows 14, 64 rows 20; floor 4.5 to 5.
 //
 // A band is 128 rows of W (256 in the tcgen05 kernel) against one tile of rows of X; its columns come in blocks of 128. With many
 // bands the CTAs take whole ones in turn, and their copies run on over the ends of bands. With few, and for what is left after the last
@@ -795,6 +795,8 @@ __global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
 // the four warps; warp 4 asks for the copies. The codes become the integers code - zero in fp16, 8-bit X becomes fp16, both
 // exact. A lane's weights of two products are one word of codes for each row, its part of X the columns 8 q .. 8 q + 7 of a 32-column
 // run, which stand where the products want 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q (the sum over columns does not mind).
+// Where a cluster shares a band, each CTA puts its sums of a row of X into the shared memory of the CTA that the row belongs to, while others
+// may still work (16 rows of 4096 x 4096: 7.0 us; 8.8 when it read them there after a barrier, and left after another).
 // Bound by the logic pipe, which turns codes into operands: 16 rows of W a warp and twice as many warps are slower (one row of
 // 128256 x 4096: 65 us for 55; 16 rows of 28672 x 4096: 22 for 20), as the loop's own instructions then serve half as many codes.
 constexpr int kRowsThreads = 160;
@@ -826,7 +828,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
   constexpr int U = NT / 8;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t xs = (smem_u32(smem_raw) + 1023) & ~1023u, ws = xs + p.stages * p.x_bytes;   // [stages] X; [stages] tiles; [stages][NT] scales of X
-  const uint32_t ss = ws + p.stages * a.w.tile_bytes;
+  const uint32_t ss = ws + p.stages * a.w.tile_bytes, rs = ss + (E4M3 ? p.stages * NT * 4 : 0);   // rs: sums from the cluster
   __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
   __shared__ unsigned s_abort;
   volatile unsigned* abort = &s_abort;
@@ -846,6 +848,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
   pdl_wait();
   __syncthreads();
 
+  if (w.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");
   float acc[2][U][4] = {};                         // rows g and g + 8 of two 16-row tiles, columns tok[2 u], tok[2 u + 1]
   auto tok = [&](int i) { return i / 2 * 8 + x_row<E4M3>(2 * q + i % 2); };   // rows of X that are this lane's columns
   if (warp == 4) {
@@ -963,27 +966,53 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<E4M3, NT>::kCtas)
       }
     }
   }
+  if (w.split == 1) return;
   const int band = w.shared_band();
-  if (w.split == 1 || band >= w.bands) return;     // (for all CTAs of the cluster)
-  __syncthreads();
-  pdl_leave();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // all CTAs' shared memory is there
+  if (band >= w.bands) return;                     // (for all CTAs of the cluster)
+  // Each row of X belongs to one CTA, which gets the others' sums for it, [CTA][its rows][128], put side by side here first
+  const int t0 = band / p.across * NT, rows = min(NT, a.T - t0), most = (rows + w.split - 1) / w.split;
   constexpr int kPitch = 136;                      // rows of X 4 apart meet no bank twice
+  __syncthreads();                                 // every stage has been read
   if (warp < 4) {
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) 
-            sts_f32(xs + 4 * (tok(2 * u + (e & 1)) * kPitch + row0 + m * 16 + (e >> 1) * 8), acc[m][u][e]);   // every stage has been read
+        for (int e = 0; e < 4; ++e) sts_f32(xs + 4 * (tok(2 * u + (e & 1)) * kPitch + row0 + m * 16 + (e >> 1) * 8), acc[m][u][e]);
+    __syncwarp();
+    for (int i = lane; i < rows * 8; i += 32) {    // four of the warp's 32 weight rows
+      const int t = i / 8, at = warp * 32 + i % 8 * 4;
+      const int owner = (w.split * (t + 1) + rows - 1) / rows - 1, slot = w.rank * most + t - rows * owner / w.split;
+      const float4 v = lds_f32x4(xs + 4 * (t * kPitch + at));
+      uint32_t there;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(rs + (slot * kW4Rows + at) * 4), "r"(owner));
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(there), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+    }
   }
   cluster_sync();
-  const int t0 = band / p.across * NT, n = band % p.across * kW4Rows + threadIdx.x;
+  const int n = band % p.across * kW4Rows + threadIdx.x;
   if (warp < 4 && n < a.w.N) {
-    const int rows = min(NT, a.T - t0), end = rows * (w.rank + 1) / w.split;
-    cluster_sums(xs + 4 * threadIdx.x, 4 * kPitch, w.split, rows * w.rank / w.split, end, 1, a.y + (size_t)t0 * a.w.N + n, a.w.N);
+    const int first = rows * w.rank / w.split, own = rows * (w.rank + 1) / w.split - first;
+    float* to = a.y + (size_t)(t0 + first) * a.w.N + n;
+    auto sums = [&](auto wide, auto ctas) {        // so many rows, and CTAs, at a time
+      constexpr int R = decltype(wide)::value, C = decltype(ctas)::value;
+      for (int t = 0; t < own; t += R) {
+        float sum[R] = {};
+#pragma unroll C
+        for (int c = 0; c < w.split; ++c)
+#pragma unroll
+          for (int i = 0; i < R; ++i)
+            sum[i] += __uint_as_float(lds32(rs + ((c * most + min(t + i, own - 1)) * kW4Rows + threadIdx.x) * 4));
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (t + i < own) to[(size_t)(t + i) * a.w.N] = sum[i];
+      }
+    };
+    if (own == 1) sums(std::integral_constant<int, 1>(), std::integral_constant<int, 8>());
+    else sums(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
   }
-  cluster_sync();
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
@@ -1023,7 +1052,6 @@ pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int 
   Gemm4Plan p;
   p.x_bytes = rows * kW4Cols * (e4m3 ? 1 : 2);
   const int stage = p.x_bytes + tiles * a.w.tile_bytes + (e4m3 ? 4 * rows : 0);
-  p.stages = std::min(kMaxStages, ring / stage);
   p.across = (a.w.n_tiles + tiles - 1) / tiles;
   p.bands = p.across * ((a.T + rows - 1) / rows);
   const auto enc = encode_tiled();
@@ -1035,12 +1063,11 @@ pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int 
                   strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return fail(PIC_ERR_CUDA, "4-bit gemm: cuTensorMapEncodeTiled failed");
-  const size_t smem = 1024 + (size_t)p.stages * stage;
   static SharedMemory<kernel> memory;
   PIC_CUDA(memory.allow(dev, 1024 + ring));
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = 1024 + ring;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1059,6 +1086,9 @@ pic_status launch_gemm4(const Gemm4Args& a, bool e4m3, int rows, int tiles, int 
     split = 2;
   }
   if (split > 1) p.whole -= rest;
+  const int t_most = std::min(rows, a.T), recv = split > 1 && tiles == 1 ? split * ((t_most + split - 1) / split) * kW4Rows * 4 : 0;
+  p.stages = std::min(kMaxStages, (ring - recv) / stage);
+  cfg.dynamicSmemBytes = 1024 + (size_t)p.stages * stage + recv;
   cfg.gridDim = dim3(p.bands >= slots ? (unsigned)slots : (unsigned)(p.bands * split));
   at[0].val.clusterDim.x = split;
   PIC_CUDA(cudaLaunchKernelEx(&cfg, kernel, map, a, p));
