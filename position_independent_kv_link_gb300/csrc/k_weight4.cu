@@ -22,22 +22,35 @@ namespace {
 //
 // One CTA packs a tile; a thread holds 32 columns of a row (16 bytes of codes), the four threads of a row's 128 columns lie
 // side by side, so that the extremes of a group of 64 or 128 are shuffles away. Bound by instructions for 16-bit weights (28672 x 4096
-// bf16 in groups of 64: 77 us, 3.8 TB/s, issue slots 69 % busy; fp16 in groups of 128: 69 us), by HBM for fp32 (109 us, 4.8 TB/s).
-// Unpacking writes 8 bytes for every one that it reads: 98 us, 5.4 TB/s, 80 % of a copy.
+// bf16 in groups of 64: 77 us, 3.8 TB/s, issue slots 69 % busy; fp16 in groups of 128: 69 us), by HBM for fp32 (89 us, 6.0 TB/s).
+// Unpacking writes 8 bytes for every one that it reads: 84 us, 6.3 TB/s, 93 % of a copy (98 us in pieces of 16 bytes a lane instead of 32).
 constexpr int kPackThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ void load32(const T* p, float* x) {   // 32 values, 16-byte aligned
-  constexpr int E = 16 / sizeof(T);
+template <bool WIDE, typename T>
+__device__ __forceinline__ void load32(const T* p, float* x) {   // 32 values, 16-byte aligned (32 when WIDE)
+  constexpr int E = 32 / sizeof(T);
 #pragma unroll
   for (int i = 0; i < 32; i += E) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + i));
-    const T* v = reinterpret_cast<const T*>(&u);
+    uint32_t u[8];
+    if constexpr (WIDE) {
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                   : "l"(p + i));
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + i)), b = __ldg(reinterpret_cast<const uint4*>(p + i) + 1);
+      u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+    }
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      if constexpr (std::is_same<T, float>::value) x[i + j] = v[j];
-      else if constexpr (std::is_same<T, __half>::value) x[i + j] = __half2float(v[j]);
-      else x[i + j] = __bfloat162float(v[j]);
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (std::is_same<T, float>::value) {
+        x[i + j] = __uint_as_float(u[j]);
+      } else if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+        x[i + 2 * j] = f.x, x[i + 2 * j + 1] = f.y;
+      } else {
+        x[i + 2 * j] = __uint_as_float(u[j] << 16);
+        x[i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      }
     }
   }
 }
@@ -151,7 +164,7 @@ __device__ __forceinline__ void put_pieces(uint8_t* tile, int r, int j, uint32_t
   *reinterpret_cast<uint4*>(tile + w4_piece(r, j)) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T>
+template <bool WIDE, typename T>
 __global__ void __launch_bounds__(kPackThreads) pack4_kernel(const T* __restrict__ W, uint8_t* __restrict__ out, W4Shape p,
                                                              unsigned* flag) {
   const int nt = blockIdx.x / p.k_tiles, kt = blockIdx.x % p.k_tiles;
@@ -164,7 +177,7 @@ __global__ void __launch_bounds__(kPackThreads) pack4_kernel(const T* __restrict
     const int n = nt * kW4Rows + r, k = kt * kW4Cols + 32 * j;
     float x[32];
     if (n < p.N && k < p.K) {
-      load32(W + (size_t)n * p.K + k, x);
+      load32<WIDE>(W + (size_t)n * p.K + k, x);
     } else {
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = 0.f;
@@ -234,23 +247,25 @@ __global__ void __launch_bounds__(kPackThreads) pack_codes4_kernel(const uint8_t
   }
 }
 
-// A warp writes a row's part of the tile, 4 values a lane.
+// A lane holds a word of codes and writes its 8 values, a warp two rows' parts of the tile.
 __global__ void __launch_bounds__(kPackThreads) unpack4_kernel(const uint8_t* __restrict__ w4, float* __restrict__ W, W4Shape p) {
   const int nt = blockIdx.x / p.k_tiles, kt = blockIdx.x % p.k_tiles;
   const uint8_t* tile = w4 + (size_t)blockIdx.x * p.tile_bytes;
-  const int per = kW4Cols / p.group, c = 4 * (threadIdx.x % 32), g = c / p.group, k = kt * kW4Cols + c;
+  const int per = kW4Cols / p.group, c = 8 * (threadIdx.x % 16), g = c / p.group, k = kt * kW4Cols + c;
   const __half* scales = reinterpret_cast<const __half*>(tile + kW4Codes) + g * kW4Rows;
   const uint8_t* zeros = tile + kW4Codes + per * kW4Rows * 2 + g * kW4Rows;
   float* to = W + (size_t)nt * kW4Rows * p.K + k;
   const int rows = min(kW4Rows, p.N - nt * kW4Rows);
   if (k >= p.K) return;
 #pragma unroll 8
-  for (int r = threadIdx.x / 32; r < rows; r += kPackThreads / 32) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + w4_piece(r, c % 32 / 8) + c / 32 * 4)) >> (c % 8 ? w4_shift(4) : 0);
+  for (int r = threadIdx.x / 16; r < rows; r += kPackThreads / 16) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(tile + w4_piece(r, c % 32 / 8) + c / 32 * 4));
     const float s = __half2float(__ldg(scales + w4_place(r)));
     const int z = __ldg(zeros + w4_place(r));
     auto value = [&](int e) { return s * (float)((int)(w >> w4_shift(e) & 15u) - z); };
-    __stcs(reinterpret_cast<float4*>(to + (size_t)r * p.K), make_float4(value(0), value(1), value(2), value(3)));
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + (size_t)r * p.K), "f"(value(0)),
+                 "f"(value(1)), "f"(value(2)), "f"(value(3)), "f"(value(4)), "f"(value(5)), "f"(value(6)), "f"(value(7))
+                 : "memory");
   }
 }
 
@@ -1116,6 +1131,14 @@ pic_status launch_gemm4(const Gemm4Args& a, int dev, cudaStream_t st) {
   return a.T <= 8 ? launch_gemm4_rows<E4M3, 8>(a, dev, st) : a.T <= 16 ? launch_gemm4_rows<E4M3, 16>(a, dev, st) : launch_gemm4_rows<E4M3, 32>(a, dev, st);
 }
 
+template <typename T>
+void launch_pack4(const T* W, void* out, const W4Shape& s, unsigned* flag, cudaStream_t st) {
+  const int grid = s.n_tiles * s.k_tiles;
+  // loads of 32 bytes a lane where W's alignment allows (28672 x 4096: fp32 89 us for 109, 16-bit weights the same)
+  if ((uintptr_t)W % 32 == 0) pack4_kernel<true><<<grid, kPackThreads, 0, st>>>(W, (uint8_t*)out, s, flag);
+  else pack4_kernel<false><<<grid, kPackThreads, 0, st>>>(W, (uint8_t*)out, s, flag);
+}
+
 constexpr int kMaxRows = 1 << 20;   // of X
 
 bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
@@ -1146,11 +1169,10 @@ pic_status pic_op_pack_weight4(int32_t dtype, const void* W, void* out, int32_t 
   unsigned* flag = nullptr;
   pic_status e = batch_flag_address(&flag);
   if (e != PIC_OK) return e;
-  const int grid = s.n_tiles * s.k_tiles;
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == PIC_F32) pack4_kernel<<<grid, kPackThreads, 0, st>>>((const float*)W, (uint8_t*)out, s, flag);
-  else if (dtype == PIC_F16) pack4_kernel<<<grid, kPackThreads, 0, st>>>((const __half*)W, (uint8_t*)out, s, flag);
-  else pack4_kernel<<<grid, kPackThreads, 0, st>>>((const __nv_bfloat16*)W, (uint8_t*)out, s, flag);
+  if (dtype == PIC_F32) launch_pack4((const float*)W, out, s, flag, st);
+  else if (dtype == PIC_F16) launch_pack4((const __half*)W, out, s, flag, st);
+  else launch_pack4((const __nv_bfloat16*)W, out, s, flag, st);
   PIC_CUDA(cudaGetLastError());
   return PIC_OK;
 }

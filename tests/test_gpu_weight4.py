@@ -103,6 +103,19 @@ def test_packing_next_to_the_borders(pkl, dtype):
     assert sync() == (7 if t.isnan().any() else 0)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_packing_of_weights_at_any_16_bytes(pkl, dtype):
+    """Weights that begin between two 32-byte borders are loaded in smaller pieces."""
+    N, K, t = 130, 160, TYPES[dtype]
+    each = 16 // torch.empty(0, dtype=t).element_size()
+    buf = randn(4, N * K + each).to(t)
+    apart = buf[each:].view(N, K)
+    assert apart.data_ptr() % 32 == 16
+    for group in (32, 64, 128):
+        a, b = pkl.pack_weight4(apart, group), pkl.pack_weight4(apart.clone(), group)
+        assert torch.equal(a.data, b.data)
+
+
 def test_packing_of_special_groups(pkl):
     """Zeros (and -0), one sign only, scales below fp16's normal range and below its least number, the greatest ones."""
     W = torch.zeros(8, 64, device="cuda")
@@ -268,6 +281,18 @@ def test_product_keeps_rows_apart(pkl, T):
     y = pkl.gemm_w4(pkl.pack_codes4(codes, scales, zeros, 128), rows(T, K, False)[0])
     keep = torch.arange(N, device="cuda") != 7
     assert torch.equal(y[:, keep], clean[:, keep]) and not torch.isfinite(y[:, 7]).any()
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 300, 1120), (40, 300, 65536)])
+def test_product_keeps_8_bit_rows_apart(pkl, T, N, K):
+    """The same for 8-bit rows, and for their scales."""
+    w, *_ = weights(pkl, N, K, 128)
+    x, sx = rows(T, K, True)
+    clean = pkl.gemm_w4(w, x, sx)
+    x[1, 100] = float("nan")
+    sx[2, 3] = float("inf")
+    y = pkl.gemm_w4(w, x, sx)
+    assert torch.equal(y[0], clean[0]) and torch.equal(y[3:], clean[3:]) and y[1].isnan().all() and not torch.isfinite(y[2]).any()
 
 
 def test_rows_of_one_sign(pkl):
