@@ -22,7 +22,7 @@ namespace {
 //
 // One CTA packs a tile; a thread holds 32 columns of a row (16 bytes of codes), the four threads of a row's 128 columns lie
 // side by side, so that the extremes of a group of 64 or 128 are shuffles away. Bound by instructions for 16-bit weights (28672 x 4096
-// bf16 in groups of 64: 77 us, 3.8 TB/s, issue slots 69 % busy; fp16 in groups of 128: 69 us), by HBM for fp32 (89 us, 6.0 TB/s).
+// bf16 in groups of 64: 76 us, 3.9 TB/s, issue slots 67 % busy; fp16 in groups of 128: 69 us), by HBM for fp32 (89 us, 6.0 TB/s).
 // Unpacking writes 8 bytes for every one that it reads: 84 us, 6.3 TB/s, 93 % of a copy (98 us in pieces of 16 bytes a lane instead of 32).
 constexpr int kPackThreads = 256;
 
@@ -110,7 +110,7 @@ __device__ __forceinline__ int nearest_quotient(float x, float s, float rs) {
 }
 
 // fp16 of fp32 of (hi - lo) / 15 in 64 bits. In fp32 the quotient is within 2^-22 of itself, so its fp16 is known unless a border lies
-// within 2^-20: only then 64 bits decide (in every group they took 110 of 117 us for 28672 x 4096: this GPU has few units for them).
+// within 2^-20: only then 64 bits decide (this GPU has few units for them: in every group, 28672 x 4096 took 117 us for 103).
 __device__ __forceinline__ __half group_scale(float lo, float hi) {
   const float q = (hi - lo) * (1.f / 15.f);
   const __half a = __float2half_rn(q * (1.f - 1.f / 1048576)), b = __float2half_rn(q * (1.f + 1.f / 1048576));
