@@ -290,7 +290,8 @@ pic_status pic_release_request(pic_store* s, pic_request r);
  * Else what the batched calls on device-resident lengths and the decode-step calls skipped or could not do: PIC_ERR_DEVICE_TIMEOUT
  * and PIC_ERR_RANGE as above, then PIC_ERR_INVALID_ARG for device metadata that does not fit together (tokens and codes
  * out of range among it), else PIC_ERR_CAPACITY, else PIC_ERR_OUT_OF_BLOCKS.
- * s may be NULL. */
+ * The flags are the device's, not the stream's: what calls on other streams have flagged by then is reported, and cleared, too;
+ * what they flag later is left for a later pic_sync. s may be NULL. */
 pic_status pic_sync(pic_store* s, pic_stream_t stream);
 
 /* Sets one of the device flags that pic_sync reports, from the host, without running a

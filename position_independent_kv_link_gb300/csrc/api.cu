@@ -1392,10 +1392,11 @@ pic_status pic_sync(pic_store* s, pic_stream_t stream) {
   (void)s;
   PIC_CUDA(cudaStreamSynchronize((cudaStream_t)stream));
   // every flag is read (and cleared) even when an earlier one is set
-  const pic_status a = attn_check_timeout();
-  const pic_status g = tc_check_timeout();
-  const pic_status r = rows_check_range();
-  const pic_status b = batch_check_flags();
+  cudaStream_t st = (cudaStream_t)stream;
+  const pic_status a = attn_check_timeout(st);
+  const pic_status g = tc_check_timeout(st);
+  const pic_status r = rows_check_range(st);
+  const pic_status b = batch_check_flags(st);
   return a != PIC_OK ? a : g != PIC_OK ? g : r != PIC_OK ? r : b;
 }
 

@@ -936,12 +936,11 @@ void attn_raise_timeout() {
   cudaMemcpyToSymbol(g_attn_timeout, &one, sizeof(int));
 }
 
-pic_status attn_check_timeout() {
-  int v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_timeout, sizeof(int));
-  if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("timeout flag: ") + cudaGetErrorString(e));
+pic_status attn_check_timeout(cudaStream_t st) {
+  unsigned v = 0;
+  const pic_status e = read_flag(g_attn_timeout, &v, st);
+  if (e != PIC_OK) return e;
   if (v) {
-    cudaMemcpyToSymbol(g_attn_timeout, &zero, sizeof(int));
     return fail(PIC_ERR_DEVICE_TIMEOUT, "the tensor-core attention kernel gave up a bounded wait");
   }
   return PIC_OK;

@@ -613,7 +613,7 @@ pic_status batch_flag_address(unsigned** out) {
   return PIC_OK;
 }
 
-pic_status batch_check_flags() {
+pic_status batch_check_flags(cudaStream_t st) {
   // without a batched call nothing has been flagged, and pic_sync is spared a copy (28 us instead of 37)
   int dev = 0;
   PIC_CUDA(cudaGetDevice(&dev));
@@ -623,11 +623,9 @@ pic_status batch_check_flags() {
     if (!g_flag_addr[dev]) return PIC_OK;
   }
   unsigned f = 0;
-  const unsigned zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&f, g_batch_flag, sizeof(f));
-  if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("batch flag: ") + cudaGetErrorString(e));
+  const pic_status e = read_flag(g_batch_flag, &f, st);
+  if (e != PIC_OK) return e;
   if (!f) return PIC_OK;
-  cudaMemcpyToSymbol(g_batch_flag, &zero, sizeof(zero));
   if (f & kBatchTimeout) return fail(PIC_ERR_DEVICE_TIMEOUT, "a kernel of the batched or decode-step calls gave up a bounded wait");
   if (f & kBatchRange)
     return fail(PIC_ERR_RANGE, "a value was beyond the type it was bound for (fp16's range, or not finite where it was to be "

@@ -718,11 +718,10 @@ pic_status tc_pack_weight(const void* W, void* out, int N, int K, cudaStream_t s
 }
 
 pic_status tc_check_pack_range() {
-  int v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_pack_range, sizeof(int));
-  if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("pack range flag: ") + cudaGetErrorString(e));
+  unsigned v = 0;
+  const pic_status e = read_flag(g_pack_range, &v, 0);
+  if (e != PIC_OK) return e;
   if (v) {
-    cudaMemcpyToSymbol(g_pack_range, &zero, sizeof(int));
     return fail(PIC_ERR_RANGE, "a projection weight is outside fp16's range (|w| > 65504 or NaN): it cannot be packed "
                                "as an fp16 tensor-core operand");
   }
@@ -734,12 +733,11 @@ void tc_raise_timeout() {
   cudaMemcpyToSymbol(g_tc_timeout, &one, sizeof(int));
 }
 
-pic_status tc_check_timeout() {
-  int v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_tc_timeout, sizeof(int));
-  if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("timeout flag: ") + cudaGetErrorString(e));
+pic_status tc_check_timeout(cudaStream_t st) {
+  unsigned v = 0;
+  const pic_status e = read_flag(g_tc_timeout, &v, st);
+  if (e != PIC_OK) return e;
   if (v) {
-    cudaMemcpyToSymbol(g_tc_timeout, &zero, sizeof(int));
     return fail(PIC_ERR_DEVICE_TIMEOUT, "a tensor-core kernel gave up a bounded wait");
   }
   return PIC_OK;

@@ -3,6 +3,7 @@
 // residual stream, SwiGLU, block copies for request-private pages, KV import. All are
 // memory-bound; float4 accesses over rows.
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "batch_plan.h"
@@ -335,12 +336,26 @@ __global__ void import_kv_kernel(int n, int G, int D, const T* __restrict__ ks, 
 
 }  // namespace
 
-pic_status rows_check_range() {
-  unsigned v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_range_flag, sizeof(v));
-  if (e != cudaSuccess) return fail(PIC_ERR_CUDA, std::string("range flag: ") + cudaGetErrorString(e));
+namespace {
+__device__ unsigned g_taken;   // the answer of the one taken at a time
+std::mutex g_taken_mu;
+__global__ void take_flag_kernel(unsigned* word) { g_taken = atomicExch(word, 0u); }
+}  // namespace
+
+pic_status take_flag(unsigned* word, unsigned* bits, cudaStream_t st) {
+  std::lock_guard<std::mutex> lock(g_taken_mu);
+  take_flag_kernel<<<1, 1, 0, st>>>(word);
+  PIC_CUDA(cudaGetLastError());
+  PIC_CUDA(cudaMemcpyFromSymbolAsync(bits, g_taken, sizeof(*bits), 0, cudaMemcpyDeviceToHost, st));
+  PIC_CUDA(cudaStreamSynchronize(st));
+  return PIC_OK;
+}
+
+pic_status rows_check_range(cudaStream_t st) {
+  unsigned v = 0;
+  const pic_status e = read_flag(g_range_flag, &v, st);
+  if (e != PIC_OK) return e;
   if (v) {
-    cudaMemcpyToSymbol(g_range_flag, &zero, sizeof(zero));
     return fail(PIC_ERR_RANGE, "a value bound for an fp16 tensor-core operand was outside fp16's range (|x| > 65504, "
                                "or > 46000 for stored K, or NaN); the outputs since the last pic_sync are invalid");
   }

@@ -26,6 +26,22 @@ pic_status fail(pic_status s, const std::string& msg);
       return ::pic::fail(PIC_ERR_CUDA, std::string(#call) + ": " + cudaGetErrorString(e_)); \
   } while (0)
 
+// ------------------------------------------------------------------ device flags
+// What a flag word holds becomes the answer, and the word 0, in one operation on the device (k_rows.cu): a bit that a kernel of
+// another stream sets at that time is in this answer or stays for the next.
+pic_status take_flag(unsigned* word, unsigned* bits, cudaStream_t st);
+// The bits of a file's flag word, which are then cleared. A word of 0 costs one copy.
+template <typename Word>
+inline pic_status read_flag(const Word& word, unsigned* bits, cudaStream_t st) {
+  static_assert(sizeof(Word) == sizeof(unsigned), "one word");
+  *bits = 0;
+  PIC_CUDA(cudaMemcpyFromSymbol(bits, word, sizeof(Word)));
+  if (!*bits) return PIC_OK;
+  void* p = nullptr;
+  PIC_CUDA(cudaGetSymbolAddress(&p, word));
+  return take_flag((unsigned*)p, bits, st);
+}
+
 // ------------------------------------------------------------------ programmatic dependent launch
 // The forward's kernels are launched as programmatic dependents of the kernel before them in
 // the stream, so a kernel's launch and prologue overlap the previous kernel's tail. Such a
@@ -136,12 +152,12 @@ size_t tc_gemm_tiles(int N, int T);
 // tile (mt, kb) at (mt * K/64 + kb) * 16 KB.
 pic_status tc_pack_weight(const void* W, void* out, int N, int K, cudaStream_t st);
 // Reads and clears the device flag set when a tcgen05 GEMM gave up a bounded wait.
-pic_status tc_check_timeout();
+pic_status tc_check_timeout(cudaStream_t st);
 // Same for the tcgen05 attention kernel (k_attn_tc.cu).
-pic_status attn_check_timeout();
+pic_status attn_check_timeout(cudaStream_t st);
 // Reads and clears the device word the row-wise kernels set when a value bound for an fp16
 // tensor-core operand is outside fp16's range (k_rows.cu): PIC_ERR_RANGE.
-pic_status rows_check_range();
+pic_status rows_check_range(cudaStream_t st);
 // Reads and clears the flag tc_pack_weight sets for a weight outside fp16's range: PIC_ERR_RANGE.
 pic_status tc_check_pack_range();
 // Set those device flags from the host, as the kernels would (pic_debug_raise_device_flag).
@@ -242,7 +258,7 @@ size_t attention_part_bytes(int n_parts, int rep, int D);
 // Device word of what the batched kernels met and skipped (batch_plan.h: kBatch* bits), and its
 // report and reset by pic_sync.
 pic_status batch_flag_address(unsigned** out);
-pic_status batch_check_flags();
+pic_status batch_check_flags(cudaStream_t st);
 
 // ------------------------------------------------------------------ dynamic selection (k_select.cu)
 // One request of a dynamic-selection pass: its query rows [row0, row0 + lq) of the pass's
