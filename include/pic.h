@@ -573,8 +573,8 @@ pic_status pic_op_gemm_w4(int32_t x_dtype, const void* W4, const void* X, int64_
                           float* Y, int32_t N, int32_t K, int32_t T, int32_t group, pic_stream_t stream);
 
 /* h[t] += delta[t] (fp32 rows, in place; delta NULL: h stays as it is and is not written), then
- * y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * gain (gain NULL: 1). out_dtype of y [T][d] (contiguous): PIC_F32; PIC_F16
- * (values beyond fp16's range are flagged, PIC_ERR_RANGE from pic_sync); PIC_E4M3, with scales [T][ceil(d / 128)] (fp32):
+ * y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * gain (gain NULL: 1), also where the squares are beyond fp32's range. out_dtype of
+ * y [T][d] (contiguous): PIC_F32; PIC_F16 (values beyond fp16's range are flagged, PIC_ERR_RANGE from pic_sync); PIC_E4M3, with scales [T][ceil(d / 128)] (fp32):
  * a group's scale is its greatest |y| / 448, its values are y / scale rounded to e4m3 (scale and values 0 where the group is
  * 0; groups with NaN or infinity are flagged as above). scales is NULL for the other types. d a multiple of 4, up to 32768 (PIC_ERR_UNSUPPORTED
  * beyond); strides in floats, multiples of 4; all pointers 16-byte aligned. h, delta, y and scales must not overlap. */

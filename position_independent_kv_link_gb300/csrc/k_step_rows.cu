@@ -38,10 +38,87 @@ __device__ __forceinline__ bool beyond(float4 v, float top) {   // or NaN
   return !(fabsf(v.x) <= top) | !(fabsf(v.y) <= top) | !(fabsf(v.z) <= top) | !(fabsf(v.w) <= top);
 }
 
+// The sum over the CTA; the same bits in every thread. `part`: a float a warp.
+__device__ __forceinline__ float cta_sum(float v, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < (int)blockDim.x >> 5; ++w) v += part[w];
+  return v;
+}
+__device__ __forceinline__ float squares(float4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
+__device__ __forceinline__ float4 times(float4 v, float f) { return make_float4(v.x * f, v.y * f, v.z * f, v.w * f); }
+
+// float4 i of row t's output is x r gain (the whole warp: a group's scale is its lanes'; `in`: i is within the row). True where the type
+// does not hold it.
+template <int OUT>
+__device__ __forceinline__ bool put(const AddNormArgs& a, int t, int i, bool in, float4 x, float r) {
+  const float4 g = in && a.gain ? reinterpret_cast<const float4*>(a.gain)[i] : make_float4(1.f, 1.f, 1.f, 1.f);
+  const float4 y = make_float4(x.x * r * g.x, x.y * r * g.y, x.z * r * g.z, x.w * r * g.w);
+  bool bad = false;
+  if constexpr (OUT == PIC_E4M3) {
+    float top = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    bad = beyond(y, FLT_MAX);
+    const float s = top / kE4m3Top;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s >= 0x1p-120f) {                    // (the reciprocal is finite)
+      q = times(y, 1.f / s);
+    } else if (s > 0.f) {
+      q = make_float4(y.x / s, y.y / s, y.z / s, y.w / s);
+    }
+    if (in) {
+      const __nv_fp8x4_e4m3 c(q);          // saturates at 448
+      reinterpret_cast<__nv_fp8x4_e4m3*>(a.y)[(size_t)t * a.d4 + i] = c;
+      if ((threadIdx.x & 31) == 0) a.scales[(size_t)t * a.groups + i / 32] = s;
+    }
+  } else if constexpr (OUT == PIC_F16) {
+    bad = beyond(y, kF16Top);
+    const __half2 lo = __floats2half2_rn(y.x, y.y), hi = __floats2half2_rn(y.z, y.w);
+    if (in)
+      reinterpret_cast<uint2*>(a.y)[(size_t)t * a.d4 + i] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    if (in) reinterpret_cast<float4*>(a.y)[(size_t)t * a.d4 + i] = y;
+  }
+  return bad;
+}
+
+// A row whose squares fp32 does not hold: |h| from 2^56 on (or not finite), or below 2^-40 with no larger eps; m: the mean that came of
+// it. With squares of h 2^-96 or h 2^95 the sum lies between 2^-108 and 2^124, and r h = (r 2^-64) (h 2^-32) or r (h 2^95) keeps the bits
+// that its type has. The row is read again, so that other rows keep no registers for it.
+template <int OUT>
+__device__ __forceinline__ bool far_row(const AddNormArgs& a, int t, const float4* h, float m, float* part) {
+  const bool large = !(m < 0x1p-96f);
+  const float f = large ? 0x1p-96f : 0x1p95f;
+  const int nt = blockDim.x;
+  float ss = 0.f;
+  for (int i = threadIdx.x; i < a.d4; i += nt) ss += squares(times(h[i], f));
+  __syncthreads();                           // `part` has been read
+  const float r = rsqrtf(cta_sum(ss, part) * a.inv_d + a.eps * f * f) * (large ? 0x1p-64f : 1.f);
+  bool bad = false;
+  for (int i0 = 0; i0 < a.d4; i0 += nt) {
+    const int i = i0 + threadIdx.x;
+    const bool in = i < a.d4;
+    bad |= put<OUT>(a, t, i, in, in ? times(h[i], large ? 0x1p-32f : f) : make_float4(0.f, 0.f, 0.f, 0.f), r);
+  }
+  return bad;
+}
+
+// The same as a call, where its registers would be too many in the kernel itself (4096 rows of 8192 to fp16: 73 us for 83); a call costs short
+// rows more (one row of 4096: 2.1 us for 2.2).
+template <int OUT>
+__device__ __noinline__ bool far_row_apart(const AddNormArgs& a, int t, const float4* h, float m, float* part) {
+  return far_row<OUT>(a, t, h, m, part);
+}
+
 template <int OUT, int VPT>
-__global__ void __launch_bounds__(1024) add_norm_kernel(AddNormArgs a) {
+__global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ AddNormArgs a) {
   __shared__ float part[32];
-  const int t = blockIdx.x, nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x, nt = blockDim.x;
   float4* h = reinterpret_cast<float4*>(a.h + t * a.h_stride);
   const float4* delta = reinterpret_cast<const float4*>(a.delta + t * a.delta_stride);
   float4 x[VPT];
@@ -64,48 +141,18 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AddNormArgs a) {
     }
   }
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) ss += x[v].x * x[v].x + x[v].y * x[v].y + x[v].z * x[v].z + x[v].w * x[v].w;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (lane == 0) part[warp] = ss;
-  __syncthreads();
-  ss = 0.f;
-  for (int w = 0; w < nt >> 5; ++w) ss += part[w];
-  const float r = rsqrtf(ss * a.inv_d + a.eps);
+  for (int v = 0; v < VPT; ++v) ss += squares(x[v]);
+  const float m = cta_sum(ss, part) * a.inv_d + a.eps;
   bool bad = false;
+  if (m >= 0x1p-96f && m <= FLT_MAX) {
+    const float r = rsqrtf(m);
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int i = threadIdx.x + v * nt;
-    const bool in = i < a.d4;
-    const float4 g = in && a.gain ? reinterpret_cast<const float4*>(a.gain)[i] : make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 y = make_float4(x[v].x * r * g.x, x[v].y * r * g.y, x[v].z * r * g.z, x[v].w * r * g.w);
-    if constexpr (OUT == PIC_E4M3) {
-      float top = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      bad |= beyond(y, FLT_MAX);
-      const float s = top / kE4m3Top;
-      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s >= 0x1p-120f) {                    // (the reciprocal is finite)
-        const float rs = 1.f / s;
-        q = make_float4(y.x * rs, y.y * rs, y.z * rs, y.w * rs);
-      } else if (s > 0.f) {
-        q = make_float4(y.x / s, y.y / s, y.z / s, y.w / s);
-      }
-      if (in) {
-        const __nv_fp8x4_e4m3 c(q);          // saturates at 448
-        reinterpret_cast<__nv_fp8x4_e4m3*>(a.y)[(size_t)t * a.d4 + i] = c;
-        if (lane == 0) a.scales[(size_t)t * a.groups + i / 32] = s;
-      }
-    } else if constexpr (OUT == PIC_F16) {
-      bad |= beyond(y, kF16Top);
-      const __half2 lo = __floats2half2_rn(y.x, y.y), hi = __floats2half2_rn(y.z, y.w);
-      if (in)
-        reinterpret_cast<uint2*>(a.y)[(size_t)t * a.d4 + i] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    } else {
-      if (in) reinterpret_cast<float4*>(a.y)[(size_t)t * a.d4 + i] = y;
+    for (int v = 0; v < VPT; ++v) {
+      const int i = threadIdx.x + v * nt;
+      bad |= put<OUT>(a, t, i, i < a.d4, x[v], r);
     }
+  } else {
+    bad = VPT <= 2 ? far_row<OUT>(a, t, h, m, part) : far_row_apart<OUT>(a, t, h, m, part);
   }
   batch_flag(a.flag, bad ? kBatchRange : 0);
 }
