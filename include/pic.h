@@ -582,9 +582,10 @@ pic_status pic_op_add_rms_norm(int32_t out_dtype, int32_t T, int32_t d, float* h
                                int64_t delta_stride, const float* gain, float eps, void* y, float* scales,
                                pic_stream_t stream);
 
-/* From logits [T][vocab] (PIC_F32, PIC_BF16 or PIC_F16; logits_stride elements from row to row, no alignment but the
- * type's own), in one pass: logprob[t] = log softmax(logits[t])[tokens[t]]; entropy[t] = -sum p log p in nats;
- * top_ids, top_logprobs [T][top]: the `top` (0..32, at most vocab) likeliest tokens in falling order, equal logits in ascending order of
+/* From logits [T][vocab] (PIC_F32, PIC_BF16 or PIC_F16; logits_stride elements from row to row, no alignment but the type's own), in one
+ * pass (two where a thousand logits and more pass for the likeliest, as in rising rows):
+ * logprob[t] = log softmax(logits[t])[tokens[t]]; entropy[t] = -sum p log p in nats; top_ids, top_logprobs [T][top]: the `top` (0..32,
+ * at most vocab) likeliest tokens in falling order, equal logits in ascending order of
  * their ids. tokens and logprob may be NULL together, entropy may be NULL; top_ids and top_logprobs are NULL when top is 0.
  * A row whose token is -1 is padding: nothing of it is read or written; other tokens outside the vocabulary are flagged
  * (PIC_ERR_INVALID_ARG from pic_sync) and their rows left likewise. Logits of -inf are tokens without probability; a row of

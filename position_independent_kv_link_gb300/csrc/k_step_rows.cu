@@ -179,10 +179,13 @@ cudaError_t launch_add_norm(const AddNormArgs& a, int T, int sms, cudaStream_t s
 // so that log sum e^(x - m) = log n + log1p(rest / n) keeps its digits when one token has nearly all of the probability. m is the
 // warp's, the others are each lane's; a chunk without a new maximum takes the short loop.
 // Alternatives: the `top`-th greatest of 64 maxima, each of what a few threads have seen, is a bound that at least `top` logits reach, and
-// a lane whose chunk reaches it puts what does on the CTA's list. After the first chunk, where the warps meet, one warp sets the bound
-// anew (chunks 2, 4, 8 ..) from the maxima as it finds them: an old bound is as right, it lets more through. At the end the list is ordered by
-// counting, for each, the greater ones. Where more reach the bound than the list holds (ties by the hundred, rising rows), the
-// share's greatest are found one after the other instead, from its logits again.
+// a lane whose chunk reaches it puts what does on the CTA's list. The warps meet to set it at the first chunk, and at the next ones while it
+// is -inf (ids masked in a run; the next chunk's logits would all reach it). Then one warp sets the bound anew (chunks 2, 4, 8 .. from there)
+// from the maxima as it finds them: an old bound is as right, it lets more through. At the end the list is ordered by counting, for each,
+// the greater ones. Where more reach the bound than the list holds (a run masked by a number, ties by the hundred, rising rows), the share is
+// read again with the last bound; where that is still too many (a few threads' columns hold all that is great), its greatest are
+// found one after the other. (1024 rows of 128256 with 32: 120 us; the first 8192 masked by -inf 118, by the lowest number 261; the
+// share searched for one after the other in such rows 5610.)
 // The CTAs of a cluster put their numbers and lists into the first one's shared memory, which joins them.
 // Bound by HBM for fp32 logits (512 rows of 128256: 48 us, 5.5 TB/s, 81 % of a copy, without alternatives; 1024 rows with 5: 102 us), by
 // instructions for 16-bit ones (1024 rows of bf16: 70 us, 55 %: conversion, exponential and two sums for every 2 bytes), and by its start,
@@ -319,6 +322,16 @@ struct LpShared {
 };
 __device__ __forceinline__ void lp_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kLpThreads) : "memory"); }   // of the warps that read
 
+// the same, and whether one of their threads says so
+__device__ __forceinline__ bool lp_sync_or(bool x) {
+  uint32_t any;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(any)
+               : "r"((uint32_t)x), "n"(kLpThreads)
+               : "memory");
+  return any != 0;
+}
+
 // The `top` greatest keys of list[0 .. n) in order into s.top (they are distinct, but for 0: none).
 __device__ __noinline__ void lp_order(LpShared& s, const Key* list, int n, int top) {
   if ((int)threadIdx.x < top) s.top[threadIdx.x] = 0;
@@ -333,6 +346,12 @@ __device__ __noinline__ void lp_order(LpShared& s, const Key* list, int n, int t
     if (k != 0 && threadIdx.x % 4 == 0 && before < top) s.top[before] = k;
   }
   lp_sync();
+}
+
+// A candidate (their order in the list does not matter). What the list does not hold is counted.
+__device__ __forceinline__ void lp_push(LpShared& s, float x, int id) {
+  const int at = atomicAdd(&s.count, 1);
+  if (at < kLpList) s.list[at] = order_key(x, id);
 }
 
 // The `top`-th greatest of the maxima, by one warp: each lane counts, for two of them, the greater ones.
@@ -351,9 +370,59 @@ __device__ __forceinline__ void lp_bound(LpShared& s, int top) {
   if (nb == top - 1) s.bound = b;
 }
 
+// The candidates among the n vectors from `from` on, whose first element is token id0, once more, by the bound that is known in the end: the
+// logits above it, and each warp's first `top` of those that equal it (it goes through them in the order of their ids).
+template <typename T>
+__device__ __forceinline__ void lp_again(LpShared& s, int top, const uint4* from, int n, int id0) {
+  constexpr int E = 16 / sizeof(T), U = 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  lp_sync();                                       // (the count has been read)
+  if (warp == 0) lp_bound(s, top);
+  if (threadIdx.x == 0) s.count = 0;
+  lp_sync();
+  const float bound = s.bound;
+  int tied = 0;
+  for (int i0 = warp * 32; i0 < n; i0 += U * kLpThreads) {
+    uint4 vec[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kLpThreads + lane;
+      vec[u] = from[min(i, n - 1)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kLpThreads + lane;
+      float x[E];
+      unpack<T>(vec[u], x);
+      unsigned above = 0, ties = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        above |= (unsigned)(x[e] > bound) << e;
+        ties |= (unsigned)(x[e] == bound) << e;
+      }
+      if (i >= n) above = ties = 0;
+      for (; above; above &= above - 1) {
+        const int e = __ffs(above) - 1;
+        lp_push(s, as_float(reinterpret_cast<const T*>(from + i)[e]), id0 + i * E + e);
+      }
+      if (tied < top && bound > -INFINITY && __any_sync(0xffffffffu, ties)) {
+        const int own = __popc(ties);
+        int upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int before = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += before;
+        }
+        for (int nth = tied + upto - own; ties && nth < top; ties &= ties - 1, ++nth) lp_push(s, bound, id0 + i * E + __ffs(ties) - 1);
+        tied += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+  }
+}
+
 // The `top` greatest of row[i0 .. i1) into s.top, one after the other.
 template <typename T>
-__device__ __noinline__ void lp_one_by_one(LpShared& s, int top, const T* row, int64_t i0, int64_t i1) {
+__device__ __forceinline__ void lp_one_by_one(LpShared& s, int top, const T* row, int64_t i0, int64_t i1) {
   Key before = ~0ull;
   for (int j = 0; j < top; ++j) {
     Key best = 0;
@@ -376,6 +445,21 @@ __device__ __noinline__ void lp_one_by_one(LpShared& s, int top, const T* row, i
     before = best;
   }
   lp_sync();
+}
+
+// The same where the list could not hold all candidates. The CTA's share: logits i0 .. id0, n vectors from id0 on, and `tail` more.
+template <typename T>
+__device__ __noinline__ void lp_crowded(LpShared& s, int top, const T* row, int i0, int id0, int n, int tail) {
+  constexpr int E = 16 / sizeof(T);
+  lp_again<T>(s, top, reinterpret_cast<const uint4*>(row + id0), n, id0);
+  const int behind = id0 + n * E, e = threadIdx.x, i = e < E ? (e < id0 - i0 ? i0 + e : -1) : e < 2 * E && e - E < tail ? behind + e - E : -1;
+  if (i >= 0) {
+    const float x = as_float(row[i]);
+    if (x > -INFINITY) lp_push(s, x, i);
+  }
+  lp_sync();
+  if (s.count <= kLpList) lp_order(s, s.list, s.count, top);
+  else lp_one_by_one(s, top, row, i0, behind + tail);
 }
 
 template <typename T>
@@ -441,10 +525,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
     LpPart mine{-INFINITY, 0.f, 0.f, 0.f};         // m the warp's
     float seen = -INFINITY;                        // this thread's maximum
     bool landed = true;                            // (after a wait that was given up chunks count as empty: the barriers below still meet)
-    auto push = [&](float x, int id) {
-      const int at = atomicAdd(&s.count, 1);       // (the order in the list does not matter)
-      if (at < kLpList) s.list[at] = order_key(x, id);
-    };
+    int settled = 0;                               // chunks since there is a bound
     // a new maximum of the warp
     auto raise = [&](float top1) {
       if (!__any_sync(0xffffffffu, top1 > mine.m)) return;
@@ -466,7 +547,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
         else mine.rest = p;
         mine.e = p * d;
       }
-      if (a.top > 0 && x > -INFINITY) push(x, i);
+      if (a.top > 0 && x > -INFINITY) lp_push(s, x, i);
     }
     int st = 0;
     uint32_t ph = 0;
@@ -525,25 +606,30 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
         float g = seen;
 #pragma unroll
         for (int o = 1; o < kLpGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        const int k = c - c0;
         if (lane % kLpGroup == 0) const_cast<volatile float*>(s.group)[tid / kLpGroup] = g;
-        if (k == 0) {
-          lp_sync();
-          if (warp == 0) lp_bound(s, a.top);
-          lp_sync();
-        } else if ((k & (k + 1)) == 0 && __popc(k) % kLpWarps == warp) {   // chunks 2, 4, 8 ..
-          __syncwarp();
-          lp_bound(s, a.top);
+        if (settled == 0) {                        // (the same in every warp)
+          if (lp_sync_or(top1 > -INFINITY)) {
+            if (warp == 0) lp_bound(s, a.top);
+            lp_sync();
+            settled = *const_cast<volatile float*>(&s.bound) > -INFINITY;
+          }
+        } else {
+          if ((settled & (settled + 1)) == 0 && __popc(settled) % kLpWarps == warp) {   // chunks 2, 4, 8 ..
+            __syncwarp();
+            lp_bound(s, a.top);
+          }
+          ++settled;
         }
         const float bound = *const_cast<volatile float*>(&s.bound);
         if (top1 >= bound && top1 > -INFINITY) {   // few lanes, of one or two logits mostly
           unsigned long long reach = 0;
 #pragma unroll
           for (int j = 0; j < kEach; ++j) reach |= (unsigned long long)(x[j] >= bound) << j;
+          if (*const_cast<volatile int*>(&s.count) > kLpList) reach = 0;   // they will be found once more anyway
           for (; reach; reach &= reach - 1) {
             const int j = __ffsll(reach) - 1;
             const float y = again(j);
-            if (j < own * E && y > -INFINITY) push(y, head + (c * kVecs + j / E * kLpThreads + tid) * E + j % E);
+            if (j < own * E && y > -INFINITY) lp_push(s, y, head + (c * kVecs + j / E * kLpThreads + tid) * E + j % E);
           }
         }
       }
@@ -556,13 +642,8 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpCtas) logprob_kernel(Logpr
     if (lane == 0) s.part[warp] = part;
     lp_sync();
     if (a.top > 0) {
-      const int n = s.count;
-      if (n <= kLpList) {
-        lp_order(s, s.list, n, a.top);
-      } else {
-        const int64_t per = kLpChunk / sizeof(T);
-        lp_one_by_one(s, a.top, row, rank == 0 ? 0 : head + c0 * per, rank == ctas - 1 ? a.V : head + c1 * per);
-      }
+      if (s.count <= kLpList) lp_order(s, s.list, s.count, a.top);
+      else lp_crowded(s, a.top, row, rank == 0 ? 0 : head + c0 * (kVecs * E), head + c0 * (kVecs * E), min(vectors, c1 * kVecs) - c0 * kVecs, rank == ctas - 1 ? tail : 0);
     }
   }
   bad = __syncthreads_or(bad);
