@@ -561,21 +561,21 @@ pic_status pic_op_pack_weight4(int32_t dtype, const void* W, void* out, int32_t 
  * and lose their upper bits. */
 pic_status pic_op_pack_codes4(const uint8_t* codes, const void* scales, const uint8_t* zeros, void* out, int32_t N,
                               int32_t K, int32_t group, pic_stream_t stream);
-/* The fp32 values [N][K] that a packed matrix stands for (each exact). */
+/* The fp32 values [N][K] that a packed matrix stands for (each exact). W 32-byte aligned, must not overlap W4. */
 pic_status pic_op_unpack_weight4(const void* W4, float* W, int32_t N, int32_t K, int32_t group, pic_stream_t stream);
 
 /* Y[T][N] (fp32, overwritten) = X[T][K] . W^T with W in the layout above. x_dtype PIC_F16: X fp16, x_scales NULL.
  * PIC_E4M3: X 8-bit, x_scales fp32 [T][ceil(K / 128)]: X[t][k] stands for that value times x_scales[t][k / 128]
  * (pic_op_add_rms_norm writes both). x_stride: elements from row to row, its bytes a multiple of 16; X, Y 16-byte aligned.
- * Products are exact, sums fp32, each group's sum times its scale in fp32. Made for few rows: the weights are read once
- * for every 64. T up to 2^20. Y must not overlap W4, X or x_scales. */
+ * Products are exact, sums fp32, each group's sum times its scale in fp32. Made for few rows: the weights are read once for every 64 of
+ * them, or every 32 where X and W make few tiles. T up to 2^20. Y must not overlap W4, X or x_scales. */
 pic_status pic_op_gemm_w4(int32_t x_dtype, const void* W4, const void* X, int64_t x_stride, const float* x_scales,
                           float* Y, int32_t N, int32_t K, int32_t T, int32_t group, pic_stream_t stream);
 
 /* h[t] += delta[t] (fp32 rows, in place; delta NULL: h stays as it is and is not written), then
  * y[t] = h[t] / sqrt(mean(h[t]^2) + eps) * gain (gain NULL: 1), also where the squares are beyond fp32's range. out_dtype of
  * y [T][d] (contiguous): PIC_F32; PIC_F16 (values beyond fp16's range are flagged, PIC_ERR_RANGE from pic_sync); PIC_E4M3, with scales [T][ceil(d / 128)] (fp32):
- * a group's scale is its greatest |y| / 448, its values are y / scale rounded to e4m3 (scale and values 0 where the group is
+ * a group's scale is its greatest |y| / 448, its values are y / scale, to 2^-22 of itself, rounded to e4m3 (scale and values 0 where the group is
  * 0; groups with NaN or infinity are flagged as above). scales is NULL for the other types. d a multiple of 4, up to 32768 (PIC_ERR_UNSUPPORTED
  * beyond); strides in floats, multiples of 4; all pointers 16-byte aligned. h, delta, y and scales must not overlap. */
 pic_status pic_op_add_rms_norm(int32_t out_dtype, int32_t T, int32_t d, float* h, int64_t h_stride, const float* delta,

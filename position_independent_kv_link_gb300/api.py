@@ -717,7 +717,7 @@ def pack_codes4(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch
 
 
 def unpack_weight4(w: Weight4, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The fp32 values [N, K] that packed weights stand for (pic_op_unpack_weight4)."""
+    """The fp32 values [N, K] that packed weights stand for (pic_op_unpack_weight4); out: 32-byte aligned."""
     idx = _device_index(w.data)
     wp = w._args(idx)
     if out is None:
@@ -811,7 +811,8 @@ def token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, 
                    out: Optional[TokenLogprobs] = None, stream=None) -> TokenLogprobs:
     """Log probabilities of the given tokens (int32 [T], -1: a padding row that is left alone), entropy and the `top`
     likeliest tokens with theirs, from logits [T, vocab] (fp32, bf16 or fp16; rows may lie apart) in one pass
-    (pic_op_token_logprobs). `out`: tensors to write; what is None in it is not computed."""
+    (pic_op_token_logprobs). `out`: tensors to write; entropy is not computed where it is None in it, logprob goes with
+    tokens, top_ids and top_logprobs with top."""
     idx = _device_index(logits)
     code = _CODE.get(logits.dtype)
     if logits.dim() != 2 or logits.stride(1) != 1 or code is None or code == L.PIC_E4M3:

@@ -16,8 +16,8 @@ namespace {
 //
 // One CTA per row, the row in registers between its sum of squares and its output: every byte is read and written once.
 // Thread i holds the float4s i, i + blockDim, ...: a warp's float4 is 128 columns, one group of 8-bit values, whose
-// greatest is five shuffles away. Bound by HBM when rows are many (8192 rows of 4096: 70 us to fp16, 6.7 TB/s, 99 % of a copy; 72 to e4m3,
-// 89 %: two divisions' reciprocals and five shuffles a group), by a launch and one round through memory when they are few (one row: 2.1 us).
+// greatest is five shuffles away. Bound by HBM when rows are many (8192 rows of 4096: 69 us to fp16, 6.8 TB/s, as a copy; 70 to e4m3,
+// 92 %: a reciprocal and five shuffles a group), by a launch and one round through memory when they are few (one row: 2.1 us).
 constexpr int kXGroup = 128;
 constexpr float kF16Top = 65504.f, kE4m3Top = 448.f;
 
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ 
 
 template <int OUT>
 cudaError_t launch_add_norm(const AddNormArgs& a, int T, int sms, cudaStream_t st) {
-  // Few rows: as many threads as there are float4s (one row of 4096: 2.4 us). Many: 512 at most, two to eight float4s a thread (8192 rows
-  // of 4096 to e4m3: 72 us; 83 with 1024 threads, 81 with 256, 92 with 128).
+  // Few rows: as many threads as there are float4s (one row of 4096: 2.1 us). Many: 512 at most, two to eight float4s a thread (8192 rows
+  // of 4096 to e4m3: 70 us; 83 with 1024 threads, 81 with 256, 92 with 128).
   const int most = T <= 2 * sms ? 1024 : 512;
   int per = 1;
   while (per < 8 && (a.d4 + per - 1) / per > most) per *= 2;
@@ -187,8 +187,8 @@ cudaError_t launch_add_norm(const AddNormArgs& a, int T, int sms, cudaStream_t s
 // found one after the other. (1024 rows of 128256 with 32: 120 us; the first 8192 masked by -inf 118, by the lowest number 261; the
 // share searched for one after the other in such rows 5610.)
 // The CTAs of a cluster put their numbers and lists into the first one's shared memory, which joins them.
-// Bound by HBM for fp32 logits (512 rows of 128256: 48 us, 5.5 TB/s, 81 % of a copy, without alternatives; 1024 rows with 5: 102 us), by
-// instructions for 16-bit ones (1024 rows of bf16: 70 us, 55 %: conversion, exponential and two sums for every 2 bytes), and by its start,
+// Bound by HBM for fp32 logits (512 rows of 128256: 48 us, 5.5 TB/s, 81 % of a copy, without alternatives; 1024 rows with 5: 100 us), by
+// instructions for 16-bit ones (1024 rows of bf16: 69 us, 56 %: conversion, exponential and two sums for every 2 bytes), and by its start,
 // the list and the joins for few rows (one of 128256 with 20 alternatives: 11 us).
 constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32, kLpChunk = 32768, kLpStages = 3, kMaxTop = 32, kLpList = 1024, kLpCluster = 8;
 constexpr int kLpCtas = 2;                         // an SM

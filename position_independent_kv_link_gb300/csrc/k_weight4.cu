@@ -284,9 +284,10 @@ struct Gemm4Args {
 };
 
 // Sums of (code - zero) x, exact products of integers below 16 with fp16 (or e4m3) numbers in fp32, times the group's scale in fp32. The
-// weights' 4 bits are the bytes that count: HBM would allow 0.19 us for a 128 x 128 block a SM. Turning codes into operands costs more: 9
-// instructions for 8 codes, and both kernels stand at about twice that time (LM head of 128256 x 4096: 1 row 55 us, 16 rows 70, 64 rows
-// 83 (fp16) and 101 (e4m3); floors 41, 42, 45). 4096 x 14336: 1 row 12 us, 16 rows 14, 64 rows 20; floor 4.5 to 5.
+// weights' 4 bits are the bytes that count: HBM would allow 0.19 us for a 128 x 128 block an SM. Turning codes into operands (9
+// instructions for 8 codes), the sums and the handshakes cost more: 0.26 us with one row, 0.33 with 16, 0.39 and 0.48 with 64 in fp16 and
+// e4m3 (LM head of 128256 x 4096: 55 us, 69, 83, 101; floors 41, 42, 45, 45). 4096 x 14336: 1 row 12 us, 16 rows 14, 64 rows 20; floor
+// 4.5 to 5.
 //
 // A band is 128 rows of W (256 in the tcgen05 kernel) against one tile of rows of X; its columns come in blocks of 128. With many
 // bands the CTAs take whole ones in turn, and their copies run on over the ends of bands. With few, and for what is left after the last
@@ -812,8 +813,10 @@ __global__ void __launch_bounds__(TcShape<E4M3, NT>::kThreads, 1)
 // run, which stand where the products want 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q (the sum over columns does not mind).
 // Where a cluster shares a band, each CTA puts its sums of a row of X into the shared memory of the CTA that the row belongs to, while others
 // may still work (16 rows of 4096 x 4096: 7.0 us; 8.8 when it read them there after a barrier, and left after another).
-// Bound by the logic pipe, which turns codes into operands: 16 rows of W a warp and twice as many warps are slower (one row of
-// 128256 x 4096: 65 us for 55; 16 rows of 28672 x 4096: 22 for 20), as the loop's own instructions then serve half as many codes.
+// No unit is full (one row of 28672 x 4096: issue slots 51 % busy, the ALU 44, the pipe of fp16 operations 36, tensor 20, HBM 47): of 3.4
+// warps an SM quarter 0.9 are ready, and start and end take 4 of 17 us. 16 rows of W a warp and twice as many warps are slower all
+// the same (one row of 128256 x 4096: 65 us for 55; 16 rows of 28672 x 4096: 22 for 20), as the loop's own instructions then serve
+// half as many codes.
 constexpr int kRowsThreads = 160;
 
 // Row of an 8-row tile of X that lane group g reads, and the column of a product that is its: rows that one access of
@@ -1043,9 +1046,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   return fn;
 }
 
-// CTAs of a cluster that share a band, or 1. An SM takes a block in about 0.19 us whatever runs on it, a CTA by itself in 0.3 (kernel of
-// few rows); so a band is shared while that spreads the blocks better, or lets more CTAs work at once, and all clusters find room
-// together: 23 clusters of 6 CTAs that fill an SM each do, a 24th waits for a whole turn (6144 x 4096, 64 rows: 29 us for 19).
+// CTAs of a cluster that share a band, or 1. What is compared: 0.19 us a block for an SM (HBM's part of it), 0.3 for a CTA by itself (kernel
+// of few rows), 0.1 a CTA for the joining; so a band is shared while that spreads the blocks better, or lets more CTAs work at once, and
+// all clusters find room together: 23 clusters of 6 CTAs that fill an SM each do, a 24th waits for a whole turn (6144 x 4096, 64 rows:
+// half as long again).
 template <typename Room>
 int gemm4_split(int bands, int blocks, int slots, int sms, Room room) {
   int best = 1;
@@ -1124,8 +1128,10 @@ pic_status launch_gemm4_tc(const Gemm4Args& a, int dev, cudaStream_t st) {
 
 template <bool E4M3>
 pic_status launch_gemm4(const Gemm4Args& a, int dev, cudaStream_t st) {
-  // tcgen05 (us; mma.sync): LM head of 128256 x 4096: 32 rows 76 (110), 64 rows 86 (212), but 16 rows 75 (70). 6144 x 4096 (1536 blocks):
-  // 17 rows 11 (12), 64 rows 14 (16). With fewer blocks its wide bands leave SMs idle: 4096 x 4096: 17 rows 10 (9), 64 rows 12 (13).
+  // tcgen05 (us; in brackets mma.sync), 17 and 64 rows in fp16, then e4m3: 8192 x 4096 (2048 blocks) 10.9 (12.6), 12.8 (19.8); 11.1 (13.8),
+  // 14.1 (22.6). 6144 x 4096 (1536) 10.1 (11.2), 12.6 (15.2); 10.2 (12.4), 13.8 (17.1). 4096 x 4096 (1024) 9.3 (8.3), 11.3 (12.4); 9.5
+  // (9.0), 13.2 (13.8). 4096 x 2048 (512), where its wide bands leave SMs idle, 7.5 (6.3), 9.3 (8.2); 7.7 (6.8), 10.7 (9.1). LM head of
+  // 128256 x 4096: 32 rows 76 (110), but 16 rows 75 (70). Few tall bands lose little by it: 128 x 199936 120 (134), 131 (134); 118 (153), 165 (153).
   if (a.T > kFewRows && (int64_t)a.w.n_tiles * a.w.k_tiles * ((a.T + 31) / 32) >= kTcBlocks)
     return a.T <= 32 ? launch_gemm4_tc<E4M3, 32>(a, dev, st) : launch_gemm4_tc<E4M3, 64>(a, dev, st);
   return a.T <= 8 ? launch_gemm4_rows<E4M3, 8>(a, dev, st) : a.T <= 16 ? launch_gemm4_rows<E4M3, 16>(a, dev, st) : launch_gemm4_rows<E4M3, 32>(a, dev, st);
